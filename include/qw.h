@@ -86,7 +86,11 @@ enum qw_weight_format {
  */
 enum qw_kv_format {
     QW_KV_F32 = 0,
-    QW_KV_BF16 = 1
+    QW_KV_BF16 = 1,
+    QW_KV_INT8_G32 = 2 /* int8 codes + one fp16 scale per 32 elements of a row, the Q8_0 block's
+                          quantiser: d = amax/127 in f32, code = round-half-away(a/d), scale =
+                          fp16(d), value = f32(code) * f32(scale).  For qw_kv_view
+                          (the cache operators); a model's own cache is f32 or bf16. */
 };
 
 /*
@@ -265,6 +269,138 @@ int qw_batch_logits(qw_batch *b, float *dst_dev, int64_t n);
 int qw_batch_debug_hidden(qw_batch *b, float *dst_dev, int64_t n);
 /* Wait for the batch's work; returns a recorded device error. */
 int qw_batch_sync(qw_batch *b);
+
+/* ---------------------------------------------- operators on caller-owned buffers */
+
+/*
+ * Drafted tokens ("speculative decoding"): a tree of up to 64 candidate continuations of each
+ * sequence is checked in one pass.  The nodes' K and V rows are appended behind the
+ * sequences' cached rows (qw_kv_append), every node attends to the cached rows and to its own
+ * ancestors (qw_tree_attention), and the nodes' logits are made ready for sampling
+ * (qw_process_logits, then qw_sample_logits).  With one node per sequence these are the
+ * operators of an ordinary batched decode step.
+ *
+ * They take no handle: every buffer is the caller's, every call is stream-ordered on its
+ * cuda_stream (of the current device) and returns after enqueueing, keeps nothing between
+ * calls, allocates nothing and can be captured into a CUDA graph.  Arguments are checked
+ * before anything is launched; lengths and counts live on the device and are checked there.
+ */
+
+/*
+ * Cache of n_seq sequences: k and v hold one row of head_dim elements (64 or 128, contiguous)
+ * per (sequence, KV head, position < max_ctx), at seq * seq_stride + head * head_stride +
+ * pos * pos_stride elements; k and v share the strides.  format is an enum qw_kv_format; for
+ * QW_KV_INT8_G32 k and v hold the codes, and k_scale and v_scale the fp16 scales [head_dim / 32]
+ * of each row with strides of their own (else they are ignored).  Rows begin on 16-byte
+ * boundaries (codes and scales too: 8 bytes for codes, head_dim / 16 bytes for scales are enough;
+ * strides are multiples of that), or QW_ALIGNMENT.
+ */
+typedef struct {
+    void *k, *v, *k_scale, *v_scale;
+    int32_t format, n_seq, n_kv_heads, head_dim, max_ctx;
+    int64_t seq_stride, head_stride, pos_stride;
+    int64_t scale_seq_stride, scale_head_stride, scale_pos_stride;
+} qw_kv_view;
+
+/* Rows to append or to read into: up to n_max rows per (sequence, KV head), dtype QW_DT_F32,
+ * QW_DT_F16 or QW_DT_BF16, strides in elements, rows on 16-byte boundaries. */
+typedef struct {
+    void *k, *v;
+    int32_t dtype, n_max;
+    int64_t seq_stride, head_stride, row_stride;
+} qw_kv_rows;
+
+/*
+ * Append: rows [0, count[b]) of sequence b go to positions start[b] .. start[b] + count[b] - 1
+ * (device int32 [n_seq]; count NULL: n_max for every sequence), converted to the cache's
+ * format.  Positions outside are left as they were.  A 32-element group of an 8-bit row that
+ * holds a NaN or an infinity, or whose largest magnitude exceeds 127 * 65504, reads back as
+ * not finite.  A sequence whose start or count does not fit (count outside [0, n_max],
+ * start < 0, start + count > max_ctx) is left alone.  The rows must not overlap the cache.
+ */
+int qw_kv_append(const qw_kv_view *kv, const qw_kv_rows *rows, const int32_t *start_dev, const int32_t *count_dev,
+                 void *cuda_stream);
+/* Read back: the reverse copy, converted to the rows' type.  Rows behind a sequence's count are
+ * left as they were. */
+int qw_kv_read(const qw_kv_view *kv, const qw_kv_rows *rows, const int32_t *start_dev, const int32_t *count_dev,
+               void *cuda_stream);
+
+/*
+ * Attention of drafted trees.  Sequence b has len[b] cached positions, and the K/V rows of its
+ * count[b] <= n_max <= QW_TREE_NODES_MAX drafted nodes at positions len[b] .. len[b] + count[b] - 1
+ * (device int32 [n_seq]; count NULL: n_max).  Node i sees every cached position, and drafted
+ * node j if bit j of mask[b][i] (device uint64 [n_seq][n_max]) is set: its ancestors and itself.
+ * Bits from count[b] on are ignored.  q and out: [n_seq][n_max][n_heads][head_dim] with element
+ * strides, dtype QW_DT_F32, QW_DT_F16 or QW_DT_BF16 for both; n_heads a multiple of the
+ * cache's KV heads (query head h reads KV head h / (n_heads / n_kv_heads)).  The softmax scale
+ * is given.  Row (b, i) of out:
+ *   sum_j softmax_j(scale q . k_j) v_j over the positions j it sees, 0 if it sees none.
+ * What a node does not see does not reach it, NaN and infinities included.  Rows i >= count[b]
+ * of out are left as they were; if len[b] or count[b] does not fit the cache (len < 0,
+ * len + count > max_ctx, count outside [0, n_max]), all n_max rows of the sequence are NaN.
+ * max_len: about the longest len[], as the host knows it; it only sizes the split of the
+ * positions (a longer sequence is right too, but slower).
+ * scratch: qw_tree_attention_scratch_bytes device bytes, 256-byte aligned, for this call alone
+ * while it runs.
+ * Arithmetic: f32 accumulation, sums and softmax statistics.  With f32 queries every product is
+ * f32.  With 16-bit queries the operands of the matrix products are 16-bit (queries as
+ * given, K, V and the softmax weights rounded to 16 bits).
+ */
+enum { QW_TREE_NODES_MAX = 64 };
+typedef struct {
+    const void *q;
+    void *out;
+    int32_t dtype, n_max, n_heads, max_len;
+    float scale;
+    int64_t q_seq_stride, q_node_stride, q_head_stride;
+    int64_t out_seq_stride, out_node_stride, out_head_stride;
+    const uint64_t *mask;
+    const int32_t *len, *count;
+} qw_tree_attention_args;
+
+/* Device scratch bytes of a call with these sizes; 0 for sizes that it refuses. */
+size_t qw_tree_attention_scratch_bytes(const qw_kv_view *kv, int32_t n_max, int32_t n_heads, int32_t max_len);
+int qw_tree_attention(const qw_kv_view *kv, const qw_tree_attention_args *args, void *scratch_dev,
+                      size_t scratch_bytes, void *cuda_stream);
+
+/*
+ * Logits made ready for sampling: rows [n_rows][vocab] (dtype QW_DT_F32, QW_DT_F16 or QW_DT_BF16,
+ * row strides in elements) to out (same dtype; out == logits with equal strides works in place,
+ * any other overlap does not).  For token t of row r, in f32 and in this order:
+ *   c = number of times t stands in history[range[r][0] .. range[r][1]) and in path[r][0 .. path_len);
+ *   if c > 0: x = x > 0 ? x / rep : x * rep, then x -= presence + frequency * c,
+ *     with (rep, presence, frequency) = penalties[r] (the penalty of qw_sample_logits, once per
+ *     distinct token, then the two additive ones);
+ *   x += bias[i] for every i of [bias_range[r][0], bias_range[r][1]) with bias_ids[i] == t,
+ *     in order of i;
+ *   x = -inf if bit t % 32 of mask[mask_index[r]][t / 32] is clear.
+ * Rows may share ranges (the nodes of a tree share their request's history, and path holds
+ * each node's own drafted tokens).  Ids outside [0, vocab) are padding and count for nothing;
+ * ranges are cut to the arrays ([0, n_history), [0, n_bias)).  mask_index[r] < 0: the row is
+ * not masked; >= n_masks: every token is; mask_index NULL: row r takes mask r.
+ * Optional (NULL): penalties (then history and path are not read), history with its
+ * range, path, bias_ids with bias and bias_range, mask.  n_rows <= 65535.
+ */
+typedef struct {
+    const void *logits;
+    void *out;
+    int32_t dtype, n_rows, vocab;
+    int64_t row_stride, out_row_stride;
+    const float *penalties;        /* [n_rows][3]: repetition (> 0), presence, frequency */
+    const int32_t *history;        /* [n_history] token ids */
+    const int32_t *history_range;  /* [n_rows][2]: begin, end */
+    int32_t n_history;
+    const int32_t *path;           /* [n_rows][path_len] token ids, negative = none */
+    int32_t path_len;
+    const int32_t *bias_ids;       /* [n_bias] token ids */
+    const float *bias;             /* [n_bias] */
+    const int32_t *bias_range;     /* [n_rows][2]: begin, end */
+    int32_t n_bias;
+    const uint32_t *mask;          /* [n_masks][(vocab + 31) / 32], bit set = allowed */
+    const int32_t *mask_index;     /* [n_rows] */
+    int32_t n_masks;
+} qw_process_logits_args;
+int qw_process_logits(const qw_process_logits_args *args, void *cuda_stream);
 
 /* -------------------------------------------------------- checkpoint files */
 

@@ -1,0 +1,334 @@
+// tree_attn.cu - attention of the nodes of drafted-token trees over their sequences' caches.
+//
+// Sequence b holds len[b] cached positions and, behind them, the rows of count[b] drafted
+// nodes.  Node i sees every cached position and the drafted rows whose bits are set in
+// mask[b][i] (its ancestors and itself).  For query head h of node i, with the KV head
+// h / G and the scores in the log2 domain:
+//   s_j = scale log2(e) q . k_j            over the positions j that node i sees
+//   out = sum_j 2^(s_j - m) v_j / sum_j 2^(s_j - m),   m = max_j s_j
+// and 0 where node i sees nothing.  One node with its own bit set is the attention of an
+// ordinary decode step.
+//
+// The positions of a sequence are split over CTAs, each with its own running maximum, sum
+// and f32 accumulator (an online softmax), and the splits are merged in order by a second
+// kernel, so the result does not depend on timing.
+#include <algorithm>
+#include <cmath>
+
+#include "qw_ops.h"
+#include "tc.cuh"
+
+namespace qw {
+namespace {
+
+constexpr int kTile = 64;       // positions per tile
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+struct TreeArgs {
+    const uint8_t *k, *v;
+    const __half *ks, *vs;
+    int64_t seq, head, pos, sseq, shead, spos;
+    const void *q;
+    void *out;
+    int dtype;                   // of q and out
+    int64_t qseq, qnode, qhead, oseq, onode, ohead;
+    const unsigned long long *mask;
+    const int32_t *len, *count;
+    int n_max, max_ctx, Hkv, G, S, row_tiles;
+    float scale_log2;
+    float *part;                 // [n_seq][Hkv][n_max * G][S][D + 2]
+};
+
+__device__ __forceinline__ float load_q(const TreeArgs &a, int64_t at) {
+    return a.dtype == QW_DT_F32   ? reinterpret_cast<const float *>(a.q)[at]
+           : a.dtype == QW_DT_F16 ? __half2float(reinterpret_cast<const __half *>(a.q)[at])
+                                  : __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(a.q)[at]);
+}
+
+__device__ __forceinline__ void store_out(const TreeArgs &a, int64_t at, float v) {
+    if (a.dtype == QW_DT_F32) reinterpret_cast<float *>(a.out)[at] = v;
+    else if (a.dtype == QW_DT_F16) reinterpret_cast<__half *>(a.out)[at] = __float2half_rn(v);
+    else reinterpret_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(v);
+}
+
+// Whether sequence b's lengths fit its cache; if not its rows come out as NaN.
+__device__ __forceinline__ bool lengths(const TreeArgs &a, int b, int &len, int &n) {
+    len = a.len[b];
+    n = a.count ? a.count[b] : a.n_max;
+    return n >= 0 && n <= a.n_max && len >= 0 && len <= a.max_ctx - n;
+}
+
+// The split's positions: equal shares of whole tiles.
+__device__ __forceinline__ void split_range(int total, int S, int s, int &p0, int &p1) {
+    const int tiles = (total + kTile - 1) / kTile;
+    const int per = tiles / S, more = tiles % S;
+    p0 = min(total, (s * per + min(s, more)) * kTile);
+    p1 = min(total, ((s + 1) * per + min(s + 1, more)) * kTile);
+}
+
+// CUDA-core form: f32 arithmetic throughout, for every type.  A CTA takes RT query rows
+// (row r = node r / G, head r % G of the KV head's group) and one split of the positions.
+// Per tile of 64 positions: K and V rows widened to f32 in shared memory; scores with one
+// position per thread and the query rows broadcast; the online softmax with one warp per
+// row; P V with four dims per lane and RT / 8 rows per warp (KW warps share a row's
+// positions when RT < 8).
+template <typename KV, int D, int RT>
+__global__ void __launch_bounds__(kThreads) tree_kernel(const TreeArgs a) {
+    constexpr int KS = D + 4;                       // padded K row: quarter warps read 8 banks groups
+    constexpr int LPR = D / 4;                      // lanes per V row
+    constexpr int KPW = 32 / LPR;                   // positions a warp takes at once in P V
+    constexpr int KW = RT < kWarps ? kWarps / RT : 1;  // warps sharing a row
+    constexpr int RW = RT < kWarps ? 1 : RT / kWarps;  // rows per warp
+    constexpr int RS = RT < 4 ? 1 : RT / 4;         // rows per thread in the scores
+    extern __shared__ __align__(16) float smf[];
+    float *sk = smf, *sv = sk + kTile * KS, *sq = sv + kTile * D, *sp = sq + RT * D;
+    float *red = sp + RT * kTile;                   // [kWarps * KPW - per row parts][D]
+    __shared__ float salpha[RT], sm[RT], sl[RT];
+    __shared__ unsigned long long smask[RT];
+    tc::chain_release();
+    const int b = blockIdx.z, h = blockIdx.y / a.row_tiles, rt = blockIdx.y % a.row_tiles, s = blockIdx.x;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int len, n;
+    if (!lengths(a, b, len, n)) return;
+    const int r0 = rt * RT, rows = n * a.G;
+    if (r0 >= rows) return;
+    const int total = len + n;
+    int p0, p1;
+    split_range(total, a.S, s, p0, p1);
+    for (int i = tid; i < RT * D; i += kThreads) {
+        const int r = r0 + i / D;
+        sq[i] = r < rows ? load_q(a, b * a.qseq + (int64_t)(r / a.G) * a.qnode +
+                                         (int64_t)(h * a.G + r % a.G) * a.qhead + i % D) * a.scale_log2
+                         : 0.f;
+    }
+    if (tid < RT) {
+        sm[tid] = -INFINITY;
+        sl[tid] = 0.f;
+        smask[tid] = r0 + tid < rows ? a.mask[(int64_t)b * a.n_max + (r0 + tid) / a.G] : 0ull;
+    }
+    float acc[RW][4];
+#pragma unroll
+    for (int i = 0; i < RW; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    const KV *kb = reinterpret_cast<const KV *>(a.k) + b * a.seq + h * a.head;
+    const KV *vb = reinterpret_cast<const KV *>(a.v) + b * a.seq + h * a.head;
+    for (int t0 = p0; t0 < p1; t0 += kTile) {
+        __syncthreads();
+        for (int i = tid; i < 2 * kTile * (D / 8); i += kThreads) {
+            const int c = i % (D / 8), j = i / (D / 8) % kTile;
+            const bool is_v = i >= kTile * (D / 8);
+            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (t0 + j < p1) {
+                const int64_t at = (int64_t)(t0 + j) * a.pos + 8 * c;
+                if constexpr (sizeof(KV) == 1) {
+                    const __half *sc = (is_v ? a.vs : a.ks) + b * a.sseq + h * a.shead + (int64_t)(t0 + j) * a.spos + c / 4;
+                    load8_q8((is_v ? vb : kb) + at, __half2float(*sc), v);
+                } else {
+                    load8((is_v ? vb : kb) + at, v);
+                }
+            }
+            store8(is_v ? sv + j * D + 8 * c : sk + j * KS + 8 * c, v);
+        }
+        __syncthreads();
+        // scores: thread = (position tid % 64, rows tid / 64 + 4 i)
+        {
+            const int j = tid & 63, rg = tid >> 6;
+            float d[RS];
+#pragma unroll
+            for (int i = 0; i < RS; ++i) d[i] = 0.f;
+            if (RT >= 4 || rg < RT) {
+#pragma unroll 4
+                for (int c = 0; c < D; c += 4) {
+                    const float4 k = *reinterpret_cast<const float4 *>(sk + j * KS + c);
+#pragma unroll
+                    for (int i = 0; i < RS; ++i) {
+                        const float4 q = *reinterpret_cast<const float4 *>(sq + (rg + 4 * i) * D + c);
+                        d[i] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, d[i]))));
+                    }
+                }
+                const int p = t0 + j;
+#pragma unroll
+                for (int i = 0; i < RS; ++i) {
+                    const int r = rg + 4 * i;
+                    const bool sees = p < len || (p < total && ((smask[r] >> (p - len)) & 1ull));
+                    sp[r * kTile + j] = p < p1 && sees ? d[i] : -INFINITY;
+                }
+            }
+        }
+        __syncthreads();
+        // online softmax: one warp per row
+        for (int r = warp; r < RT; r += kWarps) {
+            const float x0 = sp[r * kTile + lane], x1 = sp[r * kTile + 32 + lane];
+            float m = fmaxf(x0, x1);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float old = sm[r], mn = fmaxf(old, m);
+            // a row that has seen nothing yet keeps m = -inf: every weight 0
+            const float e0 = x0 == -INFINITY ? 0.f : exp2f(x0 - mn), e1 = x1 == -INFINITY ? 0.f : exp2f(x1 - mn);
+            float l = e0 + e1;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            sp[r * kTile + lane] = e0;
+            sp[r * kTile + 32 + lane] = e1;
+            if (lane == 0) {
+                const float al = old == -INFINITY ? 0.f : exp2f(old - mn);
+                salpha[r] = al;
+                sl[r] = sl[r] * al + l;
+                sm[r] = mn;
+            }
+        }
+        __syncthreads();
+        // P V: warp -> rows; a position that a row does not see adds nothing, whatever its V holds
+        {
+            const int jl = lane / LPR, c = 4 * (lane % LPR);
+            const int row0 = RT < kWarps ? warp / KW : warp * RW, jw = RT < kWarps ? warp % KW : 0;
+#pragma unroll
+            for (int i = 0; i < RW; ++i) {
+                const float al = salpha[row0 + i];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][e] *= al;
+            }
+            const bool tail = t0 + kTile > len;
+#pragma unroll 4
+            for (int j = jw * KPW + jl; j < kTile; j += KW * KPW) {
+                const float4 v = *reinterpret_cast<const float4 *>(sv + j * D + c);
+#pragma unroll
+                for (int i = 0; i < RW; ++i) {
+                    const float p = sp[(row0 + i) * kTile + j];
+                    if (tail && p == 0.f) continue;
+                    acc[i][0] = fmaf(p, v.x, acc[i][0]);
+                    acc[i][1] = fmaf(p, v.y, acc[i][1]);
+                    acc[i][2] = fmaf(p, v.z, acc[i][2]);
+                    acc[i][3] = fmaf(p, v.w, acc[i][3]);
+                }
+            }
+        }
+    }
+    // the parts of a row (KW warps x KPW lane groups) added in order
+    {
+        constexpr int PARTS = KW * KPW;
+        const int jl = lane / LPR, c = 4 * (lane % LPR);
+        const int row0 = RT < kWarps ? warp / KW : warp * RW, jw = RT < kWarps ? warp % KW : 0;
+#pragma unroll
+        for (int i = 0; i < RW; ++i)
+            *reinterpret_cast<float4 *>(red + ((row0 + i) * PARTS + jw * KPW + jl) * D + c) =
+                make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+        __syncthreads();
+        for (int i = tid; i < RT * D; i += kThreads) {
+            const int rl = i / D, d = i % D, r = r0 + rl;
+            if (r >= rows) continue;
+            float o = 0.f;
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k) o += red[(rl * PARTS + k) * D + d];
+            float *dst = a.part + ((((int64_t)b * a.Hkv + h) * a.n_max * a.G + r) * a.S + s) * (D + 2);
+            dst[d] = o;
+            if (d == 0) {
+                dst[D] = sm[rl];
+                dst[D + 1] = sl[rl];
+            }
+        }
+    }
+}
+
+// One query row per CTA: out = sum_s acc_s 2^(m_s - M) / sum_s l_s 2^(m_s - M), in order.
+template <int D>
+__global__ void __launch_bounds__(D) tree_merge_kernel(const TreeArgs a) {
+    tc::chain_wait();
+    const int r = blockIdx.x, h = blockIdx.y, b = blockIdx.z, d = threadIdx.x;
+    int len, n;
+    const bool fits = lengths(a, b, len, n);
+    if (fits && r >= n * a.G) return;
+    const int64_t at = b * a.oseq + (int64_t)(r / a.G) * a.onode + (int64_t)(h * a.G + r % a.G) * a.ohead + d;
+    if (!fits) {
+        store_out(a, at, nanf(""));
+        return;
+    }
+    const float *src = a.part + (((int64_t)b * a.Hkv + h) * a.n_max * a.G + r) * a.S * (D + 2);
+    float mx = -INFINITY;
+    for (int s = 0; s < a.S; ++s) mx = fmaxf(mx, src[(int64_t)s * (D + 2) + D]);
+    float num = 0.f, den = 0.f;
+    for (int s = 0; s < a.S; ++s) {
+        const float *ps = src + (int64_t)s * (D + 2);
+        if (ps[D] == -INFINITY && ps[D + 1] == 0.f) continue;  // the split showed the row nothing
+        const float w = exp2f(ps[D] - mx);
+        num += ps[d] * w;
+        den += ps[D + 1] * w;
+    }
+    store_out(a, at, den == 0.f ? 0.f : num / den);
+}
+
+constexpr int kRowTiles[] = {2, 4, 8, 16};
+
+int rows_per_tile(int rows) { return rows <= 2 ? 2 : rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
+
+// Splits: enough CTAs for two on every SM, none shorter than a tile.
+int splits(int n_seq, int Hkv, int row_tiles, int total) {
+    const int tiles = (total + kTile - 1) / kTile;
+    const int64_t base = (int64_t)n_seq * Hkv * row_tiles;
+    const int64_t want = (2 * 152 + base - 1) / base;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(want, tiles));
+}
+
+template <typename KV, int D, int RT>
+cudaError_t launch_tile(const TreeArgs &a, int n_seq, cudaStream_t st) {
+    constexpr int KPW = 128 / D, KW = RT < kWarps ? kWarps / RT : 1;
+    constexpr int smem = (kTile * (D + 4) + kTile * D + RT * D + RT * kTile + RT * KW * KPW * D) * 4;
+    cudaError_t e = cudaFuncSetAttribute(tree_kernel<KV, D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_k(false, tree_kernel<KV, D, RT>, dim3(a.S, a.Hkv * a.row_tiles, n_seq), dim3(kThreads), smem, st, a);
+}
+
+template <typename KV, int D>
+cudaError_t launch_rt(const TreeArgs &a, int n_seq, int rt, cudaStream_t st) {
+    cudaError_t e = rt == 2   ? launch_tile<KV, D, 2>(a, n_seq, st)
+                    : rt == 4 ? launch_tile<KV, D, 4>(a, n_seq, st)
+                    : rt == 8 ? launch_tile<KV, D, 8>(a, n_seq, st)
+                              : launch_tile<KV, D, 16>(a, n_seq, st);
+    if (e != cudaSuccess) return e;
+    return launch_k(true, tree_merge_kernel<D>, dim3(a.n_max * a.G, a.Hkv, n_seq), dim3(D), 0, st, a);
+}
+
+}  // namespace
+
+size_t tree_attn_scratch_bytes(int n_seq, int n_kv_heads, int n_max, int n_heads, int head_dim, int max_len) {
+    const int G = n_heads / n_kv_heads, rows = n_max * G, rt = rows_per_tile(rows);
+    const int S = splits(n_seq, n_kv_heads, (rows + rt - 1) / rt, max_len + n_max);
+    return ((size_t)n_seq * n_kv_heads * rows * S * (head_dim + 2) * 4 + 255) / 256 * 256;
+}
+
+cudaError_t launch_tree_attn(const qw_kv_view &kv, const qw_tree_attention_args &t, void *scratch, cudaStream_t st) {
+    if (kv.n_seq == 0 || t.n_max == 0) return cudaSuccess;
+    TreeArgs a{};
+    a.k = (const uint8_t *)kv.k;
+    a.v = (const uint8_t *)kv.v;
+    a.ks = (const __half *)kv.k_scale;
+    a.vs = (const __half *)kv.v_scale;
+    a.seq = kv.seq_stride, a.head = kv.head_stride, a.pos = kv.pos_stride;
+    a.sseq = kv.scale_seq_stride, a.shead = kv.scale_head_stride, a.spos = kv.scale_pos_stride;
+    a.q = t.q;
+    a.out = t.out;
+    a.dtype = t.dtype;
+    a.qseq = t.q_seq_stride, a.qnode = t.q_node_stride, a.qhead = t.q_head_stride;
+    a.oseq = t.out_seq_stride, a.onode = t.out_node_stride, a.ohead = t.out_head_stride;
+    a.mask = (const unsigned long long *)t.mask;
+    a.len = t.len;
+    a.count = t.count;
+    a.n_max = t.n_max;
+    a.max_ctx = kv.max_ctx;
+    a.Hkv = kv.n_kv_heads;
+    a.G = t.n_heads / kv.n_kv_heads;
+    a.scale_log2 = t.scale * kOpsLog2e;
+    a.part = (float *)scratch;
+    const int rows = t.n_max * a.G, rt = rows_per_tile(rows);
+    a.row_tiles = (rows + rt - 1) / rt;
+    a.S = splits(kv.n_seq, kv.n_kv_heads, a.row_tiles, t.max_len + t.n_max);
+    const int D = kv.head_dim;
+    if (kv.format == QW_KV_F32)
+        return D == 128 ? launch_rt<float, 128>(a, kv.n_seq, rt, st) : launch_rt<float, 64>(a, kv.n_seq, rt, st);
+    if (kv.format == QW_KV_BF16)
+        return D == 128 ? launch_rt<__nv_bfloat16, 128>(a, kv.n_seq, rt, st)
+                        : launch_rt<__nv_bfloat16, 64>(a, kv.n_seq, rt, st);
+    return D == 128 ? launch_rt<int8_t, 128>(a, kv.n_seq, rt, st) : launch_rt<int8_t, 64>(a, kv.n_seq, rt, st);
+}
+
+}  // namespace qw

@@ -34,6 +34,7 @@ W_INT8_G32 = 1
 W_Q8Q8 = 2
 KV_F32 = 0
 KV_BF16 = 1
+KV_INT8_G32 = 2
 DEBUG_HIDDEN = 1
 DEBUG_PREFILL_BY_TOKEN = 2
 DEBUG_TRACE = 4
@@ -58,9 +59,11 @@ EXPORTS = ("qw_workspace_bytes", "qw_model_create", "qw_prefill", "qw_decode_ste
            "qw_batch_destroy", "qw_batch_reset", "qw_batch_length", "qw_batch_prefill", "qw_batch_step",
            "qw_batch_logits", "qw_batch_debug_hidden", "qw_batch_sync", "qw_checkpoint_open",
            "qw_checkpoint_close", "qw_checkpoint_last_error", "qw_checkpoint_count", "qw_checkpoint_tensor",
-           "qw_checkpoint_check", "qw_checkpoint_upload_bytes", "qw_checkpoint_upload")
+           "qw_checkpoint_check", "qw_checkpoint_upload_bytes", "qw_checkpoint_upload", "qw_kv_append", "qw_kv_read",
+           "qw_tree_attention_scratch_bytes", "qw_tree_attention", "qw_process_logits")
 DT_BF16, DT_F16, DT_F32, DT_I8, DT_Q8_0 = 0, 1, 2, 3, 4
 BATCH_MAX = 8
+TREE_NODES_MAX = 64
 
 
 class CheckpointReport(ctypes.Structure):
@@ -96,6 +99,39 @@ class Sampling(ctypes.Structure):
 
 
 SAMPLE_MAX_TOP_K = 64
+
+
+class KvViewStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("format", ctypes.c_int32), ("n_seq", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("max_ctx", ctypes.c_int32),
+                ("seq_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("pos_stride", ctypes.c_int64),
+                ("scale_seq_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64),
+                ("scale_pos_stride", ctypes.c_int64)]
+
+
+class KvRowsStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("n_max", ctypes.c_int32),
+                ("seq_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64)]
+
+
+class TreeAttentionArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("n_max", ctypes.c_int32),
+                ("n_heads", ctypes.c_int32), ("max_len", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("q_seq_stride", ctypes.c_int64), ("q_node_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("out_seq_stride", ctypes.c_int64), ("out_node_stride", ctypes.c_int64),
+                ("out_head_stride", ctypes.c_int64), ("mask", ctypes.c_void_p), ("len", ctypes.c_void_p),
+                ("count", ctypes.c_void_p)]
+
+
+class ProcessLogitsArgs(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("out", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("n_rows", ctypes.c_int32), ("vocab", ctypes.c_int32), ("row_stride", ctypes.c_int64),
+                ("out_row_stride", ctypes.c_int64), ("penalties", ctypes.c_void_p), ("history", ctypes.c_void_p),
+                ("history_range", ctypes.c_void_p), ("n_history", ctypes.c_int32), ("path", ctypes.c_void_p),
+                ("path_len", ctypes.c_int32), ("bias_ids", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("bias_range", ctypes.c_void_p), ("n_bias", ctypes.c_int32), ("mask", ctypes.c_void_p),
+                ("mask_index", ctypes.c_void_p), ("n_masks", ctypes.c_int32)]
 
 
 class Weights(ctypes.Structure):
@@ -172,6 +208,13 @@ def _lib():
             L.qw_checkpoint_upload_bytes.restype = ctypes.c_size_t
             L.qw_checkpoint_upload.argtypes = [vp, ctypes.POINTER(Config), vp, ctypes.c_size_t,
                                                ctypes.POINTER(LayerWeights), ctypes.POINTER(Weights), vp]
+            L.qw_kv_append.argtypes = [ctypes.POINTER(KvViewStruct), ctypes.POINTER(KvRowsStruct), vp, vp, vp]
+            L.qw_kv_read.argtypes = [ctypes.POINTER(KvViewStruct), ctypes.POINTER(KvRowsStruct), vp, vp, vp]
+            L.qw_tree_attention_scratch_bytes.argtypes = [ctypes.POINTER(KvViewStruct), i32, i32, i32]
+            L.qw_tree_attention_scratch_bytes.restype = ctypes.c_size_t
+            L.qw_tree_attention.argtypes = [ctypes.POINTER(KvViewStruct), ctypes.POINTER(TreeAttentionArgs), vp,
+                                            ctypes.c_size_t, vp]
+            L.qw_process_logits.argtypes = [ctypes.POINTER(ProcessLogitsArgs), vp]
             L.qw_status_string.argtypes = [ctypes.c_int]
             L.qw_status_string.restype = ctypes.c_char_p
             L.qw_abi_version.argtypes = []
@@ -304,6 +347,208 @@ def sample_logits(logits, params: Sampling, rng, token_out, history=None, scratc
     _check(_lib().qw_sample_logits(logits.data_ptr(), V, history.data_ptr() if n else None, n, ctypes.byref(params),
                                    rng.data_ptr(), token_out.data_ptr(), scratch.data_ptr(), scratch.numel(),
                                    st.cuda_stream), "qw_sample_logits")
+
+
+# ------------------------------------------------------- operators on caller-owned tensors
+
+def _dtype_code(t, what):
+    import torch
+    code = {torch.float32: DT_F32, torch.float16: DT_F16, torch.bfloat16: DT_BF16}.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{what} must be float32, float16 or bfloat16")
+    return code
+
+
+def _on(device, stream, call, what):
+    """Run call(cuda_stream) with `device` current; stream None = the device's current stream."""
+    import torch
+    if torch.cuda.current_device() == device.index:
+        rc = call((stream or torch.cuda.current_stream()).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = call((stream or torch.cuda.current_stream()).cuda_stream)
+    if rc != OK:
+        raise QwError(rc, what)
+
+
+def _want(t, what, device, dtype, shape):
+    """A contiguous tensor of this type and shape on this device; None passes as a null pointer."""
+    if t is None:
+        return None
+    if t.device != device or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+class KvView:
+    """A K/V cache in the caller's tensors, for kv_append, kv_read and tree_attention.
+
+    k, v: [n_seq, n_kv_heads, max_ctx, head_dim], float32, bfloat16, or int8 codes with
+    k_scale, v_scale: float16 [n_seq, n_kv_heads, max_ctx, head_dim / 32].  Any strides with
+    a contiguous last dimension (a layer of a larger cache, a transposed layout); k and v
+    share theirs, and so do the scales.  The view keeps the tensors alive."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        import torch
+        if not k.is_cuda:
+            raise ValueError("the cache must be CUDA tensors")
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device or k.stride() != v.stride():
+            raise ValueError("k and v must be [n_seq, n_kv_heads, max_ctx, head_dim] alike in type, strides and device")
+        if k.stride(3) != 1:
+            raise ValueError("the last dimension must be contiguous")
+        fmt = {torch.float32: KV_F32, torch.bfloat16: KV_BF16, torch.int8: KV_INT8_G32}.get(k.dtype)
+        if fmt is None:
+            raise ValueError("the cache must be float32, bfloat16 or int8")
+        s = KvViewStruct(k.data_ptr(), v.data_ptr(), None, None, fmt, k.shape[0], k.shape[1], k.shape[3], k.shape[2],
+                         k.stride(0), k.stride(1), k.stride(2), 0, 0, 0)
+        if fmt == KV_INT8_G32:
+            if k_scale is None or v_scale is None:
+                raise ValueError("an int8 cache needs k_scale and v_scale")
+            want = (*k.shape[:3], k.shape[3] // 32)
+            for t in (k_scale, v_scale):
+                if t.dtype != torch.float16 or t.shape != want or t.device != k.device or t.stride(3) != 1 \
+                        or t.stride() != k_scale.stride():
+                    raise ValueError(f"the scales must be float16 {want} tensors with the same strides, beside the codes")
+            s.k_scale, s.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+            s.scale_seq_stride, s.scale_head_stride, s.scale_pos_stride = k_scale.stride()[:3]
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("only an int8 cache has scales")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device = k.device
+        self.struct = s
+        self._ref = ctypes.byref(s)
+
+
+def _kv_rows(view, k, v, what):
+    s = view.struct
+    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride() or k.stride(3) != 1 \
+            or k.device != view.device or v.device != view.device:
+        raise ValueError(f"{what} must be two tensors [n_seq, n_kv_heads, n, head_dim] alike, beside the cache, "
+                         "with a contiguous last dimension")
+    if k.shape[0] != s.n_seq or k.shape[1] != s.n_kv_heads or k.shape[3] != s.head_dim:
+        raise ValueError(f"{what} do not match the cache's sequences, heads or head_dim")
+    return KvRowsStruct(k.data_ptr(), v.data_ptr(), _dtype_code(k, what), k.shape[2], k.stride(0), k.stride(1),
+                        k.stride(2))
+
+
+def kv_append(view: KvView, k, v, start, count=None, stream=None):
+    """qw_kv_append: rows k, v [n_seq, n_kv_heads, n, head_dim] (any strides with a contiguous last
+    dimension) into positions start[b] .. start[b] + count[b] - 1 of the cache; start, count: int32
+    [n_seq] on the device (count None: all n)."""
+    import torch
+    rows = _kv_rows(view, k, v, "the rows")
+    shape = (view.struct.n_seq,)
+    at = _want(start, "start", view.device, torch.int32, shape)
+    n = _want(count, "count", view.device, torch.int32, shape)
+    _on(view.device, stream, lambda st: _lib().qw_kv_append(view._ref, ctypes.byref(rows), at, n, st), "qw_kv_append")
+
+
+def kv_read(view: KvView, k_out, v_out, start, count=None, stream=None):
+    """qw_kv_read: positions start[b] .. start[b] + count[b] - 1 of the cache into k_out, v_out."""
+    import torch
+    rows = _kv_rows(view, k_out, v_out, "the rows")
+    shape = (view.struct.n_seq,)
+    at = _want(start, "start", view.device, torch.int32, shape)
+    n = _want(count, "count", view.device, torch.int32, shape)
+    _on(view.device, stream, lambda st: _lib().qw_kv_read(view._ref, ctypes.byref(rows), at, n, st), "qw_kv_read")
+
+
+def tree_mask(parents) -> np.ndarray:
+    """uint64 masks of a drafted tree: parents[i] < i is node i's parent node, -1 for a child of the
+    last cached token; bit j of the result's entry i is set when node i sees node j (itself and its
+    ancestors)."""
+    parents = [int(p) for p in parents]
+    if len(parents) > TREE_NODES_MAX:
+        raise ValueError(f"a tree has at most {TREE_NODES_MAX} nodes")
+    out = []
+    for i, p in enumerate(parents):
+        if not -1 <= p < i:
+            raise ValueError(f"node {i}: parent {p} is not an earlier node")
+        out.append((1 << i) | (out[p] if p >= 0 else 0))
+    return np.array(out, dtype=np.uint64)
+
+
+def tree_attention_scratch(view: KvView, n_max: int, n_heads: int, max_len: int | None = None):
+    """Workspace of tree_attention calls with these sizes (max_len None: any), one call at a time."""
+    import torch
+    n = max(_lib().qw_tree_attention_scratch_bytes(view._ref, n_max, n_heads, m)
+            for m in ([view.struct.max_ctx, 0] if max_len is None else [max_len]))
+    if n == 0 and n_max:
+        raise QwError(UNSUPPORTED_SHAPE, "qw_tree_attention_scratch_bytes")
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=view.device)
+
+
+def tree_attention(view: KvView, q, mask, lens, out=None, counts=None, max_len=None, scale=None, scratch=None,
+                   stream=None):
+    """qw_tree_attention: q [n_seq, n, n_heads, head_dim] (float32, float16 or bfloat16, any strides with a
+    contiguous last dimension), mask int64 [n_seq, n] (the bits of tree_mask), lens and counts int32
+    [n_seq] on the device.  Node i of sequence b attends to cached positions [0, lens[b]) and to the
+    drafted rows lens[b] + j that mask[b, i] names.  max_len: about the longest lens (None: the cache's
+    length); scale None: 1 / sqrt(head_dim).  Returns out (rows i >= counts[b] as they were)."""
+    import torch
+    s = view.struct
+    if q.dim() != 4 or q.shape[0] != s.n_seq or q.shape[3] != s.head_dim or q.stride(3) != 1 or q.device != view.device:
+        raise ValueError("q must be [n_seq, n, n_heads, head_dim] beside the cache, with a contiguous last dimension")
+    if out is None:
+        out = torch.zeros_like(q, memory_format=torch.contiguous_format)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or out.stride(3) != 1:
+        raise ValueError("out must be like q, with a contiguous last dimension")
+    n, heads = q.shape[1], q.shape[2]
+    if max_len is None:
+        max_len = s.max_ctx
+    if scratch is None:
+        scratch = tree_attention_scratch(view, n, heads, max_len)
+    elif scratch.device != view.device or not scratch.is_contiguous():
+        raise ValueError("scratch must be contiguous, beside the cache")
+    a = TreeAttentionArgs(q.data_ptr(), out.data_ptr(), _dtype_code(q, "q"), n, heads, max_len,
+                          s.head_dim ** -0.5 if scale is None else scale, *q.stride()[:3], *out.stride()[:3],
+                          _want(mask, "mask", view.device, torch.int64, q.shape[:2]),
+                          _want(lens, "lens", view.device, torch.int32, q.shape[:1]),
+                          _want(counts, "counts", view.device, torch.int32, q.shape[:1]))
+    _on(view.device, stream, lambda st: _lib().qw_tree_attention(view._ref, ctypes.byref(a), scratch.data_ptr(),
+                                                                 scratch.numel() * scratch.element_size(), st),
+        "qw_tree_attention")
+    return out
+
+
+def process_logits(logits, out=None, *, history=None, history_range=None, path=None, penalties=None, bias_ids=None,
+                   bias=None, bias_range=None, mask=None, mask_index=None, stream=None):
+    """qw_process_logits: repetition, presence and frequency penalties, biases and grammar masks on
+    logits [n_rows, vocab] (contiguous rows); out None works in place.  penalties float32 [n_rows, 3];
+    history int32 [n], history_range int32 [n_rows, 2], path int32 [n_rows, p]; bias_ids int32 [m],
+    bias float32 [m], bias_range int32 [n_rows, 2]; mask int32 [n_masks, ceil(vocab / 32)],
+    mask_index int32 [n_rows].  Returns out."""
+    import torch
+    if logits.dim() != 2 or not logits.is_cuda or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be CUDA [n_rows, vocab] with contiguous rows")
+    if out is None:
+        out = logits
+    elif out.shape != logits.shape or out.dtype != logits.dtype or out.device != logits.device \
+            or (out.shape[1] > 1 and out.stride(1) != 1):
+        raise ValueError("out must be like logits, with contiguous rows")
+    R, V = logits.shape
+    dev, i32 = logits.device, torch.int32
+    if (history is None) != (history_range is None):
+        raise ValueError("history and history_range go together")
+    if not (bias_ids is None) == (bias is None) == (bias_range is None):
+        raise ValueError("bias_ids, bias and bias_range go together")
+    if mask_index is not None and mask is None:
+        raise ValueError("mask_index needs mask")
+    per_row = (R, 2)
+    n_bias = 0 if bias is None else bias.numel()
+    a = ProcessLogitsArgs(
+        logits.data_ptr(), out.data_ptr(), _dtype_code(logits, "logits"), R, V, logits.stride(0), out.stride(0),
+        _want(penalties, "penalties", dev, torch.float32, (R, 3)),
+        None if history is None else _want(history, "history", dev, i32, (history.numel(),)),
+        _want(history_range, "history_range", dev, i32, per_row), 0 if history is None else history.numel(),
+        None if path is None else _want(path, "path", dev, i32, (R, path.shape[-1])),
+        0 if path is None else path.shape[-1],
+        _want(bias_ids, "bias_ids", dev, i32, (n_bias,)), _want(bias, "bias", dev, torch.float32, (n_bias,)),
+        _want(bias_range, "bias_range", dev, i32, per_row), n_bias,
+        None if mask is None else _want(mask, "mask", dev, i32, (mask.shape[0], (V + 31) // 32)),
+        _want(mask_index, "mask_index", dev, i32, (R,)), 0 if mask is None else mask.shape[0])
+    _on(dev, stream, lambda st: _lib().qw_process_logits(ctypes.byref(a), st), "qw_process_logits")
+    return out
 
 
 class Model:
