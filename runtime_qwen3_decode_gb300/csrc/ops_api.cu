@@ -32,14 +32,19 @@ int check_view(const qw_kv_view *kv) {
     if (!aligned(kv->k, 16) || !aligned(kv->v, 16) || !stride_ok(kv->seq_stride, unit) ||
         !stride_ok(kv->head_stride, unit) || !stride_ok(kv->pos_stride, unit))
         return QW_ALIGNMENT;
-    if (kv->pos_stride < kv->head_dim) return QW_INVALID_ARGUMENT;
+    // no two rows may share an address
+    if ((kv->max_ctx > 1 && kv->pos_stride < kv->head_dim) || (kv->n_kv_heads > 1 && kv->head_stride < kv->head_dim) ||
+        (kv->n_seq > 1 && kv->seq_stride < kv->head_dim))
+        return QW_INVALID_ARGUMENT;
     if (kv->format == QW_KV_INT8_G32) {
         const int64_t g = kv->head_dim / qw::kQGroup;
         if (!kv->k_scale || !kv->v_scale) return QW_INVALID_ARGUMENT;
         if (!aligned(kv->k_scale, 2 * g) || !aligned(kv->v_scale, 2 * g) || !stride_ok(kv->scale_seq_stride, g) ||
             !stride_ok(kv->scale_head_stride, g) || !stride_ok(kv->scale_pos_stride, g))
             return QW_ALIGNMENT;
-        if (kv->scale_pos_stride < g) return QW_INVALID_ARGUMENT;
+        if ((kv->max_ctx > 1 && kv->scale_pos_stride < g) || (kv->n_kv_heads > 1 && kv->scale_head_stride < g) ||
+            (kv->n_seq > 1 && kv->scale_seq_stride < g))
+            return QW_INVALID_ARGUMENT;
     }
     return QW_OK;
 }

@@ -103,6 +103,15 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const void *tmap, int x, 
         : "memory");
 }
 
+// 4-D tile load, coordinates x (innermost) to w; the rule on x as above.
+__device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int x, int y, int z, int w, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+        "%5}], [%6];" ::"r"(su32(dst)),
+        "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(su32(bar))
+        : "memory");
+}
+
 // ---------------------------------------------------------------- TMEM
 
 // Allocates ncols TMEM columns (power of two, >= 32); one whole warp executes it.
@@ -140,6 +149,24 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
 // (f16), N / 8 in bits 17-22, M / 16 in bits 24-28.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Shared-memory matrix descriptor of an MN-major, 128-byte-swizzled operand tile: the K
+// index runs over rows of 64 16-bit elements (128 B) of the M or N index, 8-row groups
+// 1024 B apart (stride offset), the next 64 elements of M or N mn_stride bytes on (leading
+// offset).  A step of 16 along K is 2048 B.
+__device__ __forceinline__ uint64_t desc_sw128_mn(uint32_t saddr, uint32_t mn_stride) {
+    uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)((mn_stride & 0x3FFFFu) >> 4) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// idesc_f16_f32 with bf16 operands (formats 1), and with B MN-major (bit 16).
+__host__ __device__ constexpr uint32_t idesc_16_f32(int M, int N, bool bf16, bool b_mn_major) {
+    return idesc_f16_f32(M, N) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn_major ? 1u << 16 : 0u);
 }
 
 // ---------------------------------------------------------------- MMA
@@ -206,6 +233,17 @@ __device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t (&v)[3
         "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
         : "memory");
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Stores 16 raw 32-bit columns of this thread's TMEM lane and waits for the store.
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
 }
 
 // Stores 32 f32 columns of this thread's TMEM lane and waits for the store.

@@ -15,8 +15,8 @@
 #include <algorithm>
 #include <cmath>
 
-#include "qw_ops.h"
 #include "tc.cuh"
+#include "tree_attn.h"
 
 namespace qw {
 namespace {
@@ -24,40 +24,6 @@ namespace {
 constexpr int kTile = 64;       // positions per tile
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-
-struct TreeArgs {
-    const uint8_t *k, *v;
-    const __half *ks, *vs;
-    int64_t seq, head, pos, sseq, shead, spos;
-    const void *q;
-    void *out;
-    int dtype;                   // of q and out
-    int64_t qseq, qnode, qhead, oseq, onode, ohead;
-    const unsigned long long *mask;
-    const int32_t *len, *count;
-    int n_max, max_ctx, Hkv, G, S, row_tiles;
-    float scale_log2;
-    float *part;                 // [n_seq][Hkv][n_max * G][S][D + 2]
-};
-
-__device__ __forceinline__ float load_q(const TreeArgs &a, int64_t at) {
-    return a.dtype == QW_DT_F32   ? reinterpret_cast<const float *>(a.q)[at]
-           : a.dtype == QW_DT_F16 ? __half2float(reinterpret_cast<const __half *>(a.q)[at])
-                                  : __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(a.q)[at]);
-}
-
-__device__ __forceinline__ void store_out(const TreeArgs &a, int64_t at, float v) {
-    if (a.dtype == QW_DT_F32) reinterpret_cast<float *>(a.out)[at] = v;
-    else if (a.dtype == QW_DT_F16) reinterpret_cast<__half *>(a.out)[at] = __float2half_rn(v);
-    else reinterpret_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(v);
-}
-
-// Whether sequence b's lengths fit its cache; if not its rows come out as NaN.
-__device__ __forceinline__ bool lengths(const TreeArgs &a, int b, int &len, int &n) {
-    len = a.len[b];
-    n = a.count ? a.count[b] : a.n_max;
-    return n >= 0 && n <= a.n_max && len >= 0 && len <= a.max_ctx - n;
-}
 
 // The split's positions: equal shares of whole tiles.
 __device__ __forceinline__ void split_range(int total, int S, int s, int &p0, int &p1) {
@@ -257,8 +223,6 @@ __global__ void __launch_bounds__(D) tree_merge_kernel(const TreeArgs a) {
     store_out(a, at, den == 0.f ? 0.f : num / den);
 }
 
-constexpr int kRowTiles[] = {2, 4, 8, 16};
-
 int rows_per_tile(int rows) { return rows <= 2 ? 2 : rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
 
 // Splits: enough CTAs for two on every SM, none shorter than a tile.
@@ -293,7 +257,8 @@ cudaError_t launch_rt(const TreeArgs &a, int n_seq, int rt, cudaStream_t st) {
 size_t tree_attn_scratch_bytes(int n_seq, int n_kv_heads, int n_max, int n_heads, int head_dim, int max_len) {
     const int G = n_heads / n_kv_heads, rows = n_max * G, rt = rows_per_tile(rows);
     const int S = splits(n_seq, n_kv_heads, (rows + rt - 1) / rt, max_len + n_max);
-    return ((size_t)n_seq * n_kv_heads * rows * S * (head_dim + 2) * 4 + 255) / 256 * 256;
+    const size_t cores = ((size_t)n_seq * n_kv_heads * rows * S * (head_dim + 2) * 4 + 255) / 256 * 256;
+    return std::max(cores, tree_tc_scratch_bytes(rows, head_dim));
 }
 
 cudaError_t launch_tree_attn(const qw_kv_view &kv, const qw_tree_attention_args &t, void *scratch, cudaStream_t st) {
@@ -319,6 +284,7 @@ cudaError_t launch_tree_attn(const qw_kv_view &kv, const qw_tree_attention_args 
     a.G = t.n_heads / kv.n_kv_heads;
     a.scale_log2 = t.scale * kOpsLog2e;
     a.part = (float *)scratch;
+    if (t.dtype != QW_DT_F32) return launch_tree_tc(a, kv, t.max_len, scratch, st);
     const int rows = t.n_max * a.G, rt = rows_per_tile(rows);
     a.row_tiles = (rows + rt - 1) / rt;
     a.S = splits(kv.n_seq, kv.n_kv_heads, a.row_tiles, t.max_len + t.n_max);

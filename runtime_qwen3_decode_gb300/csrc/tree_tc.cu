@@ -1,0 +1,934 @@
+// tree_tc.cu - attention of drafted-token trees on the tensor cores (16-bit queries).
+//
+// The query rows of a KV head (row r = node r / G, head r % G of its group) fill the 128 MMA
+// rows, so the heads of a group and the nodes of a tree share every K and V row.  Per tile of
+// 128 positions S = Q K^T (one operand in TMEM, K in shared memory), the masks and the online
+// softmax in the log2 domain, O += P V (P in TMEM over its scores, V in shared memory as it is
+// cached: the MMA takes it MN-major, so nothing is transposed).  The bound is the cache's
+// bytes: 128 x 128 x 128 MMAs, even where most of the 128 rows are empty, take 1024 cycles of a
+// tile whose bytes take 3000 (bf16) or 1600 (8 bits) cycles of an SM's share of HBM.
+//
+// Work: the tiles of all (sequence, KV head, row tile) items in a row, cut into equal shares,
+// one per CTA, whatever the lengths (each CTA finds its share from len and count).  An item
+// inside one share is finished there; of one that is cut, each CTA writes a partial (O, max,
+// sum), and the merge kernel adds them in order.
+//
+// Warps: 0 loads (TMA), 1 issues the MMAs, 2-5 copy Q into TMEM and run softmax and epilogue
+// (one row per lane); for caches that are not bf16 beside bf16 queries, 6-13 convert.  bf16
+// beside bf16: TMA writes K and V tiles straight into swizzled operand tiles, three stages each.
+// Otherwise TMA fills a ring of 16 KB chunks of raw rows, and the converters write the 16-bit
+// operand tiles, double-buffered.  8-bit rows become fp16 (code * scale rounded once, 2^-11;
+// bf16 would lose three more bits and cost twice the instructions), bf16 queries beside them
+// fp16 after division by a power of two per row, so that only elements 2^-14 below the row's
+// largest lose bits.
+//
+// What a row does not see has weight 0, but 0 x NaN is NaN in the product with V: the V
+// rows behind the sequence are zeroed, and elements of drafted rows that are not finite are
+// replaced by 0 in the operand and added to the rows that do see them at the end.
+//
+// Every wait is bounded (1 s); a CTA whose wait expired says so in its status word and the
+// merge kernel then fills every output row with NaN.
+#include <cuda.h>
+
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+
+#include "tc.cuh"
+#include "tree_attn.h"
+
+namespace qw {
+namespace {
+
+using namespace tc;
+
+enum { SRC_BF16 = 0, SRC_Q8_F16 = 1, SRC_BF16_F16 = 2, SRC_F32_F16 = 3 };
+
+constexpr int kSoftWarps = 4, kConvWarps = 8, kConvThreads = 32 * kConvWarps;
+constexpr uint32_t kColO = 256, kColQ = 448;  // TMEM: S at 0 and 128 (P over each), O, Q
+
+// TERMS: 16-bit numbers per K or V element, 2 = an fp16 and the fp16 of what it leaves.
+template <int SRC, int D, int TERMS>
+struct Cfg {
+    static constexpr bool kDirect = SRC == SRC_BF16;
+    static constexpr bool kBf16 = SRC == SRC_BF16;
+    static constexpr int kElem = SRC == SRC_Q8_F16 ? 1 : SRC == SRC_F32_F16 ? 4 : 2;
+    static constexpr int kThreads = 32 * (2 + kSoftWarps + (kDirect ? 0 : kConvWarps));
+    static constexpr int kRegion = 128 * 128;              // 128 rows x 64 16-bit dims
+    static constexpr int kTerm = kRegion * (D / 64);       // one term of a K or V operand tile
+    static constexpr int kOperand = kTerm * TERMS;
+    static constexpr int kStages = kDirect ? 3 : TERMS == 2 ? 1 : 2;
+    static constexpr int kChunkRows = 16384 / (D * kElem) < 128 ? 16384 / (D * kElem) : 128;
+    static constexpr int kChunk = kChunkRows * D * kElem;  // raw bytes per ring slot
+    static constexpr int kChunks = 128 / kChunkRows;       // per tile and plane
+    static constexpr int kRing = kDirect ? 0 : 6;
+    static constexpr int kK = 0, kV = kK + kStages * kOperand, kRaw = kV + kStages * kOperand;
+    static constexpr int kBar = kRaw + kRing * kChunk;
+    static constexpr int kBytes = kBar + 512;
+    static constexpr size_t kSmem = 1024 + kBytes;
+    static_assert(kSmem <= 227 * 1024, "shared memory budget");
+    static_assert(!kDirect || TERMS == 1, "tiles that TMA writes have one term");
+};
+
+struct TcParams {
+    TreeArgs a;
+    int n_seq, rows_max;  // rows_max: query rows per partial slot (a multiple of 32)
+    int *status;
+    float *part;          // [2 CTAs][D + 2][rows_max]
+};
+
+__device__ __forceinline__ int seq_tiles(int total) { return (total + kTcTile - 1) / kTcTile; }
+
+// Tiles of sequence b over all its items; 0 for one without nodes or that does not fit.
+__device__ __forceinline__ long long seq_work(const TcParams &p, int b) {
+    int len, n;
+    if (!lengths(p.a, b, len, n) || n == 0) return 0;
+    const int nrt = (n * p.a.G + kTcRows - 1) / kTcRows;
+    return (long long)seq_tiles(len + n) * p.a.Hkv * nrt;
+}
+
+// A CTA's share is tiles [T c / C, T (c + 1) / C).
+__device__ __forceinline__ long long share_start(long long T, int c, int C) { return T * c / C; }
+
+struct Cursor {
+    int b, h, rt, tile;
+    long long left;
+};
+
+struct Seg {
+    int b, h, r0, rows;      // rows: of the whole (sequence, KV head); this tile starts at r0
+    int t0, t1, tiles;
+    int len, n, total;
+};
+
+__device__ __forceinline__ bool next_seg(const TcParams &p, Cursor &c, Seg &s) {
+    while (c.left > 0 && c.b < p.n_seq) {
+        int len, n;
+        if (!lengths(p.a, c.b, len, n) || n == 0) {
+            ++c.b;
+            continue;
+        }
+        const int nrt = (n * p.a.G + kTcRows - 1) / kTcRows;
+        s.b = c.b, s.h = c.h, s.r0 = c.rt * kTcRows, s.rows = n * p.a.G;
+        s.len = len, s.n = n, s.total = len + n;
+        s.tiles = seq_tiles(s.total);
+        s.t0 = c.tile;
+        s.t1 = (int)min((long long)s.tiles, c.tile + c.left);
+        c.left -= s.t1 - s.t0;
+        c.tile = 0;
+        if (++c.rt == nrt) {
+            c.rt = 0;
+            if (++c.h == p.a.Hkv) {
+                c.h = 0;
+                ++c.b;
+            }
+        }
+        return true;
+    }
+    return false;
+}
+
+// One whole warp: sum of seq_work over [0, n), and where the running sum passes `at`.
+__device__ long long total_work(const TcParams &p, int n) {
+    const int lane = threadIdx.x & 31;
+    long long w = 0;
+    for (int b = lane; b < n; b += 32) w += seq_work(p, b);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+    return w;
+}
+
+__device__ Cursor find_start(const TcParams &p, long long at, long long left) {
+    const int lane = threadIdx.x & 31;
+    Cursor c{p.n_seq, 0, 0, 0, left};
+    long long before = 0;
+    for (int b0 = 0; b0 < p.n_seq; b0 += 32) {
+        const long long own = b0 + lane < p.n_seq ? seq_work(p, b0 + lane) : 0;
+        long long upto = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, before + upto > at);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            const long long rest = at - before - (__shfl_sync(0xffffffffu, upto, l) - __shfl_sync(0xffffffffu, own, l));
+            c.b = b0 + l;
+            int len, n;
+            lengths(p.a, c.b, len, n);
+            const int tiles = seq_tiles(len + n), nrt = (n * p.a.G + kTcRows - 1) / kTcRows;
+            const long long item = rest / tiles;
+            c.tile = (int)(rest % tiles);
+            c.rt = (int)(item % nrt);
+            c.h = (int)(item / nrt);
+            return c;
+        }
+        before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    c.left = 0;
+    return c;
+}
+
+__device__ __forceinline__ uint8_t *smem_base() {
+    extern __shared__ __align__(1024) uint8_t smem_tree[];
+    const uint32_t off = (1024u - (su32(smem_tree) & 1023u)) & 1023u;
+    return smem_tree + off;
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t *b, unsigned parity, volatile int *abort) {
+    int ok = 1;
+    if ((threadIdx.x & 31) == 0) ok = mbar_wait(b, parity, abort, true, kWaitLimitNs);
+    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+// 2^x on the special-function unit (ex2.approx: about 2 ulp; 2^-inf = +0).
+__device__ __forceinline__ float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    if constexpr (BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+
+// Zeroes the elements of eight packed 16-bit values that are not finite; true if there were any.
+template <bool BF16>
+__device__ __forceinline__ bool only_finite(uint4 &u) {
+    constexpr uint32_t E = BF16 ? 0x7f80u : 0x7c00u;
+    uint32_t *w = reinterpret_cast<uint32_t *>(&u);
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if ((w[i] & E) == E) w[i] &= 0xffff0000u, any = true;
+        if ((w[i] & (E << 16)) == (E << 16)) w[i] &= 0x0000ffffu, any = true;
+    }
+    return any;
+}
+
+// Eight int8 codes times an fp16 scale, each rounded once to fp16, and what that leaves (it has
+// eight bits: exact where it is not subnormal).  Byte u = code + 128 beside 0x64 is the fp16
+// number 1024 + u.
+template <int TERMS>
+__device__ __forceinline__ void widen_q8(uint2 codes, __half scale, uint4 &o, uint4 &rest) {
+    const __half2 s2 = __half2half2(scale), off = __float2half2_rn(1152.f);
+    uint32_t *ow = reinterpret_cast<uint32_t *>(&o), *rw = reinterpret_cast<uint32_t *>(&rest);
+    const uint32_t in[2] = {codes.x ^ 0x80808080u, codes.y ^ 0x80808080u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t b = __byte_perm(in[i >> 1], 0x64646464u, (i & 1) ? 0x4342u : 0x4140u);
+        const __half2 c = __hsub2(*reinterpret_cast<const __half2 *>(&b), off), h = __hmul2(c, s2);
+        ow[i] = *reinterpret_cast<const uint32_t *>(&h);
+        if constexpr (TERMS == 2) {
+            const __half2 r = __hfma2(c, s2, __hneg2(h));
+            rw[i] = *reinterpret_cast<const uint32_t *>(&r);
+        }
+    }
+}
+
+// Two f32 as fp16 pairs, and what the rounding left.
+__device__ __forceinline__ uint32_t rest2(float a, float b, uint32_t hi) {
+    const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    return pack2<false>(a - h.x, b - h.y);
+}
+
+// Raw cache elements e .. e + 7 of a row as the operand holds them, for the fix-up of values that
+// are not finite.
+template <int SRC>
+__device__ __forceinline__ float operand_value(const TreeArgs &a, const uint8_t *plane, const __half *scales, int64_t row,
+                                               int64_t srow, int d) {
+    if constexpr (SRC == SRC_Q8_F16)
+        return __half2float(__float2half_rn((float)reinterpret_cast<const int8_t *>(plane)[row + d] *
+                                            __half2float(scales[srow + d / kQGroup])));
+    else if constexpr (SRC == SRC_BF16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(plane)[row + d]);
+    else if constexpr (SRC == SRC_BF16_F16)
+        return __half2float(__float2half_rn(__bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(plane)[row + d])));
+    else return __half2float(__float2half_rn(reinterpret_cast<const float *>(plane)[row + d]));
+}
+
+template <int SRC, int D, int TERMS>
+__global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
+    tree_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const TcParams p) {
+    using C = Cfg<SRC, D, TERMS>;
+    constexpr int ST = C::kStages;
+    uint8_t *base = smem_base();
+    uint8_t *sK = base + C::kK, *sV = base + C::kV, *raw = base + C::kRaw;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(base + C::kBar);
+    uint64_t *q_tm = bars, *k_full = bars + 1, *k_empty = bars + 4, *v_full = bars + 7, *v_empty = bars + 10,
+             *s_full = bars + 13, *p_full = bars + 15, *pv_done = bars + 17, *drain = bars + 18, *r_full = bars + 19,
+             *r_empty = bars + 25;
+    Cursor *start = reinterpret_cast<Cursor *>(bars + 32);
+    int *bad_seg = reinterpret_cast<int *>(bars + 40);  // [4]: 1 + the segment that last set it
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + 42);
+    volatile int *abort = reinterpret_cast<volatile int *>(tslot + 1);
+    const TreeArgs &a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        mbar_init(q_tm, kSoftWarps);
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(&k_full[i], C::kDirect ? 1 : kConvWarps);
+            mbar_init(&k_empty[i], 1);
+            mbar_init(&v_full[i], C::kDirect ? 1 : kConvWarps);
+            mbar_init(&v_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], kSoftWarps);
+        }
+        mbar_init(pv_done, 1);
+        mbar_init(drain, 1);
+        for (int i = 0; i < C::kRing; ++i) {
+            mbar_init(&r_full[i], 1);
+            mbar_init(&r_empty[i], kConvWarps);
+        }
+        for (int i = 0; i < 4; ++i) bad_seg[i] = 0;
+        *abort = 0;
+        mbar_fence_init();
+    }
+    if (warp == 1) tmem_alloc(tslot, 512);
+    chain_wait();
+    if (warp == 2) {
+        const long long T = total_work(p, p.n_seq);
+        const long long at = share_start(T, blockIdx.x, gridDim.x), end = share_start(T, blockIdx.x + 1, gridDim.x);
+        const Cursor c = find_start(p, at, end - at);
+        if (lane == 0) *start = c;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    chain_release();
+    const uint32_t tmem = *tslot;
+    const uint32_t tO = tmem + kColO;
+    Cursor cur = *start;
+    Seg s;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---- loads
+            bool ok = true;
+            if constexpr (C::kDirect) {
+                int kp[ST], vp[ST];
+                for (int i = 0; i < ST; ++i) kp[i] = vp[i] = -1;
+                int it = 0;
+                while (ok && next_seg(p, cur, s)) {
+                    for (int t = s.t0; ok && t < s.t1; ++t, ++it) {
+                        const int st = it % ST;
+                        const unsigned ph = (unsigned)(it / ST) & 1u;
+                        if (!mbar_wait(&k_empty[st], ph ^ 1u, abort, true, kWaitLimitNs)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_expect_tx(&k_full[st], C::kOperand);
+                        for (int r = 0; r < D / 64; ++r)
+                            tma_load_4d(sK + st * C::kOperand + r * C::kRegion, &tk, 64 * r, t * kTcTile, s.h, s.b, &k_full[st]);
+                        kp[st] = (int)ph;
+                        if (!mbar_wait(&v_empty[st], ph ^ 1u, abort, true, kWaitLimitNs)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_expect_tx(&v_full[st], C::kOperand);
+                        for (int r = 0; r < D / 64; ++r)
+                            tma_load_4d(sV + st * C::kOperand + r * C::kRegion, &tv, 64 * r, t * kTcTile, s.h, s.b, &v_full[st]);
+                        vp[st] = (int)ph;
+                    }
+                }
+                if (!ok) *abort = 1;
+                // no copy may land in shared memory after this CTA has exited, whoever gave up
+                for (int i = 0; i < ST; ++i) {
+                    if (kp[i] >= 0) mbar_wait(&k_full[i], (unsigned)kp[i], abort, false, kWaitLimitNs);
+                    if (vp[i] >= 0) mbar_wait(&v_full[i], (unsigned)vp[i], abort, false, kWaitLimitNs);
+                }
+            } else {
+                int rp[6] = {-1, -1, -1, -1, -1, -1};
+                int slot = 0;
+                unsigned ph = 0;
+                while (ok && next_seg(p, cur, s)) {
+                    for (int t = s.t0; ok && t < s.t1; ++t)
+                        for (int ch = 0; ch < 2 * C::kChunks; ++ch) {
+                            if (!mbar_wait(&r_empty[slot], ph ^ 1u, abort, true, kWaitLimitNs)) {
+                                ok = false;
+                                break;
+                            }
+                            mbar_expect_tx(&r_full[slot], C::kChunk);
+                            tma_load_4d(raw + slot * C::kChunk, ch < C::kChunks ? &tk : &tv, 0,
+                                        t * kTcTile + (ch % C::kChunks) * C::kChunkRows, s.h, s.b, &r_full[slot]);
+                            rp[slot] = (int)ph;
+                            if (++slot == C::kRing) slot = 0, ph ^= 1u;
+                        }
+                }
+                if (!ok) *abort = 1;
+                for (int i = 0; i < C::kRing; ++i)
+                    if (rp[i] >= 0) mbar_wait(&r_full[i], (unsigned)rp[i], abort, false, kWaitLimitNs);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ---- MMAs.  S of the segment's next tile is issued before P V of this one, so that the
+            // tensor core computes it during this tile's softmax.
+            constexpr uint32_t idS = idesc_16_f32(128, 128, C::kBf16, false), idO = idesc_16_f32(128, D, C::kBf16, true);
+            bool ok = true;
+            int it = 0, seg = 0;  // it: tiles before this segment
+            while (ok && next_seg(p, cur, s)) {
+                const int nt = s.t1 - s.t0;
+                ok = mbar_wait(q_tm, (unsigned)seg & 1u, abort, true, kWaitLimitNs);
+                for (int j = -1; ok && j < nt; ++j) {
+                    if (j + 1 < nt) {
+                        const int jn = it + j + 1, st = jn % ST;
+                        if (!mbar_wait(&k_full[st], (unsigned)(jn / ST) & 1u, abort, true, kWaitLimitNs)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t sk = su32(sK + st * C::kOperand);
+#pragma unroll
+                        for (int k = 0; k < TERMS * (D / 16); ++k) {
+                            const int term = k / (D / 16), kk = k % (D / 16);
+                            mma_f16_ts(tmem + 128u * (jn & 1), tmem + kColQ + 8u * kk,
+                                       desc_sw128(sk + term * C::kTerm + (kk >> 2) * C::kRegion) + 2u * (kk & 3), idS, k != 0);
+                        }
+                        mma_commit(&s_full[jn & 1]);
+                        mma_commit(&k_empty[st]);
+                    }
+                    if (j >= 0) {
+                        const int jj = it + j, st = jj % ST;
+                        if (!mbar_wait(&v_full[st], (unsigned)(jj / ST) & 1u, abort, true, kWaitLimitNs) ||
+                            !mbar_wait(&p_full[jj & 1], (unsigned)(jj >> 1) & 1u, abort, true, kWaitLimitNs)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t sv = su32(sV + st * C::kOperand);
+#pragma unroll
+                        for (int k = 0; k < TERMS * (kTcTile / 16); ++k) {
+                            const int term = k / (kTcTile / 16), kk = k % (kTcTile / 16);
+                            mma_f16_ts(tO, tmem + 128u * (jj & 1) + 8u * kk,
+                                       desc_sw128_mn(sv + term * C::kTerm + 2048u * kk, C::kRegion), idO, j > 0 || k > 0);
+                        }
+                        mma_commit(pv_done);
+                        mma_commit(&v_empty[st]);
+                    }
+                }
+                it += nt;
+                ++seg;
+            }
+            if (!ok) *abort = 1;
+            mma_commit(drain);  // every MMA completes before TMEM is released
+            mbar_wait(drain, 0, abort, false, kWaitLimitNs);
+        }
+    } else if (warp < 2 + kSoftWarps) {
+        // ---- softmax and epilogue: TMEM lane quarter q = warp % 4, one query row per lane
+        const int q = warp & 3, r = 32 * q + lane;
+        const uint32_t lb = (uint32_t)(32 * q) << 16;
+        bool ok = true;
+        int it = 0, seg = 0;
+        while (ok && next_seg(p, cur, s)) {
+            const int row = s.r0 + r, nt = s.t1 - s.t0;
+            const bool live = row < s.rows;
+            const bool warp_live = s.r0 + 32 * q < s.rows;
+            const int node = live ? row / a.G : 0, head = s.h * a.G + (live ? row % a.G : 0);
+            unsigned long long mask = live ? a.mask[(int64_t)s.b * a.n_max + node] : 0ull;
+            if (s.n < 64) mask &= (1ull << s.n) - 1ull;
+            float sc = fabsf(a.scale_log2);
+            // the row of Q, 16-bit pairs in K order, into TMEM; a negative scale flips its signs
+            if (warp_live) {
+                const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+                const uint16_t *src = reinterpret_cast<const uint16_t *>(a.q) + s.b * a.qseq + node * a.qnode + head * a.qhead;
+                float up = 1.f;
+                if ((SRC == SRC_Q8_F16 || SRC == SRC_F32_F16) && a.dtype == QW_DT_BF16) {
+                    float amax = 0.f;
+#pragma unroll 4
+                    for (int c = 0; c < D / 8; ++c) {
+                        const uint4 u = reinterpret_cast<const uint4 *>(src)[c];
+                        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 f = __bfloat1622float2(h[i]);
+                            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+                        }
+                    }
+                    // 2^e <= amax < 2^(e + 1): the row is divided by 2^e; e is kept where 2^-e is normal
+                    const int e = min(max((int)((__float_as_uint(amax) >> 23) & 255u) - 127, -126), 126);
+                    if (amax > 0.f && amax < INFINITY) {
+                        up = __uint_as_float((uint32_t)(127 - e) << 23);
+                        sc *= __uint_as_float((uint32_t)(127 + e) << 23);
+                    }
+                }
+#pragma unroll
+                for (int hf = 0; hf < D / 64; ++hf) {
+                    uint32_t qv[32];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        uint4 u = reinterpret_cast<const uint4 *>(src)[8 * hf + c];
+                        uint32_t *w = reinterpret_cast<uint32_t *>(&u);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if ((SRC == SRC_Q8_F16 || SRC == SRC_F32_F16) && a.dtype == QW_DT_BF16) {
+                                const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]));
+                                w[i] = pack2<false>(f.x * up, f.y * up);
+                            }
+                            qv[4 * c + i] = live && sc != 0.f ? w[i] ^ flip : 0u;
+                        }
+                    }
+                    tmem_st32u(tmem + lb + kColQ + 32u * hf, qv);
+                }
+            }
+            if (sc == 0.f) sc = 1.f;  // a scale of 0: the scores of a zero query
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_tm);
+            float m_used = -INFINITY, l = 0.f;
+            for (int j = 0; ok && j < nt; ++j) {
+                const int jj = it + j, b = jj & 1;
+                if (!warp_wait(&s_full[b], (unsigned)(jj >> 1) & 1u, abort)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const int first = (s.t0 + j) * kTcTile;
+                const bool tail = first + kTcTile > s.len;
+                const uint32_t tS = tmem + lb + 128u * b;
+                if (warp_live) {
+                    // columns of a 32-column block that the row sees, one bit each
+                    uint32_t vis[4];
+                    float mb = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float v[32];
+                        tmem_ld32(tS + 32u * c, v);
+                        if (tail) {
+                            const int off = first + 32 * c - s.len;  // drafted index of the block's first column
+                            vis[c] = off <= -32   ? 0xffffffffu
+                                     : off >= 64  ? 0u
+                                     : off >= 0   ? (uint32_t)(mask >> off)
+                                                  : (uint32_t)(mask << -off) | ((1u << -off) - 1u);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) mb = fmaxf(mb, (vis[c] >> i) & 1u ? v[i] : -INFINITY);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) mb = fmaxf(mb, v[i]);
+                        }
+                    }
+                    mb *= sc;
+                    const bool resc = mb > m_used + 8.f;
+                    const float m_new = resc ? mb : m_used;
+                    const float factor = resc ? fast_exp2(m_used - m_new) : 1.f;
+                    // O must hold the previous tile's product before it is rescaled
+                    if (j > 0 && __any_sync(0xffffffffu, resc)) {
+                        if (!warp_wait(pv_done, (unsigned)(jj - 1) & 1u, abort)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            float o[32];
+                            tmem_ld32(tO + lb + 32u * c, o);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] *= factor;
+                            tmem_st32(tO + lb + 32u * c, o);
+                        }
+                    }
+                    l *= factor;
+                    m_used = m_new;
+                    const float mm = m_used == -INFINITY ? 0.f : m_used;  // nothing seen yet: every weight 2^-inf
+                    // P over the scores: block c's 16 columns end before block c + 1's scores begin
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float v[32];
+                        tmem_ld32(tS + 32u * c, v);
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float e0 = fast_exp2(fmaf(v[2 * i], sc, -mm)), e1 = fast_exp2(fmaf(v[2 * i + 1], sc, -mm));
+                            if (tail) {
+                                e0 = (vis[c] >> (2 * i)) & 1u ? e0 : 0.f;
+                                e1 = (vis[c] >> (2 * i + 1)) & 1u ? e1 : 0.f;
+                            }
+                            l += e0;
+                            l += e1;
+                            pk[i] = pack2<C::kBf16>(e0, e1);
+                        }
+                        tmem_st16u(tS + 16u * c, pk);
+                    }
+                }
+                if constexpr (C::kDirect) {
+                    // the tile's V rows behind the sequence, and what is not finite in the drafted rows: one
+                    // position per lane of the four warps
+                    if (tail) {
+                        const int st = jj % ST;
+                        if (!warp_wait(&v_full[st], (unsigned)(jj / ST) & 1u, abort)) {
+                            ok = false;
+                            break;
+                        }
+                        const int pos = first + r;
+                        bool any = false;
+                        if (pos >= s.len) {
+                            for (int c = 0; c < D / 8; ++c) {
+                                uint4 *w = reinterpret_cast<uint4 *>(sV + st * C::kOperand + (c >> 3) * C::kRegion + swz128(r, c & 7));
+                                uint4 u = pos < s.total ? *w : make_uint4(0u, 0u, 0u, 0u);
+                                const bool hit = only_finite<true>(u);
+                                if (hit || pos >= s.total) *w = u;
+                                any |= hit;
+                            }
+                        }
+                        if (any) bad_seg[seg & 3] = seg + 1;
+                        fence_async_shared();
+                    }
+                }
+                // Every warp sees each product finish in turn: a wait on a parity must not be two phases
+                // behind.  One barrier per buffer for P: a warp without live rows runs ahead, but
+                // reaches the same buffer again only after the product that all four released.
+                if (jj > 0 && !warp_wait(pv_done, (unsigned)(jj - 1) & 1u, abort)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[b]);
+            }
+            if (ok && !warp_wait(pv_done, (unsigned)(it + nt - 1) & 1u, abort)) ok = false;
+            if (ok && warp_live) {
+                tc_fence_after();
+                const bool whole = s.t0 == 0 && s.t1 == s.tiles;
+                const bool bad = *reinterpret_cast<volatile int *>(&bad_seg[seg & 3]) == seg + 1;
+                const float inv = whole ? (l == 0.f ? 0.f : 1.0f / l) : 1.f;
+                float *part = p.part + (size_t)(2 * blockIdx.x + (s.t0 > 0 ? 0 : 1)) * (D + 2) * p.rows_max + r;
+                const int64_t at = s.b * a.oseq + node * a.onode + head * a.ohead;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[32];
+                    tmem_ld32(tO + lb + 32u * c, o);
+                    if (bad && live) {
+                        const int j0 = max(s.t0 * kTcTile - s.len, 0), j1 = min(s.t1 * kTcTile, s.total) - s.len;
+                        for (int jx = j0; jx < j1; ++jx) {
+                            if (!((mask >> jx) & 1ull)) continue;
+                            const int64_t vr = s.b * a.seq + s.h * a.head + (int64_t)(s.len + jx) * a.pos;
+                            const int64_t sr = s.b * a.sseq + s.h * a.shead + (int64_t)(s.len + jx) * a.spos;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                const float v = operand_value<SRC>(a, a.v, a.vs, vr, sr, 32 * c + i);
+                                if (!isfinite(v)) o[i] += v;
+                            }
+                        }
+                    }
+                    if (!live) continue;
+                    if (!whole) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) part[(size_t)(32 * c + i) * p.rows_max] = o[i];
+                        continue;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float w[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) w[e] = l == 0.f ? 0.f : o[8 * i + e] * inv;
+                        if (a.dtype == QW_DT_F16) store8(reinterpret_cast<__half *>(a.out) + at + 32 * c + 8 * i, w);
+                        else store8(reinterpret_cast<__nv_bfloat16 *>(a.out) + at + 32 * c + 8 * i, w);
+                    }
+                }
+                if (!whole && live) {
+                    part[(size_t)D * p.rows_max] = m_used;
+                    part[(size_t)(D + 1) * p.rows_max] = l;
+                }
+                tc_fence_before();
+            }
+            it += nt;
+            ++seg;
+        }
+        if (!ok && lane == 0) *abort = 1;
+    } else if constexpr (!C::kDirect) {
+        // ---- converters: unit = eight elements of a row; a chunk's units over 256 threads
+        constexpr int UPR = D / 8, U = C::kChunkRows * UPR / kConvThreads;  // units per row; per thread and chunk
+        static_assert(U * kConvThreads == C::kChunkRows * UPR, "whole units per thread");
+        const int ct = threadIdx.x - 32 * (2 + kSoftWarps);
+        const int c = ct % UPR, row0 = ct / UPR;
+        constexpr int RSTEP = kConvThreads / UPR;
+        bool ok = true;
+        int it = 0, seg = 0, slot = 0;
+        unsigned ph = 0;
+        while (ok && next_seg(p, cur, s)) {
+            const __half *ksc = a.ks + s.b * a.sseq + s.h * a.shead + c / 4, *vsc = a.vs + s.b * a.sseq + s.h * a.shead + c / 4;
+            // scales of the chunk that follows the one in hand: their latency hides behind its conversion
+            __half next[U];
+            auto fetch = [&](int i) {  // chunk i of the segment
+                if constexpr (SRC == SRC_Q8_F16) {
+                    const __half *src = i & 1 ? vsc : ksc;
+                    const int pos0 = (s.t0 + (i >> 1)) * kTcTile + row0;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int pos = pos0 + RSTEP * u;
+                        next[u] = pos < s.total ? src[(int64_t)pos * a.spos] : __half(0);
+                    }
+                }
+            };
+            const int chunks = (s.t1 - s.t0) * 2 * C::kChunks;
+            static_assert(SRC != SRC_Q8_F16 || C::kChunks == 1, "an 8-bit tile is one chunk per plane");
+            fetch(0);
+            for (int t = s.t0, i = 0; ok && t < s.t1; ++t, ++it) {
+                const int st = it % ST;
+                const unsigned sph = (unsigned)(it / ST) & 1u;
+                const bool tail = (t + 1) * kTcTile > s.len;
+                for (int ch = 0; ch < 2 * C::kChunks; ++ch, ++i) {
+                    const bool is_v = ch >= C::kChunks;
+                    const int crow = (ch % C::kChunks) * C::kChunkRows;
+                    __half sc[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) sc[u] = next[u];
+                    if (i + 1 < chunks) fetch(i + 1);
+                    if ((ch % C::kChunks == 0 && !warp_wait(is_v ? &v_empty[st] : &k_empty[st], sph ^ 1u, abort)) ||
+                        !warp_wait(&r_full[slot], ph, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint8_t *src = raw + slot * C::kChunk;
+                    uint8_t *dst = (is_v ? sV : sK) + st * C::kOperand + (c >> 3) * C::kRegion;
+                    bool any = false;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int row = row0 + RSTEP * u;
+                        uint4 o, rest = make_uint4(0u, 0u, 0u, 0u);
+                        if constexpr (SRC == SRC_Q8_F16) {
+                            widen_q8<TERMS>(*reinterpret_cast<const uint2 *>(src + row * D + 8 * c), sc[u], o, rest);
+                        } else {
+                            float v[8];
+                            if constexpr (C::kElem == 2) load8(reinterpret_cast<const __nv_bfloat16 *>(src) + row * D + 8 * c, v);
+                            else load8(reinterpret_cast<const float *>(src) + row * D + 8 * c, v);
+                            o = make_uint4(pack2<false>(v[0], v[1]), pack2<false>(v[2], v[3]), pack2<false>(v[4], v[5]),
+                                           pack2<false>(v[6], v[7]));
+                            if constexpr (TERMS == 2)
+                                rest = make_uint4(rest2(v[0], v[1], o.x), rest2(v[2], v[3], o.y), rest2(v[4], v[5], o.z),
+                                                  rest2(v[6], v[7], o.w));
+                        }
+                        if (tail && is_v) {
+                            const int pos = t * kTcTile + crow + row;
+                            if (pos >= s.total) o = rest = make_uint4(0u, 0u, 0u, 0u);
+                            else if (pos >= s.len && only_finite<false>(o)) {
+                                any = true;
+                                only_finite<false>(rest);  // not finite where o was not
+                            }
+                        }
+                        uint8_t *at = dst + swz128(crow + row, c & 7);
+                        *reinterpret_cast<uint4 *>(at) = o;
+                        if constexpr (TERMS == 2) *reinterpret_cast<uint4 *>(at + C::kTerm) = rest;
+                    }
+                    if (any) bad_seg[seg & 3] = seg + 1;
+                    fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&r_empty[slot]);
+                        if (ch % C::kChunks == C::kChunks - 1) mbar_arrive(is_v ? &v_full[st] : &k_full[st]);
+                    }
+                    if (++slot == C::kRing) slot = 0, ph ^= 1u;
+                }
+            }
+            ++seg;
+        }
+        if (!ok && lane == 0) *abort = 1;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    if (threadIdx.x == 0) p.status[blockIdx.x] = *abort;
+}
+
+// Merge of the items that were cut: thread = (row, four dims) of one (row tile, KV head, sequence).
+// The partials lie row-fastest, so a warp's loads are runs of neighbours, and the loads of
+// kMergeBatch partials are in flight at once: this kernel is nothing but their latency.  Also
+// fills the rows of sequences that do not fit with NaN, and every row if a CTA gave up.
+constexpr int kMergeThreads = 256;
+constexpr int kMergeBatch = 6;
+
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) tree_tc_merge_kernel(const TcParams p, int ctas) {
+    const TreeArgs &a = p.a;
+    __shared__ long long sh_before[kMergeThreads / 32], sh_total[kMergeThreads / 32];
+    const int nrt_max = (a.n_max * a.G + kTcRows - 1) / kTcRows;
+    const int rt = blockIdx.x % nrt_max, h = blockIdx.x / nrt_max, b = blockIdx.y;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    chain_wait();
+    int len, n;
+    const bool fits = lengths(a, b, len, n);
+    const int rows = (fits ? n : a.n_max) * a.G, r0 = rt * kTcRows;
+    const int nr = min(kTcRows, rows - r0);
+    const int e0 = blockIdx.z * kMergeThreads;  // this CTA's first (row, four dims)
+    if (e0 >= nr * (D / 4)) return;
+    int gave_up = 0;
+    for (int i = tid; i < ctas; i += kMergeThreads) gave_up |= p.status[i];
+    long long before = 0, total = 0;
+    for (int i = tid; i < p.n_seq; i += kMergeThreads) {
+        const long long w = seq_work(p, i);
+        total += w;
+        if (i < b) before += w;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+    }
+    if (lane == 0) sh_before[warp] = before, sh_total[warp] = total;
+    gave_up = __syncthreads_or(gave_up);
+    const int e = e0 + tid, rl = e % nr, dq = e / nr, r = r0 + rl;
+    if (dq >= D / 4) return;
+    const int64_t at = b * a.oseq + (int64_t)(r / a.G) * a.onode + (int64_t)(h * a.G + r % a.G) * a.ohead + 4 * dq;
+    if (!fits || gave_up) {
+        for (int i = 0; i < 4; ++i) store_out(a, at + i, nanf(""));
+        return;
+    }
+    before = total = 0;
+    for (int i = 0; i < kMergeThreads / 32; ++i) before += sh_before[i], total += sh_total[i];
+    const int nrt = (n * a.G + kTcRows - 1) / kTcRows, tiles = seq_tiles(len + n);
+    const long long t0 = before + ((long long)h * nrt + rt) * tiles, t1 = t0 + tiles;
+    // owner of tile t: the largest c with T c / C <= t
+    const int c0 = (int)(((t0 + 1) * ctas - 1) / total), c1 = (int)((t1 * ctas - 1) / total);
+    if (c0 == c1) return;  // finished by its one CTA
+    // c0 holds the item's first tile: its second slot; the later CTAs begin inside the item: their
+    // first.  Where there are more CTAs than tiles some shares are empty.
+    const size_t slot = (size_t)(D + 2) * p.rows_max;
+    const bool gaps = total < ctas;
+    auto partial = [&](int c) { return p.part + (size_t)(2 * c + (c == c0 ? 1 : 0)) * slot + rl; };
+    auto holds = [&](int c) { return c <= c1 && !(gaps && share_start(total, c, ctas) == share_start(total, c + 1, ctas)); };
+    float mx = -INFINITY;
+    for (int c = c0; c <= c1; c += kMergeBatch) {
+        float m[kMergeBatch];
+#pragma unroll
+        for (int i = 0; i < kMergeBatch; ++i) m[i] = holds(c + i) ? partial(c + i)[(size_t)D * p.rows_max] : -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kMergeBatch; ++i) mx = fmaxf(mx, m[i]);
+    }
+    float num[4] = {0.f, 0.f, 0.f, 0.f}, den = 0.f;
+    for (int c = c0; c <= c1; c += kMergeBatch) {
+        float m[kMergeBatch], l[kMergeBatch], v[kMergeBatch][4];
+#pragma unroll
+        for (int i = 0; i < kMergeBatch; ++i) {
+            const bool is = holds(c + i);
+            const float *src = partial(c + i);
+            m[i] = is ? src[(size_t)D * p.rows_max] : -INFINITY;
+            l[i] = is ? src[(size_t)(D + 1) * p.rows_max] : 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[i][k] = is ? src[(size_t)(4 * dq + k) * p.rows_max] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kMergeBatch; ++i) {
+            if (m[i] == -INFINITY && l[i] == 0.f) continue;  // the share showed the row nothing
+            const float w = exp2f(m[i] - mx);
+            den += l[i] * w;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) num[k] += v[i][k] * w;
+        }
+    }
+    if (den == 0.f) den = 1.f;  // a row that sees nothing: 0
+#pragma unroll
+    for (int k = 0; k < 4; ++k) num[k] /= den;
+    uint2 o;
+    if (a.dtype == QW_DT_F16) o = make_uint2(pack2<false>(num[0], num[1]), pack2<false>(num[2], num[3]));
+    else o = make_uint2(pack2<true>(num[0], num[1]), pack2<true>(num[2], num[3]));
+    *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(a.out) + at) = o;
+}
+
+// ---------------------------------------------------------------- host side
+
+typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                             const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encoder() {
+    static EncodeFn fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return (EncodeFn)f;
+    }();
+    return fn;
+}
+
+// Map of one plane of the cache, [seq][head][pos][dim] with its strides, read in boxes of
+// box_rows positions and box_dims elements.
+bool plane_map(CUtensorMap *m, const void *ptr, const qw_kv_view &kv, CUtensorMapDataType type, int elem, int box_dims,
+               int box_rows, bool swizzle) {
+    const EncodeFn enc = encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)kv.head_dim, (cuuint64_t)kv.max_ctx, (cuuint64_t)kv.n_kv_heads, (cuuint64_t)kv.n_seq};
+    // the stride of a dimension of one is never used, but has to be valid
+    const cuuint64_t row = (cuuint64_t)kv.head_dim * elem;
+    const cuuint64_t strides[3] = {kv.max_ctx > 1 ? (cuuint64_t)kv.pos_stride * elem : row,
+                                   kv.n_kv_heads > 1 ? (cuuint64_t)kv.head_stride * elem : row,
+                                   kv.n_seq > 1 ? (cuuint64_t)kv.seq_stride * elem : row};
+    const cuuint32_t box[4] = {(cuuint32_t)box_dims, (cuuint32_t)box_rows, 1, 1};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return enc(m, type, 4, const_cast<void *>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int slot_rows(int rows) { return std::min(kTcRows, (rows + 31) / 32 * 32); }
+
+template <int SRC, int D, int TERMS>
+cudaError_t launch_src(const TcParams &p, const qw_kv_view &kv, int ctas, cudaStream_t st) {
+    using C = Cfg<SRC, D, TERMS>;
+    CUtensorMap mk, mv;
+    const CUtensorMapDataType type = C::kElem == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : C::kElem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                     : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    const int dims = C::kDirect ? 64 : D, rows = C::kDirect ? kTcTile : C::kChunkRows;
+    if (!plane_map(&mk, kv.k, kv, type, C::kElem, dims, rows, C::kDirect) ||
+        !plane_map(&mv, kv.v, kv, type, C::kElem, dims, rows, C::kDirect))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel<SRC, D, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    if (e != cudaSuccess) return e;
+    e = launch_k(false, tree_tc_kernel<SRC, D, TERMS>, dim3(ctas), dim3(C::kThreads), C::kSmem, st, mk, mv, p);
+    if (e != cudaSuccess) return e;
+    const int nrt = (p.a.n_max * p.a.G + kTcRows - 1) / kTcRows;
+    const int units = std::min(kTcRows, p.a.n_max * p.a.G) * (D / 4);
+    return launch_k(true, tree_tc_merge_kernel<D>, dim3(nrt * p.a.Hkv, p.n_seq, (units + kMergeThreads - 1) / kMergeThreads),
+                    dim3(kMergeThreads), 0, st, p, ctas);
+}
+
+// 16-bit results next to fp16 operands: beside bf16 queries one rounding of K and V (2^-11) drowns in
+// the result's own (2^-8); beside fp16 queries it would be most of the error (rounded scores alone
+// left a relative error of 5.5e-4 where the result's rounding leaves 2.1e-4), so K and V
+// that fp16 does not hold exactly come as two terms.
+template <int D>
+cudaError_t launch_dim(const TcParams &p, const qw_kv_view &kv, int ctas, cudaStream_t st) {
+    const bool f16 = p.a.dtype == QW_DT_F16;
+    if (kv.format == QW_KV_INT8_G32)
+        return f16 ? launch_src<SRC_Q8_F16, D, 2>(p, kv, ctas, st) : launch_src<SRC_Q8_F16, D, 1>(p, kv, ctas, st);
+    if (kv.format == QW_KV_BF16)
+        return f16 ? launch_src<SRC_BF16_F16, D, 1>(p, kv, ctas, st) : launch_src<SRC_BF16, D, 1>(p, kv, ctas, st);
+    return f16 ? launch_src<SRC_F32_F16, D, 2>(p, kv, ctas, st) : launch_src<SRC_F32_F16, D, 1>(p, kv, ctas, st);
+}
+
+}  // namespace
+
+size_t tree_tc_scratch_bytes(int rows, int head_dim) {
+    return kTcStatusBytes + (size_t)2 * kTcCtas * (head_dim + 2) * slot_rows(rows) * 4;
+}
+
+cudaError_t launch_tree_tc(const TreeArgs &a, const qw_kv_view &kv, int max_len, void *scratch, cudaStream_t st) {
+    TcParams p{};
+    p.a = a;
+    p.n_seq = kv.n_seq;
+    p.rows_max = slot_rows(a.n_max * a.G);
+    p.status = (int *)scratch;
+    p.part = (float *)((uint8_t *)scratch + kTcStatusBytes);
+    const int nrt = (a.n_max * a.G + kTcRows - 1) / kTcRows;
+    const long long tiles = (long long)kv.n_seq * kv.n_kv_heads * nrt * ((max_len + a.n_max + kTcTile - 1) / kTcTile);
+    const int ctas = (int)std::min<long long>(kTcCtas, tiles);
+    return kv.head_dim == 128 ? launch_dim<128>(p, kv, ctas, st) : launch_dim<64>(p, kv, ctas, st);
+}
+
+}  // namespace qw

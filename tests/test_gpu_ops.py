@@ -282,6 +282,19 @@ def test_tree_longer_than_the_given_bound(qw, dt, kind):
     run_tree(qw, 2, 2, 2, 128, 5, [700, 3], None, dt, kind, max_len=700)
 
 
+@pytest.mark.parametrize("dt,kind", TYPES)
+def test_tree_long_contexts_of_many_tiles(qw, dt, kind):
+    # every CTA works through several tiles of several items, whole and cut ones
+    run_tree(qw, 3, 8, 2, 128, 21, [9000, 1, 4321], [21, 20, 3], dt, kind, ctx=9100)
+
+
+@pytest.mark.parametrize("dt,kind", [(F32, "int8"), (BF16, "bf16"), (F16, "int8")])
+def test_tree_more_sequences_than_a_warp(qw, dt, kind):
+    rng = np.random.default_rng(5)
+    lens, counts = rng.integers(0, 500, 70).tolist(), rng.integers(0, 5, 70).tolist()
+    run_tree(qw, 70, 2, 2, 64, 4, lens, counts, dt, kind)
+
+
 def test_tree_one_node_is_decode_attention(qw):
     # a chain of one: softmax over the cache and the node's own row
     run_tree(qw, 8, 8, 2, 128, 1, [511, 0, 1, 130, 200, 64, 65, 400], None, F32, "f32")
