@@ -189,6 +189,15 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
+// The columns of a 32-column block that a row sees, one bit each: drafted index `off` of its first
+// column; earlier positions are cached ones, which every row sees.
+__device__ __forceinline__ uint32_t visible(unsigned long long mask, int off) {
+    return off <= -32 ? 0xffffffffu
+           : off >= 64 ? 0u
+           : off >= 0 ? (uint32_t)(mask >> off)
+                      : (uint32_t)(mask << -off) | ((1u << -off) - 1u);
+}
+
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     if constexpr (BF16) {
@@ -218,10 +227,10 @@ __device__ __forceinline__ bool only_finite(uint4 &u) {
 // eight bits: exact where it is not subnormal).  Byte u = code + 128 beside 0x64 is the fp16
 // number 1024 + u.
 template <int TERMS>
-__device__ __forceinline__ void widen_q8(uint2 codes, __half scale, uint4 &o, uint4 &rest) {
-    const __half2 s2 = __half2half2(scale), off = __float2half2_rn(1152.f);
+__device__ __forceinline__ void widen_q8(uint32_t c0, uint32_t c1, __half2 s2, uint4 &o, uint4 &rest) {
+    const __half2 off = __float2half2_rn(1152.f);
     uint32_t *ow = reinterpret_cast<uint32_t *>(&o), *rw = reinterpret_cast<uint32_t *>(&rest);
-    const uint32_t in[2] = {codes.x ^ 0x80808080u, codes.y ^ 0x80808080u};
+    const uint32_t in[2] = {c0 ^ 0x80808080u, c1 ^ 0x80808080u};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t b = __byte_perm(in[i >> 1], 0x64646464u, (i & 1) ? 0x4342u : 0x4140u);
@@ -497,22 +506,23 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                 const bool tail = first + kTcTile > s.len;
                 const uint32_t tS = tmem + lb + 128u * b;
                 if (warp_live) {
-                    // columns of a 32-column block that the row sees, one bit each
-                    uint32_t vis[4];
+                    // blocks of 32 columns, rolled: unrolled over the tile the code outgrows the
+                    // instruction cache that all roles share
                     float mb = -INFINITY;
+                    if (tail) {
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t vis = visible(mask, first + 32 * c - s.len);
+                            float v[32];
+                            tmem_ld32(tS + 32u * c, v);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float v[32];
-                        tmem_ld32(tS + 32u * c, v);
-                        if (tail) {
-                            const int off = first + 32 * c - s.len;  // drafted index of the block's first column
-                            vis[c] = off <= -32   ? 0xffffffffu
-                                     : off >= 64  ? 0u
-                                     : off >= 0   ? (uint32_t)(mask >> off)
-                                                  : (uint32_t)(mask << -off) | ((1u << -off) - 1u);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) mb = fmaxf(mb, (vis[c] >> i) & 1u ? v[i] : -INFINITY);
-                        } else {
+                            for (int i = 0; i < 32; ++i) mb = fmaxf(mb, (vis >> i) & 1u ? v[i] : -INFINITY);
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            float v[32];
+                            tmem_ld32(tS + 32u * c, v);
 #pragma unroll
                             for (int i = 0; i < 32; ++i) mb = fmaxf(mb, v[i]);
                         }
@@ -541,22 +551,26 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                     m_used = m_new;
                     const float mm = m_used == -INFINITY ? 0.f : m_used;  // nothing seen yet: every weight 2^-inf
                     // P over the scores: block c's 16 columns end before block c + 1's scores begin
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
+                        const uint32_t vis = tail ? visible(mask, first + 32 * c - s.len) : 0xffffffffu;
                         float v[32];
                         tmem_ld32(tS + 32u * c, v);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = fast_exp2(fmaf(v[i], sc, -mm));
+                        if (vis != 0xffffffffu) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = (vis >> i) & 1u ? v[i] : 0.f;
+                        }
                         uint32_t pk[16];
+                        float l1 = 0.f;
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            float e0 = fast_exp2(fmaf(v[2 * i], sc, -mm)), e1 = fast_exp2(fmaf(v[2 * i + 1], sc, -mm));
-                            if (tail) {
-                                e0 = (vis[c] >> (2 * i)) & 1u ? e0 : 0.f;
-                                e1 = (vis[c] >> (2 * i + 1)) & 1u ? e1 : 0.f;
-                            }
-                            l += e0;
-                            l += e1;
-                            pk[i] = pack2<C::kBf16>(e0, e1);
+                            l += v[2 * i];
+                            l1 += v[2 * i + 1];
+                            pk[i] = pack2<C::kBf16>(v[2 * i], v[2 * i + 1]);
                         }
+                        l += l1;
                         tmem_st16u(tS + 16u * c, pk);
                     }
                 }
@@ -646,91 +660,139 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
         }
         if (!ok && lane == 0) *abort = 1;
     } else if constexpr (!C::kDirect) {
-        // ---- converters: unit = eight elements of a row; a chunk's units over 256 threads
-        constexpr int UPR = D / 8, U = C::kChunkRows * UPR / kConvThreads;  // units per row; per thread and chunk
-        static_assert(U * kConvThreads == C::kChunkRows * UPR, "whole units per thread");
+        // ---- converters
         const int ct = threadIdx.x - 32 * (2 + kSoftWarps);
-        const int c = ct % UPR, row0 = ct / UPR;
-        constexpr int RSTEP = kConvThreads / UPR;
         bool ok = true;
         int it = 0, seg = 0, slot = 0;
         unsigned ph = 0;
-        while (ok && next_seg(p, cur, s)) {
-            const __half *ksc = a.ks + s.b * a.sseq + s.h * a.shead + c / 4, *vsc = a.vs + s.b * a.sseq + s.h * a.shead + c / 4;
-            // scales of the chunk that follows the one in hand: their latency hides behind its conversion
-            __half next[U];
-            auto fetch = [&](int i) {  // chunk i of the segment
-                if constexpr (SRC == SRC_Q8_F16) {
-                    const __half *src = i & 1 ? vsc : ksc;
-                    const int pos0 = (s.t0 + (i >> 1)) * kTcTile + row0;
+        // Eight elements of position `pos` (o: fp16, rest: second term) into their 16-byte chunk.
+        auto put = [&](uint8_t *at, uint4 o, uint4 rest, bool check, int pos) {
+            bool any = false;
+            if (check) {  // V rows of the sequence's end
+                if (pos >= s.total) {
+                    o = rest = make_uint4(0u, 0u, 0u, 0u);
+                } else if (pos >= s.len && only_finite<false>(o)) {
+                    any = true;
+                    only_finite<false>(rest);  // not finite where o was not
+                }
+            }
+            *reinterpret_cast<uint4 *>(at) = o;
+            if constexpr (TERMS == 2) *reinterpret_cast<uint4 *>(at + C::kTerm) = rest;
+            return any;
+        };
+        // After a chunk: its slot is free, and (done) the plane's operand tile complete.
+        auto finish = [&](bool any, uint64_t *done) {
+            if (any) bad_seg[seg & 3] = seg + 1;
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&r_empty[slot]);
+                if (done) mbar_arrive(done);
+            }
+            if (++slot == C::kRing) slot = 0, ph ^= 1u;
+        };
+        if constexpr (SRC == SRC_Q8_F16) {
+            // A thread takes whole 32-element groups, one scale each: row ct / GPR + RSTEP u, group ct % GPR.
+            // Scales are loaded two tiles ahead.  The group's 32 bytes go as two halves; threads of
+            // groups 2 and 3 take the second half first, which spreads a warp's 16-byte stores
+            // over all banks.
+            constexpr int GPR = D / kQGroup, RSTEP = kConvThreads / GPR, U = 128 / RSTEP;
+            static_assert(C::kChunks == 1, "an 8-bit tile is one chunk per plane");
+            const int g = ct % GPR, row0 = ct / GPR, flip = g >> 1;
+            __half sc[2][2][U];  // [plane][tile parity ahead][u]
+            while (ok && next_seg(p, cur, s)) {
+                const int64_t sbase = s.b * a.sseq + s.h * a.shead + g;
+                auto fetch = [&](__half(&x)[U], const __half *plane, int t) {
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
-                        const int pos = pos0 + RSTEP * u;
-                        next[u] = pos < s.total ? src[(int64_t)pos * a.spos] : __half(0);
+                        const int pos = t * kTcTile + row0 + RSTEP * u;
+                        x[u] = pos < s.total ? plane[sbase + (int64_t)pos * a.spos] : __half(0);
+                    }
+                };
+                fetch(sc[0][0], a.ks, s.t0);
+                fetch(sc[1][0], a.vs, s.t0);
+                fetch(sc[0][1], a.ks, s.t0 + 1);
+                fetch(sc[1][1], a.vs, s.t0 + 1);
+                for (int t = s.t0; ok && t < s.t1; ++t, ++it) {
+                    const int st = it % ST;
+                    const unsigned sph = (unsigned)(it / ST) & 1u;
+                    const bool tail = (t + 1) * kTcTile > s.len;
+#pragma unroll
+                    for (int plane = 0; plane < 2; ++plane) {
+                        __half2 s2[U];
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            s2[u] = __half2half2(sc[plane][0][u]);
+                            sc[plane][0][u] = sc[plane][1][u];
+                        }
+                        if (t + 2 < s.t1) fetch(sc[plane][1], plane ? a.vs : a.ks, t + 2);
+                        if (!warp_wait(plane ? &v_empty[st] : &k_empty[st], sph ^ 1u, abort) ||
+                            !warp_wait(&r_full[slot], ph, abort)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint8_t *src = raw + slot * C::kChunk;
+                        uint8_t *dst = (plane ? sV : sK) + st * C::kOperand + (g >> 1) * C::kRegion;
+                        bool any = false;
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            const int row = row0 + RSTEP * u;
+#pragma unroll
+                            for (int jj = 0; jj < 2; ++jj) {
+                                const int j = jj ^ flip;
+                                const uint4 x = *reinterpret_cast<const uint4 *>(src + row * D + 32 * g + 16 * j);
+                                uint4 o, rest = make_uint4(0u, 0u, 0u, 0u);
+                                widen_q8<TERMS>(x.x, x.y, s2[u], o, rest);
+                                any |= put(dst + swz128(row, 4 * (g & 1) + 2 * j), o, rest, tail && plane, t * kTcTile + row);
+                                widen_q8<TERMS>(x.z, x.w, s2[u], o, rest);
+                                any |= put(dst + swz128(row, 4 * (g & 1) + 2 * j + 1), o, rest, tail && plane, t * kTcTile + row);
+                            }
+                        }
+                        finish(any, plane ? &v_full[st] : &k_full[st]);
                     }
                 }
-            };
-            const int chunks = (s.t1 - s.t0) * 2 * C::kChunks;
-            static_assert(SRC != SRC_Q8_F16 || C::kChunks == 1, "an 8-bit tile is one chunk per plane");
-            fetch(0);
-            for (int t = s.t0, i = 0; ok && t < s.t1; ++t, ++it) {
-                const int st = it % ST;
-                const unsigned sph = (unsigned)(it / ST) & 1u;
-                const bool tail = (t + 1) * kTcTile > s.len;
-                for (int ch = 0; ch < 2 * C::kChunks; ++ch, ++i) {
-                    const bool is_v = ch >= C::kChunks;
-                    const int crow = (ch % C::kChunks) * C::kChunkRows;
-                    __half sc[U];
+                ++seg;
+            }
+        } else {
+            // unit = eight elements of a row; a chunk's units over 256 threads
+            constexpr int UPR = D / 8, U = C::kChunkRows * UPR / kConvThreads, RSTEP = kConvThreads / UPR;
+            static_assert(U * kConvThreads == C::kChunkRows * UPR, "whole units per thread");
+            const int c = ct % UPR, row0 = ct / UPR;
+            while (ok && next_seg(p, cur, s)) {
+                for (int t = s.t0; ok && t < s.t1; ++t, ++it) {
+                    const int st = it % ST;
+                    const unsigned sph = (unsigned)(it / ST) & 1u;
+                    const bool tail = (t + 1) * kTcTile > s.len;
+                    for (int ch = 0; ch < 2 * C::kChunks; ++ch) {
+                        const bool is_v = ch >= C::kChunks;
+                        const int crow = (ch % C::kChunks) * C::kChunkRows;
+                        if ((ch % C::kChunks == 0 && !warp_wait(is_v ? &v_empty[st] : &k_empty[st], sph ^ 1u, abort)) ||
+                            !warp_wait(&r_full[slot], ph, abort)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint8_t *src = raw + slot * C::kChunk;
+                        uint8_t *dst = (is_v ? sV : sK) + st * C::kOperand + (c >> 3) * C::kRegion;
+                        bool any = false;
 #pragma unroll
-                    for (int u = 0; u < U; ++u) sc[u] = next[u];
-                    if (i + 1 < chunks) fetch(i + 1);
-                    if ((ch % C::kChunks == 0 && !warp_wait(is_v ? &v_empty[st] : &k_empty[st], sph ^ 1u, abort)) ||
-                        !warp_wait(&r_full[slot], ph, abort)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint8_t *src = raw + slot * C::kChunk;
-                    uint8_t *dst = (is_v ? sV : sK) + st * C::kOperand + (c >> 3) * C::kRegion;
-                    bool any = false;
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const int row = row0 + RSTEP * u;
-                        uint4 o, rest = make_uint4(0u, 0u, 0u, 0u);
-                        if constexpr (SRC == SRC_Q8_F16) {
-                            widen_q8<TERMS>(*reinterpret_cast<const uint2 *>(src + row * D + 8 * c), sc[u], o, rest);
-                        } else {
+                        for (int u = 0; u < U; ++u) {
+                            const int row = row0 + RSTEP * u;
                             float v[8];
                             if constexpr (C::kElem == 2) load8(reinterpret_cast<const __nv_bfloat16 *>(src) + row * D + 8 * c, v);
                             else load8(reinterpret_cast<const float *>(src) + row * D + 8 * c, v);
-                            o = make_uint4(pack2<false>(v[0], v[1]), pack2<false>(v[2], v[3]), pack2<false>(v[4], v[5]),
-                                           pack2<false>(v[6], v[7]));
+                            const uint4 o = make_uint4(pack2<false>(v[0], v[1]), pack2<false>(v[2], v[3]),
+                                                       pack2<false>(v[4], v[5]), pack2<false>(v[6], v[7]));
+                            uint4 rest = make_uint4(0u, 0u, 0u, 0u);
                             if constexpr (TERMS == 2)
                                 rest = make_uint4(rest2(v[0], v[1], o.x), rest2(v[2], v[3], o.y), rest2(v[4], v[5], o.z),
                                                   rest2(v[6], v[7], o.w));
+                            any |= put(dst + swz128(crow + row, c & 7), o, rest, tail && is_v, t * kTcTile + crow + row);
                         }
-                        if (tail && is_v) {
-                            const int pos = t * kTcTile + crow + row;
-                            if (pos >= s.total) o = rest = make_uint4(0u, 0u, 0u, 0u);
-                            else if (pos >= s.len && only_finite<false>(o)) {
-                                any = true;
-                                only_finite<false>(rest);  // not finite where o was not
-                            }
-                        }
-                        uint8_t *at = dst + swz128(crow + row, c & 7);
-                        *reinterpret_cast<uint4 *>(at) = o;
-                        if constexpr (TERMS == 2) *reinterpret_cast<uint4 *>(at + C::kTerm) = rest;
+                        finish(any, ch % C::kChunks == C::kChunks - 1 ? (is_v ? &v_full[st] : &k_full[st]) : nullptr);
                     }
-                    if (any) bad_seg[seg & 3] = seg + 1;
-                    fence_async_shared();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&r_empty[slot]);
-                        if (ch % C::kChunks == C::kChunks - 1) mbar_arrive(is_v ? &v_full[st] : &k_full[st]);
-                    }
-                    if (++slot == C::kRing) slot = 0, ph ^= 1u;
                 }
+                ++seg;
             }
-            ++seg;
         }
         if (!ok && lane == 0) *abort = 1;
     }
