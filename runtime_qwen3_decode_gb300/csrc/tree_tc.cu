@@ -2,7 +2,7 @@
 //
 // The query rows of a KV head (row r = node r / G, head r % G of its group) fill the 128 MMA
 // rows, so the heads of a group and the nodes of a tree share every K and V row.  Per tile of
-// 128 positions S = Q K^T (one operand in TMEM, K in shared memory), the masks and the online
+// 128 positions S = Q K^T (both in shared memory), the masks and the online
 // softmax in the log2 domain, O += P V (P in TMEM over its scores, V in shared memory as it is
 // cached: the MMA takes it MN-major, so nothing is transposed).  The bound is the cache's
 // bytes: 128 x 128 x 128 MMAs, even where most of the 128 rows are empty, take 1024 cycles of a
@@ -13,11 +13,14 @@
 // inside one share is finished there; of one that is cut, each CTA writes a partial (O, max,
 // sum), and the merge kernel adds them in order.
 //
-// Warps: 0 loads (TMA), 1 issues the MMAs, 2-5 copy Q into TMEM and run softmax and epilogue
-// (one row per lane); for caches that are not bf16 beside bf16 queries, 6-13 convert.  bf16
-// beside bf16: TMA writes K and V tiles straight into swizzled operand tiles, three stages each.
-// Otherwise TMA fills a ring of 16 KB chunks of raw rows, and the converters write the 16-bit
-// operand tiles, double-buffered.  8-bit rows become fp16 (code * scale rounded once, 2^-11;
+// Warps: 0-7 softmax and epilogue, one query row per lane and two groups of four: the groups
+// take the tiles in turn, each with its own scores, maximum, sum and accumulator, so that one
+// group's tile overlaps the other's (a single group needed 2800 cycles a tile, 1000 of them
+// exponentials); the two are joined at the end of an item.  8 loads (TMA), 9 issues the MMAs; for
+// caches that are not bf16 beside bf16 queries, 10-17 convert.  bf16 beside bf16: TMA writes K
+// and V tiles straight into swizzled operand tiles, three stages each.  Otherwise TMA fills a
+// ring of 16 KB chunks of raw rows, and the converters write the 16-bit operand tiles,
+// double-buffered (one stage of two-term tiles).  8-bit rows become fp16 (code * scale rounded once, 2^-11;
 // bf16 would lose three more bits and cost twice the instructions), bf16 queries beside them
 // fp16 after division by a power of two per row, so that only elements 2^-14 below the row's
 // largest lose bits.
@@ -44,8 +47,10 @@ using namespace tc;
 
 enum { SRC_BF16 = 0, SRC_Q8_F16 = 1, SRC_BF16_F16 = 2, SRC_F32_F16 = 3 };
 
-constexpr int kSoftWarps = 4, kConvWarps = 8, kConvThreads = 32 * kConvWarps;
-constexpr uint32_t kColO = 256, kColQ = 448;  // TMEM: S at 0 and 128 (P over each), O, Q
+constexpr int kSoftWarps = 8, kLoadWarp = 8, kMmaWarp = 9, kConvWarp = 10;
+constexpr int kConvWarps = 8, kConvThreads = 32 * kConvWarps;
+// TMEM columns of softmax group g: scores (and P over them) at 128 g, accumulator at 256 + 128 g
+constexpr uint32_t kColO = 256;
 
 // TERMS: 16-bit numbers per K or V element, 2 = an fp16 and the fp16 of what it leaves.
 template <int SRC, int D, int TERMS>
@@ -53,7 +58,7 @@ struct Cfg {
     static constexpr bool kDirect = SRC == SRC_BF16;
     static constexpr bool kBf16 = SRC == SRC_BF16;
     static constexpr int kElem = SRC == SRC_Q8_F16 ? 1 : SRC == SRC_F32_F16 ? 4 : 2;
-    static constexpr int kThreads = 32 * (2 + kSoftWarps + (kDirect ? 0 : kConvWarps));
+    static constexpr int kThreads = 32 * (kConvWarp + (kDirect ? 0 : kConvWarps));
     static constexpr int kRegion = 128 * 128;              // 128 rows x 64 16-bit dims
     static constexpr int kTerm = kRegion * (D / 64);       // one term of a K or V operand tile
     static constexpr int kOperand = kTerm * TERMS;
@@ -61,10 +66,10 @@ struct Cfg {
     static constexpr int kChunkRows = 16384 / (D * kElem) < 128 ? 16384 / (D * kElem) : 128;
     static constexpr int kChunk = kChunkRows * D * kElem;  // raw bytes per ring slot
     static constexpr int kChunks = 128 / kChunkRows;       // per tile and plane
-    static constexpr int kRing = kDirect ? 0 : 6;
-    static constexpr int kK = 0, kV = kK + kStages * kOperand, kRaw = kV + kStages * kOperand;
+    static constexpr int kRing = kDirect ? 0 : 4;
+    static constexpr int kQ = 0, kK = kQ + kTerm, kV = kK + kStages * kOperand, kRaw = kV + kStages * kOperand;
     static constexpr int kBar = kRaw + kRing * kChunk;
-    static constexpr int kBytes = kBar + 512;
+    static constexpr int kBytes = kBar + 512 + kTcRows * 4;  // barriers, then one score factor per row
     static constexpr size_t kSmem = 1024 + kBytes;
     static_assert(kSmem <= 227 * 1024, "shared memory budget");
     static_assert(!kDirect || TERMS == 1, "tiles that TMA writes have one term");
@@ -269,20 +274,21 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
     using C = Cfg<SRC, D, TERMS>;
     constexpr int ST = C::kStages;
     uint8_t *base = smem_base();
-    uint8_t *sK = base + C::kK, *sV = base + C::kV, *raw = base + C::kRaw;
+    uint8_t *sQ = base + C::kQ, *sK = base + C::kK, *sV = base + C::kV, *raw = base + C::kRaw;
     uint64_t *bars = reinterpret_cast<uint64_t *>(base + C::kBar);
-    uint64_t *q_tm = bars, *k_full = bars + 1, *k_empty = bars + 4, *v_full = bars + 7, *v_empty = bars + 10,
-             *s_full = bars + 13, *p_full = bars + 15, *pv_done = bars + 17, *drain = bars + 18, *r_full = bars + 19,
-             *r_empty = bars + 25;
+    uint64_t *q_full = bars, *k_full = bars + 1, *k_empty = bars + 4, *v_full = bars + 7, *v_empty = bars + 10,
+             *s_full = bars + 13, *p_full = bars + 15, *pv_done = bars + 17, *joined = bars + 19, *drain = bars + 20,
+             *r_full = bars + 21, *r_empty = bars + 25;
     Cursor *start = reinterpret_cast<Cursor *>(bars + 32);
     int *bad_seg = reinterpret_cast<int *>(bars + 40);  // [4]: 1 + the segment that last set it
     uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + 42);
     volatile int *abort = reinterpret_cast<volatile int *>(tslot + 1);
+    float *row_scale = reinterpret_cast<float *>(base + C::kBar + 512);
     const TreeArgs &a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        mbar_init(q_tm, kSoftWarps);
+        mbar_init(q_full, kSoftWarps);
         for (int i = 0; i < ST; ++i) {
             mbar_init(&k_full[i], C::kDirect ? 1 : kConvWarps);
             mbar_init(&k_empty[i], 1);
@@ -291,9 +297,10 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], kSoftWarps);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&pv_done[i], 1);
         }
-        mbar_init(pv_done, 1);
+        mbar_init(joined, kSoftWarps);
         mbar_init(drain, 1);
         for (int i = 0; i < C::kRing; ++i) {
             mbar_init(&r_full[i], 1);
@@ -303,9 +310,13 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
         *abort = 0;
         mbar_fence_init();
     }
-    if (warp == 1) tmem_alloc(tslot, 512);
+    if (warp == kMmaWarp) tmem_alloc(tslot, 512);
+    if (warp == kLoadWarp && lane == 0) {
+        prefetch_map(&tk);
+        prefetch_map(&tv);
+    }
     chain_wait();
-    if (warp == 2) {
+    if (warp == 0) {
         const long long T = total_work(p, p.n_seq);
         const long long at = share_start(T, blockIdx.x, gridDim.x), end = share_start(T, blockIdx.x + 1, gridDim.x);
         const Cursor c = find_start(p, at, end - at);
@@ -316,11 +327,10 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
     tc_fence_after();
     chain_release();
     const uint32_t tmem = *tslot;
-    const uint32_t tO = tmem + kColO;
     Cursor cur = *start;
     Seg s;
 
-    if (warp == 0) {
+    if (warp == kLoadWarp) {
         if (lane == 0) {
             // ---- loads
             bool ok = true;
@@ -357,7 +367,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                     if (vp[i] >= 0) mbar_wait(&v_full[i], (unsigned)vp[i], abort, false, kWaitLimitNs);
                 }
             } else {
-                int rp[6] = {-1, -1, -1, -1, -1, -1};
+                int rp[4] = {-1, -1, -1, -1};
                 int slot = 0;
                 unsigned ph = 0;
                 while (ok && next_seg(p, cur, s)) {
@@ -379,16 +389,16 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                     if (rp[i] >= 0) mbar_wait(&r_full[i], (unsigned)rp[i], abort, false, kWaitLimitNs);
             }
         }
-    } else if (warp == 1) {
+    } else if (warp == kMmaWarp) {
         if (lane == 0) {
-            // ---- MMAs.  S of the segment's next tile is issued before P V of this one, so that the
-            // tensor core computes it during this tile's softmax.
+            // ---- MMAs.  Tile jj's scores and product belong to softmax group jj & 1.  S of the next
+            // tile is issued before P V of this one: the groups' tiles overlap.
             constexpr uint32_t idS = idesc_16_f32(128, 128, C::kBf16, false), idO = idesc_16_f32(128, D, C::kBf16, true);
             bool ok = true;
             int it = 0, seg = 0;  // it: tiles before this segment
             while (ok && next_seg(p, cur, s)) {
                 const int nt = s.t1 - s.t0;
-                ok = mbar_wait(q_tm, (unsigned)seg & 1u, abort, true, kWaitLimitNs);
+                ok = mbar_wait(q_full, (unsigned)seg & 1u, abort, true, kWaitLimitNs);
                 for (int j = -1; ok && j < nt; ++j) {
                     if (j + 1 < nt) {
                         const int jn = it + j + 1, st = jn % ST;
@@ -397,12 +407,12 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t sk = su32(sK + st * C::kOperand);
+                        const uint32_t sq = su32(sQ), sk = su32(sK + st * C::kOperand);
 #pragma unroll
                         for (int k = 0; k < TERMS * (D / 16); ++k) {
                             const int term = k / (D / 16), kk = k % (D / 16);
-                            mma_f16_ts(tmem + 128u * (jn & 1), tmem + kColQ + 8u * kk,
-                                       desc_sw128(sk + term * C::kTerm + (kk >> 2) * C::kRegion) + 2u * (kk & 3), idS, k != 0);
+                            mma_f16(tmem + 128u * (jn & 1), desc_sw128(sq + (kk >> 2) * C::kRegion) + 2u * (kk & 3),
+                                    desc_sw128(sk + term * C::kTerm + (kk >> 2) * C::kRegion) + 2u * (kk & 3), idS, k != 0);
                         }
                         mma_commit(&s_full[jn & 1]);
                         mma_commit(&k_empty[st]);
@@ -419,10 +429,10 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < TERMS * (kTcTile / 16); ++k) {
                             const int term = k / (kTcTile / 16), kk = k % (kTcTile / 16);
-                            mma_f16_ts(tO, tmem + 128u * (jj & 1) + 8u * kk,
-                                       desc_sw128_mn(sv + term * C::kTerm + 2048u * kk, C::kRegion), idO, j > 0 || k > 0);
+                            mma_f16_ts(tmem + kColO + 128u * (jj & 1), tmem + 128u * (jj & 1) + 8u * kk,
+                                       desc_sw128_mn(sv + term * C::kTerm + 2048u * kk, C::kRegion), idO, j > 1 || k > 0);
                         }
-                        mma_commit(pv_done);
+                        mma_commit(&pv_done[jj & 1]);
                         mma_commit(&v_empty[st]);
                     }
                 }
@@ -433,80 +443,91 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
             mma_commit(drain);  // every MMA completes before TMEM is released
             mbar_wait(drain, 0, abort, false, kWaitLimitNs);
         }
-    } else if (warp < 2 + kSoftWarps) {
-        // ---- softmax and epilogue: TMEM lane quarter q = warp % 4, one query row per lane
-        const int q = warp & 3, r = 32 * q + lane;
+    } else if (warp < kSoftWarps) {
+        // ---- softmax and epilogue: group grp, TMEM lane quarter q, one query row per lane
+        const int grp = warp >> 2, q = warp & 3, r = 32 * q + lane;
         const uint32_t lb = (uint32_t)(32 * q) << 16;
+        const uint32_t tS = tmem + lb + 128u * grp, tO = tmem + kColO + lb + 128u * grp;
         bool ok = true;
         int it = 0, seg = 0;
         while (ok && next_seg(p, cur, s)) {
-            const int row = s.r0 + r, nt = s.t1 - s.t0;
-            const bool live = row < s.rows;
-            const bool warp_live = s.r0 + 32 * q < s.rows;
+            const int row = s.r0 + r, nt = s.t1 - s.t0, nr = min(kTcRows, s.rows - s.r0);
+            const bool live = r < nr, warp_live = 32 * q < nr;
             const int node = live ? row / a.G : 0, head = s.h * a.G + (live ? row % a.G : 0);
             unsigned long long mask = live ? a.mask[(int64_t)s.b * a.n_max + node] : 0ull;
             if (s.n < 64) mask &= (1ull << s.n) - 1ull;
-            float sc = fabsf(a.scale_log2);
-            // the row of Q, 16-bit pairs in K order, into TMEM; a negative scale flips its signs
-            if (warp_live) {
+            // Q into its swizzled tile: D / 8 lanes per row, the eight warps take the live rows in turn,
+            // every load of a warp in flight at once.  A negative scale flips the signs, a scale of 0
+            // makes them 0.
+            {
+                constexpr int LPR = D / 8, RPP = 8 * 32 / LPR, PASSES = kTcRows / RPP;  // rows per pass of all warps
+                const int c = lane % LPR, first = warp * (32 / LPR) + lane / LPR;
                 const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-                const uint16_t *src = reinterpret_cast<const uint16_t *>(a.q) + s.b * a.qseq + node * a.qnode + head * a.qhead;
-                float up = 1.f;
-                if ((SRC == SRC_Q8_F16 || SRC == SRC_F32_F16) && a.dtype == QW_DT_BF16) {
-                    float amax = 0.f;
-#pragma unroll 4
-                    for (int c = 0; c < D / 8; ++c) {
-                        const uint4 u = reinterpret_cast<const uint4 *>(src)[c];
-                        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
+                const bool scaled = SRC != SRC_BF16 && a.dtype == QW_DT_BF16;
+                uint4 u[PASSES];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 f = __bfloat1622float2(h[i]);
-                            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-                        }
-                    }
-                    // 2^e <= amax < 2^(e + 1): the row is divided by 2^e; e is kept where 2^-e is normal
-                    const int e = min(max((int)((__float_as_uint(amax) >> 23) & 255u) - 127, -126), 126);
-                    if (amax > 0.f && amax < INFINITY) {
-                        up = __uint_as_float((uint32_t)(127 - e) << 23);
-                        sc *= __uint_as_float((uint32_t)(127 + e) << 23);
-                    }
+                for (int i = 0; i < PASSES; ++i) {
+                    const int x = first + RPP * i, rx = s.r0 + x;
+                    u[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (x < nr && a.scale_log2 != 0.f)
+                        u[i] = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(a.q) + s.b * a.qseq +
+                                                               (rx / a.G) * a.qnode + (s.h * a.G + rx % a.G) * a.qhead)[c];
                 }
 #pragma unroll
-                for (int hf = 0; hf < D / 64; ++hf) {
-                    uint32_t qv[32];
+                for (int i = 0; i < PASSES; ++i) {
+                    const int x = first + RPP * i;
+                    uint32_t *w = reinterpret_cast<uint32_t *>(&u[i]);
+                    float down = 1.f;
+                    if (scaled) {  // bf16 queries as fp16: the row divided by 2^e, 2^e <= amax < 2^(e + 1)
+                        float f[8], amax = 0.f;
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        uint4 u = reinterpret_cast<const uint4 *>(src)[8 * hf + c];
-                        uint32_t *w = reinterpret_cast<uint32_t *>(&u);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if ((SRC == SRC_Q8_F16 || SRC == SRC_F32_F16) && a.dtype == QW_DT_BF16) {
-                                const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]));
-                                w[i] = pack2<false>(f.x * up, f.y * up);
-                            }
-                            qv[4 * c + i] = live && sc != 0.f ? w[i] ^ flip : 0u;
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[k]));
+                            f[2 * k] = v.x;
+                            f[2 * k + 1] = v.y;
+                            amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
                         }
+#pragma unroll
+                        for (int o = LPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                        float up = 1.f;
+                        if (amax > 0.f && amax < INFINITY) {
+                            const int e = min(max((int)((__float_as_uint(amax) >> 23) & 255u) - 127, -126), 126);
+                            up = __uint_as_float((uint32_t)(127 - e) << 23);
+                            down = __uint_as_float((uint32_t)(127 + e) << 23);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) w[k] = pack2<false>(f[2 * k] * up, f[2 * k + 1] * up);
                     }
-                    tmem_st32u(tmem + lb + kColQ + 32u * hf, qv);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) w[k] ^= flip;
+                    if (x < nr) {
+                        *reinterpret_cast<uint4 *>(sQ + (c >> 3) * C::kRegion + swz128(x, c & 7)) = u[i];
+                        if (c == 0) row_scale[x] = down;
+                    }
                 }
-            }
-            if (sc == 0.f) sc = 1.f;  // a scale of 0: the scores of a zero query
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_tm);
-            float m_used = -INFINITY, l = 0.f;
-            for (int j = 0; ok && j < nt; ++j) {
-                const int jj = it + j, b = jj & 1;
-                if (!warp_wait(&s_full[b], (unsigned)(jj >> 1) & 1u, abort)) {
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full);
+                if (!warp_wait(q_full, (unsigned)seg & 1u, abort)) {
                     ok = false;
                     break;
                 }
-                tc_fence_after();
+            }
+            const float sc = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2) * (live ? row_scale[r] : 1.f);
+            float m_used = -INFINITY, l = 0.f;
+            int mine = 0;  // tiles of this segment that this group has done
+            for (int j = (it & 1) == grp ? 0 : 1; ok && j < nt; j += 2, ++mine) {
+                const int jj = it + j;
+                const unsigned par = (unsigned)(jj >> 1) & 1u;
+                if (!warp_wait(&s_full[grp], par, abort)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();  // the group's last product was issued before these scores: it is done too
                 const int first = (s.t0 + j) * kTcTile;
                 const bool tail = first + kTcTile > s.len;
-                const uint32_t tS = tmem + lb + 128u * b;
                 if (warp_live) {
-                    // blocks of 32 columns, rolled: unrolled over the tile the code outgrows the
+                    // halves of 64 columns, rolled: unrolled over the tile the code outgrows the
                     // instruction cache that all roles share
                     float mb = -INFINITY;
                     if (tail) {
@@ -518,7 +539,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
 #pragma unroll
                             for (int i = 0; i < 32; ++i) mb = fmaxf(mb, (vis >> i) & 1u ? v[i] : -INFINITY);
                         }
-                    } else {
+                    } else if constexpr (!C::kDirect) {  // 18 warps: 96 registers
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
                             float v[32];
@@ -526,25 +547,32 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
 #pragma unroll
                             for (int i = 0; i < 32; ++i) mb = fmaxf(mb, v[i]);
                         }
+                    } else {
+#pragma unroll 1
+                        for (int c = 0; c < 2; ++c) {
+                            float v[2][32];
+                            tmem_ld64(tS + 64u * c, v);
+                            float m1 = -INFINITY;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                mb = fmaxf(mb, v[0][i]);
+                                m1 = fmaxf(m1, v[1][i]);
+                            }
+                            mb = fmaxf(mb, m1);
+                        }
                     }
                     mb *= sc;
                     const bool resc = mb > m_used + 8.f;
                     const float m_new = resc ? mb : m_used;
                     const float factor = resc ? fast_exp2(m_used - m_new) : 1.f;
-                    // O must hold the previous tile's product before it is rescaled
-                    if (j > 0 && __any_sync(0xffffffffu, resc)) {
-                        if (!warp_wait(pv_done, (unsigned)(jj - 1) & 1u, abort)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
+                    if (mine > 0 && __any_sync(0xffffffffu, resc)) {
 #pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
                             float o[32];
-                            tmem_ld32(tO + lb + 32u * c, o);
+                            tmem_ld32(tO + 32u * c, o);
 #pragma unroll
                             for (int i = 0; i < 32; ++i) o[i] *= factor;
-                            tmem_st32(tO + lb + 32u * c, o);
+                            tmem_st32(tO + 32u * c, o);
                         }
                     }
                     l *= factor;
@@ -598,29 +626,54 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                         fence_async_shared();
                     }
                 }
-                // Every warp sees each product finish in turn: a wait on a parity must not be two phases
-                // behind.  One barrier per buffer for P: a warp without live rows runs ahead, but
-                // reaches the same buffer again only after the product that all four released.
-                if (jj > 0 && !warp_wait(pv_done, (unsigned)(jj - 1) & 1u, abort)) {
-                    ok = false;
-                    break;
-                }
+                // A warp without live rows may run ahead, but reaches the group's next scores only
+                // after the product that all four warps released.
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[b]);
+                if (lane == 0) mbar_arrive(&p_full[grp]);
             }
-            if (ok && !warp_wait(pv_done, (unsigned)(it + nt - 1) & 1u, abort)) ok = false;
+            // the group's last product; the ones before it were done when its scores came
+            const int last = it + nt - 1 - ((it + nt - 1) & 1 ^ grp);
+            if (ok && mine > 0 && !warp_wait(&pv_done[grp], (unsigned)(last >> 1) & 1u, abort)) ok = false;
+            if (ok) {
+                // join the groups: (m, l) through the free scores, then each group finishes half of the dims
+                tc_fence_after();
+                if (warp_live) tmem_st2(tS, m_used, l);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(joined);
+                if (!warp_wait(joined, (unsigned)seg & 1u, abort)) ok = false;
+            }
             if (ok && warp_live) {
                 tc_fence_after();
+                float m_other, l_other;
+                tmem_ld2(tmem + lb + 128u * (grp ^ 1), m_other, l_other);
+                const float m = fmaxf(m_used, m_other), mm = m == -INFINITY ? 0.f : m;
+                const bool other = nt > 1;                   // a group without a tile has no accumulator to read
+                const float w_own = mine > 0 ? fast_exp2(m_used - mm) : 0.f;
+                const float w_other = mine > 0 ? (other ? fast_exp2(m_other - mm) : 0.f) : fast_exp2(m_other - mm);
+                const float lt = l * w_own + l_other * w_other;
                 const bool whole = s.t0 == 0 && s.t1 == s.tiles;
                 const bool bad = *reinterpret_cast<volatile int *>(&bad_seg[seg & 3]) == seg + 1;
-                const float inv = whole ? (l == 0.f ? 0.f : 1.0f / l) : 1.f;
+                const float inv = whole ? (lt == 0.f ? 0.f : 1.0f / lt) : 1.f;
                 float *part = p.part + (size_t)(2 * blockIdx.x + (s.t0 > 0 ? 0 : 1)) * (D + 2) * p.rows_max + r;
                 const int64_t at = s.b * a.oseq + node * a.onode + head * a.ohead;
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
+                for (int c = grp * (D / 64); c < (grp + 1) * (D / 64); ++c) {
                     float o[32];
-                    tmem_ld32(tO + lb + 32u * c, o);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                    if (mine > 0) {
+                        tmem_ld32(tO + 32u * c, o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] *= w_own;
+                    }
+                    if (mine == 0 || other) {
+                        float x[32];
+                        tmem_ld32(tmem + kColO + lb + 128u * (grp ^ 1) + 32u * c, x);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = fmaf(x[i], w_other, o[i]);
+                    }
                     if (bad && live) {
                         const int j0 = max(s.t0 * kTcTile - s.len, 0), j1 = min(s.t1 * kTcTile, s.total) - s.len;
                         for (int jx = j0; jx < j1; ++jx) {
@@ -644,14 +697,14 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                     for (int i = 0; i < 4; ++i) {
                         float w[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) w[e] = l == 0.f ? 0.f : o[8 * i + e] * inv;
+                        for (int e = 0; e < 8; ++e) w[e] = lt == 0.f ? 0.f : o[8 * i + e] * inv;
                         if (a.dtype == QW_DT_F16) store8(reinterpret_cast<__half *>(a.out) + at + 32 * c + 8 * i, w);
                         else store8(reinterpret_cast<__nv_bfloat16 *>(a.out) + at + 32 * c + 8 * i, w);
                     }
                 }
-                if (!whole && live) {
-                    part[(size_t)D * p.rows_max] = m_used;
-                    part[(size_t)(D + 1) * p.rows_max] = l;
+                if (!whole && live && grp == 0) {
+                    part[(size_t)D * p.rows_max] = m;
+                    part[(size_t)(D + 1) * p.rows_max] = lt;
                 }
                 tc_fence_before();
             }
@@ -661,7 +714,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
         if (!ok && lane == 0) *abort = 1;
     } else if constexpr (!C::kDirect) {
         // ---- converters
-        const int ct = threadIdx.x - 32 * (2 + kSoftWarps);
+        const int ct = threadIdx.x - 32 * kConvWarp;
         bool ok = true;
         int it = 0, seg = 0, slot = 0;
         unsigned ph = 0;
@@ -798,7 +851,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) {
+    if (warp == kMmaWarp) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);
