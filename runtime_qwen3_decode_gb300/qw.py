@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import numpy as np
@@ -145,6 +146,8 @@ _LOCK = threading.Lock()
 
 def _lib():
     global _LIB
+    if _LIB is not None:
+        return _LIB
     with _LOCK:
         if _LIB is None:
             if not os.path.exists(LIB_PATH):
@@ -208,13 +211,12 @@ def _lib():
             L.qw_checkpoint_upload_bytes.restype = ctypes.c_size_t
             L.qw_checkpoint_upload.argtypes = [vp, ctypes.POINTER(Config), vp, ctypes.c_size_t,
                                                ctypes.POINTER(LayerWeights), ctypes.POINTER(Weights), vp]
-            L.qw_kv_append.argtypes = [ctypes.POINTER(KvViewStruct), ctypes.POINTER(KvRowsStruct), vp, vp, vp]
-            L.qw_kv_read.argtypes = [ctypes.POINTER(KvViewStruct), ctypes.POINTER(KvRowsStruct), vp, vp, vp]
-            L.qw_tree_attention_scratch_bytes.argtypes = [ctypes.POINTER(KvViewStruct), i32, i32, i32]
+            L.qw_kv_append.argtypes = [vp, vp, vp, vp, vp]
+            L.qw_kv_read.argtypes = [vp, vp, vp, vp, vp]
+            L.qw_tree_attention_scratch_bytes.argtypes = [vp, i32, i32, i32]
             L.qw_tree_attention_scratch_bytes.restype = ctypes.c_size_t
-            L.qw_tree_attention.argtypes = [ctypes.POINTER(KvViewStruct), ctypes.POINTER(TreeAttentionArgs), vp,
-                                            ctypes.c_size_t, vp]
-            L.qw_process_logits.argtypes = [ctypes.POINTER(ProcessLogitsArgs), vp]
+            L.qw_tree_attention.argtypes = [vp, vp, vp, ctypes.c_size_t, vp]
+            L.qw_process_logits.argtypes = [vp, vp]
             L.qw_status_string.argtypes = [ctypes.c_int]
             L.qw_status_string.restype = ctypes.c_char_p
             L.qw_abi_version.argtypes = []
@@ -350,33 +352,47 @@ def sample_logits(logits, params: Sampling, rng, token_out, history=None, scratc
 
 
 # ------------------------------------------------------- operators on caller-owned tensors
+#
+# These calls sit in a step's inner loop, where their own time counts beside a few microseconds of
+# kernel: arguments go into one packed struct (the C layout of the ctypes classes above), and the
+# checks use the tensors' cheap accessors.
+
+_KV_ROWS = struct.Struct("@PPiiqqq")
+_TREE_ARGS = struct.Struct("@PPiiiif4xqqqqqqPPP")
+_LOGITS_ARGS = struct.Struct("@PPiii4xqqPPPi4xPi4xPPPi4xPPi4x")
+
 
 def _dtype_code(t, what):
     import torch
-    code = {torch.float32: DT_F32, torch.float16: DT_F16, torch.bfloat16: DT_BF16}.get(t.dtype)
-    if code is None:
-        raise ValueError(f"{what} must be float32, float16 or bfloat16")
-    return code
+    dt = t.dtype
+    if dt is torch.float32:
+        return DT_F32
+    if dt is torch.bfloat16:
+        return DT_BF16
+    if dt is torch.float16:
+        return DT_F16
+    raise ValueError(f"{what} must be float32, float16 or bfloat16")
 
 
-def _on(device, stream, call, what):
-    """Run call(cuda_stream) with `device` current; stream None = the device's current stream."""
+def _on(dev, stream, what, call, *args):
+    """call(*args, cuda_stream) with device `dev` current; stream None = that device's current stream."""
     import torch
-    if torch.cuda.current_device() == device.index:
-        rc = call((stream or torch.cuda.current_stream()).cuda_stream)
+    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        rc = call(*args, st)
     else:
-        with torch.cuda.device(device):
-            rc = call((stream or torch.cuda.current_stream()).cuda_stream)
+        with torch.cuda.device(dev):
+            rc = call(*args, st)
     if rc != OK:
         raise QwError(rc, what)
 
 
-def _want(t, what, device, dtype, shape):
-    """A contiguous tensor of this type and shape on this device; None passes as a null pointer."""
+def _want(t, what, dev, dtype, shape):
+    """Address of a contiguous tensor of this type and shape on device dev; 0 for None."""
     if t is None:
-        return None
-    if t.device != device or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+        return 0
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}")
     return t.data_ptr()
 
 
@@ -414,21 +430,23 @@ class KvView:
         elif k_scale is not None or v_scale is not None:
             raise ValueError("only an int8 cache has scales")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_seq, self.n_kv_heads, self.max_ctx, self.head_dim = k.shape
         self.device = k.device
+        self._dev = k.get_device()
         self.struct = s
         self._ref = ctypes.byref(s)
+        self._per_seq = (self.n_seq,)
 
 
 def _kv_rows(view, k, v, what):
-    s = view.struct
-    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride() or k.stride(3) != 1 \
-            or k.device != view.device or v.device != view.device:
+    shape, stride, dev = k.shape, k.stride(), view._dev
+    if len(shape) != 4 or shape != v.shape or k.dtype is not v.dtype or stride != v.stride() or stride[3] != 1 \
+            or k.get_device() != dev or v.get_device() != dev:
         raise ValueError(f"{what} must be two tensors [n_seq, n_kv_heads, n, head_dim] alike, beside the cache, "
                          "with a contiguous last dimension")
-    if k.shape[0] != s.n_seq or k.shape[1] != s.n_kv_heads or k.shape[3] != s.head_dim:
+    if shape[0] != view.n_seq or shape[1] != view.n_kv_heads or shape[3] != view.head_dim:
         raise ValueError(f"{what} do not match the cache's sequences, heads or head_dim")
-    return KvRowsStruct(k.data_ptr(), v.data_ptr(), _dtype_code(k, what), k.shape[2], k.stride(0), k.stride(1),
-                        k.stride(2))
+    return _KV_ROWS.pack(k.data_ptr(), v.data_ptr(), _dtype_code(k, what), shape[2], stride[0], stride[1], stride[2])
 
 
 def kv_append(view: KvView, k, v, start, count=None, stream=None):
@@ -436,21 +454,17 @@ def kv_append(view: KvView, k, v, start, count=None, stream=None):
     dimension) into positions start[b] .. start[b] + count[b] - 1 of the cache; start, count: int32
     [n_seq] on the device (count None: all n)."""
     import torch
-    rows = _kv_rows(view, k, v, "the rows")
-    shape = (view.struct.n_seq,)
-    at = _want(start, "start", view.device, torch.int32, shape)
-    n = _want(count, "count", view.device, torch.int32, shape)
-    _on(view.device, stream, lambda st: _lib().qw_kv_append(view._ref, ctypes.byref(rows), at, n, st), "qw_kv_append")
+    i32 = torch.int32
+    _on(view._dev, stream, "qw_kv_append", _lib().qw_kv_append, view._ref, _kv_rows(view, k, v, "the rows"),
+        _want(start, "start", view._dev, i32, view._per_seq), _want(count, "count", view._dev, i32, view._per_seq))
 
 
 def kv_read(view: KvView, k_out, v_out, start, count=None, stream=None):
     """qw_kv_read: positions start[b] .. start[b] + count[b] - 1 of the cache into k_out, v_out."""
     import torch
-    rows = _kv_rows(view, k_out, v_out, "the rows")
-    shape = (view.struct.n_seq,)
-    at = _want(start, "start", view.device, torch.int32, shape)
-    n = _want(count, "count", view.device, torch.int32, shape)
-    _on(view.device, stream, lambda st: _lib().qw_kv_read(view._ref, ctypes.byref(rows), at, n, st), "qw_kv_read")
+    i32 = torch.int32
+    _on(view._dev, stream, "qw_kv_read", _lib().qw_kv_read, view._ref, _kv_rows(view, k_out, v_out, "the rows"),
+        _want(start, "start", view._dev, i32, view._per_seq), _want(count, "count", view._dev, i32, view._per_seq))
 
 
 def tree_mask(parents) -> np.ndarray:
@@ -469,10 +483,10 @@ def tree_mask(parents) -> np.ndarray:
 
 
 def tree_attention_scratch(view: KvView, n_max: int, n_heads: int, max_len: int | None = None):
-    """Workspace of tree_attention calls with these sizes (max_len None: any), one call at a time."""
+    """Workspace of tree_attention calls with these sizes, max_len or less (None: the cache's length),
+    one call at a time."""
     import torch
-    n = max(_lib().qw_tree_attention_scratch_bytes(view._ref, n_max, n_heads, m)
-            for m in ([view.struct.max_ctx, 0] if max_len is None else [max_len]))
+    n = _lib().qw_tree_attention_scratch_bytes(view._ref, n_max, n_heads, view.max_ctx if max_len is None else max_len)
     if n == 0 and n_max:
         raise QwError(UNSUPPORTED_SHAPE, "qw_tree_attention_scratch_bytes")
     return torch.empty(max(n, 256), dtype=torch.uint8, device=view.device)
@@ -486,28 +500,27 @@ def tree_attention(view: KvView, q, mask, lens, out=None, counts=None, max_len=N
     drafted rows lens[b] + j that mask[b, i] names.  max_len: about the longest lens (None: the cache's
     length); scale None: 1 / sqrt(head_dim).  Returns out (rows i >= counts[b] as they were)."""
     import torch
-    s = view.struct
-    if q.dim() != 4 or q.shape[0] != s.n_seq or q.shape[3] != s.head_dim or q.stride(3) != 1 or q.device != view.device:
+    dev, shape, stride = view._dev, q.shape, q.stride()
+    if len(shape) != 4 or shape[0] != view.n_seq or shape[3] != view.head_dim or stride[3] != 1 or q.get_device() != dev:
         raise ValueError("q must be [n_seq, n, n_heads, head_dim] beside the cache, with a contiguous last dimension")
     if out is None:
         out = torch.zeros_like(q, memory_format=torch.contiguous_format)
-    elif out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or out.stride(3) != 1:
+    ostride = out.stride()
+    if out.shape != shape or out.dtype is not q.dtype or out.get_device() != dev or ostride[3] != 1:
         raise ValueError("out must be like q, with a contiguous last dimension")
-    n, heads = q.shape[1], q.shape[2]
+    n, heads = shape[1], shape[2]
     if max_len is None:
-        max_len = s.max_ctx
+        max_len = view.max_ctx
     if scratch is None:
         scratch = tree_attention_scratch(view, n, heads, max_len)
-    elif scratch.device != view.device or not scratch.is_contiguous():
+    elif scratch.get_device() != dev or not scratch.is_contiguous():
         raise ValueError("scratch must be contiguous, beside the cache")
-    a = TreeAttentionArgs(q.data_ptr(), out.data_ptr(), _dtype_code(q, "q"), n, heads, max_len,
-                          s.head_dim ** -0.5 if scale is None else scale, *q.stride()[:3], *out.stride()[:3],
-                          _want(mask, "mask", view.device, torch.int64, q.shape[:2]),
-                          _want(lens, "lens", view.device, torch.int32, q.shape[:1]),
-                          _want(counts, "counts", view.device, torch.int32, q.shape[:1]))
-    _on(view.device, stream, lambda st: _lib().qw_tree_attention(view._ref, ctypes.byref(a), scratch.data_ptr(),
-                                                                 scratch.numel() * scratch.element_size(), st),
-        "qw_tree_attention")
+    i32 = torch.int32
+    args = _TREE_ARGS.pack(q.data_ptr(), out.data_ptr(), _dtype_code(q, "q"), n, heads, max_len,
+                           view.head_dim ** -0.5 if scale is None else scale, stride[0], stride[1], stride[2],
+                           ostride[0], ostride[1], ostride[2], _want(mask, "mask", dev, torch.int64, shape[:2]),
+                           _want(lens, "lens", dev, i32, view._per_seq), _want(counts, "counts", dev, i32, view._per_seq))
+    _on(dev, stream, "qw_tree_attention", _lib().qw_tree_attention, view._ref, args, scratch.data_ptr(), scratch.nbytes)
     return out
 
 
@@ -519,35 +532,36 @@ def process_logits(logits, out=None, *, history=None, history_range=None, path=N
     bias float32 [m], bias_range int32 [n_rows, 2]; mask int32 [n_masks, ceil(vocab / 32)],
     mask_index int32 [n_rows].  Returns out."""
     import torch
-    if logits.dim() != 2 or not logits.is_cuda or (logits.shape[1] > 1 and logits.stride(1) != 1):
+    shape, stride, dev = logits.shape, logits.stride(), logits.get_device()
+    if len(shape) != 2 or dev < 0 or (shape[1] > 1 and stride[1] != 1):
         raise ValueError("logits must be CUDA [n_rows, vocab] with contiguous rows")
     if out is None:
-        out = logits
-    elif out.shape != logits.shape or out.dtype != logits.dtype or out.device != logits.device \
-            or (out.shape[1] > 1 and out.stride(1) != 1):
-        raise ValueError("out must be like logits, with contiguous rows")
-    R, V = logits.shape
-    dev, i32 = logits.device, torch.int32
+        out, ostride = logits, stride
+    else:
+        ostride = out.stride()
+        if out.shape != shape or out.dtype is not logits.dtype or out.get_device() != dev \
+                or (shape[1] > 1 and ostride[1] != 1):
+            raise ValueError("out must be like logits, with contiguous rows")
+    R, V = shape
+    i32, f32 = torch.int32, torch.float32
     if (history is None) != (history_range is None):
         raise ValueError("history and history_range go together")
     if not (bias_ids is None) == (bias is None) == (bias_range is None):
         raise ValueError("bias_ids, bias and bias_range go together")
     if mask_index is not None and mask is None:
         raise ValueError("mask_index needs mask")
-    per_row = (R, 2)
+    n_hist = 0 if history is None else history.numel()
+    n_path = 0 if path is None else path.shape[-1]
     n_bias = 0 if bias is None else bias.numel()
-    a = ProcessLogitsArgs(
-        logits.data_ptr(), out.data_ptr(), _dtype_code(logits, "logits"), R, V, logits.stride(0), out.stride(0),
-        _want(penalties, "penalties", dev, torch.float32, (R, 3)),
-        None if history is None else _want(history, "history", dev, i32, (history.numel(),)),
-        _want(history_range, "history_range", dev, i32, per_row), 0 if history is None else history.numel(),
-        None if path is None else _want(path, "path", dev, i32, (R, path.shape[-1])),
-        0 if path is None else path.shape[-1],
-        _want(bias_ids, "bias_ids", dev, i32, (n_bias,)), _want(bias, "bias", dev, torch.float32, (n_bias,)),
-        _want(bias_range, "bias_range", dev, i32, per_row), n_bias,
-        None if mask is None else _want(mask, "mask", dev, i32, (mask.shape[0], (V + 31) // 32)),
-        _want(mask_index, "mask_index", dev, i32, (R,)), 0 if mask is None else mask.shape[0])
-    _on(dev, stream, lambda st: _lib().qw_process_logits(ctypes.byref(a), st), "qw_process_logits")
+    n_masks = 0 if mask is None else mask.shape[0]
+    args = _LOGITS_ARGS.pack(
+        logits.data_ptr(), out.data_ptr(), _dtype_code(logits, "logits"), R, V, stride[0], ostride[0],
+        _want(penalties, "penalties", dev, f32, (R, 3)), _want(history, "history", dev, i32, (n_hist,)),
+        _want(history_range, "history_range", dev, i32, (R, 2)), n_hist, _want(path, "path", dev, i32, (R, n_path)), n_path,
+        _want(bias_ids, "bias_ids", dev, i32, (n_bias,)), _want(bias, "bias", dev, f32, (n_bias,)),
+        _want(bias_range, "bias_range", dev, i32, (R, 2)), n_bias,
+        _want(mask, "mask", dev, i32, (n_masks, (V + 31) // 32)), _want(mask_index, "mask_index", dev, i32, (R,)), n_masks)
+    _on(dev, stream, "qw_process_logits", _lib().qw_process_logits, args)
     return out
 
 

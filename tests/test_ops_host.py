@@ -136,3 +136,13 @@ def test_tree_mask(qw):
     for bad in ([0], [-1, 1], [-2], [-1, 0, 5], [-1] * 65):
         with pytest.raises(ValueError):
             qw.tree_mask(bad)
+
+
+def test_packed_arguments_have_the_c_layout(qw):
+    # the binding packs its arguments; field by field they land where the ctypes classes have them
+    for packer, cls in ((qw._KV_ROWS, qw.KvRowsStruct), (qw._TREE_ARGS, qw.TreeAttentionArgs),
+                        (qw._LOGITS_ARGS, qw.ProcessLogitsArgs)):
+        assert packer.size == ctypes.sizeof(cls)
+        values = [i + 1 for i in range(len(cls._fields_))]
+        got = cls.from_buffer_copy(packer.pack(*values))
+        assert [getattr(got, name) for name, _ in cls._fields_] == values
