@@ -23,75 +23,88 @@ struct RowArgs {
     int64_t rseq, rhead, rrow;
     const int32_t *start, *count;
     int heads, n_max, max_ctx;
-    long long rows;           // n_seq * heads * n_max
 };
 
 // T: the rows' element type; KV: float, __nv_bfloat16, or int8_t for the 8-bit format.
-// A thread's row is one of the 2 * rows (K rows, then V rows); D / 8 threads share it.
-template <typename T, typename KV, int D, bool READ>
+// blockIdx.y = sequence, blockIdx.z = K or V; the sequence's heads * n_max rows are cut into
+// blocks of U passes of kRowThreads / (D / 8) rows.  A thread issues the loads of its U rows
+// before it uses any.
+template <typename T, typename KV, int D, int U, bool READ>
 __global__ void __launch_bounds__(kRowThreads) kv_rows_kernel(const RowArgs a) {
     constexpr int TPR = D / 8;  // threads per row
     constexpr int RPB = kRowThreads / TPR;
-    const int c = threadIdx.x % TPR;
-    const long long step = (long long)gridDim.x * RPB;
-    for (long long r0 = (long long)blockIdx.x * RPB; r0 < 2 * a.rows; r0 += step) {
-        long long r = r0 + threadIdx.x / TPR;
-        bool live = r < 2 * a.rows;
-        const bool is_v = r >= a.rows;
-        if (is_v) r -= a.rows;
-        if (!live) r = 0;
-        const int i = (int)(r % a.n_max);
-        const long long bh = r / a.n_max;
-        const int h = (int)(bh % a.heads), b = (int)(bh / a.heads);
-        const int s0 = a.start[b], n = a.count ? a.count[b] : a.n_max;
-        // a sequence whose rows would leave the cache is not touched
-        live = live && i < n && n <= a.n_max && s0 >= 0 && s0 <= a.max_ctx - n;
-        const int64_t at = b * a.seq + h * a.head + (int64_t)(live ? s0 + i : 0) * a.pos + 8 * c;
-        T *row = reinterpret_cast<T *>(is_v ? a.rv : a.rk) + b * a.rseq + h * a.rhead + i * a.rrow + 8 * c;
-        KV *cache = reinterpret_cast<KV *>(is_v ? a.v : a.k) + at;
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if constexpr (sizeof(KV) == 1) {
-            __half *sc = (is_v ? a.vs : a.ks) + b * a.sseq + h * a.shead + (int64_t)(live ? s0 + i : 0) * a.spos + c / 4;
-            if constexpr (READ) {
-                if (live) {
-                    load8_q8(cache, __half2float(*sc), v);
-                    store8(row, v);
-                }
-            } else {
-                if (live) load8(row, v);
-                __half scale;
-                const uint2 u = quant8(v, scale);  // whole warp: the group's lanes share live
-                if (live) {
-                    *reinterpret_cast<uint2 *>(cache) = u;
-                    if (c % 4 == 0) *sc = scale;
-                }
+    const int c = threadIdx.x % TPR, b = blockIdx.y;
+    const bool is_v = blockIdx.z != 0;
+    const int s0 = a.start[b], n = a.count ? a.count[b] : a.n_max;
+    // a sequence whose rows would leave the cache is not touched
+    const bool fits = n >= 0 && n <= a.n_max && s0 >= 0 && s0 <= a.max_ctx - n;
+    const uint32_t rows = (uint32_t)a.heads * (uint32_t)a.n_max;
+    T *row[U];
+    KV *cache[U];
+    __half *sc[U];
+    bool live[U];
+    float v[U][8];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const uint32_t x = (blockIdx.x * U + u) * RPB + threadIdx.x / TPR;
+        const uint32_t h = x / (uint32_t)a.n_max, i = x - h * (uint32_t)a.n_max;
+        live[u] = fits && x < rows && (int)i < n;
+        const int64_t at = live[u] ? (int64_t)s0 + i : 0;
+        row[u] = reinterpret_cast<T *>(is_v ? a.rv : a.rk) + b * a.rseq + h * a.rhead + i * a.rrow + 8 * c;
+        cache[u] = reinterpret_cast<KV *>(is_v ? a.v : a.k) + b * a.seq + h * a.head + at * a.pos + 8 * c;
+        if constexpr (sizeof(KV) == 1) sc[u] = (is_v ? a.vs : a.ks) + b * a.sseq + h * a.shead + at * a.spos + c / 4;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[u][k] = 0.f;
+        if (!live[u]) continue;
+        if constexpr (!READ) load8(row[u], v[u]);
+        else if constexpr (sizeof(KV) == 1) load8_q8(cache[u], __half2float(*sc[u]), v[u]);
+        else load8(cache[u], v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if constexpr (READ) {
+            if (live[u]) store8(row[u], v[u]);
+        } else if constexpr (sizeof(KV) == 1) {
+            __half scale;
+            const uint2 q = quant8(v[u], scale);  // whole warp: a group's lanes share live
+            if (live[u]) {
+                *reinterpret_cast<uint2 *>(cache[u]) = q;
+                if (c % 4 == 0) *sc[u] = scale;
             }
-        } else if (live) {
-            if constexpr (READ) {
-                load8(cache, v);
-                store8(row, v);
-            } else {
-                load8(row, v);
-                store8(cache, v);
-            }
+        } else if (live[u]) {
+            store8(cache[u], v[u]);
         }
     }
 }
 
+template <typename T, typename KV, int D, int U, bool READ>
+cudaError_t launch_u(const RowArgs &a, int n_seq, cudaStream_t st) {
+    constexpr int per = U * kRowThreads / (D / 8);
+    const long long rows = (long long)a.heads * a.n_max;
+    return launch_k(false, kv_rows_kernel<T, KV, D, U, READ>, dim3((unsigned)((rows + per - 1) / per), n_seq, 2),
+                    dim3(kRowThreads), 0, st, a);
+}
+
+// Four rows per thread where that still leaves blocks for every SM (32768 rows of 8 heads read back
+// as bf16: see the file's head); one row for the few rows of a decode step.
 template <typename T, typename KV, bool READ>
-cudaError_t launch_rows(const RowArgs &a, int D, cudaStream_t st) {
-    const long long per = kRowThreads / (D / 8);
-    const long long blocks = (2 * a.rows + per - 1) / per;
-    const dim3 grid((unsigned)(blocks < 152 * 8 * 8 ? blocks : 152 * 8 * 8));
-    return D == 128 ? launch_k(false, kv_rows_kernel<T, KV, 128, READ>, grid, dim3(kRowThreads), 0, st, a)
-                    : launch_k(false, kv_rows_kernel<T, KV, 64, READ>, grid, dim3(kRowThreads), 0, st, a);
+cudaError_t launch_rows(const RowArgs &a, int n_seq, int D, cudaStream_t st) {
+    const long long rows = (long long)a.heads * a.n_max * n_seq;
+    const bool many = rows * 2 * (D / 8) >= 4LL * 2 * 152 * kRowThreads;
+    if (D == 128)
+        return many ? launch_u<T, KV, 128, 4, READ>(a, n_seq, st) : launch_u<T, KV, 128, 1, READ>(a, n_seq, st);
+    return many ? launch_u<T, KV, 64, 4, READ>(a, n_seq, st) : launch_u<T, KV, 64, 1, READ>(a, n_seq, st);
 }
 
 template <typename T, bool READ>
-cudaError_t launch_rows_kv(const RowArgs &a, int format, int D, cudaStream_t st) {
-    return format == QW_KV_F32    ? launch_rows<T, float, READ>(a, D, st)
-           : format == QW_KV_BF16 ? launch_rows<T, __nv_bfloat16, READ>(a, D, st)
-                                  : launch_rows<T, int8_t, READ>(a, D, st);
+cudaError_t launch_rows_kv(const RowArgs &a, const qw_kv_view &kv, cudaStream_t st) {
+    const int n = kv.n_seq, D = kv.head_dim;
+    return kv.format == QW_KV_F32    ? launch_rows<T, float, READ>(a, n, D, st)
+           : kv.format == QW_KV_BF16 ? launch_rows<T, __nv_bfloat16, READ>(a, n, D, st)
+                                     : launch_rows<T, int8_t, READ>(a, n, D, st);
 }
 
 template <bool READ>
@@ -112,11 +125,10 @@ cudaError_t launch_any(const qw_kv_view &kv, const qw_kv_rows &r, const int32_t 
     a.heads = kv.n_kv_heads;
     a.n_max = r.n_max;
     a.max_ctx = kv.max_ctx;
-    a.rows = (long long)kv.n_seq * kv.n_kv_heads * r.n_max;
-    if (a.rows == 0) return cudaSuccess;
-    return r.dtype == QW_DT_F32   ? launch_rows_kv<float, READ>(a, kv.format, kv.head_dim, st)
-           : r.dtype == QW_DT_F16 ? launch_rows_kv<__half, READ>(a, kv.format, kv.head_dim, st)
-                                  : launch_rows_kv<__nv_bfloat16, READ>(a, kv.format, kv.head_dim, st);
+    if (r.n_max == 0) return cudaSuccess;
+    return r.dtype == QW_DT_F32   ? launch_rows_kv<float, READ>(a, kv, st)
+           : r.dtype == QW_DT_F16 ? launch_rows_kv<__half, READ>(a, kv, st)
+                                  : launch_rows_kv<__nv_bfloat16, READ>(a, kv, st);
 }
 
 }  // namespace

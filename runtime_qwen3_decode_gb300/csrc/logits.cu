@@ -49,23 +49,33 @@ __device__ __forceinline__ void store4(T *p, const float (&v)[4]) {
     }
 }
 
-// [begin, end) of a row's list, kept inside the array.
-__device__ __forceinline__ void list_range(const int32_t *range, int r, int n, int &b, int &e) {
-    b = max(range[2 * r], 0);
-    e = min(range[2 * r + 1], n);
+// [begin, end) of a row's list, kept inside the array; empty without a list.
+__device__ __forceinline__ int2 list_range(const int32_t *range, int r, int n) {
+    return range ? make_int2(max(range[2 * r], 0), min(range[2 * r + 1], n)) : make_int2(0, 0);
 }
 
 // THREADS * 16 tokens per CTA.  VEC: rows start on vector boundaries; SPARSE: there are
-// lists to look at.
+// lists to look at.  Whatever does not depend on something else is loaded first: the chain of
+// a CTA is lists -> counts -> values, and its length, not the bytes, was the time.
 template <typename T, int THREADS, bool VEC, bool SPARSE>
 __global__ void __launch_bounds__(THREADS) logits_kernel(const qw_process_logits_args a) {
-    constexpr int kTok = THREADS * 4 * kVecs;
-    extern __shared__ __align__(16) uint32_t sm[];  // [kTok] counts and flags, [kTok] biases
+    constexpr int kTok = THREADS * 4 * kVecs, kAhead = 4;
+    extern __shared__ __align__(16) uint32_t sm[];  // [kTok] counts and flags, [kTok] biases of the flagged
     uint32_t *cnt = sm;
     float *add = reinterpret_cast<float *>(sm + kTok);
     const int r = blockIdx.y, base = blockIdx.x * kTok, V = a.vocab, tid = threadIdx.x;
     const T *src = reinterpret_cast<const T *>(a.logits) + (int64_t)r * a.row_stride;
     T *dst = reinterpret_cast<T *>(a.out) + (int64_t)r * a.out_row_stride;
+    const int which = a.mask ? (a.mask_index ? a.mask_index[r] : r) : -1;
+    int2 hist = make_int2(0, 0), bias = make_int2(0, 0);
+    float rep = 1.f, pres = 0.f, freq = 0.f;
+    if constexpr (SPARSE) {
+        if (a.penalties) {
+            rep = a.penalties[3 * r], pres = a.penalties[3 * r + 1], freq = a.penalties[3 * r + 2];
+            if (a.history) hist = list_range(a.history_range, r, a.n_history);
+        }
+        if (a.bias) bias = list_range(a.bias_range, r, a.n_bias);
+    }
     float v[kVecs][4];
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
@@ -81,46 +91,60 @@ __global__ void __launch_bounds__(THREADS) logits_kernel(const qw_process_logits
             }
         }
     }
-    float rep = 1.f, pres = 0.f, freq = 0.f;
     if constexpr (SPARSE) {
         uint4 *z = reinterpret_cast<uint4 *>(sm);
-        for (int i = tid; i < 2 * kTok / 4; i += THREADS) z[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (a.penalties) rep = a.penalties[3 * r], pres = a.penalties[3 * r + 1], freq = a.penalties[3 * r + 2];
-        __syncthreads();
-        // a token outside the vocabulary falls in no chunk, or behind the row's end
-        if (a.penalties) {
-            if (a.history) {
-                int b, e;
-                list_range(a.history_range, r, a.n_history, b, e);
-                for (int i = b + tid; i < e; i += THREADS) {
-                    const uint32_t t = (uint32_t)a.history[i] - (uint32_t)base;
-                    if (t < (uint32_t)kTok) atomicAdd(cnt + t, 1u);
-                }
-            }
-            if (a.path)
-                for (int i = tid; i < a.path_len; i += THREADS) {
-                    const uint32_t t = (uint32_t)a.path[(int64_t)r * a.path_len + i] - (uint32_t)base;
-                    if (t < (uint32_t)kTok) atomicAdd(cnt + t, 1u);
-                }
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) z[tid + THREADS * i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    // the mask: a vector of four tokens lies in one word
+    const bool none = which >= a.n_masks && a.mask;  // an index past the masks: nothing is allowed
+    const uint32_t *mask = which >= 0 && !none ? a.mask + (int64_t)which * ((V + 31) / 32) : nullptr;
+    uint32_t word[kVecs];
+    if constexpr (VEC) {
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+            const int t = base + 4 * (tid + THREADS * j);
+            word[j] = mask && t < V ? mask[t >> 5] >> (t & 31) : none ? 0u : ~0u;
         }
+    }
+    if constexpr (SPARSE) {
+        // a token outside the vocabulary falls in no chunk, or behind the row's end
+        auto count = [&](int32_t id) {
+            const uint32_t t = (uint32_t)id - (uint32_t)base;
+            if (t < (uint32_t)kTok) atomicAdd(cnt + t, 1u);
+        };
+        int32_t id0 = -1, own = -1;
+        if (bias.x + tid < bias.y) id0 = a.bias_ids[bias.x + tid];
+        if (a.penalties && a.path && tid < a.path_len) own = a.path[(int64_t)r * a.path_len + tid];
+        int32_t ids[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = hist.x + tid + THREADS * k;
+            ids[k] = i < hist.y ? a.history[i] : -1;
+        }
+        __syncthreads();
+        count(own);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) count(ids[k]);
+        for (int i = hist.x + tid + THREADS * kAhead; i < hist.y; i += THREADS) count(a.history[i]);
+        if (a.penalties && a.path)
+            for (int i = tid + THREADS; i < a.path_len; i += THREADS) count(a.path[(int64_t)r * a.path_len + i]);
         if (a.bias) {
-            int b, e;
-            list_range(a.bias_range, r, a.n_bias, b, e);
-            for (int i = b + tid; i < e; i += THREADS) {
-                const uint32_t t = (uint32_t)a.bias_ids[i] - (uint32_t)base;
+            for (int i = bias.x + tid; i < bias.y; i += THREADS) {
+                const uint32_t t = (uint32_t)(i == bias.x + tid ? id0 : a.bias_ids[i]) - (uint32_t)base;
                 if (t < (uint32_t)kTok && (atomicOr(cnt + t, kNamed) & kNamed)) atomicOr(cnt + t, kTwice);
             }
             __syncthreads();
-            for (int i = b + tid; i < e; i += THREADS) {
-                const int32_t id = a.bias_ids[i];
+            for (int i = bias.x + tid; i < bias.y; i += THREADS) {
+                const int32_t id = i == bias.x + tid ? id0 : a.bias_ids[i];
                 const uint32_t t = (uint32_t)id - (uint32_t)base;
                 if (t >= (uint32_t)kTok) continue;
                 float sum = a.bias[i];
                 if (cnt[t] & kTwice) {
                     bool first = true;
-                    for (int k = b; k < i && first; ++k) first = a.bias_ids[k] != id;
+                    for (int k = bias.x; k < i && first; ++k) first = a.bias_ids[k] != id;
                     if (!first) continue;
-                    for (int k = i + 1; k < e; ++k)
+                    for (int k = i + 1; k < bias.y; ++k)
                         if (a.bias_ids[k] == id) sum += a.bias[k];
                 }
                 add[t] = sum;
@@ -128,31 +152,29 @@ __global__ void __launch_bounds__(THREADS) logits_kernel(const qw_process_logits
         }
         __syncthreads();
     }
-    const uint32_t *mask = nullptr;
-    bool none = false;  // a mask index past the masks: nothing is allowed
-    if (a.mask) {
-        const int m = a.mask_index ? a.mask_index[r] : r;
-        none = m >= a.n_masks;
-        if (m >= 0 && !none) mask = a.mask + (int64_t)m * ((V + 31) / 32);
-    }
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
         const int t0 = base + 4 * (tid + THREADS * j);
         if (VEC && t0 >= V) break;
+        uint4 c4 = make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (SPARSE && VEC) c4 = reinterpret_cast<const uint4 *>(cnt)[tid + THREADS * j];
+        const uint32_t cw[4] = {c4.x, c4.y, c4.z, c4.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int t = VEC ? t0 + i : base + 4 * THREADS * j + THREADS * i + tid;
             float x = v[j][i];
             if constexpr (SPARSE) {
-                const uint32_t c = cnt[t - base];
+                const uint32_t c = VEC ? cw[i] : cnt[t - base];
                 if (c & kCount) {
                     x = x > 0.f ? x / rep : x * rep;
                     x -= pres + freq * (float)(c & kCount);
                 }
                 if (c & kNamed) x += add[t - base];
             }
-            if (mask && t < V && !((mask[t >> 5] >> (t & 31)) & 1u)) x = -INFINITY;
-            if (none) x = -INFINITY;
+            bool ok;
+            if constexpr (VEC) ok = (word[j] >> i) & 1u;
+            else ok = !none && (!mask || t >= V || ((mask[t >> 5] >> (t & 31)) & 1u));
+            x = ok ? x : -INFINITY;
             v[j][i] = x;
             if (!VEC && t < V) dst[t] = elem_from_f<T>(x);
         }

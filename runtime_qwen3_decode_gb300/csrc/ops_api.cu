@@ -54,6 +54,7 @@ int check_rows(const qw_kv_view *kv, const qw_kv_rows *r, const int32_t *start) 
     const int e = elem_bytes(r->dtype);
     if (!e) return QW_INVALID_ARGUMENT;
     if (r->n_max == 0) return QW_OK;
+    if ((int64_t)r->n_max * kv->n_kv_heads > (int64_t)1 << 30) return QW_UNSUPPORTED_SHAPE;
     if (!r->k || !r->v) return QW_INVALID_ARGUMENT;
     const int64_t unit = 16 / e;
     if (!aligned(r->k, 16) || !aligned(r->v, 16) || !stride_ok(r->seq_stride, unit) ||
