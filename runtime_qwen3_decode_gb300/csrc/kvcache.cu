@@ -4,9 +4,10 @@
 // head_dim elements: f32, bf16, or int8 codes with one fp16 scale per 32 elements (the
 // Q8_0 block of "Scalar-Native Qwen3 Reference Runtime As The Numerical Authority",
 // section 3, codes and scales in separate planes).  Both kernels are copies with a
-// conversion: bound by the bytes of the source rows and of the written rows.  A thread
-// moves eight elements of a row, so a warp's accesses are contiguous runs of 256 bytes or
-// more, and a 32-element group is four adjacent lanes: its maximum takes two shuffles.
+// conversion: bound by the bytes of the source rows and of the written rows.  A lane moves 16
+// bytes of a row, so every access of a warp is one contiguous run on both sides, and a
+// 32-element group is 4 (16-bit rows) or 8 (f32) adjacent lanes: its maximum takes two or
+// three shuffles.
 #include "qw_ops.h"
 
 namespace qw {
@@ -25,75 +26,112 @@ struct RowArgs {
     int heads, n_max, max_ctx;
 };
 
+// E consecutive elements as they lie in memory.
+template <typename T, int E>
+struct alignas(sizeof(T) * E) Pack {
+    T e[E];
+};
+
+// The 8-bit form of a 32-element group held by 32 / E adjacent lanes, E elements each: d = amax /
+// 127 in f32, code = a / d rounded half away from zero (the Q8_0 block's quantiser), scale =
+// fp16(d).  A NaN or an infinity anywhere in the group makes the scale NaN, so that the group
+// reads back as NaN instead of as some finite value.  Whole warps call it.
+template <int E>
+__device__ __forceinline__ Pack<int8_t, E> quantise(const float (&v)[E], __half &scale) {
+    float amax = 0.f, probe = 0.f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        amax = fmaxf(amax, fabsf(v[i]));
+        probe = fmaf(v[i], 0.f, probe);  // 0 unless a value is not finite, then NaN
+    }
+#pragma unroll
+    for (int o = 1; o < kQGroup / E; o <<= 1) {
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        probe += __shfl_xor_sync(0xffffffffu, probe, o);
+    }
+    const float d = amax / 127.0f;
+    Pack<int8_t, E> c;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        const float r = d > 0.f ? fminf(fmaxf(roundf(v[i] / d), -127.f), 127.f) : 0.f;
+        c.e[i] = (int8_t)(int)r;
+    }
+    scale = __float2half_rn(d + probe);
+    return c;
+}
+
 // T: the rows' element type; KV: float, __nv_bfloat16, or int8_t for the 8-bit format.
-// blockIdx.y = sequence, blockIdx.z = K or V; the sequence's heads * n_max rows are cut into
-// blocks of U passes of kRowThreads / (D / 8) rows.  A thread issues the loads of its U rows
-// before it uses any.
+// blockIdx.x = (head, block of U * kRowThreads / (D / E) rows), blockIdx.y = sequence, blockIdx.z = K
+// or V: no division but one per block.  A lane's U rows are all loaded before one is written;
+// the rest of the latency is left to the many small blocks of an SM (blocks that looped
+// over rows with the next ones prefetched needed more registers and took 73 us where these
+// take the time in launch_rows' comment).
 template <typename T, typename KV, int D, int U, bool READ>
-__global__ void __launch_bounds__(kRowThreads) kv_rows_kernel(const RowArgs a) {
-    constexpr int TPR = D / 8;  // threads per row
+__global__ void __launch_bounds__(kRowThreads) kv_rows_kernel(const RowArgs a, int blocks) {
+    constexpr int E = 16 / sizeof(T);
+    constexpr int TPR = D / E;  // lanes per row
     constexpr int RPB = kRowThreads / TPR;
-    const int c = threadIdx.x % TPR, b = blockIdx.y;
+    using Src = typename std::conditional<READ, KV, T>::type;
+    const int c = threadIdx.x % TPR, b = blockIdx.y, h = blockIdx.x / blocks;
+    const int i0 = (blockIdx.x - h * blocks) * RPB * U + threadIdx.x / TPR;
     const bool is_v = blockIdx.z != 0;
     const int s0 = a.start[b], n = a.count ? a.count[b] : a.n_max;
     // a sequence whose rows would leave the cache is not touched
-    const bool fits = n >= 0 && n <= a.n_max && s0 >= 0 && s0 <= a.max_ctx - n;
-    const uint32_t rows = (uint32_t)a.heads * (uint32_t)a.n_max;
-    T *row[U];
-    KV *cache[U];
-    __half *sc[U];
-    bool live[U];
-    float v[U][8];
+    if (n <= 0 || n > a.n_max || s0 < 0 || s0 > a.max_ctx - n) return;
+    T *row = reinterpret_cast<T *>(is_v ? a.rv : a.rk) + b * a.rseq + h * a.rhead + i0 * a.rrow + E * c;
+    KV *cache = reinterpret_cast<KV *>(is_v ? a.v : a.k) + b * a.seq + h * a.head + ((int64_t)s0 + i0) * a.pos + E * c;
+    __half *sc = (is_v ? a.vs : a.ks) + b * a.sseq + h * a.shead + ((int64_t)s0 + i0) * a.spos + E * c / kQGroup;
+    Pack<Src, E> x[U];
+    __half scale[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const uint32_t x = (blockIdx.x * U + u) * RPB + threadIdx.x / TPR;
-        const uint32_t h = x / (uint32_t)a.n_max, i = x - h * (uint32_t)a.n_max;
-        live[u] = fits && x < rows && (int)i < n;
-        const int64_t at = live[u] ? (int64_t)s0 + i : 0;
-        row[u] = reinterpret_cast<T *>(is_v ? a.rv : a.rk) + b * a.rseq + h * a.rhead + i * a.rrow + 8 * c;
-        cache[u] = reinterpret_cast<KV *>(is_v ? a.v : a.k) + b * a.seq + h * a.head + at * a.pos + 8 * c;
-        if constexpr (sizeof(KV) == 1) sc[u] = (is_v ? a.vs : a.ks) + b * a.sseq + h * a.shead + at * a.spos + c / 4;
+        if (i0 + u * RPB >= n) continue;
+        if constexpr (READ) x[u] = *reinterpret_cast<const Pack<Src, E> *>(cache + u * RPB * a.pos);
+        else x[u] = *reinterpret_cast<const Pack<Src, E> *>(row + u * RPB * a.rrow);
+        if constexpr (READ && sizeof(KV) == 1) scale[u] = sc[u * RPB * a.spos];
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+        const bool live = i0 + u * RPB < n;
+        float v[E];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[u][k] = 0.f;
-        if (!live[u]) continue;
-        if constexpr (!READ) load8(row[u], v[u]);
-        else if constexpr (sizeof(KV) == 1) load8_q8(cache[u], __half2float(*sc[u]), v[u]);
-        else load8(cache[u], v[u]);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
+        for (int k = 0; k < E; ++k) {
+            if constexpr (sizeof(Src) == 1) v[k] = live ? (float)x[u].e[k] * __half2float(scale[u]) : 0.f;
+            else v[k] = live ? elem_to_f(x[u].e[k]) : 0.f;
+        }
         if constexpr (READ) {
-            if (live[u]) store8(row[u], v[u]);
+            Pack<T, E> o;
+#pragma unroll
+            for (int k = 0; k < E; ++k) o.e[k] = elem_from_f<T>(v[k]);
+            if (live) *reinterpret_cast<Pack<T, E> *>(row + u * RPB * a.rrow) = o;
         } else if constexpr (sizeof(KV) == 1) {
-            __half scale;
-            const uint2 q = quant8(v[u], scale);  // whole warp: a group's lanes share live
-            if (live[u]) {
-                *reinterpret_cast<uint2 *>(cache[u]) = q;
-                if (c % 4 == 0) *sc[u] = scale;
+            __half s;
+            const Pack<int8_t, E> q = quantise<E>(v, s);
+            if (live) {
+                *reinterpret_cast<Pack<int8_t, E> *>(cache + u * RPB * a.pos) = q;
+                if (c % (kQGroup / E) == 0) sc[u * RPB * a.spos] = s;
             }
-        } else if (live[u]) {
-            store8(cache[u], v[u]);
+        } else {
+            Pack<KV, E> o;
+#pragma unroll
+            for (int k = 0; k < E; ++k) o.e[k] = elem_from_f<KV>(v[k]);
+            if (live) *reinterpret_cast<Pack<KV, E> *>(cache + u * RPB * a.pos) = o;
         }
     }
 }
 
 template <typename T, typename KV, int D, int U, bool READ>
 cudaError_t launch_u(const RowArgs &a, int n_seq, cudaStream_t st) {
-    constexpr int per = U * kRowThreads / (D / 8);
-    const long long rows = (long long)a.heads * a.n_max;
-    return launch_k(false, kv_rows_kernel<T, KV, D, U, READ>, dim3((unsigned)((rows + per - 1) / per), n_seq, 2),
-                    dim3(kRowThreads), 0, st, a);
+    constexpr int per = U * kRowThreads / (D * (int)sizeof(T) / 16);  // rows per block
+    const int blocks = (a.n_max + per - 1) / per;
+    return launch_k(false, kv_rows_kernel<T, KV, D, U, READ>, dim3((unsigned)(blocks * a.heads), n_seq, 2),
+                    dim3(kRowThreads), 0, st, a, blocks);
 }
 
-// Four rows per thread where that still leaves blocks for every SM (32768 rows of 8 heads read back
-// as bf16: see the file's head); one row for the few rows of a decode step.
+// Four rows per lane where they fill a block; one for the few rows of a decode step or a tree.
 template <typename T, typename KV, bool READ>
 cudaError_t launch_rows(const RowArgs &a, int n_seq, int D, cudaStream_t st) {
-    const long long rows = (long long)a.heads * a.n_max * n_seq;
-    const bool many = rows * 2 * (D / 8) >= 4LL * 2 * 152 * kRowThreads;
+    const bool many = a.n_max >= 4 * kRowThreads / (D * (int)sizeof(T) / 16);
     if (D == 128)
         return many ? launch_u<T, KV, 128, 4, READ>(a, n_seq, st) : launch_u<T, KV, 128, 1, READ>(a, n_seq, st);
     return many ? launch_u<T, KV, 64, 4, READ>(a, n_seq, st) : launch_u<T, KV, 64, 1, READ>(a, n_seq, st);

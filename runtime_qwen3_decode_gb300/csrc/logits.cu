@@ -9,18 +9,23 @@
 // in f32, rounded once to the output's type.
 //
 // One pass over the logits; the bound is their bytes, read once and written once.  A CTA
-// takes one row's chunk of kTok tokens: each thread issues its loads first, then the CTA
-// scans the row's history, path and bias lists (a few KB that every chunk of the row reads
-// again from L2) and keeps what falls in the chunk in shared memory, as a dense count and a
-// dense bias per token, and then finishes its values.  Counts are whole numbers, so the
-// order of their atomics does not matter; a bias named more than once is summed by the
-// list's first entry alone, in order, so results do not depend on timing.
+// takes a few consecutive chunks of a row.  The row's lists (a few KB) stay in registers;
+// for each chunk the CTA keeps what falls in it in shared memory, as a dense count and a
+// dense bias per token, while the chunk's logits are on their way: the loads of the next
+// chunk are issued as soon as this one's values are out.  (One chunk per CTA spent most of
+// its time waiting in turn for the lists and for the logits: 256 x 151936 f32 took 91 us.)
+// Counts are whole numbers, so the order of their atomics does not matter; a bias named more
+// than once is summed by the list's first entry alone, in order, so results do not depend
+// on timing.
 #include "qw_ops.h"
 
 namespace qw {
 namespace {
 
+constexpr int kThreads = 256;
 constexpr int kVecs = 4;          // vectors of four tokens per thread
+constexpr int kTok = kThreads * 4 * kVecs;
+constexpr int kIds = 8, kBias = 2;  // list entries that a thread keeps in registers; longer lists are read again
 constexpr uint32_t kNamed = 1u << 31, kTwice = 1u << 30, kCount = kTwice - 1;
 
 template <typename T>
@@ -54,19 +59,19 @@ __device__ __forceinline__ int2 list_range(const int32_t *range, int r, int n) {
     return range ? make_int2(max(range[2 * r], 0), min(range[2 * r + 1], n)) : make_int2(0, 0);
 }
 
-// THREADS * 16 tokens per CTA.  VEC: rows start on vector boundaries; SPARSE: there are
-// lists to look at.  Whatever does not depend on something else is loaded first: the chain of
-// a CTA is lists -> counts -> values, and its length, not the bytes, was the time.
-template <typename T, int THREADS, bool VEC, bool SPARSE>
-__global__ void __launch_bounds__(THREADS) logits_kernel(const qw_process_logits_args a) {
-    constexpr int kTok = THREADS * 4 * kVecs, kAhead = 4;
+// VEC: rows start on vector boundaries; SPARSE: there are lists to look at.
+template <typename T, bool VEC, bool SPARSE>
+__global__ void __launch_bounds__(kThreads, 4) logits_kernel(const qw_process_logits_args a, int chunks) {
     extern __shared__ __align__(16) uint32_t sm[];  // [kTok] counts and flags, [kTok] biases of the flagged
     uint32_t *cnt = sm;
     float *add = reinterpret_cast<float *>(sm + kTok);
-    const int r = blockIdx.y, base = blockIdx.x * kTok, V = a.vocab, tid = threadIdx.x;
+    const int r = blockIdx.y, V = a.vocab, tid = threadIdx.x;
+    const int end = min((int)((blockIdx.x + 1) * chunks * kTok), V);
     const T *src = reinterpret_cast<const T *>(a.logits) + (int64_t)r * a.row_stride;
     T *dst = reinterpret_cast<T *>(a.out) + (int64_t)r * a.out_row_stride;
     const int which = a.mask ? (a.mask_index ? a.mask_index[r] : r) : -1;
+    const bool none = a.mask && which >= a.n_masks;  // an index past the masks: nothing is allowed
+    const uint32_t *mask = which >= 0 && !none ? a.mask + (int64_t)which * ((V + 31) / 32) : nullptr;
     int2 hist = make_int2(0, 0), bias = make_int2(0, 0);
     float rep = 1.f, pres = 0.f, freq = 0.f;
     if constexpr (SPARSE) {
@@ -77,133 +82,147 @@ __global__ void __launch_bounds__(THREADS) logits_kernel(const qw_process_logits
         if (a.bias) bias = list_range(a.bias_range, r, a.n_bias);
     }
     float v[kVecs][4];
-#pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-        const int t = base + 4 * (tid + THREADS * j);
-        if (VEC && t + 4 <= V) {
-            load4(src + t, v[j]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                // without vectors a warp still reads runs of 32 neighbours
-                const int s = VEC ? t + i : base + 4 * THREADS * j + THREADS * i + tid;
-                v[j][i] = s < V ? elem_to_f(src[s]) : 0.f;
-            }
-        }
-    }
-    if constexpr (SPARSE) {
-        uint4 *z = reinterpret_cast<uint4 *>(sm);
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) z[tid + THREADS * i] = make_uint4(0u, 0u, 0u, 0u);
-    }
-    // the mask: a vector of four tokens lies in one word
-    const bool none = which >= a.n_masks && a.mask;  // an index past the masks: nothing is allowed
-    const uint32_t *mask = which >= 0 && !none ? a.mask + (int64_t)which * ((V + 31) / 32) : nullptr;
-    uint32_t word[kVecs];
-    if constexpr (VEC) {
+    uint32_t word[kVecs];  // a vector of four tokens lies in one word of the mask
+    auto load = [&](int base) {
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
-            const int t = base + 4 * (tid + THREADS * j);
-            word[j] = mask && t < V ? mask[t >> 5] >> (t & 31) : none ? 0u : ~0u;
-        }
-    }
-    if constexpr (SPARSE) {
-        // a token outside the vocabulary falls in no chunk, or behind the row's end
-        auto count = [&](int32_t id) {
-            const uint32_t t = (uint32_t)id - (uint32_t)base;
-            if (t < (uint32_t)kTok) atomicAdd(cnt + t, 1u);
-        };
-        int32_t id0 = -1, own = -1;
-        if (bias.x + tid < bias.y) id0 = a.bias_ids[bias.x + tid];
-        if (a.penalties && a.path && tid < a.path_len) own = a.path[(int64_t)r * a.path_len + tid];
-        int32_t ids[kAhead];
+            const int t = base + 4 * (tid + kThreads * j);
+            if (VEC && t + 4 <= V) {
+                load4(src + t, v[j]);
+            } else {
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int i = hist.x + tid + THREADS * k;
+                for (int i = 0; i < 4; ++i) {
+                    // without vectors a warp still reads runs of 32 neighbours
+                    const int s = VEC ? t + i : base + 4 * kThreads * j + kThreads * i + tid;
+                    v[j][i] = s < V ? elem_to_f(src[s]) : 0.f;
+                }
+            }
+            if constexpr (VEC) word[j] = mask && t < V ? mask[t >> 5] >> (t & 31) : none ? 0u : ~0u;
+        }
+    };
+    int base = blockIdx.x * chunks * kTok;
+    load(base);
+    int32_t ids[kIds], bid[kBias], own = -1;
+    float bval[kBias];
+    if constexpr (SPARSE) {
+#pragma unroll
+        for (int k = 0; k < kIds; ++k) {
+            const int i = hist.x + tid + kThreads * k;
             ids[k] = i < hist.y ? a.history[i] : -1;
         }
-        __syncthreads();
-        count(own);
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) count(ids[k]);
-        for (int i = hist.x + tid + THREADS * kAhead; i < hist.y; i += THREADS) count(a.history[i]);
-        if (a.penalties && a.path)
-            for (int i = tid + THREADS; i < a.path_len; i += THREADS) count(a.path[(int64_t)r * a.path_len + i]);
-        if (a.bias) {
-            for (int i = bias.x + tid; i < bias.y; i += THREADS) {
-                const uint32_t t = (uint32_t)(i == bias.x + tid ? id0 : a.bias_ids[i]) - (uint32_t)base;
-                if (t < (uint32_t)kTok && (atomicOr(cnt + t, kNamed) & kNamed)) atomicOr(cnt + t, kTwice);
-            }
-            __syncthreads();
-            for (int i = bias.x + tid; i < bias.y; i += THREADS) {
-                const int32_t id = i == bias.x + tid ? id0 : a.bias_ids[i];
+        for (int k = 0; k < kBias; ++k) {
+            const int i = bias.x + tid + kThreads * k;
+            bid[k] = i < bias.y ? a.bias_ids[i] : -1;
+            bval[k] = i < bias.y ? a.bias[i] : 0.f;
+        }
+        if (a.penalties && a.path && tid < a.path_len) own = a.path[(int64_t)r * a.path_len + tid];
+        uint4 *z = reinterpret_cast<uint4 *>(cnt);
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) z[tid + kThreads * i] = make_uint4(0u, 0u, 0u, 0u);
+        __syncthreads();
+    }
+    for (; base < end; base += kTok) {
+        if constexpr (SPARSE) {
+            // a token outside the vocabulary falls in no chunk, or behind the row's end
+            auto count = [&](int32_t id) {
                 const uint32_t t = (uint32_t)id - (uint32_t)base;
-                if (t >= (uint32_t)kTok) continue;
-                float sum = a.bias[i];
+                if (t < (uint32_t)kTok) atomicAdd(cnt + t, 1u);
+            };
+            auto name = [&](int32_t id) {
+                const uint32_t t = (uint32_t)id - (uint32_t)base;
+                if (t < (uint32_t)kTok && (atomicOr(cnt + t, kNamed) & kNamed)) atomicOr(cnt + t, kTwice);
+            };
+            // entry i of the list: its first mention in the chunk holds the sum of all
+            auto settle = [&](int i, int32_t id, float sum) {
+                const uint32_t t = (uint32_t)id - (uint32_t)base;
+                if (t >= (uint32_t)kTok) return;
                 if (cnt[t] & kTwice) {
-                    bool first = true;
-                    for (int k = bias.x; k < i && first; ++k) first = a.bias_ids[k] != id;
-                    if (!first) continue;
+                    for (int k = bias.x; k < i; ++k)
+                        if (a.bias_ids[k] == id) return;
                     for (int k = i + 1; k < bias.y; ++k)
                         if (a.bias_ids[k] == id) sum += a.bias[k];
                 }
                 add[t] = sum;
+            };
+            count(own);
+#pragma unroll
+            for (int k = 0; k < kIds; ++k) count(ids[k]);
+            for (int i = hist.x + tid + kThreads * kIds; i < hist.y; i += kThreads) count(a.history[i]);
+            if (a.penalties && a.path)
+                for (int i = tid + kThreads; i < a.path_len; i += kThreads) count(a.path[(int64_t)r * a.path_len + i]);
+            if (a.bias) {
+#pragma unroll
+                for (int k = 0; k < kBias; ++k) name(bid[k]);
+                for (int i = bias.x + tid + kThreads * kBias; i < bias.y; i += kThreads) name(a.bias_ids[i]);
+                __syncthreads();
+#pragma unroll
+                for (int k = 0; k < kBias; ++k) settle(bias.x + tid + kThreads * k, bid[k], bval[k]);
+                for (int i = bias.x + tid + kThreads * kBias; i < bias.y; i += kThreads) settle(i, a.bias_ids[i], a.bias[i]);
             }
+            __syncthreads();
         }
-        __syncthreads();
-    }
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-        const int t0 = base + 4 * (tid + THREADS * j);
-        if (VEC && t0 >= V) break;
-        uint4 c4 = make_uint4(0u, 0u, 0u, 0u);
-        if constexpr (SPARSE && VEC) c4 = reinterpret_cast<const uint4 *>(cnt)[tid + THREADS * j];
-        const uint32_t cw[4] = {c4.x, c4.y, c4.z, c4.w};
+        for (int j = 0; j < kVecs; ++j) {
+            const int l0 = 4 * (tid + kThreads * j), t0 = base + l0;
+            uint32_t cw[4] = {0u, 0u, 0u, 0u};
+            if constexpr (SPARSE && VEC) {
+                uint4 *c4 = reinterpret_cast<uint4 *>(cnt + l0);
+                const uint4 c = *c4;
+                cw[0] = c.x, cw[1] = c.y, cw[2] = c.z, cw[3] = c.w;
+                if (c.x | c.y | c.z | c.w) *c4 = make_uint4(0u, 0u, 0u, 0u);  // for the next chunk
+            }
+            if (VEC && t0 >= V) continue;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int t = VEC ? t0 + i : base + 4 * THREADS * j + THREADS * i + tid;
-            float x = v[j][i];
-            if constexpr (SPARSE) {
-                const uint32_t c = VEC ? cw[i] : cnt[t - base];
-                if (c & kCount) {
-                    x = x > 0.f ? x / rep : x * rep;
-                    x -= pres + freq * (float)(c & kCount);
+            for (int i = 0; i < 4; ++i) {
+                const int l = VEC ? l0 + i : 4 * kThreads * j + kThreads * i + tid, t = base + l;
+                float x = v[j][i];
+                if constexpr (SPARSE) {
+                    uint32_t c = cw[i];
+                    if constexpr (!VEC) {
+                        c = cnt[l];
+                        if (c) cnt[l] = 0u;
+                    }
+                    if (c & kCount) {
+                        x = x > 0.f ? x / rep : x * rep;
+                        x -= pres + freq * (float)(c & kCount);
+                    }
+                    if (c & kNamed) x += add[l];
                 }
-                if (c & kNamed) x += add[t - base];
+                bool ok;
+                if constexpr (VEC) ok = (word[j] >> i) & 1u;
+                else ok = !none && (!mask || t >= V || ((mask[t >> 5] >> (t & 31)) & 1u));
+                x = ok ? x : -INFINITY;
+                v[j][i] = x;
+                if (!VEC && t < V) dst[t] = elem_from_f<T>(x);
             }
-            bool ok;
-            if constexpr (VEC) ok = (word[j] >> i) & 1u;
-            else ok = !none && (!mask || t >= V || ((mask[t >> 5] >> (t & 31)) & 1u));
-            x = ok ? x : -INFINITY;
-            v[j][i] = x;
-            if (!VEC && t < V) dst[t] = elem_from_f<T>(x);
-        }
-        if constexpr (VEC) {
-            if (t0 + 4 <= V) {
-                store4(dst + t0, v[j]);
-            } else {
+            if constexpr (VEC) {
+                if (t0 + 4 <= V) {
+                    store4(dst + t0, v[j]);
+                } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (t0 + i < V) dst[t0 + i] = elem_from_f<T>(v[j][i]);
+                    for (int i = 0; i < 4; ++i)
+                        if (t0 + i < V) dst[t0 + i] = elem_from_f<T>(v[j][i]);
+                }
             }
+        }
+        if (base + kTok < end) {
+            load(base + kTok);
+            if constexpr (SPARSE) __syncthreads();
         }
     }
 }
 
-template <typename T, int THREADS, bool VEC>
+template <typename T, bool VEC>
 cudaError_t launch_t(const qw_process_logits_args &a, cudaStream_t st) {
-    constexpr int kTok = THREADS * 4 * kVecs;
-    const dim3 grid((a.vocab + kTok - 1) / kTok, a.n_rows);
-    if ((a.penalties && (a.history || a.path)) || a.bias) {
-        constexpr int smem = 2 * kTok * 4;
-        if (smem > 48 * 1024) {
-            const cudaError_t e = cudaFuncSetAttribute(logits_kernel<T, THREADS, VEC, true>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-            if (e != cudaSuccess) return e;
-        }
-        return launch_k(false, logits_kernel<T, THREADS, VEC, true>, grid, dim3(THREADS), smem, st, a);
-    }
-    return launch_k(false, logits_kernel<T, THREADS, VEC, false>, grid, dim3(THREADS), 0, st, a);
+    // up to four chunks per CTA, fewer while that leaves less than two rounds of four CTAs on every SM
+    const int all = (a.vocab + kTok - 1) / kTok;
+    const long long total = (long long)all * a.n_rows;
+    const int chunks = (int)(total >= 4LL * 8 * 152 ? 4 : total >= 2LL * 8 * 152 ? 2 : 1);
+    const dim3 grid((all + chunks - 1) / chunks, a.n_rows);
+    if ((a.penalties && (a.history || a.path)) || a.bias)
+        return launch_k(false, logits_kernel<T, VEC, true>, grid, dim3(kThreads), 2 * kTok * 4, st, a, chunks);
+    return launch_k(false, logits_kernel<T, VEC, false>, grid, dim3(kThreads), 0, st, a, chunks);
 }
 
 template <typename T>
@@ -211,9 +230,7 @@ cudaError_t launch_vec(const qw_process_logits_args &a, cudaStream_t st) {
     const size_t unit = 4 * sizeof(T);
     const bool vec = !((uintptr_t)a.logits % unit) && !((uintptr_t)a.out % unit) && a.row_stride % 4 == 0 &&
                      a.out_row_stride % 4 == 0;
-    const bool small = (long long)a.n_rows * ((a.vocab + 8191) / 8192) < 3 * 152;
-    if (vec) return small ? launch_t<T, 128, true>(a, st) : launch_t<T, 512, true>(a, st);
-    return small ? launch_t<T, 128, false>(a, st) : launch_t<T, 512, false>(a, st);
+    return vec ? launch_t<T, true>(a, st) : launch_t<T, false>(a, st);
 }
 
 }  // namespace

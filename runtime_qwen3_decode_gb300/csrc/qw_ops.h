@@ -77,32 +77,4 @@ __device__ __forceinline__ void load8_q8(const int8_t *codes, float scale, float
     for (int i = 0; i < 8; ++i) v[i] = (float)c[i] * scale;
 }
 
-// The 8-bit form of a 32-element group held by four adjacent lanes, eight elements each:
-// d = amax / 127 in f32, code = a / d rounded half away from zero (the Q8_0 block's
-// quantiser), scale = fp16(d).  A NaN or an infinity anywhere in the group makes the scale
-// NaN, so that the group reads back as NaN instead of as some finite value.
-__device__ __forceinline__ uint2 quant8(const float (&v)[8], __half &scale) {
-    float amax = 0.f, probe = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        amax = fmaxf(amax, fabsf(v[i]));
-        probe = fmaf(v[i], 0.f, probe);  // 0 unless a value is not finite, then NaN
-    }
-#pragma unroll
-    for (int o = 1; o <= 2; o <<= 1) {
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        probe += __shfl_xor_sync(0xffffffffu, probe, o);
-    }
-    const float d = amax / 127.0f;
-    uint2 u = make_uint2(0u, 0u);
-    int8_t *c = reinterpret_cast<int8_t *>(&u);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float r = d > 0.f ? fminf(fmaxf(roundf(v[i] / d), -127.f), 127.f) : 0.f;
-        c[i] = (int8_t)(int)r;
-    }
-    scale = __float2half_rn(d + probe);
-    return u;
-}
-
 }  // namespace qw
