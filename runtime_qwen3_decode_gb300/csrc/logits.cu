@@ -22,10 +22,8 @@
 namespace qw {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kVecs = 4;          // vectors of four tokens per thread
-constexpr int kTok = kThreads * 4 * kVecs;
-constexpr int kIds = 8, kBias = 2;  // list entries that a thread keeps in registers; longer lists are read again
+constexpr int kVecs = 4;           // vectors of four tokens per thread
+constexpr int kIds = 4, kBias = 1;  // list entries that a thread keeps in registers; longer lists are read again
 constexpr uint32_t kNamed = 1u << 31, kTwice = 1u << 30, kCount = kTwice - 1;
 
 template <typename T>
@@ -60,8 +58,9 @@ __device__ __forceinline__ int2 list_range(const int32_t *range, int r, int n) {
 }
 
 // VEC: rows start on vector boundaries; SPARSE: there are lists to look at.
-template <typename T, bool VEC, bool SPARSE>
-__global__ void __launch_bounds__(kThreads, 4) logits_kernel(const qw_process_logits_args a, int chunks) {
+template <typename T, int kThreads, bool VEC, bool SPARSE>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_kernel(const qw_process_logits_args a, int chunks) {
+    constexpr int kTok = kThreads * 4 * kVecs;
     extern __shared__ __align__(16) uint32_t sm[];  // [kTok] counts and flags, [kTok] biases of the flagged
     uint32_t *cnt = sm;
     float *add = reinterpret_cast<float *>(sm + kTok);
@@ -165,36 +164,44 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const qw_process_lo
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
             const int l0 = 4 * (tid + kThreads * j), t0 = base + l0;
-            uint32_t cw[4] = {0u, 0u, 0u, 0u};
-            if constexpr (SPARSE && VEC) {
-                uint4 *c4 = reinterpret_cast<uint4 *>(cnt + l0);
-                const uint4 c = *c4;
-                cw[0] = c.x, cw[1] = c.y, cw[2] = c.z, cw[3] = c.w;
-                if (c.x | c.y | c.z | c.w) *c4 = make_uint4(0u, 0u, 0u, 0u);  // for the next chunk
-            }
-            if (VEC && t0 >= V) continue;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int l = VEC ? l0 + i : 4 * kThreads * j + kThreads * i + tid, t = base + l;
-                float x = v[j][i];
-                if constexpr (SPARSE) {
-                    uint32_t c = cw[i];
-                    if constexpr (!VEC) {
-                        c = cnt[l];
-                        if (c) cnt[l] = 0u;
-                    }
-                    if (c & kCount) {
-                        x = x > 0.f ? x / rep : x * rep;
-                        x -= pres + freq * (float)(c & kCount);
-                    }
-                    if (c & kNamed) x += add[l];
+            // most vectors hold no listed token
+            auto listed = [&](float x, uint32_t c, int l) {
+                if (c & kCount) {
+                    x = x > 0.f ? x / rep : x * rep;
+                    x -= pres + freq * (float)(c & kCount);
                 }
-                bool ok;
-                if constexpr (VEC) ok = (word[j] >> i) & 1u;
-                else ok = !none && (!mask || t >= V || ((mask[t >> 5] >> (t & 31)) & 1u));
-                x = ok ? x : -INFINITY;
-                v[j][i] = x;
-                if (!VEC && t < V) dst[t] = elem_from_f<T>(x);
+                if (c & kNamed) x += add[l];
+                return x;
+            };
+            if constexpr (VEC) {
+                if constexpr (SPARSE) {
+                    uint4 *c4 = reinterpret_cast<uint4 *>(cnt + l0);
+                    const uint4 c = *c4;
+                    if (c.x | c.y | c.z | c.w) {
+                        *c4 = make_uint4(0u, 0u, 0u, 0u);  // for the next chunk
+                        if (c.x) v[j][0] = listed(v[j][0], c.x, l0);
+                        if (c.y) v[j][1] = listed(v[j][1], c.y, l0 + 1);
+                        if (c.z) v[j][2] = listed(v[j][2], c.z, l0 + 2);
+                        if (c.w) v[j][3] = listed(v[j][3], c.w, l0 + 3);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[j][i] = (word[j] >> i) & 1u ? v[j][i] : -INFINITY;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int l = 4 * kThreads * j + kThreads * i + tid, t = base + l;
+                    float x = v[j][i];
+                    if constexpr (SPARSE) {
+                        const uint32_t c = cnt[l];
+                        if (c) {
+                            cnt[l] = 0u;
+                            x = listed(x, c, l);
+                        }
+                    }
+                    const bool ok = !none && (!mask || t >= V || ((mask[t >> 5] >> (t & 31)) & 1u));
+                    if (t < V) dst[t] = elem_from_f<T>(ok ? x : -INFINITY);
+                }
             }
             if constexpr (VEC) {
                 if (t0 + 4 <= V) {
@@ -213,16 +220,29 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const qw_process_lo
     }
 }
 
+template <typename T, int kThreads, bool VEC>
+cudaError_t launch_n(const qw_process_logits_args &a, int chunks, cudaStream_t st) {
+    constexpr int kTok = kThreads * 4 * kVecs, smem = 2 * kTok * 4;
+    const int all = (a.vocab + kTok - 1) / kTok;
+    const dim3 grid((all + chunks - 1) / chunks, a.n_rows);
+    if ((a.penalties && (a.history || a.path)) || a.bias) {
+        if (smem > 48 * 1024) {
+            const cudaError_t e = cudaFuncSetAttribute(logits_kernel<T, kThreads, VEC, true>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
+        }
+        return launch_k(false, logits_kernel<T, kThreads, VEC, true>, grid, dim3(kThreads), smem, st, a, chunks);
+    }
+    return launch_k(false, logits_kernel<T, kThreads, VEC, false>, grid, dim3(kThreads), 0, st, a, chunks);
+}
+
+// Many tokens: chunks of 8192, several per CTA (each list entry is looked at once per chunk); few: chunks
+// of 2048, one per CTA, so that every SM gets some.
 template <typename T, bool VEC>
 cudaError_t launch_t(const qw_process_logits_args &a, cudaStream_t st) {
-    // up to four chunks per CTA, fewer while that leaves less than two rounds of four CTAs on every SM
-    const int all = (a.vocab + kTok - 1) / kTok;
-    const long long total = (long long)all * a.n_rows;
-    const int chunks = (int)(total >= 4LL * 8 * 152 ? 4 : total >= 2LL * 8 * 152 ? 2 : 1);
-    const dim3 grid((all + chunks - 1) / chunks, a.n_rows);
-    if ((a.penalties && (a.history || a.path)) || a.bias)
-        return launch_k(false, logits_kernel<T, VEC, true>, grid, dim3(kThreads), 2 * kTok * 4, st, a, chunks);
-    return launch_k(false, logits_kernel<T, VEC, false>, grid, dim3(kThreads), 0, st, a, chunks);
+    const long long large = (long long)a.n_rows * ((a.vocab + 8191) / 8192);
+    if (large < 3 * 152) return launch_n<T, 128, VEC>(a, 1, st);
+    return launch_n<T, 512, VEC>(a, large >= 4LL * 4 * 152 ? 4 : large >= 2LL * 4 * 152 ? 2 : 1, st);
 }
 
 template <typename T>

@@ -616,6 +616,27 @@ def test_logits_a_bias_named_many_times_is_summed_in_order(qw):
         np.testing.assert_array_equal(x[0].cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("R,V,n_hist,n_bias", [(3, 40000, 6000, 20), (2, 5000, 20, 3000), (70, 17000, 1500, 700)])
+def test_logits_long_lists(qw, R, V, n_hist, n_bias):
+    # more entries for a CTA's tokens than it keeps apart
+    x = 3 * torch.randn((R, V), generator=gen(V), device="cuda")
+    pen, hist, hr, path, bids, bias, br, mask, mi = make_logits(R, V, R, n_hist=n_hist, n_bias=n_bias)
+    hr[:, 0], hr[:, 1] = 0, n_hist
+    bias = (bias / 100).astype(np.float32)
+    br[:, 0], br[:, 1] = 0, n_bias
+    parts = (pen, hist, hr, path, bids, bias, br, mask, mi)
+    keep = x.clone()
+    got = call_logits(qw, x, parts)
+    ref = logits_reference(keep, *parts)
+    # frequency * count grows with the list: counts up to n_hist, each product and sum rounded once;
+    # a bias sum of n_bias terms up to 0.15 each is off by at most n_bias^2 0.15 2^-24
+    got = got.double().cpu().numpy()
+    ok = np.isfinite(ref)
+    assert np.array_equal(got[~ok], ref[~ok])
+    tol = 8 * 2.0 ** -24 * (40 + 0.3 * n_hist) + n_bias ** 2 * 0.15 * 2.0 ** -24
+    assert np.abs(got[ok] - ref[ok]).max() <= tol
+
+
 def test_logits_captured(qw):
     x = torch.randn((4, 20000), device="cuda")
     parts = make_logits(4, 20000, 21)
