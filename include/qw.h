@@ -89,8 +89,8 @@ enum qw_kv_format {
     QW_KV_BF16 = 1,
     QW_KV_INT8_G32 = 2 /* int8 codes + one fp16 scale per 32 elements of a row, the Q8_0 block's
                           quantiser: d = amax/127 in f32, code = round-half-away(a/d), scale =
-                          fp16(d), value = f32(code) * f32(scale).  For qw_kv_view
-                          (the cache operators); a model's own cache is f32 or bf16. */
+                          fp16(d), value = f32(code) * f32(scale).  For batches and qw_kv_view;
+                          a model's own cache is f32 or bf16. */
 };
 
 /*
@@ -225,7 +225,7 @@ void qw_model_destroy(qw_model *m);
  * calls).  The B rows of a step run through skinny projections that read every weight
  * row once for all B rows (the batched prefill's fp16 weight copy, f32 accumulation),
  * per-sequence split attention over each cache, and one pass of the tied lm_head for
- * all rows; the cache uses the model's format.  Requires the batched prefill
+ * all rows; the cache uses the model's format, or 8 bits (qw_batch_create_kv).  Requires the batched prefill
  * (qw_prefill's tensor-core path, which holds that weight copy) to be available and
  * query heads = 2 x KV heads, hidden, query heads x head_dim and intermediate each one
  * of 1024, 2048, 3072, 4096, 6144 (else QW_UNSUPPORTED_SHAPE); max_ctx <= the model's
@@ -269,6 +269,34 @@ int qw_batch_logits(qw_batch *b, float *dst_dev, int64_t n);
 int qw_batch_debug_hidden(qw_batch *b, float *dst_dev, int64_t n);
 /* Wait for the batch's work; returns a recorded device error. */
 int qw_batch_sync(qw_batch *b);
+
+/* The same with the cache format given: the model's own, or QW_KV_INT8_G32, where every K and V
+ * row is quantised as it is written (the group quantiser of qw_kv_append) and a prompt and every later step
+ * attend to the quantised rows.  qw_batch_workspace_bytes and qw_batch_create take the model's.
+ * QW_INVALID_ARGUMENT (0 bytes) for another format. */
+size_t qw_batch_workspace_bytes_kv(const qw_model *m, int32_t max_batch, int32_t max_ctx, int32_t kv_format);
+int qw_batch_create_kv(qw_model *m, int32_t max_batch, int32_t max_ctx, int32_t kv_format, void *workspace_dev,
+                       size_t workspace_bytes, qw_batch **out);
+
+/*
+ * Drafted tokens of one sequence, checked in one step: n <= max_batch nodes run through the
+ * batch's projections as its rows, node i at position len + its depth, and attend to the
+ * sequence's cache and to their own ancestors (qw_tree_attention).  tokens_host[i] is node i's
+ * token, parents_host[i] < i the node that it continues, or -1 for a continuation of the cache;
+ * tokens_host[0] = -1 takes the sequence's device-resident last pick.  A chain
+ * (parents -1, 0, 1, ...) gives what that many decode steps would.  picks_host [n] (optional,
+ * synchronises) receives each node's greedy pick; qw_batch_logits gives the nodes' logits.  The
+ * sequence's length does not change: the nodes' rows stand behind it until
+ * qw_batch_tree_accept, or are forgotten by the batch's next step, tree step or prefill
+ * (or a reset of the sequence).  QW_CONTEXT_EXCEEDED if len + n > max_ctx.
+ */
+int qw_batch_tree_step(qw_batch *b, int32_t seq, int32_t n, const int32_t *tokens_host, const int32_t *parents_host,
+                       int32_t *picks_host);
+/* Keep n nodes of the sequence's last tree step: a path from a root (nodes_host[0] with parent -1,
+ * each next one the child of the one before).  Their rows become positions len .. len + n - 1,
+ * and the last one's greedy pick the sequence's last pick.  n == 0 keeps none.  QW_INVALID_ARGUMENT if
+ * no tree of this sequence waits or the nodes are no such path. */
+int qw_batch_tree_accept(qw_batch *b, int32_t seq, int32_t n, const int32_t *nodes_host);
 
 /* ---------------------------------------------- operators on caller-owned buffers */
 
@@ -343,8 +371,12 @@ int qw_kv_read(const qw_kv_view *kv, const qw_kv_rows *rows, const int32_t *star
  * scratch: qw_tree_attention_scratch_bytes device bytes, 256-byte aligned, for this call alone
  * while it runs.
  * Arithmetic: f32 accumulation, sums and softmax statistics.  With f32 queries every product is
- * f32.  With 16-bit queries the operands of the matrix products are 16-bit (queries as
- * given, K, V and the softmax weights rounded to 16 bits).
+ * f32.  With 16-bit queries the products are those of 16-bit operands on the tensor cores: softmax weights
+ * rounded to the operands' type, K and V as follows.  bf16 queries over a bf16 cache: bf16, as cached.
+ * fp16 queries: fp16, with a second term for what the rounding of an 8-bit or f32 row leaves.
+ * bf16 queries over 8-bit or f32 rows: fp16, rounded once (2^-11; the result's own rounding is
+ * 2^-8), the queries scaled by a power of two per row.  With fp16 operands cached magnitudes above
+ * 65504 are infinite.
  */
 enum { QW_TREE_NODES_MAX = 64 };
 typedef struct {

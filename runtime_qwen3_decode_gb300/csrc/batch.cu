@@ -15,11 +15,13 @@
 //   batch_head_kernel   final RMSNorm of the B rows, the tied lm_head streamed once for all of
 //                       them, logits [B][V] and one packed (logit, id) argmax key per sequence
 //   batch_pick_kernel   keys -> next tokens
+//   batch_keep_kernel   the rows of an accepted path of drafted nodes to the end of the cache
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <cmath>
 
+#include "qw.h"
 #include "qw_batch.h"
 #include "tc.cuh"
 
@@ -244,11 +246,25 @@ __global__ void __launch_bounds__(32) bqkv_post_kernel(const BatchQkvPost p) {
         return;
     }
     const int kvh = is_k ? slot - p.Hq : slot - p.Hq - p.Hkv;
-    KT *dst = reinterpret_cast<KT *>(is_k ? p.kc : p.vc) + (size_t)b * p.seq_elems +
-              ((size_t)kvh * p.max_ctx + pos) * kHeadDim;
+    const size_t row = (size_t)kvh * p.max_ctx + (p.cache_pos ? p.cache_pos[b] : pos);
+    KT *dst = reinterpret_cast<KT *>(is_k ? p.kc : p.vc) + (size_t)b * p.seq_elems + row * kHeadDim;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        if constexpr (sizeof(KT) == 4) dst[lane + 32 * j] = v[j];
+        if constexpr (sizeof(KT) == 1) {
+            // dims 32 j .. 32 j + 31, one per lane, are one group of the 8-bit row: qw_kv_append's arithmetic
+            float amax = fabsf(v[j]), probe = v[j] * 0.f;  // probe: NaN if a value is not finite
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                probe += __shfl_xor_sync(0xffffffffu, probe, o);
+            }
+            const float d = amax / 127.0f;
+            const float r = d > 0.f ? fminf(fmaxf(roundf(v[j] / d), -127.f), 127.f) : 0.f;
+            dst[lane + 32 * j] = (int8_t)(int)r;
+            if (lane == 0)
+                ((is_k ? p.ks : p.vs) + (size_t)b * (p.seq_elems / 32) + row * (kHeadDim / 32))[j] =
+                    __float2half_rn(d + probe);
+        } else if constexpr (sizeof(KT) == 4) dst[lane + 32 * j] = v[j];
         else dst[lane + 32 * j] = __float2bfloat16_rn(v[j]);
     }
 }
@@ -497,6 +513,23 @@ __global__ void batch_pick_kernel(unsigned long long *keys, int B, int32_t *pick
     keys[b] = 0ull;
 }
 
+// One warp per (plane, K or V).  A path's nodes ascend and node i is never before row i, so moving
+// them in order never overwrites a row that is still to be moved; a lane moves the same bytes
+// of every row, so lanes do not meet.
+__global__ void __launch_bounds__(32) batch_keep_kernel(const BatchKeep p) {
+    const size_t plane = (size_t)blockIdx.x * p.max_ctx + p.start;
+    uint8_t *rows = reinterpret_cast<uint8_t *>(blockIdx.y ? p.vc : p.kc) + plane * p.row_bytes;
+    uint2 *scales = reinterpret_cast<uint2 *>(blockIdx.y ? p.vs : p.ks) + plane;  // four fp16 per row
+    for (int i = 0; i < p.n; ++i) {
+        const int from = p.nodes[i];
+        if (from == i) continue;
+        for (int c = 16 * threadIdx.x; c < p.row_bytes; c += 16 * 32)
+            *reinterpret_cast<uint4 *>(rows + (size_t)i * p.row_bytes + c) =
+                *reinterpret_cast<const uint4 *>(rows + (size_t)from * p.row_bytes + c);
+        if (p.ks && threadIdx.x == 0) scales[i] = scales[from];
+    }
+}
+
 // tokens[b] = the caller's token, or (-1) this sequence's previous device-resident pick
 __global__ void batch_tokens_kernel(const int32_t *in, const int32_t *picks, int B, int32_t *tokens) {
     tc::chain_wait();
@@ -554,10 +587,16 @@ cudaError_t launch_bgemv(int epi, const BatchGemv &p, int nsm, cudaStream_t st, 
                            : launch_bgemv_k<BG_SWIGLU>(p, nsm, st, chained);
 }
 
-cudaError_t launch_bqkv_post(const BatchQkvPost &p, int kv_f32, cudaStream_t st, bool chained) {
+cudaError_t launch_bqkv_post(const BatchQkvPost &p, int kv_format, cudaStream_t st, bool chained) {
     const dim3 grid(p.Hq + 2 * p.Hkv, p.B), block(32);
-    return kv_f32 ? launch_k(chained, bqkv_post_kernel<float>, grid, block, 0, st, p)
-                  : launch_k(chained, bqkv_post_kernel<__nv_bfloat16>, grid, block, 0, st, p);
+    return kv_format == QW_KV_F32    ? launch_k(chained, bqkv_post_kernel<float>, grid, block, 0, st, p)
+           : kv_format == QW_KV_BF16 ? launch_k(chained, bqkv_post_kernel<__nv_bfloat16>, grid, block, 0, st, p)
+                                     : launch_k(chained, bqkv_post_kernel<int8_t>, grid, block, 0, st, p);
+}
+
+cudaError_t launch_batch_keep(const BatchKeep &p, cudaStream_t st) {
+    if (p.n < 1 || p.n > kBatchMax) return cudaErrorInvalidValue;
+    return launch_k(false, batch_keep_kernel, dim3(p.planes, 2), dim3(32), 0, st, p);
 }
 
 cudaError_t launch_batch_tokens(const int32_t *in, const int32_t *picks, int B, int32_t *tokens, cudaStream_t st,

@@ -42,6 +42,7 @@
 #include <vector>
 
 #include "qw_batch.h"
+#include "qw_ops.h"
 #include "qw_prefill.h"
 #include "tc.cuh"
 
@@ -264,7 +265,7 @@ __device__ __forceinline__ void qkv_head_out(const QkvOut &o, uint32_t tcol, int
     const int P = o.pos0 + t;
     // frequency-major table: for each frequency the warp's 32 rows read 32 consecutive
     // positions (one coalesced request) instead of 32 rows 512 bytes apart
-    const float2 *cs = o.rope_t + min(P, o.max_ctx - 1);
+    const float2 *cs = o.rope_t + min(P, o.rope_ld - 1);
     const float *w = snorm + (is_q ? 0 : kHeadDim);
 #pragma unroll 1
     for (int j = 0; j < 2; ++j) {
@@ -646,31 +647,15 @@ cudaError_t launch_norm_rows(float *x, const int32_t *tokens, const __nv_bfloat1
 //
 // The attention reads K as fp16 [Hkv][kv_rows][128] and V transposed, V^T fp16
 // [Hkv][128][kv_rows], both with TMA.  kv_shadow_kernel fills positions [0, n_pos) of
-// one layer from the cache (f32 or bf16) and zeroes [n_pos, n_fill), so every key a
+// one layer from the cache (f32, bf16 or 8-bit with its scales) and zeroes [n_pos, n_fill), so every key a
 // 128-key block can touch holds a finite value (a masked key still meets p = 0 in P V).
 
 constexpr int kShadowPos = 64;
 
 template <typename KT>
-__device__ __forceinline__ void load8(const KT *src, float (&f)[8]) {
-    if constexpr (sizeof(KT) == 4) {
-        const float4 a = reinterpret_cast<const float4 *>(src)[0], b = reinterpret_cast<const float4 *>(src)[1];
-        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-    } else {
-        const uint4 u = *reinterpret_cast<const uint4 *>(src);
-        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 v = __bfloat1622float2(h[i]);
-            f[2 * i] = v.x;
-            f[2 * i + 1] = v.y;
-        }
-    }
-}
-
-template <typename KT>
 __global__ void __launch_bounds__(256) kv_shadow_kernel(const KT *kc, const KT *vc, int max_ctx, int n_pos, int n_fill,
-                                                       __half *k16, __half *v16t, int kv_rows) {
+                                                       __half *k16, __half *v16t, int kv_rows, const __half *ksc,
+                                                       const __half *vsc) {
     __shared__ __align__(16) __half vt[kHeadDim][kShadowPos + 8];  // padded rows (144 B, 16-B aligned)
     chain_wait();
     chain_release();
@@ -683,8 +668,14 @@ __global__ void __launch_bounds__(256) kv_shadow_kernel(const KT *kc, const KT *
         const int j = c >> 4, d0 = (c & 15) * 8, p = p0 + j;
         float fk[8], fv[8];
         if (p < n_pos) {
-            load8(ks + (size_t)p * kHeadDim + d0, fk);
-            load8(vs + (size_t)p * kHeadDim + d0, fv);
+            if constexpr (sizeof(KT) == 1) {
+                const size_t g = ((size_t)kvh * max_ctx + p) * (kHeadDim / kQGroup) + d0 / kQGroup;
+                load8_q8(ks + (size_t)p * kHeadDim + d0, __half2float(ksc[g]), fk);
+                load8_q8(vs + (size_t)p * kHeadDim + d0, __half2float(vsc[g]), fv);
+            } else {
+                load8(ks + (size_t)p * kHeadDim + d0, fk);
+                load8(vs + (size_t)p * kHeadDim + d0, fv);
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) fk[i] = fv[i] = 0.f;
@@ -1395,7 +1386,7 @@ void prefill_destroy(PrefillState *st) {
 }
 
 int prefill_run(PrefillState *st, const DecodeArgs &a, int pos0, const int32_t *tokens_host, int n, int debug,
-                cudaStream_t stream) {
+                cudaStream_t stream, const PrefillQ8 *q8) {
     PrefillImpl *im = st->impl;
     if (!im || !st->ready) return 1;
     const qw_config &c = im->cfg;
@@ -1421,6 +1412,7 @@ int prefill_run(PrefillState *st, const DecodeArgs &a, int pos0, const int32_t *
         const int p0 = pos0 + done;
         cudaError_t e = cudaMemcpyAsync(tok, tokens_host + done, (size_t)m * 4, cudaMemcpyHostToDevice, stream);
         if (e != cudaSuccess) return 1;
+        if (q8 && cudaMemcpyAsync(q8->start, &p0, 4, cudaMemcpyHostToDevice, stream) != cudaSuccess) return 1;
         CUtensorMap mh, mo, ma;
         if (!make_map(&mh, h, m, H, BM) || !make_map(&mo, o16, m, QD, BM) || !make_map(&ma, act, m, I, BM))
             return 1;
@@ -1441,18 +1433,18 @@ int prefill_run(PrefillState *st, const DecodeArgs &a, int pos0, const int32_t *
             __half *k16 = reinterpret_cast<__half *>(buf + L.k16), *v16t = reinterpret_cast<__half *>(buf + L.v16t);
             // fp16 shadows of cache rows written before this chunk (earlier chunks, decode
             // steps or an import); the chunk's own rows come from the q|k|v epilogue below
-            if (p0 > 0) {
+            if (p0 > 0 && !q8) {
                 const dim3 sg((p0 + kShadowPos - 1) / kShadowPos, Hkv);
                 cudaError_t se;
                 if (a.kv_f32)
                     se = launch_k(ch, kv_shadow_kernel<float>, sg, dim3(256), 0, stream,
                                   reinterpret_cast<const float *>(kc), reinterpret_cast<const float *>(vc), a.max_ctx,
-                                  p0, p0, k16, v16t, L.kv_rows);
+                                  p0, p0, k16, v16t, L.kv_rows, nullptr, nullptr);
                 else
                     se = launch_k(ch, kv_shadow_kernel<__nv_bfloat16>, sg, dim3(256), 0, stream,
                                   reinterpret_cast<const __nv_bfloat16 *>(kc),
                                   reinterpret_cast<const __nv_bfloat16 *>(vc), a.max_ctx, p0, p0, k16, v16t,
-                                  L.kv_rows);
+                                  L.kv_rows, nullptr, nullptr);
                 if (se != cudaSuccess) return 1;
                 ch = true;
             }
@@ -1478,7 +1470,40 @@ int prefill_run(PrefillState *st, const DecodeArgs &a, int pos0, const int32_t *
             qo.k16 = k16;
             qo.v16t = v16t;
             qo.kv_rows = L.kv_rows;
+            if (q8) {  // position p0 + t of the epilogue is row t of the f32 rows
+                qo.kc = q8->stage_k - (ptrdiff_t)p0 * kHeadDim;
+                qo.vc = q8->stage_v - (ptrdiff_t)p0 * kHeadDim;
+                qo.kv_f32 = 1;
+                qo.max_ctx = st->rows_max;
+                qo.k16 = nullptr;
+                qo.v16t = nullptr;
+            }
             if (launch_gemm<256, EPI_QKV>(mh, wm[0], gp, st->nsm, stream, ch) != cudaSuccess) return 1;
+            if (q8) {
+                const size_t plane = (size_t)Hkv * a.max_ctx * kHeadDim;
+                const qw_kv_view view{q8->kc + l * plane,
+                                      q8->vc + l * plane,
+                                      q8->ks + l * plane / kQGroup,
+                                      q8->vs + l * plane / kQGroup,
+                                      QW_KV_INT8_G32,
+                                      1,
+                                      Hkv,
+                                      kHeadDim,
+                                      a.max_ctx,
+                                      0,
+                                      (int64_t)a.max_ctx * kHeadDim,
+                                      kHeadDim,
+                                      0,
+                                      (int64_t)a.max_ctx * (kHeadDim / kQGroup),
+                                      kHeadDim / kQGroup};
+                const qw_kv_rows rows{q8->stage_k, q8->stage_v, QW_DT_F32, m, 0, (int64_t)st->rows_max * kHeadDim, kHeadDim};
+                if (launch_kv_append(view, rows, q8->start, nullptr, stream) != cudaSuccess) return 1;
+                const dim3 sg((p0 + m + kShadowPos - 1) / kShadowPos, Hkv);
+                if (launch_k(false, kv_shadow_kernel<int8_t>, sg, dim3(256), 0, stream, (const int8_t *)view.k,
+                             (const int8_t *)view.v, a.max_ctx, p0 + m, p0 + m, k16, v16t, L.kv_rows,
+                             (const __half *)view.k_scale, (const __half *)view.v_scale) != cudaSuccess)
+                    return 1;
+            }
             FaParams fp{};
             fp.n = m;
             fp.pos0 = p0;
@@ -1556,7 +1581,8 @@ int prefill_batch_step(PrefillState *st, const DecodeArgs &a, const BatchStep &b
     __half *q16 = reinterpret_cast<__half *>(buf + L.q16);
     __half *o16 = reinterpret_cast<__half *>(buf + L.o16);
     __half *act = reinterpret_cast<__half *>(buf + L.act);
-    const size_t esz = a.kv_f32 ? 4 : 2;
+    const bool q8 = bs.kv_format == QW_KV_INT8_G32;
+    const size_t esz = q8 ? 1 : bs.kv_format == QW_KV_F32 ? 4 : 2;
     const size_t plane = (size_t)Hkv * bs.max_ctx * kHeadDim;  // elements of one layer's K (or V) plane
     const DevLayer *hl = im->host_layers.data();
     const int S = batch_splits(bs.max_n);
@@ -1606,21 +1632,62 @@ int prefill_batch_step(PrefillState *st, const DecodeArgs &a, const BatchStep &b
         qp.vc = vc;
         qp.seq_elems = bs.seq_elems;
         qp.max_ctx = bs.max_ctx;
-        if (launch_bqkv_post(qp, a.kv_f32, stream, true) != cudaSuccess) return 1;
-        BatchAttn ap{};
-        ap.q16 = q16;
-        ap.q_rows = st->rows_max;
-        ap.kc = kc;
-        ap.vc = vc;
-        ap.seq_elems = bs.seq_elems;
-        ap.max_ctx = bs.max_ctx;
-        ap.row_pos = bs.row_pos;
-        ap.S = S;
-        ap.Hq = Hq;
-        ap.scale_log2 = kLog2e / sqrtf((float)kHeadDim);
-        ap.part = bs.part;
-        if (launch_batch_attn(ap, Hkv, B, a.kv_f32, stream, true) != cudaSuccess) return 1;
-        if (launch_batch_merge(bs.part, S, Hq, B, o16, QD, stream, true) != cudaSuccess) return 1;
+        qp.cache_pos = bs.cache_pos;
+        if (q8) {
+            qp.ks = bs.ks + l * plane / kQGroup;
+            qp.vs = bs.vs + l * plane / kQGroup;
+        }
+        if (launch_bqkv_post(qp, bs.kv_format, stream, true) != cudaSuccess) return 1;
+        if (bs.mask) {
+            // a tree's nodes, or one node of each sequence over 8-bit caches
+            const bool tree = bs.tree_len != nullptr;
+            const qw_kv_view view{kc,
+                                  vc,
+                                  qp.ks,
+                                  qp.vs,
+                                  bs.kv_format,
+                                  tree ? 1 : B,
+                                  Hkv,
+                                  kHeadDim,
+                                  bs.max_ctx,
+                                  (int64_t)bs.seq_elems,
+                                  (int64_t)bs.max_ctx * kHeadDim,
+                                  kHeadDim,
+                                  (int64_t)bs.seq_elems / kQGroup,
+                                  (int64_t)bs.max_ctx * (kHeadDim / kQGroup),
+                                  kHeadDim / kQGroup};
+            qw_tree_attention_args ta{};
+            ta.q = q16;
+            ta.out = o16;
+            ta.dtype = QW_DT_F16;
+            ta.n_max = tree ? B : 1;
+            ta.n_heads = Hq;
+            ta.max_len = bs.max_len;
+            ta.scale = 1.0f / sqrtf((float)kHeadDim);
+            // row b of q16 and o16: node b of the tree, or the one node of sequence b
+            ta.q_seq_stride = ta.q_node_stride = kHeadDim;
+            ta.q_head_stride = (int64_t)st->rows_max * kHeadDim;
+            ta.out_seq_stride = ta.out_node_stride = QD;
+            ta.out_head_stride = kHeadDim;
+            ta.mask = bs.mask;
+            ta.len = tree ? bs.tree_len : bs.row_pos;
+            if (launch_tree_attn(view, ta, bs.attn_scratch, stream, true) != cudaSuccess) return 1;
+        } else {
+            BatchAttn ap{};
+            ap.q16 = q16;
+            ap.q_rows = st->rows_max;
+            ap.kc = kc;
+            ap.vc = vc;
+            ap.seq_elems = bs.seq_elems;
+            ap.max_ctx = bs.max_ctx;
+            ap.row_pos = bs.row_pos;
+            ap.S = S;
+            ap.Hq = Hq;
+            ap.scale_log2 = kLog2e / sqrtf((float)kHeadDim);
+            ap.part = bs.part;
+            if (launch_batch_attn(ap, Hkv, B, a.kv_f32, stream, true) != cudaSuccess) return 1;
+            if (launch_batch_merge(bs.part, S, Hq, B, o16, QD, stream, true) != cudaSuccess) return 1;
+        }
         // x += o Wo^T
         g.W = wo;
         g.a = o16;

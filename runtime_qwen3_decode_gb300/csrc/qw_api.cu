@@ -16,6 +16,7 @@
 #include "qw.h"
 #include "qw_internal.h"
 #include "qw_batch.h"
+#include "qw_ops.h"
 #include "qw_prefill.h"
 #include "qw_sample.h"
 
@@ -683,8 +684,17 @@ int qw_debug_gemm_f16(const void *a_dev, const void *b_dev, float *c_dev, int32_
 struct qw_batch {
     qw_model *m = nullptr;
     int max_batch = 0, max_ctx = 0;
+    int kv_format = QW_KV_F32;
     size_t seq_elems = 0;                // elements of one sequence's K (or V) cache block
     uint8_t *kc = nullptr, *vc = nullptr;
+    __half *ks = nullptr, *vs = nullptr; // 8-bit caches: scales, seq_elems / 32 per sequence
+    qw::PrefillQ8 q8{};                  // 8-bit caches: the prefill's f32 rows
+    void *attn = nullptr;                // scratch of the tree attention
+    uint64_t *ones = nullptr, *mask = nullptr;        // [8] bit 0 alone; a tree's masks
+    int *cache_pos = nullptr, *tree_len = nullptr;    // [8], [1]
+    int32_t *tree_picks = nullptr;                    // [8] greedy picks of a tree's nodes
+    std::vector<int32_t> tree;           // parents of the tree that waits for qw_batch_tree_accept
+    int tree_seq = -1;                   // its sequence, -1: none
     int32_t *tok_in = nullptr, *tok = nullptr, *picks = nullptr;
     int *row_pos = nullptr;
     unsigned long long *keys = nullptr;
@@ -698,7 +708,7 @@ struct qw_batch {
     // dump only; each combination is captured once (on a private stream) into a CUDA graph and
     // replayed on the model's stream.
     struct Graph {
-        int B, S, hidden;
+        int B, S, hidden, tree;          // tree: 1 + the sequence whose tree it is, 0: a plain step
         cudaGraphExec_t exec;
     };
     std::vector<Graph> graphs;
@@ -715,14 +725,18 @@ bool live_batch(const qw_batch *b) {
 }
 
 struct BatchLayout {
-    size_t kc, vc, small, flags, part, logits, hidden, total;
+    size_t kc, vc, ks, vs, small, flags, tree, part, attn, logits, hidden, stage, total;
 };
 
-// Regions of a batch workspace (256-byte aligned): the K and V cache blocks of every sequence,
-// token / position / pick / key arrays, flags, attention partials, logits, the debug dump.
-bool batch_layout(const qw_config &c, int max_batch, int max_ctx, BatchLayout *L) {
-    const size_t esz = c.kv_format == QW_KV_F32 ? 4 : 2;
-    const size_t block = (size_t)c.n_layers * c.n_kv_heads * max_ctx * c.head_dim * esz;
+// Regions of a batch workspace (256-byte aligned): the K and V cache blocks of every sequence (and
+// the scales of 8-bit ones), token / position / pick / key arrays, flags, a tree's arrays, attention
+// partials, the tree attention's scratch, logits, the debug dump, the prefill's f32 rows
+// for 8-bit caches.
+bool batch_layout(const qw_model *m, int max_batch, int max_ctx, int kv_format, BatchLayout *L) {
+    const qw_config &c = m->cfg;
+    const bool q8 = kv_format == QW_KV_INT8_G32;
+    const size_t elems = (size_t)c.n_layers * c.n_kv_heads * max_ctx * c.head_dim;
+    const size_t block = elems * (q8 ? 1 : kv_format == QW_KV_F32 ? 4 : 2);
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -731,13 +745,24 @@ bool batch_layout(const qw_config &c, int max_batch, int max_ctx, BatchLayout *L
     };
     L->kc = take(block * max_batch);
     L->vc = take(block * max_batch);
+    L->ks = take(q8 ? elems / qw::kQGroup * 2 * max_batch : 0);
+    L->vs = take(q8 ? elems / qw::kQGroup * 2 * max_batch : 0);
     L->small = take(5 * qw::kBatchMax * 8);
     L->flags = take(sizeof(qw::StepFlags));
+    L->tree = take(5 * qw::kBatchMax * 8);
     L->part = take((size_t)max_batch * c.n_heads * qw::kBatchMaxSplits * qw::kBatchPartStride * 4);
+    const size_t one = qw::tree_attn_scratch_bytes(max_batch, c.n_kv_heads, 1, c.n_heads, c.head_dim, max_ctx);
+    const size_t all = qw::tree_attn_scratch_bytes(1, c.n_kv_heads, max_batch, c.n_heads, c.head_dim, max_ctx);
+    L->attn = take(one > all ? one : all);
     L->logits = take((size_t)max_batch * c.vocab * 4);
     L->hidden = take((size_t)(c.n_layers + 1) * max_batch * c.hidden * 4);
+    L->stage = take(q8 ? (size_t)2 * c.n_kv_heads * m->pf.rows_max * c.head_dim * 4 : 0);
     L->total = off;
     return true;
+}
+
+bool batch_format_ok(const qw_model *m, int32_t kv_format) {
+    return kv_format == m->cfg.kv_format || kv_format == QW_KV_INT8_G32;
 }
 
 int batch_read(qw_batch *b, int32_t *picks_host, int n) {
@@ -759,17 +784,30 @@ int batch_read(qw_batch *b, int32_t *picks_host, int n) {
 extern "C" {
 
 size_t qw_batch_workspace_bytes(const qw_model *m, int32_t max_batch, int32_t max_ctx) {
-    if (!live(m) || max_batch < 1 || max_batch > qw::kBatchMax || max_ctx < 1 || max_ctx > m->cfg.max_ctx) return 0;
+    return live(m) ? qw_batch_workspace_bytes_kv(m, max_batch, max_ctx, m->cfg.kv_format) : 0;
+}
+
+size_t qw_batch_workspace_bytes_kv(const qw_model *m, int32_t max_batch, int32_t max_ctx, int32_t kv_format) {
+    if (!live(m) || max_batch < 1 || max_batch > qw::kBatchMax || max_ctx < 1 || max_ctx > m->cfg.max_ctx ||
+        !batch_format_ok(m, kv_format))
+        return 0;
     BatchLayout L;
-    batch_layout(m->cfg, max_batch, max_ctx, &L);
+    batch_layout(m, max_batch, max_ctx, kv_format, &L);
     return L.total;
 }
 
 int qw_batch_create(qw_model *m, int32_t max_batch, int32_t max_ctx, void *workspace_dev, size_t workspace_bytes,
                     qw_batch **out) {
+    return qw_batch_create_kv(m, max_batch, max_ctx, live(m) ? m->cfg.kv_format : QW_KV_F32, workspace_dev,
+                              workspace_bytes, out);
+}
+
+int qw_batch_create_kv(qw_model *m, int32_t max_batch, int32_t max_ctx, int32_t kv_format, void *workspace_dev,
+                       size_t workspace_bytes, qw_batch **out) {
     if (!out) return QW_INVALID_ARGUMENT;
     *out = nullptr;
     if (!live(m)) return QW_INVALID_HANDLE;
+    if (!batch_format_ok(m, kv_format)) return QW_INVALID_ARGUMENT;
     if (max_batch < 1 || max_batch > qw::kBatchMax || max_ctx < 1 || max_ctx > m->cfg.max_ctx)
         return QW_INVALID_ARGUMENT;
     if (!qw::prefill_supported(m->pf) || max_batch > m->pf.rows_max || m->cfg.n_heads != qw::kBatchG * m->cfg.n_kv_heads)
@@ -779,7 +817,7 @@ int qw_batch_create(qw_model *m, int32_t max_batch, int32_t max_ctx, void *works
         return QW_UNSUPPORTED_SHAPE;
     if (!aligned(workspace_dev, 256)) return QW_ALIGNMENT;
     BatchLayout L;
-    batch_layout(m->cfg, max_batch, max_ctx, &L);
+    batch_layout(m, max_batch, max_ctx, kv_format, &L);
     if (workspace_bytes < L.total) return QW_OUT_OF_MEMORY;
     qw_batch *b = new (std::nothrow) qw_batch();
     if (!b) return QW_OUT_OF_MEMORY;
@@ -788,8 +826,22 @@ int qw_batch_create(qw_model *m, int32_t max_batch, int32_t max_ctx, void *works
     b->max_batch = max_batch;
     b->max_ctx = max_ctx;
     b->seq_elems = (size_t)m->cfg.n_layers * m->cfg.n_kv_heads * max_ctx * m->cfg.head_dim;
+    b->kv_format = kv_format;
     b->kc = ws + L.kc;
     b->vc = ws + L.vc;
+    if (kv_format == QW_KV_INT8_G32) {
+        b->ks = (__half *)(ws + L.ks);
+        b->vs = (__half *)(ws + L.vs);
+        b->q8.stage_k = (float *)(ws + L.stage);
+        b->q8.stage_v = b->q8.stage_k + (size_t)m->cfg.n_kv_heads * m->pf.rows_max * m->cfg.head_dim;
+    }
+    b->attn = ws + L.attn;
+    b->ones = (uint64_t *)(ws + L.tree);
+    b->mask = b->ones + qw::kBatchMax;
+    b->cache_pos = (int *)(b->mask + qw::kBatchMax);
+    b->tree_picks = b->cache_pos + qw::kBatchMax;
+    b->tree_len = b->tree_picks + qw::kBatchMax;
+    b->q8.start = b->tree_len + 1;
     b->tok_in = (int32_t *)(ws + L.small);
     b->tok = b->tok_in + qw::kBatchMax;
     b->picks = b->tok + qw::kBatchMax;
@@ -802,6 +854,9 @@ int qw_batch_create(qw_model *m, int32_t max_batch, int32_t max_ctx, void *works
     b->len.assign(max_batch, 0);
     b->has_last.assign(max_batch, 0);
     int rc = cuda_status(cudaMemsetAsync(ws + L.small, 0, L.part - L.small, m->stream));
+    uint64_t ones[qw::kBatchMax];
+    for (uint64_t &x : ones) x = 1;
+    if (!rc) rc = cuda_status(cudaMemcpyAsync(b->ones, ones, sizeof(ones), cudaMemcpyHostToDevice, m->stream));
     if (!rc) rc = cuda_status(cudaStreamSynchronize(m->stream));
     if (!rc) rc = cuda_status(cudaStreamCreateWithFlags(&b->cap, cudaStreamNonBlocking));
     if (rc) {
@@ -832,6 +887,7 @@ void qw_batch_destroy(qw_batch *b) {
 int qw_batch_reset(qw_batch *b, int32_t seq) {
     if (!live_batch(b)) return QW_INVALID_HANDLE;
     if (seq < -1 || seq >= b->max_batch) return QW_INVALID_ARGUMENT;
+    if (seq == -1 || seq == b->tree_seq) b->tree_seq = -1;
     for (int s = 0; s < b->max_batch; ++s)
         if (seq == -1 || s == seq) {
             b->len[s] = 0;
@@ -860,13 +916,23 @@ int qw_batch_prefill(qw_batch *b, int32_t seq, const int32_t *tokens_host, int32
     for (int32_t i = 0; i < n; ++i)
         if (tokens_host[i] < 0 || tokens_host[i] >= m->cfg.vocab) return QW_INVALID_ARGUMENT;
     qw::DecodeArgs a = m->args;  // the model's weights and RoPE table; this sequence's cache
-    const size_t esz = m->cfg.kv_format == QW_KV_F32 ? 4 : 2;
+    const bool is_q8 = b->kv_format == QW_KV_INT8_G32;
+    const size_t esz = is_q8 ? 1 : b->kv_format == QW_KV_F32 ? 4 : 2;
     a.kc = b->kc + (size_t)seq * b->seq_elems * esz;
     a.vc = b->vc + (size_t)seq * b->seq_elems * esz;
     a.max_ctx = b->max_ctx;
     a.logits = b->logits + (size_t)seq * m->cfg.vocab;
     a.flags = b->flags;
-    if (qw::prefill_run(&m->pf, a, b->len[seq], tokens_host, n, 0, m->stream)) return QW_CUDA_ERROR;
+    qw::PrefillQ8 q8 = b->q8;
+    if (is_q8) {
+        q8.kc = (int8_t *)a.kc;
+        q8.vc = (int8_t *)a.vc;
+        q8.ks = b->ks + (size_t)seq * (b->seq_elems / qw::kQGroup);
+        q8.vs = b->vs + (size_t)seq * (b->seq_elems / qw::kQGroup);
+    }
+    b->tree_seq = -1;
+    if (qw::prefill_run(&m->pf, a, b->len[seq], tokens_host, n, 0, m->stream, is_q8 ? &q8 : nullptr))
+        return QW_CUDA_ERROR;
     b->len[seq] += n;
     b->has_last[seq] = 1;
     int rc = cuda_status(cudaMemcpyAsync(b->picks + seq, &b->flags->next_tok, 4, cudaMemcpyDeviceToDevice, m->stream));
@@ -878,6 +944,72 @@ int qw_batch_prefill(qw_batch *b, int32_t seq, const int32_t *tokens_host, int32
     }
     return QW_OK;
 }
+
+}  // extern "C"
+
+namespace {
+
+// What every step of a batch shares; the caller adds the rows and where they go.
+qw::BatchStep batch_step_of(qw_batch *b, int rows) {
+    qw::BatchStep bs{};
+    bs.B = rows;
+    bs.tokens_in = b->tok_in;
+    bs.tokens = b->tok;
+    bs.row_pos = b->row_pos;
+    bs.kc = b->kc;
+    bs.vc = b->vc;
+    bs.ks = b->ks;
+    bs.vs = b->vs;
+    bs.kv_format = b->kv_format;
+    bs.seq_elems = b->seq_elems;
+    bs.max_ctx = b->max_ctx;
+    bs.part = b->part;
+    bs.attn_scratch = b->attn;
+    bs.logits = b->logits;
+    bs.keys = b->keys;
+    bs.picks = b->picks;
+    bs.hidden = (b->m->debug & QW_DEBUG_HIDDEN) ? b->hidden : nullptr;
+    return bs;
+}
+
+// Launches the step's captured graph, capturing it first if this combination is new.
+int batch_launch(qw_batch *b, const qw::BatchStep &bs, int S, int tree) {
+    qw_model *m = b->m;
+    const int hid = bs.hidden != nullptr;
+    cudaGraphExec_t exec = nullptr;
+    for (auto &g : b->graphs)
+        if (g.B == bs.B && g.S == S && g.hidden == hid && g.tree == tree) exec = g.exec;
+    if (!exec) {  // capture this combination's launches once
+        qw::DecodeArgs a = m->args;
+        a.flags = b->flags;
+        if (cuda_status(cudaStreamBeginCapture(b->cap, cudaStreamCaptureModeThreadLocal))) return QW_CUDA_ERROR;
+        const int frc = qw::prefill_batch_step(&m->pf, a, bs, b->cap);
+        cudaGraph_t graph = nullptr;
+        const cudaError_t ce = cudaStreamEndCapture(b->cap, &graph);
+        if (frc || ce != cudaSuccess || !graph) {
+            if (graph) cudaGraphDestroy(graph);
+            cudaGetLastError();
+            return QW_CUDA_ERROR;
+        }
+        const cudaError_t ie = cudaGraphInstantiate(&exec, graph, 0);
+        cudaGraphDestroy(graph);
+        if (ie != cudaSuccess) return cuda_status(ie);
+        b->graphs.push_back({bs.B, S, hid, tree, exec});
+    }
+    return cuda_status(cudaGraphLaunch(exec, m->stream));
+}
+
+// The tree attention's grid and split follow the longest cache, rounded up to a power of two so that
+// a step's captured graph changes only when the cache doubles.
+int batch_len_bound(int n, int max_ctx) {
+    int s = 128;
+    while (s < n) s *= 2;
+    return s < max_ctx ? s : max_ctx;
+}
+
+}  // namespace
+
+extern "C" {
 
 int qw_batch_step(qw_batch *b, int32_t n_seq, const int32_t *tokens_host, int32_t *next_tokens_host) {
     if (!live_batch(b)) return QW_INVALID_HANDLE;
@@ -895,46 +1027,18 @@ int qw_batch_step(qw_batch *b, int32_t n_seq, const int32_t *tokens_host, int32_
         pos[s] = b->len[s];
         max_n = pos[s] + 1 > max_n ? pos[s] + 1 : max_n;
     }
+    b->tree_seq = -1;
     int rc = cuda_status(cudaMemcpyAsync(b->tok_in, tok, (size_t)n_seq * 4, cudaMemcpyHostToDevice, m->stream));
     if (!rc) rc = cuda_status(cudaMemcpyAsync(b->row_pos, pos, (size_t)n_seq * 4, cudaMemcpyHostToDevice, m->stream));
     if (rc) return rc;
-    qw::BatchStep bs{};
-    bs.B = n_seq;
-    bs.tokens_in = b->tok_in;
-    bs.tokens = b->tok;
-    bs.row_pos = b->row_pos;
+    qw::BatchStep bs = batch_step_of(b, n_seq);
     bs.max_n = max_n;
-    bs.kc = b->kc;
-    bs.vc = b->vc;
-    bs.seq_elems = b->seq_elems;
-    bs.max_ctx = b->max_ctx;
-    bs.part = b->part;
-    bs.logits = b->logits;
-    bs.keys = b->keys;
-    bs.picks = b->picks;
-    bs.hidden = (m->debug & QW_DEBUG_HIDDEN) ? b->hidden : nullptr;
-    qw::DecodeArgs a = m->args;
-    a.flags = b->flags;
-    const int S = qw::batch_splits(max_n), hid = bs.hidden != nullptr;
-    cudaGraphExec_t exec = nullptr;
-    for (auto &g : b->graphs)
-        if (g.B == n_seq && g.S == S && g.hidden == hid) exec = g.exec;
-    if (!exec) {  // capture this combination's launches once
-        if (cuda_status(cudaStreamBeginCapture(b->cap, cudaStreamCaptureModeThreadLocal))) return QW_CUDA_ERROR;
-        const int frc = qw::prefill_batch_step(&m->pf, a, bs, b->cap);
-        cudaGraph_t graph = nullptr;
-        const cudaError_t ce = cudaStreamEndCapture(b->cap, &graph);
-        if (frc || ce != cudaSuccess || !graph) {
-            if (graph) cudaGraphDestroy(graph);
-            cudaGetLastError();
-            return QW_CUDA_ERROR;
-        }
-        const cudaError_t ie = cudaGraphInstantiate(&exec, graph, 0);
-        cudaGraphDestroy(graph);
-        if (ie != cudaSuccess) return cuda_status(ie);
-        b->graphs.push_back({n_seq, S, hid, exec});
+    int S = qw::batch_splits(max_n);
+    if (b->kv_format == QW_KV_INT8_G32) {
+        bs.mask = b->ones;
+        bs.max_len = S = batch_len_bound(max_n, b->max_ctx);
     }
-    rc = cuda_status(cudaGraphLaunch(exec, m->stream));
+    rc = batch_launch(b, bs, S, 0);
     if (rc) return rc;
     for (int s = 0; s < n_seq; ++s) {
         b->len[s] += 1;
@@ -942,6 +1046,103 @@ int qw_batch_step(qw_batch *b, int32_t n_seq, const int32_t *tokens_host, int32_
     }
     b->last_n = n_seq;
     if (next_tokens_host) return batch_read(b, next_tokens_host, n_seq);
+    return QW_OK;
+}
+
+int qw_batch_tree_step(qw_batch *b, int32_t seq, int32_t n, const int32_t *tokens_host, const int32_t *parents_host,
+                       int32_t *picks_host) {
+    if (!live_batch(b)) return QW_INVALID_HANDLE;
+    if (b->failed) return b->failed;
+    qw_model *m = b->m;
+    if (seq < 0 || seq >= b->max_batch || n < 1 || n > b->max_batch || !tokens_host || !parents_host)
+        return QW_INVALID_ARGUMENT;
+    const int len = b->len[seq];
+    int pos[qw::kBatchMax], row[qw::kBatchMax], depth[qw::kBatchMax];
+    uint64_t mask[qw::kBatchMax];
+    for (int i = 0; i < n; ++i) {
+        const int p = parents_host[i], t = tokens_host[i];
+        if (p < -1 || p >= i || t < (i == 0 ? -1 : 0) || t >= m->cfg.vocab) return QW_INVALID_ARGUMENT;
+        if (t == -1 && !b->has_last[seq]) return QW_INVALID_ARGUMENT;
+        depth[i] = p < 0 ? 0 : depth[p] + 1;
+        mask[i] = (1ull << i) | (p < 0 ? 0ull : mask[p]);
+        pos[i] = len + depth[i];
+        row[i] = len + i;
+    }
+    if ((int64_t)len + n > b->max_ctx) return QW_CONTEXT_EXCEEDED;
+    b->tree_seq = -1;
+    int rc = cuda_status(cudaMemcpyAsync(b->tok_in, tokens_host, (size_t)n * 4, cudaMemcpyHostToDevice, m->stream));
+    if (!rc) rc = cuda_status(cudaMemcpyAsync(b->row_pos, pos, (size_t)n * 4, cudaMemcpyHostToDevice, m->stream));
+    if (!rc) rc = cuda_status(cudaMemcpyAsync(b->cache_pos, row, (size_t)n * 4, cudaMemcpyHostToDevice, m->stream));
+    if (!rc) rc = cuda_status(cudaMemcpyAsync(b->mask, mask, (size_t)n * 8, cudaMemcpyHostToDevice, m->stream));
+    if (!rc) rc = cuda_status(cudaMemcpyAsync(b->tree_len, &len, 4, cudaMemcpyHostToDevice, m->stream));
+    // node 0 without a token takes the sequence's last pick: the step reads and writes tree_picks
+    if (!rc) rc = cuda_status(cudaMemcpyAsync(b->tree_picks, b->picks + seq, 4, cudaMemcpyDeviceToDevice, m->stream));
+    if (rc) return rc;
+    const size_t esz = b->kv_format == QW_KV_INT8_G32 ? 1 : b->kv_format == QW_KV_F32 ? 4 : 2;
+    qw::BatchStep bs = batch_step_of(b, n);
+    bs.max_n = len + n;
+    bs.kc = b->kc + (size_t)seq * b->seq_elems * esz;
+    bs.vc = b->vc + (size_t)seq * b->seq_elems * esz;
+    if (b->ks) {
+        bs.ks = b->ks + (size_t)seq * (b->seq_elems / qw::kQGroup);
+        bs.vs = b->vs + (size_t)seq * (b->seq_elems / qw::kQGroup);
+    }
+    bs.seq_elems = 0;  // every row is this sequence's
+    bs.cache_pos = b->cache_pos;
+    bs.tree_len = b->tree_len;
+    bs.mask = b->mask;
+    bs.picks = b->tree_picks;
+    bs.max_len = batch_len_bound(len + n, b->max_ctx);
+    rc = batch_launch(b, bs, bs.max_len, 1 + seq);
+    if (rc) return rc;
+    b->last_n = n;
+    b->tree.assign(parents_host, parents_host + n);
+    b->tree_seq = seq;
+    if (!picks_host) return QW_OK;
+    rc = cuda_status(cudaMemcpyAsync(picks_host, b->tree_picks, (size_t)n * 4, cudaMemcpyDeviceToHost, m->stream));
+    return rc ? rc : batch_read(b, nullptr, 0);
+}
+
+int qw_batch_tree_accept(qw_batch *b, int32_t seq, int32_t n, const int32_t *nodes_host) {
+    if (!live_batch(b)) return QW_INVALID_HANDLE;
+    if (b->failed) return b->failed;
+    if (seq < 0 || seq != b->tree_seq || n < 0 || n > (int)b->tree.size() || (n > 0 && !nodes_host))
+        return QW_INVALID_ARGUMENT;
+    for (int i = 0; i < n; ++i) {  // a path from a root: each node the child of the one before
+        const int x = nodes_host[i];
+        if (x < 0 || x >= (int)b->tree.size() || b->tree[x] != (i ? nodes_host[i - 1] : -1)) return QW_INVALID_ARGUMENT;
+    }
+    qw_model *m = b->m;
+    b->tree_seq = -1;
+    if (n == 0) return QW_OK;
+    const bool is_q8 = b->kv_format == QW_KV_INT8_G32;
+    const size_t esz = is_q8 ? 1 : b->kv_format == QW_KV_F32 ? 4 : 2;
+    qw::BatchKeep k{};
+    k.kc = b->kc + (size_t)seq * b->seq_elems * esz;
+    k.vc = b->vc + (size_t)seq * b->seq_elems * esz;
+    if (is_q8) {
+        k.ks = b->ks + (size_t)seq * (b->seq_elems / qw::kQGroup);
+        k.vs = b->vs + (size_t)seq * (b->seq_elems / qw::kQGroup);
+    }
+    k.planes = m->cfg.n_layers * m->cfg.n_kv_heads;
+    k.max_ctx = b->max_ctx;
+    k.row_bytes = (int)(m->cfg.head_dim * esz);
+    k.start = b->len[seq];
+    k.n = n;
+    bool moves = false;
+    for (int i = 0; i < n; ++i) {
+        k.nodes[i] = nodes_host[i];
+        moves = moves || nodes_host[i] != i;
+    }
+    if (moves) {
+        const int rc = cuda_status(qw::launch_batch_keep(k, m->stream));
+        if (rc) return rc;
+    }
+    const int rc = cuda_status(cudaMemcpyAsync(b->picks + seq, b->tree_picks + nodes_host[n - 1], 4,
+                                               cudaMemcpyDeviceToDevice, m->stream));
+    if (rc) return rc;
+    b->len[seq] += n;
+    b->has_last[seq] = 1;
     return QW_OK;
 }
 

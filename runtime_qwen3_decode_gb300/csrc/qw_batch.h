@@ -41,8 +41,10 @@ struct BatchQkvPost {
     __half *q16;                             // [Hq][q_rows][128]: row b = sequence b's query heads
     int q_rows;
     void *kc, *vc;                           // this layer's planes of sequence 0: [Hkv][max_ctx][128]
+    __half *ks, *vs;                         // 8-bit cache: its scales' planes [Hkv][max_ctx][4]
     size_t seq_elems;                        // elements from one sequence's cache to the next one's
     int max_ctx;
+    const int *cache_pos;                    // [B] cache row of each row's k and v, or null: row_pos
 };
 
 struct BatchAttn {
@@ -75,7 +77,16 @@ cudaError_t batch_prepare();
 cudaError_t launch_bgemv(int epi, const BatchGemv &p, int nsm, cudaStream_t st, bool chained);
 // Row lengths the skinny projection is built for (launch_bgemv refuses the others).
 inline bool bgemv_supported(int K) { return K == 1024 || K == 2048 || K == 3072 || K == 4096 || K == 6144; }
-cudaError_t launch_bqkv_post(const BatchQkvPost &p, int kv_f32, cudaStream_t st, bool chained);
+cudaError_t launch_bqkv_post(const BatchQkvPost &p, int kv_format, cudaStream_t st, bool chained);
+// Rows of an accepted path of drafted nodes to their places: rows start + nodes[i] -> start + i of every
+// (layer, KV head) plane of one sequence's cache, i < n; nodes ascending, nodes[i] >= i.
+struct BatchKeep {
+    void *kc, *vc;      // the sequence's block [planes][max_ctx][row_bytes]
+    __half *ks, *vs;    // 8-bit cache: [planes][max_ctx][4], else null
+    int planes, max_ctx, row_bytes, start, n;
+    int nodes[kBatchMax];
+};
+cudaError_t launch_batch_keep(const BatchKeep &p, cudaStream_t st);
 cudaError_t launch_batch_tokens(const int32_t *in, const int32_t *picks, int B, int32_t *tokens, cudaStream_t st,
                                 bool chained);
 cudaError_t launch_batch_attn(const BatchAttn &p, int Hkv, int B, int kv_f32, cudaStream_t st, bool chained);

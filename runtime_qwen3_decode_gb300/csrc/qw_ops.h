@@ -21,7 +21,10 @@ cudaError_t launch_kv_read(const qw_kv_view &kv, const qw_kv_rows &dst, const in
                            cudaStream_t st);
 
 size_t tree_attn_scratch_bytes(int n_seq, int n_kv_heads, int n_max, int n_heads, int head_dim, int max_len);
-cudaError_t launch_tree_attn(const qw_kv_view &kv, const qw_tree_attention_args &a, void *scratch, cudaStream_t st);
+// chained: launch with programmatic stream serialization (the previous operation of the stream
+// must be a kernel).
+cudaError_t launch_tree_attn(const qw_kv_view &kv, const qw_tree_attention_args &a, void *scratch, cudaStream_t st,
+                             bool chained = false);
 
 cudaError_t launch_process_logits(const qw_process_logits_args &a, cudaStream_t st);
 

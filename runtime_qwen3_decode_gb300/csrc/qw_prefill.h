@@ -29,8 +29,18 @@ void prefill_destroy(PrefillState *st);
 inline bool prefill_supported(const PrefillState &st) { return st.ready != 0; }
 // Runs n prompt tokens at positions pos0.. and leaves logits + greedy pick of the last row
 // (flags->next_tok); debug bit 1 dumps the last row's hidden state after every layer.
+// q8: the cache is 8-bit (a.kc and a.vc are not used): each layer's K and V rows go through f32
+// rows stage_k, stage_v [Hkv][rows_max][128] into the sequence's block of codes
+// [L][Hkv][max_ctx][128] and scales [L][Hkv][max_ctx][4], and the prompt attends to what the cache
+// then holds.  start: a device int for the append.
+struct PrefillQ8 {
+    int8_t *kc, *vc;
+    __half *ks, *vs;
+    float *stage_k, *stage_v;
+    int32_t *start;
+};
 int prefill_run(PrefillState *st, const DecodeArgs &a, int pos0, const int32_t *tokens_host, int n, int debug,
-                cudaStream_t stream);
+                cudaStream_t stream, const PrefillQ8 *q8 = nullptr);
 // One batched decode step: B sequences, one new token each (their tokens resolved on the device:
 // -1 takes the sequence's previous pick).  Sequence b's cache is the block of seq_elems elements
 // starting seq_elems * b after kc / vc ([L][Hkv][max_ctx][128]); its new row goes to position
@@ -51,6 +61,15 @@ struct BatchStep {
     unsigned long long *keys;  // [B], zero
     int32_t *picks;            // [B] in (previous picks) and out
     float *hidden;             // optional [L + 1][B][H] residual stream dump
+    int kv_format;             // the caches' format (enum qw_kv_format)
+    __half *ks, *vs;           // 8-bit caches: scales of sequence 0, seq_elems / 32 from one to the next
+    // Rows that are the drafted nodes of one sequence's tree (else null): kc, vc are that sequence's,
+    // row b goes to cache row cache_pos[b] and attends to the tree_len[0] cached positions and the nodes of
+    // mask[b].  8-bit caches attend through the same operator, one node per sequence.
+    const int *cache_pos, *tree_len;
+    const uint64_t *mask;      // [B] (8-bit caches without a tree: ones)
+    void *attn_scratch;        // of the tree attention
+    int max_len;               // about the longest cache, for its split
 };
 int prefill_batch_step(PrefillState *st, const DecodeArgs &a, const BatchStep &bs, cudaStream_t stream);
 

@@ -52,6 +52,7 @@ __global__ void __launch_bounds__(kThreads) tree_kernel(const TreeArgs a) {
     float *red = sp + RT * kTile;                   // [kWarps * KPW - per row parts][D]
     __shared__ float salpha[RT], sm[RT], sl[RT];
     __shared__ unsigned long long smask[RT];
+    tc::chain_wait();
     tc::chain_release();
     const int b = blockIdx.z, h = blockIdx.y / a.row_tiles, rt = blockIdx.y % a.row_tiles, s = blockIdx.x;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -234,20 +235,20 @@ int splits(int n_seq, int Hkv, int row_tiles, int total) {
 }
 
 template <typename KV, int D, int RT>
-cudaError_t launch_tile(const TreeArgs &a, int n_seq, cudaStream_t st) {
+cudaError_t launch_tile(const TreeArgs &a, int n_seq, cudaStream_t st, bool chained) {
     constexpr int KPW = 128 / D, KW = RT < kWarps ? kWarps / RT : 1;
     constexpr int smem = (kTile * (D + 4) + kTile * D + RT * D + RT * kTile + RT * KW * KPW * D) * 4;
     cudaError_t e = cudaFuncSetAttribute(tree_kernel<KV, D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_k(false, tree_kernel<KV, D, RT>, dim3(a.S, a.Hkv * a.row_tiles, n_seq), dim3(kThreads), smem, st, a);
+    return launch_k(chained, tree_kernel<KV, D, RT>, dim3(a.S, a.Hkv * a.row_tiles, n_seq), dim3(kThreads), smem, st, a);
 }
 
 template <typename KV, int D>
-cudaError_t launch_rt(const TreeArgs &a, int n_seq, int rt, cudaStream_t st) {
-    cudaError_t e = rt == 2   ? launch_tile<KV, D, 2>(a, n_seq, st)
-                    : rt == 4 ? launch_tile<KV, D, 4>(a, n_seq, st)
-                    : rt == 8 ? launch_tile<KV, D, 8>(a, n_seq, st)
-                              : launch_tile<KV, D, 16>(a, n_seq, st);
+cudaError_t launch_rt(const TreeArgs &a, int n_seq, int rt, cudaStream_t st, bool ch) {
+    cudaError_t e = rt == 2   ? launch_tile<KV, D, 2>(a, n_seq, st, ch)
+                    : rt == 4 ? launch_tile<KV, D, 4>(a, n_seq, st, ch)
+                    : rt == 8 ? launch_tile<KV, D, 8>(a, n_seq, st, ch)
+                              : launch_tile<KV, D, 16>(a, n_seq, st, ch);
     if (e != cudaSuccess) return e;
     return launch_k(true, tree_merge_kernel<D>, dim3(a.n_max * a.G, a.Hkv, n_seq), dim3(D), 0, st, a);
 }
@@ -261,7 +262,8 @@ size_t tree_attn_scratch_bytes(int n_seq, int n_kv_heads, int n_max, int n_heads
     return std::max(cores, tree_tc_scratch_bytes(rows, head_dim));
 }
 
-cudaError_t launch_tree_attn(const qw_kv_view &kv, const qw_tree_attention_args &t, void *scratch, cudaStream_t st) {
+cudaError_t launch_tree_attn(const qw_kv_view &kv, const qw_tree_attention_args &t, void *scratch, cudaStream_t st,
+                             bool chained) {
     if (kv.n_seq == 0 || t.n_max == 0) return cudaSuccess;
     TreeArgs a{};
     a.k = (const uint8_t *)kv.k;
@@ -284,17 +286,17 @@ cudaError_t launch_tree_attn(const qw_kv_view &kv, const qw_tree_attention_args 
     a.G = t.n_heads / kv.n_kv_heads;
     a.scale_log2 = t.scale * kOpsLog2e;
     a.part = (float *)scratch;
-    if (t.dtype != QW_DT_F32) return launch_tree_tc(a, kv, t.max_len, scratch, st);
+    if (t.dtype != QW_DT_F32) return launch_tree_tc(a, kv, t.max_len, scratch, st, chained);
     const int rows = t.n_max * a.G, rt = rows_per_tile(rows);
     a.row_tiles = (rows + rt - 1) / rt;
     a.S = splits(kv.n_seq, kv.n_kv_heads, a.row_tiles, t.max_len + t.n_max);
     const int D = kv.head_dim;
     if (kv.format == QW_KV_F32)
-        return D == 128 ? launch_rt<float, 128>(a, kv.n_seq, rt, st) : launch_rt<float, 64>(a, kv.n_seq, rt, st);
+        return D == 128 ? launch_rt<float, 128>(a, kv.n_seq, rt, st, chained) : launch_rt<float, 64>(a, kv.n_seq, rt, st, chained);
     if (kv.format == QW_KV_BF16)
-        return D == 128 ? launch_rt<__nv_bfloat16, 128>(a, kv.n_seq, rt, st)
-                        : launch_rt<__nv_bfloat16, 64>(a, kv.n_seq, rt, st);
-    return D == 128 ? launch_rt<int8_t, 128>(a, kv.n_seq, rt, st) : launch_rt<int8_t, 64>(a, kv.n_seq, rt, st);
+        return D == 128 ? launch_rt<__nv_bfloat16, 128>(a, kv.n_seq, rt, st, chained)
+                        : launch_rt<__nv_bfloat16, 64>(a, kv.n_seq, rt, st, chained);
+    return D == 128 ? launch_rt<int8_t, 128>(a, kv.n_seq, rt, st, chained) : launch_rt<int8_t, 64>(a, kv.n_seq, rt, st, chained);
 }
 
 }  // namespace qw

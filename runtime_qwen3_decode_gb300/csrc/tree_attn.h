@@ -49,6 +49,7 @@ constexpr size_t kTcStatusBytes = 1024;  // one status word per CTA, then the pa
 static_assert(kTcCtas * 4 <= kTcStatusBytes, "status words");
 
 size_t tree_tc_scratch_bytes(int rows, int head_dim);
-cudaError_t launch_tree_tc(const TreeArgs &a, const qw_kv_view &kv, int max_len, void *scratch, cudaStream_t st);
+cudaError_t launch_tree_tc(const TreeArgs &a, const qw_kv_view &kv, int max_len, void *scratch, cudaStream_t st,
+                           bool chained);
 
 }  // namespace qw

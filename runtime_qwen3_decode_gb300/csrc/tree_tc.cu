@@ -993,7 +993,7 @@ bool plane_map(CUtensorMap *m, const void *ptr, const qw_kv_view &kv, CUtensorMa
 int slot_rows(int rows) { return std::min(kTcRows, (rows + 31) / 32 * 32); }
 
 template <int SRC, int D, int TERMS>
-cudaError_t launch_src(const TcParams &p, const qw_kv_view &kv, int ctas, cudaStream_t st) {
+cudaError_t launch_src(const TcParams &p, const qw_kv_view &kv, int ctas, cudaStream_t st, bool chained) {
     using C = Cfg<SRC, D, TERMS>;
     CUtensorMap mk, mv;
     const CUtensorMapDataType type = C::kElem == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
@@ -1005,7 +1005,7 @@ cudaError_t launch_src(const TcParams &p, const qw_kv_view &kv, int ctas, cudaSt
         return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel<SRC, D, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_k(false, tree_tc_kernel<SRC, D, TERMS>, dim3(ctas), dim3(C::kThreads), C::kSmem, st, mk, mv, p);
+    e = launch_k(chained, tree_tc_kernel<SRC, D, TERMS>, dim3(ctas), dim3(C::kThreads), C::kSmem, st, mk, mv, p);
     if (e != cudaSuccess) return e;
     const int nrt = (p.a.n_max * p.a.G + kTcRows - 1) / kTcRows;
     const int units = std::min(kTcRows, p.a.n_max * p.a.G) * (D / 4);
@@ -1018,13 +1018,13 @@ cudaError_t launch_src(const TcParams &p, const qw_kv_view &kv, int ctas, cudaSt
 // left a relative error of 5.5e-4 where the result's rounding leaves 2.1e-4), so K and V
 // that fp16 does not hold exactly come as two terms.
 template <int D>
-cudaError_t launch_dim(const TcParams &p, const qw_kv_view &kv, int ctas, cudaStream_t st) {
+cudaError_t launch_dim(const TcParams &p, const qw_kv_view &kv, int ctas, cudaStream_t st, bool ch) {
     const bool f16 = p.a.dtype == QW_DT_F16;
     if (kv.format == QW_KV_INT8_G32)
-        return f16 ? launch_src<SRC_Q8_F16, D, 2>(p, kv, ctas, st) : launch_src<SRC_Q8_F16, D, 1>(p, kv, ctas, st);
+        return f16 ? launch_src<SRC_Q8_F16, D, 2>(p, kv, ctas, st, ch) : launch_src<SRC_Q8_F16, D, 1>(p, kv, ctas, st, ch);
     if (kv.format == QW_KV_BF16)
-        return f16 ? launch_src<SRC_BF16_F16, D, 1>(p, kv, ctas, st) : launch_src<SRC_BF16, D, 1>(p, kv, ctas, st);
-    return f16 ? launch_src<SRC_F32_F16, D, 2>(p, kv, ctas, st) : launch_src<SRC_F32_F16, D, 1>(p, kv, ctas, st);
+        return f16 ? launch_src<SRC_BF16_F16, D, 1>(p, kv, ctas, st, ch) : launch_src<SRC_BF16, D, 1>(p, kv, ctas, st, ch);
+    return f16 ? launch_src<SRC_F32_F16, D, 2>(p, kv, ctas, st, ch) : launch_src<SRC_F32_F16, D, 1>(p, kv, ctas, st, ch);
 }
 
 }  // namespace
@@ -1033,7 +1033,8 @@ size_t tree_tc_scratch_bytes(int rows, int head_dim) {
     return kTcStatusBytes + (size_t)2 * kTcCtas * (head_dim + 2) * slot_rows(rows) * 4;
 }
 
-cudaError_t launch_tree_tc(const TreeArgs &a, const qw_kv_view &kv, int max_len, void *scratch, cudaStream_t st) {
+cudaError_t launch_tree_tc(const TreeArgs &a, const qw_kv_view &kv, int max_len, void *scratch, cudaStream_t st,
+                           bool chained) {
     TcParams p{};
     p.a = a;
     p.n_seq = kv.n_seq;
@@ -1043,7 +1044,7 @@ cudaError_t launch_tree_tc(const TreeArgs &a, const qw_kv_view &kv, int max_len,
     const int nrt = (a.n_max * a.G + kTcRows - 1) / kTcRows;
     const long long tiles = (long long)kv.n_seq * kv.n_kv_heads * nrt * ((max_len + a.n_max + kTcTile - 1) / kTcTile);
     const int ctas = (int)std::min<long long>(kTcCtas, tiles);
-    return kv.head_dim == 128 ? launch_dim<128>(p, kv, ctas, st) : launch_dim<64>(p, kv, ctas, st);
+    return kv.head_dim == 128 ? launch_dim<128>(p, kv, ctas, st, chained) : launch_dim<64>(p, kv, ctas, st, chained);
 }
 
 }  // namespace qw

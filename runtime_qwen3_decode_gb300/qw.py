@@ -61,7 +61,8 @@ EXPORTS = ("qw_workspace_bytes", "qw_model_create", "qw_prefill", "qw_decode_ste
            "qw_batch_logits", "qw_batch_debug_hidden", "qw_batch_sync", "qw_checkpoint_open",
            "qw_checkpoint_close", "qw_checkpoint_last_error", "qw_checkpoint_count", "qw_checkpoint_tensor",
            "qw_checkpoint_check", "qw_checkpoint_upload_bytes", "qw_checkpoint_upload", "qw_kv_append", "qw_kv_read",
-           "qw_tree_attention_scratch_bytes", "qw_tree_attention", "qw_process_logits")
+           "qw_tree_attention_scratch_bytes", "qw_tree_attention", "qw_process_logits", "qw_batch_workspace_bytes_kv",
+           "qw_batch_create_kv", "qw_batch_tree_step", "qw_batch_tree_accept")
 DT_BF16, DT_F16, DT_F32, DT_I8, DT_Q8_0 = 0, 1, 2, 3, 4
 BATCH_MAX = 8
 TREE_NODES_MAX = 64
@@ -195,6 +196,11 @@ def _lib():
             L.qw_batch_logits.argtypes = [vp, vp, i64]
             L.qw_batch_debug_hidden.argtypes = [vp, vp, i64]
             L.qw_batch_sync.argtypes = [vp]
+            L.qw_batch_workspace_bytes_kv.argtypes = [vp, i32, i32, i32]
+            L.qw_batch_workspace_bytes_kv.restype = ctypes.c_size_t
+            L.qw_batch_create_kv.argtypes = [vp, i32, i32, i32, vp, ctypes.c_size_t, ctypes.POINTER(ctypes.c_void_p)]
+            L.qw_batch_tree_step.argtypes = [vp, i32, i32, i32p, i32p, i32p]
+            L.qw_batch_tree_accept.argtypes = [vp, i32, i32, i32p]
             u64 = ctypes.c_uint64
             L.qw_checkpoint_open.argtypes = [vp, u64, u64, ctypes.POINTER(ctypes.c_void_p)]
             L.qw_checkpoint_close.argtypes = [vp]
@@ -719,21 +725,23 @@ class Model:
 
 class Batch:
     """Up to BATCH_MAX sequences of one Model decoded together (qw_batch_*), each with its own
-    K/V cache and length; workspace from torch on the model's device."""
+    K/V cache and length; workspace from torch on the model's device.  kv_format: KV_INT8_G32
+    for 8-bit caches, None for the model's format."""
 
-    def __init__(self, model: "Model", max_batch: int, max_ctx: int):
+    def __init__(self, model: "Model", max_batch: int, max_ctx: int, kv_format: int | None = None):
         import torch
 
         self.model = model
         self.max_batch = max_batch
         self.max_ctx = max_ctx
-        n = _lib().qw_batch_workspace_bytes(model._h, max_batch, max_ctx)
+        self.kv_format = model.cfg.kv_format if kv_format is None else kv_format
+        n = _lib().qw_batch_workspace_bytes_kv(model._h, max_batch, max_ctx, self.kv_format)
         if n == 0:
-            raise QwError(INVALID_ARGUMENT, "qw_batch_workspace_bytes")
+            raise QwError(INVALID_ARGUMENT, "qw_batch_workspace_bytes_kv")
         self.workspace = torch.empty(n, dtype=torch.uint8, device="cuda")
         h = ctypes.c_void_p()
-        _check(_lib().qw_batch_create(model._h, max_batch, max_ctx, self.workspace.data_ptr(), n, ctypes.byref(h)),
-               "qw_batch_create")
+        _check(_lib().qw_batch_create_kv(model._h, max_batch, max_ctx, self.kv_format, self.workspace.data_ptr(), n,
+                                         ctypes.byref(h)), "qw_batch_create_kv")
         self._h = h
         self.last_n = 0
 
@@ -770,6 +778,25 @@ class Batch:
         _check(_lib().qw_batch_step(self._h, n_seq, t, out if want_tokens else None), "qw_batch_step")
         self.last_n = n_seq
         return list(out) if want_tokens else None
+
+    def tree_step(self, seq: int, tokens, parents, want_picks: bool = True):
+        """qw_batch_tree_step: drafted tokens of sequence seq in one step (parents[i] < i, -1 = a continuation
+        of the cache; tokens[0] = -1: its last pick); the nodes' greedy picks, or None."""
+        n = len(tokens)
+        if len(parents) != n:
+            raise ValueError("tokens and parents must have the same length")
+        t = (ctypes.c_int32 * n)(*[int(x) for x in tokens])
+        p = (ctypes.c_int32 * n)(*[int(x) for x in parents])
+        out = (ctypes.c_int32 * n)()
+        _check(_lib().qw_batch_tree_step(self._h, seq, n, t, p, out if want_picks else None), "qw_batch_tree_step")
+        self.last_n = n
+        return list(out) if want_picks else None
+
+    def tree_accept(self, seq: int, nodes):
+        """qw_batch_tree_accept: keep the path `nodes` of the sequence's last tree step."""
+        n = len(nodes)
+        _check(_lib().qw_batch_tree_accept(self._h, seq, n, (ctypes.c_int32 * n)(*[int(x) for x in nodes]) if n else None),
+               "qw_batch_tree_accept")
 
     def logits(self):
         import torch
