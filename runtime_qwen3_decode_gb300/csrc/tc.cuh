@@ -85,6 +85,27 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *b, unsigned parity, volatile
     }
 }
 
+// mbar_wait that lets the hardware suspend the thread for up to ~1 us at a time instead of polling:
+// for kernels whose waiting warps share an SM sub-partition with working ones.
+__device__ __forceinline__ bool mbar_sleep(uint64_t *b, unsigned parity, volatile int *abort, bool watch_abort,
+                                           unsigned long long limit_ns) {
+    if (mbar_test(b, parity)) return true;
+    const unsigned long long t0 = gtime();
+    for (;;) {
+        unsigned ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(su32(b)), "r"(parity), "r"(1000u)
+            : "memory");
+        if (ok) return true;
+        if (watch_abort && *abort) return false;
+        if (gtime() - t0 > limit_ns) return false;
+    }
+}
+
 // ---------------------------------------------------------------- proxies
 
 // Orders this thread's generic-proxy shared-memory writes before later async-proxy
@@ -102,6 +123,12 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const void *tmap, int x, 
         "l"(tmap), "r"(x), "r"(y), "r"(su32(bar))
         : "memory");
 }
+
+// 16 bytes from global to shared memory without a register; wait_copies waits for all of this thread's.
+__device__ __forceinline__ void copy16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(su32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Brings a tensor map (a kernel parameter) into the descriptor cache.
 __device__ __forceinline__ void prefetch_map(const void *tmap) {

@@ -80,6 +80,8 @@ struct TcParams {
     int n_seq, rows_max;  // rows_max: query rows per partial slot (a multiple of 32)
     int *status;
     float *part;          // [2 CTAs][D + 2][rows_max]
+    unsigned long long inv_g;  // 2^32 / G + 1: row / G for the at most 4096 rows of a KV head
+    __device__ __forceinline__ int node_of(int row) const { return (int)((unsigned)row * inv_g >> 32); }
 };
 
 __device__ __forceinline__ int seq_tiles(int total) { return (total + kTcTile - 1) / kTcTile; }
@@ -93,7 +95,9 @@ __device__ __forceinline__ long long seq_work(const TcParams &p, int b) {
 }
 
 // A CTA's share is tiles [T c / C, T (c + 1) / C).
-__device__ __forceinline__ long long share_start(long long T, int c, int C) { return T * c / C; }
+__device__ __forceinline__ long long share_start(long long T, int c, int C) {
+    return T < (1 << 24) ? (long long)((unsigned)T * (unsigned)c / (unsigned)C) : T * c / C;  // C <= 152
+}
 
 struct Cursor {
     int b, h, rt, tile;
@@ -163,10 +167,11 @@ __device__ Cursor find_start(const TcParams &p, long long at, long long left) {
             int len, n;
             lengths(p.a, c.b, len, n);
             const int tiles = seq_tiles(len + n), nrt = (n * p.a.G + kTcRows - 1) / kTcRows;
-            const long long item = rest / tiles;
-            c.tile = (int)(rest % tiles);
-            c.rt = (int)(item % nrt);
-            c.h = (int)(item / nrt);
+            // rest is below one sequence's tiles: 2^31 / 128 positions x 1024 heads x 32 row tiles
+            const unsigned long long item = rest < (1ll << 32) ? (unsigned)rest / (unsigned)tiles : rest / tiles;
+            c.tile = (int)(rest - (long long)item * tiles);
+            c.h = (int)(item / (unsigned)nrt);
+            c.rt = (int)(item - (unsigned long long)c.h * nrt);
             return c;
         }
         before += __shfl_sync(0xffffffffu, upto, 31);
@@ -183,7 +188,7 @@ __device__ __forceinline__ uint8_t *smem_base() {
 
 __device__ __forceinline__ bool warp_wait(uint64_t *b, unsigned parity, volatile int *abort) {
     int ok = 1;
-    if ((threadIdx.x & 31) == 0) ok = mbar_wait(b, parity, abort, true, kWaitLimitNs);
+    if ((threadIdx.x & 31) == 0) ok = mbar_sleep(b, parity, abort, true, kWaitLimitNs);
     return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
@@ -342,7 +347,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                     for (int t = s.t0; ok && t < s.t1; ++t, ++it) {
                         const int st = it % ST;
                         const unsigned ph = (unsigned)(it / ST) & 1u;
-                        if (!mbar_wait(&k_empty[st], ph ^ 1u, abort, true, kWaitLimitNs)) {
+                        if (!mbar_sleep(&k_empty[st], ph ^ 1u, abort, true, kWaitLimitNs)) {
                             ok = false;
                             break;
                         }
@@ -350,7 +355,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                         for (int r = 0; r < D / 64; ++r)
                             tma_load_4d(sK + st * C::kOperand + r * C::kRegion, &tk, 64 * r, t * kTcTile, s.h, s.b, &k_full[st]);
                         kp[st] = (int)ph;
-                        if (!mbar_wait(&v_empty[st], ph ^ 1u, abort, true, kWaitLimitNs)) {
+                        if (!mbar_sleep(&v_empty[st], ph ^ 1u, abort, true, kWaitLimitNs)) {
                             ok = false;
                             break;
                         }
@@ -363,8 +368,8 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                 if (!ok) *abort = 1;
                 // no copy may land in shared memory after this CTA has exited, whoever gave up
                 for (int i = 0; i < ST; ++i) {
-                    if (kp[i] >= 0) mbar_wait(&k_full[i], (unsigned)kp[i], abort, false, kWaitLimitNs);
-                    if (vp[i] >= 0) mbar_wait(&v_full[i], (unsigned)vp[i], abort, false, kWaitLimitNs);
+                    if (kp[i] >= 0) mbar_sleep(&k_full[i], (unsigned)kp[i], abort, false, kWaitLimitNs);
+                    if (vp[i] >= 0) mbar_sleep(&v_full[i], (unsigned)vp[i], abort, false, kWaitLimitNs);
                 }
             } else {
                 int rp[4] = {-1, -1, -1, -1};
@@ -373,7 +378,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                 while (ok && next_seg(p, cur, s)) {
                     for (int t = s.t0; ok && t < s.t1; ++t)
                         for (int ch = 0; ch < 2 * C::kChunks; ++ch) {
-                            if (!mbar_wait(&r_empty[slot], ph ^ 1u, abort, true, kWaitLimitNs)) {
+                            if (!mbar_sleep(&r_empty[slot], ph ^ 1u, abort, true, kWaitLimitNs)) {
                                 ok = false;
                                 break;
                             }
@@ -386,7 +391,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                 }
                 if (!ok) *abort = 1;
                 for (int i = 0; i < C::kRing; ++i)
-                    if (rp[i] >= 0) mbar_wait(&r_full[i], (unsigned)rp[i], abort, false, kWaitLimitNs);
+                    if (rp[i] >= 0) mbar_sleep(&r_full[i], (unsigned)rp[i], abort, false, kWaitLimitNs);
             }
         }
     } else if (warp == kMmaWarp) {
@@ -398,11 +403,11 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
             int it = 0, seg = 0;  // it: tiles before this segment
             while (ok && next_seg(p, cur, s)) {
                 const int nt = s.t1 - s.t0;
-                ok = mbar_wait(q_full, (unsigned)seg & 1u, abort, true, kWaitLimitNs);
+                ok = mbar_sleep(q_full, (unsigned)seg & 1u, abort, true, kWaitLimitNs);
                 for (int j = -1; ok && j < nt; ++j) {
                     if (j + 1 < nt) {
                         const int jn = it + j + 1, st = jn % ST;
-                        if (!mbar_wait(&k_full[st], (unsigned)(jn / ST) & 1u, abort, true, kWaitLimitNs)) {
+                        if (!mbar_sleep(&k_full[st], (unsigned)(jn / ST) & 1u, abort, true, kWaitLimitNs)) {
                             ok = false;
                             break;
                         }
@@ -419,8 +424,8 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                     }
                     if (j >= 0) {
                         const int jj = it + j, st = jj % ST;
-                        if (!mbar_wait(&v_full[st], (unsigned)(jj / ST) & 1u, abort, true, kWaitLimitNs) ||
-                            !mbar_wait(&p_full[jj & 1], (unsigned)(jj >> 1) & 1u, abort, true, kWaitLimitNs)) {
+                        if (!mbar_sleep(&v_full[st], (unsigned)(jj / ST) & 1u, abort, true, kWaitLimitNs) ||
+                            !mbar_sleep(&p_full[jj & 1], (unsigned)(jj >> 1) & 1u, abort, true, kWaitLimitNs)) {
                             ok = false;
                             break;
                         }
@@ -441,7 +446,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
             }
             if (!ok) *abort = 1;
             mma_commit(drain);  // every MMA completes before TMEM is released
-            mbar_wait(drain, 0, abort, false, kWaitLimitNs);
+            mbar_sleep(drain, 0, abort, false, kWaitLimitNs);
         }
     } else if (warp < kSoftWarps) {
         // ---- softmax and epilogue: group grp, TMEM lane quarter q, one query row per lane
@@ -453,56 +458,52 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
         while (ok && next_seg(p, cur, s)) {
             const int row = s.r0 + r, nt = s.t1 - s.t0, nr = min(kTcRows, s.rows - s.r0);
             const bool live = r < nr, warp_live = 32 * q < nr;
-            const int node = live ? row / a.G : 0, head = s.h * a.G + (live ? row % a.G : 0);
+            const int node = live ? p.node_of(row) : 0, head = s.h * a.G + (live ? row - node * a.G : 0);
             unsigned long long mask = live ? a.mask[(int64_t)s.b * a.n_max + node] : 0ull;
-            if (s.n < 64) mask &= (1ull << s.n) - 1ull;
-            // Q into its swizzled tile: D / 8 lanes per row, the eight warps take the live rows in turn,
-            // every load of a warp in flight at once.  A negative scale flips the signs, a scale of 0
-            // makes them 0.
+            // Q into its swizzled tile: D / 8 lanes per row, the eight warps take the live rows in turn, all
+            // copies in flight at once.  Then, in place: bf16 queries to fp16 (the row divided by 2^e, 2^e <=
+            // amax < 2^(e + 1)), a negative scale flips the signs, a scale of 0 makes them 0.
             {
-                constexpr int LPR = D / 8, RPP = 8 * 32 / LPR, PASSES = kTcRows / RPP;  // rows per pass of all warps
+                constexpr int LPR = D / 8, RPP = 8 * 32 / LPR;  // lanes per row; rows per pass of all warps
                 const int c = lane % LPR, first = warp * (32 / LPR) + lane / LPR;
-                const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
                 const bool scaled = SRC != SRC_BF16 && a.dtype == QW_DT_BF16;
-                uint4 u[PASSES];
-#pragma unroll
-                for (int i = 0; i < PASSES; ++i) {
-                    const int x = first + RPP * i, rx = s.r0 + x;
-                    u[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (x < nr && a.scale_log2 != 0.f)
-                        u[i] = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(a.q) + s.b * a.qseq +
-                                                               (rx / a.G) * a.qnode + (s.h * a.G + rx % a.G) * a.qhead)[c];
+                const uint16_t *qb = reinterpret_cast<const uint16_t *>(a.q) + s.b * a.qseq + (int64_t)s.h * a.G * a.qhead + 8 * c;
+                uint8_t *tile = sQ + (c >> 3) * C::kRegion;
+                for (int x = first; x < nr; x += RPP) {
+                    const int nd = p.node_of(s.r0 + x), g = s.r0 + x - nd * a.G;
+                    copy16(tile + swz128(x, c & 7), qb + nd * a.qnode + g * a.qhead);
                 }
+                wait_copies();
+                if (scaled || a.scale_log2 <= 0.f) {
+                    const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+                    for (int x0 = first - lane / LPR; x0 < nr; x0 += RPP) {  // whole warps: x0 is the warp's first row
+                        const int x = x0 + lane / LPR;
+                        uint4 *at = reinterpret_cast<uint4 *>(tile + swz128(x, c & 7));
+                        uint4 u = x < nr ? *at : make_uint4(0u, 0u, 0u, 0u);
+                        uint32_t *w = reinterpret_cast<uint32_t *>(&u);
+                        if (scaled) {
+                            float f[8], amax = 0.f, up = 1.f, down = 1.f;
 #pragma unroll
-                for (int i = 0; i < PASSES; ++i) {
-                    const int x = first + RPP * i;
-                    uint32_t *w = reinterpret_cast<uint32_t *>(&u[i]);
-                    float down = 1.f;
-                    if (scaled) {  // bf16 queries as fp16: the row divided by 2^e, 2^e <= amax < 2^(e + 1)
-                        float f[8], amax = 0.f;
+                            for (int k = 0; k < 4; ++k) {
+                                const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[k]));
+                                f[2 * k] = v.x;
+                                f[2 * k + 1] = v.y;
+                                amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
+                            }
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[k]));
-                            f[2 * k] = v.x;
-                            f[2 * k + 1] = v.y;
-                            amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
+                            for (int o = LPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                            if (amax > 0.f && amax < INFINITY) {
+                                const int e = min(max((int)((__float_as_uint(amax) >> 23) & 255u) - 127, -126), 126);
+                                up = __uint_as_float((uint32_t)(127 - e) << 23);
+                                down = __uint_as_float((uint32_t)(127 + e) << 23);
+                            }
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) w[k] = pack2<false>(f[2 * k] * up, f[2 * k + 1] * up);
+                            if (c == 0 && x < nr) row_scale[x] = down;
                         }
 #pragma unroll
-                        for (int o = LPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                        float up = 1.f;
-                        if (amax > 0.f && amax < INFINITY) {
-                            const int e = min(max((int)((__float_as_uint(amax) >> 23) & 255u) - 127, -126), 126);
-                            up = __uint_as_float((uint32_t)(127 - e) << 23);
-                            down = __uint_as_float((uint32_t)(127 + e) << 23);
-                        }
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) w[k] = pack2<false>(f[2 * k] * up, f[2 * k + 1] * up);
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) w[k] ^= flip;
-                    if (x < nr) {
-                        *reinterpret_cast<uint4 *>(sQ + (c >> 3) * C::kRegion + swz128(x, c & 7)) = u[i];
-                        if (c == 0) row_scale[x] = down;
+                        for (int k = 0; k < 4; ++k) w[k] = a.scale_log2 == 0.f ? 0u : w[k] ^ flip;
+                        if (x < nr) *at = u;
                     }
                 }
                 fence_async_shared();
@@ -513,7 +514,9 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                     break;
                 }
             }
-            const float sc = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2) * (live ? row_scale[r] : 1.f);
+            if (s.n < 64) mask &= (1ull << s.n) - 1ull;
+            const bool scaled_row = SRC != SRC_BF16 && a.dtype == QW_DT_BF16 && live;
+            const float sc = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2) * (scaled_row ? row_scale[r] : 1.f);
             float m_used = -INFINITY, l = 0.f;
             int mine = 0;  // tiles of this segment that this group has done
             for (int j = (it & 1) == grp ? 0 : 1; ok && j < nt; j += 2, ++mine) {
@@ -585,20 +588,23 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                         float v[32];
                         tmem_ld32(tS + 32u * c, v);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = fast_exp2(fmaf(v[i], sc, -mm));
+                        for (int i = 0; i < 32; i += 2) {
+                            const float2 z = __ffma2_rn(make_float2(v[i], v[i + 1]), make_float2(sc, sc), make_float2(-mm, -mm));
+                            v[i] = fast_exp2(z.x);
+                            v[i + 1] = fast_exp2(z.y);
+                        }
                         if (vis != 0xffffffffu) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i) v[i] = (vis >> i) & 1u ? v[i] : 0.f;
                         }
                         uint32_t pk[16];
-                        float l1 = 0.f;
+                        float2 l2 = make_float2(0.f, 0.f);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            l += v[2 * i];
-                            l1 += v[2 * i + 1];
+                            l2 = __fadd2_rn(l2, make_float2(v[2 * i], v[2 * i + 1]));
                             pk[i] = pack2<C::kBf16>(v[2 * i], v[2 * i + 1]);
                         }
-                        l += l1;
+                        l += l2.x + l2.y;
                         tmem_st16u(tS + 16u * c, pk);
                     }
                 }
@@ -861,29 +867,26 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
 
 // Merge of the items that were cut: thread = (row, four dims) of one (row tile, KV head, sequence).
 // The partials lie row-fastest, so a warp's loads are runs of neighbours, and the loads of
-// kMergeBatch partials are in flight at once: this kernel is nothing but their latency.  Also
-// fills the rows of sequences that do not fit with NaN, and every row if a CTA gave up.
-constexpr int kMergeThreads = 256;
-constexpr int kMergeBatch = 6;
+// kMergeBatch partials are in flight at once: this kernel is nothing but their latency.  What
+// does not depend on the partials comes before the wait for them, and small blocks without
+// shared memory find room beside the attention's, so that they are there when it ends.
+// Also fills the rows of sequences that do not fit with NaN, and every row if a CTA gave up.
+constexpr int kMergeThreads = 128;
+constexpr int kMergeBatch = 8;
 
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) tree_tc_merge_kernel(const TcParams p, int ctas) {
     const TreeArgs &a = p.a;
-    __shared__ long long sh_before[kMergeThreads / 32], sh_total[kMergeThreads / 32];
     const int nrt_max = (a.n_max * a.G + kTcRows - 1) / kTcRows;
     const int rt = blockIdx.x % nrt_max, h = blockIdx.x / nrt_max, b = blockIdx.y;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    chain_wait();
+    const int tid = threadIdx.x, lane = tid & 31;
     int len, n;
     const bool fits = lengths(a, b, len, n);
     const int rows = (fits ? n : a.n_max) * a.G, r0 = rt * kTcRows;
     const int nr = min(kTcRows, rows - r0);
-    const int e0 = blockIdx.z * kMergeThreads;  // this CTA's first (row, four dims)
-    if (e0 >= nr * (D / 4)) return;
-    int gave_up = 0;
-    for (int i = tid; i < ctas; i += kMergeThreads) gave_up |= p.status[i];
+    const int e = blockIdx.z * kMergeThreads + tid, rl = nr > 0 ? e % nr : 0, dq = nr > 0 ? e / nr : D, r = r0 + rl;
     long long before = 0, total = 0;
-    for (int i = tid; i < p.n_seq; i += kMergeThreads) {
+    for (int i = lane; i < p.n_seq; i += 32) {
         const long long w = seq_work(p, i);
         total += w;
         if (i < b) before += w;
@@ -893,39 +896,34 @@ __global__ void __launch_bounds__(kMergeThreads) tree_tc_merge_kernel(const TcPa
         before += __shfl_xor_sync(0xffffffffu, before, o);
         total += __shfl_xor_sync(0xffffffffu, total, o);
     }
-    if (lane == 0) sh_before[warp] = before, sh_total[warp] = total;
-    gave_up = __syncthreads_or(gave_up);
-    const int e = e0 + tid, rl = e % nr, dq = e / nr, r = r0 + rl;
-    if (dq >= D / 4) return;
-    const int64_t at = b * a.oseq + (int64_t)(r / a.G) * a.onode + (int64_t)(h * a.G + r % a.G) * a.ohead + 4 * dq;
-    if (!fits || gave_up) {
-        for (int i = 0; i < 4; ++i) store_out(a, at + i, nanf(""));
-        return;
-    }
-    before = total = 0;
-    for (int i = 0; i < kMergeThreads / 32; ++i) before += sh_before[i], total += sh_total[i];
     const int nrt = (n * a.G + kTcRows - 1) / kTcRows, tiles = seq_tiles(len + n);
-    const long long t0 = before + ((long long)h * nrt + rt) * tiles, t1 = t0 + tiles;
-    // owner of tile t: the largest c with T c / C <= t
-    const int c0 = (int)(((t0 + 1) * ctas - 1) / total), c1 = (int)((t1 * ctas - 1) / total);
-    if (c0 == c1) return;  // finished by its one CTA
+    int c0 = 0, c1 = 0;
+    if (fits && n > 0) {
+        // owner of tile t: the largest c with T c / C <= t
+        const long long t0 = before + ((long long)h * nrt + rt) * tiles, t1 = t0 + tiles;
+        c0 = (int)(total < (1 << 24) ? ((unsigned)(t0 + 1) * (unsigned)ctas - 1) / (unsigned)total : ((t0 + 1) * ctas - 1) / total);
+        c1 = (int)(total < (1 << 24) ? ((unsigned)t1 * (unsigned)ctas - 1) / (unsigned)total : (t1 * ctas - 1) / total);
+    }
     // c0 holds the item's first tile: its second slot; the later CTAs begin inside the item: their
     // first.  Where there are more CTAs than tiles some shares are empty.
     const size_t slot = (size_t)(D + 2) * p.rows_max;
     const bool gaps = total < ctas;
     auto partial = [&](int c) { return p.part + (size_t)(2 * c + (c == c0 ? 1 : 0)) * slot + rl; };
     auto holds = [&](int c) { return c <= c1 && !(gaps && share_start(total, c, ctas) == share_start(total, c + 1, ctas)); };
-    float mx = -INFINITY;
-    for (int c = c0; c <= c1; c += kMergeBatch) {
-        float m[kMergeBatch];
-#pragma unroll
-        for (int i = 0; i < kMergeBatch; ++i) m[i] = holds(c + i) ? partial(c + i)[(size_t)D * p.rows_max] : -INFINITY;
-#pragma unroll
-        for (int i = 0; i < kMergeBatch; ++i) mx = fmaxf(mx, m[i]);
+    chain_wait();
+    int gave_up = 0;
+    for (int i = lane; i < ctas; i += 32) gave_up |= p.status[i];
+    gave_up = __any_sync(0xffffffffu, gave_up);
+    if (dq >= D / 4) return;
+    const int64_t at = b * a.oseq + (int64_t)p.node_of(r) * a.onode + (int64_t)(h * a.G + r - p.node_of(r) * a.G) * a.ohead + 4 * dq;
+    if (!fits || gave_up) {
+        for (int i = 0; i < 4; ++i) store_out(a, at + i, nanf(""));
+        return;
     }
-    float num[4] = {0.f, 0.f, 0.f, 0.f}, den = 0.f;
+    if (c0 == c1) return;  // finished by its one CTA
+    float mx = -INFINITY, num[4] = {0.f, 0.f, 0.f, 0.f}, den = 0.f;
     for (int c = c0; c <= c1; c += kMergeBatch) {
-        float m[kMergeBatch], l[kMergeBatch], v[kMergeBatch][4];
+        float m[kMergeBatch], l[kMergeBatch], v[kMergeBatch][4], top = mx;
 #pragma unroll
         for (int i = 0; i < kMergeBatch; ++i) {
             const bool is = holds(c + i);
@@ -935,6 +933,13 @@ __global__ void __launch_bounds__(kMergeThreads) tree_tc_merge_kernel(const TcPa
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[i][k] = is ? src[(size_t)(4 * dq + k) * p.rows_max] : 0.f;
         }
+#pragma unroll
+        for (int i = 0; i < kMergeBatch; ++i) top = fmaxf(top, m[i]);
+        const float old = mx == -INFINITY ? 0.f : exp2f(mx - top);
+        mx = top;
+        den *= old;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) num[k] *= old;
 #pragma unroll
         for (int i = 0; i < kMergeBatch; ++i) {
             if (m[i] == -INFINITY && l[i] == 0.f) continue;  // the share showed the row nothing
@@ -1039,6 +1044,7 @@ cudaError_t launch_tree_tc(const TreeArgs &a, const qw_kv_view &kv, int max_len,
     p.a = a;
     p.n_seq = kv.n_seq;
     p.rows_max = slot_rows(a.n_max * a.G);
+    p.inv_g = (1ull << 32) / a.G + 1;
     p.status = (int *)scratch;
     p.part = (float *)((uint8_t *)scratch + kTcStatusBytes);
     const int nrt = (a.n_max * a.G + kTcRows - 1) / kTcRows;
