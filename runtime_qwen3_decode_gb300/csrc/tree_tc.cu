@@ -16,8 +16,8 @@
 // Warps: 0-7 softmax and epilogue, one query row per lane and two groups of four: the groups
 // take the tiles in turn, each with its own scores, maximum, sum and accumulator, so that one
 // group's tile overlaps the other's (a single group needed 2800 cycles a tile, 1000 of them
-// exponentials); the two are joined at the end of an item.  8 loads (TMA), 9 issues the MMAs; for
-// caches that are not bf16 beside bf16 queries, 10-17 convert.  bf16 beside bf16: TMA writes K
+// exponentials); the two are joined at the end of an item.  10 loads (TMA), 11 issues the MMAs; for
+// caches that are not bf16 beside bf16 queries, 8, 9 and 12-17 convert.  bf16 beside bf16: TMA writes K
 // and V tiles straight into swizzled operand tiles, three stages each.  Otherwise TMA fills a
 // ring of 16 KB chunks of raw rows, and the converters write the 16-bit operand tiles,
 // double-buffered (one stage of two-term tiles).  8-bit rows become fp16 (code * scale rounded once, 2^-11;
@@ -47,8 +47,10 @@ using namespace tc;
 
 enum { SRC_BF16 = 0, SRC_Q8_F16 = 1, SRC_BF16_F16 = 2, SRC_F32_F16 = 3 };
 
-constexpr int kSoftWarps = 8, kLoadWarp = 8, kMmaWarp = 9, kConvWarp = 10;
-constexpr int kConvWarps = 8, kConvThreads = 32 * kConvWarps;
+// The loading and the MMA warp sit on the SM sub-partitions of the last row quarters, whose softmax
+// warps have nothing to do for small trees.
+constexpr int kSoftWarps = 8, kLoadWarp = 10, kMmaWarp = 11, kPlainWarps = 12;
+constexpr int kConvWarps = 8, kConvThreads = 32 * kConvWarps;  // warps 8, 9 and 12-17
 // TMEM columns of softmax group g: scores (and P over them) at 128 g, accumulator at 256 + 128 g
 constexpr uint32_t kColO = 256;
 
@@ -58,7 +60,7 @@ struct Cfg {
     static constexpr bool kDirect = SRC == SRC_BF16;
     static constexpr bool kBf16 = SRC == SRC_BF16;
     static constexpr int kElem = SRC == SRC_Q8_F16 ? 1 : SRC == SRC_F32_F16 ? 4 : 2;
-    static constexpr int kThreads = 32 * (kConvWarp + (kDirect ? 0 : kConvWarps));
+    static constexpr int kThreads = 32 * (kDirect ? kPlainWarps : kPlainWarps + kConvWarps - 2);
     static constexpr int kRegion = 128 * 128;              // 128 rows x 64 16-bit dims
     static constexpr int kTerm = kRegion * (D / 64);       // one term of a K or V operand tile
     static constexpr int kOperand = kTerm * TERMS;
@@ -399,6 +401,9 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
             // ---- MMAs.  Tile jj's scores and product belong to softmax group jj & 1.  S of the next
             // tile is issued before P V of this one: the groups' tiles overlap.
             constexpr uint32_t idS = idesc_16_f32(128, 128, C::kBf16, false), idO = idesc_16_f32(128, D, C::kBf16, true);
+            // Descriptors of the first tiles; the others differ in the address field (in units of 16 bytes), which
+            // the offsets below do not carry out of: building each anew held the issue back.
+            const uint64_t dQ = desc_sw128(su32(sQ)), dK = desc_sw128(su32(sK)), dV = desc_sw128_mn(su32(sV), C::kRegion);
             bool ok = true;
             int it = 0, seg = 0;  // it: tiles before this segment
             while (ok && next_seg(p, cur, s)) {
@@ -412,12 +417,12 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t sq = su32(sQ), sk = su32(sK + st * C::kOperand);
+                        const uint64_t kd = dK + (unsigned)(st * (C::kOperand >> 4));
 #pragma unroll
                         for (int k = 0; k < TERMS * (D / 16); ++k) {
                             const int term = k / (D / 16), kk = k % (D / 16);
-                            mma_f16(tmem + 128u * (jn & 1), desc_sw128(sq + (kk >> 2) * C::kRegion) + 2u * (kk & 3),
-                                    desc_sw128(sk + term * C::kTerm + (kk >> 2) * C::kRegion) + 2u * (kk & 3), idS, k != 0);
+                            const unsigned off = (kk >> 2) * (C::kRegion >> 4) + 2u * (kk & 3);
+                            mma_f16(tmem + 128u * (jn & 1), dQ + off, kd + (off + term * (C::kTerm >> 4)), idS, k != 0);
                         }
                         mma_commit(&s_full[jn & 1]);
                         mma_commit(&k_empty[st]);
@@ -430,12 +435,13 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t sv = su32(sV + st * C::kOperand);
+                        const uint64_t vd = dV + (unsigned)(st * (C::kOperand >> 4));
+                        const uint32_t tp = tmem + 128u * (jj & 1);
 #pragma unroll
                         for (int k = 0; k < TERMS * (kTcTile / 16); ++k) {
                             const int term = k / (kTcTile / 16), kk = k % (kTcTile / 16);
-                            mma_f16_ts(tmem + kColO + 128u * (jj & 1), tmem + 128u * (jj & 1) + 8u * kk,
-                                       desc_sw128_mn(sv + term * C::kTerm + 2048u * kk, C::kRegion), idO, j > 1 || k > 0);
+                            mma_f16_ts(tp + kColO, tp + 8u * kk, vd + (unsigned)(term * (C::kTerm >> 4) + 128 * kk), idO,
+                                       j > 1 || k > 0);
                         }
                         mma_commit(&pv_done[jj & 1]);
                         mma_commit(&v_empty[st]);
@@ -720,7 +726,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
         if (!ok && lane == 0) *abort = 1;
     } else if constexpr (!C::kDirect) {
         // ---- converters
-        const int ct = threadIdx.x - 32 * kConvWarp;
+        const int ct = threadIdx.x - 32 * (warp < kLoadWarp ? kSoftWarps : kSoftWarps + 2);
         bool ok = true;
         int it = 0, seg = 0, slot = 0;
         unsigned ph = 0;
@@ -872,7 +878,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
 // shared memory find room beside the attention's, so that they are there when it ends.
 // Also fills the rows of sequences that do not fit with NaN, and every row if a CTA gave up.
 constexpr int kMergeThreads = 128;
-constexpr int kMergeBatch = 8;
+constexpr int kMergeBatch = 10;
 
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) tree_tc_merge_kernel(const TcParams p, int ctas) {
@@ -911,18 +917,13 @@ __global__ void __launch_bounds__(kMergeThreads) tree_tc_merge_kernel(const TcPa
     auto partial = [&](int c) { return p.part + (size_t)(2 * c + (c == c0 ? 1 : 0)) * slot + rl; };
     auto holds = [&](int c) { return c <= c1 && !(gaps && share_start(total, c, ctas) == share_start(total, c + 1, ctas)); };
     chain_wait();
-    int gave_up = 0;
-    for (int i = lane; i < ctas; i += 32) gave_up |= p.status[i];
-    gave_up = __any_sync(0xffffffffu, gave_up);
-    if (dq >= D / 4) return;
+    int gave_up = 0;  // read here, looked at behind the partials' loads
+#pragma unroll
+    for (int i = 0; i < (kTcCtas + 31) / 32; ++i) gave_up |= p.status[min(lane + 32 * i, ctas - 1)];
     const int64_t at = b * a.oseq + (int64_t)p.node_of(r) * a.onode + (int64_t)(h * a.G + r - p.node_of(r) * a.G) * a.ohead + 4 * dq;
-    if (!fits || gave_up) {
-        for (int i = 0; i < 4; ++i) store_out(a, at + i, nanf(""));
-        return;
-    }
-    if (c0 == c1) return;  // finished by its one CTA
+    if (dq >= D / 4) c1 = c0;
     float mx = -INFINITY, num[4] = {0.f, 0.f, 0.f, 0.f}, den = 0.f;
-    for (int c = c0; c <= c1; c += kMergeBatch) {
+    for (int c = c0; c0 < c1 && c <= c1; c += kMergeBatch) {
         float m[kMergeBatch], l[kMergeBatch], v[kMergeBatch][4], top = mx;
 #pragma unroll
         for (int i = 0; i < kMergeBatch; ++i) {
@@ -949,6 +950,13 @@ __global__ void __launch_bounds__(kMergeThreads) tree_tc_merge_kernel(const TcPa
             for (int k = 0; k < 4; ++k) num[k] += v[i][k] * w;
         }
     }
+    gave_up = __any_sync(0xffffffffu, gave_up);
+    if (dq >= D / 4) return;
+    if (!fits || gave_up) {
+        for (int i = 0; i < 4; ++i) store_out(a, at + i, nanf(""));
+        return;
+    }
+    if (c0 == c1) return;  // finished by its one CTA
     if (den == 0.f) den = 1.f;  // a row that sees nothing: 0
 #pragma unroll
     for (int k = 0; k < 4; ++k) num[k] /= den;
