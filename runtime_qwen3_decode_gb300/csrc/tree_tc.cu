@@ -17,9 +17,9 @@
 // take the tiles in turn, each with its own scores, maximum, sum and accumulator, so that one
 // group's tile overlaps the other's (a single group needed 2800 cycles a tile, 1000 of them
 // exponentials); the two are joined at the end of an item.  10 loads (TMA), 11 issues the MMAs; for
-// caches that are not bf16 beside bf16 queries, 8, 9 and 12-17 convert.  bf16 beside bf16: TMA writes K
-// and V tiles straight into swizzled operand tiles, three stages each.  Otherwise TMA fills a
-// ring of 16 KB chunks of raw rows, and the converters write the 16-bit operand tiles,
+// caches that are not bf16 beside bf16 queries, 8, 9 and 12-17 convert, four of them K and four V.  bf16 beside bf16: TMA writes K
+// and V tiles straight into swizzled operand tiles, three stages each.  Otherwise TMA fills
+// two slots of 16 KB with raw rows for each plane, and the converters write the 16-bit operand tiles,
 // double-buffered (one stage of two-term tiles).  8-bit rows become fp16 (code * scale rounded once, 2^-11;
 // bf16 would lose three more bits and cost twice the instructions), bf16 queries beside them
 // fp16 after division by a power of two per row, so that only elements 2^-14 below the row's
@@ -50,7 +50,8 @@ enum { SRC_BF16 = 0, SRC_Q8_F16 = 1, SRC_BF16_F16 = 2, SRC_F32_F16 = 3 };
 // The loading and the MMA warp sit on the SM sub-partitions of the last row quarters, whose softmax
 // warps have nothing to do for small trees.
 constexpr int kSoftWarps = 8, kLoadWarp = 10, kMmaWarp = 11, kPlainWarps = 12;
-constexpr int kConvWarps = 8, kConvThreads = 32 * kConvWarps;  // warps 8, 9 and 12-17
+constexpr int kConvWarps = 8;              // warps 8, 9 and 12-17; four convert K and four V
+constexpr int kPlaneWarps = kConvWarps / 2, kPlaneThreads = 32 * kPlaneWarps;
 // TMEM columns of softmax group g: scores (and P over them) at 128 g, accumulator at 256 + 128 g
 constexpr uint32_t kColO = 256;
 
@@ -68,7 +69,7 @@ struct Cfg {
     static constexpr int kChunkRows = 16384 / (D * kElem) < 128 ? 16384 / (D * kElem) : 128;
     static constexpr int kChunk = kChunkRows * D * kElem;  // raw bytes per ring slot
     static constexpr int kChunks = 128 / kChunkRows;       // per tile and plane
-    static constexpr int kRing = kDirect ? 0 : 4;
+    static constexpr int kRing = kDirect ? 0 : 4;          // slots of raw rows: two for K, two for V
     static constexpr int kQ = 0, kK = kQ + kTerm, kV = kK + kStages * kOperand, kRaw = kV + kStages * kOperand;
     static constexpr int kBar = kRaw + kRing * kChunk;
     static constexpr int kBytes = kBar + 512 + kTcRows * 4;  // barriers, then one score factor per row
@@ -188,10 +189,11 @@ __device__ __forceinline__ uint8_t *smem_base() {
     return smem_tree + off;
 }
 
+// The whole warp waits, bounded, with one verdict: every lane tests the barrier (one instruction for the
+// warp; a lane that waits for the others and a shuffle took 300 cycles of a tile's 3000 each time).
 __device__ __forceinline__ bool warp_wait(uint64_t *b, unsigned parity, volatile int *abort) {
-    int ok = 1;
-    if ((threadIdx.x & 31) == 0) ok = mbar_sleep(b, parity, abort, true, kWaitLimitNs);
-    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+    if (__all_sync(0xffffffffu, mbar_test(b, parity))) return true;
+    return __all_sync(0xffffffffu, mbar_sleep(b, parity, abort, true, kWaitLimitNs));
 }
 
 // 2^x on the special-function unit (ex2.approx: about 2 ulp; 2^-inf = +0).
@@ -297,9 +299,9 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
     if (threadIdx.x == 0) {
         mbar_init(q_full, kSoftWarps);
         for (int i = 0; i < ST; ++i) {
-            mbar_init(&k_full[i], C::kDirect ? 1 : kConvWarps);
+            mbar_init(&k_full[i], C::kDirect ? 1 : kPlaneWarps);
             mbar_init(&k_empty[i], 1);
-            mbar_init(&v_full[i], C::kDirect ? 1 : kConvWarps);
+            mbar_init(&v_full[i], C::kDirect ? 1 : kPlaneWarps);
             mbar_init(&v_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -311,7 +313,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
         mbar_init(drain, 1);
         for (int i = 0; i < C::kRing; ++i) {
             mbar_init(&r_full[i], 1);
-            mbar_init(&r_empty[i], kConvWarps);
+            mbar_init(&r_empty[i], kPlaneWarps);
         }
         for (int i = 0; i < 4; ++i) bad_seg[i] = 0;
         *abort = 0;
@@ -375,20 +377,23 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                 }
             } else {
                 int rp[4] = {-1, -1, -1, -1};
-                int slot = 0;
-                unsigned ph = 0;
+                int i0 = 0;  // chunks per plane of the tiles before; chunk i of a plane goes to the plane's slot i & 1
                 while (ok && next_seg(p, cur, s)) {
-                    for (int t = s.t0; ok && t < s.t1; ++t)
+                    for (int t = s.t0; ok && t < s.t1; ++t, i0 += C::kChunks)
+                        // All of K first: the scores of this tile are issued before the product of the last one,
+                        // which V's operand tile waits for, so a K chunk must not wait behind a V chunk.
                         for (int ch = 0; ch < 2 * C::kChunks; ++ch) {
+                            const int plane = ch / C::kChunks, c = ch % C::kChunks, i = i0 + c;
+                            const int slot = 2 * plane + (i & 1);
+                            const unsigned ph = (unsigned)(i >> 1) & 1u;
                             if (!mbar_sleep(&r_empty[slot], ph ^ 1u, abort, true, kWaitLimitNs)) {
                                 ok = false;
                                 break;
                             }
                             mbar_expect_tx(&r_full[slot], C::kChunk);
-                            tma_load_4d(raw + slot * C::kChunk, ch < C::kChunks ? &tk : &tv, 0,
-                                        t * kTcTile + (ch % C::kChunks) * C::kChunkRows, s.h, s.b, &r_full[slot]);
+                            tma_load_4d(raw + slot * C::kChunk, plane ? &tv : &tk, 0, t * kTcTile + c * C::kChunkRows, s.h, s.b,
+                                        &r_full[slot]);
                             rp[slot] = (int)ph;
-                            if (++slot == C::kRing) slot = 0, ph ^= 1u;
                         }
                 }
                 if (!ok) *abort = 1;
@@ -725,15 +730,18 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
         }
         if (!ok && lane == 0) *abort = 1;
     } else if constexpr (!C::kDirect) {
-        // ---- converters
-        const int ct = threadIdx.x - 32 * (warp < kLoadWarp ? kSoftWarps : kSoftWarps + 2);
+        // ---- converters: four warps for K, four for V, each with two slots of the ring (a slot that both
+        // used would have them wait for every other phase of its barrier, which a parity cannot tell apart)
+        const int cw = warp - (warp < kLoadWarp ? kSoftWarps : kSoftWarps + 2);
+        const int plane = cw / kPlaneWarps, ct = (cw % kPlaneWarps) * 32 + lane;
+        uint64_t *full = plane ? v_full : k_full, *empty = plane ? v_empty : k_empty;
+        uint8_t *operand = plane ? sV : sK;
         bool ok = true;
-        int it = 0, seg = 0, slot = 0;
-        unsigned ph = 0;
+        int it = 0, seg = 0;
         // Eight elements of position `pos` (o: fp16, rest: second term) into their 16-byte chunk.
-        auto put = [&](uint8_t *at, uint4 o, uint4 rest, bool check, int pos) {
+        auto put = [&](uint8_t *at, uint4 o, uint4 rest, auto checked, int pos) {
             bool any = false;
-            if (check) {  // V rows of the sequence's end
+            if constexpr (decltype(checked)::value) {  // V rows of the sequence's end
                 if (pos >= s.total) {
                     o = rest = make_uint4(0u, 0u, 0u, 0u);
                 } else if (pos >= s.len && only_finite<false>(o)) {
@@ -746,7 +754,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
             return any;
         };
         // After a chunk: its slot is free, and (done) the plane's operand tile complete.
-        auto finish = [&](bool any, uint64_t *done) {
+        auto finish = [&](bool any, int slot, uint64_t *done) {
             if (any) bad_seg[seg & 3] = seg + 1;
             fence_async_shared();
             __syncwarp();
@@ -754,106 +762,115 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                 mbar_arrive(&r_empty[slot]);
                 if (done) mbar_arrive(done);
             }
-            if (++slot == C::kRing) slot = 0, ph ^= 1u;
         };
         if constexpr (SRC == SRC_Q8_F16) {
             // A thread takes whole 32-element groups, one scale each: row ct / GPR + RSTEP u, group ct % GPR.
             // Scales are loaded two tiles ahead.  The group's 32 bytes go as two halves; threads of
             // groups 2 and 3 take the second half first, which spreads a warp's 16-byte stores
             // over all banks.
-            constexpr int GPR = D / kQGroup, RSTEP = kConvThreads / GPR, U = 128 / RSTEP;
+            constexpr int GPR = D / kQGroup, RSTEP = kPlaneThreads / GPR, U = 128 / RSTEP;
             static_assert(C::kChunks == 1, "an 8-bit tile is one chunk per plane");
             const int g = ct % GPR, row0 = ct / GPR, flip = g >> 1;
-            __half sc[2][2][U];  // [plane][tile parity ahead][u]
+            const __half *scales = plane ? a.vs : a.ks;
+            __half sc[2][U];  // this tile's and the next one's
             while (ok && next_seg(p, cur, s)) {
-                const int64_t sbase = s.b * a.sseq + s.h * a.shead + g;
-                auto fetch = [&](__half(&x)[U], const __half *plane, int t) {
+                const __half *base_sc = scales + s.b * a.sseq + s.h * a.shead + g;
+                auto fetch = [&](__half(&x)[U], int t) {
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
                         const int pos = t * kTcTile + row0 + RSTEP * u;
-                        x[u] = pos < s.total ? plane[sbase + (int64_t)pos * a.spos] : __half(0);
+                        x[u] = pos < s.total ? base_sc[(int64_t)pos * a.spos] : __half(0);
                     }
                 };
-                fetch(sc[0][0], a.ks, s.t0);
-                fetch(sc[1][0], a.vs, s.t0);
-                fetch(sc[0][1], a.ks, s.t0 + 1);
-                fetch(sc[1][1], a.vs, s.t0 + 1);
+                fetch(sc[0], s.t0);
+                fetch(sc[1], s.t0 + 1);
                 for (int t = s.t0; ok && t < s.t1; ++t, ++it) {
-                    const int st = it % ST;
-                    const unsigned sph = (unsigned)(it / ST) & 1u;
-                    const bool tail = (t + 1) * kTcTile > s.len;
+                    const int st = it % ST, slot = 2 * plane + (it & 1);
+                    const bool check = plane && (t + 1) * kTcTile > s.len;
+                    __half2 s2[U];
 #pragma unroll
-                    for (int plane = 0; plane < 2; ++plane) {
-                        __half2 s2[U];
+                    for (int u = 0; u < U; ++u) {
+                        s2[u] = __half2half2(sc[0][u]);
+                        sc[0][u] = sc[1][u];
+                    }
+                    if (t + 2 < s.t1) fetch(sc[1], t + 2);
+                    if (!warp_wait(&empty[st], ((unsigned)(it / ST) & 1u) ^ 1u, abort) ||
+                        !warp_wait(&r_full[slot], (unsigned)(it >> 1) & 1u, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint8_t *src = raw + slot * C::kChunk + row0 * D + 32 * g;
+                    uint8_t *dst = operand + st * C::kOperand + (g >> 1) * C::kRegion;
+                    // every read before the first write: nothing tells the compiler that they do not overlap
+                    uint4 x[U][2];
 #pragma unroll
-                        for (int u = 0; u < U; ++u) {
-                            s2[u] = __half2half2(sc[plane][0][u]);
-                            sc[plane][0][u] = sc[plane][1][u];
-                        }
-                        if (t + 2 < s.t1) fetch(sc[plane][1], plane ? a.vs : a.ks, t + 2);
-                        if (!warp_wait(plane ? &v_empty[st] : &k_empty[st], sph ^ 1u, abort) ||
-                            !warp_wait(&r_full[slot], ph, abort)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint8_t *src = raw + slot * C::kChunk;
-                        uint8_t *dst = (plane ? sV : sK) + st * C::kOperand + (g >> 1) * C::kRegion;
-                        bool any = false;
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int jj = 0; jj < 2; ++jj)
+                            x[u][jj] = *reinterpret_cast<const uint4 *>(src + RSTEP * u * D + 16 * (jj ^ flip));
+                    bool any = false;
+                    auto all = [&](auto checked) {
 #pragma unroll
                         for (int u = 0; u < U; ++u) {
                             const int row = row0 + RSTEP * u;
 #pragma unroll
                             for (int jj = 0; jj < 2; ++jj) {
-                                const int j = jj ^ flip;
-                                const uint4 x = *reinterpret_cast<const uint4 *>(src + row * D + 32 * g + 16 * j);
+                                const int c = 4 * (g & 1) + 2 * (jj ^ flip);
                                 uint4 o, rest = make_uint4(0u, 0u, 0u, 0u);
-                                widen_q8<TERMS>(x.x, x.y, s2[u], o, rest);
-                                any |= put(dst + swz128(row, 4 * (g & 1) + 2 * j), o, rest, tail && plane, t * kTcTile + row);
-                                widen_q8<TERMS>(x.z, x.w, s2[u], o, rest);
-                                any |= put(dst + swz128(row, 4 * (g & 1) + 2 * j + 1), o, rest, tail && plane, t * kTcTile + row);
+                                widen_q8<TERMS>(x[u][jj].x, x[u][jj].y, s2[u], o, rest);
+                                any |= put(dst + swz128(row, c), o, rest, checked, t * kTcTile + row);
+                                widen_q8<TERMS>(x[u][jj].z, x[u][jj].w, s2[u], o, rest);
+                                any |= put(dst + swz128(row, c + 1), o, rest, checked, t * kTcTile + row);
                             }
                         }
-                        finish(any, plane ? &v_full[st] : &k_full[st]);
-                    }
+                    };
+                    if (check) all(std::true_type());
+                    else all(std::false_type());
+                    finish(any, slot, &full[st]);
                 }
                 ++seg;
             }
         } else {
-            // unit = eight elements of a row; a chunk's units over 256 threads
-            constexpr int UPR = D / 8, U = C::kChunkRows * UPR / kConvThreads, RSTEP = kConvThreads / UPR;
-            static_assert(U * kConvThreads == C::kChunkRows * UPR, "whole units per thread");
+            // unit = eight elements of a row; a chunk's units over the plane's threads
+            constexpr int UPR = D / 8, U = C::kChunkRows * UPR / kPlaneThreads, RSTEP = kPlaneThreads / UPR;
+            static_assert(U * kPlaneThreads == C::kChunkRows * UPR, "whole units per thread");
             const int c = ct % UPR, row0 = ct / UPR;
             while (ok && next_seg(p, cur, s)) {
                 for (int t = s.t0; ok && t < s.t1; ++t, ++it) {
                     const int st = it % ST;
-                    const unsigned sph = (unsigned)(it / ST) & 1u;
-                    const bool tail = (t + 1) * kTcTile > s.len;
-                    for (int ch = 0; ch < 2 * C::kChunks; ++ch) {
-                        const bool is_v = ch >= C::kChunks;
-                        const int crow = (ch % C::kChunks) * C::kChunkRows;
-                        if ((ch % C::kChunks == 0 && !warp_wait(is_v ? &v_empty[st] : &k_empty[st], sph ^ 1u, abort)) ||
-                            !warp_wait(&r_full[slot], ph, abort)) {
+                    const bool check = plane && (t + 1) * kTcTile > s.len;
+                    for (int ch = 0; ch < C::kChunks; ++ch) {
+                        const int i = it * C::kChunks + ch, slot = 2 * plane + (i & 1), crow = ch * C::kChunkRows;
+                        if ((ch == 0 && !warp_wait(&empty[st], ((unsigned)(it / ST) & 1u) ^ 1u, abort)) ||
+                            !warp_wait(&r_full[slot], (unsigned)(i >> 1) & 1u, abort)) {
                             ok = false;
                             break;
                         }
                         const uint8_t *src = raw + slot * C::kChunk;
-                        uint8_t *dst = (is_v ? sV : sK) + st * C::kOperand + (c >> 3) * C::kRegion;
-                        bool any = false;
+                        uint8_t *dst = operand + st * C::kOperand + (c >> 3) * C::kRegion;
+                        using Raw = typename std::conditional<C::kElem == 2, __nv_bfloat16, float>::type;
+                        float v[U][8];
 #pragma unroll
-                        for (int u = 0; u < U; ++u) {
-                            const int row = row0 + RSTEP * u;
-                            float v[8];
-                            if constexpr (C::kElem == 2) load8(reinterpret_cast<const __nv_bfloat16 *>(src) + row * D + 8 * c, v);
-                            else load8(reinterpret_cast<const float *>(src) + row * D + 8 * c, v);
-                            const uint4 o = make_uint4(pack2<false>(v[0], v[1]), pack2<false>(v[2], v[3]),
-                                                       pack2<false>(v[4], v[5]), pack2<false>(v[6], v[7]));
-                            uint4 rest = make_uint4(0u, 0u, 0u, 0u);
-                            if constexpr (TERMS == 2)
-                                rest = make_uint4(rest2(v[0], v[1], o.x), rest2(v[2], v[3], o.y), rest2(v[4], v[5], o.z),
-                                                  rest2(v[6], v[7], o.w));
-                            any |= put(dst + swz128(crow + row, c & 7), o, rest, tail && is_v, t * kTcTile + crow + row);
-                        }
-                        finish(any, ch % C::kChunks == C::kChunks - 1 ? (is_v ? &v_full[st] : &k_full[st]) : nullptr);
+                        for (int u = 0; u < U; ++u)
+                            load8(reinterpret_cast<const Raw *>(src) + (row0 + RSTEP * u) * D + 8 * c, v[u]);
+                        bool any = false;
+                        auto all = [&](auto checked) {
+#pragma unroll
+                            for (int u = 0; u < U; ++u) {
+                                const int row = crow + row0 + RSTEP * u;
+                                const float *f = v[u];
+                                const uint4 o = make_uint4(pack2<false>(f[0], f[1]), pack2<false>(f[2], f[3]),
+                                                           pack2<false>(f[4], f[5]), pack2<false>(f[6], f[7]));
+                                uint4 rest = make_uint4(0u, 0u, 0u, 0u);
+                                if constexpr (TERMS == 2)
+                                    rest = make_uint4(rest2(f[0], f[1], o.x), rest2(f[2], f[3], o.y), rest2(f[4], f[5], o.z),
+                                                      rest2(f[6], f[7], o.w));
+                                any |= put(dst + swz128(row, c & 7), o, rest, checked, t * kTcTile + row);
+                            }
+                        };
+                        if (check) all(std::true_type());
+                        else all(std::false_type());
+                        finish(any, slot, ch == C::kChunks - 1 ? &full[st] : nullptr);
                     }
                 }
                 ++seg;
