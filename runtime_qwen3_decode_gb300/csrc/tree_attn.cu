@@ -33,12 +33,15 @@ __device__ __forceinline__ void split_range(int total, int S, int s, int &p0, in
     p1 = min(total, ((s + 1) * per + min(s + 1, more)) * kTile);
 }
 
-// CUDA-core form: f32 arithmetic throughout, for every type.  A CTA takes RT query rows
-// (row r = node r / G, head r % G of the KV head's group) and one split of the positions.
-// Per tile of 64 positions: K and V rows widened to f32 in shared memory; scores with one
-// position per thread and the query rows broadcast; the online softmax with one warp per
+// CUDA-core form: f32 arithmetic throughout, for f32 queries over every kind of cache.  A CTA takes
+// RT query rows (row r = node r / G, head r % G of the KV head's group) and one split of the
+// positions.  Per tile of 64 positions: K and V rows as they lie in the cache into registers (the next
+// tile's while this one is worked on; the first tile's before anything else, as the latency of
+// the first loads is most of a short call), widened to f32 in shared memory; scores with
+// one position per thread and the query rows broadcast; the online softmax with one warp per
 // row; P V with four dims per lane and RT / 8 rows per warp (KW warps share a row's
-// positions when RT < 8).
+// positions when RT < 8).  With few rows it is bound by the latency of that chain or by the
+// cache's bytes, with 16 by its arithmetic: 16 x 512 flops per position and KV head.
 template <typename KV, int D, int RT>
 __global__ void __launch_bounds__(kThreads) tree_kernel(const TreeArgs a) {
     constexpr int KS = D + 4;                       // padded K row: quarter warps read 8 banks groups
@@ -47,6 +50,7 @@ __global__ void __launch_bounds__(kThreads) tree_kernel(const TreeArgs a) {
     constexpr int KW = RT < kWarps ? kWarps / RT : 1;  // warps sharing a row
     constexpr int RW = RT < kWarps ? 1 : RT / kWarps;  // rows per warp
     constexpr int RS = RT < 4 ? 1 : RT / 4;         // rows per thread in the scores
+    constexpr int E = 16 / sizeof(KV), LPT = kTile * (D / E) / kThreads;  // elements per load; loads per thread and plane
     extern __shared__ __align__(16) float smf[];
     float *sk = smf, *sv = sk + kTile * KS, *sq = sv + kTile * D, *sp = sq + RT * D;
     float *red = sp + RT * kTile;                   // [kWarps * KPW - per row parts][D]
@@ -63,6 +67,25 @@ __global__ void __launch_bounds__(kThreads) tree_kernel(const TreeArgs a) {
     const int total = len + n;
     int p0, p1;
     split_range(total, a.S, s, p0, p1);
+    const KV *kb = reinterpret_cast<const KV *>(a.k) + b * a.seq + h * a.head;
+    const KV *vb = reinterpret_cast<const KV *>(a.v) + b * a.seq + h * a.head;
+    uint4 raw[2][LPT];
+    __half scale[2][sizeof(KV) == 1 ? LPT : 1];
+    auto fetch = [&](int t0) {
+#pragma unroll
+        for (int plane = 0; plane < 2; ++plane)
+#pragma unroll
+            for (int i = 0; i < LPT; ++i) {
+                const int x = tid + kThreads * i, c = x % (D / E), pos = t0 + x / (D / E);
+                raw[plane][i] = make_uint4(0u, 0u, 0u, 0u);
+                if constexpr (sizeof(KV) == 1) scale[plane][i] = __half(0);
+                if (pos >= p1) continue;
+                raw[plane][i] = *reinterpret_cast<const uint4 *>((plane ? vb : kb) + (int64_t)pos * a.pos + E * c);
+                if constexpr (sizeof(KV) == 1)
+                    scale[plane][i] = ((plane ? a.vs : a.ks) + b * a.sseq + h * a.shead + (int64_t)pos * a.spos)[E * c / kQGroup];
+            }
+    };
+    fetch(p0);
     for (int i = tid; i < RT * D; i += kThreads) {
         const int r = r0 + i / D;
         sq[i] = r < rows ? load_q(a, b * a.qseq + (int64_t)(r / a.G) * a.qnode +
@@ -77,25 +100,28 @@ __global__ void __launch_bounds__(kThreads) tree_kernel(const TreeArgs a) {
     float acc[RW][4];
 #pragma unroll
     for (int i = 0; i < RW; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-    const KV *kb = reinterpret_cast<const KV *>(a.k) + b * a.seq + h * a.head;
-    const KV *vb = reinterpret_cast<const KV *>(a.v) + b * a.seq + h * a.head;
     for (int t0 = p0; t0 < p1; t0 += kTile) {
         __syncthreads();
-        for (int i = tid; i < 2 * kTile * (D / 8); i += kThreads) {
-            const int c = i % (D / 8), j = i / (D / 8) % kTile;
-            const bool is_v = i >= kTile * (D / 8);
-            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (t0 + j < p1) {
-                const int64_t at = (int64_t)(t0 + j) * a.pos + 8 * c;
-                if constexpr (sizeof(KV) == 1) {
-                    const __half *sc = (is_v ? a.vs : a.ks) + b * a.sseq + h * a.shead + (int64_t)(t0 + j) * a.spos + c / 4;
-                    load8_q8((is_v ? vb : kb) + at, __half2float(*sc), v);
-                } else {
-                    load8((is_v ? vb : kb) + at, v);
+#pragma unroll
+        for (int plane = 0; plane < 2; ++plane)
+#pragma unroll
+            for (int i = 0; i < LPT; ++i) {
+                const int x = tid + kThreads * i, c = x % (D / E), j = x / (D / E);
+                float *dst = plane ? sv + j * D + E * c : sk + j * KS + E * c;
+                const KV *e = reinterpret_cast<const KV *>(&raw[plane][i]);
+#pragma unroll
+                for (int k = 0; k < E; k += 4) {
+                    float4 f;
+                    if constexpr (sizeof(KV) == 1) {
+                        const float sc = __half2float(scale[plane][i]);
+                        f = make_float4((float)e[k] * sc, (float)e[k + 1] * sc, (float)e[k + 2] * sc, (float)e[k + 3] * sc);
+                    } else {
+                        f = make_float4(elem_to_f(e[k]), elem_to_f(e[k + 1]), elem_to_f(e[k + 2]), elem_to_f(e[k + 3]));
+                    }
+                    *reinterpret_cast<float4 *>(dst + k) = f;
                 }
             }
-            store8(is_v ? sv + j * D + 8 * c : sk + j * KS + 8 * c, v);
-        }
+        if (t0 + kTile < p1) fetch(t0 + kTile);
         __syncthreads();
         // scores: thread = (position tid % 64, rows tid / 64 + 4 i)
         {
@@ -197,40 +223,59 @@ __global__ void __launch_bounds__(kThreads) tree_kernel(const TreeArgs a) {
     }
 }
 
-// One query row per CTA: out = sum_s acc_s 2^(m_s - M) / sum_s l_s 2^(m_s - M), in order.
+// One query row per CTA: out = sum_s acc_s 2^(m_s - M) / sum_s l_s 2^(m_s - M), in order.  The partials
+// of kBatch splits are loaded at once: the kernel is their latency.
+constexpr int kBatch = 8;
+
 template <int D>
 __global__ void __launch_bounds__(D) tree_merge_kernel(const TreeArgs a) {
-    tc::chain_wait();
     const int r = blockIdx.x, h = blockIdx.y, b = blockIdx.z, d = threadIdx.x;
     int len, n;
     const bool fits = lengths(a, b, len, n);
-    if (fits && r >= n * a.G) return;
     const int64_t at = b * a.oseq + (int64_t)(r / a.G) * a.onode + (int64_t)(h * a.G + r % a.G) * a.ohead + d;
+    const float *src = a.part + (((int64_t)b * a.Hkv + h) * a.n_max * a.G + r) * a.S * (D + 2);
+    tc::chain_wait();
+    if (fits && r >= n * a.G) return;
     if (!fits) {
         store_out(a, at, nanf(""));
         return;
     }
-    const float *src = a.part + (((int64_t)b * a.Hkv + h) * a.n_max * a.G + r) * a.S * (D + 2);
-    float mx = -INFINITY;
-    for (int s = 0; s < a.S; ++s) mx = fmaxf(mx, src[(int64_t)s * (D + 2) + D]);
-    float num = 0.f, den = 0.f;
-    for (int s = 0; s < a.S; ++s) {
-        const float *ps = src + (int64_t)s * (D + 2);
-        if (ps[D] == -INFINITY && ps[D + 1] == 0.f) continue;  // the split showed the row nothing
-        const float w = exp2f(ps[D] - mx);
-        num += ps[d] * w;
-        den += ps[D + 1] * w;
+    float mx = -INFINITY, num = 0.f, den = 0.f;
+    for (int s = 0; s < a.S; s += kBatch) {
+        float m[kBatch], l[kBatch], v[kBatch], top = mx;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const float *ps = src + (int64_t)(s + i) * (D + 2);
+            const bool is = s + i < a.S;
+            m[i] = is ? ps[D] : -INFINITY;
+            l[i] = is ? ps[D + 1] : 0.f;
+            v[i] = is ? ps[d] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) top = fmaxf(top, m[i]);
+        const float old = mx == -INFINITY ? 0.f : exp2f(mx - top);
+        mx = top;
+        num *= old;
+        den *= old;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (m[i] == -INFINITY && l[i] == 0.f) continue;  // the split showed the row nothing
+            const float w = exp2f(m[i] - mx);
+            num += v[i] * w;
+            den += l[i] * w;
+        }
     }
     store_out(a, at, den == 0.f ? 0.f : num / den);
 }
 
 int rows_per_tile(int rows) { return rows <= 2 ? 2 : rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
 
-// Splits: enough CTAs for two on every SM, none shorter than a tile.
+// Splits: up to four CTAs for every SM (three of them fit at 16 rows of 128 dims, and in a ragged batch
+// some have nothing to do), none shorter than a tile.
 int splits(int n_seq, int Hkv, int row_tiles, int total) {
     const int tiles = (total + kTile - 1) / kTile;
     const int64_t base = (int64_t)n_seq * Hkv * row_tiles;
-    const int64_t want = (2 * 152 + base - 1) / base;
+    const int64_t want = (4 * 152 + base - 1) / base;
     return (int)std::max<int64_t>(1, std::min<int64_t>(want, tiles));
 }
 
