@@ -57,17 +57,25 @@ __device__ __forceinline__ int2 list_range(const int32_t *range, int r, int n) {
     return range ? make_int2(max(range[2 * r], 0), min(range[2 * r + 1], n)) : make_int2(0, 0);
 }
 
-// VEC: rows start on vector boundaries; SPARSE: there are lists to look at.
-template <typename T, int kThreads, bool VEC, bool SPARSE>
+enum { ROWS_ANY, ROWS_ALIKE, ROWS_ALIGNED };
+
+// ROWS: aligned, every row begins on a vector boundary; alike, a row of logits and its output lie
+// alike to vector boundaries, `pad` elements behind one (an odd vocabulary puts every row
+// elsewhere): vectors begin there, and the first and last are cut; any, no vectors.  SPARSE: there are
+// lists to look at.  (The masks of cut vectors straddle words: treating aligned rows alike
+// took 94 us for 256 x 151936 f32 instead of 69.)
+template <typename T, int kThreads, int ROWS, bool SPARSE>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_kernel(const qw_process_logits_args a, int chunks) {
+    constexpr bool VEC = ROWS != ROWS_ANY;
     constexpr int kTok = kThreads * 4 * kVecs;
-    extern __shared__ __align__(16) uint32_t sm[];  // [kTok] counts and flags, [kTok] biases of the flagged
-    uint32_t *cnt = sm;
-    float *add = reinterpret_cast<float *>(sm + kTok);
+    extern __shared__ __align__(16) uint32_t sm[];  // [kTok] counts and flags; of the flagged: first list entry, bias
+    uint32_t *cnt = sm, *entry = sm + kTok;
+    float *add = reinterpret_cast<float *>(sm + 2 * kTok);
     const int r = blockIdx.y, V = a.vocab, tid = threadIdx.x;
-    const int end = min((int)((blockIdx.x + 1) * chunks * kTok), V);
     const T *src = reinterpret_cast<const T *>(a.logits) + (int64_t)r * a.row_stride;
     T *dst = reinterpret_cast<T *>(a.out) + (int64_t)r * a.out_row_stride;
+    const int pad = ROWS == ROWS_ALIKE ? (int)((uintptr_t)src / sizeof(T)) & 3 : 0;
+    const int end = min((int)((blockIdx.x + 1) * chunks * kTok) - pad, V);
     const int which = a.mask ? (a.mask_index ? a.mask_index[r] : r) : -1;
     const bool none = a.mask && which >= a.n_masks;  // an index past the masks: nothing is allowed
     const uint32_t *mask = which >= 0 && !none ? a.mask + (int64_t)which * ((V + 31) / 32) : nullptr;
@@ -81,25 +89,34 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_kernel(const
         if (a.bias) bias = list_range(a.bias_range, r, a.n_bias);
     }
     float v[kVecs][4];
-    uint32_t word[kVecs];  // a vector of four tokens lies in one word of the mask
+    uint32_t word[kVecs];  // the vector's mask bits
     auto load = [&](int base) {
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
             const int t = base + 4 * (tid + kThreads * j);
-            if (VEC && t + 4 <= V) {
+            if (VEC && t >= 0 && t + 4 <= V) {
                 load4(src + t, v[j]);
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     // without vectors a warp still reads runs of 32 neighbours
                     const int s = VEC ? t + i : base + 4 * kThreads * j + kThreads * i + tid;
-                    v[j][i] = s < V ? elem_to_f(src[s]) : 0.f;
+                    v[j][i] = s >= 0 && s < V ? elem_to_f(src[s]) : 0.f;
                 }
             }
-            if constexpr (VEC) word[j] = mask && t < V ? mask[t >> 5] >> (t & 31) : none ? 0u : ~0u;
+            if constexpr (ROWS == ROWS_ALIGNED) {
+                word[j] = mask && t < V ? mask[t >> 5] >> (t & 31) : none ? 0u : ~0u;
+            } else if constexpr (VEC) {
+                word[j] = none ? 0u : ~0u;
+                if (mask && t < V) {  // four bits from bit t on, of a word and perhaps the next; t may be -3 .. -1
+                    const uint32_t lo = t >= 0 ? mask[t >> 5] : 0u;
+                    const uint32_t hi = (t & 31) > 28 && ((t + 3) >> 5) < (V + 31) / 32 ? mask[(t + 3) >> 5] : 0u;
+                    word[j] = __funnelshift_r(lo, hi, t & 31);
+                }
+            }
         }
     };
-    int base = blockIdx.x * chunks * kTok;
+    int base = blockIdx.x * chunks * kTok - pad;
     load(base);
     int32_t ids[kIds], bid[kBias], own = -1;
     float bval[kBias];
@@ -118,29 +135,36 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_kernel(const
         if (a.penalties && a.path && tid < a.path_len) own = a.path[(int64_t)r * a.path_len + tid];
         uint4 *z = reinterpret_cast<uint4 *>(cnt);
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) z[tid + kThreads * i] = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < kVecs; ++i) {
+            z[tid + kThreads * i] = make_uint4(0u, 0u, 0u, 0u);
+            if (a.bias) z[tid + kThreads * (i + kVecs)] = make_uint4(~0u, ~0u, ~0u, ~0u);
+        }
         __syncthreads();
     }
     for (; base < end; base += kTok) {
         if constexpr (SPARSE) {
-            // a token outside the vocabulary falls in no chunk, or behind the row's end
+            // a token outside the vocabulary falls in no chunk, or behind or before the row (an id of -1 to -3 in
+            // the cut front of the first vector): what is computed for it is not stored
             auto count = [&](int32_t id) {
                 const uint32_t t = (uint32_t)id - (uint32_t)base;
                 if (t < (uint32_t)kTok) atomicAdd(cnt + t, 1u);
             };
-            auto name = [&](int32_t id) {
-                const uint32_t t = (uint32_t)id - (uint32_t)base;
-                if (t < (uint32_t)kTok && (atomicOr(cnt + t, kNamed) & kNamed)) atomicOr(cnt + t, kTwice);
-            };
-            // entry i of the list: its first mention in the chunk holds the sum of all
-            auto settle = [&](int i, int32_t id, float sum) {
+            auto name = [&](int i, int32_t id) {
                 const uint32_t t = (uint32_t)id - (uint32_t)base;
                 if (t >= (uint32_t)kTok) return;
+                if (atomicOr(cnt + t, kNamed) & kNamed) atomicOr(cnt + t, kTwice);
+                atomicMin(entry + t, (uint32_t)i);
+            };
+            // entry i of the list: its first mention holds the sum of all
+            auto settle = [&](int i, int32_t id, float sum) {
+                const uint32_t t = (uint32_t)id - (uint32_t)base;
+                if (t >= (uint32_t)kTok || entry[t] != (uint32_t)i) return;
                 if (cnt[t] & kTwice) {
-                    for (int k = bias.x; k < i; ++k)
-                        if (a.bias_ids[k] == id) return;
-                    for (int k = i + 1; k < bias.y; ++k)
-                        if (a.bias_ids[k] == id) sum += a.bias[k];
+#pragma unroll 8
+                    for (int k = i + 1; k < bias.y; ++k) {
+                        const int32_t other = a.bias_ids[k];
+                        if (other == id) sum += a.bias[k];
+                    }
                 }
                 add[t] = sum;
             };
@@ -152,8 +176,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_kernel(const
                 for (int i = tid + kThreads; i < a.path_len; i += kThreads) count(a.path[(int64_t)r * a.path_len + i]);
             if (a.bias) {
 #pragma unroll
-                for (int k = 0; k < kBias; ++k) name(bid[k]);
-                for (int i = bias.x + tid + kThreads * kBias; i < bias.y; i += kThreads) name(a.bias_ids[i]);
+                for (int k = 0; k < kBias; ++k) name(bias.x + tid + kThreads * k, bid[k]);
+                for (int i = bias.x + tid + kThreads * kBias; i < bias.y; i += kThreads) name(i, a.bias_ids[i]);
                 __syncthreads();
 #pragma unroll
                 for (int k = 0; k < kBias; ++k) settle(bias.x + tid + kThreads * k, bid[k], bval[k]);
@@ -170,7 +194,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_kernel(const
                     x = x > 0.f ? x / rep : x * rep;
                     x -= pres + freq * (float)(c & kCount);
                 }
-                if (c & kNamed) x += add[l];
+                if (c & kNamed) {
+                    x += add[l];
+                    entry[l] = ~0u;  // for the next chunk
+                }
                 return x;
             };
             if constexpr (VEC) {
@@ -204,12 +231,12 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_kernel(const
                 }
             }
             if constexpr (VEC) {
-                if (t0 + 4 <= V) {
+                if (t0 >= 0 && t0 + 4 <= V) {
                     store4(dst + t0, v[j]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (t0 + i < V) dst[t0 + i] = elem_from_f<T>(v[j][i]);
+                        if (t0 + i >= 0 && t0 + i < V) dst[t0 + i] = elem_from_f<T>(v[j][i]);
                 }
             }
         }
@@ -220,37 +247,41 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_kernel(const
     }
 }
 
-template <typename T, int kThreads, bool VEC>
+template <typename T, int kThreads, int ROWS>
 cudaError_t launch_n(const qw_process_logits_args &a, int chunks, cudaStream_t st) {
-    constexpr int kTok = kThreads * 4 * kVecs, smem = 2 * kTok * 4;
-    const int all = (a.vocab + kTok - 1) / kTok;
+    constexpr int kTok = kThreads * 4 * kVecs, smem = 3 * kTok * 4;
+    const int all = (a.vocab + (ROWS == ROWS_ALIKE ? 3 : 0) + kTok - 1) / kTok;  // a row may begin up to three elements into a vector
     const dim3 grid((all + chunks - 1) / chunks, a.n_rows);
     if ((a.penalties && (a.history || a.path)) || a.bias) {
         if (smem > 48 * 1024) {
-            const cudaError_t e = cudaFuncSetAttribute(logits_kernel<T, kThreads, VEC, true>,
+            const cudaError_t e = cudaFuncSetAttribute(logits_kernel<T, kThreads, ROWS, true>,
                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
             if (e != cudaSuccess) return e;
         }
-        return launch_k(false, logits_kernel<T, kThreads, VEC, true>, grid, dim3(kThreads), smem, st, a, chunks);
+        return launch_k(false, logits_kernel<T, kThreads, ROWS, true>, grid, dim3(kThreads), smem, st, a, chunks);
     }
-    return launch_k(false, logits_kernel<T, kThreads, VEC, false>, grid, dim3(kThreads), 0, st, a, chunks);
+    return launch_k(false, logits_kernel<T, kThreads, ROWS, false>, grid, dim3(kThreads), 0, st, a, chunks);
 }
 
 // Many tokens: chunks of 8192, several per CTA (each list entry is looked at once per chunk); few: chunks
 // of 2048, one per CTA, so that every SM gets some.
-template <typename T, bool VEC>
+template <typename T, int ROWS>
 cudaError_t launch_t(const qw_process_logits_args &a, cudaStream_t st) {
     const long long large = (long long)a.n_rows * ((a.vocab + 8191) / 8192);
-    if (large < 3 * 152) return launch_n<T, 128, VEC>(a, 1, st);
-    return launch_n<T, 512, VEC>(a, large >= 4LL * 4 * 152 ? 4 : large >= 2LL * 4 * 152 ? 2 : 1, st);
+    if (large < 3 * 152) return launch_n<T, 128, ROWS>(a, 1, st);
+    return launch_n<T, 512, ROWS>(a, large >= 4LL * 4 * 152 ? 4 : large >= 2LL * 4 * 152 ? 2 : 1, st);
 }
 
 template <typename T>
 cudaError_t launch_vec(const qw_process_logits_args &a, cudaStream_t st) {
     const size_t unit = 4 * sizeof(T);
-    const bool vec = !((uintptr_t)a.logits % unit) && !((uintptr_t)a.out % unit) && a.row_stride % 4 == 0 &&
-                     a.out_row_stride % 4 == 0;
-    return vec ? launch_t<T, true>(a, st) : launch_t<T, false>(a, st);
+    const bool one = a.n_rows == 1;
+    if ((uintptr_t)a.logits % unit == 0 && (uintptr_t)a.out % unit == 0 &&
+        (one || (a.row_stride % 4 == 0 && a.out_row_stride % 4 == 0)))
+        return launch_t<T, ROWS_ALIGNED>(a, st);
+    if (((uintptr_t)a.logits - (uintptr_t)a.out) % unit == 0 && (one || (a.row_stride - a.out_row_stride) % 4 == 0))
+        return launch_t<T, ROWS_ALIKE>(a, st);
+    return launch_t<T, ROWS_ANY>(a, st);
 }
 
 }  // namespace

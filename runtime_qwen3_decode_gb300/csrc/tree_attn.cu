@@ -41,7 +41,8 @@ __device__ __forceinline__ void split_range(int total, int S, int s, int &p0, in
 // one position per thread and the query rows broadcast; the online softmax with one warp per
 // row; P V with four dims per lane and RT / 8 rows per warp (KW warps share a row's
 // positions when RT < 8).  With few rows it is bound by the latency of that chain or by the
-// cache's bytes, with 16 by its arithmetic: 16 x 512 flops per position and KV head.
+// cache's bytes, with many by its arithmetic: 512 flops per row, position and KV head, in pairs
+// (FFMA2); tiles of 32 rows read K, V and the weights from shared memory once for all.
 template <typename KV, int D, int RT>
 __global__ void __launch_bounds__(kThreads) tree_kernel(const TreeArgs a) {
     constexpr int KS = D + 4;                       // padded K row: quarter warps read 8 banks groups
@@ -97,9 +98,9 @@ __global__ void __launch_bounds__(kThreads) tree_kernel(const TreeArgs a) {
         sl[tid] = 0.f;
         smask[tid] = r0 + tid < rows ? a.mask[(int64_t)b * a.n_max + (r0 + tid) / a.G] : 0ull;
     }
-    float acc[RW][4];
+    float2 acc[RW][2];
 #pragma unroll
-    for (int i = 0; i < RW; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    for (int i = 0; i < RW; ++i) acc[i][0] = acc[i][1] = make_float2(0.f, 0.f);
     for (int t0 = p0; t0 < p1; t0 += kTile) {
         __syncthreads();
 #pragma unroll
@@ -126,9 +127,9 @@ __global__ void __launch_bounds__(kThreads) tree_kernel(const TreeArgs a) {
         // scores: thread = (position tid % 64, rows tid / 64 + 4 i)
         {
             const int j = tid & 63, rg = tid >> 6;
-            float d[RS];
+            float2 d[RS];
 #pragma unroll
-            for (int i = 0; i < RS; ++i) d[i] = 0.f;
+            for (int i = 0; i < RS; ++i) d[i] = make_float2(0.f, 0.f);
             if (RT >= 4 || rg < RT) {
 #pragma unroll 4
                 for (int c = 0; c < D; c += 4) {
@@ -136,7 +137,8 @@ __global__ void __launch_bounds__(kThreads) tree_kernel(const TreeArgs a) {
 #pragma unroll
                     for (int i = 0; i < RS; ++i) {
                         const float4 q = *reinterpret_cast<const float4 *>(sq + (rg + 4 * i) * D + c);
-                        d[i] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, d[i]))));
+                        d[i] = __ffma2_rn(make_float2(q.x, q.y), make_float2(k.x, k.y), d[i]);
+                        d[i] = __ffma2_rn(make_float2(q.z, q.w), make_float2(k.z, k.w), d[i]);
                     }
                 }
                 const int p = t0 + j;
@@ -144,7 +146,7 @@ __global__ void __launch_bounds__(kThreads) tree_kernel(const TreeArgs a) {
                 for (int i = 0; i < RS; ++i) {
                     const int r = rg + 4 * i;
                     const bool sees = p < len || (p < total && ((smask[r] >> (p - len)) & 1ull));
-                    sp[r * kTile + j] = p < p1 && sees ? d[i] : -INFINITY;
+                    sp[r * kTile + j] = p < p1 && sees ? d[i].x + d[i].y : -INFINITY;
                 }
             }
         }
@@ -179,20 +181,26 @@ __global__ void __launch_bounds__(kThreads) tree_kernel(const TreeArgs a) {
             for (int i = 0; i < RW; ++i) {
                 const float al = salpha[row0 + i];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][e] *= al;
+                for (int e = 0; e < 2; ++e) acc[i][e] = __fmul2_rn(acc[i][e], make_float2(al, al));
             }
             const bool tail = t0 + kTile > len;
-#pragma unroll 4
-            for (int j = jw * KPW + jl; j < kTile; j += KW * KPW) {
-                const float4 v = *reinterpret_cast<const float4 *>(sv + j * D + c);
+            // four positions' weights per read: they are most of this loop's shared-memory traffic
+            constexpr int STEP = KW * KPW;
+#pragma unroll 2
+            for (int j0 = 4 * (jw * KPW + jl); j0 < kTile; j0 += 4 * STEP) {
+                float4 v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const float4 *>(sv + (j0 + k) * D + c);
 #pragma unroll
                 for (int i = 0; i < RW; ++i) {
-                    const float p = sp[(row0 + i) * kTile + j];
-                    if (tail && p == 0.f) continue;
-                    acc[i][0] = fmaf(p, v.x, acc[i][0]);
-                    acc[i][1] = fmaf(p, v.y, acc[i][1]);
-                    acc[i][2] = fmaf(p, v.z, acc[i][2]);
-                    acc[i][3] = fmaf(p, v.w, acc[i][3]);
+                    const float4 w = *reinterpret_cast<const float4 *>(sp + (row0 + i) * kTile + j0);
+                    const float p[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (tail && p[k] == 0.f) continue;
+                        acc[i][0] = __ffma2_rn(make_float2(p[k], p[k]), make_float2(v[k].x, v[k].y), acc[i][0]);
+                        acc[i][1] = __ffma2_rn(make_float2(p[k], p[k]), make_float2(v[k].z, v[k].w), acc[i][1]);
+                    }
                 }
             }
         }
@@ -205,7 +213,7 @@ __global__ void __launch_bounds__(kThreads) tree_kernel(const TreeArgs a) {
 #pragma unroll
         for (int i = 0; i < RW; ++i)
             *reinterpret_cast<float4 *>(red + ((row0 + i) * PARTS + jw * KPW + jl) * D + c) =
-                make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+                make_float4(acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y);
         __syncthreads();
         for (int i = tid; i < RT * D; i += kThreads) {
             const int rl = i / D, d = i % D, r = r0 + rl;
@@ -268,7 +276,7 @@ __global__ void __launch_bounds__(D) tree_merge_kernel(const TreeArgs a) {
     store_out(a, at, den == 0.f ? 0.f : num / den);
 }
 
-int rows_per_tile(int rows) { return rows <= 2 ? 2 : rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
+int rows_per_tile(int rows) { return rows <= 2 ? 2 : rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
 
 // Splits: up to four CTAs for every SM (three of them fit at 16 rows of 128 dims, and in a ragged batch
 // some have nothing to do), none shorter than a tile.
@@ -293,7 +301,8 @@ cudaError_t launch_rt(const TreeArgs &a, int n_seq, int rt, cudaStream_t st, boo
     cudaError_t e = rt == 2   ? launch_tile<KV, D, 2>(a, n_seq, st, ch)
                     : rt == 4 ? launch_tile<KV, D, 4>(a, n_seq, st, ch)
                     : rt == 8 ? launch_tile<KV, D, 8>(a, n_seq, st, ch)
-                              : launch_tile<KV, D, 16>(a, n_seq, st, ch);
+                    : rt == 16 ? launch_tile<KV, D, 16>(a, n_seq, st, ch)
+                               : launch_tile<KV, D, 32>(a, n_seq, st, ch);
     if (e != cudaSuccess) return e;
     return launch_k(true, tree_merge_kernel<D>, dim3(a.n_max * a.G, a.Hkv, n_seq), dim3(D), 0, st, a);
 }

@@ -592,13 +592,13 @@ def test_logits_rows_off_vector_boundaries(qw, dt):
     R, V = 3, 5000
     whole = torch.randn((R, V + 7), generator=gen(2), device="cuda").to(dt)
     parts = make_logits(R, V, 9)
-    for off in (0, 1, 3):
+    for off, at, wide in ((0, 2, 9), (1, 2, 9), (3, 2, 9), (1, 1, 7), (2, 2, 7), (3, 3, 7), (2, 6, 11)):
         x = whole[:, off:off + V]
-        dst = torch.full((R, V + 9), 9.0, dtype=dt, device="cuda")
-        out = dst[:, 2:2 + V]
+        dst = torch.full((R, V + wide), 9.0, dtype=dt, device="cuda")
+        out = dst[:, at:at + V]
         call_logits(qw, x, parts, out)
         check_logits(out, logits_reference(x.clone(), *parts), x.clone(), parts, dt)
-        assert (dst[:, :2] == 9.0).all() and (dst[:, 2 + V:] == 9.0).all()
+        assert (dst[:, :at] == 9.0).all() and (dst[:, at + V:] == 9.0).all()
 
 
 def test_logits_a_bias_named_many_times_is_summed_in_order(qw):
