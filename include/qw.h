@@ -359,8 +359,8 @@ int qw_kv_read(const qw_kv_view *kv, const qw_kv_rows *rows, const int32_t *star
  * (device int32 [n_seq]; count NULL: n_max).  Node i sees every cached position, and drafted
  * node j if bit j of mask[b][i] (device uint64 [n_seq][n_max]) is set: its ancestors and itself.
  * Bits from count[b] on are ignored.  q and out: [n_seq][n_max][n_heads][head_dim] with element
- * strides, dtype QW_DT_F32, QW_DT_F16 or QW_DT_BF16 for both; n_heads a multiple of the
- * cache's KV heads (query head h reads KV head h / (n_heads / n_kv_heads)).  The softmax scale
+ * strides, dtype QW_DT_F32, QW_DT_F16 or QW_DT_BF16 for both; n_heads <= 16384 a multiple of the
+ * cache's KV heads, at most 64 times them (query head h reads KV head h / (n_heads / n_kv_heads)).  The softmax scale
  * is given.  Row (b, i) of out:
  *   sum_j softmax_j(scale q . k_j) v_j over the positions j it sees, 0 if it sees none.
  * What a node does not see does not reach it, NaN and infinities included.  Rows i >= count[b]
@@ -409,7 +409,8 @@ int qw_tree_attention(const qw_kv_view *kv, const qw_tree_attention_args *args, 
  * Rows may share ranges (the nodes of a tree share their request's history, and path holds
  * each node's own drafted tokens).  Ids outside [0, vocab) are padding and count for nothing;
  * ranges are cut to the arrays ([0, n_history), [0, n_bias)).  mask_index[r] < 0: the row is
- * not masked; >= n_masks: every token is; mask_index NULL: row r takes mask r.
+ * not masked; >= n_masks: every token is; mask_index NULL: row r takes mask r.  Lists of up to
+ * 2^30 entries.
  * Optional (NULL): penalties (then history and path are not read), history with its
  * range, path, bias_ids with bias and bias_range, mask.  n_rows <= 65535.
  */

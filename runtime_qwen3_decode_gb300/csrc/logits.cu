@@ -52,9 +52,9 @@ __device__ __forceinline__ void store4(T *p, const float (&v)[4]) {
     }
 }
 
-// [begin, end) of a row's list, kept inside the array; empty without a list.
+// [begin, end) of a row's list, both kept inside the array; empty without a list.
 __device__ __forceinline__ int2 list_range(const int32_t *range, int r, int n) {
-    return range ? make_int2(max(range[2 * r], 0), min(range[2 * r + 1], n)) : make_int2(0, 0);
+    return range ? make_int2(min(max(range[2 * r], 0), n), min(range[2 * r + 1], n)) : make_int2(0, 0);
 }
 
 enum { ROWS_ANY, ROWS_ALIKE, ROWS_ALIGNED };
@@ -253,11 +253,8 @@ cudaError_t launch_n(const qw_process_logits_args &a, int chunks, cudaStream_t s
     const int all = (a.vocab + (ROWS == ROWS_ALIKE ? 3 : 0) + kTok - 1) / kTok;  // a row may begin up to three elements into a vector
     const dim3 grid((all + chunks - 1) / chunks, a.n_rows);
     if ((a.penalties && (a.history || a.path)) || a.bias) {
-        if (smem > 48 * 1024) {
-            const cudaError_t e = cudaFuncSetAttribute(logits_kernel<T, kThreads, ROWS, true>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-            if (e != cudaSuccess) return e;
-        }
+        const cudaError_t e = allow_smem<logits_kernel<T, kThreads, ROWS, true>>(smem);
+        if (e != cudaSuccess) return e;
         return launch_k(false, logits_kernel<T, kThreads, ROWS, true>, grid, dim3(kThreads), smem, st, a, chunks);
     }
     return launch_k(false, logits_kernel<T, kThreads, ROWS, false>, grid, dim3(kThreads), 0, st, a, chunks);

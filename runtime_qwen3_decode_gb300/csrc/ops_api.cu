@@ -20,6 +20,8 @@ int elem_bytes(int32_t dtype) {
     return dtype == QW_DT_F32 ? 4 : dtype == QW_DT_F16 || dtype == QW_DT_BF16 ? 2 : 0;
 }
 
+constexpr int32_t kMostEntries = 1 << 30;  // of a list: its indices and a CTA's step stay within 32 bits
+
 bool stride_ok(int64_t s, int64_t unit) { return s >= 0 && s % unit == 0; }
 
 int check_view(const qw_kv_view *kv) {
@@ -66,7 +68,8 @@ int check_rows(const qw_kv_view *kv, const qw_kv_rows *r, const int32_t *start) 
 
 int check_tree_sizes(const qw_kv_view *kv, int32_t n_max, int32_t n_heads, int32_t max_len) {
     if (n_max < 0 || n_heads < 1 || max_len < 0 || max_len > kv->max_ctx) return QW_INVALID_ARGUMENT;
-    if (n_max > QW_TREE_NODES_MAX || n_heads % kv->n_kv_heads || n_heads / kv->n_kv_heads > 64)
+    // 16384 heads: (KV head, row tile) pairs are one dimension of a grid
+    if (n_max > QW_TREE_NODES_MAX || n_heads > 16384 || n_heads % kv->n_kv_heads || n_heads / kv->n_kv_heads > 64)
         return QW_UNSUPPORTED_SHAPE;
     return QW_OK;
 }
@@ -127,6 +130,7 @@ int qw_process_logits(const qw_process_logits_args *a, void *cuda_stream) {
     if (!aligned(a->logits, e) || !aligned(a->out, e)) return QW_ALIGNMENT;
     if (a->out == a->logits && a->row_stride != a->out_row_stride && a->n_rows > 1) return QW_INVALID_ARGUMENT;
     if (a->n_history < 0 || a->path_len < 0 || a->n_bias < 0 || a->n_masks < 0) return QW_INVALID_ARGUMENT;
+    if (a->n_history > kMostEntries || a->path_len > kMostEntries || a->n_bias > kMostEntries) return QW_UNSUPPORTED_SHAPE;
     if (a->history && !a->history_range) return QW_INVALID_ARGUMENT;
     if ((a->bias || a->bias_ids) && !(a->bias && a->bias_ids && a->bias_range)) return QW_INVALID_ARGUMENT;
     return status_of(qw::launch_process_logits(*a, (cudaStream_t)cuda_stream));

@@ -6,6 +6,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "qw.h"
 #include "qw_internal.h"
 
@@ -27,6 +29,21 @@ cudaError_t launch_tree_attn(const qw_kv_view &kv, const qw_tree_attention_args 
                              bool chained = false);
 
 cudaError_t launch_process_logits(const qw_process_logits_args &a, cudaStream_t st);
+
+// Lets kernel K use `bytes` of dynamic shared memory on the current device; the driver is asked once
+// per kernel and device, as the answer does not change and the call costs part of a microsecond.
+template <auto K>
+cudaError_t allow_smem(int bytes) {
+    static std::atomic<unsigned> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned bit = dev < 32 ? 1u << dev : 0u;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // ---------------------------------------------------------------- element conversions
 

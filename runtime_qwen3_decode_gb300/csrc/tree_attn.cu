@@ -291,7 +291,7 @@ template <typename KV, int D, int RT>
 cudaError_t launch_tile(const TreeArgs &a, int n_seq, cudaStream_t st, bool chained) {
     constexpr int KPW = 128 / D, KW = RT < kWarps ? kWarps / RT : 1;
     constexpr int smem = (kTile * (D + 4) + kTile * D + RT * D + RT * kTile + RT * KW * KPW * D) * 4;
-    cudaError_t e = cudaFuncSetAttribute(tree_kernel<KV, D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_smem<tree_kernel<KV, D, RT>>(smem);
     if (e != cudaSuccess) return e;
     return launch_k(chained, tree_kernel<KV, D, RT>, dim3(a.S, a.Hkv * a.row_tiles, n_seq), dim3(kThreads), smem, st, a);
 }

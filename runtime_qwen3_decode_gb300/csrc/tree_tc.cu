@@ -35,7 +35,6 @@
 
 #include <algorithm>
 #include <cmath>
-#include <mutex>
 
 #include "tc.cuh"
 #include "tree_attn.h"
@@ -1033,7 +1032,7 @@ cudaError_t launch_src(const TcParams &p, const qw_kv_view &kv, int ctas, cudaSt
     if (!plane_map(&mk, kv.k, kv, type, C::kElem, dims, rows, C::kDirect) ||
         !plane_map(&mv, kv.v, kv, type, C::kElem, dims, rows, C::kDirect))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel<SRC, D, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    cudaError_t e = allow_smem<tree_tc_kernel<SRC, D, TERMS>>((int)C::kSmem);
     if (e != cudaSuccess) return e;
     e = launch_k(chained, tree_tc_kernel<SRC, D, TERMS>, dim3(ctas), dim3(C::kThreads), C::kSmem, st, mk, mv, p);
     if (e != cudaSuccess) return e;

@@ -366,28 +366,32 @@ def sample_logits(logits, params: Sampling, rng, token_out, history=None, scratc
 _KV_ROWS = struct.Struct("@PPiiqqq")
 _TREE_ARGS = struct.Struct("@PPiiiif4xqqqqqqPPP")
 _LOGITS_ARGS = struct.Struct("@PPiii4xqqPPPi4xPi4xPPPi4xPPi4x")
+_T = None  # torch, once one of these operators is used
+_DTYPES = {}
+
+
+def _use_torch():
+    global _T
+    if _T is None:
+        import torch
+        _DTYPES.update({torch.float32: DT_F32, torch.bfloat16: DT_BF16, torch.float16: DT_F16})
+        _T = torch
 
 
 def _dtype_code(t, what):
-    import torch
-    dt = t.dtype
-    if dt is torch.float32:
-        return DT_F32
-    if dt is torch.bfloat16:
-        return DT_BF16
-    if dt is torch.float16:
-        return DT_F16
-    raise ValueError(f"{what} must be float32, float16 or bfloat16")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{what} must be float32, float16 or bfloat16")
+    return code
 
 
 def _on(dev, stream, what, call, *args):
     """call(*args, cuda_stream) with device `dev` current; stream None = that device's current stream."""
-    import torch
-    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev:
+    st = _T._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if _T._C._cuda_getDevice() == dev:
         rc = call(*args, st)
     else:
-        with torch.cuda.device(dev):
+        with _T.cuda.device(dev):
             rc = call(*args, st)
     if rc != OK:
         raise QwError(rc, what)
@@ -411,7 +415,8 @@ class KvView:
     share theirs, and so do the scales.  The view keeps the tensors alive."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
-        import torch
+        _use_torch()
+        torch = _T
         if not k.is_cuda:
             raise ValueError("the cache must be CUDA tensors")
         if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device or k.stride() != v.stride():
@@ -459,16 +464,14 @@ def kv_append(view: KvView, k, v, start, count=None, stream=None):
     """qw_kv_append: rows k, v [n_seq, n_kv_heads, n, head_dim] (any strides with a contiguous last
     dimension) into positions start[b] .. start[b] + count[b] - 1 of the cache; start, count: int32
     [n_seq] on the device (count None: all n)."""
-    import torch
-    i32 = torch.int32
+    i32 = _T.int32
     _on(view._dev, stream, "qw_kv_append", _lib().qw_kv_append, view._ref, _kv_rows(view, k, v, "the rows"),
         _want(start, "start", view._dev, i32, view._per_seq), _want(count, "count", view._dev, i32, view._per_seq))
 
 
 def kv_read(view: KvView, k_out, v_out, start, count=None, stream=None):
     """qw_kv_read: positions start[b] .. start[b] + count[b] - 1 of the cache into k_out, v_out."""
-    import torch
-    i32 = torch.int32
+    i32 = _T.int32
     _on(view._dev, stream, "qw_kv_read", _lib().qw_kv_read, view._ref, _kv_rows(view, k_out, v_out, "the rows"),
         _want(start, "start", view._dev, i32, view._per_seq), _want(count, "count", view._dev, i32, view._per_seq))
 
@@ -491,11 +494,10 @@ def tree_mask(parents) -> np.ndarray:
 def tree_attention_scratch(view: KvView, n_max: int, n_heads: int, max_len: int | None = None):
     """Workspace of tree_attention calls with these sizes, max_len or less (None: the cache's length),
     one call at a time."""
-    import torch
     n = _lib().qw_tree_attention_scratch_bytes(view._ref, n_max, n_heads, view.max_ctx if max_len is None else max_len)
     if n == 0 and n_max:
         raise QwError(UNSUPPORTED_SHAPE, "qw_tree_attention_scratch_bytes")
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=view.device)
+    return _T.empty(max(n, 256), dtype=_T.uint8, device=view.device)
 
 
 def tree_attention(view: KvView, q, mask, lens, out=None, counts=None, max_len=None, scale=None, scratch=None,
@@ -505,12 +507,11 @@ def tree_attention(view: KvView, q, mask, lens, out=None, counts=None, max_len=N
     [n_seq] on the device.  Node i of sequence b attends to cached positions [0, lens[b]) and to the
     drafted rows lens[b] + j that mask[b, i] names.  max_len: about the longest lens (None: the cache's
     length); scale None: 1 / sqrt(head_dim).  Returns out (rows i >= counts[b] as they were)."""
-    import torch
     dev, shape, stride = view._dev, q.shape, q.stride()
     if len(shape) != 4 or shape[0] != view.n_seq or shape[3] != view.head_dim or stride[3] != 1 or q.get_device() != dev:
         raise ValueError("q must be [n_seq, n, n_heads, head_dim] beside the cache, with a contiguous last dimension")
     if out is None:
-        out = torch.zeros_like(q, memory_format=torch.contiguous_format)
+        out = _T.zeros_like(q, memory_format=_T.contiguous_format)
     ostride = out.stride()
     if out.shape != shape or out.dtype is not q.dtype or out.get_device() != dev or ostride[3] != 1:
         raise ValueError("out must be like q, with a contiguous last dimension")
@@ -521,10 +522,10 @@ def tree_attention(view: KvView, q, mask, lens, out=None, counts=None, max_len=N
         scratch = tree_attention_scratch(view, n, heads, max_len)
     elif scratch.get_device() != dev or not scratch.is_contiguous():
         raise ValueError("scratch must be contiguous, beside the cache")
-    i32 = torch.int32
+    i32 = _T.int32
     args = _TREE_ARGS.pack(q.data_ptr(), out.data_ptr(), _dtype_code(q, "q"), n, heads, max_len,
                            view.head_dim ** -0.5 if scale is None else scale, stride[0], stride[1], stride[2],
-                           ostride[0], ostride[1], ostride[2], _want(mask, "mask", dev, torch.int64, shape[:2]),
+                           ostride[0], ostride[1], ostride[2], _want(mask, "mask", dev, _T.int64, shape[:2]),
                            _want(lens, "lens", dev, i32, view._per_seq), _want(counts, "counts", dev, i32, view._per_seq))
     _on(dev, stream, "qw_tree_attention", _lib().qw_tree_attention, view._ref, args, scratch.data_ptr(), scratch.nbytes)
     return out
@@ -537,7 +538,7 @@ def process_logits(logits, out=None, *, history=None, history_range=None, path=N
     history int32 [n], history_range int32 [n_rows, 2], path int32 [n_rows, p]; bias_ids int32 [m],
     bias float32 [m], bias_range int32 [n_rows, 2]; mask int32 [n_masks, ceil(vocab / 32)],
     mask_index int32 [n_rows].  Returns out."""
-    import torch
+    _use_torch()
     shape, stride, dev = logits.shape, logits.stride(), logits.get_device()
     if len(shape) != 2 or dev < 0 or (shape[1] > 1 and stride[1] != 1):
         raise ValueError("logits must be CUDA [n_rows, vocab] with contiguous rows")
@@ -549,7 +550,7 @@ def process_logits(logits, out=None, *, history=None, history_range=None, path=N
                 or (shape[1] > 1 and ostride[1] != 1):
             raise ValueError("out must be like logits, with contiguous rows")
     R, V = shape
-    i32, f32 = torch.int32, torch.float32
+    i32, f32 = _T.int32, _T.float32
     if (history is None) != (history_range is None):
         raise ValueError("history and history_range go together")
     if not (bias_ids is None) == (bias is None) == (bias_range is None):

@@ -587,6 +587,17 @@ def test_logits_special_values_and_masks(qw):
     assert (got[0, 8] == -float("inf")).all()
 
 
+def test_logits_ranges_outside_the_lists(qw):
+    V, top = 3000, 2**31 - 1
+    pen, hist, hr, path, bids, bias, br, mask, mi = make_logits(6, V, 8)
+    hr[:] = [[-5, 10], [top, top], [top, -top], [0, top], [-top, 7], [59, 58]]
+    br[:] = [[-1, 3], [top, top], [4, top], [-top, -3], [19, 20], [20, 5]]
+    parts = (pen, hist, hr, path, bids, bias, br, mask, mi)
+    x = torch.randn((6, V), generator=gen(3), device="cuda")
+    keep = x.clone()
+    check_logits(call_logits(qw, x, parts), logits_reference(keep, *parts), keep, parts, F32)
+
+
 @pytest.mark.parametrize("dt", [F32, BF16])
 def test_logits_rows_off_vector_boundaries(qw, dt):
     R, V = 3, 5000

@@ -36,7 +36,8 @@ BAD_VIEWS = [
     (dict(head_dim=96), "UNSUPPORTED_SHAPE"), (dict(head_dim=256), "UNSUPPORTED_SHAPE"),
     (dict(n_seq=65536), "UNSUPPORTED_SHAPE"), (dict(k=P + 8), "ALIGNMENT"), (dict(v=P + 1), "ALIGNMENT"),
     (dict(pos_stride=136), "ALIGNMENT"), (dict(head_stride=8), "ALIGNMENT"), (dict(seq_stride=-16), "ALIGNMENT"),
-    (dict(pos_stride=64), "INVALID_ARGUMENT"), (dict(k_scale=P + 4), "ALIGNMENT"), (dict(scale_pos_stride=6), "ALIGNMENT"),
+    (dict(pos_stride=64), "INVALID_ARGUMENT"), (dict(head_stride=0), "INVALID_ARGUMENT"), (dict(seq_stride=64), "INVALID_ARGUMENT"),
+    (dict(scale_head_stride=0), "INVALID_ARGUMENT"), (dict(k_scale=P + 4), "ALIGNMENT"), (dict(scale_pos_stride=6), "ALIGNMENT"),
     (dict(scale_pos_stride=0), "INVALID_ARGUMENT"),
 ]
 
@@ -74,7 +75,7 @@ def tree_args(qw, **kw):
     (dict(q=None), "INVALID_ARGUMENT"), (dict(out=None), "INVALID_ARGUMENT"), (dict(mask=None), "INVALID_ARGUMENT"),
     (dict(len=None), "INVALID_ARGUMENT"), (dict(dtype=4), "INVALID_ARGUMENT"), (dict(dtype=3), "INVALID_ARGUMENT"),
     (dict(n_max=-1), "INVALID_ARGUMENT"), (dict(n_max=65), "UNSUPPORTED_SHAPE"), (dict(n_heads=12), "UNSUPPORTED_SHAPE"),
-    (dict(n_heads=0), "INVALID_ARGUMENT"), (dict(n_heads=8 * 65), "UNSUPPORTED_SHAPE"), (dict(max_len=-1), "INVALID_ARGUMENT"),
+    (dict(n_heads=0), "INVALID_ARGUMENT"), (dict(n_heads=8 * 65), "UNSUPPORTED_SHAPE"), (dict(n_heads=16392), "UNSUPPORTED_SHAPE"), (dict(max_len=-1), "INVALID_ARGUMENT"),
     (dict(max_len=65), "INVALID_ARGUMENT"), (dict(scale=float("nan")), "INVALID_ARGUMENT"), (dict(q=P + 8), "ALIGNMENT"),
     (dict(out=P + 2), "ALIGNMENT"), (dict(q_head_stride=130), "ALIGNMENT"), (dict(out_node_stride=4), "ALIGNMENT")])
 def test_tree_refusals(qw, bad, code):
@@ -118,7 +119,8 @@ def logits_args(qw, **kw):
     (dict(row_stride=1024), "INVALID_ARGUMENT"), (dict(history_range=None), "INVALID_ARGUMENT"),
     (dict(bias=None), "INVALID_ARGUMENT"), (dict(bias_ids=None), "INVALID_ARGUMENT"), (dict(bias_range=None), "INVALID_ARGUMENT"),
     (dict(n_history=-1), "INVALID_ARGUMENT"), (dict(path_len=-1), "INVALID_ARGUMENT"), (dict(n_bias=-1), "INVALID_ARGUMENT"),
-    (dict(n_masks=-1), "INVALID_ARGUMENT")])
+    (dict(n_masks=-1), "INVALID_ARGUMENT"), (dict(n_history=2**30 + 1), "UNSUPPORTED_SHAPE"),
+    (dict(n_bias=2**30 + 1), "UNSUPPORTED_SHAPE")])
 def test_logits_refusals(qw, bad, code):
     a = logits_args(qw, **bad)
     assert qw.lib().qw_process_logits(ctypes.byref(a), None) == getattr(qw, code)
