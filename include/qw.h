@@ -370,12 +370,12 @@ int qw_kv_read(const qw_kv_view *kv, const qw_kv_rows *rows, const int32_t *star
  * positions (a longer sequence is right too, but slower).
  * scratch: qw_tree_attention_scratch_bytes device bytes, 256-byte aligned, for this call alone
  * while it runs.
- * Arithmetic: f32 accumulation, sums and softmax statistics.  With f32 queries every product is
- * f32.  With 16-bit queries the products are those of 16-bit operands on the tensor cores: softmax weights
- * rounded to the operands' type, K and V as follows.  bf16 queries over a bf16 cache: bf16, as cached.
- * fp16 queries: fp16, with a second term for what the rounding of an 8-bit or f32 row leaves.
- * bf16 queries over 8-bit or f32 rows: fp16, rounded once (2^-11; the result's own rounding is
- * 2^-8), the queries scaled by a power of two per row.  With fp16 operands cached magnitudes above
+ * Arithmetic: f32 accumulation, sums and softmax statistics.  With f32 queries, and in small calls,
+ * every product is f32.  Otherwise the products are those of 16-bit operands on the tensor cores:
+ * softmax weights rounded to the operands' type, K and V as follows.  bf16 queries over a bf16 cache:
+ * bf16, as cached.  fp16 queries: fp16, with a second term for what the rounding of an 8-bit or f32 row
+ * leaves.  bf16 queries over 8-bit or f32 rows: fp16, rounded once (2^-11; the result's own rounding
+ * is 2^-8), the queries scaled by a power of two per row.  With fp16 operands cached magnitudes above
  * 65504 are infinite.
  */
 enum { QW_TREE_NODES_MAX = 64 };

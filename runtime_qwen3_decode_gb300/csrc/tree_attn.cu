@@ -33,7 +33,7 @@ __device__ __forceinline__ void split_range(int total, int S, int s, int &p0, in
     p1 = min(total, ((s + 1) * per + min(s + 1, more)) * kTile);
 }
 
-// CUDA-core form: f32 arithmetic throughout, for f32 queries over every kind of cache.  A CTA takes
+// CUDA-core form: f32 arithmetic throughout, for f32 queries over every kind of cache and for small calls.  A CTA takes
 // RT query rows (row r = node r / G, head r % G of the KV head's group) and one split of the
 // positions.  Per tile of 64 positions: K and V rows as they lie in the cache into registers (the next
 // tile's while this one is worked on; the first tile's before anything else, as the latency of
@@ -287,6 +287,23 @@ int splits(int n_seq, int Hkv, int row_tiles, int total) {
     return (int)std::max<int64_t>(1, std::min<int64_t>(want, tiles));
 }
 
+// Whether a call with 16-bit queries is better off on the CUDA cores: they need no set-up of barriers,
+// tensor memory and conversions (6 us for one node over 64 positions where the tensor cores take
+// 9 to 11), but 0.018 us per tile of up to 4 rows and 0.03 of up to 8 (8 heads, 8-bit rows).
+// Measured, us, CUDA against tensor cores, one row of two heads: 8 sequences over 512 8-bit positions
+// (576 tiles) 17 : 24, over 1024 25 : 26; bf16 beside bf16 over 256 (320) 9 : 16, over 1024 (1088)
+// 21 : 18.  Four nodes (8 rows): one sequence over 1024 8-bit positions (136) 11 : 14, over 4096 (520)
+// 27 : 21; bf16 10 : 12 and 26 : 15.  Sixteen rows: never clearly.  f32 rows cost the
+// conversion most and the CUDA cores nothing: up to four query rows always (one row of two heads, 8
+// sequences over 4096: 70 against 89).
+bool small_call(const qw_kv_view &kv, const qw_tree_attention_args &t) {
+    const int64_t tiles = (int64_t)kv.n_seq * kv.n_kv_heads * ((t.max_len + t.n_max + kTile - 1) / kTile);
+    const int rows = t.n_max * (t.n_heads / kv.n_kv_heads);
+    const bool direct = t.dtype == QW_DT_BF16 && kv.format == QW_KV_BF16;
+    if (kv.format == QW_KV_F32 && rows <= 4) return true;
+    return rows <= 4 ? tiles <= (direct ? 3 : 4) * 152 : rows <= 8 && tiles <= (direct ? 1 : 2) * 152;
+}
+
 template <typename KV, int D, int RT>
 cudaError_t launch_tile(const TreeArgs &a, int n_seq, cudaStream_t st, bool chained) {
     constexpr int KPW = 128 / D, KW = RT < kWarps ? kWarps / RT : 1;
@@ -340,7 +357,7 @@ cudaError_t launch_tree_attn(const qw_kv_view &kv, const qw_tree_attention_args 
     a.G = t.n_heads / kv.n_kv_heads;
     a.scale_log2 = t.scale * kOpsLog2e;
     a.part = (float *)scratch;
-    if (t.dtype != QW_DT_F32) return launch_tree_tc(a, kv, t.max_len, scratch, st, chained);
+    if (t.dtype != QW_DT_F32 && !small_call(kv, t)) return launch_tree_tc(a, kv, t.max_len, scratch, st, chained);
     const int rows = t.n_max * a.G, rt = rows_per_tile(rows);
     a.row_tiles = (rows + rt - 1) / rt;
     a.S = splits(kv.n_seq, kv.n_kv_heads, a.row_tiles, t.max_len + t.n_max);

@@ -288,6 +288,12 @@ def test_tree_long_contexts_of_many_tiles(qw, dt, kind):
     run_tree(qw, 3, 8, 2, 128, 21, [9000, 1, 4321], [21, 20, 3], dt, kind, ctx=9100)
 
 
+@pytest.mark.parametrize("dt,kind", TYPES[3:])
+@pytest.mark.parametrize("B,n,L", [(1, 1, 3600), (1, 1, 5000), (4, 1, 500), (4, 1, 1200), (1, 4, 900), (1, 4, 2500), (1, 5, 100)])
+def test_tree_few_rows_on_both_sides_of_the_small_call(qw, dt, kind, B, n, L):
+    run_tree(qw, B, 8, 2, 128, n, [L] * B, None, dt, kind)
+
+
 @pytest.mark.parametrize("dt,kind", [(F32, "int8"), (BF16, "bf16"), (F16, "int8")])
 def test_tree_more_sequences_than_a_warp(qw, dt, kind):
     rng = np.random.default_rng(5)
