@@ -25,6 +25,11 @@ constexpr int kTile = 64;       // positions per tile
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
+// Where row r of a KV head's queries lies in out.
+__device__ __forceinline__ int64_t out_row(const TreeArgs &a, int b, int h, int r) {
+    return b * a.oseq + (int64_t)(r / a.G) * a.onode + (int64_t)(h * a.G + r % a.G) * a.ohead;
+}
+
 // The split's positions: equal shares of whole tiles.
 __device__ __forceinline__ void split_range(int total, int S, int s, int &p0, int &p1) {
     const int tiles = (total + kTile - 1) / kTile;
@@ -39,22 +44,24 @@ __device__ __forceinline__ void split_range(int total, int S, int s, int &p0, in
 // tile's while this one is worked on; the first tile's before anything else, as the latency of
 // the first loads is most of a short call), widened to f32 in shared memory; scores with
 // one position per thread and the query rows broadcast; the online softmax with one warp per
-// row; P V with four dims per lane and RT / 8 rows per warp (KW warps share a row's
-// positions when RT < 8).  With few rows it is bound by the latency of that chain or by the
+// row; P V with four dims per lane and up to four rows per warp, the other warps taking other rows or
+// other positions, so that a V row is read from shared memory once per four rows (eight rows per
+// warp read less but left one CTA per SM: 800 us for 64 nodes over 32768 positions instead of 670).  With few rows it is bound by the latency of that chain or by the
 // cache's bytes, with many by its arithmetic: 512 flops per row, position and KV head, in pairs
 // (FFMA2); tiles of 32 rows read K, V and the weights from shared memory once for all.
 template <typename KV, int D, int RT>
-__global__ void __launch_bounds__(kThreads) tree_kernel(const TreeArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeArgs a) {
     constexpr int KS = D + 4;                       // padded K row: quarter warps read 8 banks groups
     constexpr int LPR = D / 4;                      // lanes per V row
     constexpr int KPW = 32 / LPR;                   // positions a warp takes at once in P V
-    constexpr int KW = RT < kWarps ? kWarps / RT : 1;  // warps sharing a row
-    constexpr int RW = RT < kWarps ? 1 : RT / kWarps;  // rows per warp
+    constexpr int RW = RT < 4 ? RT : 4;             // rows per warp in P V
+    constexpr int KW = kWarps / (RT / RW);          // warps that share them, each with its positions
     constexpr int RS = RT < 4 ? 1 : RT / 4;         // rows per thread in the scores
     constexpr int E = 16 / sizeof(KV), LPT = kTile * (D / E) / kThreads;  // elements per load; loads per thread and plane
     extern __shared__ __align__(16) float smf[];
     float *sk = smf, *sv = sk + kTile * KS, *sq = sv + kTile * D, *sp = sq + RT * D;
-    float *red = sp + RT * kTile;                   // [kWarps * KPW - per row parts][D]
+    float *red = smf;                               // at the end, over K and V: [RT][KW * KPW parts][D]
+    static_assert(RT * KW * KPW * D <= kTile * (KS + D), "the parts fit over K and V");
     __shared__ float salpha[RT], sm[RT], sl[RT];
     __shared__ unsigned long long smask[RT];
     tc::chain_wait();
@@ -62,8 +69,13 @@ __global__ void __launch_bounds__(kThreads) tree_kernel(const TreeArgs a) {
     const int b = blockIdx.z, h = blockIdx.y / a.row_tiles, rt = blockIdx.y % a.row_tiles, s = blockIdx.x;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int len, n;
-    if (!lengths(a, b, len, n)) return;
+    const bool fits = lengths(a, b, len, n);
     const int r0 = rt * RT, rows = n * a.G;
+    if (!fits) {  // without a merge kernel behind it this one fills the rows
+        for (int i = tid; a.S == 1 && i < RT * D; i += kThreads)
+            if (r0 + i / D < a.n_max * a.G) store_out(a, out_row(a, b, h, r0 + i / D) + i % D, nanf(""));
+        return;
+    }
     if (r0 >= rows) return;
     const int total = len + n;
     int p0, p1;
@@ -176,7 +188,7 @@ __global__ void __launch_bounds__(kThreads) tree_kernel(const TreeArgs a) {
         // P V: warp -> rows; a position that a row does not see adds nothing, whatever its V holds
         {
             const int jl = lane / LPR, c = 4 * (lane % LPR);
-            const int row0 = RT < kWarps ? warp / KW : warp * RW, jw = RT < kWarps ? warp % KW : 0;
+            const int row0 = warp / KW * RW, jw = warp % KW;
 #pragma unroll
             for (int i = 0; i < RW; ++i) {
                 const float al = salpha[row0 + i];
@@ -209,7 +221,8 @@ __global__ void __launch_bounds__(kThreads) tree_kernel(const TreeArgs a) {
     {
         constexpr int PARTS = KW * KPW;
         const int jl = lane / LPR, c = 4 * (lane % LPR);
-        const int row0 = RT < kWarps ? warp / KW : warp * RW, jw = RT < kWarps ? warp % KW : 0;
+        const int row0 = warp / KW * RW, jw = warp % KW;
+        __syncthreads();
 #pragma unroll
         for (int i = 0; i < RW; ++i)
             *reinterpret_cast<float4 *>(red + ((row0 + i) * PARTS + jw * KPW + jl) * D + c) =
@@ -221,6 +234,10 @@ __global__ void __launch_bounds__(kThreads) tree_kernel(const TreeArgs a) {
             float o = 0.f;
 #pragma unroll
             for (int k = 0; k < PARTS; ++k) o += red[(rl * PARTS + k) * D + d];
+            if (a.S == 1) {  // the only split: nothing to merge
+                store_out(a, out_row(a, b, h, r) + d, sl[rl] == 0.f ? 0.f : o / sl[rl]);
+                continue;
+            }
             float *dst = a.part + ((((int64_t)b * a.Hkv + h) * a.n_max * a.G + r) * a.S + s) * (D + 2);
             dst[d] = o;
             if (d == 0) {
@@ -240,7 +257,7 @@ __global__ void __launch_bounds__(D) tree_merge_kernel(const TreeArgs a) {
     const int r = blockIdx.x, h = blockIdx.y, b = blockIdx.z, d = threadIdx.x;
     int len, n;
     const bool fits = lengths(a, b, len, n);
-    const int64_t at = b * a.oseq + (int64_t)(r / a.G) * a.onode + (int64_t)(h * a.G + r % a.G) * a.ohead + d;
+    const int64_t at = out_row(a, b, h, r) + d;
     const float *src = a.part + (((int64_t)b * a.Hkv + h) * a.n_max * a.G + r) * a.S * (D + 2);
     tc::chain_wait();
     if (fits && r >= n * a.G) return;
@@ -280,34 +297,34 @@ int rows_per_tile(int rows) { return rows <= 2 ? 2 : rows <= 4 ? 4 : rows <= 8 ?
 
 // Splits: up to four CTAs for every SM (three of them fit at 16 rows of 128 dims, and in a ragged batch
 // some have nothing to do), none shorter than a tile.
-int splits(int n_seq, int Hkv, int row_tiles, int total) {
+int splits(int n_seq, int Hkv, int row_tiles, int rt, int total) {
     const int tiles = (total + kTile - 1) / kTile;
     const int64_t base = (int64_t)n_seq * Hkv * row_tiles;
     const int64_t want = (4 * 152 + base - 1) / base;
+    if (tiles <= 2 && rt <= 4) return 1;  // a second tile costs less than the merge's launch
     return (int)std::max<int64_t>(1, std::min<int64_t>(want, tiles));
 }
 
 // Whether a call with 16-bit queries is better off on the CUDA cores: they need no set-up of barriers,
-// tensor memory and conversions (6 us for one node over 64 positions where the tensor cores take
-// 9 to 11), but 0.018 us per tile of up to 4 rows and 0.03 of up to 8 (8 heads, 8-bit rows).
-// Measured, us, CUDA against tensor cores, one row of two heads: 8 sequences over 512 8-bit positions
-// (576 tiles) 17 : 24, over 1024 25 : 26; bf16 beside bf16 over 256 (320) 9 : 16, over 1024 (1088)
-// 21 : 18.  Four nodes (8 rows): one sequence over 1024 8-bit positions (136) 11 : 14, over 4096 (520)
-// 27 : 21; bf16 10 : 12 and 26 : 15.  Sixteen rows: never clearly.  f32 rows cost the
-// conversion most and the CUDA cores nothing: up to four query rows always (one row of two heads, 8
-// sequences over 4096: 70 against 89).
+// tensor memory and conversions, but time grows with every tile of 64 positions.  Measured, us,
+// CUDA cores against tensor cores, 8 KV heads of two query heads.  Two rows (one node): one sequence
+// over 64 8-bit positions 7 : 11, 8 sequences over 512 (576 tiles) 14 : 22, over 1024 (1088) 24 : 25; bf16
+// beside bf16 6 : 9, 13 : 17 and 21 : 18.  Eight rows: one sequence over 1024 8-bit positions
+// (136) 10 : 13, over 4096 (520) 25 : 21; bf16 10 : 12 and 23 : 15.  Sixteen rows, 8-bit: over 512 (72)
+// 12 : 13, over 2048 (264) 18 : 15; bf16 11 : 11 and 17 : 14.  f32 rows cost the conversion most and
+// the CUDA cores nothing: up to four rows always (8 sequences of one node over 4096: 65 : 89).
 bool small_call(const qw_kv_view &kv, const qw_tree_attention_args &t) {
     const int64_t tiles = (int64_t)kv.n_seq * kv.n_kv_heads * ((t.max_len + t.n_max + kTile - 1) / kTile);
     const int rows = t.n_max * (t.n_heads / kv.n_kv_heads);
     const bool direct = t.dtype == QW_DT_BF16 && kv.format == QW_KV_BF16;
-    if (kv.format == QW_KV_F32 && rows <= 4) return true;
-    return rows <= 4 ? tiles <= (direct ? 3 : 4) * 152 : rows <= 8 && tiles <= (direct ? 1 : 2) * 152;
+    if (rows <= 4) return kv.format == QW_KV_F32 || tiles <= 4 * 152;
+    if (rows <= 8) return tiles <= (direct ? 1 : 2) * 152;
+    return rows <= 16 && !direct && tiles <= 152;
 }
 
 template <typename KV, int D, int RT>
 cudaError_t launch_tile(const TreeArgs &a, int n_seq, cudaStream_t st, bool chained) {
-    constexpr int KPW = 128 / D, KW = RT < kWarps ? kWarps / RT : 1;
-    constexpr int smem = (kTile * (D + 4) + kTile * D + RT * D + RT * kTile + RT * KW * KPW * D) * 4;
+    constexpr int smem = (kTile * (D + 4) + kTile * D + RT * D + RT * kTile) * 4;
     cudaError_t e = allow_smem<tree_kernel<KV, D, RT>>(smem);
     if (e != cudaSuccess) return e;
     return launch_k(chained, tree_kernel<KV, D, RT>, dim3(a.S, a.Hkv * a.row_tiles, n_seq), dim3(kThreads), smem, st, a);
@@ -320,7 +337,7 @@ cudaError_t launch_rt(const TreeArgs &a, int n_seq, int rt, cudaStream_t st, boo
                     : rt == 8 ? launch_tile<KV, D, 8>(a, n_seq, st, ch)
                     : rt == 16 ? launch_tile<KV, D, 16>(a, n_seq, st, ch)
                                : launch_tile<KV, D, 32>(a, n_seq, st, ch);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || a.S == 1) return e;
     return launch_k(true, tree_merge_kernel<D>, dim3(a.n_max * a.G, a.Hkv, n_seq), dim3(D), 0, st, a);
 }
 
@@ -328,7 +345,7 @@ cudaError_t launch_rt(const TreeArgs &a, int n_seq, int rt, cudaStream_t st, boo
 
 size_t tree_attn_scratch_bytes(int n_seq, int n_kv_heads, int n_max, int n_heads, int head_dim, int max_len) {
     const int G = n_heads / n_kv_heads, rows = n_max * G, rt = rows_per_tile(rows);
-    const int S = splits(n_seq, n_kv_heads, (rows + rt - 1) / rt, max_len + n_max);
+    const int S = splits(n_seq, n_kv_heads, (rows + rt - 1) / rt, rt, max_len + n_max);
     const size_t cores = ((size_t)n_seq * n_kv_heads * rows * S * (head_dim + 2) * 4 + 255) / 256 * 256;
     return std::max(cores, tree_tc_scratch_bytes(rows, head_dim));
 }
@@ -360,7 +377,7 @@ cudaError_t launch_tree_attn(const qw_kv_view &kv, const qw_tree_attention_args 
     if (t.dtype != QW_DT_F32 && !small_call(kv, t)) return launch_tree_tc(a, kv, t.max_len, scratch, st, chained);
     const int rows = t.n_max * a.G, rt = rows_per_tile(rows);
     a.row_tiles = (rows + rt - 1) / rt;
-    a.S = splits(kv.n_seq, kv.n_kv_heads, a.row_tiles, t.max_len + t.n_max);
+    a.S = splits(kv.n_seq, kv.n_kv_heads, a.row_tiles, rt, t.max_len + t.n_max);
     const int D = kv.head_dim;
     if (kv.format == QW_KV_F32)
         return D == 128 ? launch_rt<float, 128>(a, kv.n_seq, rt, st, chained) : launch_rt<float, 64>(a, kv.n_seq, rt, st, chained);

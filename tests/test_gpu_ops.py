@@ -289,7 +289,7 @@ def test_tree_long_contexts_of_many_tiles(qw, dt, kind):
 
 
 @pytest.mark.parametrize("dt,kind", TYPES[3:])
-@pytest.mark.parametrize("B,n,L", [(1, 1, 3600), (1, 1, 5000), (4, 1, 500), (4, 1, 1200), (1, 4, 900), (1, 4, 2500), (1, 5, 100)])
+@pytest.mark.parametrize("B,n,L", [(1, 1, 3600), (1, 1, 5000), (4, 1, 500), (4, 1, 1200), (1, 4, 900), (1, 4, 2500), (1, 5, 100), (1, 8, 1000), (1, 8, 1400)])
 def test_tree_few_rows_on_both_sides_of_the_small_call(qw, dt, kind, B, n, L):
     run_tree(qw, B, 8, 2, 128, n, [L] * B, None, dt, kind)
 
