@@ -62,10 +62,11 @@ __device__ __forceinline__ Pack<int8_t, E> quantise(const float (&v)[E], __half 
 
 // T: the rows' element type; KV: float, __nv_bfloat16, or int8_t for the 8-bit format.
 // blockIdx.x = (head, block of U * kRowThreads / (D / E) rows), blockIdx.y = sequence, blockIdx.z = K
-// or V: no division but one per block.  A lane's U rows are all loaded before one is written;
-// the rest of the latency is left to the many small blocks of an SM (blocks that looped
-// over rows with the next ones prefetched needed more registers and took 73 us where these
-// take the time in launch_rows' comment).
+// or V: one division per block (a division per row, in 64 bits, was most of the time).  A lane's U
+// rows are all loaded before one is written; the rest of the latency is left to the many small
+// blocks of an SM.  32768 rows of 8 heads of 128 read back as bf16: 40 us, 5.2 TB/s, 77% of the
+// measured copy rate (blocks that looped over rows with the next ones prefetched needed more
+// registers and took 73); 2048 f32 rows of 8 heads appended: 11 us under the profiler, one wave.
 template <typename T, typename KV, int D, int U, bool READ>
 __global__ void __launch_bounds__(kRowThreads) kv_rows_kernel(const RowArgs a, int blocks) {
     constexpr int E = 16 / sizeof(T);

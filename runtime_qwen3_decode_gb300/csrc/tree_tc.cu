@@ -2,11 +2,11 @@
 //
 // The query rows of a KV head (row r = node r / G, head r % G of its group) fill the 128 MMA
 // rows, so the heads of a group and the nodes of a tree share every K and V row.  Per tile of
-// 128 positions S = Q K^T (both in shared memory), the masks and the online
-// softmax in the log2 domain, O += P V (P in TMEM over its scores, V in shared memory as it is
-// cached: the MMA takes it MN-major, so nothing is transposed).  The bound is the cache's
-// bytes: 128 x 128 x 128 MMAs, even where most of the 128 rows are empty, take 1024 cycles of a
-// tile whose bytes take 3000 (bf16) or 1600 (8 bits) cycles of an SM's share of HBM.
+// 128 positions S = Q K^T (both in shared memory), the masks and the online softmax in the
+// log2 domain, O += P V (P in TMEM over its scores, V in shared memory as it is cached: the
+// MMA takes it MN-major, so nothing is transposed).  The bound is the cache's bytes: 128 x
+// 128 x 128 MMAs, even where most of the 128 rows are empty, take 1024 cycles of a tile whose
+// bytes take 3000 (bf16) or 1600 (8 bits) cycles of an SM's share of HBM.
 //
 // Work: the tiles of all (sequence, KV head, row tile) items in a row, cut into equal shares,
 // one per CTA, whatever the lengths (each CTA finds its share from len and count).  An item
@@ -16,14 +16,21 @@
 // Warps: 0-7 softmax and epilogue, one query row per lane and two groups of four: the groups
 // take the tiles in turn, each with its own scores, maximum, sum and accumulator, so that one
 // group's tile overlaps the other's (a single group needed 2800 cycles a tile, 1000 of them
-// exponentials); the two are joined at the end of an item.  10 loads (TMA), 11 issues the MMAs; for
-// caches that are not bf16 beside bf16 queries, 8, 9 and 12-17 convert, four of them K and four V.  bf16 beside bf16: TMA writes K
-// and V tiles straight into swizzled operand tiles, three stages each.  Otherwise TMA fills
-// two slots of 16 KB with raw rows for each plane, and the converters write the 16-bit operand tiles,
-// double-buffered (one stage of two-term tiles).  8-bit rows become fp16 (code * scale rounded once, 2^-11;
-// bf16 would lose three more bits and cost twice the instructions), bf16 queries beside them
-// fp16 after division by a power of two per row, so that only elements 2^-14 below the row's
-// largest lose bits.
+// exponentials); the two are joined at the end of an item.  10 loads (TMA), 11 issues the
+// MMAs; for caches that are not bf16 beside bf16 queries, 8, 9 and 12-17 convert, four of
+// them K and four V.  bf16 beside bf16: TMA writes K and V tiles straight into swizzled operand
+// tiles, three stages each.  Otherwise TMA fills two slots of 16 KB with raw rows for each
+// plane, and the converters write the 16-bit operand tiles, double-buffered (one stage of
+// two-term tiles).  8-bit rows become fp16 (code * scale rounded once, 2^-11; bf16 would lose
+// three more bits and cost twice the instructions), bf16 queries beside them fp16 after
+// division by a power of two per row, so that only elements 2^-14 below the row's largest
+// lose bits.
+//
+// Measured (device time with the merge; HBM floor): 64 nodes over 32768 bf16 positions 37 us
+// (20): HBM while it streams, 5 us until the first tiles arrive, 8 us of last tile and merge.
+// 16 sequences of up to 33 nodes over 8-bit caches of up to 4096 57 us (14): the chain softmax,
+// product, next scores of each group, 2700 cycles a tile.  64 fp16 nodes over 32768 8-bit
+// positions 52 us (11), over f32 ones 96 us (40).
 //
 // What a row does not see has weight 0, but 0 x NaN is NaN in the product with V: the V
 // rows behind the sequence are zeroed, and elements of drafted rows that are not finite are
@@ -402,54 +409,66 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
         }
     } else if (warp == kMmaWarp) {
         if (lane == 0) {
-            // ---- MMAs.  Tile jj's scores and product belong to softmax group jj & 1.  S of the next
-            // tile is issued before P V of this one: the groups' tiles overlap.
+            // ---- MMAs.  Tile jj's scores and product belong to softmax group jj & 1.  A group's next scores
+            // follow its product at once (they overwrite the weights that the product reads), and
+            // what they need is waited for before the weights are: that wait is the one that both groups'
+            // time hangs on.  With one stage K of two tiles on cannot be there yet (its chunks come
+            // behind V chunks that wait for this product): there S runs one tile ahead.
             constexpr uint32_t idS = idesc_16_f32(128, 128, C::kBf16, false), idO = idesc_16_f32(128, D, C::kBf16, true);
+            constexpr int kAhead = ST >= 2 ? 2 : 1;
             // Descriptors of the first tiles; the others differ in the address field (in units of 16 bytes), which
             // the offsets below do not carry out of: building each anew held the issue back.
             const uint64_t dQ = desc_sw128(su32(sQ)), dK = desc_sw128(su32(sK)), dV = desc_sw128_mn(su32(sV), C::kRegion);
+            auto wait_k = [&](int jn) {
+                return mbar_sleep(&k_full[jn % ST], (unsigned)(jn / ST) & 1u, abort, true, kWaitLimitNs);
+            };
+            auto scores = [&](int jn) {
+                const int st = jn % ST;
+                tc_fence_after();
+                const uint64_t kd = dK + (unsigned)(st * (C::kOperand >> 4));
+#pragma unroll
+                for (int k = 0; k < TERMS * (D / 16); ++k) {
+                    const int term = k / (D / 16), kk = k % (D / 16);
+                    const unsigned off = (kk >> 2) * (C::kRegion >> 4) + 2u * (kk & 3);
+                    mma_f16(tmem + 128u * (jn & 1), dQ + off, kd + (off + term * (C::kTerm >> 4)), idS, k != 0);
+                }
+                mma_commit(&s_full[jn & 1]);
+                mma_commit(&k_empty[st]);
+            };
             bool ok = true;
             int it = 0, seg = 0;  // it: tiles before this segment
             while (ok && next_seg(p, cur, s)) {
                 const int nt = s.t1 - s.t0;
                 ok = mbar_sleep(q_full, (unsigned)seg & 1u, abort, true, kWaitLimitNs);
-                for (int j = -1; ok && j < nt; ++j) {
-                    if (j + 1 < nt) {
-                        const int jn = it + j + 1, st = jn % ST;
-                        if (!mbar_sleep(&k_full[st], (unsigned)(jn / ST) & 1u, abort, true, kWaitLimitNs)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint64_t kd = dK + (unsigned)(st * (C::kOperand >> 4));
-#pragma unroll
-                        for (int k = 0; k < TERMS * (D / 16); ++k) {
-                            const int term = k / (D / 16), kk = k % (D / 16);
-                            const unsigned off = (kk >> 2) * (C::kRegion >> 4) + 2u * (kk & 3);
-                            mma_f16(tmem + 128u * (jn & 1), dQ + off, kd + (off + term * (C::kTerm >> 4)), idS, k != 0);
-                        }
-                        mma_commit(&s_full[jn & 1]);
-                        mma_commit(&k_empty[st]);
+                for (int j = 0; ok && j < min(nt, kAhead); ++j) {
+                    ok = wait_k(it + j);
+                    if (ok) scores(it + j);
+                }
+                for (int j = 0; ok && j < nt; ++j) {
+                    const int jj = it + j, st = jj % ST;
+                    const bool more = j + kAhead < nt;
+                    if (kAhead == 1 && more) {
+                        ok = wait_k(jj + 1);
+                        if (ok) scores(jj + 1);
                     }
-                    if (j >= 0) {
-                        const int jj = it + j, st = jj % ST;
-                        if (!mbar_sleep(&v_full[st], (unsigned)(jj / ST) & 1u, abort, true, kWaitLimitNs) ||
-                            !mbar_sleep(&p_full[jj & 1], (unsigned)(jj >> 1) & 1u, abort, true, kWaitLimitNs)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint64_t vd = dV + (unsigned)(st * (C::kOperand >> 4));
-                        const uint32_t tp = tmem + 128u * (jj & 1);
-#pragma unroll
-                        for (int k = 0; k < TERMS * (kTcTile / 16); ++k) {
-                            const int term = k / (kTcTile / 16), kk = k % (kTcTile / 16);
-                            mma_f16_ts(tp + kColO, tp + 8u * kk, vd + (unsigned)(term * (C::kTerm >> 4) + 128 * kk), idO,
-                                       j > 1 || k > 0);
-                        }
-                        mma_commit(&pv_done[jj & 1]);
-                        mma_commit(&v_empty[st]);
+                    if (!ok || (kAhead == 2 && more && !wait_k(jj + 2)) ||
+                        !mbar_sleep(&v_full[st], (unsigned)(jj / ST) & 1u, abort, true, kWaitLimitNs) ||
+                        !mbar_sleep(&p_full[jj & 1], (unsigned)(jj >> 1) & 1u, abort, true, kWaitLimitNs)) {
+                        ok = false;
+                        break;
                     }
+                    tc_fence_after();
+                    const uint64_t vd = dV + (unsigned)(st * (C::kOperand >> 4));
+                    const uint32_t tp = tmem + 128u * (jj & 1);
+#pragma unroll
+                    for (int k = 0; k < TERMS * (kTcTile / 16); ++k) {
+                        const int term = k / (kTcTile / 16), kk = k % (kTcTile / 16);
+                        mma_f16_ts(tp + kColO, tp + 8u * kk, vd + (unsigned)(term * (C::kTerm >> 4) + 128 * kk), idO,
+                                   j > 1 || k > 0);
+                    }
+                    mma_commit(&pv_done[jj & 1]);
+                    mma_commit(&v_empty[st]);
+                    if (kAhead == 2 && more) scores(jj + 2);
                 }
                 it += nt;
                 ++seg;
