@@ -410,7 +410,7 @@ int qw_tree_attention(const qw_kv_view *kv, const qw_tree_attention_args *args, 
  * each node's own drafted tokens).  Ids outside [0, vocab) are padding and count for nothing;
  * ranges are cut to the arrays ([0, n_history), [0, n_bias)).  mask_index[r] < 0: the row is
  * not masked; >= n_masks: every token is; mask_index NULL: row r takes mask r.  Lists of up to
- * 2^30 entries.
+ * 2^28 entries.
  * Optional (NULL): penalties (then history and path are not read), history with its
  * range, path, bias_ids with bias and bias_range, mask.  n_rows <= 65535.
  */

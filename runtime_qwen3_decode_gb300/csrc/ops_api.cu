@@ -20,7 +20,7 @@ int elem_bytes(int32_t dtype) {
     return dtype == QW_DT_F32 ? 4 : dtype == QW_DT_F16 || dtype == QW_DT_BF16 ? 2 : 0;
 }
 
-constexpr int32_t kMostEntries = 1 << 30;  // of a list: its indices and a CTA's step stay within 32 bits
+constexpr int32_t kMostEntries = 1 << 28;  // of a list: a token's count in two of them stays below 2^30, where the flags are
 
 bool stride_ok(int64_t s, int64_t unit) { return s >= 0 && s % unit == 0; }
 
@@ -51,8 +51,10 @@ int check_view(const qw_kv_view *kv) {
     return QW_OK;
 }
 
-int check_rows(const qw_kv_view *kv, const qw_kv_rows *r, const int32_t *start) {
+// written: the rows are the call's output, of which no two may share an address.
+int check_rows(const qw_kv_view *kv, const qw_kv_rows *r, const int32_t *start, const int32_t *count, bool written) {
     if (!r || !start || r->n_max < 0) return QW_INVALID_ARGUMENT;
+    if (!aligned(start, 4) || !aligned(count, 4)) return QW_ALIGNMENT;
     const int e = elem_bytes(r->dtype);
     if (!e) return QW_INVALID_ARGUMENT;
     if (r->n_max == 0) return QW_OK;
@@ -63,6 +65,8 @@ int check_rows(const qw_kv_view *kv, const qw_kv_rows *r, const int32_t *start) 
         !stride_ok(r->head_stride, unit) || !stride_ok(r->row_stride, unit))
         return QW_ALIGNMENT;
     if (r->row_stride < kv->head_dim && r->n_max > 1) return QW_INVALID_ARGUMENT;
+    if (written && ((kv->n_kv_heads > 1 && r->head_stride < kv->head_dim) || (kv->n_seq > 1 && r->seq_stride < kv->head_dim)))
+        return QW_INVALID_ARGUMENT;
     return QW_OK;
 }
 
@@ -81,7 +85,7 @@ extern "C" {
 int qw_kv_append(const qw_kv_view *kv, const qw_kv_rows *rows, const int32_t *start_dev, const int32_t *count_dev,
                  void *cuda_stream) {
     int rc = check_view(kv);
-    if (!rc) rc = check_rows(kv, rows, start_dev);
+    if (!rc) rc = check_rows(kv, rows, start_dev, count_dev, false);
     if (rc) return rc;
     return status_of(qw::launch_kv_append(*kv, *rows, start_dev, count_dev, (cudaStream_t)cuda_stream));
 }
@@ -89,7 +93,7 @@ int qw_kv_append(const qw_kv_view *kv, const qw_kv_rows *rows, const int32_t *st
 int qw_kv_read(const qw_kv_view *kv, const qw_kv_rows *rows, const int32_t *start_dev, const int32_t *count_dev,
                void *cuda_stream) {
     int rc = check_view(kv);
-    if (!rc) rc = check_rows(kv, rows, start_dev);
+    if (!rc) rc = check_rows(kv, rows, start_dev, count_dev, true);
     if (rc) return rc;
     return status_of(qw::launch_kv_read(*kv, *rows, start_dev, count_dev, (cudaStream_t)cuda_stream));
 }
@@ -114,8 +118,12 @@ int qw_tree_attention(const qw_kv_view *kv, const qw_tree_attention_args *a, voi
     if (!aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(scratch_dev, 256) || !stride_ok(a->q_seq_stride, unit) ||
         !stride_ok(a->q_node_stride, unit) || !stride_ok(a->q_head_stride, unit) ||
         !stride_ok(a->out_seq_stride, unit) || !stride_ok(a->out_node_stride, unit) ||
-        !stride_ok(a->out_head_stride, unit))
+        !stride_ok(a->out_head_stride, unit) || !aligned(a->mask, 8) || !aligned(a->len, 4) || !aligned(a->count, 4))
         return QW_ALIGNMENT;
+    const int D = kv->head_dim;  // no two rows of the result may share an address
+    if ((kv->n_seq > 1 && a->out_seq_stride < D) || (a->n_max > 1 && a->out_node_stride < D) ||
+        (a->n_heads > 1 && a->out_head_stride < D))
+        return QW_INVALID_ARGUMENT;
     if (scratch_bytes < qw_tree_attention_scratch_bytes(kv, a->n_max, a->n_heads, a->max_len)) return QW_OUT_OF_MEMORY;
     return status_of(qw::launch_tree_attn(*kv, *a, scratch_dev, (cudaStream_t)cuda_stream));
 }
@@ -128,6 +136,10 @@ int qw_process_logits(const qw_process_logits_args *a, void *cuda_stream) {
     if (a->n_rows > 65535) return QW_UNSUPPORTED_SHAPE;
     const int e = elem_bytes(a->dtype);
     if (!aligned(a->logits, e) || !aligned(a->out, e)) return QW_ALIGNMENT;
+    for (const void *p : {(const void *)a->penalties, (const void *)a->history, (const void *)a->history_range,
+                          (const void *)a->path, (const void *)a->bias_ids, (const void *)a->bias,
+                          (const void *)a->bias_range, (const void *)a->mask, (const void *)a->mask_index})
+        if (!aligned(p, 4)) return QW_ALIGNMENT;
     if (a->out == a->logits && a->row_stride != a->out_row_stride && a->n_rows > 1) return QW_INVALID_ARGUMENT;
     if (a->n_history < 0 || a->path_len < 0 || a->n_bias < 0 || a->n_masks < 0) return QW_INVALID_ARGUMENT;
     if (a->n_history > kMostEntries || a->path_len > kMostEntries || a->n_bias > kMostEntries) return QW_UNSUPPORTED_SHAPE;

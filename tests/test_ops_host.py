@@ -148,3 +148,31 @@ def test_packed_arguments_have_the_c_layout(qw):
         values = [i + 1 for i in range(len(cls._fields_))]
         got = cls.from_buffer_copy(packer.pack(*values))
         assert [getattr(got, name) for name, _ in cls._fields_] == values
+
+
+def test_arrays_off_their_types_boundary_are_refused(qw):
+    v, r, L = view(qw), rows(qw), qw.lib()
+    for call in (L.qw_kv_append, L.qw_kv_read):
+        assert call(ctypes.byref(v), ctypes.byref(r), P + 2, None, None) == qw.ALIGNMENT
+        assert call(ctypes.byref(v), ctypes.byref(r), P, P + 1, None) == qw.ALIGNMENT
+    for bad in (dict(mask=P + 4), dict(len=P + 2), dict(count=P + 2)):
+        a = tree_args(qw, **bad)
+        assert L.qw_tree_attention(ctypes.byref(v), ctypes.byref(a), P, 1 << 40, None) == qw.ALIGNMENT
+    for name in ("penalties", "history", "history_range", "path", "bias_ids", "bias", "bias_range", "mask", "mask_index"):
+        a = logits_args(qw, **{name: P + 2})
+        assert L.qw_process_logits(ctypes.byref(a), None) == qw.ALIGNMENT, name
+
+
+def test_results_that_share_an_address_are_refused(qw):
+    v, L = view(qw), qw.lib()
+    for bad in (dict(head_stride=0), dict(seq_stride=64)):
+        assert L.qw_kv_read(ctypes.byref(v), ctypes.byref(rows(qw, **bad)), P, None, None) == qw.INVALID_ARGUMENT
+    for bad in (dict(out_seq_stride=0), dict(out_node_stride=64), dict(out_head_stride=0)):
+        a = tree_args(qw, **bad)
+        assert L.qw_tree_attention(ctypes.byref(v), ctypes.byref(a), P, 1 << 40, None) == qw.INVALID_ARGUMENT
+
+
+def test_lists_longer_than_the_counters_are_refused(qw):
+    for bad in (dict(n_history=2**28 + 1), dict(path_len=2**28 + 1), dict(n_bias=2**28 + 1)):
+        a = logits_args(qw, **bad)
+        assert qw.lib().qw_process_logits(ctypes.byref(a), None) == qw.UNSUPPORTED_SHAPE
