@@ -510,17 +510,19 @@ def tree_attention(view: KvView, q, mask, lens, out=None, counts=None, max_len=N
     dev, shape, stride = view._dev, q.shape, q.stride()
     if len(shape) != 4 or shape[0] != view.n_seq or shape[3] != view.head_dim or stride[3] != 1 or q.get_device() != dev:
         raise ValueError("q must be [n_seq, n, n_heads, head_dim] beside the cache, with a contiguous last dimension")
-    if out is None:
-        out = _T.zeros_like(q, memory_format=_T.contiguous_format)
-    ostride = out.stride()
-    if out.shape != shape or out.dtype is not q.dtype or out.get_device() != dev or ostride[3] != 1:
-        raise ValueError("out must be like q, with a contiguous last dimension")
     n, heads = shape[1], shape[2]
     if max_len is None:
         max_len = view.max_ctx
-    if scratch is None:
-        scratch = tree_attention_scratch(view, n, heads, max_len)
-    elif scratch.get_device() != dev or not scratch.is_contiguous():
+    if out is None or scratch is None:
+        with _T.cuda.stream(stream):  # what is allocated here belongs to the stream that uses it
+            if out is None:
+                out = _T.zeros_like(q, memory_format=_T.contiguous_format)
+            if scratch is None:
+                scratch = tree_attention_scratch(view, n, heads, max_len)
+    ostride = out.stride()
+    if out.shape != shape or out.dtype is not q.dtype or out.get_device() != dev or ostride[3] != 1:
+        raise ValueError("out must be like q, with a contiguous last dimension")
+    if scratch.get_device() != dev or not scratch.is_contiguous():
         raise ValueError("scratch must be contiguous, beside the cache")
     i32 = _T.int32
     args = _TREE_ARGS.pack(q.data_ptr(), out.data_ptr(), _dtype_code(q, "q"), n, heads, max_len,
@@ -557,6 +559,8 @@ def process_logits(logits, out=None, *, history=None, history_range=None, path=N
         raise ValueError("bias_ids, bias and bias_range go together")
     if mask_index is not None and mask is None:
         raise ValueError("mask_index needs mask")
+    if mask is not None and mask.shape[0] == 0:
+        raise ValueError("mask must hold a mask")
     n_hist = 0 if history is None else history.numel()
     n_path = 0 if path is None else path.shape[-1]
     n_bias = 0 if bias is None else bias.numel()

@@ -144,6 +144,26 @@ def test_append_values_at_the_edges(qw):
     assert (o[0, 0, :, 32:] == float(one)).all()  # the other group is untouched by its neighbour
 
 
+@pytest.mark.parametrize("dt", [F32, F16, BF16])
+def test_append_codes_near_the_halves(qw, dt):
+    # elements within a few ulp of every half step of their group, at scales from subnormal to large
+    D, n = 128, 400
+    g = np.random.default_rng(12)
+    amax = (10.0 ** g.uniform(-38 if dt != F16 else -4, 6 if dt != F16 else 4, size=(n, D // 32, 1))).astype(np.float32)
+    d = amax / np.float32(127)
+    x = (g.integers(-127, 127, size=(n, D // 32, 32)) + 0.5).astype(np.float32) * d
+    x = np.nextafter(x, np.where(g.random(x.shape) < 0.5, np.inf, -np.inf).astype(np.float32))
+    x[:, :, :1] = amax
+    rows = torch.from_numpy(x.reshape(1, 1, n, D)).cuda().to(dt)
+    rows = torch.where(torch.isfinite(rows), rows, torch.ones_like(rows))
+    k, v, ks, vs = make_cache("int8", (1, 1, n, D), gen(1))
+    qw.kv_append(qw.KvView(k, v, ks, vs), rows, -rows, i32(0))
+    qc, qs = quantise(rows.float().cpu().numpy())
+    np.testing.assert_array_equal(k.cpu().numpy(), qc)
+    np.testing.assert_array_equal(v.cpu().numpy(), -qc)
+    np.testing.assert_array_equal(ks.cpu().numpy(), qs)
+
+
 def test_append_leaves_a_sequence_that_does_not_fit_alone(qw):
     k, v, ks, vs = make_cache("int8", (6, 2, 8, 64), gen(2))
     view = qw.KvView(k, v, ks, vs)
@@ -437,6 +457,26 @@ def test_tree_same_result_every_time_on_a_stream_and_in_a_graph(qw, dt, kind):
     assert torch.equal(outs[0], now) and torch.equal(outs[1], now) and not torch.equal(now, want)
 
 
+def test_tree_makes_its_result_on_the_stream_that_it_runs_on(qw):
+    view = qw.KvView(*make_cache("int8", (2, 2, 300, 64), gen(13)))
+    q = torch.randn((2, 5, 4, 64), device="cuda").to(BF16)
+    mask = torch.full((2, 5), 31, dtype=torch.int64, device="cuda")
+    lens = i32(290, 0)
+    want = qw.tree_attention(view, q, mask, lens).clone()
+    busy = torch.ones(1 << 26, device="cuda")
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    for _ in range(100):  # some 10 ms of work on the current stream, which the call does not wait for
+        busy.mul_(1.0)
+    out = qw.tree_attention(view, q, mask, lens, stream=st)
+    st.synchronize()
+    early = torch.empty_like(out)
+    with torch.cuda.stream(st):
+        early.copy_(out)
+    torch.cuda.synchronize()
+    assert torch.equal(early, want) and torch.equal(out, want)
+
+
 @pytest.mark.parametrize("dt", [F32, BF16])
 def test_cache_offsets_past_32_bits(qw, dt):
     D, C = 64, (1 << 26) + 100  # 4.3 GB of codes per plane
@@ -716,6 +756,22 @@ def test_binding_refusals(qw):
                 dict(mask=torch.zeros((1, 1), dtype=torch.int32, device="cuda")), dict(bias_ids=i32(1)), dict(path=i32(1))):
         with pytest.raises(ValueError):
             qw.process_logits(y, **bad)
+
+
+def test_results_over_one_another_and_empty_masks_are_refused(qw):
+    view = qw.KvView(*make_cache("int8", (2, 2, 16, 64), gen(1)))
+    x = torch.zeros((2, 2, 3, 64), device="cuda")
+    wide = x[:, :1].expand(2, 2, 3, 64)
+    qw.kv_append(view, wide, wide, i32(0, 0))  # one row for every head is a source like another
+    with pytest.raises(qw.QwError) as e:
+        qw.kv_read(view, wide, wide, i32(0, 0))
+    assert e.value.code == qw.INVALID_ARGUMENT
+    q = torch.zeros((2, 3, 4, 64), device="cuda")
+    with pytest.raises(qw.QwError) as e:
+        qw.tree_attention(view, q, torch.zeros((2, 3), dtype=torch.int64, device="cuda"), i32(0, 0), out=q[:1].expand(2, 3, 4, 64))
+    assert e.value.code == qw.INVALID_ARGUMENT
+    with pytest.raises(ValueError):
+        qw.process_logits(torch.zeros((2, 50), device="cuda"), mask=torch.zeros((0, 2), dtype=torch.int32, device="cuda"))
 
 
 # ---------------------------------------------------------------- together
