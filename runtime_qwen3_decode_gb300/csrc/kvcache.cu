@@ -26,11 +26,14 @@ struct RowArgs {
     int heads, n_max, max_ctx;
 };
 
-// E consecutive elements as they lie in memory.
+// E consecutive elements as they lie in memory.  Rows begin on 16-byte boundaries and no more, so eight
+// f32 elements (32 bytes) are two accesses of 16: a type aligned to 32 would let the compiler make
+// one access of 32 of them, which faults on a row that begins between two such boundaries.
 template <typename T, int E>
-struct alignas(sizeof(T) * E) Pack {
+struct alignas(sizeof(T) * E < 16 ? sizeof(T) * E : 16) Pack {
     T e[E];
 };
+static_assert(alignof(Pack<float, 8>) == 16, "rows are aligned to 16 bytes");
 
 // The 8-bit form of a 32-element group held by 32 / E adjacent lanes, E elements each: d = amax /
 // 127 in f32, code = a / d rounded half away from zero (the Q8_0 block's quantiser), scale =

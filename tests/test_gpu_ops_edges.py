@@ -1,0 +1,64 @@
+"""The operators on caller-owned buffers where their types, strides and lengths end: rows on the smallest
+alignment, values at the edges of the types, long contexts, and errors no larger than the number formats of
+the operands leave.
+
+Tolerances count roundings: u = eps / 2 of a type is the largest relative error of rounding to it.
+"""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from test_gpu_ops import BF16, F16, F32, U, gen, i32, make_cache, quantise, widen  # noqa: E402, F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def qw():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from runtime_qwen3_decode_gb300 import build, qw as binding
+    build.build()
+    return binding
+
+
+# ---------------------------------------------------------------- append and read
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "int8"])
+@pytest.mark.parametrize("dt", [F32, F16, BF16])
+@pytest.mark.parametrize("D,n", [(128, 3), (64, 300)])
+def test_rows_on_16_byte_boundaries_and_no_larger_ones(qw, kind, dt, D, n):
+    # the cache and the rows begin 16 bytes behind a larger boundary, and their rows are 16 bytes longer
+    B, H, C = 2, 3, n + 5
+    ct = {"f32": F32, "bf16": BF16, "int8": torch.int8}[kind]
+
+    def off(shape, t):
+        unit = 16 // torch.empty((), dtype=t).element_size()
+        whole = torch.zeros(int(np.prod(shape[:-1])) * (shape[-1] + unit) + unit, dtype=t, device="cuda")
+        x = whole[unit:].view(*shape[:-1], shape[-1] + unit)[..., :shape[-1]]
+        assert x.data_ptr() % 32 == 16
+        return x
+    k, v = off((B, H, C, D), ct), off((B, H, C, D), ct)
+    ks, vs = (torch.zeros((B, H, C, D // 32), dtype=F16, device="cuda") for _ in range(2)) if kind == "int8" else (None, None)
+    view = qw.KvView(k, v, ks, vs)
+    rows = [off((B, H, n, D), dt) for _ in range(2)]
+    for i, r in enumerate(rows):
+        r.copy_(torch.randn((B, H, n, D), generator=gen(40 + i), device="cuda").to(dt))
+    outs = [off((B, H, n, D), dt) for _ in range(2)]
+    start = i32(5, 2)
+    qw.kv_append(view, *rows, start)
+    qw.kv_read(view, *outs, start)
+    for r, c, s, o in zip(rows, (k, v), (ks, vs), outs):
+        for b, at in enumerate((5, 2)):
+            x = r[b].float()
+            if kind == "int8":
+                qc, qs = quantise(x.cpu().numpy())
+                want = torch.from_numpy(qc).cuda(), torch.from_numpy(qs).cuda()
+                assert torch.equal(s[b, :, at:at + n], want[1])
+                val = widen(*want).float()
+            else:
+                want = (x.to(ct),)
+                val = want[0].float()
+            assert torch.equal(c[b, :, at:at + n], want[0])
+            assert torch.equal(o[b], val.to(dt))
