@@ -372,7 +372,8 @@ int qw_kv_read(const qw_kv_view *kv, const qw_kv_rows *rows, const int32_t *star
  * while it runs.
  * Arithmetic: f32 accumulation, sums and softmax statistics.  With f32 queries, and in small calls,
  * every product is f32.  Otherwise the products are those of 16-bit operands on the tensor cores:
- * softmax weights rounded to the operands' type, K and V as follows.  bf16 queries over a bf16 cache:
+ * softmax weights rounded to the operands' type (in fp16, weights below 2^-34 of the largest
+ * count for nothing), K and V as follows.  bf16 queries over a bf16 cache:
  * bf16, as cached.  fp16 queries: fp16, with a second term for what the rounding of an 8-bit or f32 row
  * leaves.  bf16 queries over 8-bit or f32 rows: fp16, rounded once (2^-11; the result's own rounding
  * is 2^-8), the queries scaled by a power of two per row.  With fp16 operands cached magnitudes above

@@ -62,3 +62,33 @@ def test_rows_on_16_byte_boundaries_and_no_larger_ones(qw, kind, dt, D, n):
                 val = want[0].float()
             assert torch.equal(c[b, :, at:at + n], want[0])
             assert torch.equal(o[b], val.to(dt))
+
+
+# ---------------------------------------------------------------- tree attention
+
+@pytest.mark.parametrize("dt,kind", [(F16, "int8"), (F16, "f32"), (F16, "bf16"), (BF16, "int8"), (BF16, "f32"), (BF16, "bf16")])
+def test_a_long_tail_of_small_weights_counts(qw, dt, kind):
+    # One key stands out; each of the 2^17 others weighs 2^-25.2 of it, together 0.34% of the whole.  Their
+    # values are 1 and the key's own is 0, so the result is the tail's share.  max_len keeps the positions together.
+    C, D, n, heads = 1 << 17, 64, 16, 2
+    ct = {"f32": F32, "bf16": BF16, "int8": torch.int8}[kind]
+    k, v = (torch.zeros((1, 1, C + n, D), dtype=ct, device="cuda") for _ in range(2))
+    ks = vs = None
+    k[:, :, 12345, 0] = 64
+    v[:, :, :C] = 1
+    v[:, :, 12345] = 0
+    if kind == "int8":
+        ks, vs = (torch.ones((1, 1, C + n, D // 32), dtype=F16, device="cuda") for _ in range(2))
+    q = torch.zeros((1, n, heads, D), device="cuda")
+    q[..., 0] = 2.1875                                   # the key's score is 140 scale: exact in every type
+    scale = 25.2 * float(np.log(2)) / 140
+    mask = torch.zeros((1, n), dtype=torch.int64, device="cuda")  # nodes that see the cached positions only
+    got = qw.tree_attention(qw.KvView(k, v, ks, vs), q.to(dt), mask, i32(C), scale=scale, max_len=0).double()
+    tail = (C - 1) * 2.0 ** -25.2
+    want = tail / (1 + tail)
+    # Relative to the result: the score (an f32 product, 2^-24 of 25.2) and exp2 (2^-21) change a weight by under
+    # 2^-18 of it; its 16 bits by 2^-8 in bf16, and in fp16, held 2^9 above their reference, by 2^-25 of
+    # 2^-16.2; V is exact; a running f32 sum takes up to 2^15 additions of 2^-24 each; the result's own rounding.
+    weight = U[BF16] if dt is BF16 and kind != "int8" else 2.0 ** -8.8
+    tol = 2.0 ** -18 + weight + 2.0 ** -9 + U[dt]
+    assert ((got - want).abs() <= tol * want).all(), (float(got.min()), float(got.max()), want)
