@@ -276,6 +276,20 @@ __device__ __forceinline__ uint32_t rest2(float a, float b, uint32_t hi) {
     return pack2<false>(a - h.x, b - h.y);
 }
 
+// Whether one of eight fp16 numbers is infinite (or both of a pair's are NaN).
+__device__ __forceinline__ bool any_infinite(const uint4 &o) {
+    const __half2 *h = reinterpret_cast<const __half2 *>(&o);
+    const __half2 top = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])), __hmax2(__habs2(h[2]), __habs2(h[3])));
+    return !__hbne2(top, __half2half2(__ushort_as_half(0x7c00)));
+}
+
+// Second terms beside infinite first ones become 0, so that the two together are that infinity and not NaN.
+__device__ __noinline__ void drop_rest(const uint8_t *first, uint8_t *rest) {
+    const __half *h = reinterpret_cast<const __half *>(first);
+    for (int i = 0; i < 8; ++i)
+        if (__hisinf(h[i])) reinterpret_cast<uint16_t *>(rest)[i] = 0;
+}
+
 // Raw cache elements e .. e + 7 of a row as the operand holds them, for the fix-up of values that
 // are not finite.
 template <int SRC>
@@ -813,9 +827,11 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                     const int st = it % ST, slot = 2 * plane + (it & 1);
                     const bool check = plane && (t + 1) * kTcTile > s.len;
                     __half2 s2[U];
+                    bool over = false;  // codes times a scale above 65504 / 127 may be infinite
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
                         s2[u] = __half2half2(sc[0][u]);
+                        if constexpr (TERMS == 2) over |= !(__habs(sc[0][u]) <= __float2half_rn(515.f));
                         sc[0][u] = sc[1][u];
                     }
                     if (t + 2 < s.t1) fetch(sc[1], t + 2);
@@ -851,6 +867,15 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                     };
                     if (check) all(std::true_type());
                     else all(std::false_type());
+                    if constexpr (TERMS == 2) {
+                        if (over) {
+#pragma unroll 1
+                            for (int i = 0; i < 4 * U; ++i) {
+                                uint8_t *at = dst + swz128(row0 + RSTEP * (i >> 2), 4 * (g & 1) + (i & 3));
+                                drop_rest(at, at + C::kTerm);
+                            }
+                        }
+                    }
                     finish(any, slot, &full[st]);
                 }
                 ++seg;
@@ -878,7 +903,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
 #pragma unroll
                         for (int u = 0; u < U; ++u)
                             load8(reinterpret_cast<const Raw *>(src) + (row0 + RSTEP * u) * D + 8 * c, v[u]);
-                        bool any = false;
+                        bool any = false, over = false;
                         auto all = [&](auto checked) {
 #pragma unroll
                             for (int u = 0; u < U; ++u) {
@@ -887,14 +912,25 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                                 const uint4 o = make_uint4(pack2<false>(f[0], f[1]), pack2<false>(f[2], f[3]),
                                                            pack2<false>(f[4], f[5]), pack2<false>(f[6], f[7]));
                                 uint4 rest = make_uint4(0u, 0u, 0u, 0u);
-                                if constexpr (TERMS == 2)
+                                if constexpr (TERMS == 2) {
                                     rest = make_uint4(rest2(f[0], f[1], o.x), rest2(f[2], f[3], o.y), rest2(f[4], f[5], o.z),
                                                       rest2(f[6], f[7], o.w));
+                                    over |= any_infinite(o);
+                                }
                                 any |= put(dst + swz128(row, c & 7), o, rest, checked, t * kTcTile + row);
                             }
                         };
                         if (check) all(std::true_type());
                         else all(std::false_type());
+                        if constexpr (TERMS == 2) {
+                            if (over) {
+#pragma unroll 1
+                                for (int u = 0; u < U; ++u) {
+                                    uint8_t *at = dst + swz128(crow + row0 + RSTEP * u, c & 7);
+                                    drop_rest(at, at + C::kTerm);
+                                }
+                            }
+                        }
                         finish(any, slot, ch == C::kChunks - 1 ? &full[st] : nullptr);
                     }
                 }

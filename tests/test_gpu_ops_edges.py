@@ -92,3 +92,43 @@ def test_a_long_tail_of_small_weights_counts(qw, dt, kind):
     weight = U[BF16] if dt is BF16 and kind != "int8" else 2.0 ** -8.8
     tol = 2.0 ** -18 + weight + 2.0 ** -9 + U[dt]
     assert ((got - want).abs() <= tol * want).all(), (float(got.min()), float(got.max()), want)
+
+
+@pytest.mark.parametrize("kind", ["f32", "int8"])
+@pytest.mark.parametrize("drafted", [False, True])
+def test_what_fp16_operands_cannot_hold_is_infinite(qw, kind, drafted):
+    # fp16 queries, 16 x 2 rows: 16-bit operands.  Cached magnitudes above 65504 are infinite: not NaN, and the same
+    # for cached rows and drafted ones.
+    n, L, D = 16, 200, 128
+    ct = F32 if kind == "f32" else torch.int8
+    k, v = (torch.zeros((1, 1, L + n, D), dtype=ct, device="cuda") for _ in range(2))
+    ks = vs = None
+    if kind == "int8":
+        ks, vs = (torch.ones((1, 1, L + n, D // 32), dtype=F16, device="cuda") for _ in range(2))
+    v[:] = 1
+    at = L + 3 if drafted else 77
+    if kind == "f32":
+        v[0, 0, at, 5], v[0, 0, at, 6] = 1e5, -float("inf")
+        v[0, 0, at, 70] = -65504.0 * 1.5
+        k[0, 0, at - 2, 9] = 1e6
+    else:
+        vs[0, 0, at, 0], vs[0, 0, at, 2] = 1000, 1000        # groups of dims 0-31 and 64-95
+        v[0, 0, at, :32] = 0
+        v[0, 0, at, 64:96] = 0
+        v[0, 0, at, 5], v[0, 0, at, 6], v[0, 0, at, 70] = 100, -127, -66
+        ks[0, 0, at - 2, 0] = 60000
+        k[0, 0, at - 2, 9] = 100
+    q = torch.zeros((1, n, 2, D), dtype=F16, device="cuda")
+    q[..., 9] = -1                                           # -inf for that key: weight 0
+    mask = torch.full((1, n), (1 << n) - 1, dtype=torch.int64, device="cuda")
+    got = qw.tree_attention(qw.KvView(k, v, ks, vs), q, mask, i32(L))[0].float()
+    inf = float("inf")
+    assert (got[..., 5] == inf).all() and (got[..., 6] == -inf).all() and (got[..., 70] == -inf).all()
+    keep = torch.ones(D, dtype=torch.bool, device="cuda")
+    keep[[5, 6, 70]] = False
+    if kind == "int8":                                       # the bad row's zeros beside 214 ones
+        keep[:32] = keep[64:96] = False
+        rest = torch.cat([got[..., 7:32], got[..., 71:96]], -1)
+        assert ((rest - 214 / 215).abs() <= 2 * U[F16]).all()
+    # equal weights of 215 keys on ones: exact but for the weights' sum and the quotient in f32, then one rounding
+    assert ((got[..., keep] - 1).abs() <= U[F16]).all()
