@@ -374,10 +374,10 @@ int qw_kv_read(const qw_kv_view *kv, const qw_kv_rows *rows, const int32_t *star
  * every product is f32.  Otherwise the products are those of 16-bit operands on the tensor cores:
  * softmax weights rounded to the operands' type (in fp16, weights below 2^-34 of the largest
  * count for nothing), K and V as follows.  bf16 queries over a bf16 cache:
- * bf16, as cached.  fp16 queries: fp16, with a second term for what the rounding of an 8-bit or f32 row
- * leaves.  bf16 queries over 8-bit or f32 rows: fp16, rounded once (2^-11; the result's own rounding
- * is 2^-8), the queries scaled by a power of two per row.  With fp16 operands cached magnitudes above
- * 65504 are infinite.
+ * bf16, as cached; over an f32 cache two bf16 terms (2^-16, f32's range); over 8-bit rows fp16, rounded
+ * once (2^-11; the result's own rounding is 2^-8), the queries scaled by a power of two per row.  fp16 queries:
+ * fp16, with a second term for what the rounding of an 8-bit or f32 row leaves.  With fp16 operands cached
+ * magnitudes above 65504 are infinite, and what lies below 2^-25 is 0.
  */
 enum { QW_TREE_NODES_MAX = 64 };
 typedef struct {

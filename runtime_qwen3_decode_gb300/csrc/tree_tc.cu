@@ -24,13 +24,14 @@
 // two-term tiles).  8-bit rows become fp16 (code * scale rounded once, 2^-11; bf16 would lose
 // three more bits and cost twice the instructions), bf16 queries beside them fp16 after
 // division by a power of two per row, so that only elements 2^-14 below the row's largest
-// lose bits.
+// lose bits.  f32 rows become two fp16 terms beside fp16 queries and two bf16 terms beside bf16 ones,
+// whose range they keep (one fp16 term took 77 us instead of 96, and made V infinite above 65504).
 //
 // Measured (device time with the merge; HBM floor): 64 nodes over 32768 bf16 positions 37 us
 // (20): HBM while it streams, 5 us until the first tiles arrive, 8 us of last tile and merge.
 // 16 sequences of up to 33 nodes over 8-bit caches of up to 4096 57 us (14): the chain softmax,
 // product, next scores of each group, 2700 cycles a tile.  64 fp16 nodes over 32768 8-bit
-// positions 52 us (11), over f32 ones 96 us (40).
+// positions 52 us (11); over f32 ones 97 us (40), bf16 nodes 96 us.
 //
 // What a row does not see has weight 0, but 0 x NaN is NaN in the product with V: the V
 // rows behind the sequence are zeroed, and elements of drafted rows that are not finite are
@@ -51,7 +52,8 @@ namespace {
 
 using namespace tc;
 
-enum { SRC_BF16 = 0, SRC_Q8_F16 = 1, SRC_BF16_F16 = 2, SRC_F32_F16 = 3 };
+// cache rows and, behind it, the operands' type where they are converted
+enum { SRC_BF16 = 0, SRC_Q8_F16 = 1, SRC_BF16_F16 = 2, SRC_F32_F16 = 3, SRC_F32_BF16 = 4 };
 
 // The loading and the MMA warp sit on the SM sub-partitions of the last row quarters, whose softmax
 // warps have nothing to do for small trees.
@@ -61,11 +63,11 @@ constexpr int kPlaneWarps = kConvWarps / 2, kPlaneThreads = 32 * kPlaneWarps;
 // TMEM columns of softmax group g: scores (and P over them) at 128 g, accumulator at 256 + 128 g
 constexpr uint32_t kColO = 256;
 
-// TERMS: 16-bit numbers per K or V element, 2 = an fp16 and the fp16 of what it leaves.
+// TERMS: 16-bit numbers per K or V element, 2 = a number of the operands' type and the one of what it leaves.
 template <int SRC, int D, int TERMS>
 struct Cfg {
     static constexpr bool kDirect = SRC == SRC_BF16;
-    static constexpr bool kBf16 = SRC == SRC_BF16;
+    static constexpr bool kBf16 = SRC == SRC_BF16 || SRC == SRC_F32_BF16;  // the operands' type, else fp16
     // A tile's weights are 2^(score - reference + kLift).  The reference follows the maximum only when that has
     // risen by more than kLag (rescaling an accumulator costs a pass over it), so weights end below
     // 2^(kLag + kLift).  fp16 drops what is below 2^-25: lifted by 9, that is 2^-34 of the reference, and a
@@ -73,7 +75,7 @@ struct Cfg {
     // whole counted for half of that).  A lag of 4 and a lift of 11 took 58.3 us for the 16-sequence case below
     // instead of 57.4, 8 and 7 56.7.  bf16 has f32's range.
     static constexpr float kLag = kBf16 ? 8.f : 6.f, kLift = kBf16 ? 0.f : 9.f;
-    static constexpr int kElem = SRC == SRC_Q8_F16 ? 1 : SRC == SRC_F32_F16 ? 4 : 2;
+    static constexpr int kElem = SRC == SRC_Q8_F16 ? 1 : SRC == SRC_F32_F16 || SRC == SRC_F32_BF16 ? 4 : 2;
     static constexpr int kThreads = 32 * (kDirect ? kPlainWarps : kPlainWarps + kConvWarps - 2);
     static constexpr int kRegion = 128 * 128;              // 128 rows x 64 16-bit dims
     static constexpr int kTerm = kRegion * (D / 64);       // one term of a K or V operand tile
@@ -276,6 +278,18 @@ __device__ __forceinline__ uint32_t rest2(float a, float b, uint32_t hi) {
     return pack2<false>(a - h.x, b - h.y);
 }
 
+// Two f32 as two bf16 terms each: the first cut, so that what is finite stays finite, the second the rest
+// rounded; together they are off by 2^-16 at most.  Beside an infinity the rest, inf - inf, is made finite.
+__device__ __forceinline__ uint32_t cut2(float a, float b) {
+    uint32_t d;
+    asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+    return d;
+}
+__device__ __forceinline__ uint32_t cut_rest2(float a, float b, uint32_t hi) {
+    const float ha = __uint_as_float(hi << 16), hb = __uint_as_float(hi & 0xffff0000u);
+    return pack2<true>(fmaxf(a - ha, -1e38f), fmaxf(b - hb, -1e38f));
+}
+
 // Whether one of eight fp16 numbers is infinite (or both of a pair's are NaN).
 __device__ __forceinline__ bool any_infinite(const uint4 &o) {
     const __half2 *h = reinterpret_cast<const __half2 *>(&o);
@@ -284,8 +298,9 @@ __device__ __forceinline__ bool any_infinite(const uint4 &o) {
 }
 
 // Second terms beside infinite first ones become 0, so that the two together are that infinity and not NaN.
-__device__ __noinline__ void drop_rest(const uint8_t *first, uint8_t *rest) {
+__device__ __forceinline__ void drop_rest(const uint8_t *first, uint8_t *rest) {
     const __half *h = reinterpret_cast<const __half *>(first);
+#pragma unroll 1
     for (int i = 0; i < 8; ++i)
         if (__hisinf(h[i])) reinterpret_cast<uint16_t *>(rest)[i] = 0;
 }
@@ -301,6 +316,7 @@ __device__ __forceinline__ float operand_value(const TreeArgs &a, const uint8_t 
     else if constexpr (SRC == SRC_BF16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(plane)[row + d]);
     else if constexpr (SRC == SRC_BF16_F16)
         return __half2float(__float2half_rn(__bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(plane)[row + d])));
+    else if constexpr (SRC == SRC_F32_BF16) return reinterpret_cast<const float *>(plane)[row + d];
     else return __half2float(__float2half_rn(reinterpret_cast<const float *>(plane)[row + d]));
 }
 
@@ -516,7 +532,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
             {
                 constexpr int LPR = D / 8, RPP = 8 * 32 / LPR;  // lanes per row; rows per pass of all warps
                 const int c = lane % LPR, first = warp * (32 / LPR) + lane / LPR;
-                const bool scaled = SRC != SRC_BF16 && a.dtype == QW_DT_BF16;
+                const bool scaled = !C::kBf16 && a.dtype == QW_DT_BF16;
                 const uint16_t *qb = reinterpret_cast<const uint16_t *>(a.q) + s.b * a.qseq + (int64_t)s.h * a.G * a.qhead + 8 * c;
                 uint8_t *tile = sQ + (c >> 3) * C::kRegion;
                 for (int x = first; x < nr; x += RPP) {
@@ -565,7 +581,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                 }
             }
             if (s.n < 64) mask &= (1ull << s.n) - 1ull;
-            const bool scaled_row = SRC != SRC_BF16 && a.dtype == QW_DT_BF16 && live;
+            const bool scaled_row = !C::kBf16 && a.dtype == QW_DT_BF16 && live;
             const float sc = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2) * (scaled_row ? row_scale[r] : 1.f);
             float m_used = -INFINITY, l = 0.f;
             int mine = 0;  // tiles of this segment that this group has done
@@ -783,9 +799,9 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
             if constexpr (decltype(checked)::value) {  // V rows of the sequence's end
                 if (pos >= s.total) {
                     o = rest = make_uint4(0u, 0u, 0u, 0u);
-                } else if (pos >= s.len && only_finite<false>(o)) {
+                } else if (pos >= s.len && only_finite<C::kBf16>(o)) {
                     any = true;
-                    only_finite<false>(rest);  // not finite where o was not
+                    only_finite<C::kBf16>(rest);  // not finite where o was not
                 }
             }
             *reinterpret_cast<uint4 *>(at) = o;
@@ -909,10 +925,14 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                             for (int u = 0; u < U; ++u) {
                                 const int row = crow + row0 + RSTEP * u;
                                 const float *f = v[u];
-                                const uint4 o = make_uint4(pack2<false>(f[0], f[1]), pack2<false>(f[2], f[3]),
-                                                           pack2<false>(f[4], f[5]), pack2<false>(f[6], f[7]));
+                                auto first = [](float x, float y) { return C::kBf16 ? cut2(x, y) : pack2<false>(x, y); };
+                                const uint4 o = make_uint4(first(f[0], f[1]), first(f[2], f[3]), first(f[4], f[5]),
+                                                           first(f[6], f[7]));
                                 uint4 rest = make_uint4(0u, 0u, 0u, 0u);
-                                if constexpr (TERMS == 2) {
+                                if constexpr (C::kBf16) {
+                                    rest = make_uint4(cut_rest2(f[0], f[1], o.x), cut_rest2(f[2], f[3], o.y),
+                                                      cut_rest2(f[4], f[5], o.z), cut_rest2(f[6], f[7], o.w));
+                                } else if constexpr (TERMS == 2) {
                                     rest = make_uint4(rest2(f[0], f[1], o.x), rest2(f[2], f[3], o.y), rest2(f[4], f[5], o.z),
                                                       rest2(f[6], f[7], o.w));
                                     over |= any_infinite(o);
@@ -1106,10 +1126,11 @@ cudaError_t launch_src(const TcParams &p, const qw_kv_view &kv, int ctas, cudaSt
                     dim3(kMergeThreads), 0, st, p, ctas);
 }
 
-// 16-bit results next to fp16 operands: beside bf16 queries one rounding of K and V (2^-11) drowns in
+// 16-bit results next to fp16 operands: beside bf16 queries one rounding of 8-bit K and V (2^-11) drowns in
 // the result's own (2^-8); beside fp16 queries it would be most of the error (rounded scores alone
 // left a relative error of 5.5e-4 where the result's rounding leaves 2.1e-4), so K and V
-// that fp16 does not hold exactly come as two terms.
+// that fp16 does not hold exactly come as two terms.  bf16 queries over f32 rows: fp16 would lose the range that
+// both the rows and the result have, and one bf16 term most of the rows' bits, so two bf16 terms.
 template <int D>
 cudaError_t launch_dim(const TcParams &p, const qw_kv_view &kv, int ctas, cudaStream_t st, bool ch) {
     const bool f16 = p.a.dtype == QW_DT_F16;
@@ -1117,7 +1138,7 @@ cudaError_t launch_dim(const TcParams &p, const qw_kv_view &kv, int ctas, cudaSt
         return f16 ? launch_src<SRC_Q8_F16, D, 2>(p, kv, ctas, st, ch) : launch_src<SRC_Q8_F16, D, 1>(p, kv, ctas, st, ch);
     if (kv.format == QW_KV_BF16)
         return f16 ? launch_src<SRC_BF16_F16, D, 1>(p, kv, ctas, st, ch) : launch_src<SRC_BF16, D, 1>(p, kv, ctas, st, ch);
-    return f16 ? launch_src<SRC_F32_F16, D, 2>(p, kv, ctas, st, ch) : launch_src<SRC_F32_F16, D, 1>(p, kv, ctas, st, ch);
+    return f16 ? launch_src<SRC_F32_F16, D, 2>(p, kv, ctas, st, ch) : launch_src<SRC_F32_BF16, D, 2>(p, kv, ctas, st, ch);
 }
 
 }  // namespace

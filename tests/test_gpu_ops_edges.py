@@ -9,7 +9,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_ops import BF16, F16, F32, U, gen, i32, make_cache, quantise, widen  # noqa: E402, F401
+from test_gpu_ops import BF16, F16, F32, U, gen, i32, make_cache, quantise, tree_reference, widen  # noqa: E402, F401
 
 pytestmark = pytest.mark.gpu
 
@@ -132,3 +132,23 @@ def test_what_fp16_operands_cannot_hold_is_infinite(qw, kind, drafted):
         assert ((rest - 214 / 215).abs() <= 2 * U[F16]).all()
     # equal weights of 215 keys on ones: exact but for the weights' sum and the quotient in f32, then one rounding
     assert ((got[..., keep] - 1).abs() <= U[F16]).all()
+
+
+@pytest.mark.parametrize("max_len", [0, 300])
+@pytest.mark.parametrize("n,heads", [(16, 2), (1, 2)])
+@pytest.mark.parametrize("sk,sv", [(1.0, 1e-8), (1.0, 1e6), (1e-9, 1e30), (1e8, 1e-30)])
+def test_bf16_queries_over_f32_rows_keep_their_range(qw, sk, sv, n, heads, max_len):
+    # the result can hold what f32 rows hold; how long the caller thinks that the sequences are changes nothing
+    L, D = 300, 128
+    g = gen(50)
+    k, v = (torch.randn((1, 1, L + n, D), generator=g, device="cuda") * s for s in (sk, sv))
+    q = torch.randn((1, n, heads, D), generator=g, device="cuda").to(BF16)
+    scale = D ** -0.5 / sk
+    mask = torch.from_numpy(qw.tree_mask(range(-1, n - 1)).view(np.int64)).cuda()[None]
+    got = qw.tree_attention(qw.KvView(k, v), q, mask, i32(L), scale=scale, max_len=max_len)
+    ref, mag, vmax = tree_reference(q, (k, v, None, None), mask, [L], [n], scale)
+    # K and V are two bf16 terms (2^-16 at most); a score error e changes the mean of v by at most 2 e max|v|; f32
+    # sums of D and of L + n terms; exp2; weights in bf16, and the result
+    score = mag * (2.0 ** -16 + (D + 4) * 2.0 ** -24)
+    tol = (2 * score + U[BF16] + 2.0 ** -16 + 2.0 ** -20 + (L + n) * 2.0 ** -24) * vmax
+    assert ((got.double() - ref).abs() <= tol[..., None] + ref.abs() * U[BF16]).all()
