@@ -15,9 +15,9 @@
 // chunk are issued as soon as this one's values are out.  (One chunk per CTA spent most of
 // its time waiting in turn for the lists and for the logits: 256 x 151936 f32 took 91 us; now 74,
 // 4.2 TB/s, 62% of the measured copy rate.)
-// Counts are whole numbers, so the order of their atomics does not matter; a bias named more
-// than once is summed by the list's first entry alone, in order, so results do not depend
-// on timing.
+// Counts are whole numbers, so the order of their atomics does not matter; the biases of a token that
+// is named more than once are added to its logit by the list's first entry alone, in order,
+// so results do not depend on timing.
 #include "qw_ops.h"
 
 namespace qw {
@@ -69,7 +69,8 @@ template <typename T, int kThreads, int ROWS, bool SPARSE>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_kernel(const qw_process_logits_args a, int chunks) {
     constexpr bool VEC = ROWS != ROWS_ANY;
     constexpr int kTok = kThreads * 4 * kVecs;
-    extern __shared__ __align__(16) uint32_t sm[];  // [kTok] counts and flags; of the flagged: first list entry, bias
+    // [kTok] counts and flags; of the flagged: first list entry, and the bias or (named twice) the biased logit
+    extern __shared__ __align__(16) uint32_t sm[];
     uint32_t *cnt = sm, *entry = sm + kTok;
     float *add = reinterpret_cast<float *>(sm + 2 * kTok);
     const int r = blockIdx.y, V = a.vocab, tid = threadIdx.x;
@@ -89,6 +90,13 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_kernel(const
         }
         if (a.bias) bias = list_range(a.bias_range, r, a.n_bias);
     }
+    auto penalised = [&](float x, uint32_t c) {
+        if (c & kCount) {
+            x = x > 0.f ? x / rep : x * rep;
+            x -= pres + freq * (float)(c & kCount);
+        }
+        return x;
+    };
     float v[kVecs][4];
     uint32_t word[kVecs];  // the vector's mask bits
     auto load = [&](int base) {
@@ -156,18 +164,21 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_kernel(const
                 if (atomicOr(cnt + t, kNamed) & kNamed) atomicOr(cnt + t, kTwice);
                 atomicMin(entry + t, (uint32_t)i);
             };
-            // entry i of the list: its first mention holds the sum of all
-            auto settle = [&](int i, int32_t id, float sum) {
+            // entry i of the list: the first mention of a token does the work of all.  Its logit is still in src, in
+            // place too: this chunk is written behind the barrier below.
+            auto settle = [&](int i, int32_t id, float x) {
                 const uint32_t t = (uint32_t)id - (uint32_t)base;
                 if (t >= (uint32_t)kTok || entry[t] != (uint32_t)i) return;
-                if (cnt[t] & kTwice) {
+                const uint32_t c = cnt[t];
+                if ((c & kTwice) && (uint32_t)id < (uint32_t)V) {
+                    x += penalised(elem_to_f(src[id]), c);
 #pragma unroll 8
                     for (int k = i + 1; k < bias.y; ++k) {
                         const int32_t other = a.bias_ids[k];
-                        if (other == id) sum += a.bias[k];
+                        if (other == id) x += a.bias[k];
                     }
                 }
-                add[t] = sum;
+                add[t] = x;
             };
             count(own);
 #pragma unroll
@@ -191,12 +202,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_kernel(const
             const int l0 = 4 * (tid + kThreads * j), t0 = base + l0;
             // most vectors hold no listed token
             auto listed = [&](float x, uint32_t c, int l) {
-                if (c & kCount) {
-                    x = x > 0.f ? x / rep : x * rep;
-                    x -= pres + freq * (float)(c & kCount);
-                }
+                x = penalised(x, c);
                 if (c & kNamed) {
-                    x += add[l];
+                    x = c & kTwice ? add[l] : x + add[l];
                     entry[l] = ~0u;  // for the next chunk
                 }
                 return x;

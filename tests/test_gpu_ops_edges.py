@@ -152,3 +152,42 @@ def test_bf16_queries_over_f32_rows_keep_their_range(qw, sk, sv, n, heads, max_l
     score = mag * (2.0 ** -16 + (D + 4) * 2.0 ** -24)
     tol = (2 * score + U[BF16] + 2.0 ** -16 + 2.0 ** -20 + (L + n) * 2.0 ** -24) * vmax
     assert ((got.double() - ref).abs() <= tol[..., None] + ref.abs() * U[BF16]).all()
+
+
+# ---------------------------------------------------------------- logits
+
+@pytest.mark.parametrize("dt", [F32, F16, BF16])
+@pytest.mark.parametrize("V,off,in_place", [(5000, 0, True), (5000, 0, False), (4099, 3, False), (4099, 3, True), (40, 0, True)])
+def test_biases_of_a_token_are_added_one_after_the_other(qw, dt, V, off, in_place):
+    # behind the penalties, each sum rounded: large logits swallow biases that would count if they were added up first
+    R = 3
+    g = np.random.default_rng(V)
+    named = [t for t in (0, 1, 2, 31, 39, 2047, 2048, V - 1) if t < V]
+    x0 = (g.choice([-1.0, 1.0], size=(R, V)) * g.choice([0.5, 3.0, 60.0], size=(R, V))).astype(np.float32)
+    big = np.float32(2.0 ** 25 if dt != F16 else 2.0 ** 15)
+    x0[:, named] = big * g.choice([-1.0, 1.0], size=(R, len(named)))
+    ids = np.array(named * 5 + [-1, V, V + 1], dtype=np.int32)
+    g.shuffle(ids)
+    bias = g.choice([-3.0, -1.0, 1.0, 3.0, 2.0 ** -12], size=ids.size).astype(np.float32)
+    bias[0] = -big
+    whole = torch.zeros((R, V + off + 1), dtype=dt, device="cuda")
+    x = whole[:, off:off + V]
+    x.copy_(torch.from_numpy(x0).cuda())
+    x0 = x.float().cpu().numpy()
+    hist = np.array([named[0], named[1], named[1], 5], np.int32)
+    want = x0.copy()
+    for r in range(R):
+        for t in set(hist.tolist()):
+            c = int((hist == t).sum())
+            z = want[r, t]
+            z = z / np.float32(2) if z > 0 else z * np.float32(2)
+            want[r, t] = z - (np.float32(0.25) + np.float32(0.5) * np.float32(c))
+        for i, b in zip(ids, bias):
+            if 0 <= i < V:
+                want[r, i] = np.float32(want[r, i] + b)
+    cu = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    out = x if in_place else torch.empty_like(whole)[:, off:off + V]
+    qw.process_logits(x, out, penalties=cu(np.array([[2, 0.25, 0.5]] * R, np.float32)), history=cu(hist),
+                      history_range=cu(np.array([[0, 4]] * R, np.int32)), bias_ids=cu(ids), bias=cu(bias),
+                      bias_range=cu(np.array([[0, ids.size]] * R, np.int32)))
+    assert torch.equal(out.float(), cu(want).to(dt).float())
