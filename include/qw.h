@@ -322,6 +322,10 @@ int qw_batch_tree_accept(qw_batch *b, int32_t seq, int32_t n, const int32_t *nod
  * of each row with strides of their own (else they are ignored).  Rows begin on 16-byte
  * boundaries (codes and scales too: 8 bytes for codes, head_dim / 16 bytes for scales are enough;
  * strides are multiples of that), or QW_ALIGNMENT.
+ * n_seq <= 65535, n_kv_heads <= 1024.  A cache that is written (qw_kv_append) has an address of its own
+ * for every row: of the strides of dimensions longer than one, sorted, each one is at least what the ones
+ * before it span; and k is not v.  The same holds for the rows of qw_kv_read and the out of
+ * qw_tree_attention.  QW_INVALID_ARGUMENT otherwise.
  */
 typedef struct {
     void *k, *v, *k_scale, *v_scale;

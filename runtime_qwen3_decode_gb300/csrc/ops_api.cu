@@ -1,6 +1,7 @@
 // ops_api.cu - argument checks of the operators on caller-owned buffers (qw_kv_append,
 // qw_kv_read, qw_tree_attention, qw_process_logits).  Everything is checked before a launch;
 // nothing here touches the device.
+#include <algorithm>
 #include <cmath>
 
 #include "qw.h"
@@ -24,6 +25,34 @@ constexpr int32_t kMostEntries = 1 << 28;  // of a list: a token's count in two 
 
 bool stride_ok(int64_t s, int64_t unit) { return s >= 0 && s % unit == 0; }
 
+// Whether rows of `len` elements along three dimensions have addresses of their own: taken from the smallest
+// stride up, each one is no shorter than all that the dimensions before it span.
+struct Dim {
+    int64_t size, stride;
+};
+bool rows_apart(int64_t len, Dim a, Dim b, Dim c) {
+    Dim d[3] = {a, b, c};
+    std::sort(d, d + 3, [](const Dim &x, const Dim &y) { return x.stride < y.stride; });
+    __int128 span = len;
+    for (const Dim &x : d) {
+        if (x.size <= 1) continue;
+        if (x.stride < span) return false;
+        span += (__int128)(x.size - 1) * x.stride;
+    }
+    return true;
+}
+
+// The cache as something that is written: no two of its rows may share an address, nor may its planes.
+bool writable(const qw_kv_view *kv) {
+    if (kv->k == kv->v || !rows_apart(kv->head_dim, {kv->n_seq, kv->seq_stride}, {kv->n_kv_heads, kv->head_stride},
+                                      {kv->max_ctx, kv->pos_stride}))
+        return false;
+    return kv->format != QW_KV_INT8_G32 ||
+           (kv->k_scale != kv->v_scale &&
+            rows_apart(kv->head_dim / qw::kQGroup, {kv->n_seq, kv->scale_seq_stride}, {kv->n_kv_heads, kv->scale_head_stride},
+                       {kv->max_ctx, kv->scale_pos_stride}));
+}
+
 int check_view(const qw_kv_view *kv) {
     if (!kv || !kv->k || !kv->v) return QW_INVALID_ARGUMENT;
     if (kv->format != QW_KV_F32 && kv->format != QW_KV_BF16 && kv->format != QW_KV_INT8_G32) return QW_INVALID_ARGUMENT;
@@ -34,7 +63,7 @@ int check_view(const qw_kv_view *kv) {
     if (!aligned(kv->k, 16) || !aligned(kv->v, 16) || !stride_ok(kv->seq_stride, unit) ||
         !stride_ok(kv->head_stride, unit) || !stride_ok(kv->pos_stride, unit))
         return QW_ALIGNMENT;
-    // no two rows may share an address
+    // rows of one dimension do not overlap (those of a cache that is written share no address at all: writable())
     if ((kv->max_ctx > 1 && kv->pos_stride < kv->head_dim) || (kv->n_kv_heads > 1 && kv->head_stride < kv->head_dim) ||
         (kv->n_seq > 1 && kv->seq_stride < kv->head_dim))
         return QW_INVALID_ARGUMENT;
@@ -65,7 +94,8 @@ int check_rows(const qw_kv_view *kv, const qw_kv_rows *r, const int32_t *start, 
         !stride_ok(r->head_stride, unit) || !stride_ok(r->row_stride, unit))
         return QW_ALIGNMENT;
     if (r->row_stride < kv->head_dim && r->n_max > 1) return QW_INVALID_ARGUMENT;
-    if (written && ((kv->n_kv_heads > 1 && r->head_stride < kv->head_dim) || (kv->n_seq > 1 && r->seq_stride < kv->head_dim)))
+    if (written && (r->k == r->v || !rows_apart(kv->head_dim, {kv->n_seq, r->seq_stride}, {kv->n_kv_heads, r->head_stride},
+                                                {r->n_max, r->row_stride})))
         return QW_INVALID_ARGUMENT;
     return QW_OK;
 }
@@ -86,6 +116,7 @@ int qw_kv_append(const qw_kv_view *kv, const qw_kv_rows *rows, const int32_t *st
                  void *cuda_stream) {
     int rc = check_view(kv);
     if (!rc) rc = check_rows(kv, rows, start_dev, count_dev, false);
+    if (!rc && !writable(kv)) rc = QW_INVALID_ARGUMENT;
     if (rc) return rc;
     return status_of(qw::launch_kv_append(*kv, *rows, start_dev, count_dev, (cudaStream_t)cuda_stream));
 }
@@ -120,9 +151,9 @@ int qw_tree_attention(const qw_kv_view *kv, const qw_tree_attention_args *a, voi
         !stride_ok(a->out_seq_stride, unit) || !stride_ok(a->out_node_stride, unit) ||
         !stride_ok(a->out_head_stride, unit) || !aligned(a->mask, 8) || !aligned(a->len, 4) || !aligned(a->count, 4))
         return QW_ALIGNMENT;
-    const int D = kv->head_dim;  // no two rows of the result may share an address
-    if ((kv->n_seq > 1 && a->out_seq_stride < D) || (a->n_max > 1 && a->out_node_stride < D) ||
-        (a->n_heads > 1 && a->out_head_stride < D))
+    // no two rows of the result may share an address
+    if (!rows_apart(kv->head_dim, {kv->n_seq, a->out_seq_stride}, {a->n_max, a->out_node_stride},
+                    {a->n_heads, a->out_head_stride}))
         return QW_INVALID_ARGUMENT;
     if (scratch_bytes < qw_tree_attention_scratch_bytes(kv, a->n_max, a->n_heads, a->max_len)) return QW_OUT_OF_MEMORY;
     return status_of(qw::launch_tree_attn(*kv, *a, scratch_dev, (cudaStream_t)cuda_stream));
