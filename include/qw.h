@@ -320,8 +320,7 @@ int qw_batch_tree_accept(qw_batch *b, int32_t seq, int32_t n, const int32_t *nod
  * pos * pos_stride elements; k and v share the strides.  format is an enum qw_kv_format; for
  * QW_KV_INT8_G32 k and v hold the codes, and k_scale and v_scale the fp16 scales [head_dim / 32]
  * of each row with strides of their own (else they are ignored).  Rows begin on 16-byte
- * boundaries (codes and scales too: 8 bytes for codes, head_dim / 16 bytes for scales are enough;
- * strides are multiples of that), or QW_ALIGNMENT.
+ * boundaries (those of scales on head_dim / 16 bytes) and strides are multiples of that, or QW_ALIGNMENT.
  * n_seq <= 65535, n_kv_heads <= 1024.  A cache that is written (qw_kv_append) has an address of its own
  * for every row: of the strides of dimensions longer than one, sorted, each one is at least what the ones
  * before it span; and k is not v.  The same holds for the rows of qw_kv_read and the out of
