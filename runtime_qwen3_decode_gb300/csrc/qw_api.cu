@@ -1057,12 +1057,15 @@ int qw_batch_tree_step(qw_batch *b, int32_t seq, int32_t n, const int32_t *token
     if (seq < 0 || seq >= b->max_batch || n < 1 || n > b->max_batch || !tokens_host || !parents_host)
         return QW_INVALID_ARGUMENT;
     const int len = b->len[seq];
-    int pos[qw::kBatchMax], row[qw::kBatchMax], depth[qw::kBatchMax];
+    // what the copies below read is this call's own: the caller's arrays may be pinned, and then a copy
+    // would read them some time after the call has returned
+    int tok[qw::kBatchMax], pos[qw::kBatchMax], row[qw::kBatchMax], depth[qw::kBatchMax];
     uint64_t mask[qw::kBatchMax];
     for (int i = 0; i < n; ++i) {
         const int p = parents_host[i], t = tokens_host[i];
         if (p < -1 || p >= i || t < (i == 0 ? -1 : 0) || t >= m->cfg.vocab) return QW_INVALID_ARGUMENT;
         if (t == -1 && !b->has_last[seq]) return QW_INVALID_ARGUMENT;
+        tok[i] = t;
         depth[i] = p < 0 ? 0 : depth[p] + 1;
         mask[i] = (1ull << i) | (p < 0 ? 0ull : mask[p]);
         pos[i] = len + depth[i];
@@ -1070,7 +1073,7 @@ int qw_batch_tree_step(qw_batch *b, int32_t seq, int32_t n, const int32_t *token
     }
     if ((int64_t)len + n > b->max_ctx) return QW_CONTEXT_EXCEEDED;
     b->tree_seq = -1;
-    int rc = cuda_status(cudaMemcpyAsync(b->tok_in, tokens_host, (size_t)n * 4, cudaMemcpyHostToDevice, m->stream));
+    int rc = cuda_status(cudaMemcpyAsync(b->tok_in, tok, (size_t)n * 4, cudaMemcpyHostToDevice, m->stream));
     if (!rc) rc = cuda_status(cudaMemcpyAsync(b->row_pos, pos, (size_t)n * 4, cudaMemcpyHostToDevice, m->stream));
     if (!rc) rc = cuda_status(cudaMemcpyAsync(b->cache_pos, row, (size_t)n * 4, cudaMemcpyHostToDevice, m->stream));
     if (!rc) rc = cuda_status(cudaMemcpyAsync(b->mask, mask, (size_t)n * 8, cudaMemcpyHostToDevice, m->stream));
