@@ -693,8 +693,8 @@ struct qw_batch {
     uint64_t *ones = nullptr, *mask = nullptr;        // [8] bit 0 alone; a tree's masks
     int *cache_pos = nullptr, *tree_len = nullptr;    // [8], [1]
     int32_t *tree_picks = nullptr;                    // [8] greedy picks of a tree's nodes
-    std::vector<int32_t> tree;           // parents of the tree that waits for qw_batch_tree_accept
-    int tree_seq = -1;                   // its sequence, -1: none
+    int32_t tree[qw::kBatchMax] = {};    // parents of the tree that waits for qw_batch_tree_accept
+    int tree_n = 0, tree_seq = -1;       // its nodes and its sequence, -1: none
     int32_t *tok_in = nullptr, *tok = nullptr, *picks = nullptr;
     int *row_pos = nullptr;
     unsigned long long *keys = nullptr;
@@ -994,7 +994,12 @@ int batch_launch(qw_batch *b, const qw::BatchStep &bs, int S, int tree) {
         const cudaError_t ie = cudaGraphInstantiate(&exec, graph, 0);
         cudaGraphDestroy(graph);
         if (ie != cudaSuccess) return cuda_status(ie);
-        b->graphs.push_back({bs.B, S, hid, tree, exec});
+        try {  // the callers are C entry points
+            b->graphs.push_back({bs.B, S, hid, tree, exec});
+        } catch (const std::bad_alloc &) {
+            cudaGraphExecDestroy(exec);
+            return QW_OUT_OF_MEMORY;
+        }
     }
     return cuda_status(cudaGraphLaunch(exec, m->stream));
 }
@@ -1099,7 +1104,8 @@ int qw_batch_tree_step(qw_batch *b, int32_t seq, int32_t n, const int32_t *token
     rc = batch_launch(b, bs, bs.max_len, 1 + seq);
     if (rc) return rc;
     b->last_n = n;
-    b->tree.assign(parents_host, parents_host + n);
+    for (int i = 0; i < n; ++i) b->tree[i] = parents_host[i];
+    b->tree_n = n;
     b->tree_seq = seq;
     if (!picks_host) return QW_OK;
     rc = cuda_status(cudaMemcpyAsync(picks_host, b->tree_picks, (size_t)n * 4, cudaMemcpyDeviceToHost, m->stream));
@@ -1109,11 +1115,11 @@ int qw_batch_tree_step(qw_batch *b, int32_t seq, int32_t n, const int32_t *token
 int qw_batch_tree_accept(qw_batch *b, int32_t seq, int32_t n, const int32_t *nodes_host) {
     if (!live_batch(b)) return QW_INVALID_HANDLE;
     if (b->failed) return b->failed;
-    if (seq < 0 || seq != b->tree_seq || n < 0 || n > (int)b->tree.size() || (n > 0 && !nodes_host))
+    if (seq < 0 || seq != b->tree_seq || n < 0 || n > b->tree_n || (n > 0 && !nodes_host))
         return QW_INVALID_ARGUMENT;
     for (int i = 0; i < n; ++i) {  // a path from a root: each node the child of the one before
         const int x = nodes_host[i];
-        if (x < 0 || x >= (int)b->tree.size() || b->tree[x] != (i ? nodes_host[i - 1] : -1)) return QW_INVALID_ARGUMENT;
+        if (x < 0 || x >= b->tree_n || b->tree[x] != (i ? nodes_host[i - 1] : -1)) return QW_INVALID_ARGUMENT;
     }
     qw_model *m = b->m;
     b->tree_seq = -1;
