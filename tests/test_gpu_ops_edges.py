@@ -64,6 +64,38 @@ def test_rows_on_16_byte_boundaries_and_no_larger_ones(qw, kind, dt, D, n):
             assert torch.equal(o[b], val.to(dt))
 
 
+@pytest.mark.parametrize("dt", [F32, F16, BF16])
+def test_edge_values_of_k_and_v_each_in_their_plane(qw, dt):
+    n, D = 9, 64
+    x = torch.zeros((2, 1, 1, n, D), device="cuda")              # K and V
+    ramp = torch.arange(32, device="cuda")
+    x[:, 0, 0, 0, :32] = ramp - 15.5                             # ties: amax 16.5, d = 16.5 / 127
+    x[:, 0, 0, 1, :32] = (ramp % 7 - 3.0) * 127                  # whole codes
+    x[:, 0, 0, 2, 5], x[:, 0, 0, 3, 6] = float("nan"), float("inf")
+    x[:, 0, 0, 4, 7] = 127 * 65504.0 * 1.01 if dt is not F16 else float("inf")  # the scale overflows fp16
+    x[:, 0, 0, 5, 8] = 1e-9                                      # the scale underflows to 0
+    x[:, 0, 0, 6, :32] = -0.0
+    x[:, 0, 0, 7, :32] = torch.linspace(-3e-5, 3e-5, 32)         # a subnormal scale
+    x[:, ..., 32:] = 1.0
+    x[1] *= -3                                                   # V's own values: a mixed-up plane shows
+    x[1, 0, 0, 8, :32] = 40 + ramp
+    x = x.to(dt)
+    k, v, ks, vs = make_cache("int8", (1, 1, n, D), gen(1))
+    view = qw.KvView(k, v, ks, vs)
+    qw.kv_append(view, x[0], x[1], i32(0))
+    out = [torch.empty_like(x[0]) for _ in range(2)]
+    qw.kv_read(view, *out, i32(0))
+    fin = [0, 1, 5, 6, 7, 8]
+    for rows, codes, scales, o in zip(x, (k, v), (ks, vs), out):
+        qc, qs = quantise(rows.float().cpu().numpy()[0, 0, fin])
+        np.testing.assert_array_equal(codes[0, 0, fin].cpu().numpy(), qc)
+        np.testing.assert_array_equal(scales[0, 0, fin].cpu().numpy(), qs)
+        val = torch.from_numpy(qc.astype(np.float32) * np.repeat(qs.astype(np.float32), 32, -1)).cuda().to(dt)
+        assert torch.equal(o[0, 0, fin], val)
+        assert torch.isnan(o[0, 0, 2:4, :32]).all() and not torch.isfinite(o[0, 0, 4, 7])
+        assert torch.equal(o[0, 0, 2:5, 32:], o[0, 0, :1, 32:].expand(3, 32))  # a bad group leaves its neighbour alone
+
+
 # ---------------------------------------------------------------- tree attention
 
 @pytest.mark.parametrize("dt,kind", [(F16, "int8"), (F16, "f32"), (F16, "bf16"), (BF16, "int8"), (BF16, "f32"), (BF16, "bf16")])
@@ -152,6 +184,80 @@ def test_bf16_queries_over_f32_rows_keep_their_range(qw, sk, sv, n, heads, max_l
     score = mag * (2.0 ** -16 + (D + 4) * 2.0 ** -24)
     tol = (2 * score + U[BF16] + 2.0 ** -16 + 2.0 ** -20 + (L + n) * 2.0 ** -24) * vmax
     assert ((got.double() - ref).abs() <= tol[..., None] + ref.abs() * U[BF16]).all()
+
+
+def rel(a, b):
+    return float((a.double() - b).norm() / b.norm())
+
+
+@pytest.mark.parametrize("dt,kind", [(F16, "int8"), (F16, "f32"), (F16, "bf16"), (BF16, "f32"), (BF16, "bf16")])
+@pytest.mark.parametrize("D,L", [(128, 900), (64, 2000)])
+def test_errors_are_those_of_the_weights_and_the_result(qw, dt, kind, D, L):
+    # Scores of tens, where one rounding of K to 16 bits would be most of the error.
+    n, H, G = 17, 2, 4
+    g = gen(60)
+    cache = make_cache(kind, (1, H, L + n, D), g)
+    q = (8 * torch.randn((1, n, H * G, D), generator=g, device="cuda")).to(dt)
+    mask = torch.from_numpy(qw.tree_mask(range(-1, n - 1)).view(np.int64)).cuda()[None]
+    got = qw.tree_attention(qw.KvView(*cache), q, mask, i32(L))
+    ref, _, _ = tree_reference(q, cache, mask, [L], [n], D ** -0.5)
+    # Independent roundings of a relative error of at most u are u / sqrt(3) or less in the mean square: the
+    # weights', the result's.  Two-term K: 2^-16 (bf16) of q k, whose mean square over the D terms, scaled, is
+    # 8 times K's rms of 1.2 or less; f32 sums of D terms, some 2^-19 of scores up to 100.
+    u = U[dt]
+    bound = u * (2 / 3) ** 0.5 + 10 * 2.0 ** -16 * (dt is BF16 and kind == "f32") + 100 * 2.0 ** -19
+    assert rel(got, ref) <= bound
+    if kind != "bf16":  # and the bound would not have let one-term operands pass
+        one = [widen(t, s).to(dt).double() for t, s in ((cache[0], cache[2]), (cache[1], cache[3]))]
+        far, _, _ = tree_reference(q, one + [None, None], mask, [L], [n], D ** -0.5)
+        assert rel(far, ref) > bound
+
+
+@pytest.mark.parametrize("dt,kind", [(F16, "int8"), (F16, "f32"), (BF16, "f32")])
+def test_values_that_nearly_cancel_keep_their_second_term(qw, dt, kind):
+    # every node sees two keys of equal weight whose values differ in sign and a few of their last bits
+    n, D = 16, 128
+    g = gen(61)
+    if kind == "f32":
+        v = torch.randn((1, 1, n, D), generator=g, device="cuda")
+        v[:, :, 1::2] = -v[:, :, ::2] * (1 + 2.0 ** -12 * torch.rand((1, 1, n // 2, D), generator=g, device="cuda"))
+        cache = [torch.randn_like(v), v, None, None]
+    else:
+        cache = make_cache("int8", (1, 1, n, D), g)
+        cache[1][:, :, 1::2] = -cache[1][:, :, ::2]
+        bits = cache[3].view(torch.int16)
+        bits[:, :, 1::2] = bits[:, :, ::2] + 1               # the next fp16 scale
+    q = torch.zeros((1, n, 2, D), dtype=dt, device="cuda")
+    mask = torch.tensor([[3 << (i // 2 * 2) for i in range(n)]], dtype=torch.int64, device="cuda")
+    got = qw.tree_attention(qw.KvView(*cache), q, mask, i32(0))
+    ref, _, vmax = tree_reference(q, cache, mask, [0], [n], 1.0)
+    # what two terms leave of V, and four f32 operations, of max|v|; the result's rounding
+    left = 2.0 ** -22 if dt is F16 else 2.0 ** -16
+    tol = (left + 4 * 2.0 ** -24) * vmax + ref.abs() * U[dt]
+    assert ((got.double() - ref).abs() <= tol).all()
+    one = [None, widen(cache[1], cache[3]).to(dt).double()]
+    far, _, _ = tree_reference(q, [cache[0] if kind == "f32" else widen(cache[0], cache[2]), one[1], None, None], mask, [0], [n], 1.0)
+    assert ((far - ref).abs() > tol).any()  # one-term values would not have passed
+
+
+@pytest.mark.parametrize("dt,kind", [(F32, "f32"), (F16, "int8"), (BF16, "int8"), (F16, "f32"), (BF16, "bf16")])
+def test_a_cache_that_is_only_read_may_overlap(qw, dt, kind):
+    # windows of one long row of positions, a few positions apart: sequences that share a prefix's end
+    B, L, n, D, step = 3, 100, 5, 64, 20
+    whole = make_cache(kind, (1, 1, (B - 1) * step + L + n, D), gen(62))
+    cut = [None if t is None else t.as_strided((B, 1, L + n, t.shape[-1]), (step * t.shape[-1], t.stride(1), t.shape[-1], 1))
+           for t in whole]
+    q = torch.randn((B, n, 8, D), generator=gen(63), device="cuda").to(dt)
+    mask = torch.full((B, n), 31, dtype=torch.int64, device="cuda")
+    got = qw.tree_attention(qw.KvView(*cut), q, mask, i32(L, L, 7))
+    want = qw.tree_attention(qw.KvView(*[None if t is None else t.contiguous() for t in cut]), q, mask, i32(L, L, 7))
+    assert torch.equal(got, want)
+    out = [torch.empty((B, 1, L + n, D), device="cuda") for _ in range(2)]
+    qw.kv_read(qw.KvView(*cut), *out, i32(0, 0, 0))
+    assert torch.equal(out[1], widen(cut[1], cut[3]).float())
+    with pytest.raises(qw.QwError) as e:
+        qw.kv_append(qw.KvView(*cut), *out, i32(0, 0, 0))
+    assert e.value.code == qw.INVALID_ARGUMENT
 
 
 # ---------------------------------------------------------------- logits

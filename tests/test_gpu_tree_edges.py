@@ -8,7 +8,8 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import qw_inputs as qi  # noqa: E402
-from test_gpu_tree import setup  # noqa: E402
+from _helpers import HIDDEN_REL_L2, check_position, rel_l2  # noqa: E402
+from test_gpu_tree import Q8_ROW, cache_tensors, path_of, setup, values  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +45,72 @@ def test_a_tree_step_is_done_with_the_callers_memory_when_it_returns(qw):
     assert torch.equal(b.logits(), want)
     b.close()
     m.close()
+
+
+LONG = 1300  # with the tiny model's 8 KV heads: past the calls that attend on the CUDA cores
+
+
+@pytest.mark.parametrize("kv", ["f32", "bf16"])
+def test_every_node_of_a_long_sequence_is_its_path(qw, kv):
+    """Against a batch that takes each node's path one decode step at a time (the attention of plain steps)."""
+    wl = qi.WORKLOADS["tiny"].with_(kv_format=kv)
+    host, m, b = setup(qw, wl, 8, LONG + 200)
+    one = qw.Batch(m, 1, LONG + 200)
+    g = np.random.default_rng(11)
+    done = [int(t) for t in g.integers(0, wl.vocab, size=LONG)]
+    b.prefill(3, done)
+    parents = [-1, 0, 1, 1, 0, 4, 5, -1]
+    for keep in ([0, 1, 3], [7]):
+        toks = [int(t) for t in g.integers(0, wl.vocab, size=8)]
+        picks = b.tree_step(3, toks, parents)
+        lg, hid = b.logits().cpu().numpy(), b.debug_hidden().cpu().numpy()
+        for i in (2, 3, 6, 7):
+            path = [toks[j] for j in path_of(parents, i)]
+            one.reset(0)
+            one.prefill(0, done)
+            for t in path:
+                last = one.step(1, [t])
+            check_position(lg[i], one.logits().cpu().numpy()[0], hid[:, i], one.debug_hidden().cpu().numpy()[:, 0],
+                           picks[i], last[0], what=f"node {i}", hidden_tol=HIDDEN_REL_L2 * (1 if kv == "f32" else 2))
+        b.tree_accept(3, keep)
+        done += [toks[j] for j in keep]
+        assert b.length(3) == len(done)
+    for o in (b, one, m):
+        o.close()
+
+
+@pytest.mark.parametrize("tree", [False, True])
+def test_a_long_8_bit_step_is_the_f32_step_over_the_values(qw, tree):
+    wl = qi.WORKLOADS["tiny"]
+    host, m, b8 = setup(qw, wl, 8, LONG + 200, 2)
+    bf = qw.Batch(m, 8, LONG + 200)
+    g = np.random.default_rng(12)
+    lens = [LONG, 3, 700, 1100]
+    for s, n in enumerate(lens):
+        p = g.integers(0, wl.vocab, size=n)
+        b8.prefill(s, p)
+        bf.prefill(s, p)
+    parents = [-1, 0, 0, 1, 3, 2, 5, -1]
+    for step in range(2):
+        k8, v8, ks, vs = cache_tensors(qw, b8)
+        kf, vf = cache_tensors(qw, bf)
+        kf.copy_(values(k8, ks))
+        vf.copy_(values(v8, vs))
+        n = 8 if tree else 4
+        toks = g.integers(0, wl.vocab, size=n)
+        for b in (b8, bf):
+            if tree:
+                b.tree_step(0, toks, parents)
+            else:
+                b.step(4, toks)
+        h8, hf = b8.debug_hidden().cpu().numpy(), bf.debug_hidden().cpu().numpy()
+        assert torch.isfinite(b8.logits()).all()
+        for i in range(n):
+            for l in range(wl.n_layers + 1):
+                assert rel_l2(h8[l, i], hf[l, i]) <= HIDDEN_REL_L2 + Q8_ROW, (step, i, l)
+        if tree:
+            for b in (b8, bf):
+                b.tree_accept(0, [0, 1, 3])
+                assert b.length(0) == LONG + 3 * (step + 1)
+    for o in (b8, bf, m):
+        o.close()
