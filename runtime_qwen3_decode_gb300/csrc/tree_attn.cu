@@ -309,18 +309,21 @@ int splits(int n_seq, int Hkv, int row_tiles, int rt, int total) {
 
 // Whether a call with 16-bit queries is better off on the CUDA cores: they need no set-up of barriers,
 // tensor memory and conversions, but time grows with every tile of 64 positions.  Measured, us,
-// CUDA cores against tensor cores, 8 KV heads of two query heads.  Two rows (one node): one sequence
-// over 64 8-bit positions 7 : 11, 8 sequences over 512 (576 tiles) 14 : 22, over 1024 (1088) 24 : 25; bf16
-// beside bf16 6 : 9, 13 : 17 and 21 : 18.  Eight rows: one sequence over 1024 8-bit positions
-// (136) 10 : 13, over 4096 (520) 25 : 21; bf16 10 : 12 and 23 : 15.  Sixteen rows, 8-bit: over 512 (72)
-// 12 : 13, over 2048 (264) 18 : 15; bf16 11 : 11 and 17 : 14.  f32 rows cost the conversion most and
-// the CUDA cores nothing: up to four rows always (8 sequences of one node over 4096: 65 : 89).
+// CUDA cores against tensor cores, 8 KV heads of two query heads of 128 dims.  Two rows (one node), fp16
+// queries: one sequence over 64 8-bit positions 7 : 11, 8 sequences over 512 (576 tiles) 14 : 23, over 1024 (1088)
+// 24 : 26; bf16 beside bf16 6 : 9, 13 : 17 and 21 : 18, but one sequence over 4096 (520) 17 : 14.  Eight rows:
+// one sequence over 1024 8-bit positions (136) 10 : 14, over 4096 (520) 25 : 21; bf16 10 : 12 and 23 : 14.  Sixteen
+// rows, 8-bit: over 512 (72) 12 : 14, over 2048 (264) 18 : 16; bf16 11 : 12 and 17 : 14.  f32 rows cost the
+// conversion most and the CUDA cores nothing: up to four rows always (8 sequences of one node over 4096:
+// 64 : 91), up to eight until 608 tiles (8 sequences of four nodes over 512, 576 tiles: 20 : 25; over 1024: 36 : 33).
+// bf16 queries over f32 rows measure as fp16 ones.
 bool small_call(const qw_kv_view &kv, const qw_tree_attention_args &t) {
     const int64_t tiles = (int64_t)kv.n_seq * kv.n_kv_heads * ((t.max_len + t.n_max + kTile - 1) / kTile);
     const int rows = t.n_max * (t.n_heads / kv.n_kv_heads);
     const bool direct = t.dtype == QW_DT_BF16 && kv.format == QW_KV_BF16;
-    if (rows <= 4) return kv.format == QW_KV_F32 || tiles <= 4 * 152;
-    if (rows <= 8) return tiles <= (direct ? 1 : 2) * 152;
+    const bool f32 = kv.format == QW_KV_F32;
+    if (rows <= 4) return f32 || tiles <= 4 * 152;
+    if (rows <= 8) return tiles <= (direct ? 1 : f32 ? 4 : 2) * 152;
     return rows <= 16 && !direct && tiles <= 152;
 }
 
