@@ -369,12 +369,13 @@ int qw_kv_read(const qw_kv_view *kv, const qw_kv_rows *rows, const int32_t *star
  * What a node does not see does not reach it, NaN and infinities included.  Rows i >= count[b]
  * of out are left as they were; if len[b] or count[b] does not fit the cache (len < 0,
  * len + count > max_ctx, count outside [0, n_max]), all n_max rows of the sequence are NaN.
- * max_len: about the longest len[], as the host knows it; it only sizes the split of the
- * positions (a longer sequence is right too, but slower).
+ * max_len: about the longest len[], as the host knows it; it sizes the split of the positions (a longer
+ * sequence is right too, but slower) and, with the other sizes and types, tells which calls are small.  Results of
+ * different max_len may so differ by their roundings, and where fp16 operands end (see below).
  * scratch: qw_tree_attention_scratch_bytes device bytes, 256-byte aligned, for this call alone
  * while it runs.
  * Arithmetic: f32 accumulation, sums and softmax statistics.  With f32 queries, and in small calls,
- * every product is f32.  Otherwise the products are those of 16-bit operands on the tensor cores:
+ * every product is f32.  Otherwise (16-bit queries) the products are those of 16-bit operands on the tensor cores:
  * softmax weights rounded to the operands' type (in fp16, weights below 2^-34 of the largest
  * count for nothing), K and V as follows.  bf16 queries over a bf16 cache:
  * bf16, as cached; over an f32 cache two bf16 terms (2^-16, f32's range); over 8-bit rows fp16, rounded
