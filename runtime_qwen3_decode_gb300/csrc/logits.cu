@@ -13,8 +13,8 @@
 // for each chunk the CTA keeps what falls in it in shared memory, as a dense count and a
 // dense bias per token, while the chunk's logits are on their way: the loads of the next
 // chunk are issued as soon as this one's values are out.  (One chunk per CTA spent most of
-// its time waiting in turn for the lists and for the logits: 256 x 151936 f32 took 91 us; now 74,
-// 4.2 TB/s, 62% of the measured copy rate.)
+// its time waiting in turn for the lists and for the logits: 256 x 151936 f32 took 91 us; now 75,
+// 4.1 TB/s, 61% of the measured copy rate.)
 // Counts are whole numbers, so the order of their atomics does not matter; the biases of a token that
 // is named more than once are added to its logit by the list's first entry alone, in order,
 // so results do not depend on timing.

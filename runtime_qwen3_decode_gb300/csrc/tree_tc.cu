@@ -29,7 +29,7 @@
 //
 // Measured (device time with the merge; HBM floor): 64 nodes over 32768 bf16 positions 37 us
 // (20): HBM while it streams, 5 us until the first tiles arrive, 8 us of last tile and merge.
-// 16 sequences of up to 33 nodes over 8-bit caches of up to 4096 57 us (14): the chain softmax,
+// 16 sequences of up to 33 nodes over 8-bit caches of up to 4096 58 us (14): the chain softmax,
 // product, next scores of each group, 2700 cycles a tile.  64 fp16 nodes over 32768 8-bit
 // positions 52 us (11); over f32 ones 97 us (40), bf16 nodes 96 us.
 //
