@@ -31,7 +31,7 @@
 // (20): HBM while it streams, 5 us until the first tiles arrive, 8 us of last tile and merge.
 // 16 sequences of up to 33 nodes over 8-bit caches of up to 4096 58 us (14): the chain softmax,
 // product, next scores of each group, 2700 cycles a tile.  64 fp16 nodes over 32768 8-bit
-// positions 52 us (11); over f32 ones 97 us (40), bf16 nodes 96 us.
+// positions 51 us (11); over f32 ones 98 us (40), bf16 nodes 96 us.
 //
 // What a row does not see has weight 0, but 0 x NaN is NaN in the product with V: the V
 // rows behind the sequence are zeroed, and elements of drafted rows that are not finite are
@@ -881,17 +881,28 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                             }
                         }
                     };
-                    if (check) all(std::true_type());
-                    else all(std::false_type());
-                    if constexpr (TERMS == 2) {
-                        if (over) {
+                    // A tile with such scales, element chunk by chunk.  It stands apart from the others' code: any check
+                    // between their conversion and finish() costs a call of one tile 0.5 of 15 us.
+                    auto careful = [&] {
 #pragma unroll 1
-                            for (int i = 0; i < 4 * U; ++i) {
-                                uint8_t *at = dst + swz128(row0 + RSTEP * (i >> 2), 4 * (g & 1) + (i & 3));
+                        for (int i = 0; i < 2 * U; ++i) {
+                            const int row = row0 + RSTEP * (i >> 1), pos = t * kTcTile + row, c = 4 * (g & 1) + 2 * (i & 1);
+                            const uint4 y = *reinterpret_cast<const uint4 *>(src + RSTEP * (i >> 1) * D + 16 * (i & 1));
+                            const __half2 sv = __half2half2(pos < s.total ? base_sc[(int64_t)pos * a.spos] : __half(0));
+#pragma unroll 1
+                            for (int k = 0; k < 2; ++k) {
+                                uint4 o, rest = make_uint4(0u, 0u, 0u, 0u);
+                                widen_q8<TERMS>(k ? y.z : y.x, k ? y.w : y.y, sv, o, rest);
+                                uint8_t *at = dst + swz128(row, c + k);
+                                if (check) any |= put(at, o, rest, std::true_type(), pos);
+                                else put(at, o, rest, std::false_type(), pos);
                                 drop_rest(at, at + C::kTerm);
                             }
                         }
-                    }
+                    };
+                    if (TERMS == 2 && over) careful();
+                    else if (check) all(std::true_type());
+                    else all(std::false_type());
                     finish(any, slot, &full[st]);
                 }
                 ++seg;
