@@ -440,6 +440,37 @@ typedef struct {
 } qw_process_logits_args;
 int qw_process_logits(const qw_process_logits_args *args, void *cuda_stream);
 
+/*
+ * The next token of many rows of logits [n_rows][vocab] (dtype QW_DT_F32, QW_DT_F16 or QW_DT_BF16, row stride in
+ * elements; not modified), drawn with given random numbers u[r] of [0, 1).  Of a row, tokens stand in order of
+ * falling logit x, ties by rising id; NaN and -inf are no candidates (+inf counts as the greatest finite
+ * number, -0 as 0).  With w_j = e^((x_j - x_1) / temperature[r]):
+ *   n_k = top_k[r] (<= 0, or no fewer than there are candidates: all of them), Z = w_1 + .. + w_(n_k);
+ *   n_p = the least j with w_1 + .. + w_j >= top_p[r] Z (1: n_k);
+ *   n_m = how many have w_j >= min_p[r] (0: all of them);
+ *   n = min(n_k, n_p, n_m), S = w_1 + .. + w_n;
+ *   tokens[r] = the first j with w_1 + .. + w_j > u[r] S, probs[r] = its w_j / S, kept[r] = n.
+ * Any top_k and the whole vocabulary: qw_sample_logits' order and steps, without its limit of
+ * QW_SAMPLE_MAX_TOP_K, and with the caller's numbers in the place of PCG32.  Temperature 0 takes the first
+ * token (probs 1, kept 1) whatever the others are.  Temperatures otherwise of [1e-6, 1e6], top_p of (0, 1],
+ * min_p of [0, 1], u of [0, 1): a row with another one, and a row without candidates, gets token -1, probs 0,
+ * kept 0.  The running sums are exact sums of weights right to about 3e-10, the same on every call.
+ * NULL: temperature 1, top_k 0, top_p 1, min_p 0; probs and kept may be NULL.  All parameters and results
+ * are device arrays [n_rows].  n_rows <= 65535, vocab <= 2^24.
+ */
+typedef struct {
+    const void *logits;
+    int32_t dtype, n_rows, vocab;
+    int64_t row_stride;
+    const float *u, *temperature;
+    const int32_t *top_k;
+    const float *top_p, *min_p;
+    int32_t *tokens;
+    float *probs;
+    int32_t *kept;
+} qw_sample_rows_args;
+int qw_sample_rows(const qw_sample_rows_args *args, void *cuda_stream);
+
 /* -------------------------------------------------------- checkpoint files */
 
 /*

@@ -1,5 +1,5 @@
 // ops_api.cu - argument checks of the operators on caller-owned buffers (qw_kv_append,
-// qw_kv_read, qw_tree_attention, qw_process_logits).  Everything is checked before a launch;
+// qw_kv_read, qw_tree_attention, qw_process_logits, qw_sample_rows).  Everything is checked before a launch;
 // nothing here touches the device.
 #include <algorithm>
 #include <cmath>
@@ -177,6 +177,18 @@ int qw_process_logits(const qw_process_logits_args *a, void *cuda_stream) {
     if (a->history && !a->history_range) return QW_INVALID_ARGUMENT;
     if ((a->bias || a->bias_ids) && !(a->bias && a->bias_ids && a->bias_range)) return QW_INVALID_ARGUMENT;
     return status_of(qw::launch_process_logits(*a, (cudaStream_t)cuda_stream));
+}
+
+int qw_sample_rows(const qw_sample_rows_args *a, void *cuda_stream) {
+    if (!a || !elem_bytes(a->dtype) || a->n_rows < 0 || a->vocab < 1 || a->vocab > (1 << 24)) return QW_INVALID_ARGUMENT;
+    if (a->n_rows == 0) return QW_OK;
+    if (!a->logits || !a->u || !a->tokens || a->row_stride < 0) return QW_INVALID_ARGUMENT;
+    if (a->n_rows > 65535) return QW_UNSUPPORTED_SHAPE;
+    if (!aligned(a->logits, elem_bytes(a->dtype))) return QW_ALIGNMENT;
+    for (const void *p : {(const void *)a->u, (const void *)a->temperature, (const void *)a->top_k, (const void *)a->top_p,
+                          (const void *)a->min_p, (const void *)a->tokens, (const void *)a->probs, (const void *)a->kept})
+        if (!aligned(p, 4)) return QW_ALIGNMENT;
+    return status_of(qw::launch_sample_rows(*a, (cudaStream_t)cuda_stream));
 }
 
 }  // extern "C"

@@ -30,6 +30,8 @@ cudaError_t launch_tree_attn(const qw_kv_view &kv, const qw_tree_attention_args 
 
 cudaError_t launch_process_logits(const qw_process_logits_args &a, cudaStream_t st);
 
+cudaError_t launch_sample_rows(const qw_sample_rows_args &a, cudaStream_t st);
+
 // Lets kernel K use `bytes` of dynamic shared memory on the current device; CUDA is asked once
 // per kernel and device, as the answer does not change and the call costs part of a microsecond.
 template <auto K>

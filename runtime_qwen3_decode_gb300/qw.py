@@ -61,7 +61,7 @@ EXPORTS = ("qw_workspace_bytes", "qw_model_create", "qw_prefill", "qw_decode_ste
            "qw_batch_logits", "qw_batch_debug_hidden", "qw_batch_sync", "qw_checkpoint_open",
            "qw_checkpoint_close", "qw_checkpoint_last_error", "qw_checkpoint_count", "qw_checkpoint_tensor",
            "qw_checkpoint_check", "qw_checkpoint_upload_bytes", "qw_checkpoint_upload", "qw_kv_append", "qw_kv_read",
-           "qw_tree_attention_scratch_bytes", "qw_tree_attention", "qw_process_logits", "qw_batch_workspace_bytes_kv",
+           "qw_tree_attention_scratch_bytes", "qw_tree_attention", "qw_process_logits", "qw_sample_rows", "qw_batch_workspace_bytes_kv",
            "qw_batch_create_kv", "qw_batch_tree_step", "qw_batch_tree_accept")
 DT_BF16, DT_F16, DT_F32, DT_I8, DT_Q8_0 = 0, 1, 2, 3, 4
 BATCH_MAX = 8
@@ -134,6 +134,14 @@ class ProcessLogitsArgs(ctypes.Structure):
                 ("path_len", ctypes.c_int32), ("bias_ids", ctypes.c_void_p), ("bias", ctypes.c_void_p),
                 ("bias_range", ctypes.c_void_p), ("n_bias", ctypes.c_int32), ("mask", ctypes.c_void_p),
                 ("mask_index", ctypes.c_void_p), ("n_masks", ctypes.c_int32)]
+
+
+class SampleRowsArgs(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("n_rows", ctypes.c_int32),
+                ("vocab", ctypes.c_int32), ("row_stride", ctypes.c_int64), ("u", ctypes.c_void_p),
+                ("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p),
+                ("min_p", ctypes.c_void_p), ("tokens", ctypes.c_void_p), ("probs", ctypes.c_void_p),
+                ("kept", ctypes.c_void_p)]
 
 
 class Weights(ctypes.Structure):
@@ -223,6 +231,7 @@ def _lib():
             L.qw_tree_attention_scratch_bytes.restype = ctypes.c_size_t
             L.qw_tree_attention.argtypes = [vp, vp, vp, ctypes.c_size_t, vp]
             L.qw_process_logits.argtypes = [vp, vp]
+            L.qw_sample_rows.argtypes = [vp, vp]
             L.qw_status_string.argtypes = [ctypes.c_int]
             L.qw_status_string.restype = ctypes.c_char_p
             L.qw_abi_version.argtypes = []
@@ -366,6 +375,7 @@ def sample_logits(logits, params: Sampling, rng, token_out, history=None, scratc
 _KV_ROWS = struct.Struct("@PPiiqqq")
 _TREE_ARGS = struct.Struct("@PPiiiif4xqqqqqqPPP")
 _LOGITS_ARGS = struct.Struct("@PPiii4xqqPPPi4xPi4xPPPi4xPPi4x")
+_SAMPLE_ARGS = struct.Struct("@PiiiqPPPPPPPP")
 _T = None  # torch, once one of these operators is used
 _DTYPES = {}
 
@@ -574,6 +584,33 @@ def process_logits(logits, out=None, *, history=None, history_range=None, path=N
         _want(mask, "mask", dev, i32, (n_masks, (V + 31) // 32)), _want(mask_index, "mask_index", dev, i32, (R,)), n_masks)
     _on(dev, stream, "qw_process_logits", _lib().qw_process_logits, args)
     return out
+
+
+def sample_rows(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, probs=None, kept=None,
+                stream=None):
+    """qw_sample_rows: the next token of every row of logits [n_rows, vocab] (float32, float16 or bfloat16, contiguous
+    rows), drawn with the given random numbers u float32 [n_rows] of [0, 1).  temperature, top_p, min_p
+    float32 [n_rows], top_k int32 [n_rows], on the device; None: 1, 1, 0, 0 (all tokens).  tokens int32
+    [n_rows] (None: a new tensor) receives the picks, probs float32 and kept int32 [n_rows], if given, each
+    one's probability among the kept tokens and their number.  Returns tokens."""
+    _use_torch()
+    shape, stride, dev = logits.shape, logits.stride(), logits.get_device()
+    if len(shape) != 2 or dev < 0 or (shape[1] > 1 and stride[1] != 1):
+        raise ValueError("logits must be CUDA [n_rows, vocab] with contiguous rows")
+    if u is None:
+        raise ValueError("u must be given")
+    i32, f32, per_row = _T.int32, _T.float32, (shape[0],)
+    if tokens is None:
+        with _T.cuda.stream(stream):  # what is allocated here belongs to the stream that uses it
+            tokens = _T.empty(per_row, dtype=i32, device=logits.device)
+    args = _SAMPLE_ARGS.pack(
+        logits.data_ptr(), _dtype_code(logits, "logits"), shape[0], shape[1], stride[0], _want(u, "u", dev, f32, per_row),
+        _want(temperature, "temperature", dev, f32, per_row), _want(top_k, "top_k", dev, i32, per_row),
+        _want(top_p, "top_p", dev, f32, per_row), _want(min_p, "min_p", dev, f32, per_row),
+        _want(tokens, "tokens", dev, i32, per_row), _want(probs, "probs", dev, f32, per_row),
+        _want(kept, "kept", dev, i32, per_row))
+    _on(dev, stream, "qw_sample_rows", _lib().qw_sample_rows, args)
+    return tokens
 
 
 class Model:
