@@ -454,7 +454,7 @@ int qw_process_logits(const qw_process_logits_args *args, void *cuda_stream);
  * QW_SAMPLE_MAX_TOP_K, and with the caller's numbers in the place of PCG32.  Temperature 0 takes the first
  * token (probs 1, kept 1) whatever the others are.  Temperatures otherwise of [1e-6, 1e6], top_p of (0, 1],
  * min_p of [0, 1], u of [0, 1): a row with another one, and a row without candidates, gets token -1, probs 0,
- * kept 0.  The running sums are exact sums of weights right to about 3e-10, the same on every call.
+ * kept 0.  The running sums are exact sums of weights right to 2.4e-9, the same on every call.
  * NULL: temperature 1, top_k 0, top_p 1, min_p 0; probs and kept may be NULL.  All parameters and results
  * are device arrays [n_rows].  n_rows <= 65535, vocab <= 2^24.
  */

@@ -10,16 +10,18 @@
 //
 // Nothing is sorted but the few tokens that stay in question.  A row belongs to the CTAs of one cluster,
 // each with a piece of it in shared memory:
-//   1. the greatest (logit, id) of the row;
-//   2. every token's weight, added up per octave below the greatest: how many tokens and how much weight
-//      each octave holds tells which of them the borders (top_k, top_p, min_p) fall in;
-//   3. the tokens down to that octave, if they are at most kList, are gathered in the first CTA, sorted and
-//      run through the definition.  Otherwise each border is looked for by itself: the octave's range of (logit, id)
-//      keys is cut in kBins parts, counted and weighed again until what is left fits the list.
+//   1. the greatest logit of the row;
+//   2. every token counted (and, where weights matter, weighed) by the octave of weight that it lies in below the greatest,
+//      the last of kBins parts taking the rest: that tells which of them the lowest border falls in;
+//   3. that part is cut in kBins again, by logits and at last by (logit, id) keys, until the tokens down to the border
+//      are at most kList: the first CTA gathers and sorts them and runs the definition on them.
+//   4. Where more tokens are kept, each border (top_k, top_p, the draw) is looked for by itself, and only the part
+//      that it falls in is sorted.
+// top_k needs counts alone: its passes weigh nothing.
 //
 // Weights are whole numbers, 2^wb for the weight 1 (wb >= 38, 44 at a vocabulary of 151,936), so that their
 // sums are exact: they do not depend on the order of addition, on the number of CTAs or on timing, and a
-// border that is met exactly is met.  A weight itself is off by about 3e-10 (weigh()): where it is decided by a
+// border that is met exactly is met.  A weight itself is off by 2.4e-9 at most (weigh()): where it is decided by a
 // running sum which token is drawn, f32 weights (6e-8, and 4e-7 from the product with 1 / T) would move a border
 // past a token of weight 1e-6 in every tenth row.
 #include <cooperative_groups.h>
@@ -27,6 +29,7 @@
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
+#include <type_traits>
 
 #include "qw_ops.h"
 
@@ -37,29 +40,32 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 16;
-constexpr int kList = 2048;
+constexpr int kBins = 8;
+constexpr int kKeys = 4;              // sorted keys of a thread
+constexpr int kList = kKeys * kThreads;  // tokens that are sorted at once, in one CTA
+constexpr int kMostShort = 1200;     // top_k up to which the short way is tried
+constexpr int kPart = kThreads;            // of a part that one border is looked for in, in every CTA
+constexpr int kShort = 512, kNear = 128; // a border's tokens are cut down to this many, or to this many about it
 constexpr int kMaxCluster = 8;
 constexpr int kCountBit = 52;     // of a thread's bin: its sum of weights below, its count above
-constexpr int kMantBits = 37;     // of a weight's mantissa
-constexpr int kSteps = 64;        // of the table of 2^(i / 64)
-static_assert(kWarps == kBins, "one warp adds up one bin");
+constexpr int kMantBits = 36;     // of a weight's mantissa behind its point
+constexpr int kSteps = 32;        // of the table of 2^(i / 32)
+static_assert(kWarps >= kBins, "one warp adds up one bin");
 
 using u64 = unsigned long long;
 
+// 2^(i / 32) in units of 2^-31, and in f32 in units of 2^-36: two words that each lie in a bank of their own for every i,
+// so that 32 lanes read them at once whatever their i (16-byte entries of 64 steps took 12 turns a read: 8.3 us instead of
+// XX a pass).
 struct Table {
-    u64 fix[kSteps];  // 2^(i / 64) in units of 2^-37
-};
-struct Step {
-    u64 fix;          // the same
-    float f;          // and in f32
-    unsigned pad;
+    unsigned fix[kSteps];
+    float f[kSteps];
 };
 
 struct SampleArgs {
     const void *logits;
     int64_t stride;
-    int V, per, id_bits, wb;      // per: tokens per CTA of the cluster
+    int V, per, id_bits, wb;      // per: tokens per CTA of the cluster, a multiple of 8
     const float *u, *temperature, *top_p, *min_p;
     const int32_t *top_k;
     int32_t *tokens, *kept;
@@ -76,8 +82,7 @@ __device__ __forceinline__ float ord_value(uint32_t e) {
 
 // NaN is -inf, -0 is +0, +inf the greatest finite number.
 __device__ __forceinline__ float canonical(float x) {
-    x = x == x ? fminf(x, FLT_MAX) : -INFINITY;
-    return x + 0.f;
+    return fminf(fmaxf(x, -INFINITY), FLT_MAX) + 0.f;
 }
 
 // What is the same for all tokens of a row.
@@ -89,45 +94,65 @@ struct Row {
     int wb;
 };
 
-constexpr float kMagic = 196608.f;  // 1.5 x 2^17: adding it rounds to multiples of 2^-6
+constexpr float kMagic = 393216.f;  // 1.5 x 2^18: adding it rounds to multiples of 2^-5
 
-// z = x log2(e) / T (far: (x - top) log2(e) / T) as q / 64 + r, |r| <= 1/128, r right to about 2^-31.  q does not fall as x rises.
-// Products and sums that must not be contracted are spelt out.
-__device__ __forceinline__ void split(const Row &w, float x, int &q, float &r) {
-    float p, e;
+// z = x log2(e) / T (far: (x - top) log2(e) / T) of two logits as q / 32 + r, |r| <= 1/64, r right to about 2^-31.  q does not
+// fall as x rises.  Products and sums that must not be contracted are spelt out; in pairs, as the passes are bound by the
+// number of their instructions.
+__device__ __forceinline__ void split2(const Row &w, float2 x, int (&q)[2], float2 &r) {
+    const float2 chi = make_float2(w.chi, w.chi), clo = make_float2(w.clo, w.clo), magic = make_float2(kMagic, kMagic);
+    const float2 minus = make_float2(-kMagic, -kMagic);
+    auto neg = [](float2 v) { return make_float2(-v.x, -v.y); };
+    float2 p, e;
     if (!w.far) {
-        p = __fmul_rn(x, w.chi);
-        e = __fmaf_rn(x, w.clo, __fmaf_rn(x, w.chi, -p));
+        p = __fmul2_rn(x, chi);
+        e = __ffma2_rn(x, clo, __ffma2_rn(x, chi, neg(p)));
     } else {
-        const float s = __fsub_rn(x, w.top), b = __fsub_rn(s, x);
-        const float rest = __fadd_rn(__fsub_rn(x, __fsub_rn(s, b)), __fsub_rn(-w.top, b));  // x - top = s + rest
-        p = fmaxf(__fmul_rn(s, w.chi), -4096.f);
-        e = __fmaf_rn(s, w.clo, __fmaf_rn(s, w.chi, -p));
-        e = p > -4096.f ? __fmaf_rn(rest, w.chi, e) : 0.f;
+        const float2 top = make_float2(-w.top, -w.top);
+        const float2 s = __fadd2_rn(x, top), b = __fadd2_rn(s, neg(x));
+        const float2 rest = __fadd2_rn(__fadd2_rn(x, neg(__fadd2_rn(s, neg(b)))), __fadd2_rn(top, neg(b)));  // x - top = s + rest
+        p = __fmul2_rn(s, chi);
+        p = make_float2(fmaxf(p.x, -4096.f), fmaxf(p.y, -4096.f));
+        e = __ffma2_rn(rest, chi, __ffma2_rn(s, clo, __ffma2_rn(s, chi, neg(p))));
+        e = make_float2(p.x > -4096.f ? e.x : 0.f, p.y > -4096.f ? e.y : 0.f);
     }
-    p = fmaxf(p, -65000.f);
-    const float t = __fadd_rn(p, kMagic);
-    q = __float_as_int(t) - __float_as_int(kMagic);
-    r = __fadd_rn(__fsub_rn(p, __fsub_rn(t, kMagic)), e);
+    p = make_float2(fmaxf(p.x, -65000.f), fmaxf(p.y, -65000.f));
+    const float2 t = __fadd2_rn(p, magic);
+    q[0] = __float_as_int(t.x) - __float_as_int(kMagic);
+    q[1] = __float_as_int(t.y) - __float_as_int(kMagic);
+    r = __fadd2_rn(__fadd2_rn(p, neg(__fadd2_rn(t, minus))), e);
 }
 
-// Octaves below the greatest weight, and the weight in units of 2^-wb: 2^(q / 64) from the table, times 2^r - 1 by
-// its series to r^3 (the rest is 4e-11), which is small (0.0055) and so right to 3e-10 in f32.
-__device__ __forceinline__ u64 weigh(const Row &w, const Step *step, float x, int &oct) {
-    int q;
-    float r;
-    split(w, x, q, r);
-    oct = w.oct - (q >> 6);
-    if (oct > 63) return 0ull;
-    const Step m = step[q & (kSteps - 1)];
-    const float up = r * fmaf(r, fmaf(r, 0.05550411f, 0.24022651f), 0.69314718f);   // ln2, ln2^2 / 2, ln2^3 / 6
-    const u64 mant = m.fix + (long long)__float2int_rn(m.f * up);
-    const u64 wide = mant << (w.wb - kMantBits - 1);
-    return oct ? (wide + (1ull << (oct - 1))) >> oct : wide;
+// Two weights in units of 2^-wb: 2^(q / 32) from the table, times 2^r - 1 by its series to r^4, which is small (0.011) and so
+// right to 2.4e-9 in f32: r to 2^-31, the series to 2^-31, the table's f32 and its product with the series to 2^-24 of 0.011
+// each; the table's whole number to 2^-32.  These errors do not add up over many tokens: they have either sign.
+__device__ __forceinline__ void weigh2(const Row &w, const Table &t, float2 x, u64 (&out)[2]) {
+    int q[2];
+    float2 r;
+    split2(w, x, q, r);
+    auto both = [](float v) { return make_float2(v, v); };
+    // ln2, ln2^2 / 2, ln2^3 / 6, ln2^4 / 24
+    const float2 up = __fmul2_rn(r, __ffma2_rn(r, __ffma2_rn(r, __ffma2_rn(r, both(0.0096181291f), both(0.055504109f)), both(0.24022651f)),
+                                               both(0.69314718f)));
+    const float2 part = __fmul2_rn(make_float2(t.f[q[0] & (kSteps - 1)], t.f[q[1] & (kSteps - 1)]), up);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        // in units of 2^-63, then shifted to 2^-(wb + 1) and rounded to 2^-wb; shr gives 0 for shifts of 64 and more
+        const u64 mant = ((u64)t.fix[q[k] & (kSteps - 1)] << 32) +
+                         (u64)((long long)__float2int_rn(k ? part.y : part.x) * (1ll << (63 - kMantBits)));
+        u64 half;
+        asm("shr.u64 %0, %1, %2;" : "=l"(half) : "l"(mant), "r"((unsigned)(62 - w.wb + w.oct - (q[k] >> 5))));
+        out[k] = (half + 1ull) >> 1;
+    }
+}
+__device__ __forceinline__ u64 weigh(const Row &w, const Table &t, float x) {
+    u64 v[2];
+    weigh2(w, t, make_float2(x, x), v);
+    return v[0];
 }
 
 __device__ __forceinline__ u64 key_of(float x, int id, int id_bits) {
-    return ((u64)ord_bits(x) << id_bits) | (((1ull << id_bits) - 1ull) - (u64)id);
+    return ((u64)ord_bits(x) << id_bits) | (u64)(((1u << id_bits) - 1u) & ~(unsigned)id);
 }
 
 __device__ __forceinline__ u64 shfl_xor64(u64 v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
@@ -138,167 +163,232 @@ __device__ __forceinline__ u64 times(float p, u64 Z, bool up) {
     return __umul64hi(f, Z) + (up && f * Z != 0ull ? 1ull : 0ull);
 }
 
+// Weight and number of some tokens; `low`: how many of them the CTAs before this one have.
 struct Total {
     u64 w;
-    unsigned n, pad;
-};
-
-// A token's key, and the number and weight of the tokens down to it.
-struct Border {
-    u64 key, w;
-    unsigned n, pad;
+    unsigned n, low;
 };
 
 struct Shared {
-    Step step[kSteps];
+    Table table;
     Total xch[2][kMaxCluster][kBins];   // a pass's bins of every CTA of the cluster
     Total total[kBins];                 // and their sums
     Total cum[kBins];                   // of the octaves: each with the ones above it
-    u64 best[kMaxCluster];              // greatest key of every CTA
-    u64 warp_best[kWarps];
-    u64 list[kList];
+    float top[kMaxCluster], least[kMaxCluster];  // greatest and least logit of every CTA
+    float group[kThreads];                       // greatest logits of kThreads parts of the row
+    unsigned count[kMaxCluster];                 // tokens in every CTA's part of the short list
+    int first_id[kMaxCluster];                   // temperature 0: its first token with the greatest logit
+    float warp_top[kWarps], warp_least[kWarps];
     u64 scan[kWarps];
-    unsigned listed;
-    int first[3];                       // places in the sorted list
-    Border found;                       // of a search
+    unsigned listed, edge[2];
+    int first[3];
     float cut;                          // the least logit that min_p keeps
+    float at;                           // the logit from which on tokens are listed
+};
+
+// In the place of the passes' bins: a list is written by other CTAs when this one has summed its bins, and read
+// before it clears them.  Two lists of parts in turn: a CTA that is ahead writes the next one.
+struct Parts {
+    u64 list[2][kPart], buf[2][kPart];
+};
+constexpr int kBinBytes = kBins * kThreads * 8;
+static_assert(sizeof(Parts) <= kBinBytes && kList * 8 <= kBinBytes, "fits over the bins");
+
+// How a pass cuts its tokens in kBins parts, the greatest first: by logit, top - x in units of 1 / inv (the last part takes
+// the rest), or by key, (key - lo) >> shift.
+struct Cut {
+    bool by_value;
+    float top, inv;
+    u64 lo;
+    int shift;
+    // the whole part of (top - x) inv, cut at kBins - 1, by adding 2^23 rounding down
+    __device__ __forceinline__ int slot(float x) const {
+        return __float_as_int(__fadd_rd(fminf((top - x) * inv, kBins - 1.f), 8388608.f)) & (kBins - 1);
+    }
+};
+
+// The keys [lo, end) in question, how many tokens they are, and what lies above them.
+struct Zone {
+    u64 lo, end;
+    Total above, inside;
 };
 
 template <typename T, bool RES>
 struct Piece {
     const T *src;         // the row
-    const float *kept;    // its piece in shared memory, canonical
+    const float *kept;    // its piece in shared memory, canonical, padded to a multiple of four with -inf
     int begin, end;       // tokens of this CTA
-    __device__ __forceinline__ float at(int i) const {
-        if constexpr (RES) return kept[i - begin];
-        else return canonical(elem_to_f(src[i]));
+    __device__ __forceinline__ int quads() const { return (end - begin + 3) >> 2; }
+    __device__ __forceinline__ float4 at(int quad) const {
+        if constexpr (RES) {
+            return reinterpret_cast<const float4 *>(kept)[quad];
+        } else {
+            float v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = begin + 4 * quad + k;
+                v[k] = i < end ? canonical(elem_to_f(src[i])) : -INFINITY;
+            }
+            return make_float4(v[0], v[1], v[2], v[3]);
+        }
     }
 };
 
-// One pass: every token that `bin` gives a bin in [0, kBins) is counted and weighed there; sh.total has the cluster's sums.
-template <typename P, typename F>
-__device__ void tally(const P &piece, Shared &sh, u64 *bins, cg::cluster_group &cl, int &turn, F bin) {
+// One pass: every token of the zone is counted in the part of it that the cut gives, and weighed if asked; sh.total has
+// the cluster's sums.  Each thread has bins of its own.  No branch but the one past four tokens outside: the others'
+// numbers are 0 and go to the last bin.  ROW: the zone has no upper end and is cut by logits.
+template <bool WEIGHED, bool ROW, typename P>
+__device__ __forceinline__ void tally(const P &piece, Shared &sh, const Row &row, u64 *bins, cg::cluster_group &cl, int turn,
+                                      const Zone &z, const Cut &c, int id_bits) {
+    const u64 id_mask = (1ull << id_bits) - 1ull;
+    const float xl = ord_value((unsigned)(z.lo >> id_bits)), xh = ord_value((unsigned)((z.end - 1ull) >> id_bits));
+    const int last = (int)(id_mask - (z.lo & id_mask)), first = (int)(id_mask - ((z.end - 1ull) & id_mask));
+    const bool ties = ((z.lo | z.end) & id_mask) != 0ull;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr u64 kSum = (1ull << kCountBit) - 1ull;
 #pragma unroll
     for (int b = 0; b < kBins; ++b) bins[b * kThreads + tid] = 0ull;
-    for (int i = piece.begin + tid; i < piece.end; i += kThreads) {
-        u64 w;
-        const int b = bin(piece.at(i), i, w);
-        if (b >= 0) bins[b * kThreads + tid] += (1ull << kCountBit) + w;
+    const int quads = piece.quads();
+    for (int g = tid; g < quads; g += kThreads) {
+        const float4 v = piece.at(g);
+        const float x[4] = {v.x, v.y, v.z, v.w};
+        int b[4];
+        bool is[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            is[k] = x[k] >= xl;
+            if constexpr (!ROW) is[k] &= x[k] <= xh;
+            b[k] = c.slot(x[k]);
+        }
+        if (ties) {  // an end of the zone is between tokens of one logit
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = piece.begin + 4 * g + k;
+                is[k] &= !((x[k] == xl) & (i > last)) & (ROW || !((x[k] == xh) & (i < first)));
+            }
+        }
+        if (!(is[0] | is[1] | is[2] | is[3])) continue;
+        if (!ROW && !c.by_value) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                b[k] = kBins - 1 - (int)((key_of(x[k], piece.begin + 4 * g + k, id_bits) - z.lo) >> c.shift);
+        }
+        u64 w[4] = {0ull, 0ull, 0ull, 0ull};
+        if constexpr (WEIGHED) {
+            u64 a[2], c[2];
+            weigh2(row, sh.table, make_float2(x[0], x[1]), a);
+            weigh2(row, sh.table, make_float2(x[2], x[3]), c);
+            w[0] = a[0], w[1] = a[1], w[2] = c[0], w[3] = c[1];
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            w[k] = is[k] ? w[k] + (1ull << kCountBit) : 0ull;
+            b[k] = is[k] ? b[k] : kBins - 1;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) bins[b[k] * kThreads + tid] += w[k];
     }
+    auto add = [&](u64 &w, unsigned &n) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            w += shfl_xor64(w, o);
+            n += __shfl_xor_sync(0xffffffffu, n, o);
+        }
+    };
     __syncthreads();
-    u64 w = 0;
-    unsigned n = 0;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) {
-        const u64 v = bins[warp * kThreads + lane + 32 * i];
-        w += v & ((1ull << kCountBit) - 1ull);
-        n += (unsigned)(v >> kCountBit);
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        w += shfl_xor64(w, o);
-        n += __shfl_xor_sync(0xffffffffu, n, o);
-    }
     const unsigned ctas = cl.num_blocks(), me = cl.block_rank();
-    if (lane < ctas) *cl.map_shared_rank(&sh.xch[turn][me][warp], lane) = Total{w, n, 0u};
+    if (warp < kBins) {
+        u64 w = 0;
+        unsigned n = 0;
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) {
+            const u64 v = bins[warp * kThreads + lane + 32 * i];
+            w += v & kSum;
+            n += (unsigned)(v >> kCountBit);
+        }
+        add(w, n);
+        if (lane < ctas) *cl.map_shared_rank(&sh.xch[turn][me][warp], lane) = Total{w, n, 0u};
+    }
     if (ctas > 1) cl.sync();
     else __syncthreads();
     if (tid < kBins) {
         Total t{0ull, 0u, 0u};
         for (unsigned c = 0; c < ctas; ++c) {
-            t.w += sh.xch[turn][c][tid].w;
-            t.n += sh.xch[turn][c][tid].n;
+            const Total &x = sh.xch[turn][c][tid];
+            t.w += x.w;
+            t.n += x.n;
+            if (c < me) t.low += x.n;
         }
         sh.total[tid] = t;
     }
-    turn ^= 1;  // a CTA that is ahead writes the other half
     __syncthreads();
 }
 
-// Descending bitonic sort of the list, n a power of two.
-__device__ void sort_list(u64 *k, int n) {
-    for (int size = 2; size <= n; size <<= 1)
+// The least order number of [low, high] for which slot() is at most j (high + 1: none).  One warp: the 32 places about where it
+// should be, which hold it but where logits lie close to 0; then by halves.
+__device__ unsigned edge_of(const Cut &c, int j, unsigned low, unsigned high) {
+    const unsigned lane = threadIdx.x & 31;
+    unsigned no = low, yes = high + 1u;  // below `no` it is not, from `yes` on it is
+    const unsigned guess = min(max(ord_bits(c.top - (float)(j + 1) / c.inv), low), high);
+    const unsigned from = guess - min(guess - low, 16u), o = from + lane;
+    const unsigned is = __ballot_sync(0xffffffffu, o <= high && c.slot(ord_value(o)) <= j);
+    const unsigned in = __ballot_sync(0xffffffffu, o <= high);
+    if (is) yes = from + __ffs(is) - 1;
+    if (in & ~is) no = from + 32 - __clz(in & ~is);
+    while (no < yes) {
+        const unsigned m = no + (yes - no) / 2;
+        if (c.slot(ord_value(m)) <= j) yes = m;
+        else no = m + 1u;
+    }
+    return yes;
+}
+
+// Descending bitonic sort of n keys, K neighbours per thread, exchanged in registers, between lanes by shuffles and
+// between warps through two buffers in turn.
+template <int K>
+__device__ __forceinline__ void sort_keys(u64 (&key)[K], u64 *buf, u64 *other_buf, int n) {
+    const int tid = threadIdx.x;
+    int pow2 = 32;
+    while (pow2 < n) pow2 <<= 1;
+    for (int size = 2; size <= pow2; size <<= 1)
         for (int stride = size >> 1; stride > 0; stride >>= 1) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < n / 2; i += kThreads) {
-                const int lo = 2 * i - (i & (stride - 1)), hi = lo + stride;
-                const u64 a = k[lo], b = k[hi];
-                if ((a < b) == ((lo & size) == 0)) {
-                    k[lo] = b;
-                    k[hi] = a;
+            if (stride < K) {
+#pragma unroll
+                for (int s = 1; s < K; s <<= 1) {
+                    if (s != stride) continue;
+#pragma unroll
+                    for (int k = 0; k < K; ++k) {
+                        if (k & s) continue;
+                        const bool down = ((K * tid + k) & size) == 0;
+                        const u64 hi = max(key[k], key[k | s]), lo = min(key[k], key[k | s]);
+                        key[k] = down ? hi : lo;
+                        key[k | s] = down ? lo : hi;
+                    }
+                }
+                continue;
+            }
+            const int far = stride / K;  // in threads
+            const bool greater = ((K * tid & size) == 0) == ((tid & far) == 0);
+            if (far >= 32) {
+#pragma unroll
+                for (int k = 0; k < K; ++k) buf[k * kThreads + tid] = key[k];
+                __syncthreads();
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const u64 other = buf[k * kThreads + (tid ^ far)];
+                    key[k] = greater ? max(key[k], other) : min(key[k], other);
+                }
+                u64 *t = buf;
+                buf = other_buf;
+                other_buf = t;
+            } else {
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const u64 other = shfl_xor64(key[k], far);
+                    key[k] = greater ? max(key[k], other) : min(key[k], other);
                 }
             }
         }
-    __syncthreads();
-}
-
-// The tokens that `take` names go to the first CTA's list (sh.listed of them, at most kList), where they are sorted, with the running
-// sums of their weights in cum, from `above` on.  False in the other CTAs.
-template <typename P, typename F>
-__device__ bool gather(const P &piece, Shared &sh, u64 *cum, cg::cluster_group &cl, const Row &row, int id_bits, u64 above, F take) {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const unsigned ctas = cl.num_blocks();
-    u64 *list = cl.map_shared_rank(sh.list, 0);
-    unsigned *listed = cl.map_shared_rank(&sh.listed, 0);
-    for (int i0 = piece.begin + 32 * warp; i0 < piece.end; i0 += kThreads) {
-        const int i = i0 + lane;
-        const float x = i < piece.end ? piece.at(i) : -INFINITY;
-        const bool mine = x > -INFINITY && take(x, i);
-        const unsigned who = __ballot_sync(0xffffffffu, mine);
-        if (!who) continue;
-        unsigned base = 0;
-        if (lane == 0) base = atomicAdd(listed, (unsigned)__popc(who));
-        base = __shfl_sync(0xffffffffu, base, 0) + __popc(who & ((1u << lane) - 1u));
-        if (mine && base < kList) list[base] = key_of(x, i, id_bits);
-    }
-    if (ctas > 1) cl.sync();
-    else __syncthreads();
-    if (cl.block_rank() != 0) return false;
-    const int n = min((int)sh.listed, kList);
-    int pow2 = 32;
-    while (pow2 < n) pow2 <<= 1;
-    for (int i = n + tid; i < pow2; i += kThreads) sh.list[i] = 0ull;
-    sort_list(sh.list, pow2);
-    // running sums: each thread takes a few neighbours
-    const int each = (n + kThreads - 1) / kThreads;
-    u64 mine[kList / kThreads], sum = 0;
-    int oct;
-    for (int j = 0; j < each; ++j) {
-        const int i = tid * each + j;
-        mine[j] = i < n ? weigh(row, sh.step, ord_value((uint32_t)(sh.list[i] >> id_bits)), oct) : 0ull;
-        sum += mine[j];
-    }
-    u64 upto = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const u64 v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
-    }
-    if (lane == 31) sh.scan[warp] = upto;
-    __syncthreads();
-    u64 run = above + upto - sum;
-    for (int k = 0; k < warp; ++k) run += sh.scan[k];
-    for (int j = 0; j < each; ++j) {
-        run += mine[j];
-        if (tid * each + j < n) cum[tid * each + j] = run;
-    }
-    __syncthreads();
-    return true;
-}
-
-// First place of the sorted list for which `is` holds, n if none does.
-template <typename F>
-__device__ int first_of(Shared &sh, int n, int slot, F is) {
-    if (threadIdx.x == 0) sh.first[slot] = n;
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kThreads)
-        if (is(i)) {
-            atomicMin(&sh.first[slot], i);
-            break;
-        }
-    __syncthreads();
-    return sh.first[slot];
 }
 
 // W / S, both up to 2^63, in f32
@@ -310,12 +400,12 @@ __device__ __forceinline__ float ratio(u64 W, u64 S) {
 }
 
 template <typename T, bool RES>
-__global__ void __launch_bounds__(kThreads) sample_rows_kernel(const __grid_constant__ SampleArgs a,
-                                                               const __grid_constant__ Table table) {
+__global__ void __launch_bounds__(kThreads, 2) sample_rows_kernel(const __grid_constant__ SampleArgs a,
+                                                                  const __grid_constant__ Table table) {
     extern __shared__ __align__(16) uint8_t smem_sample[];
     Shared &sh = *reinterpret_cast<Shared *>(smem_sample);
     u64 *bins = reinterpret_cast<u64 *>(smem_sample + (sizeof(Shared) + 15) / 16 * 16);
-    float *sx = reinterpret_cast<float *>(bins + kBins * kThreads);
+    float *sx = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(bins) + kBinBytes);
     cg::cluster_group cl = cg::this_cluster();
     const unsigned ctas = cl.num_blocks(), me = cl.block_rank();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -328,28 +418,26 @@ __global__ void __launch_bounds__(kThreads) sample_rows_kernel(const __grid_cons
     const bool greedy = T_ == 0.f;
     const bool valid = greedy || (T_ >= 1e-6f && T_ <= 1e6f && top_p > 0.f && top_p <= 1.f && min_p >= 0.f && min_p <= 1.f &&
                                   u >= 0.f && u < 1.f);
-    if (tid < kSteps) sh.step[tid] = Step{table.fix[tid], (float)table.fix[tid], 0u};
-    if (tid == 0) sh.listed = 0;
+    if (tid < kSteps) sh.table.fix[tid] = table.fix[tid], sh.table.f[tid] = table.f[tid];
 
-    // the row's piece, and its greatest key
+    // 1. the row's piece, its greatest and its least logit
     Piece<T, RES> piece;
     piece.src = reinterpret_cast<const T *>(a.logits) + (int64_t)r * a.stride;
     piece.begin = min(a.V, (int)me * a.per);
     piece.end = min(a.V, piece.begin + a.per);
     piece.kept = sx;
-    u64 best = 0;
+    float top = -INFINITY, least = INFINITY;
     {
         constexpr int E = 16 / sizeof(T);
         const T *p = piece.src + piece.begin;
         const int n = piece.end - piece.begin;
         const int head = min(n, (int)((16u - (unsigned)((uintptr_t)p & 15u)) & 15u) / (int)sizeof(T));
         const int vecs = (n - head) / E;
-        float mx = -INFINITY;
-        int at = 0;
         auto take = [&](int i, float v) {
             const float x = canonical(v);
             if constexpr (RES) sx[i] = x;
-            if (x > mx || (x == mx && i < at)) mx = x, at = i;
+            top = fmaxf(top, x);
+            least = x > -INFINITY ? fminf(least, x) : least;
         };
         const uint4 *pv = reinterpret_cast<const uint4 *>(p + head);
         constexpr int U = 4;
@@ -368,49 +456,84 @@ __global__ void __launch_bounds__(kThreads) sample_rows_kernel(const __grid_cons
         }
         for (int i = tid; i < head; i += kThreads) take(i, elem_to_f(p[i]));
         for (int i = head + vecs * E + tid; i < n; i += kThreads) take(i, elem_to_f(p[i]));
-        if (mx > -INFINITY) best = key_of(mx, piece.begin + at, a.id_bits);
+        if constexpr (RES)
+            if (tid < 3 && n + tid < (n + 3) / 4 * 4) sx[n + tid] = -INFINITY;
     }
+    float group = top;  // of `ctas` neighbouring threads: kThreads groups in the cluster
+    for (unsigned o = 1; o < ctas; o <<= 1) group = fmaxf(group, __shfl_xor_sync(0xffffffffu, group, o));
 #pragma unroll
-    for (int o = 16; o; o >>= 1) best = max(best, shfl_xor64(best, o));
-    if (lane == 0) sh.warp_best[warp] = best;
+    for (int o = 16; o; o >>= 1) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+    }
+    if (lane == 0) sh.warp_top[warp] = top, sh.warp_least[warp] = least;
     __syncthreads();
-    best = 0;
-    for (int k = 0; k < kWarps; ++k) best = max(best, sh.warp_best[k]);
+    for (int k = 0; k < kWarps; ++k) {
+        top = fmaxf(top, sh.warp_top[k]);
+        least = fminf(least, sh.warp_least[k]);
+    }
     if (ctas > 1) {
         asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA of the cluster is there
-        if (tid < ctas) *cl.map_shared_rank(&sh.best[me], tid) = best;
+        if (tid < ctas) {
+            *cl.map_shared_rank(&sh.top[me], tid) = top;
+            *cl.map_shared_rank(&sh.least[me], tid) = least;
+        }
+        *cl.map_shared_rank(&sh.group[me * (kThreads / ctas) + tid / ctas], tid % ctas) = group;
         cl.sync();
-        for (unsigned c = 0; c < ctas; ++c) best = max(best, sh.best[c]);
+        for (unsigned c = 0; c < ctas; ++c) {
+            top = fmaxf(top, sh.top[c]);
+            least = fminf(least, sh.least[c]);
+        }
     }
-    const u64 id_mask = (1ull << a.id_bits) - 1ull;
+    if (ctas == 1) sh.group[tid] = group;
     auto answer = [&](int token, float prob, int kept) {
         a.tokens[r] = token;
         if (a.probs) a.probs[r] = prob;
         if (a.kept) a.kept[r] = kept;
     };
-    if (!valid || best == 0 || greedy) {
+    if (!valid || top == -INFINITY) {
+        if (me == 0 && tid == 0) answer(-1, 0.f, 0);
+        return;
+    }
+    if (greedy) {  // the first token with the greatest logit
+        if (tid == 0) sh.edge[0] = a.V;
+        __syncthreads();
+        int id = a.V;
+        for (int g = tid; g < piece.quads(); g += kThreads) {
+            const float4 v = piece.at(g);
+            const int k = v.x == top ? 0 : v.y == top ? 1 : v.z == top ? 2 : v.w == top ? 3 : a.V;
+            id = min(id, piece.begin + 4 * g + k);
+            if (k < 4) break;
+        }
+        id = __reduce_min_sync(0xffffffffu, id);
+        if (lane == 0 && id < a.V) atomicMin(&sh.edge[0], (unsigned)id);
+        __syncthreads();
+        if (tid == 0) cl.map_shared_rank(sh.first_id, 0)[me] = (int)sh.edge[0];
+        if (ctas > 1) cl.sync();
+        else __syncthreads();
         if (me == 0 && tid == 0) {
-            if (!valid || best == 0) answer(-1, 0.f, 0);
-            else answer((int)(id_mask - (best & id_mask)), 1.f, 1);
+            for (unsigned c = 0; c < ctas; ++c) id = min(id, sh.first_id[c]);
+            answer(id, 1.f, 1);
         }
         return;
     }
 
+    const u64 id_mask = (1ull << a.id_bits) - 1ull;
     Row row;
-    row.top = ord_value((uint32_t)(best >> a.id_bits));
+    row.top = top;
     row.wb = a.wb;
     // log2(e) in two terms, divided by T in two terms
     row.chi = __fdiv_rn(1.44269502f, T_);
     row.clo = __fdiv_rn(__fadd_rn(__fmaf_rn(-row.chi, T_, 1.44269502f), 1.92596299e-8f), T_);
     row.far = !(fabsf(row.top * row.chi) < 60000.f);
     {
-        int q;
-        float f;
-        split(row, row.top, q, f);
-        row.oct = q >> 6;
+        int q[2];
+        float2 f;
+        split2(row, make_float2(row.top, row.top), q, f);
+        row.oct = q[0] >> 5;
     }
     // logits below this are less than min_p of the greatest
-    float cut = -INFINITY;
+    float cut = -FLT_MAX;
     if (min_p > 0.f) {
         if (tid == 0) {
             const double m = (double)row.top + (double)T_ * log((double)min_p);
@@ -419,163 +542,300 @@ __global__ void __launch_bounds__(kThreads) sample_rows_kernel(const __grid_cons
             sh.cut = f;
         }
         __syncthreads();
-        cut = sh.cut;
+        cut = fmaxf(cut, sh.cut);
     }
+    const bool has_p = top_p < 1.f;
+    // 2. octaves are no narrower than a few of the greatest logit's last places
+    Cut octaves{};
+    octaves.by_value = true;
+    octaves.top = row.top;
+    octaves.inv = 1.f / fmaxf(fmaxf(T_ * 0.69314718f, fabsf(row.top) * 1e-6f), 1e-30f);
+    // The whole row: the tokens with keys from `bottom` on.  Without top_p, what min_p leaves out counts for nothing else; with it
+    // the weights that it takes its part of do.
+    Zone rows{(u64)ord_bits(fmaxf(least, has_p ? -FLT_MAX : cut)) << a.id_bits, ((u64)ord_bits(row.top) + 1ull) << a.id_bits, {}, {}};
 
-    int turn = 0;
-    auto octave = [&](int oct) { return min(oct, kBins - 1); };
-    tally(piece, sh, bins, cl, turn, [&](float x, int, u64 &w) {
-        if (x == -INFINITY) return -1;
-        int oct;
-        w = weigh(row, sh.step, x, oct);
-        return octave(oct);
-    });
-    if (tid < kBins) {
-        Total t{0ull, 0u, 0u};
-        for (int b = 0; b <= tid; ++b) {
-            t.w += sh.total[b].w;
-            t.n += sh.total[b].n;
+    // 1b. A short way for top_k alone, and for min_p alone: the tokens from some logit on, listed at once.  For min_p that is
+    // `cut`; for top_k it is taken from the order of the greatest logits of kThreads parts of the row: if tokens are spread
+    // evenly, g of them leave a share of e^(-g / kThreads) of the parts without one.  Aimed at a few more than
+    // top_k; where there are fewer after all, or more than fit, the long way is taken.
+    const unsigned seg = kList / ctas;  // of the list, for each CTA
+    unsigned listed = 0;
+    const float floor = fmaxf(least, has_p ? -FLT_MAX : cut);
+    if ((top_k > 0 && top_k <= kMostShort) || (top_k <= 0 && !has_p && min_p > 0.f)) {
+        float from = floor;
+        if (top_k > 0) {
+            const float aim = (float)top_k + 3.f * sqrtf((float)top_k) + 8.f;
+            const int m = min(kThreads - 1, (int)((float)kThreads * (1.f - __expf(-aim / kThreads))));
+            // the m-th greatest: a descending sort, one per thread
+            float v = sh.group[tid];
+            for (int size = 2; size <= kThreads; size <<= 1)
+                for (int stride = size >> 1; stride > 0; stride >>= 1) {
+                    float o;
+                    if (stride >= 32) {
+                        __syncthreads();
+                        sh.group[tid] = v;
+                        __syncthreads();
+                        o = sh.group[tid ^ stride];
+                    } else {
+                        o = __shfl_xor_sync(0xffffffffu, v, stride);
+                    }
+                    v = ((tid & size) == 0) == ((tid & stride) == 0) ? fmaxf(v, o) : fminf(v, o);
+                }
+            if (tid == m) sh.at = v;
         }
-        sh.cum[tid] = t;
-    }
-    __syncthreads();
-    const Total whole = sh.cum[kBins - 1];
-    const bool has_k = top_k > 0 && (unsigned)top_k < whole.n, has_p = top_p < 1.f;
-    int oct_m = kBins - 1;  // octave of the least logit that min_p keeps
-    if (min_p > 0.f) {
-        int q;
-        float f;
-        split(row, cut, q, f);
-        oct_m = octave(row.oct - (q >> 6));
-    }
-    // the octave in which the count, or the weight, reaches a number
-    auto first_n = [&](unsigned n) {
-        int b = 0;
-        while (b < kBins - 1 && sh.cum[b].n < n) ++b;
-        return b;
-    };
-    auto first_w = [&](u64 w) {
-        int b = 0;
-        while (b < kBins - 1 && sh.cum[b].w < w) ++b;
-        return b;
-    };
-    // the last octave that can matter
-    int last = has_k ? first_n((unsigned)top_k) : kBins - 1;
-    if (has_p) {
-        if (!has_k) last = min(first_w(times(top_p, whole.w, true)), oct_m);
-    } else {
-        last = min(last, oct_m);
-    }
-
-    if (sh.cum[last].n <= kList) {
-        if (!gather(piece, sh, bins, cl, row, a.id_bits, 0ull, [&](float x, int) {
-                int q;
-                float f;
-                split(row, x, q, f);
-                return octave(row.oct - (q >> 6)) <= last;
-            }))
-            return;
-        const u64 *run = bins;
-        int n = (int)sh.listed;
-        u64 Z = whole.w;
-        if (has_k) {
-            n = min(n, top_k);
-            Z = run[n - 1];
-        }
-        if (has_p) {
-            const u64 goal = times(top_p, Z, true);
-            n = min(n, 1 + first_of(sh, n, 0, [&](int i) { return run[i] >= goal; }));
-        }
-        if (min_p > 0.f) n = first_of(sh, n, 1, [&](int i) { return ord_value((uint32_t)(sh.list[i] >> a.id_bits)) < cut; });
-        const u64 S = run[n - 1], goal = times(u, S, false) + 1ull;
-        const int j = min(n - 1, first_of(sh, n, 2, [&](int i) { return run[i] >= goal; }));
-        if (tid == 0) answer((int)(id_mask - (sh.list[j] & id_mask)), ratio(run[j] - (j ? run[j - 1] : 0ull), S), n);
-        return;
-    }
-
-    // Each border by itself: the token at which the count, or the weight, of those down to it reaches `goal`.
-    auto search = [&](bool by_count, u64 goal) {
-        const int oct = by_count ? first_n((unsigned)goal) : first_w(goal);
-        Total above = oct ? sh.cum[oct - 1] : Total{0ull, 0u, 0u};
-        unsigned inside = sh.cum[oct].n - above.n;
-        // the octave's keys [lo, end), with room for the roundings of its ends
-        u64 lo, end;
-        {
-            const float base = row.far ? row.top : 0.f;
-            auto edge = [&](int q) { return base + (float)q * (1.f / kSteps) / row.chi; };
-            float hi = edge((row.oct - oct + 1) * kSteps + 1), low = edge((row.oct - oct) * kSteps - 1);
-            hi += (fabsf(hi) + fabsf(base)) * 1e-6f;
-            low -= (fabsf(low) + fabsf(base)) * 1e-6f;
-            if (!(hi < row.top)) hi = row.top;
-            if (oct == kBins - 1 || !(low > -FLT_MAX)) low = -FLT_MAX;
-            lo = (u64)ord_bits(canonical(low)) << a.id_bits;
-            end = ((u64)ord_bits(canonical(hi)) + 1ull) << a.id_bits;
-        }
-        auto in_range = [&](float x, int i, u64 &key) {
-            int q;
-            float f;
-            split(row, x, q, f);
-            key = key_of(x, i, a.id_bits);
-            return octave(row.oct - (q >> 6)) == oct && key >= lo && key < end;
-        };
-        while (inside > kList) {  // shorter by four bits each time; a single key is one token
-            int shift = 0;
-            while ((end - lo - 1ull) >> shift >= (u64)kBins) ++shift;
-            tally(piece, sh, bins, cl, turn, [&](float x, int i, u64 &w) {
-                u64 key;
-                if (x == -INFINITY || !in_range(x, i, key)) return -1;
-                int o;
-                w = weigh(row, sh.step, x, o);
-                return kBins - 1 - (int)((key - lo) >> shift);  // the greatest keys first
-            });
-            int b = 0;
-            for (; b < kBins - 1; ++b) {
-                const Total t = sh.total[b];
-                if ((by_count ? (u64)(above.n + t.n) : above.w + t.w) >= goal) break;
-                above.w += t.w;
-                above.n += t.n;
+        if (tid == 0) sh.listed = 0;
+        __syncthreads();
+        if (top_k > 0) from = fmaxf(from, sh.at);
+        u64 *list = cl.map_shared_rank(bins, 0) + me * seg;
+        const int quads = piece.quads();
+        for (int g = tid; g < quads; g += kThreads) {
+            const float4 v = piece.at(g);
+            if (!(fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) >= from)) continue;
+            const float x[4] = {v.x, v.y, v.z, v.w};
+            for (int k = 0; k < 4; ++k) {
+                if (!(x[k] >= from)) continue;
+                const unsigned at = atomicAdd(&sh.listed, 1u);
+                if (at < seg) list[at] = key_of(x[k], piece.begin + 4 * g + k, a.id_bits);
             }
-            inside = sh.total[b].n;
-            lo += (u64)(kBins - 1 - b) << shift;
-            end = min(end, lo + (1ull << shift));
-            __syncthreads();
         }
-        if (gather(piece, sh, bins, cl, row, a.id_bits, above.w, [&](float x, int i) {
-                u64 key;
-                return in_range(x, i, key);
-            })) {
-            const int n = (int)sh.listed;
-            int j = by_count ? (int)(goal - above.n) - 1 : first_of(sh, n, 0, [&](int i) { return bins[i] >= goal; });
-            j = max(0, min(j, n - 1));
-            if (tid < ctas) *cl.map_shared_rank(&sh.found, tid) = Border{sh.list[j], bins[j], above.n + (unsigned)j + 1u, 0u};
-            __syncthreads();
-            if (tid == 0) sh.listed = 0;
+        __syncthreads();
+        if (tid < ctas) cl.map_shared_rank(sh.count, tid)[me] = sh.listed;
+        if (ctas > 1) cl.sync();
+        else __syncthreads();
+        bool fit = true;
+        for (unsigned i = 0; i < ctas; ++i) {
+            listed += sh.count[i];
+            fit &= sh.count[i] <= seg;
+        }
+        if (!fit || (listed < (unsigned)max(top_k, 0) && from > floor)) listed = 0;
+    }
+
+    // The row's way through passes and lists, in one loop so that each of them stands in the code once.
+    // stage 0: top_k, by counts.  1: top_p, by weights.  2: the draw.  `seek`: a border is looked for, at which the count or the
+    // weight of the tokens down to it reaches goal.
+    int stage = top_k > 0 ? 0 : 1, side = 0, turn = 0;
+    enum { kOctaves, kNarrow, kMinP, kNone } pass = kOctaves;
+    bool seek = false, from_octaves = true;
+    u64 goal = 0;
+    Total whole{}, kept{};
+    Zone z = rows;
+    Cut c = octaves;
+    for (;;) {
+        bool all = listed != 0;
+        u64 *list = bins;
+        unsigned room = kList;
+        int n = (int)listed;
+        if (all) {  // by the short way
+            seek = (unsigned)top_k < listed && top_k > 0;
+            whole.n = listed;
+        } else {
+        if (pass != kNone) {
+            if (pass != kNarrow) {
+                if (stage == 0) tally<false, true>(piece, sh, row, bins, cl, turn, z, c, a.id_bits);
+                else tally<true, true>(piece, sh, row, bins, cl, turn, z, c, a.id_bits);
+            } else {
+                if (stage == 0) tally<false, false>(piece, sh, row, bins, cl, turn, z, c, a.id_bits);
+                else tally<true, false>(piece, sh, row, bins, cl, turn, z, c, a.id_bits);
+            }
+            turn ^= 1;  // a CTA that is ahead writes the other half
+            if (pass == kOctaves) {
+                if (tid < kBins) {
+                    Total t{0ull, 0u, 0u};
+                    for (int b = 0; b <= tid; ++b) {
+                        t.w += sh.total[b].w;
+                        t.n += sh.total[b].n;
+                        t.low += sh.total[b].low;
+                    }
+                    sh.cum[tid] = t;
+                }
+                __syncthreads();
+                whole = kept = rows.inside = sh.cum[kBins - 1];
+                seek = stage == 0 ? (unsigned)top_k < whole.n : has_p;
+                goal = stage == 0 ? (u64)top_k : max(1ull, times(top_p, whole.w, true));
+                z = rows;
+            } else if (pass == kMinP) {
+                kept = Total{0ull, 0u, 0u};
+                for (int b = 0; b < kBins; ++b) kept.w += sh.total[b].w, kept.n += sh.total[b].n;
+                stage = 2;
+            }
+            from_octaves = pass != kNarrow;
+        }
+        if (stage == 2 && pass != kNarrow) {
+            seek = from_octaves = true;
+            goal = times(u, kept.w, false) + 1ull;
+            z = rows;
+        }
+        if (seek) {  // into the part in which the border is
+            const Total *total = from_octaves ? sh.cum : sh.total;
+            if (from_octaves) c = octaves;
+            Total t{0ull, 0u, 0u}, before{0ull, 0u, 0u};
+            int b = 0;
+            for (;; ++b) {
+                const Total x = total[b];
+                t = from_octaves ? x : Total{before.w + x.w, before.n + x.n, before.low + x.low};
+                if (b == kBins - 1 || (stage == 0 ? (u64)(z.above.n + t.n) : z.above.w + t.w) >= goal) break;
+                before = t;
+            }
+            z.inside = Total{t.w - before.w, t.n - before.n, t.low - before.low};
+            z.above = Total{z.above.w + before.w, z.above.n + before.n, z.above.low + before.low};
+            if (c.by_value) {
+                const unsigned low = (unsigned)(z.lo >> a.id_bits), high = (unsigned)((z.end - 1ull) >> a.id_bits);
+                if (warp < 2 && (warp ? b < kBins - 1 : b > 0)) {
+                    const unsigned e = edge_of(c, b - 1 + warp, low, high);
+                    if (lane == 0) sh.edge[warp] = e;
+                }
+                __syncthreads();
+                if (b > 0) z.end = min(z.end, (u64)sh.edge[0] << a.id_bits);
+                if (b < kBins - 1) z.lo = max(z.lo, (u64)sh.edge[1] << a.id_bits);
+            } else {
+                z.lo += (u64)(kBins - 1 - b) << c.shift;
+                z.end = min(z.end, z.lo + (1ull << c.shift));
+            }
+            __syncthreads();  // sh.edge and sh.total are read
+        }
+
+        // 3. the tokens down to the border, if they are few; 4. else the part about it
+        const unsigned down = z.above.n + z.inside.n;
+        const bool cut_more = seek && (stage < 2 && z.above.n < 3u * kList / 4 ? down > (unsigned)kShort && z.inside.n > (unsigned)kNear
+                                                                              : z.inside.n > (unsigned)kPart);
+        all = !cut_more && stage < 2 && down <= (unsigned)kList;
+        if (cut_more) {
+            // in parts of equal spans of logits while they have places enough between them, then of keys
+            const unsigned low = (unsigned)(z.lo >> a.id_bits), high = (unsigned)((z.end - 1ull) >> a.id_bits);
+            const float xl = ord_value(low), xh = ord_value(high), width = xh * (1.f / kBins) - xl * (1.f / kBins);
+            c.by_value = high - low > 64u && width > fmaxf(fmaxf(fabsf(xl), fabsf(xh)) * 1e-6f, 1e-30f);
+            c.top = xh;
+            c.inv = 1.f / width;
+            c.shift = 0;
+            while ((z.end - z.lo - 1ull) >> c.shift >= (u64)kBins) ++c.shift;
+            pass = kNarrow;
+            continue;
+        }
+        if (!all && !seek) {  // nothing is left out
+            stage = stage + 1;
+            pass = stage == 1 ? kOctaves : kNone;
+            z = rows, c = octaves;
+            continue;
+        }
+
+        // A list: the tokens of the zone (all: and the ones above it) to the first CTA, or to every one.
+        if (!all) list = reinterpret_cast<Parts *>(bins)->list[side], room = kPart;
+        side ^= 1;
+        if (tid == 0) sh.listed = z.inside.low + (all ? z.above.low : 0u);
+        __syncthreads();
+        {
+            const float xl = ord_value((unsigned)(z.lo >> a.id_bits)),
+                        xh = all ? row.top : ord_value((unsigned)((z.end - 1ull) >> a.id_bits));
+            const int quads = piece.quads();
+            for (int g = tid; g < quads; g += kThreads) {
+                const float4 v = piece.at(g);
+                const float x[4] = {v.x, v.y, v.z, v.w};
+                if (!(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= xl)) continue;
+                for (int k = 0; k < 4; ++k) {
+                    if (!(x[k] >= xl && x[k] <= xh)) continue;
+                    const u64 key = key_of(x[k], piece.begin + 4 * g + k, a.id_bits);
+                    if (key < z.lo || (!all && key >= z.end)) continue;
+                    const unsigned at = atomicAdd(&sh.listed, 1u);
+                    if (at >= room) continue;
+                    for (unsigned to = 0; to < (all ? 1u : ctas); ++to) cl.map_shared_rank(list, to)[at] = key;
+                }
+            }
         }
         if (ctas > 1) cl.sync();
         else __syncthreads();
-        const Border f = sh.found;
+        n = (int)min(room, z.inside.n + (all ? z.above.n : 0u));
+        }
+        if (all && me != 0) return;
+        auto entry = [&](unsigned i) {  // of the list, which the short way leaves in parts
+            if (listed == 0) return list[i];
+            unsigned part = 0;
+            while (i >= sh.count[part]) i -= sh.count[part++];
+            return list[part * seg + i];
+        };
+        // sorted, with the running sums of their weights; the first CTA is done with its piece of the row
+        u64 *runs = all ? reinterpret_cast<u64 *>(sx) : reinterpret_cast<Parts *>(bins)->buf[0];
+        u64 *keys = all ? runs + kList : reinterpret_cast<Parts *>(bins)->buf[1];
+        if (tid < 3) sh.first[tid] = kList;
+        auto order = [&](auto per) {
+            constexpr int K = decltype(per)::value;
+            u64 key[K], run[K];
+#pragma unroll
+            for (int k = 0; k < K; ++k) key[k] = K * tid + k < n ? entry(K * tid + k) : 0ull;
+            sort_keys(key, runs, keys, n);
+            u64 sum = 0;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                if (K * tid + k < n) sum += weigh(row, sh.table, ord_value((uint32_t)(key[k] >> a.id_bits)));
+                run[k] = sum;
+            }
+            u64 upto = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const u64 v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            if (lane == 31) sh.scan[warp] = upto;
+            __syncthreads();
+            upto += (all ? 0ull : z.above.w) - sum;
+            for (int k = 0; k < warp; ++k) upto += sh.scan[k];
+#pragma unroll
+            for (int k = 0; k < K; ++k) keys[K * tid + k] = key[k], runs[K * tid + k] = run[k] + upto;
+        };
+        if (n <= kThreads) order(std::integral_constant<int, 1>());
+        else order(std::integral_constant<int, kKeys>());
         __syncthreads();
-        return f;
-    };
-    Border kept{0ull, whole.w, whole.n, 0u};
-    if (has_k) kept = search(true, (u64)top_k);
-    if (has_p) kept = search(false, max(1ull, times(top_p, kept.w, true)));
-    if (min_p > 0.f) {
-        tally(piece, sh, bins, cl, turn, [&](float x, int i, u64 &w) {
-            if (x == -INFINITY || x < cut || key_of(x, i, a.id_bits) < kept.key) return -1;
-            int o;
-            w = weigh(row, sh.step, x, o);
-            return 0;
-        });
-        kept.w = sh.total[0].w;
-        kept.n = sh.total[0].n;
+        // first place for which something holds that holds from there on, n if none
+        auto first_of = [&](int slot, auto holds) {
+            int at = n;
+            for (int i = tid; i < n; i += kThreads)
+                if (holds(i)) {
+                    at = i;
+                    break;
+                }
+            at = __reduce_min_sync(0xffffffffu, at);
+            if (lane == 0 && at < n) atomicMin(&sh.first[slot], at);
+            __syncthreads();
+            return min(n, sh.first[slot]);
+        };
+        if (all) {
+            u64 Z = whole.w;
+            const bool has_k = stage == 0 && seek;
+            if (has_k || (unsigned)n == whole.n) {
+                if (has_k) n = min(n, top_k);
+                Z = runs[n - 1];
+            }
+            if (has_p) {
+                const u64 at_p = times(top_p, Z, true);
+                n = min(n, 1 + first_of(0, [&](int i) { return runs[i] >= at_p; }));
+                if (min_p > 0.f) n = first_of(1, [&](int i) { return ord_value((uint32_t)(keys[i] >> a.id_bits)) < cut; });
+            }
+            const u64 S = runs[n - 1], at_u = times(u, S, false) + 1ull;
+            const int j = min(n - 1, first_of(2, [&](int i) { return runs[i] >= at_u; }));
+            if (tid == 0) answer((int)(id_mask - (keys[j] & id_mask)), ratio(j ? runs[j] - runs[j - 1] : runs[0], S), n);
+            return;
+        }
+        int j = stage == 0 ? (int)(goal - z.above.n) - 1 : first_of(0, [&](int i) { return runs[i] >= goal; });
+        j = max(0, min(j, n - 1));
+        const u64 at = keys[j], weight = j ? runs[j] - runs[j - 1] : runs[0] - z.above.w;
+        const Total to_it{runs[j], z.above.n + (unsigned)j + 1u, 0u};
         __syncthreads();
-    }
-    const Border drawn = search(false, times(u, kept.w, false) + 1ull);
-    if (me == 0 && tid == 0) {
-        int o;
-        const u64 w = weigh(row, sh.step, ord_value((uint32_t)(drawn.key >> a.id_bits)), o);
-        answer((int)(id_mask - (drawn.key & id_mask)), ratio(w, kept.w), (int)kept.n);
+        if (stage == 2) {
+            if (me == 0 && tid == 0) answer((int)(id_mask - (at & id_mask)), ratio(weight, kept.w), (int)kept.n);
+            return;
+        }
+        if (stage == 0) {  // the tokens below top_k count for nothing from here on
+            stage = 1;
+            rows.lo = at;
+            pass = kOctaves;
+        } else if (min_p > 0.f) {
+            pass = kMinP;
+        } else {
+            stage = 2;
+            kept = to_it;
+            pass = kNone;
+        }
+        z = rows, c = octaves;
+        if (pass == kMinP) z.lo = max(at, (u64)ord_bits(cut) << a.id_bits);
     }
 }
 
@@ -600,7 +860,11 @@ cudaError_t launch_rows(const SampleArgs &a, const Table &t, int rows, int ctas,
 const Table &table() {
     static const Table t = [] {
         Table x;
-        for (int i = 0; i < kSteps; ++i) x.fix[i] = (u64)std::llround(std::ldexp(std::exp2((double)i / kSteps), kMantBits));
+        for (int i = 0; i < kSteps; ++i) {
+            const double v = std::exp2((double)i / kSteps);
+            x.fix[i] = (unsigned)std::llround(std::ldexp(v, 31));
+            x.f[i] = (float)std::ldexp(v, kMantBits);
+        }
         return x;
     }();
     return t;
@@ -615,7 +879,7 @@ int bits_for(int64_t n) {  // least b with n <= 2^b
 }  // namespace
 
 cudaError_t launch_sample_rows(const qw_sample_rows_args &q, cudaStream_t st) {
-    const size_t fixed = (sizeof(Shared) + 15) / 16 * 16 + (size_t)kBins * kThreads * 8;
+    const size_t fixed = (sizeof(Shared) + 15) / 16 * 16 + kBinBytes;
     const size_t room = 227 * 1024 - fixed;
     int ctas = 1;
     auto per = [&] { return (int)(((int64_t)q.vocab + ctas - 1) / ctas + 7) / 8 * 8; };
@@ -626,11 +890,11 @@ cudaError_t launch_sample_rows(const qw_sample_rows_args &q, cudaStream_t st) {
     a.V = q.vocab;
     a.per = per();
     a.id_bits = bits_for(q.vocab);
-    a.wb = std::min(62 - a.id_bits, kCountBit - 1 - bits_for((a.per + kThreads - 1) / kThreads));
+    a.wb = std::min(62 - a.id_bits, kCountBit - 1 - bits_for((a.per + 4 * kThreads - 1) / (4 * kThreads) * 4));  // a thread's tokens fit its bins
     a.u = q.u, a.temperature = q.temperature, a.top_p = q.top_p, a.min_p = q.min_p, a.top_k = q.top_k;
     a.tokens = q.tokens, a.kept = q.kept, a.probs = q.probs;
     const bool res = (size_t)a.per * 4 <= room;
-    const size_t smem = fixed + (res ? (size_t)a.per * 4 : 0);
+    const size_t smem = fixed + std::max<size_t>(res ? (size_t)a.per * 4 : 0, (size_t)kList * 16);  // define() sorts where the row was
     const Table &t = table();
     if (q.dtype == QW_DT_F32) return res ? launch_rows<float, true>(a, t, q.n_rows, ctas, smem, st) : launch_rows<float, false>(a, t, q.n_rows, ctas, smem, st);
     if (q.dtype == QW_DT_F16) return res ? launch_rows<__half, true>(a, t, q.n_rows, ctas, smem, st) : launch_rows<__half, false>(a, t, q.n_rows, ctas, smem, st);

@@ -1,9 +1,10 @@
 """The draw of many rows' next tokens (qw_sample_rows) against its definition in 64 bits.
 
 Whole numbers (token, how many were kept) have to be those of the definition unless the border that decides
-them lies within the weights' error of a running sum: a weight is off by 4e-10 of itself at most (an f32 series of
-magnitude 0.0055 by 2^-24 of that, the next term of the series 4e-11, whole numbers of 2^-38), so a running sum over Z by
-less than 1e-9, and a row may differ only where the definition's own border is that near.
+them lies within the weights' error of a running sum.  A weight is 2^(q / 32) 2^r, |r| <= 1/64: r is rounded to half a place of
+2^-30 (3.2e-10 of the weight), 2^r - 1 <= 0.011 too (4.7e-10), the table's f32 and the product with it to 2^-24 of
+0.011 (6.5e-10 each), the table's whole number to 2^-32 (2.3e-10): 2.4e-9 together.  A border compares a running sum
+with a part of another one, so a row may differ only where the definition's own border is within 5e-9 of the sum.
 """
 import math
 
@@ -15,7 +16,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
-NEAR = 1e-9
+NEAR = 5e-9
 
 
 @pytest.fixture(scope="module")
@@ -83,8 +84,8 @@ def check(qw, x, u, t=None, k=None, p=None, m=None, out_sure=0.98):
             continue
         n_sure += 1
         assert (tok[r], kept[r]) == want[:2], (r, tok[r], kept[r], want)
-        # W and S off by 1e-9, an f32 quotient (2^-24, its parts' roundings 2^-24 more)
-        assert abs(probs[r] - want[2]) <= 2e-9 * want[2] + 2 ** -23 * want[2]
+        # W and S off by 2.4e-9 each, an f32 quotient (2^-24, its parts' roundings 2^-24 more)
+        assert abs(probs[r] - want[2]) <= 5e-9 * want[2] + 2 ** -23 * want[2]
     assert n_sure >= out_sure * R
     return tok
 
