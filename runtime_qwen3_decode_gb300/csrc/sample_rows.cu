@@ -171,7 +171,8 @@ struct Total {
 
 struct Shared {
     Table table;
-    Total xch[2][kMaxCluster][kBins];   // a pass's bins of every CTA of the cluster
+    u64 xch_w[2][kMaxCluster][kBins];   // a pass's bins of every CTA of the cluster
+    unsigned xch_n[2][kMaxCluster][kBins];
     Total total[kBins];                 // and their sums
     Total cum[kBins];                   // of the octaves: each with the ones above it
     float top[kMaxCluster], least[kMaxCluster];  // greatest and least logit of every CTA
@@ -194,16 +195,16 @@ struct Parts {
 constexpr int kBinBytes = kBins * kThreads * 8;
 static_assert(sizeof(Parts) <= kBinBytes && kList * 8 <= kBinBytes, "fits over the bins");
 
-// How a pass cuts its tokens in kBins parts, the greatest first: by logit, top - x in units of 1 / inv (the last part takes
-// the rest), or by key, (key - lo) >> shift.
+// How a pass cuts its tokens in kBins parts, the greatest first: by logit, top - x in units of 1 / inv (the first and the
+// last part take the rest), or by key, (key - lo) >> shift.
 struct Cut {
     bool by_value;
     float top, inv;
     u64 lo;
     int shift;
-    // the whole part of (top - x) inv, cut at kBins - 1, by adding 2^23 rounding down
+    // the whole part of (top - x) inv, cut at 0 and kBins - 1, by adding 2^23 rounding down
     __device__ __forceinline__ int slot(float x) const {
-        return __float_as_int(__fadd_rd(fminf((top - x) * inv, kBins - 1.f), 8388608.f)) & (kBins - 1);
+        return __float_as_int(__fadd_rd(fminf(fmaxf((top - x) * inv, 0.f), kBins - 1.f), 8388608.f)) & (kBins - 1);
     }
 };
 
@@ -307,17 +308,20 @@ __device__ __forceinline__ void tally(const P &piece, Shared &sh, const Row &row
             n += (unsigned)(v >> kCountBit);
         }
         add(w, n);
-        if (lane < ctas) *cl.map_shared_rank(&sh.xch[turn][me][warp], lane) = Total{w, n, 0u};
+        if (lane < ctas) {
+            *cl.map_shared_rank(&sh.xch_w[turn][me][warp], lane) = w;
+            *cl.map_shared_rank(&sh.xch_n[turn][me][warp], lane) = n;
+        }
     }
     if (ctas > 1) cl.sync();
     else __syncthreads();
     if (tid < kBins) {
         Total t{0ull, 0u, 0u};
         for (unsigned c = 0; c < ctas; ++c) {
-            const Total &x = sh.xch[turn][c][tid];
-            t.w += x.w;
-            t.n += x.n;
-            if (c < me) t.low += x.n;
+            const unsigned n = sh.xch_n[turn][c][tid];
+            t.w += sh.xch_w[turn][c][tid];
+            t.n += n;
+            if (c < me) t.low += n;
         }
         sh.total[tid] = t;
     }
@@ -549,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rows_kernel(const __grid_c
     Cut octaves{};
     octaves.by_value = true;
     octaves.top = row.top;
-    octaves.inv = 1.f / fmaxf(fmaxf(T_ * 0.69314718f, fabsf(row.top) * 1e-6f), 1e-30f);
+    octaves.inv = 1.f / fmaxf(fmaxf(T_ * 1.38629436f, fabsf(row.top) * 1e-6f), 1e-30f);
     // The whole row: the tokens with keys from `bottom` on.  Without top_p, what min_p leaves out counts for nothing else; with it
     // the weights that it takes its part of do.
     Zone rows{(u64)ord_bits(fmaxf(least, has_p ? -FLT_MAX : cut)) << a.id_bits, ((u64)ord_bits(row.top) + 1ull) << a.id_bits, {}, {}};
@@ -616,6 +620,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rows_kernel(const __grid_c
     int stage = top_k > 0 ? 0 : 1, side = 0, turn = 0;
     enum { kOctaves, kNarrow, kMinP, kNone } pass = kOctaves;
     bool seek = false, from_octaves = true;
+    float near = -1.f;  // of the octave that was entered: the share of its width above the border, < 0: not known
     u64 goal = 0;
     Total whole{}, kept{};
     Zone z = rows;
@@ -667,6 +672,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rows_kernel(const __grid_c
         }
         if (seek) {  // into the part in which the border is
             const Total *total = from_octaves ? sh.cum : sh.total;
+            near = -1.f;
             if (from_octaves) c = octaves;
             Total t{0ull, 0u, 0u}, before{0ull, 0u, 0u};
             int b = 0;
@@ -675,6 +681,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rows_kernel(const __grid_c
                 t = from_octaves ? x : Total{before.w + x.w, before.n + x.n, before.low + x.low};
                 if (b == kBins - 1 || (stage == 0 ? (u64)(z.above.n + t.n) : z.above.w + t.w) >= goal) break;
                 before = t;
+            }
+            if (from_octaves && b > 0 && b < kBins - 2) {
+                // About where in the octave the border is, if what octaves hold grows by the same factor g^2 from the one above to the
+                // one below: 1 + share (g - 1) = g^near.
+                auto held = [&](int i) {
+                    const Total x = sh.cum[i], y = i ? sh.cum[i - 1] : Total{0ull, 0u, 0u};
+                    return stage == 0 ? (float)(x.n - y.n) : (float)(x.w - y.w);
+                };
+                const float g = sqrtf(held(b + 1) / held(b - 1)), share = (float)(goal - (stage == 0 ? (u64)before.n : before.w)) / held(b);
+                near = fabsf(g - 1.f) < 1e-3f ? share : __logf(1.f + share * (g - 1.f)) / __logf(g);
+                if (!(near >= 0.f && near <= 1.f)) near = -1.f;
             }
             z.inside = Total{t.w - before.w, t.n - before.n, t.low - before.low};
             z.above = Total{z.above.w + before.w, z.above.n + before.n, z.above.low + before.low};
@@ -706,6 +723,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rows_kernel(const __grid_c
             c.by_value = high - low > 64u && width > fmaxf(fmaxf(fabsf(xl), fabsf(xh)) * 1e-6f, 1e-30f);
             c.top = xh;
             c.inv = 1.f / width;
+            if (near >= 0.f && c.by_value) {  // narrow parts about the place where the border should be
+                const float part = width * 0.25f;
+                if (part > fmaxf(fabsf(xl), fabsf(xh)) * 1e-6f) c.top = xh - near * kBins * width + kBins / 2 * part, c.inv = 1.f / part;
+            }
             c.shift = 0;
             while ((z.end - z.lo - 1ull) >> c.shift >= (u64)kBins) ++c.shift;
             pass = kNarrow;
@@ -876,30 +897,35 @@ int bits_for(int64_t n) {  // least b with n <= 2^b
     return b;
 }
 
-}  // namespace
-
-cudaError_t launch_sample_rows(const qw_sample_rows_args &q, cudaStream_t st) {
+template <typename T>
+cudaError_t launch_typed(const qw_sample_rows_args &q, cudaStream_t st) {
     const size_t fixed = (sizeof(Shared) + 15) / 16 * 16 + kBinBytes;
     const size_t room = 227 * 1024 - fixed;
+    // As many CTAs for a row as there are SMs to take them, or as hold it with another CTA on the SM.  (Clusters of 16 for up to
+    // nine rows took 15.5 us instead of 14.2 at 8 x 151,936: what grows with the cluster outweighs the shorter pieces.)
     int ctas = 1;
-    auto per = [&] { return (int)(((int64_t)q.vocab + ctas - 1) / ctas + 7) / 8 * 8; };
-    while (ctas < kMaxCluster && per() > 4096 && ((int64_t)q.n_rows * ctas < 152 || (size_t)per() * 4 > room / 2)) ctas *= 2;
+    auto per = [&](int n) { return (int)(((int64_t)q.vocab + n - 1) / n + 7) / 8 * 8; };
+    while (ctas < kMaxCluster && per(ctas) > 4096 && ((int64_t)q.n_rows * ctas * 2 <= 152 || (size_t)per(ctas) * 4 > room / 2)) ctas *= 2;
     SampleArgs a{};
     a.logits = q.logits;
     a.stride = q.row_stride;
     a.V = q.vocab;
-    a.per = per();
+    a.per = per(ctas);
     a.id_bits = bits_for(q.vocab);
     a.wb = std::min(62 - a.id_bits, kCountBit - 1 - bits_for((a.per + 4 * kThreads - 1) / (4 * kThreads) * 4));  // a thread's tokens fit its bins
     a.u = q.u, a.temperature = q.temperature, a.top_p = q.top_p, a.min_p = q.min_p, a.top_k = q.top_k;
     a.tokens = q.tokens, a.kept = q.kept, a.probs = q.probs;
     const bool res = (size_t)a.per * 4 <= room;
-    const size_t smem = fixed + std::max<size_t>(res ? (size_t)a.per * 4 : 0, (size_t)kList * 16);  // define() sorts where the row was
-    const Table &t = table();
-    if (q.dtype == QW_DT_F32) return res ? launch_rows<float, true>(a, t, q.n_rows, ctas, smem, st) : launch_rows<float, false>(a, t, q.n_rows, ctas, smem, st);
-    if (q.dtype == QW_DT_F16) return res ? launch_rows<__half, true>(a, t, q.n_rows, ctas, smem, st) : launch_rows<__half, false>(a, t, q.n_rows, ctas, smem, st);
-    return res ? launch_rows<__nv_bfloat16, true>(a, t, q.n_rows, ctas, smem, st)
-               : launch_rows<__nv_bfloat16, false>(a, t, q.n_rows, ctas, smem, st);
+    const size_t smem = fixed + std::max<size_t>(res ? (size_t)a.per * 4 : 0, (size_t)kList * 16);  // lists are sorted where the row was
+    return res ? launch_rows<T, true>(a, table(), q.n_rows, ctas, smem, st) : launch_rows<T, false>(a, table(), q.n_rows, ctas, smem, st);
+}
+
+}  // namespace
+
+cudaError_t launch_sample_rows(const qw_sample_rows_args &q, cudaStream_t st) {
+    return q.dtype == QW_DT_F32   ? launch_typed<float>(q, st)
+           : q.dtype == QW_DT_F16 ? launch_typed<__half>(q, st)
+                                  : launch_typed<__nv_bfloat16>(q, st);
 }
 
 }  // namespace qw
