@@ -401,6 +401,24 @@ int qw_tree_attention(const qw_kv_view *kv, const qw_tree_attention_args *args, 
                       size_t scratch_bytes, void *cuda_stream);
 
 /*
+ * Attention of a batch that shares a prefix: qw_tree_attention for sequences that all see the same prefix_len[0]
+ * positions (device int32) before their own, as the continuations of one prompt do.  The prefix's rows are read
+ * once for all sequences.  prefix: a view of n_seq 1 with the format, KV heads and head_dim of kv, which holds each
+ * sequence's own positions (numbered from 0: the row behind the prefix is position 0 of kv).  Node i of
+ * sequence b sees the prefix, the len[b] cached positions of its own and, of the drafted rows behind them, those of its mask; args->mask
+ * NULL: itself and the ones before it (one node: the attention of a batched decode step).  Row (b, i) of out is
+ *   sum_j softmax_j(scale q . k_j) v_j over the prefix's and its own positions j that it sees, 0 if it sees none.
+ * args, its rows that are left as they were and its arithmetic are qw_tree_attention's; what one sequence holds does not
+ * reach another one, NaN and infinities included.  A prefix_len outside [0, prefix->max_ctx] makes every row NaN.
+ * max_prefix: about the prefix's length as the host knows it (see max_len).  n_seq x n_max x query heads of a KV head <= 2^20.
+ */
+size_t qw_prefix_attention_scratch_bytes(const qw_kv_view *prefix, const qw_kv_view *kv, int32_t n_max, int32_t n_heads,
+                                         int32_t max_len, int32_t max_prefix);
+int qw_prefix_attention(const qw_kv_view *prefix, const qw_kv_view *kv, const qw_tree_attention_args *args,
+                        const int32_t *prefix_len_dev, int32_t max_prefix, void *scratch_dev, size_t scratch_bytes,
+                        void *cuda_stream);
+
+/*
  * Logits made ready for sampling: rows [n_rows][vocab] (dtype QW_DT_F32, QW_DT_F16 or QW_DT_BF16,
  * row strides in elements) to out (same dtype; out == logits with equal strides works in place,
  * any other overlap does not).  For token t of row r, in f32 and in this order:

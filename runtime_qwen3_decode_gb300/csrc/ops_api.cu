@@ -1,5 +1,5 @@
 // ops_api.cu - argument checks of the operators on caller-owned buffers (qw_kv_append,
-// qw_kv_read, qw_tree_attention, qw_process_logits, qw_sample_rows).  Everything is checked before a launch;
+// qw_kv_read, qw_tree_attention, qw_prefix_attention, qw_process_logits, qw_sample_rows).  Everything is checked before a launch;
 // nothing here touches the device.
 #include <algorithm>
 #include <cmath>
@@ -108,6 +108,38 @@ int check_tree_sizes(const qw_kv_view *kv, int32_t n_max, int32_t n_heads, int32
     return QW_OK;
 }
 
+// What the two attentions check of their arguments beside the sizes; masks: they must be given.
+int check_attention(const qw_kv_view *kv, const qw_tree_attention_args *a, const void *scratch, bool masks) {
+    const int e = elem_bytes(a->dtype);
+    if (!a->q || !a->out || (masks && !a->mask) || !scratch) return QW_INVALID_ARGUMENT;
+    const int64_t unit = 16 / e;
+    if (!aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(scratch, 256) || !stride_ok(a->q_seq_stride, unit) ||
+        !stride_ok(a->q_node_stride, unit) || !stride_ok(a->q_head_stride, unit) ||
+        !stride_ok(a->out_seq_stride, unit) || !stride_ok(a->out_node_stride, unit) ||
+        !stride_ok(a->out_head_stride, unit) || !aligned(a->mask, 8) || !aligned(a->len, 4) || !aligned(a->count, 4))
+        return QW_ALIGNMENT;
+    // no two rows of the result may share an address
+    if (!rows_apart(kv->head_dim, {kv->n_seq, a->out_seq_stride}, {a->n_max, a->out_node_stride},
+                    {a->n_heads, a->out_head_stride}))
+        return QW_INVALID_ARGUMENT;
+    return QW_OK;
+}
+
+int check_prefix(const qw_kv_view *prefix, const qw_kv_view *kv, int32_t n_max, int32_t n_heads, int32_t max_len,
+                 int32_t max_prefix) {
+    int rc = check_view(prefix);
+    if (!rc) rc = check_view(kv);
+    if (rc) return rc;
+    if (prefix->n_seq != 1 || prefix->format != kv->format || prefix->n_kv_heads != kv->n_kv_heads ||
+        prefix->head_dim != kv->head_dim || max_prefix < 0 || max_prefix > prefix->max_ctx)
+        return QW_INVALID_ARGUMENT;
+    rc = check_tree_sizes(kv, n_max, n_heads, max_len);
+    if (rc) return rc;
+    // the rows that share the prefix are numbered in a word, and divided by what a sequence has of them in another
+    if ((int64_t)kv->n_seq * n_max * (n_heads / kv->n_kv_heads) > 1 << 20) return QW_UNSUPPORTED_SHAPE;
+    return QW_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -144,19 +176,33 @@ int qw_tree_attention(const qw_kv_view *kv, const qw_tree_attention_args *a, voi
     const int e = elem_bytes(a->dtype);
     if (!e || !a->len || !std::isfinite(a->scale)) return QW_INVALID_ARGUMENT;
     if (a->n_max == 0) return QW_OK;
-    if (!a->q || !a->out || !a->mask || !scratch_dev) return QW_INVALID_ARGUMENT;
-    const int64_t unit = 16 / e;
-    if (!aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(scratch_dev, 256) || !stride_ok(a->q_seq_stride, unit) ||
-        !stride_ok(a->q_node_stride, unit) || !stride_ok(a->q_head_stride, unit) ||
-        !stride_ok(a->out_seq_stride, unit) || !stride_ok(a->out_node_stride, unit) ||
-        !stride_ok(a->out_head_stride, unit) || !aligned(a->mask, 8) || !aligned(a->len, 4) || !aligned(a->count, 4))
-        return QW_ALIGNMENT;
-    // no two rows of the result may share an address
-    if (!rows_apart(kv->head_dim, {kv->n_seq, a->out_seq_stride}, {a->n_max, a->out_node_stride},
-                    {a->n_heads, a->out_head_stride}))
-        return QW_INVALID_ARGUMENT;
+    rc = check_attention(kv, a, scratch_dev, true);
+    if (rc) return rc;
     if (scratch_bytes < qw_tree_attention_scratch_bytes(kv, a->n_max, a->n_heads, a->max_len)) return QW_OUT_OF_MEMORY;
     return status_of(qw::launch_tree_attn(*kv, *a, scratch_dev, (cudaStream_t)cuda_stream));
+}
+
+size_t qw_prefix_attention_scratch_bytes(const qw_kv_view *prefix, const qw_kv_view *kv, int32_t n_max, int32_t n_heads,
+                                         int32_t max_len, int32_t max_prefix) {
+    if (check_prefix(prefix, kv, n_max, n_heads, max_len, max_prefix) || n_max == 0) return 0;
+    return qw::prefix_attn_scratch_bytes(*kv, n_max, n_heads, max_len, max_prefix);
+}
+
+int qw_prefix_attention(const qw_kv_view *prefix, const qw_kv_view *kv, const qw_tree_attention_args *a,
+                        const int32_t *prefix_len_dev, int32_t max_prefix, void *scratch_dev, size_t scratch_bytes,
+                        void *cuda_stream) {
+    if (!prefix || !kv || !a) return QW_INVALID_ARGUMENT;
+    int rc = check_prefix(prefix, kv, a->n_max, a->n_heads, a->max_len, max_prefix);
+    if (rc) return rc;
+    if (!elem_bytes(a->dtype) || !a->len || !prefix_len_dev || !std::isfinite(a->scale)) return QW_INVALID_ARGUMENT;
+    if (!aligned(prefix_len_dev, 4)) return QW_ALIGNMENT;
+    if (a->n_max == 0) return QW_OK;
+    rc = check_attention(kv, a, scratch_dev, false);
+    if (rc) return rc;
+    const size_t need = qw::prefix_attn_scratch_bytes(*kv, a->n_max, a->n_heads, a->max_len, max_prefix);
+    if (need == 0) return QW_UNSUPPORTED_SHAPE;
+    if (scratch_bytes < need) return QW_OUT_OF_MEMORY;
+    return status_of(qw::launch_prefix_attn(*prefix, *kv, *a, prefix_len_dev, max_prefix, scratch_dev, (cudaStream_t)cuda_stream));
 }
 
 int qw_process_logits(const qw_process_logits_args *a, void *cuda_stream) {

@@ -28,6 +28,11 @@ size_t tree_attn_scratch_bytes(int n_seq, int n_kv_heads, int n_max, int n_heads
 cudaError_t launch_tree_attn(const qw_kv_view &kv, const qw_tree_attention_args &a, void *scratch, cudaStream_t st,
                              bool chained = false);
 
+// Attention of a batch whose sequences see a prefix before their own caches; 0 bytes for sizes that no grid holds.
+size_t prefix_attn_scratch_bytes(const qw_kv_view &kv, int n_max, int n_heads, int max_len, int max_prefix);
+cudaError_t launch_prefix_attn(const qw_kv_view &prefix, const qw_kv_view &kv, const qw_tree_attention_args &t,
+                               const int32_t *prefix_len, int max_prefix, void *scratch, cudaStream_t st, bool chained = false);
+
 cudaError_t launch_process_logits(const qw_process_logits_args &a, cudaStream_t st);
 
 cudaError_t launch_sample_rows(const qw_sample_rows_args &a, cudaStream_t st);

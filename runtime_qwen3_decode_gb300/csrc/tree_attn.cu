@@ -51,8 +51,13 @@ __device__ __forceinline__ void split_range(int total, int S, int s, int &p0, in
 // (FFMA2), whose operands keep its reads at 87% of their rate; tiles of up to 32 rows share them.
 // One token of 8 sequences over f32 caches of up to 512: 9 us (floor 3); 8 nodes over 32768 f32
 // positions: 123 us (40); 64 nodes over 32768 8-bit positions: 680 us (11).
-template <typename KV, int D, int RT>
-__global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeArgs a) {
+//
+// PREFIX: the same kernel for a batch whose sequences all see a prefix, in one grid of two kinds of blocks.  The first p_blocks take
+// tiles of RT rows of all sequences together (row = (sequence, node, head of the group)) and splits of the prefix, so that the prefix
+// is read once for RT rows, whatever sequences they belong to; the others each sequence's own positions, as above.
+// Every block writes partials: splits [0, Sp) of a row are the prefix's, the rest its sequence's.
+template <typename KV, int D, int RT, bool PREFIX = false>
+__global__ void __launch_bounds__(kThreads, 2) tree_kernel(const AttnArgs<PREFIX> a) {
     constexpr int KS = D + 4;                       // padded K row: quarter warps read 8 banks groups
     constexpr int LPR = D / 4;                      // lanes per V row
     constexpr int KPW = 32 / LPR;                   // positions a warp takes at once in P V
@@ -68,11 +73,53 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeArgs a) {
     __shared__ unsigned long long smask[RT];
     tc::chain_wait();
     tc::chain_release();
-    const int b = blockIdx.z, h = blockIdx.y / a.row_tiles, rt = blockIdx.y % a.row_tiles, s = blockIdx.x;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    int len, n;
-    const bool fits = lengths(a, b, len, n);
-    const int r0 = rt * RT, rows = n * a.G;
+    int b = blockIdx.z, h = blockIdx.y / a.row_tiles, rt = blockIdx.y % a.row_tiles, s = blockIdx.x, S = a.S, s0 = 0, len, n, rows;
+    const KV *kb, *vb;
+    const __half *ksb, *vsb;
+    int64_t pstride, sstride;
+    bool fits, pre = false;
+    if constexpr (PREFIX) {
+        int x = blockIdx.x;
+        pre = x < a.p_blocks;
+        if (pre) {
+            s = x % a.Sp, x /= a.Sp;
+            rt = x % a.p_row_tiles, h = x / a.p_row_tiles, b = 0, S = a.Sp;
+        } else {
+            x -= a.p_blocks;
+            s0 = a.Sp, S = a.S - a.Sp;
+            s = x % S, x /= S;
+            rt = x % a.row_tiles, x /= a.row_tiles;
+            h = x % a.Hkv, b = x / a.Hkv;
+        }
+    }
+    if constexpr (PREFIX) {
+        if (pre) {
+            fits = prefix_length(a, len);
+            n = 0, rows = a.n_seq * a.n_max * a.G;
+            kb = reinterpret_cast<const KV *>(a.pk) + h * a.phead, vb = reinterpret_cast<const KV *>(a.pv) + h * a.phead;
+            ksb = a.pks + h * a.pshead, vsb = a.pvs + h * a.pshead;
+            pstride = a.ppos, sstride = a.pspos;
+        }
+    }
+    if (!pre) {
+        fits = lengths(a, b, len, n);
+        rows = n * a.G;
+        kb = reinterpret_cast<const KV *>(a.k) + b * a.seq + h * a.head, vb = reinterpret_cast<const KV *>(a.v) + b * a.seq + h * a.head;
+        ksb = a.ks + b * a.sseq + h * a.shead, vsb = a.vs + b * a.sseq + h * a.shead;
+        pstride = a.pos, sstride = a.spos;
+    }
+    const int r0 = rt * RT;
+    if constexpr (PREFIX) {
+        if (!fits) return;  // the merge fills the rows
+    }
+    // row r of this block's kind: its sequence, and which row of it
+    auto place = [&](int r, int &seq, int &row) {
+        seq = b, row = r;
+        if constexpr (PREFIX) {
+            if (pre) seq = (int)((unsigned)r * a.inv_rows >> 32), row = r - seq * a.n_max * a.G;
+        }
+    };
     if (!fits) {  // without a merge kernel behind it this one fills the rows
         for (int i = tid; a.S == 1 && i < RT * D; i += kThreads)
             if (r0 + i / D < a.n_max * a.G) store_out(a, out_row(a, b, h, r0 + i / D) + i % D, nanf(""));
@@ -81,9 +128,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeArgs a) {
     if (r0 >= rows) return;
     const int total = len + n;
     int p0, p1;
-    split_range(total, a.S, s, p0, p1);
-    const KV *kb = reinterpret_cast<const KV *>(a.k) + b * a.seq + h * a.head;
-    const KV *vb = reinterpret_cast<const KV *>(a.v) + b * a.seq + h * a.head;
+    split_range(total, S, s, p0, p1);
     uint4 raw[2][LPT];
     __half scale[2][sizeof(KV) == 1 ? LPT : 1];
     auto fetch = [&](int t0) {
@@ -95,22 +140,24 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeArgs a) {
                 raw[plane][i] = make_uint4(0u, 0u, 0u, 0u);
                 if constexpr (sizeof(KV) == 1) scale[plane][i] = __half(0);
                 if (pos >= p1) continue;
-                raw[plane][i] = *reinterpret_cast<const uint4 *>((plane ? vb : kb) + (int64_t)pos * a.pos + E * c);
+                raw[plane][i] = *reinterpret_cast<const uint4 *>((plane ? vb : kb) + (int64_t)pos * pstride + E * c);
                 if constexpr (sizeof(KV) == 1)
-                    scale[plane][i] = ((plane ? a.vs : a.ks) + b * a.sseq + h * a.shead + (int64_t)pos * a.spos)[E * c / kQGroup];
+                    scale[plane][i] = ((plane ? vsb : ksb) + (int64_t)pos * sstride)[E * c / kQGroup];
             }
     };
     fetch(p0);
     for (int i = tid; i < RT * D; i += kThreads) {
-        const int r = r0 + i / D;
-        sq[i] = r < rows ? load_q(a, b * a.qseq + (int64_t)(r / a.G) * a.qnode +
-                                         (int64_t)(h * a.G + r % a.G) * a.qhead + i % D) * a.scale_log2
-                         : 0.f;
+        int seq, r = r0 + i / D;
+        const bool is = r < rows;
+        if (is) place(r, seq, r);
+        sq[i] = is ? load_q(a, seq * a.qseq + (int64_t)(r / a.G) * a.qnode + (int64_t)(h * a.G + r % a.G) * a.qhead + i % D) *
+                         a.scale_log2
+                   : 0.f;
     }
     if (tid < RT) {
         sm[tid] = -INFINITY;
         sl[tid] = 0.f;
-        smask[tid] = r0 + tid < rows ? a.mask[(int64_t)b * a.n_max + (r0 + tid) / a.G] : 0ull;
+        smask[tid] = !pre && r0 + tid < rows ? node_mask(a, b, (r0 + tid) / a.G) : 0ull;
     }
     float2 acc[RW][2];
 #pragma unroll
@@ -231,16 +278,18 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeArgs a) {
                 make_float4(acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y);
         __syncthreads();
         for (int i = tid; i < RT * D; i += kThreads) {
-            const int rl = i / D, d = i % D, r = r0 + rl;
+            const int rl = i / D, d = i % D;
+            int r = r0 + rl, seq;
             if (r >= rows) continue;
+            place(r, seq, r);
             float o = 0.f;
 #pragma unroll
             for (int k = 0; k < PARTS; ++k) o += red[(rl * PARTS + k) * D + d];
-            if (a.S == 1) {  // the only split: nothing to merge
+            if (!PREFIX && a.S == 1) {  // the only split: nothing to merge
                 store_out(a, out_row(a, b, h, r) + d, sl[rl] == 0.f ? 0.f : o / sl[rl]);
                 continue;
             }
-            float *dst = a.part + ((((int64_t)b * a.Hkv + h) * a.n_max * a.G + r) * a.S + s) * (D + 2);
+            float *dst = a.part + ((((int64_t)seq * a.Hkv + h) * a.n_max * a.G + r) * a.S + s0 + s) * (D + 2);
             dst[d] = o;
             if (d == 0) {
                 dst[D] = sm[rl];
@@ -254,11 +303,15 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeArgs a) {
 // of kBatch splits are loaded at once: the kernel is their latency.
 constexpr int kBatch = 8;
 
-template <int D>
-__global__ void __launch_bounds__(D) tree_merge_kernel(const TreeArgs a) {
+template <int D, bool PREFIX = false>
+__global__ void __launch_bounds__(D) tree_merge_kernel(const AttnArgs<PREFIX> a) {
     const int r = blockIdx.x, h = blockIdx.y, b = blockIdx.z, d = threadIdx.x;
     int len, n;
-    const bool fits = lengths(a, b, len, n);
+    bool fits = lengths(a, b, len, n);
+    if constexpr (PREFIX) {
+        int prefix;
+        fits &= prefix_length(a, prefix);
+    }
     const int64_t at = out_row(a, b, h, r) + d;
     const float *src = a.part + (((int64_t)b * a.Hkv + h) * a.n_max * a.G + r) * a.S * (D + 2);
     tc::chain_wait();
@@ -346,19 +399,59 @@ cudaError_t launch_rt(const TreeArgs &a, int n_seq, int rt, cudaStream_t st, boo
     return launch_k(true, tree_merge_kernel<D>, dim3(a.n_max * a.G, a.Hkv, n_seq), dim3(D), 0, st, a);
 }
 
-}  // namespace
+// ---------------------------------------------------------------- a shared prefix
 
-size_t tree_attn_scratch_bytes(int n_seq, int n_kv_heads, int n_max, int n_heads, int head_dim, int max_len) {
-    const int G = n_heads / n_kv_heads, rows = n_max * G, rt = rows_per_tile(rows);
-    const int S = splits(n_seq, n_kv_heads, (rows + rt - 1) / rt, rt, max_len + n_max);
-    const size_t cores = ((size_t)n_seq * n_kv_heads * rows * S * (head_dim + 2) * 4 + 255) / 256 * 256;
-    return std::max(cores, tree_tc_scratch_bytes(rows, head_dim));
+// Rows per tile, for both kinds of blocks: the least of what the tiles cost at each choice.  A tile of 64 positions takes about
+// 15.5 + 0.9 RT ns of the whole GPU's time (1,089 tiles of 2 rows 17 us, 16,384 of 32 rows 680 us); with more rows per tile the
+// prefix has fewer tiles, but the sequences' own tiles, which hold few rows, cost more.
+struct PrefixPlan {
+    int rt, row_tiles, p_row_tiles, Sp, S;
+    int64_t p_blocks, blocks;
+};
+PrefixPlan plan_prefix(int n_seq, int Hkv, int n_max, int G, int max_len, int max_prefix) {
+    const int64_t rows = (int64_t)n_max * G, all = rows * n_seq;
+    const int64_t own = (max_len + n_max + kTile - 1) / kTile, pre = std::max((max_prefix + kTile - 1) / kTile, 1);
+    PrefixPlan best{};
+    double least = 0;
+    for (int rt = 2; rt <= 32; rt *= 2) {
+        const int64_t rt_own = (rows + rt - 1) / rt, rt_pre = (all + rt - 1) / rt;
+        const int64_t tiles = Hkv * (rt_own * n_seq * own + rt_pre * pre);
+        const double cost = (15.5 + 0.9 * rt) * (double)tiles;
+        if (best.rt && cost >= least) continue;
+        least = cost;
+        // splits: up to four CTAs for every SM, none shorter than a tile
+        const int64_t share = std::max<int64_t>(1, (tiles + 4 * 152 - 1) / (4 * 152));
+        const int64_t Sp = (pre + share - 1) / share, So = (own + share - 1) / share;
+        best = {rt, (int)rt_own, (int)rt_pre, (int)Sp, (int)(Sp + So), Sp * rt_pre * Hkv, Sp * rt_pre * Hkv + So * rt_own * Hkv * n_seq};
+    }
+    return best;
 }
 
-cudaError_t launch_tree_attn(const qw_kv_view &kv, const qw_tree_attention_args &t, void *scratch, cudaStream_t st,
-                             bool chained) {
-    if (kv.n_seq == 0 || t.n_max == 0) return cudaSuccess;
-    TreeArgs a{};
+template <typename KV, int D, int RT>
+cudaError_t launch_prefix_tile(const PrefixArgs &a, int64_t blocks, cudaStream_t st, bool chained) {
+    constexpr int smem = (kTile * (D + 4) + kTile * D + RT * D + RT * kTile) * 4;
+    cudaError_t e = allow_smem<tree_kernel<KV, D, RT, true>>(smem);
+    if (e != cudaSuccess) return e;
+    e = launch_k(chained, tree_kernel<KV, D, RT, true>, dim3((unsigned)blocks), dim3(kThreads), smem, st, a);
+    if (e != cudaSuccess) return e;
+    return launch_k(true, tree_merge_kernel<D, true>, dim3(a.n_max * a.G, a.Hkv, a.n_seq), dim3(D), 0, st, a);
+}
+
+template <typename KV, int D>
+cudaError_t launch_prefix_rt(const PrefixArgs &a, const PrefixPlan &p, cudaStream_t st, bool ch) {
+    return p.rt == 2   ? launch_prefix_tile<KV, D, 2>(a, p.blocks, st, ch)
+           : p.rt == 4 ? launch_prefix_tile<KV, D, 4>(a, p.blocks, st, ch)
+           : p.rt == 8 ? launch_prefix_tile<KV, D, 8>(a, p.blocks, st, ch)
+           : p.rt == 16 ? launch_prefix_tile<KV, D, 16>(a, p.blocks, st, ch)
+                        : launch_prefix_tile<KV, D, 32>(a, p.blocks, st, ch);
+}
+
+template <typename KV>
+cudaError_t launch_prefix_dim(const PrefixArgs &a, const PrefixPlan &p, int D, cudaStream_t st, bool ch) {
+    return D == 128 ? launch_prefix_rt<KV, 128>(a, p, st, ch) : launch_prefix_rt<KV, 64>(a, p, st, ch);
+}
+
+void fill(TreeArgs &a, const qw_kv_view &kv, const qw_tree_attention_args &t, void *scratch) {
     a.k = (const uint8_t *)kv.k;
     a.v = (const uint8_t *)kv.v;
     a.ks = (const __half *)kv.k_scale;
@@ -379,6 +472,57 @@ cudaError_t launch_tree_attn(const qw_kv_view &kv, const qw_tree_attention_args 
     a.G = t.n_heads / kv.n_kv_heads;
     a.scale_log2 = t.scale * kOpsLog2e;
     a.part = (float *)scratch;
+}
+
+}  // namespace
+
+// For every call with these sizes and these lengths or less: a plan's splits are no more than tiles, nor than its share of 4 x 152
+// blocks gives the tiles of at most 32 rows.
+size_t prefix_attn_scratch_bytes(const qw_kv_view &kv, int n_max, int n_heads, int max_len, int max_prefix) {
+    const int64_t rows = (int64_t)n_max * (n_heads / kv.n_kv_heads), all = rows * kv.n_seq, most = 4 * 152;
+    const int64_t own = (max_len + n_max + kTile - 1) / kTile, pre = std::max((max_prefix + kTile - 1) / kTile, 1);
+    const int64_t Sp = std::min(pre, most / (kv.n_kv_heads * ((all + 31) / 32)) + 1);
+    const int64_t So = std::min(own, most / (kv.n_kv_heads * ((rows + 31) / 32) * kv.n_seq) + 1);
+    if (plan_prefix(kv.n_seq, kv.n_kv_heads, n_max, n_heads / kv.n_kv_heads, max_len, max_prefix).blocks > INT32_MAX) return 0;
+    return ((size_t)(all * kv.n_kv_heads * (Sp + So)) * (kv.head_dim + 2) * 4 + 255) / 256 * 256;
+}
+
+cudaError_t launch_prefix_attn(const qw_kv_view &prefix, const qw_kv_view &kv, const qw_tree_attention_args &t,
+                               const int32_t *prefix_len, int max_prefix, void *scratch, cudaStream_t st, bool chained) {
+    if (t.n_max == 0) return cudaSuccess;
+    PrefixArgs a{};
+    fill(a, kv, t, scratch);
+    a.pk = (const uint8_t *)prefix.k;
+    a.pv = (const uint8_t *)prefix.v;
+    a.pks = (const __half *)prefix.k_scale;
+    a.pvs = (const __half *)prefix.v_scale;
+    a.phead = prefix.head_stride, a.ppos = prefix.pos_stride;
+    a.pshead = prefix.scale_head_stride, a.pspos = prefix.scale_pos_stride;
+    a.plen = prefix_len;
+    a.p_max = prefix.max_ctx;
+    a.n_seq = kv.n_seq;
+    a.inv_rows = (1ull << 32) / (a.n_max * a.G) + 1;
+    a.inv_g = (1ull << 32) / a.G + 1;
+    const PrefixPlan p = plan_prefix(kv.n_seq, kv.n_kv_heads, t.n_max, a.G, t.max_len, max_prefix);
+    a.row_tiles = p.row_tiles, a.p_row_tiles = p.p_row_tiles;
+    a.Sp = p.Sp, a.S = p.S, a.p_blocks = (int)p.p_blocks;
+    return kv.format == QW_KV_F32    ? launch_prefix_dim<float>(a, p, kv.head_dim, st, chained)
+           : kv.format == QW_KV_BF16 ? launch_prefix_dim<__nv_bfloat16>(a, p, kv.head_dim, st, chained)
+                                     : launch_prefix_dim<int8_t>(a, p, kv.head_dim, st, chained);
+}
+
+size_t tree_attn_scratch_bytes(int n_seq, int n_kv_heads, int n_max, int n_heads, int head_dim, int max_len) {
+    const int G = n_heads / n_kv_heads, rows = n_max * G, rt = rows_per_tile(rows);
+    const int S = splits(n_seq, n_kv_heads, (rows + rt - 1) / rt, rt, max_len + n_max);
+    const size_t cores = ((size_t)n_seq * n_kv_heads * rows * S * (head_dim + 2) * 4 + 255) / 256 * 256;
+    return std::max(cores, tree_tc_scratch_bytes(rows, head_dim));
+}
+
+cudaError_t launch_tree_attn(const qw_kv_view &kv, const qw_tree_attention_args &t, void *scratch, cudaStream_t st,
+                             bool chained) {
+    if (kv.n_seq == 0 || t.n_max == 0) return cudaSuccess;
+    TreeArgs a{};
+    fill(a, kv, t, scratch);
     if (t.dtype != QW_DT_F32 && !small_call(kv, t)) return launch_tree_tc(a, kv, t.max_len, scratch, st, chained);
     const int rows = t.n_max * a.G, rt = rows_per_tile(rows);
     a.row_tiles = (rows + rt - 1) / rt;

@@ -2,6 +2,8 @@
 // f32 throughout; tree_tc.cu: tensor cores on 16-bit operands).
 #pragma once
 
+#include <type_traits>
+
 #include "qw_ops.h"
 
 namespace qw {
@@ -20,6 +22,31 @@ struct TreeArgs {
     float scale_log2;
     float *part;                 // [n_seq][Hkv][n_max * G][S][D + 2]
 };
+
+// The same with a prefix that all sequences see, in planes of its own: [head][position][dim] (prefix attention).
+struct PrefixArgs : TreeArgs {
+    const uint8_t *pk, *pv;
+    const __half *pks, *pvs;
+    int64_t phead, ppos, pshead, pspos;
+    const int32_t *plen;
+    int p_max, n_seq;
+    int Sp, p_row_tiles, p_blocks;  // CUDA-core form: splits of the prefix, tiles of all sequences' rows, their blocks
+    unsigned long long inv_rows;    // 2^32 / (n_max G) + 1: row / (n_max G) for fewer than 2^20 rows
+    unsigned long long inv_g;
+};
+template <bool PREFIX>
+using AttnArgs = typename std::conditional<PREFIX, PrefixArgs, TreeArgs>::type;
+
+// The prefix's length, if it fits its cache; else every row is NaN.
+__device__ __forceinline__ bool prefix_length(const PrefixArgs &a, int &len) {
+    len = *a.plen;
+    return len >= 0 && len <= a.p_max;
+}
+
+// The drafted rows that node i of sequence b sees: its mask, or without masks itself and the ones before it.
+__device__ __forceinline__ unsigned long long node_mask(const TreeArgs &a, int b, int i) {
+    return a.mask ? a.mask[(int64_t)b * a.n_max + i] : ~0ull >> (63 - i);
+}
 
 __device__ __forceinline__ float load_q(const TreeArgs &a, int64_t at) {
     return a.dtype == QW_DT_F32   ? reinterpret_cast<const float *>(a.q)[at]

@@ -61,7 +61,8 @@ EXPORTS = ("qw_workspace_bytes", "qw_model_create", "qw_prefill", "qw_decode_ste
            "qw_batch_logits", "qw_batch_debug_hidden", "qw_batch_sync", "qw_checkpoint_open",
            "qw_checkpoint_close", "qw_checkpoint_last_error", "qw_checkpoint_count", "qw_checkpoint_tensor",
            "qw_checkpoint_check", "qw_checkpoint_upload_bytes", "qw_checkpoint_upload", "qw_kv_append", "qw_kv_read",
-           "qw_tree_attention_scratch_bytes", "qw_tree_attention", "qw_process_logits", "qw_sample_rows", "qw_batch_workspace_bytes_kv",
+           "qw_tree_attention_scratch_bytes", "qw_tree_attention", "qw_prefix_attention_scratch_bytes",
+           "qw_prefix_attention", "qw_process_logits", "qw_sample_rows", "qw_batch_workspace_bytes_kv",
            "qw_batch_create_kv", "qw_batch_tree_step", "qw_batch_tree_accept")
 DT_BF16, DT_F16, DT_F32, DT_I8, DT_Q8_0 = 0, 1, 2, 3, 4
 BATCH_MAX = 8
@@ -230,6 +231,9 @@ def _lib():
             L.qw_tree_attention_scratch_bytes.argtypes = [vp, i32, i32, i32]
             L.qw_tree_attention_scratch_bytes.restype = ctypes.c_size_t
             L.qw_tree_attention.argtypes = [vp, vp, vp, ctypes.c_size_t, vp]
+            L.qw_prefix_attention_scratch_bytes.argtypes = [vp, vp, i32, i32, i32, i32]
+            L.qw_prefix_attention_scratch_bytes.restype = ctypes.c_size_t
+            L.qw_prefix_attention.argtypes = [vp, vp, vp, vp, i32, vp, ctypes.c_size_t, vp]
             L.qw_process_logits.argtypes = [vp, vp]
             L.qw_sample_rows.argtypes = [vp, vp]
             L.qw_status_string.argtypes = [ctypes.c_int]
@@ -517,10 +521,7 @@ def tree_attention(view: KvView, q, mask, lens, out=None, counts=None, max_len=N
     [n_seq] on the device.  Node i of sequence b attends to cached positions [0, lens[b]) and to the
     drafted rows lens[b] + j that mask[b, i] names.  max_len: about the longest lens (None: the cache's
     length); scale None: 1 / sqrt(head_dim).  Returns out (rows i >= counts[b] as they were)."""
-    dev, shape, stride = view._dev, q.shape, q.stride()
-    if len(shape) != 4 or shape[0] != view.n_seq or shape[3] != view.head_dim or stride[3] != 1 or q.get_device() != dev:
-        raise ValueError("q must be [n_seq, n, n_heads, head_dim] beside the cache, with a contiguous last dimension")
-    n, heads = shape[1], shape[2]
+    dev, n, heads = _check_q(view, q)
     if max_len is None:
         max_len = view.max_ctx
     if out is None or scratch is None:
@@ -529,17 +530,67 @@ def tree_attention(view: KvView, q, mask, lens, out=None, counts=None, max_len=N
                 out = _T.zeros_like(q, memory_format=_T.contiguous_format)
             if scratch is None:
                 scratch = tree_attention_scratch(view, n, heads, max_len)
-    ostride = out.stride()
+    args = _attention_args(view, q, out, scratch, max_len, scale, _want(mask, "mask", dev, _T.int64, q.shape[:2]), lens, counts)
+    _on(dev, stream, "qw_tree_attention", _lib().qw_tree_attention, view._ref, args, scratch.data_ptr(), scratch.nbytes)
+    return out
+
+
+def _check_q(view, q):
+    shape, dev = q.shape, view._dev
+    if len(shape) != 4 or shape[0] != view.n_seq or shape[3] != view.head_dim or q.stride(3) != 1 or q.get_device() != dev:
+        raise ValueError("q must be [n_seq, n, n_heads, head_dim] beside the cache, with a contiguous last dimension")
+    return dev, shape[1], shape[2]
+
+
+def _attention_args(view, q, out, scratch, max_len, scale, mask, lens, counts):
+    """The packed qw_tree_attention_args."""
+    dev, shape, stride, ostride = view._dev, q.shape, q.stride(), out.stride()
     if out.shape != shape or out.dtype is not q.dtype or out.get_device() != dev or ostride[3] != 1:
         raise ValueError("out must be like q, with a contiguous last dimension")
     if scratch.get_device() != dev or not scratch.is_contiguous():
         raise ValueError("scratch must be contiguous, beside the cache")
     i32 = _T.int32
-    args = _TREE_ARGS.pack(q.data_ptr(), out.data_ptr(), _dtype_code(q, "q"), n, heads, max_len,
+    return _TREE_ARGS.pack(q.data_ptr(), out.data_ptr(), _dtype_code(q, "q"), shape[1], shape[2], max_len,
                            view.head_dim ** -0.5 if scale is None else scale, stride[0], stride[1], stride[2],
-                           ostride[0], ostride[1], ostride[2], _want(mask, "mask", dev, _T.int64, shape[:2]),
-                           _want(lens, "lens", dev, i32, view._per_seq), _want(counts, "counts", dev, i32, view._per_seq))
-    _on(dev, stream, "qw_tree_attention", _lib().qw_tree_attention, view._ref, args, scratch.data_ptr(), scratch.nbytes)
+                           ostride[0], ostride[1], ostride[2], mask, _want(lens, "lens", dev, i32, view._per_seq),
+                           _want(counts, "counts", dev, i32, view._per_seq))
+
+
+def prefix_attention_scratch(prefix: KvView, view: KvView, n_max: int, n_heads: int, max_len: int | None = None,
+                             max_prefix: int | None = None):
+    """Workspace of prefix_attention calls with these sizes (None: the caches' lengths), one call at a time."""
+    n = _lib().qw_prefix_attention_scratch_bytes(prefix._ref, view._ref, n_max, n_heads,
+                                                 view.max_ctx if max_len is None else max_len,
+                                                 prefix.max_ctx if max_prefix is None else max_prefix)
+    if n == 0 and n_max:
+        raise QwError(UNSUPPORTED_SHAPE, "qw_prefix_attention_scratch_bytes")
+    return _T.empty(max(n, 256), dtype=_T.uint8, device=view.device)
+
+
+def prefix_attention(prefix: KvView, view: KvView, q, lens, prefix_len, mask=None, out=None, counts=None, max_len=None,
+                     max_prefix=None, scale=None, scratch=None, stream=None):
+    """qw_prefix_attention: tree_attention for sequences that all see the first prefix_len (int32 [1] on the
+    device) positions of `prefix`, a view of one sequence, before their own positions in `view`.  mask int64
+    [n_seq, n], or None: every row sees itself and the drafted rows before it.  max_len, max_prefix: about the
+    longest lens and the prefix's length (None: the caches' lengths).  Returns out."""
+    dev, n, heads = _check_q(view, q)
+    if prefix._dev != dev:
+        raise ValueError("the prefix must be beside the cache")
+    if prefix_len is None:
+        raise ValueError("prefix_len must be given")
+    if max_len is None:
+        max_len = view.max_ctx
+    if max_prefix is None:
+        max_prefix = prefix.max_ctx
+    if out is None or scratch is None:
+        with _T.cuda.stream(stream):  # what is allocated here belongs to the stream that uses it
+            if out is None:
+                out = _T.zeros_like(q, memory_format=_T.contiguous_format)
+            if scratch is None:
+                scratch = prefix_attention_scratch(prefix, view, n, heads, max_len, max_prefix)
+    args = _attention_args(view, q, out, scratch, max_len, scale, _want(mask, "mask", dev, _T.int64, q.shape[:2]), lens, counts)
+    _on(dev, stream, "qw_prefix_attention", _lib().qw_prefix_attention, prefix._ref, view._ref, args,
+        _want(prefix_len, "prefix_len", dev, _T.int32, (1,)), max_prefix, scratch.data_ptr(), scratch.nbytes)
     return out
 
 
