@@ -1,0 +1,87 @@
+// prefix_tc.cu - the tensor-core form of the attention of a batch that shares a prefix (tree_tc.cuh): its merge and launches.
+#include "tree_tc.cuh"
+
+namespace qw {
+namespace {
+
+// Merge of the items that were cut: thread = (row, four dims) of one (row tile, KV head), as in tree_tc.cu.  Also fills the rows of
+// sequences that do not fit with NaN, and every row if the prefix does not or a CTA gave up.
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) prefix_tc_merge_kernel(const Prefix p, int ctas) {
+    const PrefixArgs &a = p.a;
+    const int rt = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+    const int nr = min(kTcRows, row_count(p) - rt * kTcRows);
+    const int e = blockIdx.z * kMergeThreads + tid, rl = e % nr, dq = e / nr;
+    int b, node, g, len, n, plen;
+    p.place(rt * kTcRows + rl, b, node, g);
+    const bool fits = lengths(a, b, len, n) && prefix_length(a, plen);
+    const int64_t at = b * a.oseq + (int64_t)node * a.onode + (int64_t)(h * a.G + g) * a.ohead + 4 * dq;
+    chain_wait();
+    const long long first = p.starts[rt], tiles = p.starts[rt + 1] - first, total = p.starts[row_tiles(p)] * a.Hkv;
+    int gave_up = 0;
+#pragma unroll
+    for (int i = 0; i < (kTcCtas + 31) / 32; ++i) gave_up |= p.status[min(lane + 32 * i, ctas - 1)];
+    int c0 = 0, c1 = 0;
+    if (tiles > 0 && dq < D / 4) {
+        // owner of tile t: the largest c with T c / C <= t
+        const long long t0 = first * a.Hkv + h * tiles, t1 = t0 + tiles;
+        c0 = (int)(total < (1 << 24) ? ((unsigned)(t0 + 1) * (unsigned)ctas - 1) / (unsigned)total : ((t0 + 1) * ctas - 1) / total);
+        c1 = (int)(total < (1 << 24) ? ((unsigned)t1 * (unsigned)ctas - 1) / (unsigned)total : (t1 * ctas - 1) / total);
+    }
+    const bool there = fits && node < n;
+    float num[4] = {0.f, 0.f, 0.f, 0.f}, den = 0.f;
+    if (there) add_partials<D>(p, ctas, total, c0, c1, rl, dq, num, den);
+    gave_up = __any_sync(0xffffffffu, gave_up);
+    if (dq >= D / 4 || (fits && !there)) return;
+    if (!fits || gave_up) {
+        for (int i = 0; i < 4; ++i) store_out(a, at + i, nanf(""));
+        return;
+    }
+    if (c0 == c1) return;  // finished by its one CTA
+    if (den == 0.f) den = 1.f;  // a row that sees nothing: 0
+#pragma unroll
+    for (int k = 0; k < 4; ++k) num[k] /= den;
+    uint2 o;
+    if (a.dtype == QW_DT_F16) o = make_uint2(pack2<false>(num[0], num[1]), pack2<false>(num[2], num[3]));
+    else o = make_uint2(pack2<true>(num[0], num[1]), pack2<true>(num[2], num[3]));
+    *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(a.out) + at) = o;
+}
+
+template <int D>
+cudaError_t launch_prefix_dim(const Prefix &p, const qw_kv_view &prefix, const qw_kv_view &kv, int ctas, cudaStream_t st, bool chained) {
+    const cudaError_t e = launch_dim<D>(p, kv, &prefix, ctas, st, chained);
+    if (e != cudaSuccess) return e;
+    const int rows = p.n_seq * p.a.n_max * p.a.G, units = std::min(kTcRows, rows) * (D / 4);
+    return launch_k(true, prefix_tc_merge_kernel<D>, dim3((rows + kTcRows - 1) / kTcRows, p.a.Hkv, (units + kMergeThreads - 1) / kMergeThreads),
+                    dim3(kMergeThreads), 0, st, p, ctas);
+}
+
+size_t starts_bytes(int64_t rows) { return (((rows + kTcRows - 1) / kTcRows + 1) * 8 + 255) / 256 * 256; }
+
+}  // namespace
+
+size_t prefix_tc_scratch_bytes(int64_t rows, int head_dim) {
+    return starts_bytes(rows) + tree_tc_scratch_bytes((int)std::min<int64_t>(rows, kTcRows), head_dim);
+}
+
+cudaError_t launch_prefix_tc(const PrefixArgs &a, const qw_kv_view &prefix, const qw_kv_view &kv, int max_len, int max_prefix,
+                             void *scratch, cudaStream_t st, bool chained) {
+    Prefix p{};
+    const int rows = kv.n_seq * a.n_max * a.G;
+    p.a = a;
+    p.n_seq = kv.n_seq;
+    p.rows_max = slot_rows(rows);
+    p.inv_g = a.inv_g;
+    p.starts = (long long *)scratch;
+    uint8_t *rest = (uint8_t *)scratch + starts_bytes(rows);
+    p.status = (int *)rest;
+    p.part = (float *)(rest + kTcStatusBytes);
+    const long long nrt = (rows + kTcRows - 1) / kTcRows;
+    const long long tiles = kv.n_kv_heads * (nrt * ((max_prefix + kTcTile - 1) / kTcTile) +
+                                             (long long)kv.n_seq * ((max_len + a.n_max + kTcTile - 1) / kTcTile));
+    const int ctas = (int)std::min<long long>(kTcCtas, tiles);
+    return kv.head_dim == 128 ? launch_prefix_dim<128>(p, prefix, kv, ctas, st, chained)
+                              : launch_prefix_dim<64>(p, prefix, kv, ctas, st, chained);
+}
+
+}  // namespace qw

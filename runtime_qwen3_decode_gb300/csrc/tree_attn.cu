@@ -484,7 +484,8 @@ size_t prefix_attn_scratch_bytes(const qw_kv_view &kv, int n_max, int n_heads, i
     const int64_t Sp = std::min(pre, most / (kv.n_kv_heads * ((all + 31) / 32)) + 1);
     const int64_t So = std::min(own, most / (kv.n_kv_heads * ((rows + 31) / 32) * kv.n_seq) + 1);
     if (plan_prefix(kv.n_seq, kv.n_kv_heads, n_max, n_heads / kv.n_kv_heads, max_len, max_prefix).blocks > INT32_MAX) return 0;
-    return ((size_t)(all * kv.n_kv_heads * (Sp + So)) * (kv.head_dim + 2) * 4 + 255) / 256 * 256;
+    const size_t cores = ((size_t)(all * kv.n_kv_heads * (Sp + So)) * (kv.head_dim + 2) * 4 + 255) / 256 * 256;
+    return std::max(cores, prefix_tc_scratch_bytes(all, kv.head_dim));
 }
 
 cudaError_t launch_prefix_attn(const qw_kv_view &prefix, const qw_kv_view &kv, const qw_tree_attention_args &t,
@@ -504,6 +505,7 @@ cudaError_t launch_prefix_attn(const qw_kv_view &prefix, const qw_kv_view &kv, c
     a.inv_rows = (1ull << 32) / (a.n_max * a.G) + 1;
     a.inv_g = (1ull << 32) / a.G + 1;
     const PrefixPlan p = plan_prefix(kv.n_seq, kv.n_kv_heads, t.n_max, a.G, t.max_len, max_prefix);
+    if (t.dtype != QW_DT_F32) return launch_prefix_tc(a, prefix, kv, t.max_len, max_prefix, scratch, st, chained);
     a.row_tiles = p.row_tiles, a.p_row_tiles = p.p_row_tiles;
     a.Sp = p.Sp, a.S = p.S, a.p_blocks = (int)p.p_blocks;
     return kv.format == QW_KV_F32    ? launch_prefix_dim<float>(a, p, kv.head_dim, st, chained)

@@ -78,5 +78,8 @@ static_assert(kTcCtas * 4 <= kTcStatusBytes, "status words");
 size_t tree_tc_scratch_bytes(int rows, int head_dim);
 cudaError_t launch_tree_tc(const TreeArgs &a, const qw_kv_view &kv, int max_len, void *scratch, cudaStream_t st,
                            bool chained);
+size_t prefix_tc_scratch_bytes(int64_t rows, int head_dim);
+cudaError_t launch_prefix_tc(const PrefixArgs &a, const qw_kv_view &prefix, const qw_kv_view &kv, int max_len, int max_prefix,
+                             void *scratch, cudaStream_t st, bool chained);
 
 }  // namespace qw
