@@ -43,8 +43,10 @@
 // own tile costs the tensor cores what any tile does, though only its rows see it (the others' weights are 0, and warps
 // without any of its rows do no softmax), but its bytes are read once and the stream of tiles never stops: with the own parts as
 // items of their own, every one of them began with a wait for its queries and ended with an epilogue.  What is not finite in
-// an own tile's V must not reach the other sequences' rows as 0 x NaN: it is taken out of every own tile as above, bf16 tiles
-// being looked through by two warps (8 and 9) that have nothing else to do there.
+// an own tile's V must not reach the other sequences' rows as 0 x NaN.  Looking every own tile through for it took three times as
+// long as the tile otherwise needs (6,600 cycles instead of XX), so a CTA does its share without looking, and where a row's
+// accumulator comes out not finite does it all again, with such elements taken out as above (bf16 tiles by warps 8 and 9, which
+// zero the rows behind an end in the first pass).
 //
 // Every wait is bounded (1 s); a CTA whose wait expired says so in its status word and the
 // merge kernel then fills every output row with NaN.
@@ -377,17 +379,20 @@ template <>
 struct Walk<true> {
     int b, pos, len, end, b1, next_len, next_n;
     bool pre;
-    __device__ __forceinline__ void look(const Prefix &p) {  // at the sequence behind b
-        next_n = 0;
-        if (b < b1 && !lengths(p.a, b + 1, next_len, next_n)) next_n = 0;
+    __device__ __forceinline__ void look(const Prefix &p) {  // at the sequence behind b: loads whose values nothing needs yet
+        const int i = min(b + 1, b1);
+        next_len = p.a.len[i];
+        next_n = p.a.count ? p.a.count[i] : p.a.n_max;
     }
     __device__ __forceinline__ void step(const Prefix &p) {  // to the next sequence with rows
         int n;
+        bool is;
         do {
             ++b;
             len = next_len, n = next_n;
             look(p);
-        } while (n == 0 && b < b1);
+            is = n > 0 && n <= p.a.n_max && len >= 0 && len <= p.a.max_ctx - n;
+        } while (!is && b < b1);
         pre = false, pos = 0, end = len + n;
     }
     __device__ __forceinline__ void start(const Prefix &p, const Seg &s) {
@@ -551,6 +556,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
     int *bad_seg = reinterpret_cast<int *>(bars + 40);  // [4]: 1 + the segment that last set it
     uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + 42);
     volatile int *abort = reinterpret_cast<volatile int *>(tslot + 1);
+    volatile int *redo = abort + 1;  // PREFIX: a row of the first pass is not finite
     float *row_scale = reinterpret_cast<float *>(base + C::kBar + 512);
     unsigned *own = reinterpret_cast<unsigned *>(base + C::kBar + 512 + kTcRows * 4);  // PREFIX: [kOwnTable]
     uint64_t *v_ready = bars + 21;  // PREFIX, bf16 tiles from TMA (which have no ring): looked through
@@ -580,6 +586,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
             for (int i = 0; i < ST; ++i) mbar_init(&v_ready[i], 2);
         for (int i = 0; i < 4; ++i) bad_seg[i] = 0;
         *abort = 0;
+        *redo = 0;
         mbar_fence_init();
     }
     if (warp == kMmaWarp) tmem_alloc(tslot, 512);
@@ -607,18 +614,25 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
     tc_fence_after();
     chain_release();
     const uint32_t tmem = *tslot;
-    Cursor cur = *start;
     Seg s;
     Walk<PREFIX> w;
+    bool ok = true;
+    // What a role has done so far: tiles (they give the phases of the barriers), segments; PREFIX, bf16: phase of each stage's v_ready
+    int it = 0, seg = 0;
+    unsigned looked = 0;
+
+#pragma unroll 1
+    for (int pass = 0; pass < (PREFIX ? 2 : 1); ++pass) {
+    Cursor cur = *start;
+    const bool careful_pass = PREFIX && pass > 0;
+    const bool look = !PREFIX || careful_pass;  // drafted (PREFIX: and own) rows for what is not finite
 
     if (warp == kLoadWarp) {
         if (lane == 0) {
             // ---- loads
-            bool ok = true;
             if constexpr (C::kDirect) {
                 int kp[ST], vp[ST];
                 for (int i = 0; i < ST; ++i) kp[i] = vp[i] = -1;
-                int it = 0;
                 while (ok && next_seg(p, cur, s, own)) {
                     w.start(p, s);
                     for (int t = s.t0; ok && t < s.t1; ++t, ++it) {
@@ -653,7 +667,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                 }
             } else {
                 int rp[4] = {-1, -1, -1, -1};
-                int i0 = 0;  // chunks per plane of the tiles before; chunk i of a plane goes to the plane's slot i & 1
+                int i0 = it;  // chunks per plane of the tiles before; chunk i of a plane goes to the plane's slot i & 1
                 while (ok && next_seg(p, cur, s, own)) {
                     w.start(p, s);
                     for (int t = s.t0; ok && t < s.t1; ++t, i0 += C::kChunks) {
@@ -676,6 +690,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                         }
                     }
                 }
+                it = i0;
                 if (!ok) *abort = 1;
                 for (int i = 0; i < C::kRing; ++i)
                     if (rp[i] >= 0) mbar_sleep(&r_full[i], (unsigned)rp[i], abort, false, kWaitLimitNs);
@@ -709,9 +724,6 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                 mma_commit(&s_full[jn & 1]);
                 mma_commit(&k_empty[st]);
             };
-            bool ok = true;
-            unsigned looked = 0;  // PREFIX, bf16: phase of each stage's v_ready
-            int it = 0, seg = 0;  // it: tiles before this segment
             while (ok && next_seg(p, cur, s, own)) {
                 const int nt = s.t1 - s.t0;
                 ok = mbar_sleep(q_full, (unsigned)seg & 1u, abort, true, kWaitLimitNs);
@@ -733,7 +745,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                         break;
                     }
                     if constexpr (PREFIX && C::kDirect) {
-                        if (s.t0 + j >= s.len / kTcTile) {
+                        if (s.t0 + j >= s.len / kTcTile) {  // not a whole tile of the prefix
                             if (!mbar_sleep(&v_ready[st], looked >> st & 1u, abort, true, kWaitLimitNs)) {
                                 ok = false;
                                 break;
@@ -759,15 +771,13 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
             }
             if (!ok) *abort = 1;
             mma_commit(drain);  // every MMA completes before TMEM is released
-            mbar_sleep(drain, 0, abort, false, kWaitLimitNs);
+            mbar_sleep(drain, (unsigned)pass & 1u, abort, false, kWaitLimitNs);
         }
     } else if (warp < kSoftWarps) {
         // ---- softmax and epilogue: group grp, TMEM lane quarter q, one query row per lane
         const int grp = warp >> 2, q = warp & 3, r = 32 * q + lane;
         const uint32_t lb = (uint32_t)(32 * q) << 16;
         const uint32_t tS = tmem + lb + 128u * grp, tO = tmem + kColO + lb + 128u * grp;
-        bool ok = true;
-        int it = 0, seg = 0;
         while (ok && next_seg(p, cur, s, own)) {
             const int row = s.r0 + r, nt = s.t1 - s.t0, nr = min(kTcRows, s.rows - s.r0);
             bool live = r < nr;
@@ -865,7 +875,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                 const int first = w.pos;
                 // rows of other sequences see nothing of a sequence's own tile
                 const bool sees = !PREFIX || w.pre || w.b == mb_;
-                const bool tail = first + kTcTile > w.len || (PREFIX && !w.pre);
+                const bool tail = first + kTcTile > w.len;
                 const unsigned long long seen = PREFIX && w.pre ? 0ull : mask;
                 bool busy = warp_live;
                 if constexpr (PREFIX) busy = __any_sync(0xffffffffu, live && sees);
@@ -883,7 +893,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                     if (tail) {
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
-                            const uint32_t vis = sees ? visible(seen, first + 32 * c - w.len) : 0u;
+                            const uint32_t vis = visible(seen, first + 32 * c - w.len);
                             float v[32];
                             tmem_ld32(tS + 32u * c, v);
 #pragma unroll
@@ -911,6 +921,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                             mb = fmaxf(mb, m1);
                         }
                     }
+                    if (PREFIX && !sees) mb = -INFINITY;
                     mb *= sc;
                     const bool resc = mb > m_used + C::kLag;
                     const float m_new = resc ? mb : m_used;
@@ -931,7 +942,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                     // P over the scores: block c's 16 columns end before block c + 1's scores begin
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
-                        const uint32_t vis = !sees ? 0u : tail ? visible(seen, first + 32 * c - w.len) : 0xffffffffu;
+                        const uint32_t vis = tail ? visible(seen, first + 32 * c - w.len) : 0xffffffffu;
                         float v[32];
                         tmem_ld32(tS + 32u * c, v);
 #pragma unroll
@@ -943,6 +954,10 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                         if (vis != 0xffffffffu) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i) v[i] = (vis >> i) & 1u ? v[i] : 0.f;
+                        }
+                        if constexpr (PREFIX) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = sees ? v[i] : 0.f;
                         }
                         uint32_t pk[16];
                         float2 l2 = make_float2(0.f, 0.f);
@@ -1052,6 +1067,14 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                         }
                     }
                     if (!live) continue;
+                    if constexpr (PREFIX) {
+                        if (pass == 0 && m != -INFINITY) {  // NaN if one of them is not finite
+                            float2 probe = make_float2(0.f, 0.f);
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) probe = __ffma2_rn(make_float2(o[i], o[i + 1]), make_float2(0.f, 0.f), probe);
+                            if (!(probe.x + probe.y == 0.f)) *redo = 1;
+                        }
+                    }
                     if (!whole) {
                         if (PREFIX && m == -INFINITY) continue;  // nothing seen: the merge does not look at it
 #pragma unroll
@@ -1084,15 +1107,13 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
         const int plane = cw / kPlaneWarps, ct = (cw % kPlaneWarps) * 32 + lane;
         uint64_t *full = plane ? v_full : k_full, *empty = plane ? v_empty : k_empty;
         uint8_t *operand = plane ? sV : sK;
-        bool ok = true;
-        int it = 0, seg = 0;
         // Eight elements of position `pos` (o: fp16, rest: second term) into their 16-byte chunk.
         auto put = [&](uint8_t *at, uint4 o, uint4 rest, auto checked, int pos) {
             bool any = false;
             if constexpr (decltype(checked)::value) {  // V rows of the sequence's end
                 if (pos >= w.end) {
                     o = rest = make_uint4(0u, 0u, 0u, 0u);
-                } else if (pos >= (PREFIX ? w.pre ? w.end : 0 : w.len) && only_finite<C::kBf16>(o)) {
+                } else if (look && pos >= (PREFIX ? w.pre ? w.end : 0 : w.len) && only_finite<C::kBf16>(o)) {
                     any = true;
                     only_finite<C::kBf16>(rest);  // not finite where o was not
                 }
@@ -1151,7 +1172,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                 for (int t = s.t0; ok && t < s.t1; ++t, ++it) {
                     if (t > s.t0) w.next(p);
                     const int st = it % ST, slot = 2 * plane + (it & 1);
-                    const bool check = plane && (w.pos + kTcTile > w.len || (PREFIX && !w.pre));
+                    const bool check = plane && (w.pos + kTcTile > (PREFIX ? w.end : w.len) || (careful_pass && !w.pre));
                     __half2 s2[U];
                     bool over = false;  // codes times a scale above 65504 / 127 may be infinite
 #pragma unroll
@@ -1232,7 +1253,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                 for (int t = s.t0; ok && t < s.t1; ++t, ++it) {
                     if (t > s.t0) w.next(p);
                     const int st = it % ST;
-                    const bool check = plane && (w.pos + kTcTile > w.len || (PREFIX && !w.pre));
+                    const bool check = plane && (w.pos + kTcTile > (PREFIX ? w.end : w.len) || (careful_pass && !w.pre));
                     for (int ch = 0; ch < C::kChunks; ++ch) {
                         const int i = it * C::kChunks + ch, slot = 2 * plane + (i & 1), crow = ch * C::kChunkRows;
                         if ((ch == 0 && !warp_wait(&empty[st], ((unsigned)(it / ST) & 1u) ^ 1u, abort)) ||
@@ -1287,10 +1308,8 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
         }
         if (!ok && lane == 0) *abort = 1;
     } else if constexpr (PREFIX) {
-        // ---- bf16 tiles that TMA wrote: V rows behind the end are zeroed, and what is not finite in a sequence's own rows.  Warps 8
-        // and 9, half of the rows each; eight chunks of a row at once, so that a tile takes less time than its copy.
-        bool ok = true;
-        int it = 0, seg = 0;
+        // ---- bf16 tiles that TMA wrote: V rows behind the end are zeroed, and in the second pass what is not finite in a sequence's
+        // own rows.  Warps 8 and 9, half of the rows each.
         while (ok && next_seg(p, cur, s, own)) {
             w.start(p, s);
             for (int t = s.t0; ok && t < s.t1; ++t, ++it) {
@@ -1304,24 +1323,19 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                 if (t < s.len / kTcTile) continue;  // a whole tile of the prefix: every row sees it
                 bool any = false;
                 constexpr int CH = D / 8;  // chunks of a row
+                const int half = (warp - kSoftWarps) * (kTcTile / 2), r0 = careful_pass && !w.pre ? half : max(half, w.end - w.pos);
 #pragma unroll 1
-                for (int x0 = (warp - kSoftWarps) * (kTcTile / 2) * CH; x0 < (warp - kSoftWarps + 1) * (kTcTile / 2) * CH; x0 += 8 * 32) {
-                    uint4 u[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int x = x0 + 32 * k + lane, row = x / CH, c = x % CH;
-                        u[k] = *reinterpret_cast<const uint4 *>(sV + st * C::kOperand + (c >> 3) * C::kRegion + swz128(row, c & 7));
+                for (int x = r0 * CH + lane; x < (half + kTcTile / 2) * CH; x += 32) {
+                    const int row = x / CH, c = x % CH;
+                    uint4 *at = reinterpret_cast<uint4 *>(sV + st * C::kOperand + (c >> 3) * C::kRegion + swz128(row, c & 7));
+                    uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                    bool write = w.pos + row >= w.end;
+                    if (!write) {
+                        u = *at;
+                        write = only_finite<true>(u);
+                        any |= write;
                     }
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int x = x0 + 32 * k + lane, row = x / CH, c = x % CH;
-                        const bool behind = w.pos + row >= w.end;
-                        bool hit = false;
-                        if (behind) u[k] = make_uint4(0u, 0u, 0u, 0u);
-                        else if (!w.pre) hit = only_finite<true>(u[k]);
-                        if (behind || hit) *reinterpret_cast<uint4 *>(sV + st * C::kOperand + (c >> 3) * C::kRegion + swz128(row, c & 7)) = u[k];
-                        any |= hit;
-                    }
+                    if (write) *at = u;
                 }
                 if (any) bad_seg[seg & 3] = seg + 1;
                 fence_async_shared();
@@ -1331,6 +1345,11 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
             ++seg;
         }
         if (!ok && lane == 0) *abort = 1;
+    }
+    if constexpr (PREFIX) {
+        __syncthreads();  // every row of the pass is finished
+        if (!*redo || *abort) break;
+    }
     }
     tc_fence_before();
     __syncthreads();
