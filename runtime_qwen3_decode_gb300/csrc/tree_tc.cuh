@@ -877,6 +877,8 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                 const bool sees = !PREFIX || w.pre || w.b == mb_;
                 const bool tail = first + kTcTile > w.len;
                 const unsigned long long seen = PREFIX && w.pre ? 0ull : mask;
+                // blocks of 32 columns up to the end (a sequence's last tile may hold few)
+                const int blocks = PREFIX ? min(4, (w.end - first + 31) >> 5) : 4;
                 bool busy = warp_live;
                 if constexpr (PREFIX) busy = __any_sync(0xffffffffu, live && sees);
                 if (PREFIX && warp_live && !busy) {
@@ -892,7 +894,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                     float mb = -INFINITY;
                     if (tail) {
 #pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
+                        for (int c = 0; c < blocks; ++c) {
                             const uint32_t vis = visible(seen, first + 32 * c - w.len);
                             float v[32];
                             tmem_ld32(tS + 32u * c, v);
@@ -941,7 +943,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                     const float mm = m_used == -INFINITY ? 0.f : m_used - C::kLift;  // nothing seen yet: every weight 2^-inf
                     // P over the scores: block c's 16 columns end before block c + 1's scores begin
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < blocks; ++c) {
                         const uint32_t vis = tail ? visible(seen, first + 32 * c - w.len) : 0xffffffffu;
                         float v[32];
                         tmem_ld32(tS + 32u * c, v);
@@ -968,6 +970,13 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                         }
                         l += l2.x + l2.y;
                         tmem_st16u(tS + 16u * c, pk);
+                    }
+                    if constexpr (PREFIX) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) pk[i] = 0u;
+#pragma unroll 1
+                        for (int c = blocks; c < 4; ++c) tmem_st16u(tS + 16u * c, pk);
                     }
                 }
                 if constexpr (C::kDirect && !PREFIX) {
@@ -1323,19 +1332,19 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                 if (t < s.len / kTcTile) continue;  // a whole tile of the prefix: every row sees it
                 bool any = false;
                 constexpr int CH = D / 8;  // chunks of a row
-                const int half = (warp - kSoftWarps) * (kTcTile / 2), r0 = careful_pass && !w.pre ? half : max(half, w.end - w.pos);
-#pragma unroll 1
-                for (int x = r0 * CH + lane; x < (half + kTcTile / 2) * CH; x += 32) {
-                    const int row = x / CH, c = x % CH;
-                    uint4 *at = reinterpret_cast<uint4 *>(sV + st * C::kOperand + (c >> 3) * C::kRegion + swz128(row, c & 7));
-                    uint4 u = make_uint4(0u, 0u, 0u, 0u);
-                    bool write = w.pos + row >= w.end;
-                    if (!write) {
-                        u = *at;
-                        write = only_finite<true>(u);
-                        any |= write;
+                // rows alternate between the two warps; TMA has zeroed the ones behind the cache
+                const int r1 = min(kTcTile, (w.pre ? a.p_max : a.max_ctx) - w.pos), r0 = careful_pass && !w.pre ? 0 : w.end - w.pos;
+                const int sub = lane / CH, c = lane % CH;
+                uint8_t *column = sV + st * C::kOperand + (c >> 3) * C::kRegion;
+#pragma unroll 4
+                for (int row = r0 + (32 / CH) * (warp - kSoftWarps) + sub; row < r1; row += 2 * (32 / CH)) {
+                    uint4 *at = reinterpret_cast<uint4 *>(column + swz128(row, c & 7));
+                    if (w.pos + row >= w.end) {
+                        *at = make_uint4(0u, 0u, 0u, 0u);
+                    } else {
+                        uint4 u = *at;
+                        if (only_finite<true>(u)) *at = u, any = true;
                     }
-                    if (write) *at = u;
                 }
                 if (any) bad_seg[seg & 3] = seg + 1;
                 fence_async_shared();
