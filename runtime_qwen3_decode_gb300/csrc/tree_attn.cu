@@ -407,6 +407,7 @@ cudaError_t launch_rt(const TreeArgs &a, int n_seq, int rt, cudaStream_t st, boo
 struct PrefixPlan {
     int rt, row_tiles, p_row_tiles, Sp, S;
     int64_t p_blocks, blocks;
+    double ns;   // about what its tiles cost
 };
 PrefixPlan plan_prefix(int n_seq, int Hkv, int n_max, int G, int max_len, int max_prefix) {
     const int64_t rows = (int64_t)n_max * G, all = rows * n_seq;
@@ -422,9 +423,25 @@ PrefixPlan plan_prefix(int n_seq, int Hkv, int n_max, int G, int max_len, int ma
         // splits: up to four CTAs for every SM, none shorter than a tile
         const int64_t share = std::max<int64_t>(1, (tiles + 4 * 152 - 1) / (4 * 152));
         const int64_t Sp = (pre + share - 1) / share, So = (own + share - 1) / share;
-        best = {rt, (int)rt_own, (int)rt_pre, (int)Sp, (int)(Sp + So), Sp * rt_pre * Hkv, Sp * rt_pre * Hkv + So * rt_own * Hkv * n_seq};
+        best = {rt, (int)rt_own, (int)rt_pre, (int)Sp, (int)(Sp + So), Sp * rt_pre * Hkv, Sp * rt_pre * Hkv + So * rt_own * Hkv * n_seq, cost};
     }
     return best;
+}
+
+// Whether a call with 16-bit queries is better off on the CUDA cores: by estimates of both times that follow what was measured (us,
+// CUDA cores : tensor cores, 8 KV heads of two query heads of 128 dims, one row per sequence).  bf16 beside bf16: one sequence of 100
+// positions behind a prefix of 2048 9.5 : 15, of 16384 33 : 24; 8 sequences of 64 behind 512 13 : 14, of 100 behind 2048
+// 24 : 18; 32 of 16 behind 64 14 : 17.  fp16 over 8-bit rows: 8 of 100 behind 2048 26 : 25, of 300 behind 4096 41 : 28.
+// fp16 over f32 rows, whose tiles cost the tensor cores most: 8 of 100 behind 2048 25 : 26, of 300 behind 4096 40 : 31; 32 of
+// 400 behind 512 58 : 61.
+bool small_prefix_call(const qw_kv_view &kv, const qw_tree_attention_args &t, const PrefixPlan &p, int max_prefix) {
+    const bool f16 = t.dtype == QW_DT_F16;
+    const int64_t rows = (int64_t)kv.n_seq * t.n_max * (t.n_heads / kv.n_kv_heads);
+    const double tiles = (double)kv.n_kv_heads * ((double)((rows + kTcRows - 1) / kTcRows) * ((max_prefix + kTcTile - 1) / kTcTile) +
+                                                  (double)kv.n_seq * ((t.max_len + t.n_max + kTcTile - 1) / kTcTile));
+    const double start = kv.format == QW_KV_F32 ? 10.7 : kv.format == QW_KV_INT8_G32 ? 14.1 : f16 ? 12.9 : 13.5;  // us
+    const double wave = kv.format == QW_KV_F32 ? 6.9 : kv.format == QW_KV_INT8_G32 ? (f16 ? 4.5 : 2.8) : f16 ? 2.9 : 1.8;
+    return 6. + 0.25 * p.rt + p.ns * 1e-3 < start + wave * std::max(1., tiles / kTcCtas);
 }
 
 template <typename KV, int D, int RT>
@@ -505,7 +522,8 @@ cudaError_t launch_prefix_attn(const qw_kv_view &prefix, const qw_kv_view &kv, c
     a.inv_rows = (1ull << 32) / (a.n_max * a.G) + 1;
     a.inv_g = (1ull << 32) / a.G + 1;
     const PrefixPlan p = plan_prefix(kv.n_seq, kv.n_kv_heads, t.n_max, a.G, t.max_len, max_prefix);
-    if (t.dtype != QW_DT_F32) return launch_prefix_tc(a, prefix, kv, t.max_len, max_prefix, scratch, st, chained);
+    if (t.dtype != QW_DT_F32 && !small_prefix_call(kv, t, p, max_prefix))
+        return launch_prefix_tc(a, prefix, kv, t.max_len, max_prefix, scratch, st, chained);
     a.row_tiles = p.row_tiles, a.p_row_tiles = p.p_row_tiles;
     a.Sp = p.Sp, a.S = p.S, a.p_blocks = (int)p.p_blocks;
     return kv.format == QW_KV_F32    ? launch_prefix_dim<float>(a, p, kv.head_dim, st, chained)

@@ -21,6 +21,14 @@ def qw():
     return binding
 
 
+ROOM = 60000  # the hint of a prefix of this length sends 16-bit queries to the tensor cores
+
+
+def make_prefix(kind, shape, g, tc):
+    """A prefix's cache; tc: with room for the hint of a long one."""
+    return make_cache(kind, (shape[0], shape[1], max(shape[2], ROOM) if tc else shape[2], shape[3]), g)
+
+
 def joined(pre, own, P):
     """The caches [prefix | own] of every sequence."""
     B = own[0].shape[0]
@@ -54,28 +62,38 @@ def run(qw, B, H, G, D, n, P, lens, counts, dt, kind, seed=0, layout="head", max
 
 @pytest.mark.parametrize("dt,kind", TYPES)
 @pytest.mark.parametrize("H,G,D", [(8, 2, 128), (2, 7, 64), (3, 1, 128), (8, 2, 64), (1, 64, 64)])
-def test_types_and_heads(qw, dt, kind, H, G, D):
-    run(qw, 3, H, G, D, 5, 260, [130, 0, 77], [5, 2, 1], dt, kind)
+@pytest.mark.parametrize("max_prefix", [None, 20000])
+def test_types_and_heads(qw, dt, kind, H, G, D, max_prefix):
+    run(qw, 3, H, G, D, 5, 260, [130, 0, 77], [5, 2, 1], dt, kind, max_prefix=max_prefix, room=20000 if max_prefix else 7)
 
 
 @pytest.mark.parametrize("dt,kind", TYPES)
 @pytest.mark.parametrize("P,L", [(0, 0), (0, 5), (1, 0), (1, 1), (63, 1), (64, 64), (65, 127), (127, 128), (128, 129), (500, 0), (2100, 300)])
-def test_lengths(qw, dt, kind, P, L):
-    run(qw, 4, 2, 2, 128, 1, P, [L, 0, L // 2, L], None, dt, kind, chain=True)
+@pytest.mark.parametrize("max_prefix", [None, 40000])
+def test_lengths(qw, dt, kind, P, L, max_prefix):
+    run(qw, 4, 2, 2, 128, 1, P, [L, 0, L // 2, L], None, dt, kind, chain=True, max_prefix=max_prefix, room=40000 if max_prefix else 7)
 
 
-@pytest.mark.parametrize("dt,kind", [(F32, "f32"), (BF16, "bf16"), (F16, "int8"), (F16, "f32")])
+@pytest.mark.parametrize("max_prefix", [None, 30000])  # the hint of a long prefix sends 16-bit queries to the tensor cores
+@pytest.mark.parametrize("dt,kind", [(F32, "f32"), (BF16, "bf16"), (F16, "int8"), (F16, "f32"), (F16, "bf16"), (BF16, "int8"), (BF16, "f32")])
 @pytest.mark.parametrize("B,n", [(1, 1), (2, 1), (63, 1), (64, 1), (65, 1), (130, 1), (5, 13), (7, 64), (43, 3), (3, 33)])
-def test_rows_over_tiles(qw, dt, kind, B, n):
+def test_rows_over_tiles(qw, dt, kind, B, n, max_prefix):
     """Rows of a sequence within one tile of rows, across two and across many."""
     rng = np.random.default_rng(B * n)
-    run(qw, B, 2, 2, 64, n, 333, rng.integers(0, 200, B).tolist(), rng.integers(0, n + 1, B).tolist(), dt, kind, seed=n)
+    run(qw, B, 2, 2, 64, n, 333, rng.integers(0, 200, B).tolist(), rng.integers(0, n + 1, B).tolist(), dt, kind, seed=n,
+        max_prefix=max_prefix, room=30000 if max_prefix else 7)
 
 
 @pytest.mark.parametrize("dt,kind", TYPES)
 def test_long_prefix_many_sequences(qw, dt, kind):
     rng = np.random.default_rng(3)
     run(qw, 40, 4, 2, 128, 1, 9001, rng.integers(0, 700, 40).tolist(), None, dt, kind, chain=True)
+
+
+@pytest.mark.parametrize("dt,kind", TYPES[3:])
+@pytest.mark.parametrize("B,n,P,L", [(1, 1, 9000, 50), (8, 1, 600, 60), (8, 1, 4096, 300), (32, 1, 512, 400), (8, 4, 64, 16), (3, 2, 20000, 1)])
+def test_both_sides_of_the_small_call(qw, dt, kind, B, n, P, L):
+    run(qw, B, 8, 2, 128, n, P, [L] * B, None, dt, kind, chain=True)
 
 
 @pytest.mark.parametrize("dt,kind", [(F32, "int8"), (BF16, "bf16"), (F16, "int8"), (BF16, "f32")])
@@ -102,13 +120,14 @@ def test_without_a_prefix_it_is_tree_attention(qw, dt, kind):
     assert ((a - b).abs() <= 2 * U[dt] * a.abs() + (2 * U[dt] + 300 * 2.0 ** -24) * float(a.abs().max())).all()
 
 
+@pytest.mark.parametrize("tc", [False, True])
 @pytest.mark.parametrize("dt,kind", TYPES)
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
-def test_sequences_do_not_reach_one_another(qw, dt, kind, bad):
+def test_sequences_do_not_reach_one_another(qw, tc, dt, kind, bad):
     """What one sequence holds, and what stands behind the prefix and the sequences, reaches no other."""
     B, H, D, n, P = 6, 2, 128, 3, 200
     g = gen(11)
-    pre, own = make_cache(kind, (1, H, P + 60, D), g), make_cache(kind, (B, H, 340, D), g)
+    pre, own = make_prefix(kind, (1, H, P + 60, D), g, tc), make_cache(kind, (B, H, 340, D), g)
     q = torch.randn((B, n, 4, D), generator=g, device="cuda").to(dt)
     lens, counts = [300, 0, 150, 128, 64, 333], [3, 3, 2, 3, 1, 3]
     mask = torch.from_numpy(np.stack([qw.tree_mask([-1, 0, 0])] * B).view(np.int64)).cuda()
@@ -130,11 +149,12 @@ def test_sequences_do_not_reach_one_another(qw, dt, kind, bad):
                 assert torch.equal(got[b, i], clean[b, i]), (b, i)
 
 
+@pytest.mark.parametrize("tc", [False, True])
 @pytest.mark.parametrize("dt,kind", [(F32, "f32"), (BF16, "bf16"), (BF16, "int8"), (F16, "f32"), (F16, "int8")])
-def test_one_bad_value_of_a_cached_v_row(qw, dt, kind):
+def test_one_bad_value_of_a_cached_v_row(qw, tc, dt, kind):
     """An element of one sequence's V that is not finite: the others keep their results, its own rows lose that element."""
     g = gen(12)
-    pre, own = make_cache(kind, (1, 1, 300, 128), g), make_cache(kind, (3, 1, 200, 128), g)
+    pre, own = make_prefix(kind, (1, 1, 300, 128), g, tc), make_cache(kind, (3, 1, 200, 128), g)
     q = torch.randn((3, 1, 2, 128), generator=g, device="cuda").to(dt)
     args = (qw.KvView(*pre), qw.KvView(*own), q, i32(190, 150, 20), i32(290))
     clean = qw.prefix_attention(*args).clone()
@@ -149,10 +169,11 @@ def test_one_bad_value_of_a_cached_v_row(qw, dt, kind):
     assert torch.equal(got[0], clean[0]) and torch.equal(got[2], clean[2])
 
 
+@pytest.mark.parametrize("tc", [False, True])
 @pytest.mark.parametrize("dt,kind", [(F32, "f32"), (BF16, "bf16"), (BF16, "int8"), (F16, "f32")])
-def test_rows_that_see_nothing(qw, dt, kind):
+def test_rows_that_see_nothing(qw, tc, dt, kind):
     g = gen(13)
-    pre, own = make_cache(kind, (1, 2, 40, 128), g), make_cache(kind, (3, 2, 70, 128), g)
+    pre, own = make_prefix(kind, (1, 2, 40, 128), g, tc), make_cache(kind, (3, 2, 70, 128), g)
     q = torch.randn((3, 4, 4, 128), device="cuda").to(dt)
     mask = torch.zeros((3, 4), dtype=torch.int64, device="cuda")
     mask[:, 2] = 0b0100
@@ -169,25 +190,27 @@ def test_rows_that_see_nothing(qw, dt, kind):
         assert ((got[:, i].double() - v).abs() <= v.abs() * 2 * U[dt]).all()
 
 
+@pytest.mark.parametrize("tc", [False, True])
 @pytest.mark.parametrize("dt,kind", [(F32, "f32"), (BF16, "bf16"), (BF16, "int8"), (F16, "f32")])
-def test_lengths_that_do_not_fit_give_nan(qw, dt, kind):
+def test_lengths_that_do_not_fit_give_nan(qw, tc, dt, kind):
     g = gen(14)
-    pre, own = make_cache(kind, (1, 2, 40, 128), g), make_cache(kind, (6, 2, 40, 128), g)
+    pre, own = make_prefix(kind, (1, 2, 40, 128), g, tc), make_cache(kind, (6, 2, 40, 128), g)
     q = torch.randn((6, 4, 4, 128), device="cuda").to(dt)
     a = (qw.KvView(*pre), qw.KvView(*own), q, i32(-1, 37, 2**31 - 1, 0, 0, 36))
     got = qw.prefix_attention(*a, i32(40), counts=i32(4, 4, 4, 5, -1, 4), max_len=36)
     assert torch.isnan(got[:5]).all() and torch.isfinite(got[5]).all()
-    for bad in (-1, 41, 2**31 - 1):
+    for bad in (-1, pre[0].shape[2] + 1, 2**31 - 1):
         assert torch.isnan(qw.prefix_attention(*a, i32(bad), counts=i32(4, 4, 4, 5, -1, 4), max_len=36)).all()
 
 
+@pytest.mark.parametrize("tc", [False, True])
 @pytest.mark.parametrize("dt,kind", [(F32, "f32"), (BF16, "bf16"), (F16, "int8"), (BF16, "int8")])
 @pytest.mark.parametrize("scale", [0.0, -0.1, 3.0])
-def test_scales(qw, dt, kind, scale):
+def test_scales(qw, tc, dt, kind, scale):
     """Scores in the thousands (the maximum moves from tile to tile and most weights underflow), equal and negative ones."""
     B, H, D, n, P = 3, 2, 128, 2, 400
     g = gen(15)
-    pre, own = make_cache(kind, (1, H, P, D), g), make_cache(kind, (B, H, 300, D), g)
+    pre, own = make_prefix(kind, (1, H, P, D), g, tc), make_cache(kind, (B, H, 300, D), g)
     q = (torch.randn((B, n, 4, D), generator=g, device="cuda") * 3).to(dt)
     got = qw.prefix_attention(qw.KvView(*pre), qw.KvView(*own), q, i32(250, 3, 0), i32(P), scale=scale)
     mask = torch.full((B, n), 3, dtype=torch.int64, device="cuda")
