@@ -262,6 +262,24 @@ int qw_batch_prefill(qw_batch *b, int32_t seq, const int32_t *tokens_host, int32
  * QW_NUMERICAL_FAILURE, reported by the next synchronising call, after which the batch
  * refuses work until qw_batch_reset(b, -1). */
 int qw_batch_step(qw_batch *b, int32_t n_seq, const int32_t *tokens_host, int32_t *next_tokens_host);
+/*
+ * Continuations of one prompt: sequence dst forgets what it holds and takes positions 0 .. n - 1 of sequence src (1 <= n <= its
+ * length), from where it goes on by itself; if that is all of src, its last pick and logits too.  The rows are
+ * copied; sequences made from one another remember how many they have in common, and a qw_batch_step whose sequences
+ * all share 256 positions or more reads those once for all of them (qw_prefix_attention), until one of them is reset
+ * or forked anew.  Its results are then those of the prefix attention's arithmetic.
+ */
+int qw_batch_fork(qw_batch *b, int32_t src, int32_t dst, int32_t n);
+/*
+ * Draw the next tokens of sequences 0 .. n_seq - 1 from the logits of their last positions (of the last qw_batch_step
+ * or qw_batch_prefill of each, or what qw_batch_fork took over; QW_INVALID_ARGUMENT if one's are not there, after a
+ * tree step for instance) with the given random numbers u[s] and settings, as qw_sample_rows does; device arrays
+ * [n_seq], NULL: its defaults.  They take the place of the greedy picks: qw_batch_step(-1) goes on with them.  A row that
+ * draws nothing (a setting outside its range) keeps its pick and records QW_INVALID_ARGUMENT, reported as a non-finite
+ * logit is.  next_tokens_host [n_seq] (optional) receives the tokens and synchronises.
+ */
+int qw_batch_sample(qw_batch *b, int32_t n_seq, const float *u_dev, const float *temperature_dev, const int32_t *top_k_dev,
+                    const float *top_p_dev, const float *min_p_dev, int32_t *next_tokens_host);
 /* f32 logits [n_seq][vocab] of the last step (device), n = n_seq * vocab. */
 int qw_batch_logits(qw_batch *b, float *dst_dev, int64_t n);
 /* f32 [n_layers + 1][n_seq][hidden] residual stream of the last step (the model's

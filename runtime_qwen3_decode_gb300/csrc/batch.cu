@@ -15,6 +15,7 @@
 //   batch_head_kernel   final RMSNorm of the B rows, the tied lm_head streamed once for all of
 //                       them, logits [B][V] and one packed (logit, id) argmax key per sequence
 //   batch_pick_kernel   keys -> next tokens
+//   batch_take_kernel   drawn tokens -> next tokens
 //   batch_keep_kernel   the rows of an accepted path of drafted nodes to the end of the cache
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -530,6 +531,13 @@ __global__ void __launch_bounds__(32) batch_keep_kernel(const BatchKeep p) {
     }
 }
 
+__global__ void batch_take_kernel(const int32_t *drawn, int B, int32_t *picks, StepFlags *flags) {
+    const int b = threadIdx.x;
+    if (b >= B) return;
+    if (drawn[b] >= 0) picks[b] = drawn[b];
+    else atomicCAS(&flags->err, 0u, kErrInvalidArgument);
+}
+
 // tokens[b] = the caller's token, or (-1) this sequence's previous device-resident pick
 __global__ void batch_tokens_kernel(const int32_t *in, const int32_t *picks, int B, int32_t *tokens) {
     tc::chain_wait();
@@ -597,6 +605,10 @@ cudaError_t launch_bqkv_post(const BatchQkvPost &p, int kv_format, cudaStream_t 
 cudaError_t launch_batch_keep(const BatchKeep &p, cudaStream_t st) {
     if (p.n < 1 || p.n > kBatchMax) return cudaErrorInvalidValue;
     return launch_k(false, batch_keep_kernel, dim3(p.planes, 2), dim3(32), 0, st, p);
+}
+
+cudaError_t launch_batch_take(const int32_t *drawn, int B, int32_t *picks, StepFlags *flags, cudaStream_t st) {
+    return launch_k(false, batch_take_kernel, dim3(1), dim3(32), 0, st, drawn, B, picks, flags);
 }
 
 cudaError_t launch_batch_tokens(const int32_t *in, const int32_t *picks, int B, int32_t *tokens, cudaStream_t st,

@@ -1638,7 +1638,36 @@ int prefill_batch_step(PrefillState *st, const DecodeArgs &a, const BatchStep &b
             qp.vs = bs.vs + l * plane / kQGroup;
         }
         if (launch_bqkv_post(qp, bs.kv_format, stream, true) != cudaSuccess) return 1;
-        if (bs.mask) {
+        if (bs.prefix) {
+            // positions [0, prefix) of sequence 0 for all, then each sequence's own
+            const int P = bs.prefix;
+            const int64_t head = (int64_t)bs.max_ctx * kHeadDim, sp = kHeadDim / kQGroup;
+            qw_kv_view pre{kc,   vc,   qp.ks, qp.vs, bs.kv_format, 1, Hkv, kHeadDim, bs.max_ctx, (int64_t)bs.seq_elems,
+                           head, kHeadDim, (int64_t)bs.seq_elems / kQGroup, head / kQGroup, sp};
+            qw_kv_view own = pre;
+            own.k = kc + (size_t)P * kHeadDim * esz;
+            own.v = vc + (size_t)P * kHeadDim * esz;
+            if (q8) {
+                own.k_scale = qp.ks + P * sp;
+                own.v_scale = qp.vs + P * sp;
+            }
+            own.n_seq = B;
+            own.max_ctx = bs.max_ctx - P;
+            qw_tree_attention_args ta{};
+            ta.q = q16;
+            ta.out = o16;
+            ta.dtype = QW_DT_F16;
+            ta.n_max = 1;
+            ta.n_heads = Hq;
+            ta.max_len = bs.max_len;
+            ta.scale = 1.0f / sqrtf((float)kHeadDim);
+            ta.q_seq_stride = ta.q_node_stride = kHeadDim;
+            ta.q_head_stride = (int64_t)st->rows_max * kHeadDim;
+            ta.out_seq_stride = ta.out_node_stride = QD;
+            ta.out_head_stride = kHeadDim;
+            ta.len = bs.own_len;
+            if (launch_prefix_attn(pre, own, ta, bs.prefix_len, P, bs.attn_scratch, stream, true) != cudaSuccess) return 1;
+        } else if (bs.mask) {
             // a tree's nodes, or one node of each sequence over 8-bit caches
             const bool tree = bs.tree_len != nullptr;
             const qw_kv_view view{kc,

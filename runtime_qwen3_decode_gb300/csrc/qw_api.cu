@@ -695,6 +695,12 @@ struct qw_batch {
     int32_t *tree_picks = nullptr;                    // [8] greedy picks of a tree's nodes
     int32_t tree[qw::kBatchMax] = {};    // parents of the tree that waits for qw_batch_tree_accept
     int tree_n = 0, tree_seq = -1;       // its nodes and its sequence, -1: none
+    // Forked sequences: those of one group (> 0) hold the same rows [0, shared), as far as the least of theirs goes; the sequence
+    // that a group began with shares all of its rows (INT32_MAX).
+    int32_t group[qw::kBatchMax] = {}, shared[qw::kBatchMax] = {}, groups = 0;
+    bool fresh[qw::kBatchMax] = {};      // row s of logits is sequence s's last position's
+    int *own_len = nullptr;              // [8] positions behind a shared prefix
+    int32_t *prefix_len = nullptr, *drawn = nullptr;  // [1], [8]
     int32_t *tok_in = nullptr, *tok = nullptr, *picks = nullptr;
     int *row_pos = nullptr;
     unsigned long long *keys = nullptr;
@@ -708,7 +714,7 @@ struct qw_batch {
     // dump only; each combination is captured once (on a private stream) into a CUDA graph and
     // replayed on the model's stream.
     struct Graph {
-        int B, S, hidden, tree;          // tree: 1 + the sequence whose tree it is, 0: a plain step
+        int B, S, hidden, tree, prefix;  // tree: 1 + the sequence whose tree it is, 0: a plain step
         cudaGraphExec_t exec;
     };
     std::vector<Graph> graphs;
@@ -753,7 +759,10 @@ bool batch_layout(const qw_model *m, int max_batch, int max_ctx, int kv_format, 
     L->part = take((size_t)max_batch * c.n_heads * qw::kBatchMaxSplits * qw::kBatchPartStride * 4);
     const size_t one = qw::tree_attn_scratch_bytes(max_batch, c.n_kv_heads, 1, c.n_heads, c.head_dim, max_ctx);
     const size_t all = qw::tree_attn_scratch_bytes(1, c.n_kv_heads, max_batch, c.n_heads, c.head_dim, max_ctx);
-    L->attn = take(one > all ? one : all);
+    qw_kv_view own{};
+    own.n_seq = max_batch, own.n_kv_heads = c.n_kv_heads, own.head_dim = c.head_dim;
+    const size_t pre = qw::prefix_attn_scratch_bytes(own, 1, c.n_heads, max_ctx, max_ctx);
+    L->attn = take(std::max(std::max(one, all), pre));
     L->logits = take((size_t)max_batch * c.vocab * 4);
     L->hidden = take((size_t)(c.n_layers + 1) * max_batch * c.hidden * 4);
     L->stage = take(q8 ? (size_t)2 * c.n_kv_heads * m->pf.rows_max * c.head_dim * 4 : 0);
@@ -842,6 +851,10 @@ int qw_batch_create_kv(qw_model *m, int32_t max_batch, int32_t max_ctx, int32_t 
     b->tree_picks = b->cache_pos + qw::kBatchMax;
     b->tree_len = b->tree_picks + qw::kBatchMax;
     b->q8.start = b->tree_len + 1;
+    b->own_len = b->tree_len + 4;
+    b->prefix_len = b->own_len + qw::kBatchMax;
+    b->drawn = b->prefix_len + 4;
+    static_assert(2 * 8 + 2 * 4 + (4 + 8 + 4 + 8) * 4 / qw::kBatchMax <= 5 * 8, "the region of the trees' arrays holds these");
     b->tok_in = (int32_t *)(ws + L.small);
     b->tok = b->tok_in + qw::kBatchMax;
     b->picks = b->tok + qw::kBatchMax;
@@ -892,6 +905,8 @@ int qw_batch_reset(qw_batch *b, int32_t seq) {
         if (seq == -1 || s == seq) {
             b->len[s] = 0;
             b->has_last[s] = 0;
+            b->group[s] = 0;
+            b->fresh[s] = false;
         }
     if (seq == -1) {
         b->failed = 0;
@@ -935,6 +950,7 @@ int qw_batch_prefill(qw_batch *b, int32_t seq, const int32_t *tokens_host, int32
         return QW_CUDA_ERROR;
     b->len[seq] += n;
     b->has_last[seq] = 1;
+    b->fresh[seq] = true;
     int rc = cuda_status(cudaMemcpyAsync(b->picks + seq, &b->flags->next_tok, 4, cudaMemcpyDeviceToDevice, m->stream));
     if (rc) return rc;
     if (next_token_host) {
@@ -972,13 +988,27 @@ qw::BatchStep batch_step_of(qw_batch *b, int rows) {
     return bs;
 }
 
+constexpr int kPrefixGraphs = 16;     // captured steps over shared prefixes that are kept
+// Steps of sequences that share at least this many positions read them once.
+constexpr int kSharedMin = 256;
+
+// Positions that sequences 0 .. n - 1 share, 0 where that is not worth it.
+int shared_prefix(const qw_batch *b, int n) {
+    int P = INT32_MAX;
+    for (int s = 0; s < n; ++s) {
+        if (n < 2 || b->group[s] == 0 || b->group[s] != b->group[0]) return 0;
+        P = std::min(P, std::min(b->shared[s], b->len[s]));
+    }
+    return P >= kSharedMin ? P : 0;
+}
+
 // Launches the step's captured graph, capturing it first if this combination is new.
 int batch_launch(qw_batch *b, const qw::BatchStep &bs, int S, int tree) {
     qw_model *m = b->m;
     const int hid = bs.hidden != nullptr;
     cudaGraphExec_t exec = nullptr;
     for (auto &g : b->graphs)
-        if (g.B == bs.B && g.S == S && g.hidden == hid && g.tree == tree) exec = g.exec;
+        if (g.B == bs.B && g.S == S && g.hidden == hid && g.tree == tree && g.prefix == bs.prefix) exec = g.exec;
     if (!exec) {  // capture this combination's launches once
         qw::DecodeArgs a = m->args;
         a.flags = b->flags;
@@ -994,8 +1024,16 @@ int batch_launch(qw_batch *b, const qw::BatchStep &bs, int S, int tree) {
         const cudaError_t ie = cudaGraphInstantiate(&exec, graph, 0);
         cudaGraphDestroy(graph);
         if (ie != cudaSuccess) return cuda_status(ie);
+        // steps over prefixes of other lengths do not pile up
+        int kept = 0;
+        for (size_t i = b->graphs.size(); bs.prefix && i-- > 0;) {
+            if (!b->graphs[i].prefix || ++kept < kPrefixGraphs) continue;
+            cudaStreamSynchronize(m->stream);
+            cudaGraphExecDestroy(b->graphs[i].exec);
+            b->graphs.erase(b->graphs.begin() + (ptrdiff_t)i);
+        }
         try {  // the callers are C entry points
-            b->graphs.push_back({bs.B, S, hid, tree, exec});
+            b->graphs.push_back({bs.B, S, hid, tree, bs.prefix, exec});
         } catch (const std::bad_alloc &) {
             cudaGraphExecDestroy(exec);
             return QW_OUT_OF_MEMORY;
@@ -1039,7 +1077,16 @@ int qw_batch_step(qw_batch *b, int32_t n_seq, const int32_t *tokens_host, int32_
     qw::BatchStep bs = batch_step_of(b, n_seq);
     bs.max_n = max_n;
     int S = qw::batch_splits(max_n);
-    if (b->kv_format == QW_KV_INT8_G32) {
+    if ((bs.prefix = shared_prefix(b, n_seq)) > 0) {
+        int own[qw::kBatchMax];
+        for (int s = 0; s < n_seq; ++s) own[s] = pos[s] - bs.prefix;
+        rc = cuda_status(cudaMemcpyAsync(b->own_len, own, (size_t)n_seq * 4, cudaMemcpyHostToDevice, m->stream));
+        if (!rc) rc = cuda_status(cudaMemcpyAsync(b->prefix_len, &bs.prefix, 4, cudaMemcpyHostToDevice, m->stream));
+        if (rc) return rc;
+        bs.own_len = b->own_len;
+        bs.prefix_len = b->prefix_len;
+        bs.max_len = S = batch_len_bound(max_n - bs.prefix, b->max_ctx - bs.prefix);
+    } else if (b->kv_format == QW_KV_INT8_G32) {
         bs.mask = b->ones;
         bs.max_len = S = batch_len_bound(max_n, b->max_ctx);
     }
@@ -1048,6 +1095,7 @@ int qw_batch_step(qw_batch *b, int32_t n_seq, const int32_t *tokens_host, int32_
     for (int s = 0; s < n_seq; ++s) {
         b->len[s] += 1;
         b->has_last[s] = 1;
+        b->fresh[s] = true;
     }
     b->last_n = n_seq;
     if (next_tokens_host) return batch_read(b, next_tokens_host, n_seq);
@@ -1104,6 +1152,7 @@ int qw_batch_tree_step(qw_batch *b, int32_t seq, int32_t n, const int32_t *token
     rc = batch_launch(b, bs, bs.max_len, 1 + seq);
     if (rc) return rc;
     b->last_n = n;
+    for (int i = 0; i < n; ++i) b->fresh[i] = false;  // the nodes' logits
     for (int i = 0; i < n; ++i) b->tree[i] = parents_host[i];
     b->tree_n = n;
     b->tree_seq = seq;
@@ -1153,6 +1202,77 @@ int qw_batch_tree_accept(qw_batch *b, int32_t seq, int32_t n, const int32_t *nod
     b->len[seq] += n;
     b->has_last[seq] = 1;
     return QW_OK;
+}
+
+int qw_batch_fork(qw_batch *b, int32_t src, int32_t dst, int32_t n) {
+    if (!live_batch(b)) return QW_INVALID_HANDLE;
+    if (b->failed) return b->failed;
+    qw_model *m = b->m;
+    if (src < 0 || src >= b->max_batch || dst < 0 || dst >= b->max_batch || src == dst || n < 1 || n > b->len[src])
+        return QW_INVALID_ARGUMENT;
+    const bool is_q8 = b->kv_format == QW_KV_INT8_G32;
+    const size_t row = m->cfg.head_dim * (is_q8 ? 1 : b->kv_format == QW_KV_F32 ? 4 : 2);
+    const size_t planes = (size_t)m->cfg.n_layers * m->cfg.n_kv_heads, block = planes * b->max_ctx;
+    // rows [0, n) of every (layer, KV head) plane
+    auto copy = [&](void *base, size_t bytes) {
+        uint8_t *p = (uint8_t *)base;
+        return cuda_status(cudaMemcpy2DAsync(p + dst * block * bytes, b->max_ctx * bytes, p + src * block * bytes, b->max_ctx * bytes,
+                                             n * bytes, planes, cudaMemcpyDeviceToDevice, m->stream));
+    };
+    int rc = copy(b->kc, row);
+    if (!rc) rc = copy(b->vc, row);
+    const size_t scales = m->cfg.head_dim / qw::kQGroup * 2;
+    if (!rc && is_q8) rc = copy(b->ks, scales);
+    if (!rc && is_q8) rc = copy(b->vs, scales);
+    const bool whole = n == b->len[src];
+    const size_t V = m->cfg.vocab;
+    if (!rc && whole && b->has_last[src])
+        rc = cuda_status(cudaMemcpyAsync(b->picks + dst, b->picks + src, 4, cudaMemcpyDeviceToDevice, m->stream));
+    if (!rc && whole && b->fresh[src])
+        rc = cuda_status(cudaMemcpyAsync(b->logits + dst * V, b->logits + src * V, V * 4, cudaMemcpyDeviceToDevice, m->stream));
+    if (dst == b->tree_seq) b->tree_seq = -1;
+    b->group[dst] = 0;
+    b->len[dst] = 0;
+    b->has_last[dst] = 0;
+    b->fresh[dst] = false;
+    if (rc) return rc;
+    bool alone = true;
+    for (int s = 0; s < b->max_batch; ++s) alone = alone && (s == src || b->group[src] == 0 || b->group[s] != b->group[src]);
+    if (alone) {  // the first fork of these rows
+        b->group[src] = ++b->groups;
+        b->shared[src] = INT32_MAX;
+    }
+    b->group[dst] = b->group[src];
+    b->shared[dst] = std::min(n, b->shared[src]);
+    b->len[dst] = n;
+    b->has_last[dst] = whole && b->has_last[src];
+    b->fresh[dst] = whole && b->fresh[src];
+    return QW_OK;
+}
+
+int qw_batch_sample(qw_batch *b, int32_t n_seq, const float *u_dev, const float *temperature_dev, const int32_t *top_k_dev,
+                    const float *top_p_dev, const float *min_p_dev, int32_t *next_tokens_host) {
+    if (!live_batch(b)) return QW_INVALID_HANDLE;
+    if (b->failed) return b->failed;
+    if (n_seq < 1 || n_seq > b->max_batch) return QW_INVALID_ARGUMENT;
+    for (int s = 0; s < n_seq; ++s)
+        if (!b->fresh[s]) return QW_INVALID_ARGUMENT;
+    qw_sample_rows_args a{};
+    a.logits = b->logits;
+    a.dtype = QW_DT_F32;
+    a.n_rows = n_seq;
+    a.vocab = b->m->cfg.vocab;
+    a.row_stride = a.vocab;
+    a.u = u_dev;
+    a.temperature = temperature_dev;
+    a.top_k = top_k_dev;
+    a.top_p = top_p_dev;
+    a.min_p = min_p_dev;
+    a.tokens = b->drawn;
+    int rc = qw_sample_rows(&a, b->m->stream);
+    if (!rc) rc = cuda_status(qw::launch_batch_take(b->drawn, n_seq, b->picks, b->flags, b->m->stream));
+    if (rc) return rc;
+    return next_tokens_host ? batch_read(b, next_tokens_host, n_seq) : QW_OK;
 }
 
 int qw_batch_logits(qw_batch *b, float *dst_dev, int64_t n) {

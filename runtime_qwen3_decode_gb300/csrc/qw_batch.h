@@ -89,6 +89,8 @@ struct BatchKeep {
 cudaError_t launch_batch_keep(const BatchKeep &p, cudaStream_t st);
 cudaError_t launch_batch_tokens(const int32_t *in, const int32_t *picks, int B, int32_t *tokens, cudaStream_t st,
                                 bool chained);
+// Drawn tokens [B] become the sequences' picks; one that is negative records an error instead.
+cudaError_t launch_batch_take(const int32_t *drawn, int B, int32_t *picks, StepFlags *flags, cudaStream_t st);
 cudaError_t launch_batch_attn(const BatchAttn &p, int Hkv, int B, int kv_f32, cudaStream_t st, bool chained);
 cudaError_t launch_batch_merge(const float *part, int S, int Hq, int B, __half *o16, int ldo, cudaStream_t st,
                                bool chained);

@@ -68,7 +68,12 @@ struct BatchStep {
     // mask[b].  8-bit caches attend through the same operator, one node per sequence.
     const int *cache_pos, *tree_len;
     const uint64_t *mask;      // [B] (8-bit caches without a tree: ones)
-    void *attn_scratch;        // of the tree attention
+    // Sequences that share their first `prefix` positions (0: none do): those are read once, from sequence 0's cache, and
+    // each sequence's own_len[b] positions behind them from its own.
+    int prefix;
+    const int *own_len;        // device [B]
+    const int32_t *prefix_len; // device [1] = prefix
+    void *attn_scratch;        // of the tree and the prefix attention
     int max_len;               // about the longest cache, for its split
 };
 int prefill_batch_step(PrefillState *st, const DecodeArgs &a, const BatchStep &bs, cudaStream_t stream);

@@ -63,7 +63,7 @@ EXPORTS = ("qw_workspace_bytes", "qw_model_create", "qw_prefill", "qw_decode_ste
            "qw_checkpoint_check", "qw_checkpoint_upload_bytes", "qw_checkpoint_upload", "qw_kv_append", "qw_kv_read",
            "qw_tree_attention_scratch_bytes", "qw_tree_attention", "qw_prefix_attention_scratch_bytes",
            "qw_prefix_attention", "qw_process_logits", "qw_sample_rows", "qw_batch_workspace_bytes_kv",
-           "qw_batch_create_kv", "qw_batch_tree_step", "qw_batch_tree_accept")
+           "qw_batch_create_kv", "qw_batch_tree_step", "qw_batch_tree_accept", "qw_batch_fork", "qw_batch_sample")
 DT_BF16, DT_F16, DT_F32, DT_I8, DT_Q8_0 = 0, 1, 2, 3, 4
 BATCH_MAX = 8
 TREE_NODES_MAX = 64
@@ -210,6 +210,8 @@ def _lib():
             L.qw_batch_create_kv.argtypes = [vp, i32, i32, i32, vp, ctypes.c_size_t, ctypes.POINTER(ctypes.c_void_p)]
             L.qw_batch_tree_step.argtypes = [vp, i32, i32, i32p, i32p, i32p]
             L.qw_batch_tree_accept.argtypes = [vp, i32, i32, i32p]
+            L.qw_batch_fork.argtypes = [vp, i32, i32, i32]
+            L.qw_batch_sample.argtypes = [vp, i32, vp, vp, vp, vp, vp, i32p]
             u64 = ctypes.c_uint64
             L.qw_checkpoint_open.argtypes = [vp, u64, u64, ctypes.POINTER(ctypes.c_void_p)]
             L.qw_checkpoint_close.argtypes = [vp]
@@ -890,6 +892,24 @@ class Batch:
         n = len(nodes)
         _check(_lib().qw_batch_tree_accept(self._h, seq, n, (ctypes.c_int32 * n)(*[int(x) for x in nodes]) if n else None),
                "qw_batch_tree_accept")
+
+    def fork(self, src: int, dst: int, n: int | None = None):
+        """qw_batch_fork: sequence dst becomes a continuation of the first n positions of src (None: all of them)."""
+        _check(_lib().qw_batch_fork(self._h, src, dst, self.length(src) if n is None else n), "qw_batch_fork")
+
+    def sample(self, n_seq: int, u, temperature=None, top_k=None, top_p=None, min_p=None, want_tokens: bool = True):
+        """qw_batch_sample: the next tokens of sequences 0..n_seq-1 drawn with the random numbers u (float32 [n_seq] on
+        the device, as are the settings; None: sample_rows' defaults), in the place of their greedy picks."""
+        _use_torch()
+        dev, shape = self.workspace.get_device(), (n_seq,)
+        if u is None:
+            raise ValueError("u must be given")
+        args = [_want(t, name, dev, dt, shape) for t, name, dt in
+                ((u, "u", _T.float32), (temperature, "temperature", _T.float32), (top_k, "top_k", _T.int32),
+                 (top_p, "top_p", _T.float32), (min_p, "min_p", _T.float32))]
+        out = (ctypes.c_int32 * n_seq)()
+        _check(_lib().qw_batch_sample(self._h, n_seq, *args, out if want_tokens else None), "qw_batch_sample")
+        return list(out) if want_tokens else None
 
     def logits(self):
         import torch
