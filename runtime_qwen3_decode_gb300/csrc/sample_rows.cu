@@ -40,17 +40,18 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 8;
+// Parts of a pass's zone, B in what follows: every thread has a bin of its own for each, 4 KB a part.  32 where a CTA has an SM for
+// itself anyway, which saves passes; else 8, so that two CTAs share one.
+constexpr int kFewBins = 8, kManyBins = 32;
 constexpr int kKeys = 4;              // sorted keys of a thread
 constexpr int kList = kKeys * kThreads;  // tokens that are sorted at once, in one CTA
 constexpr int kMostShort = 1200;     // top_k up to which the short way is tried
 constexpr int kPart = kThreads;            // of a part that one border is looked for in, in every CTA
 constexpr int kShort = 512, kNear = 128; // a border's tokens are cut down to this many, or to this many about it
 constexpr int kMaxCluster = 8;
-constexpr int kCountBit = 52;     // of a thread's bin: its sum of weights below, its count above
+constexpr int kCountBit = 51;     // of a thread's bin: its sum of weights below, its count (up to 4096) above
 constexpr int kMantBits = 36;     // of a weight's mantissa behind its point
 constexpr int kSteps = 32;        // of the table of 2^(i / 32)
-static_assert(kWarps >= kBins, "one warp adds up one bin");
 
 using u64 = unsigned long long;
 
@@ -169,12 +170,13 @@ struct Total {
     unsigned n, low;
 };
 
+template <int B>
 struct Shared {
     Table table;
-    u64 xch_w[2][kMaxCluster][kBins];   // a pass's bins of every CTA of the cluster
-    unsigned xch_n[2][kMaxCluster][kBins];
-    Total total[kBins];                 // and their sums
-    Total cum[kBins];                   // of the octaves: each with the ones above it
+    u64 xch_w[2][kMaxCluster][B];       // a pass's bins of every CTA of the cluster
+    unsigned xch_n[2][kMaxCluster][B];
+    Total total[B];                     // and their sums, each with the ones above it
+    Total cum[B];                       // the same of the octaves
     float top[kMaxCluster], least[kMaxCluster];  // greatest and least logit of every CTA
     float group[kThreads];                       // greatest logits of kThreads parts of the row
     unsigned count[kMaxCluster];                 // tokens in every CTA's part of the short list
@@ -192,19 +194,21 @@ struct Shared {
 struct Parts {
     u64 list[2][kPart], buf[2][kPart];
 };
-constexpr int kBinBytes = kBins * kThreads * 8;
-static_assert(sizeof(Parts) <= kBinBytes && kList * 8 <= kBinBytes, "fits over the bins");
+template <int B>
+constexpr int kBinBytes = B * kThreads * 8;
+static_assert(sizeof(Parts) <= kBinBytes<kFewBins> && kList * 8 <= kBinBytes<kFewBins>, "fits over the bins");
 
-// How a pass cuts its tokens in kBins parts, the greatest first: by logit, top - x in units of 1 / inv (the first and the
+// How a pass cuts its tokens in B parts, the greatest first: by logit, top - x in units of 1 / inv (the first and the
 // last part take the rest), or by key, (key - lo) >> shift.
+template <int B>
 struct Cut {
     bool by_value;
     float top, inv;
     u64 lo;
     int shift;
-    // the whole part of (top - x) inv, cut at 0 and kBins - 1, by adding 2^23 rounding down
+    // the whole part of (top - x) inv, cut at 0 and B - 1, by adding 2^23 rounding down
     __device__ __forceinline__ int slot(float x) const {
-        return __float_as_int(__fadd_rd(fminf(fmaxf((top - x) * inv, 0.f), kBins - 1.f), 8388608.f)) & (kBins - 1);
+        return __float_as_int(__fadd_rd(fminf(fmaxf((top - x) * inv, 0.f), B - 1.f), 8388608.f)) & (B - 1);
     }
 };
 
@@ -238,9 +242,9 @@ struct Piece {
 // One pass: every token of the zone is counted in the part of it that the cut gives, and weighed if asked; sh.total has
 // the cluster's sums.  Each thread has bins of its own.  No branch but the one past four tokens outside: the others'
 // numbers are 0 and go to the last bin.  ROW: the zone has no upper end and is cut by logits.
-template <bool WEIGHED, bool ROW, typename P>
-__device__ __forceinline__ void tally(const P &piece, Shared &sh, const Row &row, u64 *bins, cg::cluster_group &cl, int turn,
-                                      const Zone &z, const Cut &c, int id_bits) {
+template <int B, bool WEIGHED, bool ROW, typename P>
+__device__ __forceinline__ void tally(const P &piece, Shared<B> &sh, const Row &row, u64 *bins, cg::cluster_group &cl, int turn,
+                                      const Zone &z, const Cut<B> &c, int id_bits) {
     const u64 id_mask = (1ull << id_bits) - 1ull;
     const float xl = ord_value((unsigned)(z.lo >> id_bits)), xh = ord_value((unsigned)((z.end - 1ull) >> id_bits));
     const int last = (int)(id_mask - (z.lo & id_mask)), first = (int)(id_mask - ((z.end - 1ull) & id_mask));
@@ -248,7 +252,7 @@ __device__ __forceinline__ void tally(const P &piece, Shared &sh, const Row &row
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr u64 kSum = (1ull << kCountBit) - 1ull;
 #pragma unroll
-    for (int b = 0; b < kBins; ++b) bins[b * kThreads + tid] = 0ull;
+    for (int b = 0; b < B; ++b) bins[b * kThreads + tid] = 0ull;
     const int quads = piece.quads();
     for (int g = tid; g < quads; g += kThreads) {
         const float4 v = piece.at(g);
@@ -272,7 +276,7 @@ __device__ __forceinline__ void tally(const P &piece, Shared &sh, const Row &row
         if (!ROW && !c.by_value) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                b[k] = kBins - 1 - (int)((key_of(x[k], piece.begin + 4 * g + k, id_bits) - z.lo) >> c.shift);
+                b[k] = B - 1 - (int)((key_of(x[k], piece.begin + 4 * g + k, id_bits) - z.lo) >> c.shift);
         }
         u64 w[4] = {0ull, 0ull, 0ull, 0ull};
         if constexpr (WEIGHED) {
@@ -284,7 +288,7 @@ __device__ __forceinline__ void tally(const P &piece, Shared &sh, const Row &row
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             w[k] = is[k] ? w[k] + (1ull << kCountBit) : 0ull;
-            b[k] = is[k] ? b[k] : kBins - 1;
+            b[k] = is[k] ? b[k] : B - 1;
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) bins[b[k] * kThreads + tid] += w[k];
@@ -298,39 +302,47 @@ __device__ __forceinline__ void tally(const P &piece, Shared &sh, const Row &row
     };
     __syncthreads();
     const unsigned ctas = cl.num_blocks(), me = cl.block_rank();
-    if (warp < kBins) {
+    for (int bin = warp; bin < B; bin += kWarps) {
         u64 w = 0;
         unsigned n = 0;
 #pragma unroll
         for (int i = 0; i < kThreads / 32; ++i) {
-            const u64 v = bins[warp * kThreads + lane + 32 * i];
+            const u64 v = bins[bin * kThreads + lane + 32 * i];
             w += v & kSum;
             n += (unsigned)(v >> kCountBit);
         }
         add(w, n);
         if (lane < ctas) {
-            *cl.map_shared_rank(&sh.xch_w[turn][me][warp], lane) = w;
-            *cl.map_shared_rank(&sh.xch_n[turn][me][warp], lane) = n;
+            *cl.map_shared_rank(&sh.xch_w[turn][me][bin], lane) = w;
+            *cl.map_shared_rank(&sh.xch_n[turn][me][bin], lane) = n;
         }
     }
     if (ctas > 1) cl.sync();
     else __syncthreads();
-    if (tid < kBins) {
+    if (warp == 0) {
         Total t{0ull, 0u, 0u};
-        for (unsigned c = 0; c < ctas; ++c) {
-            const unsigned n = sh.xch_n[turn][c][tid];
-            t.w += sh.xch_w[turn][c][tid];
-            t.n += n;
-            if (c < me) t.low += n;
+        if (lane < B)
+            for (unsigned c = 0; c < ctas; ++c) {
+                const unsigned n = sh.xch_n[turn][c][lane];
+                t.w += sh.xch_w[turn][c][lane];
+                t.n += n;
+                if (c < me) t.low += n;
+            }
+#pragma unroll
+        for (int o = 1; o < B; o <<= 1) {
+            const u64 w = __shfl_up_sync(0xffffffffu, t.w, o);
+            const unsigned n = __shfl_up_sync(0xffffffffu, t.n, o), low = __shfl_up_sync(0xffffffffu, t.low, o);
+            if (lane >= o) t.w += w, t.n += n, t.low += low;
         }
-        sh.total[tid] = t;
+        if (lane < B) sh.total[lane] = t;
     }
     __syncthreads();
 }
 
 // The least order number of [low, high] for which slot() is at most j (high + 1: none).  One warp: the 32 places about where it
 // should be, which hold it but where logits lie close to 0; then by halves.
-__device__ unsigned edge_of(const Cut &c, int j, unsigned low, unsigned high) {
+template <int B>
+__device__ unsigned edge_of(const Cut<B> &c, int j, unsigned low, unsigned high) {
     const unsigned lane = threadIdx.x & 31;
     unsigned no = low, yes = high + 1u;  // below `no` it is not, from `yes` on it is
     const unsigned guess = min(max(ord_bits(c.top - (float)(j + 1) / c.inv), low), high);
@@ -403,13 +415,13 @@ __device__ __forceinline__ float ratio(u64 W, u64 S) {
     return q + (fmaf(-q, s, w) + fmaf(-q, sl, wl)) / s;
 }
 
-template <typename T, bool RES>
-__global__ void __launch_bounds__(kThreads, 2) sample_rows_kernel(const __grid_constant__ SampleArgs a,
+template <typename T, bool RES, int B>
+__global__ void __launch_bounds__(kThreads, B == kFewBins ? 2 : 1) sample_rows_kernel(const __grid_constant__ SampleArgs a,
                                                                   const __grid_constant__ Table table) {
     extern __shared__ __align__(16) uint8_t smem_sample[];
-    Shared &sh = *reinterpret_cast<Shared *>(smem_sample);
-    u64 *bins = reinterpret_cast<u64 *>(smem_sample + (sizeof(Shared) + 15) / 16 * 16);
-    float *sx = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(bins) + kBinBytes);
+    Shared<B> &sh = *reinterpret_cast<Shared<B> *>(smem_sample);
+    u64 *bins = reinterpret_cast<u64 *>(smem_sample + (sizeof(Shared<B>) + 15) / 16 * 16);
+    float *sx = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(bins) + kBinBytes<B>);
     cg::cluster_group cl = cg::this_cluster();
     const unsigned ctas = cl.num_blocks(), me = cl.block_rank();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -550,10 +562,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rows_kernel(const __grid_c
     }
     const bool has_p = top_p < 1.f;
     // 2. octaves are no narrower than a few of the greatest logit's last places
-    Cut octaves{};
+    Cut<B> octaves{};
     octaves.by_value = true;
     octaves.top = row.top;
-    octaves.inv = 1.f / fmaxf(fmaxf(T_ * 1.38629436f, fabsf(row.top) * 1e-6f), 1e-30f);
+    octaves.inv = 1.f / fmaxf(fmaxf(T_ * (0.69314718f * 16.f / B), fabsf(row.top) * 1e-6f), 1e-30f);
     // The whole row: the tokens with keys from `bottom` on.  Without top_p, what min_p leaves out counts for nothing else; with it
     // the weights that it takes its part of do.
     Zone rows{(u64)ord_bits(fmaxf(least, has_p ? -FLT_MAX : cut)) << a.id_bits, ((u64)ord_bits(row.top) + 1ull) << a.id_bits, {}, {}};
@@ -624,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rows_kernel(const __grid_c
     u64 goal = 0;
     Total whole{}, kept{};
     Zone z = rows;
-    Cut c = octaves;
+    Cut<B> c = octaves;
     for (;;) {
         bool all = listed != 0;
         u64 *list = bins;
@@ -636,31 +648,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rows_kernel(const __grid_c
         } else {
         if (pass != kNone) {
             if (pass != kNarrow) {
-                if (stage == 0) tally<false, true>(piece, sh, row, bins, cl, turn, z, c, a.id_bits);
-                else tally<true, true>(piece, sh, row, bins, cl, turn, z, c, a.id_bits);
+                if (stage == 0) tally<B, false, true>(piece, sh, row, bins, cl, turn, z, c, a.id_bits);
+                else tally<B, true, true>(piece, sh, row, bins, cl, turn, z, c, a.id_bits);
             } else {
-                if (stage == 0) tally<false, false>(piece, sh, row, bins, cl, turn, z, c, a.id_bits);
-                else tally<true, false>(piece, sh, row, bins, cl, turn, z, c, a.id_bits);
+                if (stage == 0) tally<B, false, false>(piece, sh, row, bins, cl, turn, z, c, a.id_bits);
+                else tally<B, true, false>(piece, sh, row, bins, cl, turn, z, c, a.id_bits);
             }
             turn ^= 1;  // a CTA that is ahead writes the other half
             if (pass == kOctaves) {
-                if (tid < kBins) {
-                    Total t{0ull, 0u, 0u};
-                    for (int b = 0; b <= tid; ++b) {
-                        t.w += sh.total[b].w;
-                        t.n += sh.total[b].n;
-                        t.low += sh.total[b].low;
-                    }
-                    sh.cum[tid] = t;
-                }
+                if (tid < B) sh.cum[tid] = sh.total[tid];
                 __syncthreads();
-                whole = kept = rows.inside = sh.cum[kBins - 1];
+                whole = kept = rows.inside = sh.cum[B - 1];
                 seek = stage == 0 ? (unsigned)top_k < whole.n : has_p;
                 goal = stage == 0 ? (u64)top_k : max(1ull, times(top_p, whole.w, true));
                 z = rows;
             } else if (pass == kMinP) {
-                kept = Total{0ull, 0u, 0u};
-                for (int b = 0; b < kBins; ++b) kept.w += sh.total[b].w, kept.n += sh.total[b].n;
+                kept = sh.total[B - 1];
                 stage = 2;
             }
             from_octaves = pass != kNarrow;
@@ -674,15 +677,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rows_kernel(const __grid_c
             const Total *total = from_octaves ? sh.cum : sh.total;
             near = -1.f;
             if (from_octaves) c = octaves;
-            Total t{0ull, 0u, 0u}, before{0ull, 0u, 0u};
-            int b = 0;
-            for (;; ++b) {
-                const Total x = total[b];
-                t = from_octaves ? x : Total{before.w + x.w, before.n + x.n, before.low + x.low};
-                if (b == kBins - 1 || (stage == 0 ? (u64)(z.above.n + t.n) : z.above.w + t.w) >= goal) break;
-                before = t;
-            }
-            if (from_octaves && b > 0 && b < kBins - 2) {
+            Total t = lane < B ? total[lane] : Total{~0ull >> 1, ~0u >> 1, 0u}, before;
+            const unsigned there = __ballot_sync(0xffffffffu, (stage == 0 ? (u64)(z.above.n + t.n) : z.above.w + t.w) >= goal);
+            const int b = there ? min(__ffs(there) - 1, B - 1) : B - 1;
+            before = b ? total[b - 1] : Total{0ull, 0u, 0u};
+            t = total[b];
+            if (from_octaves && b > 0 && b < B - 2) {
                 // About where in the octave the border is, if what octaves hold grows by the same factor g^2 from the one above to the
                 // one below: 1 + share (g - 1) = g^near.
                 auto held = [&](int i) {
@@ -697,15 +697,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rows_kernel(const __grid_c
             z.above = Total{z.above.w + before.w, z.above.n + before.n, z.above.low + before.low};
             if (c.by_value) {
                 const unsigned low = (unsigned)(z.lo >> a.id_bits), high = (unsigned)((z.end - 1ull) >> a.id_bits);
-                if (warp < 2 && (warp ? b < kBins - 1 : b > 0)) {
+                if (warp < 2 && (warp ? b < B - 1 : b > 0)) {
                     const unsigned e = edge_of(c, b - 1 + warp, low, high);
                     if (lane == 0) sh.edge[warp] = e;
                 }
                 __syncthreads();
                 if (b > 0) z.end = min(z.end, (u64)sh.edge[0] << a.id_bits);
-                if (b < kBins - 1) z.lo = max(z.lo, (u64)sh.edge[1] << a.id_bits);
+                if (b < B - 1) z.lo = max(z.lo, (u64)sh.edge[1] << a.id_bits);
             } else {
-                z.lo += (u64)(kBins - 1 - b) << c.shift;
+                z.lo += (u64)(B - 1 - b) << c.shift;
                 z.end = min(z.end, z.lo + (1ull << c.shift));
             }
             __syncthreads();  // sh.edge and sh.total are read
@@ -719,16 +719,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rows_kernel(const __grid_c
         if (cut_more) {
             // in parts of equal spans of logits while they have places enough between them, then of keys
             const unsigned low = (unsigned)(z.lo >> a.id_bits), high = (unsigned)((z.end - 1ull) >> a.id_bits);
-            const float xl = ord_value(low), xh = ord_value(high), width = xh * (1.f / kBins) - xl * (1.f / kBins);
+            const float xl = ord_value(low), xh = ord_value(high), width = xh * (1.f / B) - xl * (1.f / B);
             c.by_value = high - low > 64u && width > fmaxf(fmaxf(fabsf(xl), fabsf(xh)) * 1e-6f, 1e-30f);
             c.top = xh;
             c.inv = 1.f / width;
             if (near >= 0.f && c.by_value) {  // narrow parts about the place where the border should be
                 const float part = width * 0.25f;
-                if (part > fmaxf(fabsf(xl), fabsf(xh)) * 1e-6f) c.top = xh - near * kBins * width + kBins / 2 * part, c.inv = 1.f / part;
+                if (part > fmaxf(fabsf(xl), fabsf(xh)) * 1e-6f) c.top = xh - near * B * width + B / 2 * part, c.inv = 1.f / part;
             }
             c.shift = 0;
-            while ((z.end - z.lo - 1ull) >> c.shift >= (u64)kBins) ++c.shift;
+            while ((z.end - z.lo - 1ull) >> c.shift >= (u64)B) ++c.shift;
             pass = kNarrow;
             continue;
         }
@@ -860,9 +860,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rows_kernel(const __grid_c
     }
 }
 
-template <typename T, bool RES>
+template <typename T, bool RES, int B>
 cudaError_t launch_rows(const SampleArgs &a, const Table &t, int rows, int ctas, size_t smem, cudaStream_t st) {
-    cudaError_t e = allow_smem<sample_rows_kernel<T, RES>>(227 * 1024);
+    cudaError_t e = allow_smem<sample_rows_kernel<T, RES, B>>(227 * 1024);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)rows * ctas);
@@ -875,7 +875,7 @@ cudaError_t launch_rows(const SampleArgs &a, const Table &t, int rows, int ctas,
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, sample_rows_kernel<T, RES>, a, t);
+    return cudaLaunchKernelEx(&cfg, sample_rows_kernel<T, RES, B>, a, t);
 }
 
 const Table &table() {
@@ -899,8 +899,11 @@ int bits_for(int64_t n) {  // least b with n <= 2^b
 
 template <typename T>
 cudaError_t launch_typed(const qw_sample_rows_args &q, cudaStream_t st) {
-    const size_t fixed = (sizeof(Shared) + 15) / 16 * 16 + kBinBytes;
-    const size_t room = 227 * 1024 - fixed;
+    auto fixed = [](int bins) {
+        return bins == kFewBins ? (sizeof(Shared<kFewBins>) + 15) / 16 * 16 + kBinBytes<kFewBins>
+                                : (sizeof(Shared<kManyBins>) + 15) / 16 * 16 + kBinBytes<kManyBins>;
+    };
+    const size_t most = 227 * 1024, room = most - fixed(kFewBins);
     // As many CTAs for a row as there are SMs to take them, or as hold it with another CTA on the SM.  (Clusters of 16 for up to
     // nine rows took 15.5 us instead of 14.2 at 8 x 151,936: what grows with the cluster outweighs the shorter pieces.)
     int ctas = 1;
@@ -916,8 +919,11 @@ cudaError_t launch_typed(const qw_sample_rows_args &q, cudaStream_t st) {
     a.u = q.u, a.temperature = q.temperature, a.top_p = q.top_p, a.min_p = q.min_p, a.top_k = q.top_k;
     a.tokens = q.tokens, a.kept = q.kept, a.probs = q.probs;
     const bool res = (size_t)a.per * 4 <= room;
-    const size_t smem = fixed + std::max<size_t>(res ? (size_t)a.per * 4 : 0, (size_t)kList * 16);  // lists are sorted where the row was
-    return res ? launch_rows<T, true>(a, table(), q.n_rows, ctas, smem, st) : launch_rows<T, false>(a, table(), q.n_rows, ctas, smem, st);
+    const size_t row = std::max<size_t>(res ? (size_t)a.per * 4 : 0, (size_t)kList * 16);  // lists are sorted where the row was
+    if (!res) return launch_rows<T, false, kFewBins>(a, table(), q.n_rows, ctas, fixed(kFewBins) + row, st);
+    if ((int64_t)q.n_rows * ctas <= 152 && fixed(kManyBins) + row <= most)
+        return launch_rows<T, true, kManyBins>(a, table(), q.n_rows, ctas, fixed(kManyBins) + row, st);
+    return launch_rows<T, true, kFewBins>(a, table(), q.n_rows, ctas, fixed(kFewBins) + row, st);
 }
 
 }  // namespace
