@@ -40,8 +40,9 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-// Parts of a pass's zone, B in what follows: every thread has a bin of its own for each, 4 KB a part.  32 where a CTA has an SM for
-// itself anyway, which saves passes; else 8, so that two CTAs share one.
+// Parts of a pass's zone, B in what follows: every thread has a bin of its own for each, 2 or 8 KB a warp.  32 up to some waves of
+// CTAs, which saves passes but leaves one CTA to an SM (8 x 151,936 drawn from nearly everything 48 us, 82 with 8; 64 rows of mixed
+// settings 113, 118); else 8, so that two CTAs share an SM (256 such rows 316 and 318).
 constexpr int kFewBins = 8, kManyBins = 32;
 constexpr int kKeys = 4;              // sorted keys of a thread
 constexpr int kList = kKeys * kThreads;  // tokens that are sorted at once, in one CTA
@@ -921,7 +922,7 @@ cudaError_t launch_typed(const qw_sample_rows_args &q, cudaStream_t st) {
     const bool res = (size_t)a.per * 4 <= room;
     const size_t row = std::max<size_t>(res ? (size_t)a.per * 4 : 0, (size_t)kList * 16);  // lists are sorted where the row was
     if (!res) return launch_rows<T, false, kFewBins>(a, table(), q.n_rows, ctas, fixed(kFewBins) + row, st);
-    if ((int64_t)q.n_rows * ctas <= 152 && fixed(kManyBins) + row <= most)
+    if ((int64_t)q.n_rows * ctas <= 4 * 152 && fixed(kManyBins) + row <= most)
         return launch_rows<T, true, kManyBins>(a, table(), q.n_rows, ctas, fixed(kManyBins) + row, st);
     return launch_rows<T, true, kFewBins>(a, table(), q.n_rows, ctas, fixed(kFewBins) + row, st);
 }
