@@ -68,6 +68,7 @@ struct SampleArgs {
     const void *logits;
     int64_t stride;
     int V, per, id_bits, wb;      // per: tokens per CTA of the cluster, a multiple of 8
+    int rows, sorted;             // sorted: rows that take long first
     const float *u, *temperature, *top_p, *min_p;
     const int32_t *top_k;
     int32_t *tokens, *kept;
@@ -416,6 +417,38 @@ __device__ __forceinline__ float ratio(u64 W, u64 S) {
     return q + (fmaf(-q, s, w) + fmaf(-q, sl, wl)) / s;
 }
 
+// Whether a row takes more than the short way (see below).
+__device__ __forceinline__ bool takes_long(const SampleArgs &a, int r) {
+    const int k = a.top_k ? a.top_k[r] : 0;
+    if ((a.temperature && a.temperature[r] == 0.f) || (k > 0 && k <= kMostShort)) return false;
+    return k > 0 || !a.min_p || !(a.min_p[r] > 0.f) || (a.top_p && a.top_p[r] < 1.f);
+}
+
+// The row of cluster c, the ones that take long first, so that none of them begins when the others are done.  All threads.
+template <int B>
+__device__ int row_of(const SampleArgs &a, Shared<B> &sh, int c) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int longs = 0;
+    for (int r0 = 0; r0 < a.rows; r0 += kThreads) longs += __syncthreads_count(r0 + tid < a.rows && takes_long(a, r0 + tid));
+    const bool want = c < longs;
+    int left = want ? c : c - longs;
+    for (int r0 = 0; r0 < a.rows; r0 += kThreads) {
+        const bool is = r0 + tid < a.rows && takes_long(a, r0 + tid) == want;
+        const unsigned who = __ballot_sync(0xffffffffu, is);
+        if (lane == 0) sh.scan[warp] = __popc(who);
+        const int n = __syncthreads_count(is);
+        if (left < n) {
+            int before = __popc(who & ((1u << lane) - 1u));
+            for (int k = 0; k < warp; ++k) before += (int)sh.scan[k];
+            if (is && before == left) sh.first[0] = r0 + tid;
+            __syncthreads();
+            return sh.first[0];
+        }
+        left -= n;
+    }
+    return c;
+}
+
 template <typename T, bool RES, int B>
 __global__ void __launch_bounds__(kThreads, B == kFewBins ? 2 : 1) sample_rows_kernel(const __grid_constant__ SampleArgs a,
                                                                   const __grid_constant__ Table table) {
@@ -426,8 +459,9 @@ __global__ void __launch_bounds__(kThreads, B == kFewBins ? 2 : 1) sample_rows_k
     cg::cluster_group cl = cg::this_cluster();
     const unsigned ctas = cl.num_blocks(), me = cl.block_rank();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int r = blockIdx.x / ctas;
     if (ctas > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+    int r = blockIdx.x / ctas;
+    if (a.sorted) r = row_of(a, sh, r);
 
     const float T_ = a.temperature ? a.temperature[r] : 1.f, u = a.u[r];
     const float top_p = a.top_p ? a.top_p[r] : 1.f, min_p = a.min_p ? a.min_p[r] : 0.f;
@@ -917,6 +951,9 @@ cudaError_t launch_typed(const qw_sample_rows_args &q, cudaStream_t st) {
     a.per = per(ctas);
     a.id_bits = bits_for(q.vocab);
     a.wb = std::min(62 - a.id_bits, kCountBit - 1 - bits_for((a.per + 4 * kThreads - 1) / (4 * kThreads) * 4));  // a thread's tokens fit its bins
+    a.rows = q.n_rows;
+    // One wave has no last ones; beyond some thousand rows the search costs more than it gives.
+    a.sorted = (int64_t)q.n_rows * ctas > 2 * 152 && q.n_rows <= 2048;
     a.u = q.u, a.temperature = q.temperature, a.top_p = q.top_p, a.min_p = q.min_p, a.top_k = q.top_k;
     a.tokens = q.tokens, a.kept = q.kept, a.probs = q.probs;
     const bool res = (size_t)a.per * 4 <= room;

@@ -43,8 +43,8 @@
 // own tile costs the tensor cores what any tile does, though only its rows see it (the others' weights are 0, and warps
 // without any of its rows do no softmax), but its bytes are read once and the stream of tiles never stops: with the own parts as
 // items of their own, every one of them began with a wait for its queries and ended with an epilogue.  What is not finite in
-// an own tile's V must not reach the other sequences' rows as 0 x NaN.  Looking every own tile through for it took three times as
-// long as the tile otherwise needs (6,600 cycles instead of XX), so a CTA does its share without looking, and where a row's
+// an own tile's V must not reach the other sequences' rows as 0 x NaN.  Looking every own tile through for it took twice as
+// long as the tile otherwise needs (6,600 cycles instead of 3,100 over long bf16 ones), so a CTA does its share without looking, and where a row's
 // accumulator comes out not finite does it all again, with such elements taken out as above (bf16 tiles by warps 8 and 9, which
 // zero the rows behind an end in the first pass).
 //
@@ -449,6 +449,18 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
         return *reinterpret_cast<const uint32_t *>(&h);
     } else {
         const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+
+// Two packed weights times a power of two.
+template <bool BF16>
+__device__ __forceinline__ uint32_t scale2(uint32_t p, float f) {
+    if constexpr (BF16) {
+        const __nv_bfloat162 h = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&p), __float2bfloat162_rn(f));
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&p), __float2half2_rn(f));
         return *reinterpret_cast<const uint32_t *>(&h);
     }
 }
@@ -888,13 +900,75 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) tmem_st16u(tS + 16u * c, pk);
                 }
-                if (busy) {
+                if constexpr (PREFIX) {
+                    if (busy) {
+                        // One pass, 32 columns at a time, each with the reference that the ones before it left: the reference follows the
+                        // maximum only when that has risen by more than kLag, which it seldom does behind a row's first tiles,
+                        // and then the accumulator and the tile's weights so far are scaled by a power of two.  (With a pass for the
+                        // maximum first, as below, 64 sequences of 64 rows over 4096 bf16 positions took 189 us instead of 182.)
+#pragma unroll 1
+                        for (int c = 0; c < blocks; ++c) {
+                            const uint32_t vis = tail ? visible(seen, first + 32 * c - w.len) : 0xffffffffu;
+                            float v[32];
+                            tmem_ld32(tS + 32u * c, v);
+                            float top = -INFINITY;
+                            if (vis != 0xffffffffu) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) v[i] = (vis >> i) & 1u ? v[i] : -INFINITY;
+                            }
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) top = fmaxf(top, v[i]);
+                            top = sees ? top * sc : -INFINITY;
+                            const bool resc = top > m_used + C::kLag;
+                            if (__any_sync(0xffffffffu, resc)) {
+                                const float m_new = resc ? ceilf(top) : m_used, factor = resc ? fast_exp2(m_used - m_new) : 1.f;
+                                if (mine > 0) {
+#pragma unroll 1
+                                    for (int k = 0; k < D / 16; ++k) {
+                                        uint32_t o[16];
+                                        tmem_ld16u(tO + 16u * k, o);
+#pragma unroll
+                                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
+                                        tmem_st16u(tO + 16u * k, o);
+                                    }
+                                }
+#pragma unroll 1
+                                for (int k = 0; k < c; ++k) {
+                                    uint32_t pk[16];
+                                    tmem_ld16u(tS + 16u * k, pk);
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) pk[i] = scale2<C::kBf16>(pk[i], factor);
+                                    tmem_st16u(tS + 16u * k, pk);
+                                }
+                                l *= factor;
+                                m_used = m_new;
+                            }
+                            const float mm = m_used == -INFINITY ? 0.f : m_used - C::kLift;  // nothing seen yet: every weight 2^-inf
+                            uint32_t pk[16];
+                            float2 l2 = make_float2(0.f, 0.f);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const float2 z = __ffma2_rn(make_float2(v[2 * i], v[2 * i + 1]), make_float2(sc, sc), make_float2(-mm, -mm));
+                                const float2 e = make_float2(sees ? fast_exp2(z.x) : 0.f, sees ? fast_exp2(z.y) : 0.f);
+                                l2 = __fadd2_rn(l2, e);
+                                pk[i] = pack2<C::kBf16>(e.x, e.y);
+                            }
+                            l += l2.x + l2.y;
+                            tmem_st16u(tS + 16u * c, pk);
+                        }
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) pk[i] = 0u;
+#pragma unroll 1
+                        for (int c = blocks; c < 4; ++c) tmem_st16u(tS + 16u * c, pk);
+                    }
+                } else if (busy) {
                     // halves of 64 columns, rolled: unrolled over the tile the code outgrows the
                     // instruction cache that all roles share
                     float mb = -INFINITY;
                     if (tail) {
 #pragma unroll 1
-                        for (int c = 0; c < blocks; ++c) {
+                        for (int c = 0; c < 4; ++c) {
                             const uint32_t vis = visible(seen, first + 32 * c - w.len);
                             float v[32];
                             tmem_ld32(tS + 32u * c, v);
@@ -923,7 +997,6 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                             mb = fmaxf(mb, m1);
                         }
                     }
-                    if (PREFIX && !sees) mb = -INFINITY;
                     mb *= sc;
                     const bool resc = mb > m_used + C::kLag;
                     const float m_new = resc ? mb : m_used;
@@ -943,7 +1016,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                     const float mm = m_used == -INFINITY ? 0.f : m_used - C::kLift;  // nothing seen yet: every weight 2^-inf
                     // P over the scores: block c's 16 columns end before block c + 1's scores begin
 #pragma unroll 1
-                    for (int c = 0; c < blocks; ++c) {
+                    for (int c = 0; c < 4; ++c) {
                         const uint32_t vis = tail ? visible(seen, first + 32 * c - w.len) : 0xffffffffu;
                         float v[32];
                         tmem_ld32(tS + 32u * c, v);
@@ -957,10 +1030,6 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
 #pragma unroll
                             for (int i = 0; i < 32; ++i) v[i] = (vis >> i) & 1u ? v[i] : 0.f;
                         }
-                        if constexpr (PREFIX) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = sees ? v[i] : 0.f;
-                        }
                         uint32_t pk[16];
                         float2 l2 = make_float2(0.f, 0.f);
 #pragma unroll
@@ -971,14 +1040,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                         l += l2.x + l2.y;
                         tmem_st16u(tS + 16u * c, pk);
                     }
-                    if constexpr (PREFIX) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) pk[i] = 0u;
-#pragma unroll 1
-                        for (int c = blocks; c < 4; ++c) tmem_st16u(tS + 16u * c, pk);
-                    }
-                }
+                                }
                 if constexpr (C::kDirect && !PREFIX) {
                     // the tile's V rows behind the sequence, and what is not finite in the drafted rows: one
                     // position per lane of the four warps
