@@ -4,14 +4,19 @@
 namespace qw {
 namespace {
 
-// Merge of the items that were cut: thread = (row, four dims) of one (row tile, KV head), as in tree_tc.cu.  Also fills the rows of
-// sequences that do not fit with NaN, and every row if the prefix does not or a CTA gave up.
-template <int D>
+// Merge of the items that were cut: as in tree_tc.cu, (row, four dims) of one (row tile, KV head), but with SHARES threads in as many warps
+// for each, which take every SHARES-th partial: with one row tile an item has some 20 of them, and the kernel is the latency of their
+// loads (8 KV heads behind a prefix of 32768: 3.9 us with four threads, 7.2 with one; 64 row tiles, whose items are hardly cut,
+// 100 us more).  Also fills the rows of sequences that do not fit with NaN, and every row if the prefix does not or a CTA gave up.
+template <int D, int SHARES>
 __global__ void __launch_bounds__(kMergeThreads) prefix_tc_merge_kernel(const Prefix p, int ctas) {
     const PrefixArgs &a = p.a;
     const int rt = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
     const int nr = min(kTcRows, row_count(p) - rt * kTcRows);
-    const int e = blockIdx.z * kMergeThreads + tid, rl = e % nr, dq = e / nr;
+    constexpr int UNITS = kMergeThreads / SHARES;
+    __shared__ float part[SHARES][UNITS][6];  // a thread's sums and their reference
+    const int share = tid / UNITS, unit = tid % UNITS;
+    const int e = blockIdx.z * UNITS + unit, rl = e % nr, dq = e / nr;
     int b, node, g, len, n, plen;
     p.place(rt * kTcRows + rl, b, node, g);
     const bool fits = lengths(a, b, len, n) && prefix_length(a, plen);
@@ -29,10 +34,34 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_tc_merge_kernel(const Pr
         c1 = (int)(total < (1 << 24) ? ((unsigned)t1 * (unsigned)ctas - 1) / (unsigned)total : (t1 * ctas - 1) / total);
     }
     const bool there = fits && node < n;
-    float num[4] = {0.f, 0.f, 0.f, 0.f}, den = 0.f;
-    if (there) add_partials<D>(p, ctas, total, c0, c1, rl, dq, num, den);
+    float num[4] = {0.f, 0.f, 0.f, 0.f}, den = 0.f, mx = -INFINITY;
+    if (there) add_partials<D>(p, ctas, total, c0, c1, rl, dq, num, den, mx, share, SHARES);
     gave_up = __any_sync(0xffffffffu, gave_up);
-    if (dq >= D / 4 || (fits && !there)) return;
+    if constexpr (SHARES > 1) {
+        float *mine = part[share][unit];
+        mine[0] = mx, mine[1] = den;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mine[2 + k] = num[k];
+        __syncthreads();
+        if (share == 0) {
+            float top = mx;
+#pragma unroll
+            for (int i = 1; i < SHARES; ++i) top = fmaxf(top, part[i][unit][0]);
+            den = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) num[k] = 0.f;
+#pragma unroll
+            for (int i = 0; i < SHARES; ++i) {
+                const float *x = part[i][unit];
+                if (x[0] == -INFINITY && x[1] == 0.f) continue;  // nothing seen
+                const float w = exp2f(x[0] - top);
+                den += x[1] * w;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) num[k] += x[2 + k] * w;
+            }
+        }
+    }
+    if (share != 0 || dq >= D / 4 || (fits && !there)) return;
     if (!fits || gave_up) {
         for (int i = 0; i < 4; ++i) store_out(a, at + i, nanf(""));
         return;
@@ -51,9 +80,11 @@ template <int D>
 cudaError_t launch_prefix_dim(const Prefix &p, const qw_kv_view &prefix, const qw_kv_view &kv, int ctas, cudaStream_t st, bool chained) {
     const cudaError_t e = launch_dim<D>(p, kv, &prefix, ctas, st, chained);
     if (e != cudaSuccess) return e;
-    const int rows = p.n_seq * p.a.n_max * p.a.G, units = std::min(kTcRows, rows) * (D / 4);
-    return launch_k(true, prefix_tc_merge_kernel<D>, dim3((rows + kTcRows - 1) / kTcRows, p.a.Hkv, (units + kMergeThreads - 1) / kMergeThreads),
-                    dim3(kMergeThreads), 0, st, p, ctas);
+    const int rows = p.n_seq * p.a.n_max * p.a.G, nrt = (rows + kTcRows - 1) / kTcRows, units = std::min(kTcRows, rows) * (D / 4);
+    auto merge = [&](auto kernel, int per_block) {
+        return launch_k(true, kernel, dim3(nrt, p.a.Hkv, (units + per_block - 1) / per_block), dim3(kMergeThreads), 0, st, p, ctas);
+    };
+    return nrt * p.a.Hkv * 12 <= ctas ? merge(prefix_tc_merge_kernel<D, 4>, kMergeThreads / 4) : merge(prefix_tc_merge_kernel<D, 1>, kMergeThreads);
 }
 
 size_t starts_bytes(int64_t rows) { return (((rows + kTcRows - 1) / kTcRows + 1) * 8 + 255) / 256 * 256; }

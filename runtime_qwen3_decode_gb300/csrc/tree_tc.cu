@@ -46,8 +46,8 @@ __global__ void __launch_bounds__(kMergeThreads) tree_tc_merge_kernel(const Tree
     for (int i = 0; i < (kTcCtas + 31) / 32; ++i) gave_up |= p.status[min(lane + 32 * i, ctas - 1)];
     const int64_t at = b * a.oseq + (int64_t)p.node_of(r) * a.onode + (int64_t)(h * a.G + r - p.node_of(r) * a.G) * a.ohead + 4 * dq;
     if (dq >= D / 4) c1 = c0;
-    float num[4] = {0.f, 0.f, 0.f, 0.f}, den = 0.f;
-    add_partials<D>(p, ctas, total, c0, c1, rl, dq, num, den);
+    float num[4] = {0.f, 0.f, 0.f, 0.f}, den = 0.f, mx;
+    add_partials<D>(p, ctas, total, c0, c1, rl, dq, num, den, mx);
     gave_up = __any_sync(0xffffffffu, gave_up);
     if (dq >= D / 4) return;
     if (!fits || gave_up) {

@@ -147,6 +147,7 @@ struct Cursor {
     int b, h, rt, tile;
     long long left;
     int first_rt, own_tile;  // PREFIX: of the table of tiles; where in sequence b's own tiles the first segment begins
+    int plen;                // PREFIX: the prefix's length
 };
 
 struct Seg {
@@ -195,7 +196,7 @@ __device__ long long total_work(const Tree &p, int n) {
 
 __device__ Cursor find_start(const Tree &p, long long at, long long left) {
     const int lane = threadIdx.x & 31;
-    Cursor c{p.n_seq, 0, 0, 0, left, 0, 0};
+    Cursor c{p.n_seq, 0, 0, 0, left, 0, 0, 0};
     long long before = 0;
     for (int b0 = 0; b0 < p.n_seq; b0 += 32) {
         const long long own = b0 + lane < p.n_seq ? seq_work(p, b0 + lane) : 0;
@@ -245,7 +246,7 @@ __device__ __forceinline__ void sequences(const Prefix &p, int rt, int &b0, int 
 __device__ __forceinline__ bool next_seg(const Prefix &p, Cursor &c, Seg &s, const unsigned *own) {
     const int nrt = row_tiles(p);
     while (c.left > 0 && c.rt < nrt) {
-        prefix_length(p.a, s.len);
+        s.len = c.plen;
         sequences(p, c.rt, s.b, s.b1);
         unsigned mine = 0;
         if (c.rt - c.first_rt < kOwnTable) mine = own[c.rt - c.first_rt];
@@ -274,26 +275,50 @@ __device__ __forceinline__ bool next_seg(const Prefix &p, Cursor &c, Seg &s, con
 }
 __device__ __forceinline__ bool next_seg(const Tree &p, Cursor &c, Seg &s, const unsigned *) { return next_seg(p, c, s); }
 
-// All warps: tiles of every row tile's sequences into the table at `all` (shared memory that nothing else uses yet).
-__device__ __forceinline__ void own_tables(const Prefix &p, unsigned *all) {
+// Tables in shared memory that nothing else uses yet: tiles of every row tile's sequences [2^20 / 128], and of the sequences
+// themselves while they are few.
+constexpr int kRowTilesMax = (1 << 20) / kTcRows, kSeqTable = 4096;
+struct Tables {
+    unsigned rows[kRowTilesMax];
+    int seq[kSeqTable];
+};
+
+__device__ __forceinline__ int tiles_of(const Prefix &p, const Tables &t, int b) {
+    return p.n_seq <= kSeqTable ? t.seq[b] : own_tiles(p, b);
+}
+
+// All warps.
+__device__ __forceinline__ void own_tables(const Prefix &p, Tables &t) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    if (p.n_seq <= kSeqTable) {
+        for (int b = threadIdx.x; b < p.n_seq; b += blockDim.x) t.seq[b] = own_tiles(p, b);
+        __syncthreads();
+    }
     for (int rt = warp; rt < row_tiles(p); rt += warps) {
         int b0, b1;
         sequences(p, rt, b0, b1);
         unsigned w = 0;
-        for (int b = b0 + lane; b <= b1; b += 32) w += own_tiles(p, b);
+        for (int b = b0 + lane; b <= b1; b += 32) w += tiles_of(p, t, b);
         w = __reduce_add_sync(0xffffffffu, w);
-        if (lane == 0) all[rt] = w;
+        if (lane == 0) t.rows[rt] = w;
     }
 }
 
+__device__ __forceinline__ long long scan64(long long v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
+
 // One whole warp: where this CTA's share begins, and the part of the table that it needs.  CTA 0 leaves the row tiles' starts
-// for the merge.
-__device__ __forceinline__ Cursor find_start(const Prefix &p, const unsigned *all, unsigned *own) {
+// for the merge.  plen: the prefix's length, negative if it does not fit.
+__device__ __forceinline__ Cursor find_start(const Prefix &p, const Tables &t, unsigned *own, int plen) {
     const int lane = threadIdx.x & 31, nrt = row_tiles(p);
-    Cursor c{0, 0, nrt, 0, 0, 0, -1};
-    int plen;
-    if (!prefix_length(p.a, plen)) {
+    Cursor c{0, 0, nrt, 0, 0, 0, -1, plen};
+    if (plen < 0) {
         if (blockIdx.x == 0)
             for (int i = lane; i <= nrt; i += 32) p.starts[i] = 0;
         return c;
@@ -301,13 +326,7 @@ __device__ __forceinline__ Cursor find_start(const Prefix &p, const unsigned *al
     const int ptiles = seq_tiles(plen);
     long long T = 0;
     for (int r0 = 0; r0 < nrt; r0 += 32) {
-        const long long mine = r0 + lane < nrt ? (long long)ptiles + all[r0 + lane] : 0;
-        long long upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += v;
-        }
+        const long long mine = r0 + lane < nrt ? (long long)ptiles + t.rows[r0 + lane] : 0, upto = scan64(mine, lane);
         if (blockIdx.x == 0 && r0 + lane < nrt) p.starts[r0 + lane] = T + upto - mine;
         T += __shfl_sync(0xffffffffu, upto, 31);
     }
@@ -317,31 +336,25 @@ __device__ __forceinline__ Cursor find_start(const Prefix &p, const unsigned *al
     c.left = share_start(T, blockIdx.x + 1, gridDim.x) - at;
     long long before = 0;
     for (int r0 = 0; r0 < nrt && c.left > 0; r0 += 32) {
-        const long long mine = r0 + lane < nrt ? ((long long)ptiles + all[r0 + lane]) * p.a.Hkv : 0;
-        long long upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += v;
-        }
+        const long long mine = r0 + lane < nrt ? ((long long)ptiles + t.rows[r0 + lane]) * p.a.Hkv : 0, upto = scan64(mine, lane);
         const unsigned hit = __ballot_sync(0xffffffffu, before + upto > at);
         if (hit) {
             const int l = __ffs(hit) - 1;
             c.rt = c.first_rt = r0 + l;
-            const long long tiles = __shfl_sync(0xffffffffu, mine, l) / p.a.Hkv;
-            const long long rest = at - before - (__shfl_sync(0xffffffffu, upto, l) - tiles * p.a.Hkv);
-            c.h = (int)(rest / tiles);
+            const long long tiles = (long long)ptiles + t.rows[c.rt];
+            const long long rest = at - before - (__shfl_sync(0xffffffffu, upto, l) - __shfl_sync(0xffffffffu, mine, l));
+            c.h = (int)(T < (1ll << 32) ? (unsigned)rest / (unsigned)tiles : rest / tiles);  // a 64-bit division takes 0.2 us
             c.tile = (int)(rest - c.h * tiles);
             break;
         }
         before += __shfl_sync(0xffffffffu, upto, 31);
     }
-    for (int i = lane; i < kOwnTable; i += 32) own[i] = c.rt + i < nrt ? all[c.rt + i] : 0u;
+    for (int i = lane; i < kOwnTable; i += 32) own[i] = c.rt + i < nrt ? t.rows[c.rt + i] : 0u;
     if (c.rt < nrt && c.tile > ptiles) {  // inside the sequences' own tiles: whose
         int b0, b1, at_tile = c.tile - ptiles;
         sequences(p, c.rt, b0, b1);
         for (; b0 <= b1; b0 += 32) {
-            const int mine = b0 + lane <= b1 ? own_tiles(p, b0 + lane) : 0;
+            const int mine = b0 + lane <= b1 ? tiles_of(p, t, b0 + lane) : 0;
             int upto = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -607,11 +620,13 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
     }
     chain_wait();
     if constexpr (PREFIX) {
-        unsigned *all = reinterpret_cast<unsigned *>(base);  // in the place of operand tiles: 2^20 / 128 row tiles at most
-        own_tables(p, all);
+        Tables &tables = *reinterpret_cast<Tables *>(base);  // in the place of operand tiles
+        static_assert(sizeof(Tables) <= C::kBar, "fits over them");
+        const int plen = *a.plen;  // on its way while the tables are made
+        own_tables(p, tables);
         __syncthreads();
         if (warp == 0) {
-            const Cursor c = find_start(p, all, own);
+            const Cursor c = find_start(p, tables, own, plen >= 0 && plen <= a.p_max ? plen : -1);
             if (lane == 0) *start = c;
         }
         fence_async_shared();  // before copies write there
@@ -1437,22 +1452,23 @@ constexpr int kMergeBatch = 10;
 
 // The partials of one row and four dims (4 dq ..) of an item that CTAs c0 .. c1 had parts of, added in order: num / den.  `total`:
 // tiles of all CTAs.  The loads of kMergeBatch partials are in flight at once: the merge is nothing but their latency.
+// first, step: which of them (mx is the greatest maximum of those).
 template <int D, bool PREFIX>
 __device__ __forceinline__ void add_partials(const TcParams<PREFIX> &p, int ctas, long long total, int c0, int c1, int rl, int dq,
-                                             float (&num)[4], float &den) {
+                                             float (&num)[4], float &den, float &mx, int first = 0, int step = 1) {
     // c0 holds the item's first tile: its second slot; the later CTAs begin inside the item: their
     // first.  Where there are more CTAs than tiles some shares are empty.
     const size_t slot = (size_t)(D + 2) * p.rows_max;
     const bool gaps = total < ctas;
     auto partial = [&](int c) { return p.part + (size_t)(2 * c + (c == c0 ? 1 : 0)) * slot + rl; };
     auto holds = [&](int c) { return c <= c1 && !(gaps && share_start(total, c, ctas) == share_start(total, c + 1, ctas)); };
-    float mx = -INFINITY;
-    for (int c = c0; c0 < c1 && c <= c1; c += kMergeBatch) {
+    mx = -INFINITY;
+    for (int c = c0 + first; c0 < c1 && c <= c1; c += kMergeBatch * step) {
         float m[kMergeBatch], l[kMergeBatch], v[kMergeBatch][4], top = mx;
 #pragma unroll
         for (int i = 0; i < kMergeBatch; ++i) {
-            const bool is = holds(c + i);
-            const float *src = partial(c + i);
+            const bool is = holds(c + i * step);
+            const float *src = partial(c + i * step);
             m[i] = is ? src[(size_t)D * p.rows_max] : -INFINITY;
             l[i] = is ? src[(size_t)(D + 1) * p.rows_max] : 0.f;
 #pragma unroll

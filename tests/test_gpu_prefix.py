@@ -281,3 +281,58 @@ def test_same_result_every_time_on_a_stream_and_in_a_graph(qw, dt, kind):
     now = qw.prefix_attention(*views, q, lens, plen)
     torch.cuda.synchronize()
     assert torch.equal(outs[0], now) and torch.equal(outs[1], now) and not torch.equal(now, want)
+
+
+@pytest.mark.parametrize("dt,kind", [(F32, "f32"), (BF16, "bf16"), (F16, "int8")])
+@pytest.mark.parametrize("tc", [False, True])
+def test_thousands_of_sequences_most_without_rows(qw, dt, kind, tc):
+    """More sequences than the tables in shared memory hold, and row tiles without any key between ones with some."""
+    B, D = 9001, 64
+    g = gen(21)
+    pre, own = make_prefix(kind, (1, 1, 30, D), g, tc), make_cache(kind, (B, 1, 9, D), g)
+    q = torch.randn((B, 1, 2, D), generator=g, device="cuda").to(dt)
+    counts = torch.zeros(B, dtype=torch.int32, device="cuda")
+    there = [0, 1, 63, 64, 4095, 4096, 4097, 8999, 9000]
+    counts[there] = 1
+    lens = torch.randint(0, 8, (B,), generator=g, device="cuda", dtype=torch.int32)
+    for P in (0, 30):
+        out = torch.full_like(q, 7.0)
+        qw.prefix_attention(qw.KvView(*pre), qw.KvView(*own), q, lens, i32(P), out=out, counts=counts, max_len=8,
+                            max_prefix=ROOM if tc else 30)
+        cache = [None if o is None else torch.cat([p[:, :, :P].expand(len(there), -1, -1, -1), o[there]], 2) for p, o in zip(pre, own)]
+        n = [P + int(lens[b]) for b in there]
+        mask = torch.ones((len(there), 1), dtype=torch.int64, device="cuda")
+        ref, mag, vmax = tree_reference(q[there], cache, mask, n, [1] * len(there), D ** -0.5)
+        assert ((out[there].double() - ref).abs() <= tolerance(dt, kind, mag, vmax, max(n) + 1, D)).all()
+        rest = torch.ones(B, dtype=torch.bool, device="cuda")
+        rest[there] = False
+        assert (out[rest] == 7.0).all()
+
+
+@pytest.mark.parametrize("tc", [False, True])
+def test_offsets_past_32_bits(qw, tc):
+    """Sequences and heads whose rows lie more than 2^32 bytes apart."""
+    g = gen(22)
+    far = (1 << 31) + 64
+    big = torch.empty(3 * far + 200 * 64, dtype=BF16, device="cuda")
+
+    def plane(shape, strides, at):
+        t = big.as_strided(shape, (*strides, 1), at)
+        t.copy_(torch.randn(shape, generator=g, device="cuda"))
+        return t
+    own = [plane((3, 2, 20, 64), (far, 32 * 64, 64), 0), plane((3, 2, 20, 64), (far, 32 * 64, 64), 100 * 64)]
+    room = ROOM if tc else 40
+    pre = [torch.randn((1, 2, room, 64), generator=g, device="cuda").to(BF16) for _ in range(2)]
+    q = torch.randn((3, 1, 4, 64), generator=g, device="cuda").to(BF16)
+    lens = i32(19, 0, 7)
+    got = qw.prefix_attention(qw.KvView(*pre), qw.KvView(*own), q, lens, i32(33), max_len=19, max_prefix=room)
+    mask = torch.ones((3, 1), dtype=torch.int64, device="cuda")
+    own += [None, None]
+    ref, mag, vmax = tree_reference(q, joined(pre + [None, None], own, 33), mask, [52, 33, 40], [1] * 3, 64 ** -0.5)
+    assert ((got.double() - ref).abs() <= tolerance(BF16, "bf16", mag, vmax, 53, 64)).all()
+    # and a prefix whose heads lie that far apart
+    pre = [plane((1, 2, 40, 64), (far, far, 64), at) for at in (0, 50 * 64)]
+    near = make_cache("bf16", (3, 2, 20, 64), g)
+    got = qw.prefix_attention(qw.KvView(*pre), qw.KvView(*near), q, lens, i32(33), max_len=19, max_prefix=40)
+    ref, mag, vmax = tree_reference(q, joined(pre + [None, None], near, 33), mask, [52, 33, 40], [1] * 3, 64 ** -0.5)
+    assert ((got.double() - ref).abs() <= tolerance(BF16, "bf16", mag, vmax, 53, 64)).all()

@@ -263,3 +263,34 @@ def oracle_word(old):
     x = (((old >> 18) ^ old) >> 27) & 0xFFFFFFFF
     rot = old >> 59
     return ((x >> rot) | (x << ((32 - rot) & 31))) & 0xFFFFFFFF
+
+
+def test_the_largest_vocabulary_and_rows_far_apart(qw):
+    """2^24 tokens, all of one CTA's in the same part of a pass; rows more than 2^32 bytes apart."""
+    V = 1 << 24
+    x = torch.zeros((1, V), dtype=F16, device="cuda")
+    kept = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for u in (0.0, 0.3, 1 - 2 ** -24):
+        tok = qw.sample_rows(x, torch.tensor([u], device="cuda"), kept=kept)
+        # equal weights: token j is drawn for u in [j / V, (j + 1) / V); u is an f32
+        assert int(tok) == int(np.float64(np.float32(u)) * V) and int(kept) == V
+    tok = qw.sample_rows(x, torch.tensor([0.5], device="cuda"), top_p=torch.tensor([0.25], device="cuda"), kept=kept)
+    assert int(kept) == V // 4 and int(tok) == V // 8
+    far = (1 << 31) + 5
+    big = torch.empty(2 * far, dtype=F16, device="cuda")
+    rows = big.as_strided((2, 5000), (far, 1), 3)
+    rows.copy_(peaked(gen(4), 2, 5000))
+    check(qw, rows, np.array([0.4, 0.7], np.float32), 0.9, 50, 0.9, None, out_sure=0.5)
+
+
+@pytest.mark.parametrize("R", [300, 2100])
+def test_many_rows_with_settings_of_their_own(qw, R):
+    """Rows that take the short way and the long one in one call, in more than one wave."""
+    g = gen(R)
+    x = peaked(g, R, 3001)
+    r = np.random.default_rng(R)
+    t = np.where(r.random(R) < 0.2, 0, r.uniform(0.3, 3, R)).astype(np.float32)
+    k = np.where(r.random(R) < 0.5, 0, r.integers(1, 3000, R)).astype(np.int32)
+    p = np.where(r.random(R) < 0.5, 1, r.uniform(0.2, 1, R)).astype(np.float32)
+    m = np.where(r.random(R) < 0.5, 0, r.uniform(0, 0.2, R)).astype(np.float32)
+    check(qw, x, r.random(R).astype(np.float32), t, k, p, m, out_sure=0.9)
