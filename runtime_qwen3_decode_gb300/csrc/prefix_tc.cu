@@ -22,12 +22,18 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_tc_merge_kernel(const Pr
     const bool fits = lengths(a, b, len, n) && prefix_length(a, plen);
     const int64_t at = b * a.oseq + (int64_t)node * a.onode + (int64_t)(h * a.G + g) * a.ohead + 4 * dq;
     chain_wait();
-    const long long first = p.starts[rt], tiles = p.starts[rt + 1] - first, total = p.starts[row_tiles(p)] * a.Hkv;
+    const int nrt = row_tiles(p);
+    const long long first = p.starts[rt], tiles = p.starts[rt + 1] - first, whole = p.starts[nrt];
+    const bool by_item = p.starts[nrt + 1] != 0;
+    const long long total = by_item ? ctas : whole * a.Hkv;  // no share is empty where items have CTAs of their own
     int gave_up = 0;
 #pragma unroll
     for (int i = 0; i < (kTcCtas + 31) / 32; ++i) gave_up |= p.status[min(lane + 32 * i, ctas - 1)];
     int c0 = 0, c1 = 0;
-    if (tiles > 0 && dq < D / 4) {
+    if (by_item && dq < D / 4) {
+        const int k = (int)tiles / a.Hkv;
+        if (k > 0) c0 = (int)first + h * k, c1 = c0 + k - 1;
+    } else if (tiles > 0 && dq < D / 4) {
         // owner of tile t: the largest c with T c / C <= t
         const long long t0 = first * a.Hkv + h * tiles, t1 = t0 + tiles;
         c0 = (int)(total < (1 << 24) ? ((unsigned)(t0 + 1) * (unsigned)ctas - 1) / (unsigned)total : ((t0 + 1) * ctas - 1) / total);
@@ -87,7 +93,7 @@ cudaError_t launch_prefix_dim(const Prefix &p, const qw_kv_view &prefix, const q
     return nrt * p.a.Hkv * 12 <= ctas ? merge(prefix_tc_merge_kernel<D, 4>, kMergeThreads / 4) : merge(prefix_tc_merge_kernel<D, 1>, kMergeThreads);
 }
 
-size_t starts_bytes(int64_t rows) { return (((rows + kTcRows - 1) / kTcRows + 1) * 8 + 255) / 256 * 256; }
+size_t starts_bytes(int64_t rows) { return (((rows + kTcRows - 1) / kTcRows + 2) * 8 + 255) / 256 * 256; }
 
 }  // namespace
 

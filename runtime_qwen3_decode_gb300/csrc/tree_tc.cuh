@@ -112,7 +112,7 @@ struct TcParams {
     int n_seq, rows_max;  // rows_max: query rows per partial slot (a multiple of 4)
     int *status;
     float *part;          // [2 CTAs][D + 2][rows_max]
-    long long *starts;    // PREFIX: [row tiles + 1] tiles of a KV head before each tile of rows
+    long long *starts;    // PREFIX: [row tiles + 2] tiles of a KV head before each tile of rows, and 0; or its first CTA, and 1
     unsigned long long inv_g;  // 2^32 / G + 1: row / G for the at most 4096 rows of a KV head
     __device__ __forceinline__ int node_of(int row) const { return (int)((unsigned)row * inv_g >> 32); }
     // The sequence, node and head of its group of row r: of KV head's rows of sequence b, or (PREFIX) of all sequences.
@@ -313,42 +313,9 @@ __device__ __forceinline__ long long scan64(long long v, int lane) {
     return v;
 }
 
-// One whole warp: where this CTA's share begins, and the part of the table that it needs.  CTA 0 leaves the row tiles' starts
-// for the merge.  plen: the prefix's length, negative if it does not fit.
-__device__ __forceinline__ Cursor find_start(const Prefix &p, const Tables &t, unsigned *own, int plen) {
-    const int lane = threadIdx.x & 31, nrt = row_tiles(p);
-    Cursor c{0, 0, nrt, 0, 0, 0, -1, plen};
-    if (plen < 0) {
-        if (blockIdx.x == 0)
-            for (int i = lane; i <= nrt; i += 32) p.starts[i] = 0;
-        return c;
-    }
-    const int ptiles = seq_tiles(plen);
-    long long T = 0;
-    for (int r0 = 0; r0 < nrt; r0 += 32) {
-        const long long mine = r0 + lane < nrt ? (long long)ptiles + t.rows[r0 + lane] : 0, upto = scan64(mine, lane);
-        if (blockIdx.x == 0 && r0 + lane < nrt) p.starts[r0 + lane] = T + upto - mine;
-        T += __shfl_sync(0xffffffffu, upto, 31);
-    }
-    if (blockIdx.x == 0 && lane == 0) p.starts[nrt] = T;
-    T *= p.a.Hkv;
-    const long long at = share_start(T, blockIdx.x, gridDim.x);
-    c.left = share_start(T, blockIdx.x + 1, gridDim.x) - at;
-    long long before = 0;
-    for (int r0 = 0; r0 < nrt && c.left > 0; r0 += 32) {
-        const long long mine = r0 + lane < nrt ? ((long long)ptiles + t.rows[r0 + lane]) * p.a.Hkv : 0, upto = scan64(mine, lane);
-        const unsigned hit = __ballot_sync(0xffffffffu, before + upto > at);
-        if (hit) {
-            const int l = __ffs(hit) - 1;
-            c.rt = c.first_rt = r0 + l;
-            const long long tiles = (long long)ptiles + t.rows[c.rt];
-            const long long rest = at - before - (__shfl_sync(0xffffffffu, upto, l) - __shfl_sync(0xffffffffu, mine, l));
-            c.h = (int)(T < (1ll << 32) ? (unsigned)rest / (unsigned)tiles : rest / tiles);  // a 64-bit division takes 0.2 us
-            c.tile = (int)(rest - c.h * tiles);
-            break;
-        }
-        before += __shfl_sync(0xffffffffu, upto, 31);
-    }
+// The part of the table that this CTA needs, and where in whose own tiles its first segment begins.
+__device__ __forceinline__ void find_own(const Prefix &p, const Tables &t, unsigned *own, Cursor &c, int ptiles, int lane) {
+    const int nrt = row_tiles(p);
     for (int i = lane; i < kOwnTable; i += 32) own[i] = c.rt + i < nrt ? t.rows[c.rt + i] : 0u;
     if (c.rt < nrt && c.tile > ptiles) {  // inside the sequences' own tiles: whose
         int b0, b1, at_tile = c.tile - ptiles;
@@ -371,6 +338,74 @@ __device__ __forceinline__ Cursor find_start(const Prefix &p, const Tables &t, u
             at_tile -= __shfl_sync(0xffffffffu, upto, 31);
         }
     }
+}
+
+// One whole warp: where this CTA's share begins, and the part of the table that it needs.  CTA 0 leaves the row tiles' starts
+// for the merge.  plen: the prefix's length, negative if it does not fit.
+__device__ __forceinline__ Cursor find_start(const Prefix &p, const Tables &t, unsigned *own, int plen) {
+    const int lane = threadIdx.x & 31, nrt = row_tiles(p);
+    Cursor c{0, 0, nrt, 0, 0, 0, -1, plen};
+    if (plen < 0) {
+        if (blockIdx.x == 0)
+            for (int i = lane; i <= nrt + 1; i += 32) p.starts[i] = 0;
+        return c;
+    }
+    const int ptiles = seq_tiles(plen);
+    long long T = 0;
+    for (int r0 = 0; r0 < nrt; r0 += 32) {
+        const long long mine = r0 + lane < nrt ? (long long)ptiles + t.rows[r0 + lane] : 0, upto = scan64(mine, lane);
+        if (blockIdx.x == 0 && r0 + lane < nrt) p.starts[r0 + lane] = T + upto - mine;
+        T += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    if (blockIdx.x == 0 && lane == 0) p.starts[nrt] = T, p.starts[nrt + 1] = 0;
+    T *= p.a.Hkv;
+    const int C = (int)gridDim.x;
+    if (nrt * p.a.Hkv * 2 <= C && T > 0 && T < (1ll << 31)) {
+        // Few items: each to CTAs of its own if that makes no share longer than two tiles more.  A CTA whose share spans two items ends
+        // one with an epilogue and waits for the next one's queries, which is some 5 us.
+        const unsigned fair = (unsigned)((T + C - 1) / C), size = fair + (unsigned)lane;
+        unsigned need = 0;
+        for (int rt = 0; rt < nrt; ++rt) need += (unsigned)p.a.Hkv * ((ptiles + t.rows[rt] + size - 1u) / size);
+        const unsigned fit = __ballot_sync(0xffffffffu, need <= (unsigned)C);
+        if (fit & 7u) {
+            const unsigned longest = fair + (unsigned)__ffs(fit) - 1u;
+            int base = 0;
+            for (int rt = 0; rt < nrt; ++rt) {
+                const unsigned tiles = ptiles + t.rows[rt];
+                const int k = (int)((tiles + longest - 1u) / longest), at = (int)blockIdx.x - base;
+                if (blockIdx.x == 0 && lane == 0) p.starts[rt] = base;
+                if (at >= 0 && at < p.a.Hkv * k) {
+                    const int j = at % k;
+                    c.rt = c.first_rt = rt;
+                    c.h = at / k;
+                    c.tile = (int)((long long)tiles * j / k);
+                    c.left = (int)((long long)tiles * (j + 1) / k) - c.tile;
+                }
+                base += p.a.Hkv * k;
+            }
+            if (blockIdx.x == 0 && lane == 0) p.starts[nrt] = base, p.starts[nrt + 1] = 1;
+            find_own(p, t, own, c, ptiles, lane);
+            return c;
+        }
+    }
+    const long long at = share_start(T, blockIdx.x, gridDim.x);
+    c.left = share_start(T, blockIdx.x + 1, gridDim.x) - at;
+    long long before = 0;
+    for (int r0 = 0; r0 < nrt && c.left > 0; r0 += 32) {
+        const long long mine = r0 + lane < nrt ? ((long long)ptiles + t.rows[r0 + lane]) * p.a.Hkv : 0, upto = scan64(mine, lane);
+        const unsigned hit = __ballot_sync(0xffffffffu, before + upto > at);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            c.rt = c.first_rt = r0 + l;
+            const long long tiles = (long long)ptiles + t.rows[c.rt];
+            const long long rest = at - before - (__shfl_sync(0xffffffffu, upto, l) - __shfl_sync(0xffffffffu, mine, l));
+            c.h = (int)(T < (1ll << 32) ? (unsigned)rest / (unsigned)tiles : rest / tiles);  // a 64-bit division takes 0.2 us
+            c.tile = (int)(rest - c.h * tiles);
+            break;
+        }
+        before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    find_own(p, t, own, c, ptiles, lane);
     return c;
 }
 
