@@ -378,9 +378,10 @@ __device__ __forceinline__ void sort_keys(u64 (&key)[K], u64 *buf, u64 *other_bu
                     for (int k = 0; k < K; ++k) {
                         if (k & s) continue;
                         const bool down = ((K * tid + k) & size) == 0;
-                        const u64 hi = max(key[k], key[k | s]), lo = min(key[k], key[k | s]);
-                        key[k] = down ? hi : lo;
-                        key[k | s] = down ? lo : hi;
+                        const u64 a = key[k], b = key[k | s];
+                        const bool swap = (b > a) == down;
+                        key[k] = swap ? b : a;
+                        key[k | s] = swap ? a : b;
                     }
                 }
                 continue;
@@ -394,7 +395,7 @@ __device__ __forceinline__ void sort_keys(u64 (&key)[K], u64 *buf, u64 *other_bu
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
                     const u64 other = buf[k * kThreads + (tid ^ far)];
-                    key[k] = greater ? max(key[k], other) : min(key[k], other);
+                    key[k] = (other > key[k]) == greater ? other : key[k];
                 }
                 u64 *t = buf;
                 buf = other_buf;
@@ -403,7 +404,7 @@ __device__ __forceinline__ void sort_keys(u64 (&key)[K], u64 *buf, u64 *other_bu
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
                     const u64 other = shfl_xor64(key[k], far);
-                    key[k] = greater ? max(key[k], other) : min(key[k], other);
+                    key[k] = (other > key[k]) == greater ? other : key[k];
                 }
             }
         }
