@@ -920,12 +920,16 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
             w.start(p, s);
             int walked = 0;
             for (int j = (it & 1) == grp ? 0 : 1; ok && j < nt; j += 2, ++mine) {
-                for (; walked <= j; ++walked) {
-                    if (walked > 0) w.next(p);
-                    if (PREFIX && !w.pre && w.b == mb_) {
-                        if (own_hi == 0) own_lo = w.pos;
-                        own_hi = min(w.pos + kTcTile, w.end);
+                if constexpr (PREFIX) {
+                    for (; walked <= j; ++walked) {
+                        if (walked > 0) w.next(p);
+                        if (!w.pre && w.b == mb_) {
+                            if (own_hi == 0) own_lo = w.pos;
+                            own_hi = min(w.pos + kTcTile, w.end);
+                        }
                     }
+                } else {
+                    w.pos = (s.t0 + j) * kTcTile;
                 }
                 const int jj = it + j;
                 const unsigned par = (unsigned)(jj >> 1) & 1u;
@@ -1264,15 +1268,17 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
             const __half *scales = plane ? a.vs : a.ks;
             __half sc[2][U];  // this tile's and the next one's
             while (ok && next_seg(p, cur, s, own)) {
+                const __half *own_scales = scales + s.b * a.sseq + s.h * a.shead + g;
                 auto plane_scales = [&](const Walk<PREFIX> &x, int64_t &stride) {
+                    stride = a.spos;
                     if constexpr (PREFIX) {
                         if (x.pre) {
                             stride = a.pspos;
                             return (plane ? a.pvs : a.pks) + s.h * a.pshead + g;
                         }
+                        return scales + x.b * a.sseq + s.h * a.shead + g;
                     }
-                    stride = a.spos;
-                    return scales + x.b * a.sseq + s.h * a.shead + g;
+                    return own_scales;
                 };
                 auto fetch = [&](__half(&x)[U], const Walk<PREFIX> &at) {
                     int64_t stride;
