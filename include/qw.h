@@ -428,7 +428,8 @@ int qw_tree_attention(const qw_kv_view *kv, const qw_tree_attention_args *args, 
  *   sum_j softmax_j(scale q . k_j) v_j over the prefix's and its own positions j that it sees, 0 if it sees none.
  * args, its rows that are left as they were and its arithmetic are qw_tree_attention's; what one sequence holds does not
  * reach another one, NaN and infinities included.  A prefix_len outside [0, prefix->max_ctx] makes every row NaN.
- * max_prefix: about the prefix's length as the host knows it (see max_len).  n_seq x n_max x query heads of a KV head <= 2^20.
+ * max_prefix: about the prefix's length as the host knows it (see max_len).  A scratch for some sizes does for smaller ones.
+ * n_seq x n_max x query heads of a KV head <= 2^20.
  */
 size_t qw_prefix_attention_scratch_bytes(const qw_kv_view *prefix, const qw_kv_view *kv, int32_t n_max, int32_t n_heads,
                                          int32_t max_len, int32_t max_prefix);

@@ -493,15 +493,17 @@ void fill(TreeArgs &a, const qw_kv_view &kv, const qw_tree_attention_args &t, vo
 
 }  // namespace
 
-// For every call with these sizes and these lengths or less: a plan's splits are no more than tiles, nor than its share of 4 x 152
-// blocks gives the tiles of at most 32 rows.
+// For every call with these numbers of sequences and rows and these lengths or less.  A plan's splits are no more than tiles, nor,
+// as it has at most 4 x 152 shares of them, than 4 x 152 / (blocks of at most 32 rows) + 1; with n rows in such blocks that are
+// 4 x 152 min(n, 32) + n partials, which no larger n makes fewer.
 size_t prefix_attn_scratch_bytes(const qw_kv_view &kv, int n_max, int n_heads, int max_len, int max_prefix) {
     const int64_t rows = (int64_t)n_max * (n_heads / kv.n_kv_heads), all = rows * kv.n_seq, most = 4 * 152;
     const int64_t own = (max_len + n_max + kTile - 1) / kTile, pre = std::max((max_prefix + kTile - 1) / kTile, 1);
-    const int64_t Sp = std::min(pre, most / (kv.n_kv_heads * ((all + 31) / 32)) + 1);
-    const int64_t So = std::min(own, most / (kv.n_kv_heads * ((rows + 31) / 32) * kv.n_seq) + 1);
+    const int64_t heads = all * kv.n_kv_heads;
+    const int64_t parts = std::min(heads * pre, most * std::min<int64_t>(all, 32) + heads) +
+                          std::min(heads * own, most * std::min<int64_t>(rows, 32) + heads);
     if (plan_prefix(kv.n_seq, kv.n_kv_heads, n_max, n_heads / kv.n_kv_heads, max_len, max_prefix).blocks > INT32_MAX) return 0;
-    const size_t cores = ((size_t)(all * kv.n_kv_heads * (Sp + So)) * (kv.head_dim + 2) * 4 + 255) / 256 * 256;
+    const size_t cores = ((size_t)parts * (kv.head_dim + 2) * 4 + 255) / 256 * 256;
     return std::max(cores, prefix_tc_scratch_bytes(all, kv.head_dim));
 }
 

@@ -61,6 +61,20 @@ def test_scratch_of_a_bound_covers_shorter_lengths(qw):  # noqa: F811
                 last = now
 
 
+@pytest.mark.parametrize("Hkv,G", [(8, 2), (2, 7), (1, 64), (3, 3)])
+def test_scratch_covers_fewer_sequences_and_rows(qw, Hkv, G):  # noqa: F811
+    def need(n_seq, n_max, ctx):
+        big = dict(max_ctx=ctx, n_kv_heads=Hkv, seq_stride=Hkv * ctx * 128, head_stride=ctx * 128, scale_seq_stride=Hkv * ctx * 4,
+                   scale_head_stride=ctx * 4)
+        p, o = view(qw, n_seq=1, **big), view(qw, n_seq=n_seq, **big)
+        return qw.lib().qw_prefix_attention_scratch_bytes(ctypes.byref(p), ctypes.byref(o), n_max, Hkv * G, ctx, ctx)
+    for ctx in (64, 700, 4096, 32768):
+        for other in (1, 3, 8):
+            by_seq = [need(n, other, ctx) for n in range(1, 70)]
+            by_row = [need(other, n, ctx) for n in range(1, 65)]
+            assert by_seq == sorted(by_seq) and by_row == sorted(by_row) and min(by_seq + by_row) > 0
+
+
 def sample(lib, **kw):
     d = dict(logits=P, dtype=lib.DT_F32, n_rows=2, vocab=100, row_stride=100, u=P, temperature=P, top_k=P, top_p=P, min_p=P, tokens=P,
              probs=P, kept=P)
