@@ -347,7 +347,7 @@ template <int B>
 __device__ unsigned edge_of(const Cut<B> &c, int j, unsigned low, unsigned high) {
     const unsigned lane = threadIdx.x & 31;
     unsigned no = low, yes = high + 1u;  // below `no` it is not, from `yes` on it is
-    const unsigned guess = min(max(ord_bits(c.top - (float)(j + 1) / c.inv), low), high);
+    const unsigned guess = min(max(ord_bits(c.top - __fdividef((float)(j + 1), c.inv)), low), high);
     const unsigned from = guess - min(guess - low, 16u), o = from + lane;
     const unsigned is = __ballot_sync(0xffffffffu, o <= high && c.slot(ord_value(o)) <= j);
     const unsigned in = __ballot_sync(0xffffffffu, o <= high);
@@ -725,8 +725,9 @@ __global__ void __launch_bounds__(kThreads, B == kFewBins ? 2 : 1) sample_rows_k
                     const Total x = sh.cum[i], y = i ? sh.cum[i - 1] : Total{0ull, 0u, 0u};
                     return stage == 0 ? (float)(x.n - y.n) : (float)(x.w - y.w);
                 };
-                const float g = sqrtf(held(b + 1) / held(b - 1)), share = (float)(goal - (stage == 0 ? (u64)before.n : before.w)) / held(b);
-                near = fabsf(g - 1.f) < 1e-3f ? share : __logf(1.f + share * (g - 1.f)) / __logf(g);
+                const float lg = 0.5f * __logf(__fdividef(held(b + 1), held(b - 1))), g = __expf(lg);
+                const float share = __fdividef((float)(goal - (stage == 0 ? (u64)before.n : before.w)), held(b));
+                near = fabsf(g - 1.f) < 1e-3f ? share : __fdividef(__logf(1.f + share * (g - 1.f)), lg);
                 if (!(near >= 0.f && near <= 1.f)) near = -1.f;
             }
             z.inside = Total{t.w - before.w, t.n - before.n, t.low - before.low};
@@ -764,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, B == kFewBins ? 2 : 1) sample_rows_k
                 if (part > fmaxf(fabsf(xl), fabsf(xh)) * 1e-6f) c.top = xh - near * B * width + B / 2 * part, c.inv = 1.f / part;
             }
             c.shift = 0;
-            while ((z.end - z.lo - 1ull) >> c.shift >= (u64)B) ++c.shift;
+            if (z.end - z.lo > (u64)B) c.shift = 64 - __clzll((long long)((z.end - z.lo - 1ull) / B));
             pass = kNarrow;
             continue;
         }

@@ -1094,7 +1094,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                         l += l2.x + l2.y;
                         tmem_st16u(tS + 16u * c, pk);
                     }
-                                }
+                }
                 if constexpr (C::kDirect && !PREFIX) {
                     // the tile's V rows behind the sequence, and what is not finite in the drafted rows: one
                     // position per lane of the four warps
