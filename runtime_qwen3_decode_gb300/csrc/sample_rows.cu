@@ -187,6 +187,7 @@ struct Shared {
     u64 scan[kWarps];
     unsigned listed, edge[2];
     int first[3];
+    float near;                         // see below
     float cut;                          // the least logit that min_p keeps
     float at;                           // the logit from which on tokens are listed
 };
@@ -295,12 +296,14 @@ __device__ __forceinline__ void tally(const P &piece, Shared<B> &sh, const Row &
 #pragma unroll
         for (int k = 0; k < 4; ++k) bins[b[k] * kThreads + tid] += w[k];
     }
+    // 32 lanes' sums, the weights' in three words of 27 bits, which leave room for them
     auto add = [&](u64 &w, unsigned &n) {
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            w += shfl_xor64(w, o);
-            n += __shfl_xor_sync(0xffffffffu, n, o);
-        }
+        n = __reduce_add_sync(0xffffffffu, n);
+        if constexpr (!WEIGHED) return;
+        constexpr unsigned kWord = (1u << 27) - 1u;
+        const unsigned a = __reduce_add_sync(0xffffffffu, (unsigned)w & kWord), b = __reduce_add_sync(0xffffffffu, (unsigned)(w >> 27) & kWord),
+                       c = __reduce_add_sync(0xffffffffu, (unsigned)(w >> 54));
+        w = (u64)a + ((u64)b << 27) + ((u64)c << 54);
     };
     __syncthreads();
     const unsigned ctas = cl.num_blocks(), me = cl.block_rank();
@@ -718,7 +721,8 @@ __global__ void __launch_bounds__(kThreads, B == kFewBins ? 2 : 1) sample_rows_k
             const int b = there ? min(__ffs(there) - 1, B - 1) : B - 1;
             before = b ? total[b - 1] : Total{0ull, 0u, 0u};
             t = total[b];
-            if (from_octaves && b > 0 && b < B - 2) {
+            const bool inner = from_octaves && b > 0 && b < B - 2;
+            if (inner && warp == 2) {
                 // About where in the octave the border is, if what octaves hold grows by the same factor g^2 from the one above to the
                 // one below: 1 + share (g - 1) = g^near.
                 auto held = [&](int i) {
@@ -728,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, B == kFewBins ? 2 : 1) sample_rows_k
                 const float lg = 0.5f * __logf(__fdividef(held(b + 1), held(b - 1))), g = __expf(lg);
                 const float share = __fdividef((float)(goal - (stage == 0 ? (u64)before.n : before.w)), held(b));
                 near = fabsf(g - 1.f) < 1e-3f ? share : __fdividef(__logf(1.f + share * (g - 1.f)), lg);
-                if (!(near >= 0.f && near <= 1.f)) near = -1.f;
+                if (lane == 0) sh.near = near >= 0.f && near <= 1.f ? near : -1.f;
             }
             z.inside = Total{t.w - before.w, t.n - before.n, t.low - before.low};
             z.above = Total{z.above.w + before.w, z.above.n + before.n, z.above.low + before.low};
@@ -741,6 +745,7 @@ __global__ void __launch_bounds__(kThreads, B == kFewBins ? 2 : 1) sample_rows_k
                 __syncthreads();
                 if (b > 0) z.end = min(z.end, (u64)sh.edge[0] << a.id_bits);
                 if (b < B - 1) z.lo = max(z.lo, (u64)sh.edge[1] << a.id_bits);
+                near = inner ? sh.near : -1.f;
             } else {
                 z.lo += (u64)(B - 1 - b) << c.shift;
                 z.end = min(z.end, z.lo + (1ull << c.shift));
