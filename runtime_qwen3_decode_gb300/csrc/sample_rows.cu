@@ -240,11 +240,11 @@ struct Piece {
             return make_float4(v[0], v[1], v[2], v[3]);
         }
     }
+    __device__ __forceinline__ float one(int i) const { return RES ? kept[i] : canonical(elem_to_f(src[begin + i])); }
 };
 
 // One pass: every token of the zone is counted in the part of it that the cut gives, and weighed if asked; sh.total has
-// the cluster's sums.  Each thread has bins of its own.  No branch but the one past four tokens outside: the others'
-// numbers are 0 and go to the last bin.  ROW: the zone has no upper end and is cut by logits.
+// the cluster's sums.  Each thread has bins of its own.  ROW: the zone has no upper end and is cut by logits.
 template <int B, bool WEIGHED, bool ROW, typename P>
 __device__ __forceinline__ void tally(const P &piece, Shared<B> &sh, const Row &row, u64 *bins, cg::cluster_group &cl, int turn,
                                       const Zone &z, const Cut<B> &c, int id_bits) {
@@ -257,44 +257,76 @@ __device__ __forceinline__ void tally(const P &piece, Shared<B> &sh, const Row &
 #pragma unroll
     for (int b = 0; b < B; ++b) bins[b * kThreads + tid] = 0ull;
     const int quads = piece.quads();
-    for (int g = tid; g < quads; g += kThreads) {
-        const float4 v = piece.at(g);
-        const float x[4] = {v.x, v.y, v.z, v.w};
-        int b[4];
-        bool is[4];
+    if constexpr (ROW) {
+        // No branch but the one past four tokens outside: the others' numbers are 0 and go to the last bin.
+        for (int g = tid; g < quads; g += kThreads) {
+            const float4 v = piece.at(g);
+            const float x[4] = {v.x, v.y, v.z, v.w};
+            bool is[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            is[k] = x[k] >= xl;
-            if constexpr (!ROW) is[k] &= x[k] <= xh;
-            b[k] = c.slot(x[k]);
+            for (int k = 0; k < 4; ++k) is[k] = x[k] >= xl;
+            if (ties) {  // the zone's end is between tokens of one logit
+#pragma unroll
+                for (int k = 0; k < 4; ++k) is[k] &= !((x[k] == xl) & (piece.begin + 4 * g + k > last));
+            }
+            if (!(is[0] | is[1] | is[2] | is[3])) continue;
+            u64 w[4] = {0ull, 0ull, 0ull, 0ull};
+            if constexpr (WEIGHED) {
+                u64 a[2], c[2];
+                weigh2(row, sh.table, make_float2(x[0], x[1]), a);
+                weigh2(row, sh.table, make_float2(x[2], x[3]), c);
+                w[0] = a[0], w[1] = a[1], w[2] = c[0], w[3] = c[1];
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) bins[(is[k] ? c.slot(x[k]) : B - 1) * kThreads + tid] += is[k] ? w[k] + (1ull << kCountBit) : 0ull;
         }
-        if (ties) {  // an end of the zone is between tokens of one logit
+    } else {
+        // A part of a part is a tenth of the row, but nearly every warp has some of it in any 32 quads: a thread marks its tokens
+        // first, 64 at a time, and then weighs the marked ones, two by two.
+        for (int g0 = tid; g0 < quads; g0 += 16 * kThreads) {
+            u64 marks = 0ull;
+            for (int i = 0, g = g0; i < 16 && g < quads; ++i, g += kThreads) {
+                const float4 v = piece.at(g);
+                const float x[4] = {v.x, v.y, v.z, v.w};
+                unsigned m = 0u;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int i = piece.begin + 4 * g + k;
-                is[k] &= !((x[k] == xl) & (i > last)) & (ROW || !((x[k] == xh) & (i < first)));
+                for (int k = 0; k < 4; ++k) {
+                    bool is = (x[k] >= xl) & (x[k] <= xh);
+                    if (ties) {
+                        const int id = piece.begin + 4 * g + k;
+                        is &= !((x[k] == xl) & (id > last)) & !((x[k] == xh) & (id < first));
+                    }
+                    m |= is ? 1u << k : 0u;
+                }
+                marks |= (u64)m << (4 * i);
+            }
+            while (marks) {
+                int at[2];
+                float x[2];
+                const bool both = (marks & (marks - 1ull)) != 0ull;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    if (k == 1 && !both) {
+                        at[1] = at[0];
+                        break;
+                    }
+                    const int m = __ffsll((long long)marks) - 1;
+                    marks &= marks - 1ull;
+                    at[k] = 4 * (g0 + (m >> 2) * kThreads) + (m & 3);
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) x[k] = piece.one(at[k]);
+                u64 w[2] = {0ull, 0ull};
+                if constexpr (WEIGHED) weigh2(row, sh.table, make_float2(x[0], x[1]), w);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    if (k == 1 && !both) break;
+                    const int bin = c.by_value ? c.slot(x[k])
+                                               : B - 1 - (int)((key_of(x[k], piece.begin + at[k], id_bits) - z.lo) >> c.shift);
+                    bins[bin * kThreads + tid] += w[k] + (1ull << kCountBit);
+                }
             }
         }
-        if (!(is[0] | is[1] | is[2] | is[3])) continue;
-        if (!ROW && !c.by_value) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                b[k] = B - 1 - (int)((key_of(x[k], piece.begin + 4 * g + k, id_bits) - z.lo) >> c.shift);
-        }
-        u64 w[4] = {0ull, 0ull, 0ull, 0ull};
-        if constexpr (WEIGHED) {
-            u64 a[2], c[2];
-            weigh2(row, sh.table, make_float2(x[0], x[1]), a);
-            weigh2(row, sh.table, make_float2(x[2], x[3]), c);
-            w[0] = a[0], w[1] = a[1], w[2] = c[0], w[3] = c[1];
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            w[k] = is[k] ? w[k] + (1ull << kCountBit) : 0ull;
-            b[k] = is[k] ? b[k] : B - 1;
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) bins[b[k] * kThreads + tid] += w[k];
     }
     // 32 lanes' sums, the weights' in three words of 27 bits, which leave room for them
     auto add = [&](u64 &w, unsigned &n) {
