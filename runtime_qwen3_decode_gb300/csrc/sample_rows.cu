@@ -11,13 +11,18 @@
 // Nothing is sorted but the few tokens that stay in question.  A row belongs to the CTAs of one cluster,
 // each with a piece of it in shared memory:
 //   1. the greatest logit of the row;
-//   2. every token counted (and, where weights matter, weighed) by the octave of weight that it lies in below the greatest,
-//      the last of kBins parts taking the rest: that tells which of them the lowest border falls in;
-//   3. that part is cut in kBins again, by logits and at last by (logit, id) keys, until the tokens down to the border
-//      are at most kList: the first CTA gathers and sorts them and runs the definition on them.
+//   2. every token counted (and, where weights matter, weighed) by the double octave of weight that it lies in below the
+//      greatest, the last of B parts taking the rest: that tells which of them the lowest border falls in;
+//   3. that part is cut in B again, by logits about the place where the border should be and at last by (logit, id) keys,
+//      until the tokens down to the border are few: the first CTA gathers and sorts them and runs the definition on them.
 //   4. Where more tokens are kept, each border (top_k, top_p, the draw) is looked for by itself, and only the part
-//      that it falls in is sorted.
+//      that it falls in is sorted, by every CTA.
+//   1b. top_k up to kMostShort, and min_p alone, list their tokens without a pass (8 rows of 151,936 13.4 us instead of 20.0).
 // top_k needs counts alone: its passes weigh nothing.
+//
+// Bound by the number of instructions where passes weigh whole rows (47 a token), else by the time that a pass takes
+// whatever it holds: some 3 us for its bins, the cluster's exchange and the search for the next zone's ends.  256 rows of
+// 151,936 with mixed settings 262 us (HBM floor 23), 8 drawn from nearly everything 47, 8 of usual settings 13.4.
 //
 // Weights are whole numbers, 2^wb for the weight 1 (wb >= 38, 44 at a vocabulary of 151,936), so that their
 // sums are exact: they do not depend on the order of addition, on the number of CTAs or on timing, and a
@@ -40,9 +45,9 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-// Parts of a pass's zone, B in what follows: every thread has a bin of its own for each, 2 or 8 KB a warp.  32 up to some waves of
-// CTAs, which saves passes but leaves one CTA to an SM (8 x 151,936 drawn from nearly everything 48 us, 82 with 8; 64 rows of mixed
-// settings 113, 118); else 8, so that two CTAs share an SM (256 such rows 316 and 318).
+// Parts of a pass's zone, B in what follows: every thread has a bin of its own for each, 2 or 8 KB a warp.  32 up to two CTAs for
+// every SM, which saves passes but leaves one CTA to an SM (us with 32 and with 8, rows of 151,936: 8 drawn from nearly everything 47
+// and 68, 32 of mixed settings 62 and 67); else 8, so that two CTAs share an SM (64 bf16 ones 96 and 74, 256 347 and 261).
 constexpr int kFewBins = 8, kManyBins = 32;
 constexpr int kKeys = 4;              // sorted keys of a thread
 constexpr int kList = kKeys * kThreads;  // tokens that are sorted at once, in one CTA
@@ -57,8 +62,7 @@ constexpr int kSteps = 32;        // of the table of 2^(i / 32)
 using u64 = unsigned long long;
 
 // 2^(i / 32) in units of 2^-31, and in f32 in units of 2^-36: two words that each lie in a bank of their own for every i,
-// so that 32 lanes read them at once whatever their i (16-byte entries of 64 steps took 12 turns a read: 8.3 us instead of
-// XX a pass).
+// so that 32 lanes read them at once whatever their i (16-byte entries of 64 steps took 12 turns a read).
 struct Table {
     unsigned fix[kSteps];
     float f[kSteps];
@@ -979,7 +983,7 @@ cudaError_t launch_typed(const qw_sample_rows_args &q, cudaStream_t st) {
     };
     const size_t most = 227 * 1024, room = most - fixed(kFewBins);
     // As many CTAs for a row as there are SMs to take them, or as hold it with another CTA on the SM.  (Clusters of 16 for up to
-    // nine rows took 15.5 us instead of 14.2 at 8 x 151,936: what grows with the cluster outweighs the shorter pieces.)
+    // nine rows took 1.3 us more at 8 x 151,936: what grows with the cluster outweighs the shorter pieces.)
     int ctas = 1;
     auto per = [&](int n) { return (int)(((int64_t)q.vocab + n - 1) / n + 7) / 8 * 8; };
     while (ctas < kMaxCluster && per(ctas) > 4096 && ((int64_t)q.n_rows * ctas * 2 <= 152 || (size_t)per(ctas) * 4 > room / 2)) ctas *= 2;
@@ -991,14 +995,17 @@ cudaError_t launch_typed(const qw_sample_rows_args &q, cudaStream_t st) {
     a.id_bits = bits_for(q.vocab);
     a.wb = std::min(62 - a.id_bits, kCountBit - 1 - bits_for((a.per + 4 * kThreads - 1) / (4 * kThreads) * 4));  // a thread's tokens fit its bins
     a.rows = q.n_rows;
-    // One wave has no last ones; beyond some thousand rows the search costs more than it gives.
-    a.sorted = (int64_t)q.n_rows * ctas > 2 * 152 && q.n_rows <= 2048;
+    // Worth it for one to eight waves of rows of four or more CTAs (us, mixed settings, with it and without: 48 rows of 151,936 70
+    // and 78, 128 139 and 150; 150 of 65,000 92 and 95); more of them, or smaller ones, run better side by side with short ones (512 of
+    // 151,936 481 and 462; 1,200 of 32,000 296 and 277).
+    const int64_t all = (int64_t)q.n_rows * ctas;
+    a.sorted = ctas >= 4 && all > 2 * 152 && all <= 16 * 152;
     a.u = q.u, a.temperature = q.temperature, a.top_p = q.top_p, a.min_p = q.min_p, a.top_k = q.top_k;
     a.tokens = q.tokens, a.kept = q.kept, a.probs = q.probs;
     const bool res = (size_t)a.per * 4 <= room;
     const size_t row = std::max<size_t>(res ? (size_t)a.per * 4 : 0, (size_t)kList * 16);  // lists are sorted where the row was
     if (!res) return launch_rows<T, false, kFewBins>(a, table(), q.n_rows, ctas, fixed(kFewBins) + row, st);
-    if ((int64_t)q.n_rows * ctas <= 4 * 152 && fixed(kManyBins) + row <= most)
+    if (all <= 2 * 152 && fixed(kManyBins) + row <= most)
         return launch_rows<T, true, kManyBins>(a, table(), q.n_rows, ctas, fixed(kManyBins) + row, st);
     return launch_rows<T, true, kFewBins>(a, table(), q.n_rows, ctas, fixed(kFewBins) + row, st);
 }
