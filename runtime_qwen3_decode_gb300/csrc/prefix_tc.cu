@@ -93,6 +93,18 @@ cudaError_t launch_prefix_dim(const Prefix &p, const qw_kv_view &prefix, const q
     return nrt * p.a.Hkv * 12 <= ctas ? merge(prefix_tc_merge_kernel<D, 4>, kMergeThreads / 4) : merge(prefix_tc_merge_kernel<D, 1>, kMergeThreads);
 }
 
+// Positions of a tile.  Operands of two terms fill the shared memory with one tile of 128, but two of 64, so that one is converted
+// while the other is used (us, 128 : 64, 8 KV heads, one fp16 node a sequence, over f32 rows: 8 sequences of 300 behind 4096 28 : 25, 32
+// of 512 behind 32768 145 : 104, 64 of 4096 357 : 357).  Over 8-bit rows, which convert faster, what a tile takes whatever it
+// holds counts more: a tile of 128 of the prefix, whose rows are all live, gains some 0.8 us, one of a single sequence, whose rows are
+// mostly others', loses 0.6, and the first tile is ready some 3 us earlier (256 sequences behind 32768 283 : 241, 16 of 5 nodes
+// and 500 behind 2048 39 : 34, 64 of 1024 97 : 112, 64 of 4096 302 : 367).
+int tile_log2(int format, int dtype, long long prefix_tiles, long long own_tiles) {
+    const bool two = format == QW_KV_F32 || (format == QW_KV_INT8_G32 && dtype == QW_DT_F16);
+    if (!two) return 7;
+    return format == QW_KV_F32 || 3 * own_tiles <= 4 * prefix_tiles + 15 * kTcCtas ? 6 : 7;
+}
+
 size_t starts_bytes(int64_t rows) { return (((rows + kTcRows - 1) / kTcRows + 2) * 8 + 255) / 256 * 256; }
 
 }  // namespace
@@ -114,9 +126,10 @@ cudaError_t launch_prefix_tc(const PrefixArgs &a, const qw_kv_view &prefix, cons
     p.status = (int *)rest;
     p.part = (float *)(rest + kTcStatusBytes);
     const long long nrt = (rows + kTcRows - 1) / kTcRows;
-    const long long tiles = kv.n_kv_heads * (nrt * ((max_prefix + kTcTile - 1) / kTcTile) +
-                                             (long long)kv.n_seq * ((max_len + a.n_max + kTcTile - 1) / kTcTile));
-    const int ctas = (int)std::min<long long>(kTcCtas, tiles);
+    auto tiles = [&](int log2, long long positions) { return (long long)kv.n_kv_heads * ((positions + (1 << log2) - 1) >> log2); };
+    p.tile_log2 = tile_log2(kv.format, a.dtype, nrt * tiles(7, max_prefix), kv.n_seq * tiles(7, max_len + a.n_max));
+    const long long all = nrt * tiles(p.tile_log2, max_prefix) + kv.n_seq * tiles(p.tile_log2, max_len + a.n_max);
+    const int ctas = (int)std::min<long long>(kTcCtas, all);
     return kv.head_dim == 128 ? launch_prefix_dim<128>(p, prefix, kv, ctas, st, chained)
                               : launch_prefix_dim<64>(p, prefix, kv, ctas, st, chained);
 }

@@ -431,16 +431,16 @@ PrefixPlan plan_prefix(int n_seq, int Hkv, int n_max, int G, int max_len, int ma
 // Whether a call with 16-bit queries is better off on the CUDA cores: by estimates of both times that follow what was measured (us,
 // CUDA cores : tensor cores, 8 KV heads of two query heads of 128 dims, one row per sequence).  bf16 beside bf16: one sequence of 100
 // positions behind a prefix of 2048 9.5 : 15, of 16384 33 : 24; 8 sequences of 64 behind 512 13 : 14, of 100 behind 2048
-// 24 : 18; 32 of 16 behind 64 14 : 17.  fp16 over 8-bit rows: 8 of 100 behind 2048 26 : 25, of 300 behind 4096 41 : 28.
-// fp16 over f32 rows, whose tiles cost the tensor cores most: 8 of 100 behind 2048 25 : 26, of 300 behind 4096 40 : 31; 32 of
-// 400 behind 512 58 : 61.
+// 24 : 18; 32 of 16 behind 64 14 : 17.  fp16 over 8-bit rows: 8 of 64 behind 512 14 : 18, of 100 behind 2048 26 : 21, of 300 behind 4096
+// 41 : 25.  16-bit queries over f32 rows: 8 of 64 behind 512 14 : 18, of 100 behind 2048 25 : 20, 32 of 16 behind 64 14 : 18, of
+// 400 behind 512 57 : 45.
 bool small_prefix_call(const qw_kv_view &kv, const qw_tree_attention_args &t, const PrefixPlan &p, int max_prefix) {
     const bool f16 = t.dtype == QW_DT_F16;
     const int64_t rows = (int64_t)kv.n_seq * t.n_max * (t.n_heads / kv.n_kv_heads);
     const double tiles = (double)kv.n_kv_heads * ((double)((rows + kTcRows - 1) / kTcRows) * ((max_prefix + kTcTile - 1) / kTcTile) +
                                                   (double)kv.n_seq * ((t.max_len + t.n_max + kTcTile - 1) / kTcTile));
-    const double start = kv.format == QW_KV_F32 ? 10.7 : kv.format == QW_KV_INT8_G32 ? 14.1 : f16 ? 12.9 : 13.5;  // us
-    const double wave = kv.format == QW_KV_F32 ? 6.9 : kv.format == QW_KV_INT8_G32 ? (f16 ? 4.5 : 2.8) : f16 ? 2.9 : 1.8;
+    const double start = kv.format == QW_KV_F32 ? 12.3 : kv.format == QW_KV_INT8_G32 ? (f16 ? 13.5 : 14.1) : f16 ? 12.9 : 13.5;  // us
+    const double wave = kv.format == QW_KV_F32 ? 4.7 : kv.format == QW_KV_INT8_G32 ? (f16 ? 4.1 : 2.8) : f16 ? 2.9 : 1.8;
     return 6. + 0.25 * p.rt + p.ns * 1e-3 < start + wave * std::max(1., tiles / kTcCtas);
 }
 

@@ -21,7 +21,7 @@
 // them K and four V.  bf16 beside bf16: TMA writes K and V tiles straight into swizzled operand
 // tiles, three stages each.  Otherwise TMA fills two slots of 16 KB with raw rows for each
 // plane, and the converters write the 16-bit operand tiles, double-buffered (one stage of
-// two-term tiles).  8-bit rows become fp16 (code * scale rounded once, 2^-11; bf16 would lose
+// two-term tiles of 128 positions; PREFIX has two of 64, see tile_log2 in prefix_tc.cu).  8-bit rows become fp16 (code * scale rounded once, 2^-11; bf16 would lose
 // three more bits and cost twice the instructions), bf16 queries beside them fp16 after
 // division by a power of two per row, so that only elements 2^-14 below the row's largest
 // lose bits.  f32 rows become two fp16 terms beside fp16 queries and two bf16 terms beside bf16 ones,
@@ -55,6 +55,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <type_traits>
 #include <cmath>
 
 #include "tc.cuh"
@@ -77,7 +78,8 @@ constexpr int kPlaneWarps = kConvWarps / 2, kPlaneThreads = 32 * kPlaneWarps;
 constexpr uint32_t kColO = 256;
 
 // TERMS: 16-bit numbers per K or V element, 2 = a number of the operands' type and the one of what it leaves.
-template <int SRC, int D, int TERMS>
+// TILE: positions of a tile.
+template <int SRC, int D, int TERMS, int TILE>
 struct Cfg {
     static constexpr bool kDirect = SRC == SRC_BF16;
     static constexpr bool kBf16 = SRC == SRC_BF16 || SRC == SRC_F32_BF16;  // the operands' type, else fp16
@@ -90,15 +92,17 @@ struct Cfg {
     static constexpr float kLag = kBf16 ? 8.f : 6.f, kLift = kBf16 ? 0.f : 9.f;
     static constexpr int kElem = SRC == SRC_Q8_F16 ? 1 : SRC == SRC_F32_F16 || SRC == SRC_F32_BF16 ? 4 : 2;
     static constexpr int kThreads = 32 * (kDirect ? kPlainWarps : kPlainWarps + kConvWarps - 2);
-    static constexpr int kRegion = 128 * 128;              // 128 rows x 64 16-bit dims
-    static constexpr int kTerm = kRegion * (D / 64);       // one term of a K or V operand tile
+    static constexpr int kTile = TILE;
+    static constexpr int kQRegion = kTcRows * 128;         // 128 rows x 64 16-bit dims
+    static constexpr int kRegion = kTile * 128;            // the same of a K or V operand tile
+    static constexpr int kTerm = kRegion * (D / 64);       // one term of it
     static constexpr int kOperand = kTerm * TERMS;
-    static constexpr int kStages = kDirect ? 3 : TERMS == 2 ? 1 : 2;
-    static constexpr int kChunkRows = 16384 / (D * kElem) < 128 ? 16384 / (D * kElem) : 128;
+    static constexpr int kStages = kDirect ? 3 : kTile * TERMS > 128 ? 1 : 2;
+    static constexpr int kChunkRows = 16384 / (D * kElem) < kTile ? 16384 / (D * kElem) : kTile;
     static constexpr int kChunk = kChunkRows * D * kElem;  // raw bytes per ring slot
-    static constexpr int kChunks = 128 / kChunkRows;       // per tile and plane
+    static constexpr int kChunks = kTile / kChunkRows;       // per tile and plane
     static constexpr int kRing = kDirect ? 0 : 4;          // slots of raw rows: two for K, two for V
-    static constexpr int kQ = 0, kK = kQ + kTerm, kV = kK + kStages * kOperand, kRaw = kV + kStages * kOperand;
+    static constexpr int kQ = 0, kK = kQ + kQRegion * (D / 64), kV = kK + kStages * kOperand, kRaw = kV + kStages * kOperand;
     static constexpr int kBar = kRaw + kRing * kChunk;
     static constexpr int kBytes = kBar + 512 + kTcRows * 4 + 256;  // barriers, one score factor per row, PREFIX: own tiles
     static constexpr size_t kSmem = 1024 + kBytes;
@@ -113,6 +117,7 @@ struct TcParams {
     int *status;
     float *part;          // [2 CTAs][D + 2][rows_max]
     long long *starts;    // PREFIX: [row tiles + 2] tiles of a KV head before each tile of rows, and 0; or its first CTA, and 1
+    int tile_log2;        // PREFIX: of the positions of a tile
     unsigned long long inv_g;  // 2^32 / G + 1: row / G for the at most 4096 rows of a KV head
     __device__ __forceinline__ int node_of(int row) const { return (int)((unsigned)row * inv_g >> 32); }
     // The sequence, node and head of its group of row r: of KV head's rows of sequence b, or (PREFIX) of all sequences.
@@ -129,6 +134,7 @@ using Tree = TcParams<false>;
 using Prefix = TcParams<true>;
 
 __device__ __forceinline__ int seq_tiles(int total) { return (total + kTcTile - 1) / kTcTile; }
+__device__ __forceinline__ int seq_tiles(const Prefix &p, int total) { return (total + (1 << p.tile_log2) - 1) >> p.tile_log2; }
 
 // Tiles of sequence b over all its items; 0 for one without nodes or that does not fit.
 __device__ __forceinline__ long long seq_work(const Tree &p, int b) {
@@ -233,7 +239,7 @@ constexpr int kOwnTable = 64;  // row tiles whose own tiles a CTA keeps at hand;
 
 __device__ __forceinline__ int own_tiles(const Prefix &p, int b) {
     int len, n;
-    return lengths(p.a, b, len, n) && n > 0 ? seq_tiles(len + n) : 0;
+    return lengths(p.a, b, len, n) && n > 0 ? seq_tiles(p, len + n) : 0;
 }
 __device__ __forceinline__ int row_count(const Prefix &p) { return p.n_seq * p.a.n_max * p.a.G; }
 __device__ __forceinline__ int row_tiles(const Prefix &p) { return (row_count(p) + kTcRows - 1) / kTcRows; }
@@ -252,7 +258,7 @@ __device__ __forceinline__ bool next_seg(const Prefix &p, Cursor &c, Seg &s, con
         if (c.rt - c.first_rt < kOwnTable) mine = own[c.rt - c.first_rt];
         else
             for (int b = s.b; b <= s.b1; ++b) mine += own_tiles(p, b);
-        s.tiles = seq_tiles(s.len) + (int)mine;
+        s.tiles = seq_tiles(p, s.len) + (int)mine;
         if (s.tiles == 0) {
             ++c.rt;
             continue;
@@ -350,7 +356,7 @@ __device__ __forceinline__ Cursor find_start(const Prefix &p, const Tables &t, u
             for (int i = lane; i <= nrt + 1; i += 32) p.starts[i] = 0;
         return c;
     }
-    const int ptiles = seq_tiles(plen);
+    const int ptiles = seq_tiles(p, plen);
     long long T = 0;
     for (int r0 = 0; r0 < nrt; r0 += 32) {
         const long long mine = r0 + lane < nrt ? (long long)ptiles + t.rows[r0 + lane] : 0, upto = scan64(mine, lane);
@@ -445,18 +451,19 @@ struct Walk<true> {
     }
     __device__ __forceinline__ void start(const Prefix &p, const Seg &s) {
         b1 = s.b1;
-        pre = s.t0 < seq_tiles(s.len);
+        pre = s.t0 < seq_tiles(p, s.len);
         b = s.b - 1;
         look(p);
         if (pre) {
-            pos = s.t0 * kTcTile, len = end = s.len;
+            pos = s.t0 << p.tile_log2, len = end = s.len;
             return;
         }
         step(p);
-        if (s.own_tile > 0) pos = s.own_tile * kTcTile;
+        if (s.own_tile > 0) pos = s.own_tile << p.tile_log2;
     }
     __device__ __forceinline__ void next(const Prefix &p) {
-        if (pos + kTcTile < end) pos += kTcTile;
+        const int tile = 1 << p.tile_log2;
+        if (pos + tile < end) pos += tile;
         else step(p);
     }
 };
@@ -601,10 +608,10 @@ struct Maps {
     CUtensorMap m[PREFIX ? 4 : 2];
 };
 
-template <int SRC, int D, int TERMS, bool PREFIX>
-__global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
+template <int SRC, int D, int TERMS, bool PREFIX, int TILE>
+__global__ void __launch_bounds__(Cfg<SRC, D, TERMS, TILE>::kThreads, 1)
     tree_tc_kernel(const __grid_constant__ Maps<PREFIX> maps, const TcParams<PREFIX> p) {
-    using C = Cfg<SRC, D, TERMS>;
+    using C = Cfg<SRC, D, TERMS, TILE>;
     constexpr int ST = C::kStages;
     uint8_t *base = smem_base();
     uint8_t *sQ = base + C::kQ, *sK = base + C::kK, *sV = base + C::kV, *raw = base + C::kRaw;
@@ -765,7 +772,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
             // what they need is waited for before the weights are: that wait is the one that both groups'
             // time hangs on.  With one stage K of two tiles on cannot be there yet (its chunks come
             // behind V chunks that wait for this product): there S runs one tile ahead.
-            constexpr uint32_t idS = idesc_16_f32(128, 128, C::kBf16, false), idO = idesc_16_f32(128, D, C::kBf16, true);
+            constexpr uint32_t idS = idesc_16_f32(128, C::kTile, C::kBf16, false), idO = idesc_16_f32(128, D, C::kBf16, true);
             constexpr int kAhead = ST >= 2 ? 2 : 1;
             // Descriptors of the first tiles; the others differ in the address field (in units of 16 bytes), which
             // the offsets below do not carry out of: building each anew held the issue back.
@@ -780,8 +787,9 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < TERMS * (D / 16); ++k) {
                     const int term = k / (D / 16), kk = k % (D / 16);
-                    const unsigned off = (kk >> 2) * (C::kRegion >> 4) + 2u * (kk & 3);
-                    mma_f16(tmem + 128u * (jn & 1), dQ + off, kd + (off + term * (C::kTerm >> 4)), idS, k != 0);
+                    const unsigned step = 2u * (kk & 3);
+                    mma_f16(tmem + 128u * (jn & 1), dQ + ((kk >> 2) * (C::kQRegion >> 4) + step),
+                            kd + ((kk >> 2) * (C::kRegion >> 4) + step + term * (C::kTerm >> 4)), idS, k != 0);
                 }
                 mma_commit(&s_full[jn & 1]);
                 mma_commit(&k_empty[st]);
@@ -819,8 +827,8 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                     const uint64_t vd = dV + (unsigned)(st * (C::kOperand >> 4));
                     const uint32_t tp = tmem + 128u * (jj & 1);
 #pragma unroll
-                    for (int k = 0; k < TERMS * (kTcTile / 16); ++k) {
-                        const int term = k / (kTcTile / 16), kk = k % (kTcTile / 16);
+                    for (int k = 0; k < TERMS * (C::kTile / 16); ++k) {
+                        const int term = k / (C::kTile / 16), kk = k % (C::kTile / 16);
                         mma_f16_ts(tp + kColO, tp + 8u * kk, vd + (unsigned)(term * (C::kTerm >> 4) + 128 * kk), idO,
                                    j > 1 || k > 0);
                     }
@@ -865,7 +873,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                 const int c = lane % LPR, first = warp * (32 / LPR) + lane / LPR;
                 const bool scaled = !C::kBf16 && a.dtype == QW_DT_BF16;
                 const uint16_t *qb = reinterpret_cast<const uint16_t *>(a.q) + (int64_t)s.h * a.G * a.qhead + 8 * c;
-                uint8_t *tile = sQ + (c >> 3) * C::kRegion;
+                uint8_t *tile = sQ + (c >> 3) * C::kQRegion;
                 for (int x = first; x < nr; x += RPP) {
                     int b = s.b, nd, g;
                     p.place(s.r0 + x, b, nd, g);
@@ -925,7 +933,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                         if (walked > 0) w.next(p);
                         if (!w.pre && w.b == mb_) {
                             if (own_hi == 0) own_lo = w.pos;
-                            own_hi = min(w.pos + kTcTile, w.end);
+                            own_hi = min(w.pos + C::kTile, w.end);
                         }
                     }
                 } else {
@@ -941,10 +949,10 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                 const int first = w.pos;
                 // rows of other sequences see nothing of a sequence's own tile
                 const bool sees = !PREFIX || w.pre || w.b == mb_;
-                const bool tail = first + kTcTile > w.len;
+                const bool tail = first + C::kTile > w.len;
                 const unsigned long long seen = PREFIX && w.pre ? 0ull : mask;
                 // blocks of 32 columns up to the end (a sequence's last tile may hold few)
-                const int blocks = PREFIX ? min(4, (w.end - first + 31) >> 5) : 4;
+                const int blocks = PREFIX ? min(C::kTile / 32, (w.end - first + 31) >> 5) : 4;
                 bool busy = warp_live;
                 if constexpr (PREFIX) busy = __any_sync(0xffffffffu, live && sees);
                 if (PREFIX && warp_live && !busy) {
@@ -952,7 +960,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) pk[i] = 0u;
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) tmem_st16u(tS + 16u * c, pk);
+                    for (int c = 0; c < C::kTile / 32; ++c) tmem_st16u(tS + 16u * c, pk);
                 }
                 if constexpr (PREFIX) {
                     if (busy) {
@@ -1014,7 +1022,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 16; ++i) pk[i] = 0u;
 #pragma unroll 1
-                        for (int c = blocks; c < 4; ++c) tmem_st16u(tS + 16u * c, pk);
+                        for (int c = blocks; c < C::kTile / 32; ++c) tmem_st16u(tS + 16u * c, pk);
                     }
                 } else if (busy) {
                     // halves of 64 columns, rolled: unrolled over the tile the code outgrows the
@@ -1130,7 +1138,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                     if (walked > 0) w.next(p);
                     if (!w.pre && w.b == mb_) {
                         if (own_hi == 0) own_lo = w.pos;
-                        own_hi = min(w.pos + kTcTile, w.end);
+                        own_hi = min(w.pos + C::kTile, w.end);
                     }
                 }
             }
@@ -1262,7 +1270,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
             // Scales are loaded two tiles ahead.  The group's 32 bytes go as two halves; threads of
             // groups 2 and 3 take the second half first, which spreads a warp's 16-byte stores
             // over all banks.
-            constexpr int GPR = D / kQGroup, RSTEP = kPlaneThreads / GPR, U = 128 / RSTEP;
+            constexpr int GPR = D / kQGroup, RSTEP = kPlaneThreads / GPR, U = C::kTile / RSTEP;
             static_assert(C::kChunks == 1, "an 8-bit tile is one chunk per plane");
             const int g = ct % GPR, row0 = ct / GPR, flip = g >> 1;
             const __half *scales = plane ? a.vs : a.ks;
@@ -1299,7 +1307,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                 for (int t = s.t0; ok && t < s.t1; ++t, ++it) {
                     if (t > s.t0) w.next(p);
                     const int st = it % ST, slot = 2 * plane + (it & 1);
-                    const bool check = plane && (w.pos + kTcTile > (PREFIX ? w.end : w.len) || (careful_pass && !w.pre));
+                    const bool check = plane && (w.pos + C::kTile > (PREFIX ? w.end : w.len) || (careful_pass && !w.pre));
                     __half2 s2[U];
                     bool over = false;  // codes times a scale above 65504 / 127 may be infinite
 #pragma unroll
@@ -1380,7 +1388,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS>::kThreads, 1)
                 for (int t = s.t0; ok && t < s.t1; ++t, ++it) {
                     if (t > s.t0) w.next(p);
                     const int st = it % ST;
-                    const bool check = plane && (w.pos + kTcTile > (PREFIX ? w.end : w.len) || (careful_pass && !w.pre));
+                    const bool check = plane && (w.pos + C::kTile > (PREFIX ? w.end : w.len) || (careful_pass && !w.pre));
                     for (int ch = 0; ch < C::kChunks; ++ch) {
                         const int i = it * C::kChunks + ch, slot = 2 * plane + (i & 1), crow = ch * C::kChunkRows;
                         if ((ch == 0 && !warp_wait(&empty[st], ((unsigned)(it / ST) & 1u) ^ 1u, abort)) ||
@@ -1575,9 +1583,9 @@ bool plane_map(CUtensorMap *m, const void *ptr, const qw_kv_view &kv, CUtensorMa
 int slot_rows(int rows) { return std::min(kTcRows, (rows + 3) / 4 * 4); }
 
 // prefix: PREFIX only.  The merge is the caller's.
-template <int SRC, int D, int TERMS, bool PREFIX>
+template <int SRC, int D, int TERMS, bool PREFIX, int TILE>
 cudaError_t launch_src(const TcParams<PREFIX> &p, const qw_kv_view &kv, const qw_kv_view *prefix, int ctas, cudaStream_t st, bool chained) {
-    using C = Cfg<SRC, D, TERMS>;
+    using C = Cfg<SRC, D, TERMS, TILE>;
     Maps<PREFIX> maps;
     const CUtensorMapDataType type = C::kElem == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                      : C::kElem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
@@ -1587,9 +1595,9 @@ cudaError_t launch_src(const TcParams<PREFIX> &p, const qw_kv_view &kv, const qw
         const qw_kv_view &view = i < 2 ? kv : *prefix;
         if (!plane_map(&maps.m[i], i & 1 ? view.v : view.k, view, type, C::kElem, dims, rows, C::kDirect)) return cudaErrorInvalidValue;
     }
-    cudaError_t e = allow_smem<tree_tc_kernel<SRC, D, TERMS, PREFIX>>((int)C::kSmem);
+    cudaError_t e = allow_smem<tree_tc_kernel<SRC, D, TERMS, PREFIX, TILE>>((int)C::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_k(chained, tree_tc_kernel<SRC, D, TERMS, PREFIX>, dim3(ctas), dim3(C::kThreads), C::kSmem, st, maps, p);
+    return launch_k(chained, tree_tc_kernel<SRC, D, TERMS, PREFIX, TILE>, dim3(ctas), dim3(C::kThreads), C::kSmem, st, maps, p);
 }
 
 // 16-bit results next to fp16 operands: beside bf16 queries one rounding of 8-bit K and V (2^-11) drowns in
@@ -1600,11 +1608,23 @@ cudaError_t launch_src(const TcParams<PREFIX> &p, const qw_kv_view &kv, const qw
 template <int D, bool PREFIX>
 cudaError_t launch_dim(const TcParams<PREFIX> &p, const qw_kv_view &kv, const qw_kv_view *pre, int ctas, cudaStream_t st, bool ch) {
     const bool f16 = p.a.dtype == QW_DT_F16;
-    if (kv.format == QW_KV_INT8_G32)
-        return f16 ? launch_src<SRC_Q8_F16, D, 2, PREFIX>(p, kv, pre, ctas, st, ch) : launch_src<SRC_Q8_F16, D, 1, PREFIX>(p, kv, pre, ctas, st, ch);
+    auto go = [&](auto src, auto terms, auto tile) {
+        return launch_src<decltype(src)::value, D, decltype(terms)::value, PREFIX, decltype(tile)::value>(p, kv, pre, ctas, st, ch);
+    };
+    constexpr std::integral_constant<int, 1> one{};
+    constexpr std::integral_constant<int, 2> two{};
+    constexpr std::integral_constant<int, kTcTile> whole{};
+    constexpr std::integral_constant<int, PREFIX ? 64 : kTcTile> half{};
+    if (kv.format == QW_KV_INT8_G32) {
+        constexpr std::integral_constant<int, SRC_Q8_F16> src{};
+        if constexpr (PREFIX) {
+            if (f16 && p.tile_log2 == 6) return go(src, two, half);
+        }
+        return f16 ? go(src, two, whole) : go(src, one, whole);
+    }
     if (kv.format == QW_KV_BF16)
-        return f16 ? launch_src<SRC_BF16_F16, D, 1, PREFIX>(p, kv, pre, ctas, st, ch) : launch_src<SRC_BF16, D, 1, PREFIX>(p, kv, pre, ctas, st, ch);
-    return f16 ? launch_src<SRC_F32_F16, D, 2, PREFIX>(p, kv, pre, ctas, st, ch) : launch_src<SRC_F32_BF16, D, 2, PREFIX>(p, kv, pre, ctas, st, ch);
+        return f16 ? go(std::integral_constant<int, SRC_BF16_F16>(), one, whole) : go(std::integral_constant<int, SRC_BF16>(), one, whole);
+    return f16 ? go(std::integral_constant<int, SRC_F32_F16>(), two, half) : go(std::integral_constant<int, SRC_F32_BF16>(), two, half);
 }
 
 }  // namespace
