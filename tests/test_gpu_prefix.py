@@ -96,6 +96,16 @@ def test_both_sides_of_the_small_call(qw, dt, kind, B, n, P, L):
     run(qw, B, 8, 2, 128, n, P, [L] * B, None, dt, kind, chain=True)
 
 
+# Most positions the sequences' own (tiles of 128 for fp16 over 8 bits), or the prefix's (of 64); ends on both sides of tiles and blocks.
+@pytest.mark.parametrize("dt,kind,D", [(F16, "int8", 128), (F16, "int8", 64), (F16, "f32", 128), (F16, "f32", 64), (BF16, "f32", 128)])
+@pytest.mark.parametrize("B,P,L", [(70, 0, 511), (70, 33, 450), (66, 129, 640), (40, 4033, 31), (70, 1985, 97)])
+def test_tiles_of_both_sizes(qw, dt, kind, D, B, P, L):
+    rng = np.random.default_rng(B + P + L)
+    lens = [int(x) for x in rng.integers(0, L + 1, B)]
+    lens[0], lens[-1], lens[7] = L, 64, 63
+    run(qw, B, 8, 2, D, 1, P, lens, None, dt, kind, seed=L)
+
+
 @pytest.mark.parametrize("dt,kind", [(F32, "int8"), (BF16, "bf16"), (F16, "int8"), (BF16, "f32")])
 def test_token_major_caches(qw, dt, kind):
     run(qw, 9, 2, 4, 128, 4, 900, [0, 1, 900, 17, 300, 64, 129, 5, 128], [4, 0, 3, 4, 1, 2, 4, 2, 4], dt, kind, layout="token")
