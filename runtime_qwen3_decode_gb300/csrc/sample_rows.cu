@@ -11,18 +11,18 @@
 // Nothing is sorted but the few tokens that stay in question.  A row belongs to the CTAs of one cluster,
 // each with a piece of it in shared memory:
 //   1. the greatest logit of the row;
-//   2. every token counted (and, where weights matter, weighed) by the double octave of weight that it lies in below the
-//      greatest, the last of B parts taking the rest: that tells which of them the lowest border falls in;
+//   2. every token counted (and, where weights matter, weighed) by the octaves of weight that it lies below the greatest (two
+//      or half of one to a part), the last of B parts taking the rest: that tells which of them the lowest border falls in;
 //   3. that part is cut in B again, by logits about the place where the border should be and at last by (logit, id) keys,
 //      until the tokens down to the border are few: the first CTA gathers and sorts them and runs the definition on them.
 //   4. Where more tokens are kept, each border (top_k, top_p, the draw) is looked for by itself, and only the part
 //      that it falls in is sorted, by every CTA.
-//   1b. top_k up to kMostShort, and min_p alone, list their tokens without a pass (8 rows of 151,936 13.4 us instead of 20.0).
+//   1b. top_k up to kMostShort, and min_p alone, list their tokens without a pass (8 rows of 151,936 12.3 us instead of 20.0).
 // top_k needs counts alone: its passes weigh nothing.
 //
 // Bound by the number of instructions where passes weigh whole rows (47 a token), else by the time that a pass takes
 // whatever it holds: some 3 us for its bins, the cluster's exchange and the search for the next zone's ends.  256 rows of
-// 151,936 with mixed settings 262 us (HBM floor 23), 8 drawn from nearly everything 47, 8 of usual settings 13.4.
+// 151,936 with mixed settings 258 us (HBM floor 23), 8 drawn from nearly everything 46, 8 of usual settings 12.3.
 //
 // Weights are whole numbers, 2^wb for the weight 1 (wb >= 38, 44 at a vocabulary of 151,936), so that their
 // sums are exact: they do not depend on the order of addition, on the number of CTAs or on timing, and a
@@ -576,7 +576,10 @@ __global__ void __launch_bounds__(kThreads, B == kFewBins ? 2 : 1) sample_rows_k
             least = fminf(least, sh.least[c]);
         }
     }
-    if (ctas == 1) sh.group[tid] = group;
+    if (ctas == 1) {
+        sh.group[tid] = group;
+        __syncthreads();
+    }
     auto answer = [&](int token, float prob, int kept) {
         a.tokens[r] = token;
         if (a.probs) a.probs[r] = prob;
@@ -657,22 +660,26 @@ __global__ void __launch_bounds__(kThreads, B == kFewBins ? 2 : 1) sample_rows_k
         if (top_k > 0) {
             const float aim = (float)top_k + 3.f * sqrtf((float)top_k) + 8.f;
             const int m = min(kThreads - 1, (int)((float)kThreads * (1.f - __expf(-aim / kThreads))));
-            // the m-th greatest: a descending sort, one per thread
-            float v = sh.group[tid];
-            for (int size = 2; size <= kThreads; size <<= 1)
-                for (int stride = size >> 1; stride > 0; stride >>= 1) {
-                    float o;
-                    if (stride >= 32) {
-                        __syncthreads();
-                        sh.group[tid] = v;
-                        __syncthreads();
-                        o = sh.group[tid ^ stride];
-                    } else {
-                        o = __shfl_xor_sync(0xffffffffu, v, stride);
-                    }
-                    v = ((tid & size) == 0) == ((tid & stride) == 0) ? fmaxf(v, o) : fminf(v, o);
+            // About the m-th greatest, by halves of the order numbers: a value that m + 1 groups or a few more reach (few where nearly all
+            // groups do, as each then stands for many tokens).
+            if (warp == 0) {
+                float v[kThreads / 32];
+#pragma unroll
+                for (int i = 0; i < kThreads / 32; ++i) v[i] = sh.group[lane + 32 * i];
+                unsigned yes = ord_bits(floor), no = ord_bits(row.top) + 1u;
+                while (no - yes > 1u) {
+                    const unsigned mid = yes + (no - yes) / 2;
+                    const float at = ord_value(mid);
+                    int n = 0;
+#pragma unroll
+                    for (int i = 0; i < kThreads / 32; ++i) n += v[i] >= at ? 1 : 0;
+                    n = __reduce_add_sync(0xffffffffu, n);
+                    if (n > m) yes = mid;
+                    else no = mid;
+                    if (n > m && n <= m + 1 + min(m, kThreads - m) / 8) break;
                 }
-            if (tid == m) sh.at = v;
+                if (lane == 0) sh.at = ord_value(yes);
+            }
         }
         if (tid == 0) sh.listed = 0;
         __syncthreads();
@@ -860,7 +867,21 @@ __global__ void __launch_bounds__(kThreads, B == kFewBins ? 2 : 1) sample_rows_k
             u64 key[K], run[K];
 #pragma unroll
             for (int k = 0; k < K; ++k) key[k] = K * tid + k < n ? entry(K * tid + k) : 0ull;
-            sort_keys(key, runs, keys, n);
+            if (K == 1 && n <= kThreads / 4) {  // a key's place is the number of greater ones: four threads count them (a bitonic sort takes 1.2 us more)
+                runs[tid] = key[0];
+                __syncthreads();
+                const int i = tid >> 2;
+                const u64 mine = runs[i];
+                int place = 0;
+                for (int j = tid & 3; j < n; j += 4) place += runs[j] > mine ? 1 : 0;
+                place += __shfl_xor_sync(0xffffffffu, place, 1);
+                place += __shfl_xor_sync(0xffffffffu, place, 2);
+                if (i < n && (tid & 3) == 0) keys[place] = mine;
+                __syncthreads();
+                key[0] = tid < n ? keys[tid] : 0ull;
+            } else {
+                sort_keys(key, runs, keys, n);
+            }
             u64 sum = 0;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
