@@ -366,7 +366,7 @@ __device__ __forceinline__ Cursor find_start(const Prefix &p, const Tables &t, u
     if (blockIdx.x == 0 && lane == 0) p.starts[nrt] = T, p.starts[nrt + 1] = 0;
     T *= p.a.Hkv;
     const int C = (int)gridDim.x;
-    if (nrt * p.a.Hkv * 2 <= C && T > 0 && T < (1ll << 31)) {
+    if (nrt * p.a.Hkv * 2 <= C && T > 0 && T < (1ll << 24)) {  // 32-bit products
         // Few items: each to CTAs of its own if that makes no share longer than two tiles more.  A CTA whose share spans two items ends
         // one with an epilogue and waits for the next one's queries, which is some 5 us.
         const unsigned fair = (unsigned)((T + C - 1) / C), size = fair + (unsigned)lane;
@@ -384,8 +384,8 @@ __device__ __forceinline__ Cursor find_start(const Prefix &p, const Tables &t, u
                     const int j = at % k;
                     c.rt = c.first_rt = rt;
                     c.h = at / k;
-                    c.tile = (int)((long long)tiles * j / k);
-                    c.left = (int)((long long)tiles * (j + 1) / k) - c.tile;
+                    c.tile = (int)(tiles * (unsigned)j / (unsigned)k);
+                    c.left = (int)(tiles * (unsigned)(j + 1) / (unsigned)k) - c.tile;
                 }
                 base += p.a.Hkv * k;
             }
