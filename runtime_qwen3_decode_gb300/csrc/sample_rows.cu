@@ -79,12 +79,15 @@ struct SampleArgs {
     float *probs;
 };
 
+// Order numbers: a float's bits as a whole number that rises with its value, one step a float.  -0 and +0 share one: with a
+// number for each, a zone that ended between them held every +0 where tokens are compared as floats, and only the tokens below where
+// they are compared by keys.
 __device__ __forceinline__ uint32_t ord_bits(float v) {
     const uint32_t u = __float_as_uint(v);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    return (u & 0x80000000u) ? 0u - u : (u | 0x80000000u);
 }
 __device__ __forceinline__ float ord_value(uint32_t e) {
-    return __uint_as_float((e & 0x80000000u) ? (e & 0x7fffffffu) : ~e);
+    return __uint_as_float((e & 0x80000000u) ? (e & 0x7fffffffu) : 0u - e);
 }
 
 // NaN is -inf, -0 is +0, +inf the greatest finite number.

@@ -1,0 +1,31 @@
+"""Edges of the draw of many rows' next tokens (qw_sample_rows): logits about zero, small weights, calls of other sizes."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from test_gpu_sample_rows import check, gen, qw  # noqa: E402, F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("many", [False, True])  # passes of 32 and of 8 parts
+@pytest.mark.parametrize("zeros,below,bits,above", [(10000, 30000, 22, 0), (10328, 38399, 21, 0), (3000, 5000, 8, 300), (700, 20000, 12, 0),
+                                                    (12000, 0, 1, 2000)])
+def test_zeros_beside_numbers_next_to_zero(qw, zeros, below, bits, above, many):  # noqa: F811
+    """Borders on both sides of the place between the greatest negative number and 0.  Every weight is 1, so that
+    the running sums are exact."""
+    r = np.random.default_rng(zeros)
+    x = np.concatenate([np.zeros(zeros, np.float32), -r.integers(1, 1 << bits, below).astype(np.uint32).view(np.float32),
+                        r.integers(1, 1000, above).astype(np.uint32).view(np.float32)])
+    x[: zeros // 2] *= -1.0                             # -0 is 0
+    x = x[r.permutation(len(x))]
+    n = 8 if not many else 160 if len(x) > 24000 else 320
+    share = np.array([zeros + above, above + 1, zeros + above + 1, (zeros + above) // 2, len(x) - 1], np.float64) / len(x)
+    p = np.tile(np.concatenate([[0.26, 0.5, 0.9], share[share < 1]]), n)[:n].astype(np.float32)
+    u = np.resize(np.array([0.0, 0.3, 0.77, 0.9999], np.float32), n)
+    rows = torch.from_numpy(x).cuda().expand(n, len(x))
+    check(qw, rows, u, None, None, p, out_sure=1.0)
+    k = np.resize(np.array([1500, max(1, zeros + above - 1), zeros + above, zeros + above + 1, len(x) - 1], np.int32), n)
+    check(qw, rows, u, None, k, None, out_sure=1.0)
+    check(qw, rows, u, 1e6, k, p, out_sure=1.0)
