@@ -272,11 +272,12 @@ int qw_batch_step(qw_batch *b, int32_t n_seq, const int32_t *tokens_host, int32_
 int qw_batch_fork(qw_batch *b, int32_t src, int32_t dst, int32_t n);
 /*
  * Draw the next tokens of sequences 0 .. n_seq - 1 from the logits of their last positions (of the last qw_batch_step
- * or qw_batch_prefill of each, or what qw_batch_fork took over; QW_INVALID_ARGUMENT if one's are not there, after a
- * tree step for instance) with the given random numbers u[s] and settings, as qw_sample_rows does; device arrays
- * [n_seq], NULL: its defaults.  They take the place of the greedy picks: qw_batch_step(-1) goes on with them.  A row that
- * draws nothing (a setting outside its range) keeps its pick and records QW_INVALID_ARGUMENT, reported as a non-finite
- * logit is.  next_tokens_host [n_seq] (optional) receives the tokens and synchronises.
+ * or qw_batch_prefill of each, or what qw_batch_fork took over) with the given random numbers u[s] and settings, as
+ * qw_sample_rows does; device arrays [n_seq], NULL: its defaults.  QW_INVALID_ARGUMENT if one's logits are not there: a
+ * tree step writes its nodes' over the rows of sequences 0 .. n - 1, and a sequence that accepted nodes has none, until
+ * the next step or prompt of each.  The tokens take the place of the greedy picks: qw_batch_step(-1) goes on with them.  A row
+ * that draws nothing (a setting outside its range) keeps its pick and records QW_INVALID_ARGUMENT, reported as a
+ * non-finite logit is.  next_tokens_host [n_seq] (optional) receives the tokens and synchronises.
  */
 int qw_batch_sample(qw_batch *b, int32_t n_seq, const float *u_dev, const float *temperature_dev, const int32_t *top_k_dev,
                     const float *top_p_dev, const float *min_p_dev, int32_t *next_tokens_host);

@@ -1201,6 +1201,7 @@ int qw_batch_tree_accept(qw_batch *b, int32_t seq, int32_t n, const int32_t *nod
     if (rc) return rc;
     b->len[seq] += n;
     b->has_last[seq] = 1;
+    b->fresh[seq] = false;  // the last position is a node's, whose logits are at the node's row
     return QW_OK;
 }
 
