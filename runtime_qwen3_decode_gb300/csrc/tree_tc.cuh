@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS, TILE>::kThreads, 1)
             mbar_init(&k_full[i], C::kDirect ? 1 : kPlaneWarps);
             mbar_init(&k_empty[i], 1);
             mbar_init(&v_full[i], C::kDirect ? 1 : kPlaneWarps);
-            mbar_init(&v_empty[i], 1);
+            mbar_init(&v_empty[i], PREFIX && C::kDirect ? 3 : 1);  // the MMAs, and warps 8 and 9 where they look V through
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
@@ -1450,12 +1450,16 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS, TILE>::kThreads, 1)
             for (int t = s.t0; ok && t < s.t1; ++t, ++it) {
                 if (t > s.t0) w.next(p);
                 const int st = it % ST;
-                // every tile is waited for: a parity does not tell this phase of a stage from the one before the last
+                // Every tile is waited for and given back: a parity does not tell this phase of a stage from the one before the last,
+                // so the stage must not be filled again while a warp has yet to see that it was.
                 if (!warp_wait(&v_full[st], (unsigned)(it / ST) & 1u, abort)) {
                     ok = false;
                     break;
                 }
-                if (t < s.len / kTcTile) continue;  // a whole tile of the prefix: every row sees it
+                if (t < s.len / kTcTile) {  // a whole tile of the prefix: every row sees it
+                    if (lane == 0) mbar_arrive(&v_empty[st]);
+                    continue;
+                }
                 bool any = false;
                 constexpr int CH = D / 8;  // chunks of a row
                 // rows alternate between the two warps; TMA has zeroed the ones behind the cache
@@ -1475,7 +1479,10 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS, TILE>::kThreads, 1)
                 if (any) bad_seg[seg & 3] = seg + 1;
                 fence_async_shared();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&v_ready[st]);
+                if (lane == 0) {
+                    mbar_arrive(&v_ready[st]);
+                    mbar_arrive(&v_empty[st]);
+                }
             }
             ++seg;
         }
