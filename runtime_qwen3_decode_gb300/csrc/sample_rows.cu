@@ -24,11 +24,12 @@
 // whatever it holds: some 3 us for its bins, the cluster's exchange and the search for the next zone's ends.  256 rows of
 // 151,936 with mixed settings 258 us (HBM floor 23), 8 drawn from nearly everything 46, 8 of usual settings 12.3.
 //
-// Weights are whole numbers, 2^wb for the weight 1 (wb >= 38, 44 at a vocabulary of 151,936), so that their
-// sums are exact: they do not depend on the order of addition, on the number of CTAs or on timing, and a
-// border that is met exactly is met.  A weight itself is off by 2.4e-9 at most (weigh()): where it is decided by a
-// running sum which token is drawn, f32 weights (6e-8, and 4e-7 from the product with 1 / T) would move a border
-// past a token of weight 1e-6 in every tenth row.
+// Weights are whole numbers, 2^wb for the weight 1 (wb by the vocabulary: 44 at 151,936, never below 38), so that their
+// sums are exact: they do not depend on the order of addition, on the number of CTAs, on the other rows or on timing, and a
+// border that is met exactly is met.  A weight itself is off by 2.4e-9 of itself (weigh()) and half a unit at most: where it is
+// decided by a running sum which token is drawn, f32 weights (6e-8, and 4e-7 from the product with 1 / T) would move a border
+// past a token of weight 1e-6 in every tenth row.  Half units can all have one sign, V 2^-(wb + 1) together: 4.3e-9 at 151,936
+// tokens, where u and top_p have steps of 6e-8, but 3e-5 at 2^24, as 64-bit sums leave no room for smaller units.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -135,7 +136,8 @@ __device__ __forceinline__ void split2(const Row &w, float2 x, int (&q)[2], floa
 
 // Two weights in units of 2^-wb: 2^(q / 32) from the table, times 2^r - 1 by its series to r^4, which is small (0.011) and so
 // right to 2.4e-9 in f32: r to 2^-31, the series to 2^-31, the table's f32 and its product with the series to 2^-24 of 0.011
-// each; the table's whole number to 2^-32.  These errors do not add up over many tokens: they have either sign.
+// each; the table's whole number to 2^-32.  These errors do not add up over many tokens: they have either sign.  Rounding to a unit
+// is off by half of one more.
 __device__ __forceinline__ void weigh2(const Row &w, const Table &t, float2 x, u64 (&out)[2]) {
     int q[2];
     float2 r;
@@ -1008,16 +1010,22 @@ cudaError_t launch_typed(const qw_sample_rows_args &q, cudaStream_t st) {
     const size_t most = 227 * 1024, room = most - fixed(kFewBins);
     // As many CTAs for a row as there are SMs to take them, or as hold it with another CTA on the SM.  (Clusters of 16 for up to
     // nine rows took 1.3 us more at 8 x 151,936: what grows with the cluster outweighs the shorter pieces.)
-    int ctas = 1;
     auto per = [&](int n) { return (int)(((int64_t)q.vocab + n - 1) / n + 7) / 8 * 8; };
-    while (ctas < kMaxCluster && per(ctas) > 4096 && ((int64_t)q.n_rows * ctas * 2 <= 152 || (size_t)per(ctas) * 4 > room / 2)) ctas *= 2;
+    auto ctas_for = [&](int64_t rows) {
+        int n = 1;
+        while (n < kMaxCluster && per(n) > 4096 && (rows * n * 2 <= 152 || (size_t)per(n) * 4 > room / 2)) n *= 2;
+        return n;
+    };
+    const int ctas = ctas_for(q.n_rows);
     SampleArgs a{};
     a.logits = q.logits;
     a.stride = q.row_stride;
     a.V = q.vocab;
     a.per = per(ctas);
     a.id_bits = bits_for(q.vocab);
-    a.wb = std::min(62 - a.id_bits, kCountBit - 1 - bits_for((a.per + 4 * kThreads - 1) / (4 * kThreads) * 4));  // a thread's tokens fit its bins
+    // A thread's tokens fit its bins, whatever the number of rows: the weights' unit, and with it what a row draws, goes by the
+    // vocabulary alone.
+    a.wb = std::min(62 - a.id_bits, kCountBit - 1 - bits_for((per(ctas_for(INT32_MAX)) + 4 * kThreads - 1) / (4 * kThreads) * 4));
     a.rows = q.n_rows;
     // Worth it for one to eight waves of rows of four or more CTAs (us, mixed settings, with it and without: 48 rows of 151,936 70
     // and 78, 128 139 and 150; 150 of 65,000 92 and 95); more of them, or smaller ones, run better side by side with short ones (512 of

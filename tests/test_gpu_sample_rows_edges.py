@@ -29,3 +29,27 @@ def test_zeros_beside_numbers_next_to_zero(qw, zeros, below, bits, above, many):
     k = np.resize(np.array([1500, max(1, zeros + above - 1), zeros + above, zeros + above + 1, len(x) - 1], np.int32), n)
     check(qw, rows, u, None, k, None, out_sure=1.0)
     check(qw, rows, u, 1e6, k, p, out_sure=1.0)
+
+
+@pytest.mark.parametrize("V", [8192, 20011, 40000, 65000])
+def test_a_row_draws_the_same_alone_and_among_many(qw, V):  # noqa: F811
+    """The number of rows decides how many CTAs a row has; tokens of 2^-29 of the first one's weight show in their
+    probabilities what unit weights have."""
+    g = gen(V)
+    x = (-20.0 + 0.5 * torch.randn((1, V), generator=g, device="cuda")).contiguous()
+    x[0, V // 3] = 0.0
+    n = 24
+    u = torch.cat([torch.rand((n // 2,), generator=g, device="cuda"), 1 - 2.0 ** -24 * torch.arange(1, 13, device="cuda") * V / 4096])
+    many = 320 // n * n + n
+
+    def draw(rows, u, k, p, m):
+        f = lambda v, d: torch.full((rows,), v, dtype=d, device="cuda")  # noqa: E731
+        kept, probs = torch.zeros(rows, dtype=torch.int32, device="cuda"), torch.zeros(rows, device="cuda")
+        tok = qw.sample_rows(x.expand(rows, V), u, f(1.0, torch.float32), f(k, torch.int32), f(p, torch.float32), f(m, torch.float32),
+                             probs=probs, kept=kept)
+        return torch.stack([tok.double(), kept.double(), probs.double()])
+    for k, p, m in ((0, 1.0, 0.0), (0, 0.99999, 0.0), (3000, 1.0, 0.0), (900, 1.0, 0.0), (0, 0.99999, 1e-9), (0, 1.0, 2e-9)):
+        alone = torch.cat([draw(1, u[i:i + 1], k, p, m) for i in range(n)], 1)
+        assert alone[0].unique().numel() > 1
+        for rows in (n, many):
+            assert torch.equal(draw(rows, u.repeat(rows // n), k, p, m), alone.repeat(1, rows // n)), (k, p, m, rows)
