@@ -492,7 +492,12 @@ int qw_process_logits(const qw_process_logits_args *args, void *cuda_stream);
  * QW_SAMPLE_MAX_TOP_K, and with the caller's numbers in the place of PCG32.  Temperature 0 takes the first
  * token (probs 1, kept 1) whatever the others are.  Temperatures otherwise of [1e-6, 1e6], top_p of (0, 1],
  * min_p of [0, 1], u of [0, 1): a row with another one, and a row without candidates, gets token -1, probs 0,
- * kept 0.  The running sums are exact sums of weights right to 2.4e-9, the same on every call.
+ * kept 0.
+ * The running sums are exact sums of weights that are whole multiples of 2^-b of w_1 and right to 2.4e-9 of themselves
+ * and half a multiple: b >= 44 up to vocab 2^18, 62 - log2(vocab) (rounded up) above.  All of a row's tokens together
+ * so move by at most 2.4e-9 of their sum and vocab 2^-(b + 1) of w_1: 4.3e-9 at 151,936 tokens, less than one step of u or
+ * top_p; 3.1e-5 at 2^24, where weights below 2^-39 of w_1 count for nothing.  What a row draws depends on its logits, u and
+ * settings alone: it is the same on every call, whatever other rows the call has.
  * NULL: temperature 1, top_k 0, top_p 1, min_p 0; probs and kept may be NULL.  All parameters and results
  * are device arrays [n_rows].  n_rows <= 65535, vocab <= 2^24.
  */

@@ -53,3 +53,35 @@ def test_a_row_draws_the_same_alone_and_among_many(qw, V):  # noqa: F811
         assert alone[0].unique().numel() > 1
         for rows in (n, many):
             assert torch.equal(draw(rows, u.repeat(rows // n), k, p, m), alone.repeat(1, rows // n)), (k, p, m, rows)
+
+
+def unit_bits(V):
+    return 44 if V <= 1 << 18 else 62 - (V - 1).bit_length()
+
+
+@pytest.mark.parametrize("V", [151936, 1 << 20, 1 << 22])
+@pytest.mark.parametrize("units", [0.49, 0.51, 1.45, 1.55, 3.4, 30.45])
+def test_long_tails_of_small_weights(qw, V, units):  # noqa: F811
+    """One sure token and V - 1 whose weights are `units` of the unit: each is off by 2.4e-9 of itself and half a unit at
+    most, so any running sum by `off`, and what is drawn is what the definition draws within that of its border."""
+    unit = 2.0 ** -unit_bits(V)
+    tail = np.float32(np.log(units * unit))
+    x = torch.full((1, V), float(tail), device="cuda")
+    x[0, 0] = 0.0
+    w = np.exp(np.float64(tail))
+    S = 1 + (V - 1) * w
+    off = 2.4e-9 * S + (V - 1) * unit / 2
+    u = (1 - np.arange(1, 9) * 2.0 ** -24).astype(np.float32)
+    kept, probs = torch.zeros(8, dtype=torch.int32, device="cuda"), torch.zeros(8, device="cuda")
+    tok = qw.sample_rows(x.expand(8, V), torch.from_numpy(u).cuda(), kept=kept, probs=probs).cpu().numpy()
+    assert (kept == V).all()                            # all of them are candidates, whatever they weigh
+    for t, uu, pr in zip(tok, u.astype(np.float64), probs.cpu().numpy().astype(np.float64)):
+        before, upto = (0 if t == 0 else 1 + (t - 1) * w), 1 + t * w
+        # the sums that are compared are those before and up to the token, and u times the last one
+        assert before - 2 * off <= uu * S < upto + 2 * off
+        wt = 1.0 if t == 0 else w
+        assert abs(pr - wt / S) <= (2.4e-9 * wt + unit / 2 + pr * off) / S * (1 + 1e-6) + 2 ** -23 * (wt / S + pr)
+    p = (1 - np.arange(1, 9) * 2.0 ** -24).astype(np.float32)
+    qw.sample_rows(x.expand(8, V), torch.zeros(8, device="cuda"), top_p=torch.from_numpy(p).cuda(), kept=kept)
+    for n, pp in zip(kept.tolist(), p.astype(np.float64)):
+        assert 1 + (n - 2) * w - 2 * off < pp * S <= 1 + (n - 1) * w + 2 * off or (n == 1 and pp * S <= 1 + 2 * off)
