@@ -197,10 +197,11 @@ static void *row_worker(void *p) {
     return NULL;
 }
 
-static void parallel_rows(int nthreads, int64_t n, row_fn fn, void *ctx) {
+/* fn over [0, n), cut into equal parts, one per thread; by the caller alone where n is below `least`. */
+static void parallel_rows(int nthreads, int64_t n, int64_t least, row_fn fn, void *ctx) {
     if (nthreads < 1) nthreads = 1;
     if (nthreads > 256) nthreads = 256;
-    if (n < 64 || nthreads == 1) {
+    if (n < least || nthreads == 1) {
         fn(ctx, 0, n);
         return;
     }
@@ -276,7 +277,7 @@ static void matvec(int nthreads, const ora_mat *m, const float *x, float *y, con
         c.xq = xq;
         c.xs = xs;
     }
-    parallel_rows(nthreads, m->rows, matvec_rows, &c);
+    parallel_rows(nthreads, m->rows, 64, matvec_rows, &c);
     free(xq);
     free(xs);
 }
@@ -568,7 +569,9 @@ static int layer_step(ora_model *md, int l, float *x, int pos, float *buf) {
     attn_ctx ac;
     ac.m = md; ac.l = l; ac.pos = pos; ac.q = q; ac.o = o; ac.scratch = scratch;
     memset(ac.rc, 0, sizeof(ac.rc));
-    parallel_rows(Hq >= 4 ? nt : 1, Hq, attn_heads, &ac);
+    /* heads on threads of their own once a head is work enough to start one (some 100 us of 256 positions); a head's
+     * arithmetic is the same on any thread */
+    parallel_rows(pos + 1 >= 256 ? nt : 1, Hq, 4, attn_heads, &ac);
     for (int hh = 0; hh < Hq; ++hh)
         if (ac.rc[hh]) return ac.rc[hh];
     /* 7. output projection with residual */
