@@ -107,6 +107,7 @@ def lib():
             L.ora_kv_reset.restype = None
             L.ora_kv_import.argtypes = [vp, u16p, u16p, ctypes.c_int32]
             L.ora_step.argtypes = [vp, ctypes.c_int32, f32p, vp]
+            L.ora_prompt.argtypes = [vp, ctypes.POINTER(ctypes.c_int32), ctypes.c_int32]
             L.ora_full.argtypes = [vp, ctypes.POINTER(ctypes.c_int32), ctypes.c_int32, f32p]
             L.ora_set_kv_round_bf16.argtypes = [vp, ctypes.c_int]
             L.ora_set_kv_round_bf16.restype = None
@@ -337,6 +338,13 @@ class OracleModel:
             raise OracleError(rc, "step")
         return logits, hidden
 
+    def prompt(self, tokens):
+        """Prompt rows whose logits nobody reads: the same bits in the cache as one step for each, in blocks."""
+        t = np.ascontiguousarray(tokens, dtype=np.int32)
+        rc = lib().ora_prompt(self._h, t.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)), t.size)
+        if rc:
+            raise OracleError(rc, "prompt")
+
     def full(self, tokens) -> np.ndarray:
         """No-cache, causal-mask recomputation of every position's logits [T, V]."""
         t = np.ascontiguousarray(tokens, dtype=np.int32)
@@ -354,14 +362,17 @@ def top2_margin(logits: np.ndarray) -> float:
 
 
 def run_sequence(model: OracleModel, prompt, n_decode: int, want_hidden: bool = False, forced=None):
-    """Prefill token by token, then greedy decode (or teacher-force `forced`).
+    """Prefill, then greedy decode (or teacher-force `forced`).
 
+    Prompts of more than 16 tokens go in blocks up to the last one, which gives the bits that they give token by token.
     Returns dict with per-step logits (only for the last prompt position and
     each decode step), tokens fed, greedy picks, and hidden states if asked.
     """
     out = {"logits": [], "hidden": [], "inputs": [], "picks": []}
     last = None
-    for i, tok in enumerate(prompt):
+    done = len(prompt) - 1 if len(prompt) > 16 else 0
+    model.prompt(prompt[:done])
+    for i, tok in enumerate(prompt[done:], done):
         is_last = i == len(prompt) - 1
         logits, hid = model.step(int(tok), want_hidden and is_last, want_logits=is_last)
         last = logits

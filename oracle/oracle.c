@@ -634,6 +634,156 @@ int ora_step(ora_model *md, int32_t token, float *logits, float *hidden) {
     return rc;
 }
 
+/* ------------------------------------------------------- prompt rows in blocks */
+
+/*
+ * A block of prompt rows through a matrix: every (row, token) dot is mat_row_dot's, products and sums in the same order
+ * over k; the tokens of a group stand side by side, so that one conversion of a weight row serves them all and
+ * their sums do not wait for one another.
+ */
+enum { GROUP = 8, BLOCK = 64 };
+
+typedef struct {
+    const ora_mat *m;
+    const float *xt;  /* [tokens / GROUP][cols][GROUP] */
+    int T;
+    float *y;         /* [T][rows] */
+    int add;          /* y += dot, else y = dot */
+} matmat_ctx;
+
+static void matmat_rows(void *p, int64_t b, int64_t e) {
+    matmat_ctx *c = (matmat_ctx *)p;
+    const ora_mat *m = c->m;
+    float *w = (float *)malloc(sizeof(float) * (size_t)m->cols);
+    for (int64_t r = b; r < e; ++r) {
+        if (m->fmt == ORA_W_BF16) {
+            const uint16_t *row = (const uint16_t *)m->w + r * m->cols;
+            for (int k = 0; k < m->cols; ++k) w[k] = ora_bf16_to_f32(row[k]);
+        } else {
+            const int8_t *q = (const int8_t *)m->w + r * m->cols;
+            const uint16_t *s = m->s + r * (m->cols / 32);
+            for (int k = 0; k < m->cols; ++k) w[k] = (float)q[k] * ora_f16_to_f32(s[k / 32]);
+        }
+        for (int t0 = 0; t0 < c->T; t0 += GROUP) {
+            const float *x = c->xt + (size_t)t0 * m->cols;
+            float acc[GROUP] = {0.0f};
+            for (int k = 0; k < m->cols; ++k)
+                for (int i = 0; i < GROUP; ++i) acc[i] += x[(size_t)k * GROUP + i] * w[k];
+            for (int i = 0; i < GROUP && t0 + i < c->T; ++i) {
+                float *y = c->y + (size_t)(t0 + i) * m->rows + r;
+                *y = c->add ? *y + acc[i] : acc[i];
+            }
+        }
+    }
+    free(w);
+}
+
+static void matmat(int nthreads, const ora_mat *m, const float *x, int T, float *y, int add, float *xt) {
+    if (m->fmt == ORA_W_Q8Q8) {
+        for (int t = 0; t < T; ++t) {
+            float *yt = y + (size_t)t * m->rows;
+            matvec(nthreads, m, x + (size_t)t * m->cols, yt, add ? yt : NULL);
+        }
+        return;
+    }
+    for (int t0 = 0; t0 < T; t0 += GROUP)
+        for (int k = 0; k < m->cols; ++k)
+            for (int i = 0; i < GROUP; ++i)
+                xt[(size_t)t0 * m->cols + (size_t)k * GROUP + i] = t0 + i < T ? x[(size_t)(t0 + i) * m->cols + k] : 0.0f;
+    matmat_ctx c = {m, xt, T, y, add};
+    parallel_rows(nthreads, m->rows, 64, matmat_rows, &c);
+}
+
+typedef struct {
+    const ora_model *m;
+    int l, pos, T;
+    const float *q; /* [T][Hq][d] */
+    float *o;
+    int *rc;        /* [T][Hq] */
+} attn_block_ctx;
+
+static void attn_block(void *p, int64_t b, int64_t e) {
+    attn_block_ctx *a = (attn_block_ctx *)p;
+    const ora_config *c = &a->m->cfg;
+    const int Hq = c->n_heads, d = c->head_dim;
+    float *scratch = (float *)malloc(sizeof(float) * (size_t)(a->pos + a->T));
+    for (int64_t i = b; i < e; ++i) {
+        const int t = (int)(i / Hq), kvh = (int)(i % Hq) / (Hq / c->n_kv_heads);
+        a->rc[i] = ora_attention_head(a->q + i * d, kv_row(a->m, a->m->k_cache, a->l, kvh, 0),
+                                      kv_row(a->m, a->m->v_cache, a->l, kvh, 0), a->pos + t + 1, d, d, a->o + i * d, scratch);
+    }
+    free(scratch);
+}
+
+/* layer_step for T tokens at positions pos, pos + 1, ..; X [T][H] updated in place. */
+static int layer_block(ora_model *md, int l, float *X, int pos, int T, float *buf, int *rc) {
+    const ora_config *c = &md->cfg;
+    const ora_layer *ly = &md->layers[l];
+    const int H = c->hidden, d = c->head_dim, Hq = c->n_heads, Hkv = c->n_kv_heads, I = c->intermediate, nt = c->nthreads;
+    const size_t B = BLOCK;
+    float *h = buf, *q = h + B * H, *k = q + B * Hq * d, *v = k + B * Hkv * d, *o = v + B * Hkv * d, *g = o + B * Hq * d,
+          *u = g + B * I, *tmp = u + B * I, *xt = tmp + d;
+    ora_mat mq = layer_mat(md, ly, M_Q), mk = layer_mat(md, ly, M_K), mv = layer_mat(md, ly, M_V), mo = layer_mat(md, ly, M_O);
+    ora_mat mg = layer_mat(md, ly, M_GATE), mu = layer_mat(md, ly, M_UP), mdn = layer_mat(md, ly, M_DOWN);
+    for (int t = 0; t < T; ++t) ora_rmsnorm(X + (size_t)t * H, ly->input_norm, H, c->rms_eps, h + (size_t)t * H);
+    matmat(nt, &mq, h, T, q, 0, xt);
+    matmat(nt, &mk, h, T, k, 0, xt);
+    matmat(nt, &mv, h, T, v, 0, xt);
+    for (int t = 0; t < T; ++t) {
+        const float *cs = md->cos_t + (size_t)(pos + t) * (d / 2), *sn = md->sin_t + (size_t)(pos + t) * (d / 2);
+        for (int hh = 0; hh < Hq; ++hh) ora_qk_norm_rope(q + ((size_t)t * Hq + hh) * d, ly->q_norm, d, c->rms_eps, cs, sn, tmp);
+        for (int hh = 0; hh < Hkv; ++hh) {
+            float *kt = k + ((size_t)t * Hkv + hh) * d, *vt = v + ((size_t)t * Hkv + hh) * d;
+            ora_qk_norm_rope(kt, ly->k_norm, d, c->rms_eps, cs, sn, tmp);
+            float *kd = kv_row(md, md->k_cache, l, hh, pos + t), *vd = kv_row(md, md->v_cache, l, hh, pos + t);
+            for (int i = 0; i < d; ++i) {
+                kd[i] = md->kv_round_bf16 ? round_bf16(kt[i]) : kt[i];
+                vd[i] = md->kv_round_bf16 ? round_bf16(vt[i]) : vt[i];
+            }
+        }
+    }
+    attn_block_ctx ac = {md, l, pos, T, q, o, rc};
+    parallel_rows(nt, (int64_t)T * Hq, 4, attn_block, &ac);
+    for (int i = 0; i < T * Hq; ++i)
+        if (rc[i]) return rc[i];
+    matmat(nt, &mo, o, T, X, 1, xt);
+    for (int t = 0; t < T; ++t) ora_rmsnorm(X + (size_t)t * H, ly->post_norm, H, c->rms_eps, h + (size_t)t * H);
+    matmat(nt, &mg, h, T, g, 0, xt);
+    matmat(nt, &mu, h, T, u, 0, xt);
+    for (size_t i = 0; i < (size_t)T * I; ++i) g[i] = ora_silu(g[i]) * u[i];
+    matmat(nt, &mdn, g, T, X, 1, xt);
+    return finite_all(X, (int64_t)T * H) ? ORA_OK : ORA_NUMERICAL_FAILURE;
+}
+
+/*
+ * T prompt rows whose logits nobody reads, BLOCK at a time: the cache is left as T calls of ora_step leave it, bit for
+ * bit.  On an error the length is that of the blocks before the failing one.
+ */
+int ora_prompt(ora_model *md, const int32_t *tokens, int32_t T) {
+    const ora_config *c = &md->cfg;
+    if (T < 0) return ORA_INVALID_ARGUMENT;
+    for (int t = 0; t < T; ++t)
+        if (tokens[t] < 0 || tokens[t] >= c->vocab) return ORA_INVALID_ARGUMENT;
+    if (T > c->max_ctx - md->len) return ORA_CONTEXT_EXCEEDED;
+    const size_t H = c->hidden, I = c->intermediate, d = c->head_dim, qd = (size_t)c->n_heads * d, kvd = (size_t)c->n_kv_heads * d;
+    const size_t widest = H > I ? (H > qd ? H : qd) : (I > qd ? I : qd);
+    float *X = (float *)malloc(sizeof(float) * BLOCK * H);
+    float *buf = (float *)malloc(sizeof(float) * (BLOCK * (H + 2 * qd + 2 * kvd + 2 * I + widest) + d));
+    int *rcs = (int *)malloc(sizeof(int) * BLOCK * (size_t)c->n_heads);
+    int rc = ORA_OK;
+    for (int t0 = 0; t0 < T && !rc; t0 += BLOCK) {
+        const int n = T - t0 < BLOCK ? T - t0 : BLOCK;
+        for (int t = 0; t < n; ++t)
+            for (size_t i = 0; i < H; ++i) X[(size_t)t * H + i] = ora_bf16_to_f32(md->embed[(size_t)tokens[t0 + t] * H + i]);
+        for (int l = 0; l < c->n_layers && !rc; ++l) rc = layer_block(md, l, X, md->len, n, buf, rcs);
+        if (!rc) md->len += n;
+    }
+    free(X);
+    free(buf);
+    free(rcs);
+    return rc;
+}
+
 /*
  * Full-sequence recomputation with no cache reuse: all T positions pass
  * through each layer together and attention applies the causal mask
