@@ -55,8 +55,9 @@
 #include <cuda.h>
 
 #include <algorithm>
-#include <type_traits>
+#include <cfloat>
 #include <cmath>
+#include <type_traits>
 
 #include "tc.cuh"
 #include "tree_attn.h"
@@ -922,7 +923,8 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS, TILE>::kThreads, 1)
             }
             if (nodes < 64) mask &= (1ull << nodes) - 1ull;
             const bool scaled_row = !C::kBf16 && a.dtype == QW_DT_BF16 && live;
-            const float sc = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2) * (scaled_row ? row_scale[r] : 1.f);
+            // not below the least normal number: times 0 a hidden score would be NaN, and such a row's seen ones round to 0 all the same
+            const float sc = a.scale_log2 == 0.f ? 1.f : fmaxf(fabsf(a.scale_log2) * (scaled_row ? row_scale[r] : 1.f), FLT_MIN);
             float m_used = -INFINITY, l = 0.f;
             int mine = 0;  // tiles of this segment that this group has done
             w.start(p, s);

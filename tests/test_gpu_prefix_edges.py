@@ -29,3 +29,21 @@ def test_long_runs_of_tiles(qw, B, P, L, D):  # noqa: F811
     at = [None if o is None else o[some] for o in own]
     ref, mag, vmax = tree_reference(q[some], joined(pre, at, P), mask[some], [P + int(lens[b]) for b in some], [1] * 3, D ** -0.5)
     assert ((want[some].double() - ref).abs() <= tolerance(BF16, "bf16", mag, vmax, P + L + 1, D)).all()
+
+
+@pytest.mark.parametrize("tc", [False, True])
+@pytest.mark.parametrize("dt,kind,D", [(BF16, "int8", 128), (BF16, "int8", 64), (BF16, "bf16", 128), (F16, "f32", 128), (F32, "f32", 64)])
+def test_scores_that_underflow(qw, tc, dt, kind, D):  # noqa: F811
+    """Queries near the type's smallest numbers and a small scale: every score rounds to 0, and a row is the mean of what it
+    sees.  The factor of a row's scores underflows, and what is hidden must not become 0 x -inf."""
+    B, H, n, P = 3, 2, 4, 300
+    g = gen(30)
+    pre, own = make_prefix(kind, (1, H, P, D), g, tc), make_cache(kind, (B, H, 200, D), g)
+    tiny = float(torch.finfo(dt).tiny)
+    q = (tiny * torch.randn((B, n, 2 * H, D), generator=g, device="cuda")).to(dt)
+    lens = [150, 0, 31]
+    mask = torch.tensor([[1, 3, 5, 9]] * B, dtype=torch.int64, device="cuda")
+    scale = 1e-9
+    got = qw.prefix_attention(qw.KvView(*pre), qw.KvView(*own), q, i32(*lens), i32(P), mask=mask, scale=scale)
+    ref, mag, vmax = tree_reference(q, joined(pre, own, P), mask, [P + x for x in lens], [n] * B, scale)
+    assert ((got.double() - ref).abs() <= tolerance(dt, kind, mag, vmax, P + 200, D)).all()
