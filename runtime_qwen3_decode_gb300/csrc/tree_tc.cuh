@@ -91,6 +91,10 @@ struct Cfg {
     // whole counted for half of that).  A lag of 4 and a lift of 11 took 58.3 us for the 16-sequence case below
     // instead of 57.4, 8 and 7 56.7.  bf16 has f32's range.
     static constexpr float kLag = kBf16 ? 8.f : 6.f, kLift = kBf16 ? 0.f : 9.f;
+    // PREFIX: sums of softmax weights are of the rounded ones, so that the result is a mean and what a large weight is off by does
+    // not move it (16 rows over 200 keys: up to 1.43 times as far off as one rounding of the result leaves them, else
+    // 1.77).  bf16 results beside fp16 weights (8-bit rows) do not show it, and would pay 8%.
+    static constexpr bool kSumRounded = !(SRC == SRC_Q8_F16 && TERMS == 1);
     static constexpr int kElem = SRC == SRC_Q8_F16 ? 1 : SRC == SRC_F32_F16 || SRC == SRC_F32_BF16 ? 4 : 2;
     static constexpr int kThreads = 32 * (kDirect ? kPlainWarps : kPlainWarps + kConvWarps - 2);
     static constexpr int kTile = TILE;
@@ -507,6 +511,16 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
         const __half2 h = __floats2half2_rn(a, b);
         return *reinterpret_cast<const uint32_t *>(&h);
     }
+}
+
+// Two packed weights added to a pair of f32 sums (by unpacking them, fp16 ones take 8% of a call; the mixed addition takes 1%,
+// but of bf16 ones, which are f32's upper halves, a percent more than that).
+template <bool BF16>
+__device__ __forceinline__ void add2(float2 &l, uint32_t p) {
+    if constexpr (BF16)
+        l = __fadd2_rn(l, make_float2(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u)));
+    else
+        asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tadd.rn.f32.f16 %0, a, %0;\n\tadd.rn.f32.f16 %1, b, %1;}" : "+f"(l.x), "+f"(l.y) : "r"(p));
 }
 
 // Two packed weights times a power of two.
@@ -1014,8 +1028,9 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS, TILE>::kThreads, 1)
                             for (int i = 0; i < 16; ++i) {
                                 const float2 z = __ffma2_rn(make_float2(v[2 * i], v[2 * i + 1]), make_float2(sc, sc), make_float2(-mm, -mm));
                                 const float2 e = make_float2(sees ? fast_exp2(z.x) : 0.f, sees ? fast_exp2(z.y) : 0.f);
-                                l2 = __fadd2_rn(l2, e);
                                 pk[i] = pack2<C::kBf16>(e.x, e.y);
+                                if constexpr (C::kSumRounded) add2<C::kBf16>(l2, pk[i]);
+                                else l2 = __fadd2_rn(l2, e);
                             }
                             l += l2.x + l2.y;
                             tmem_st16u(tS + 16u * c, pk);

@@ -4,7 +4,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_ops import BF16, F16, F32, gen, i32, make_cache, tolerance, tree_reference  # noqa: E402, F401
+from test_gpu_ops import BF16, F16, F32, U, gen, i32, make_cache, tolerance, tree_reference  # noqa: E402, F401
 from test_gpu_prefix import ROOM, joined, make_prefix, qw, run  # noqa: E402, F401
 
 pytestmark = pytest.mark.gpu
@@ -47,3 +47,38 @@ def test_scores_that_underflow(qw, tc, dt, kind, D):  # noqa: F811
     got = qw.prefix_attention(qw.KvView(*pre), qw.KvView(*own), q, i32(*lens), i32(P), mask=mask, scale=scale)
     ref, mag, vmax = tree_reference(q, joined(pre, own, P), mask, [P + x for x in lens], [n] * B, scale)
     assert ((got.double() - ref).abs() <= tolerance(dt, kind, mag, vmax, P + 200, D)).all()
+
+
+@pytest.mark.parametrize("tc", [False, True])
+@pytest.mark.parametrize("dt,kind", [(BF16, "bf16"), (BF16, "int8"), (BF16, "f32"), (F16, "int8"), (F16, "f32"), (F16, "bf16")])
+@pytest.mark.parametrize("where", ["prefix", "own"])
+def test_a_row_that_sees_one_key_is_its_value(qw, tc, dt, kind, where):  # noqa: F811
+    """One score some 50 above all others: whatever its weight is rounded to, the result is that position's V.  The others
+    are at most 700 e^-45 = 2e-17 of it; the result's rounding leaves u, f32 sums and quotients 2^-20, V as the products
+    hold it 2^-21 (two fp16 terms) or 2^-16 (two of bf16).  8-bit rows beside bf16 queries: V and the weight, which the sum
+    takes unrounded, are one fp16 number each, 2^-11."""
+    B, H, D, P = 64, 2, 128, 500
+    g = gen(31)
+    pre, own = make_prefix(kind, (1, H, P, D), g, tc), make_cache(kind, (B, H, 200, D), g)
+    u = torch.randint(0, 2, (D,), generator=g, device="cuda") * 2.0 - 1.0
+    for t, at in ((pre, (0, slice(None), 77)), (own, (slice(None), slice(None), 33))):
+        k = t[0]
+        if kind == "int8":
+            k.copy_(torch.randint(-3, 4, k.shape, generator=g, device="cuda").to(k.dtype))
+            t[2].fill_(0.01)
+        else:
+            k.mul_(0.03)
+        if (t is pre) == (where == "prefix"):
+            k[at] = (100 * u).to(k.dtype) if kind == "int8" else u.to(k.dtype)
+    # every row another score of the one key: its weight lies anywhere between two powers of two
+    a = (4.0 + 3.0 * torch.rand((B, 1, H, 1), generator=g, device="cuda")).to(dt)
+    q = (a.float() * u).to(dt)
+    lens = i32(*[40 + 2 * b for b in range(B)])
+    got = qw.prefix_attention(qw.KvView(*pre), qw.KvView(*own), q, lens, i32(P)).double()
+    at = (pre, (slice(None), slice(None), 77)) if where == "prefix" else (own, (slice(None), slice(None), 33))
+    v = at[0][1][at[1]].double()
+    if kind == "int8":
+        v = v * at[0][3][at[1]].double().repeat_interleave(32, -1)
+    v = v.expand(B, H, D).unsqueeze(1)
+    tol = U[dt] + (2 * 2.0 ** -11 if dt is BF16 and kind == "int8" else 2.0 ** -16 if dt is BF16 else 2.0 ** -21) + 2.0 ** -20
+    assert ((got - v).abs() <= tol * v.abs() + 1e-7).all(), float(((got - v).abs() / v.abs().clamp(min=1e-3)).max())
