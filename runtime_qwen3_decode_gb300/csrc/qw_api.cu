@@ -989,8 +989,12 @@ qw::BatchStep batch_step_of(qw_batch *b, int rows) {
 }
 
 constexpr int kPrefixGraphs = 16;     // captured steps over shared prefixes that are kept
-// Steps of sequences that share at least this many positions read them once.
-constexpr int kSharedMin = 256;
+// Steps of n sequences that share at least this many positions read them once.  Measured, 0.6B shape, ms a step over copies and
+// shared: 256 positions of f32 rows, two sequences 0.957 and 0.936, eight 1.418 and 1.392 (three and four lose 0.05 until 512,
+// where they gain 0.06 and 0.08).  8-bit copies are a quarter of the bytes, so that few of them cost little: two sequences 512 1.006
+// and 1.039, 1,024 1.069 and 1.063; three 512 1.073 and 1.119, 768 1.185 and 1.129; five 512 1.314 and 1.340, 768 1.486 and
+// 1.353; six 256 1.326 and 1.263.
+int shared_min(int n, int kv_format) { return kv_format != QW_KV_INT8_G32 || n > 5 ? 256 : n == 2 ? 1024 : 768; }
 
 // Positions that sequences 0 .. n - 1 share, 0 where that is not worth it.
 int shared_prefix(const qw_batch *b, int n) {
@@ -999,7 +1003,7 @@ int shared_prefix(const qw_batch *b, int n) {
         if (n < 2 || b->group[s] == 0 || b->group[s] != b->group[0]) return 0;
         P = std::min(P, std::min(b->shared[s], b->len[s]));
     }
-    return P >= kSharedMin ? P : 0;
+    return P >= shared_min(n, b->kv_format) ? P : 0;
 }
 
 // Launches the step's captured graph, capturing it first if this combination is new.

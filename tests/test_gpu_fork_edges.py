@@ -65,6 +65,15 @@ def test_a_tree_of_which_nothing_is_kept_leaves_the_logits(qw, tiny):  # noqa: F
     b.close()
 
 
+@pytest.fixture(scope="module")
+def long(qw):  # noqa: F811
+    wl = qi.WORKLOADS["tiny"]
+    m = qw.Model(wl, qw.weights_to_device(qi.make_weights(wl), int8=False), max_ctx=4200)
+    m.set_debug(qw.DEBUG_HIDDEN)
+    yield wl, m
+    m.close()
+
+
 LAYERS, KV_HEADS, DIM = 2, 8, 128                    # of the small model
 
 
@@ -75,8 +84,7 @@ def key_rows(b, seq, kv, ctx):
     return t[seq * n:(seq + 1) * n].view(LAYERS, KV_HEADS, ctx, DIM)
 
 
-@pytest.mark.parametrize("kv", ["model", "int8"])
-@pytest.mark.parametrize("n_seq,n", [(2, 256), (3, 300), (8, 511)])
+@pytest.mark.parametrize("kv,n_seq,n", [("model", 2, 256), ("model", 3, 300), ("model", 8, 511), ("int8", 8, 256), ("int8", 6, 511)])
 def test_shared_positions_are_read_once(qw, tiny, kv, n_seq, n):  # noqa: F811
     """A step's result does not depend on a later sequence's copies of what all share, and does on the first one's; where
     nothing is known to be shared it is the other way round."""
@@ -109,6 +117,27 @@ def test_shared_positions_are_read_once(qw, tiny, kv, n_seq, n):  # noqa: F811
     assert torch.equal(moved[0], want[0]) and not torch.equal(moved[last], want[last])
 
 
+@pytest.mark.parametrize("n_seq,n", [(2, 1023), (3, 767), (5, 767), (2, 1024), (3, 768), (5, 768)])
+def test_few_sequences_over_8_bits_share_long_prefixes_only(qw, long, n_seq, n):  # noqa: F811
+    """Below the bound a step is the one over copies, bit for bit; from it on it does not read a later sequence's copy."""
+    wl, m = long
+    p = prompt(wl, n, n)
+    out = []
+    for spoilt in (False, True):
+        b = qw.Batch(m, n_seq, 1100, qw.KV_INT8_G32)
+        b.prefill(0, p)
+        for s in range(1, n_seq):
+            b.fork(0, s)
+        if spoilt:
+            rows = key_rows(b, n_seq - 1, "int8", 1100)
+            rows[:, :, 100] = rows[:, :, 100].flip(-1)
+        b.step(n_seq, list(range(5, 5 + n_seq)))
+        out.append(b.logits().clone())
+        b.close()
+    assert torch.equal(out[0][:-1], out[1][:-1])
+    assert torch.equal(out[0][-1], out[1][-1]) == (n in (768, 1024))
+
+
 def test_the_first_draw_is_from_the_logits_that_a_fork_took_over(qw, tiny):  # noqa: F811
     wl, _, m = tiny
     b = qw.Batch(m, 4, 400)
@@ -133,15 +162,6 @@ def test_the_first_draw_is_from_the_logits_that_a_fork_took_over(qw, tiny):  # n
     assert torch.equal(b.logits(), c.logits())
     b.close()
     c.close()
-
-
-@pytest.fixture(scope="module")
-def long(qw):  # noqa: F811
-    wl = qi.WORKLOADS["tiny"]
-    m = qw.Model(wl, qw.weights_to_device(qi.make_weights(wl), int8=False), max_ctx=4200)
-    m.set_debug(qw.DEBUG_HIDDEN)
-    yield wl, m
-    m.close()
 
 
 @pytest.mark.parametrize("kv", ["model", "int8"])
