@@ -501,7 +501,8 @@ int qw_process_logits(const qw_process_logits_args *args, void *cuda_stream);
  * top_p; 3.1e-5 at 2^24, where weights below 2^-39 of w_1 count for nothing.  What a row draws depends on its logits, u and
  * settings alone: it is the same on every call, whatever other rows the call has.
  * NULL: temperature 1, top_k 0, top_p 1, min_p 0; probs and kept may be NULL.  All parameters and results
- * are device arrays [n_rows].  n_rows <= 65535, vocab <= 2^24.
+ * are device arrays [n_rows]; tokens, probs and kept share no element with one another nor with the settings
+ * (QW_INVALID_ARGUMENT).  n_rows <= 65535, vocab <= 2^24.
  */
 typedef struct {
     const void *logits;

@@ -25,6 +25,12 @@ constexpr int32_t kMostEntries = 1 << 28;  // of a list: a token's count in two 
 
 bool stride_ok(int64_t s, int64_t unit) { return s >= 0 && s % unit == 0; }
 
+// Whether two arrays of n 32-bit elements share any (NULL: there is none).
+bool arrays_meet(const void *a, const void *b, int64_t n) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return a && b && (x < y ? y - x : x - y) < (uintptr_t)n * 4;
+}
+
 // Whether rows of `len` elements along three dimensions have addresses of their own: taken from the smallest
 // stride up, each one is no shorter than all that the dimensions before it span.
 struct Dim {
@@ -234,6 +240,14 @@ int qw_sample_rows(const qw_sample_rows_args *a, void *cuda_stream) {
     for (const void *p : {(const void *)a->u, (const void *)a->temperature, (const void *)a->top_k, (const void *)a->top_p,
                           (const void *)a->min_p, (const void *)a->tokens, (const void *)a->probs, (const void *)a->kept})
         if (!aligned(p, 4)) return QW_ALIGNMENT;
+    // a row is answered while others have yet to read every row's settings: which of them take long
+    const void *const in[] = {a->temperature, a->top_k, a->top_p, a->min_p}, *const out[] = {a->tokens, a->probs, a->kept};
+    for (int i = 0; i < 3; ++i) {
+        for (const void *p : in)
+            if (arrays_meet(out[i], p, a->n_rows)) return QW_INVALID_ARGUMENT;
+        for (int j = 0; j < i; ++j)
+            if (arrays_meet(out[i], out[j], a->n_rows)) return QW_INVALID_ARGUMENT;
+    }
     return status_of(qw::launch_sample_rows(*a, (cudaStream_t)cuda_stream));
 }
 
