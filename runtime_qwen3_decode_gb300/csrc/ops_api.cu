@@ -208,6 +208,7 @@ int qw_prefix_attention(const qw_kv_view *prefix, const qw_kv_view *kv, const qw
     const size_t need = qw::prefix_attn_scratch_bytes(*kv, a->n_max, a->n_heads, a->max_len, max_prefix);
     if (need == 0) return QW_UNSUPPORTED_SHAPE;
     if (scratch_bytes < need) return QW_OUT_OF_MEMORY;
+    if (a->q == a->out) return QW_INVALID_ARGUMENT;  // rows are read again where a result was not finite
     return status_of(qw::launch_prefix_attn(*prefix, *kv, *a, prefix_len_dev, max_prefix, scratch_dev, (cudaStream_t)cuda_stream));
 }
 

@@ -4,7 +4,7 @@ import ctypes
 import pytest
 
 from test_ops_host import P, qw  # noqa: F401
-from test_ops_host_prefix import sample
+from test_ops_host_prefix import call, sample
 
 
 def apart(**kw):
@@ -22,3 +22,7 @@ def test_results_over_settings_or_one_another(qw, out, other, shift):  # noqa: F
     d = apart()
     a = sample(qw, **{**d, out: d[other] + shift})
     assert qw.lib().qw_sample_rows(ctypes.byref(a), None) == qw.INVALID_ARGUMENT
+
+
+def test_prefix_attention_in_place(qw):  # noqa: F811
+    assert call(qw, args=dict(q=P + 4096, out=P + 4096)) == qw.INVALID_ARGUMENT
