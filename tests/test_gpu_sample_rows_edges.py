@@ -4,7 +4,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_sample_rows import check, gen, qw  # noqa: E402, F401
+from test_gpu_sample_rows import check, gen, peaked, qw  # noqa: E402, F401
 
 pytestmark = pytest.mark.gpu
 
@@ -85,3 +85,18 @@ def test_long_tails_of_small_weights(qw, V, units):  # noqa: F811
     qw.sample_rows(x.expand(8, V), torch.zeros(8, device="cuda"), top_p=torch.from_numpy(p).cuda(), kept=kept)
     for n, pp in zip(kept.tolist(), p.astype(np.float64)):
         assert 1 + (n - 2) * w - 2 * off < pp * S <= 1 + (n - 1) * w + 2 * off or (n == 1 and pp * S <= 1 + 2 * off)
+
+
+@pytest.mark.parametrize("dt,V", [(torch.bfloat16, 1 << 20), (torch.float32, 700001), (torch.float16, 400003)])
+def test_rows_that_shared_memory_does_not_hold(qw, dt, V):  # noqa: F811
+    """Rows that are read again in every pass, at random logits whose borders are clear: all but a few are compared."""
+    g = gen(V)
+    R = 8
+    x = peaked(g, R, V, dt)
+    u = torch.rand((R,), generator=g, device="cuda").cpu().numpy()
+    for t, k, p, m in ((1.0, 200, 0.9, None), (0.8, 5000, 0.95, None), (1.0, None, None, 0.01), (0.0, None, None, None)):
+        check(qw, x, u, t, k, p, m, out_sure=0.9)
+    flat = torch.randn((R, V), generator=g, device="cuda").to(dt)
+    # a running sum passes a border by a weight of some 1e-6, next to which 5e-9 are seldom
+    for t, k, p, m in ((1.0, None, 0.9, None), (1.3, V // 2, None, None), (1.0, None, 0.99, 0.001)):
+        check(qw, flat, u, t, k, p, m, out_sure=0.75)
