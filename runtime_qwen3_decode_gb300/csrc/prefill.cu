@@ -713,6 +713,9 @@ __global__ void __launch_bounds__(256) kv_shadow_kernel(const KT *kc, const KT *
 // memory.  Per block, shared memory then carries the two 32 KB TMA writes and the two
 // 32 KB operand reads; staging Q and P there as well doubled that traffic, and it was
 // shared-memory bandwidth, not the tensor core or the softmax, that set the block time.
+// A softmax warp may be one block ahead of another, as S_{j+1} waits for no P_j: P_j and P_{j+1} have barriers of their own (on one
+// barrier the faster warp's two arrivals stood for the slower one's, and P_j V_j ran with 32 rows of an older P, in one of
+// some 300 prompts of 2,000 rows).  Two ahead it is not: S_{j+2} is issued behind P_j V_j.
 // O is rescaled only when a row's running max grows by more than 8 (factor 256): O and
 // the row sum l always refer to the same reference max, so O / l is unaffected, and
 // p <= 2^8 stays well inside fp16.
@@ -776,7 +779,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
     uint8_t *sQ = base + FaSmem::kQ, *sK = base + FaSmem::kK, *sV = base + FaSmem::kV;
     uint64_t *bars = reinterpret_cast<uint64_t *>(base + FaSmem::kBar);
     uint64_t *q_full = bars, *q_tm = bars + 1, *k_full = bars + 2, *k_empty = bars + 5, *v_full = bars + 8,
-             *v_empty = bars + 11, *s_full = bars + 14, *p_full = bars + 18, *pv_done = bars + 19,
+             *v_empty = bars + 11, *s_full = bars + 14, *p_full = bars + 16, *pv_done = bars + 18,
              *drain = bars + 24;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + 25);
     volatile int *abort = reinterpret_cast<volatile int *>(tslot + 1);
@@ -804,9 +807,11 @@ __global__ void __launch_bounds__(kFaThreads, 1)
             mbar_init(&v_full[i], 1);
             mbar_init(&v_empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1);
-        mbar_init(p_full, kFaSoftmaxWarps);
-        mbar_init(pv_done, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], kFaSoftmaxWarps);
+            mbar_init(&pv_done[i], 1);
+        }
         mbar_init(drain, 1);
         *abort = 0;
         mbar_fence_init();
@@ -910,7 +915,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                 if (j >= 0) {
                     const int st = j % kFaStages;
                     if (!mbar_wait(&v_full[st], (unsigned)(j / kFaStages) & 1u, abort, true, kWaitLimitNs) ||
-                        !mbar_wait(p_full, (unsigned)j & 1u, abort, true, kWaitLimitNs)) {
+                        !mbar_wait(&p_full[j & 1], (unsigned)(j >> 1) & 1u, abort, true, kWaitLimitNs)) {
                         ok = false;
                         break;
                     }
@@ -921,7 +926,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                         const uint64_t bd = desc_sw128(sv + (k >> 2) * 16384) + 2u * (k & 3);
                         mma_f16_ts(tO, tmem + 128u * (j & 1) + 8u * k, bd, idesc, j > 0 || k > 0);
                     }
-                    mma_commit(pv_done);
+                    mma_commit(&pv_done[j & 1]);
                     mma_commit(&v_empty[st]);
                 }
             }
@@ -994,7 +999,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
             const float factor = resc ? fast_exp2(m_used - m_new) : 1.f;
             // O must hold P_{j-1} V_{j-1} before it is rescaled
             if (j > 0 && __any_sync(0xffffffffu, resc)) {
-                if (!warp_wait(pv_done, (unsigned)(j - 1) & 1u, abort)) {
+                if (!warp_wait(&pv_done[(j - 1) & 1], (unsigned)((j - 1) >> 1) & 1u, abort)) {
                     ok = false;
                     break;
                 }
@@ -1029,9 +1034,9 @@ __global__ void __launch_bounds__(kFaThreads, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(p_full);
+            if (lane == 0) mbar_arrive(&p_full[b]);
         }
-        if (ok && !warp_wait(pv_done, (unsigned)(nkb - 1) & 1u, abort)) ok = false;
+        if (ok && !warp_wait(&pv_done[(nkb - 1) & 1], (unsigned)((nkb - 1) >> 1) & 1u, abort)) ok = false;
         if (ok) {
             tc_fence_after();
             const float inv = 1.0f / l;
