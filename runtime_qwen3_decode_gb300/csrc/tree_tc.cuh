@@ -21,8 +21,9 @@
 // them K and four V.  bf16 beside bf16: TMA writes K and V tiles straight into swizzled operand
 // tiles, three stages each.  Otherwise TMA fills two slots of 16 KB with raw rows for each
 // plane, and the converters write the 16-bit operand tiles, double-buffered (one stage of
-// two-term tiles of 128 positions; PREFIX has two of 64, see tile_log2 in prefix_tc.cu).  8-bit rows become fp16 (code * scale rounded once, 2^-11; bf16 would lose
-// three more bits and cost twice the instructions), bf16 queries beside them fp16 after
+// two-term tiles of 128 positions; PREFIX has two of 64, see tile_log2 in prefix_tc.cu).  8-bit rows
+// become fp16 (code * scale rounded once, 2^-11; bf16 would lose three more bits and cost twice the
+// instructions), bf16 queries beside them fp16 after
 // division by a power of two per row, so that only elements 2^-14 below the row's largest
 // lose bits.  f32 rows become two fp16 terms beside fp16 queries and two bf16 terms beside bf16 ones,
 // whose range they keep (one fp16 term took 77 us instead of 96, and made V infinite above 65504).
