@@ -719,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, B == kFewBins ? 2 : 1) sample_rows_k
     int stage = top_k > 0 ? 0 : 1, side = 0, turn = 0;
     enum { kOctaves, kNarrow, kMinP, kNone } pass = kOctaves;
     bool seek = false, from_octaves = true;
-    float near = -1.f;  // of the octave that was entered: the share of its width above the border, < 0: not known
+    float near = -1.f;  // of the octave that was entered: the share of its width above the border; -1: not known; -2: cut by keys
     u64 goal = 0;
     Total whole{}, kept{};
     Zone z = rows;
@@ -770,6 +770,7 @@ __global__ void __launch_bounds__(kThreads, B == kFewBins ? 2 : 1) sample_rows_k
             before = b ? total[b - 1] : Total{0ull, 0u, 0u};
             t = total[b];
             const bool inner = from_octaves && b > 0 && b < B - 2;
+            if (!from_octaves && (!c.by_value || t.n - before.n == z.inside.n)) near = -2.f;
             if (inner && warp == 2) {
                 // About where in the octave the border is, if what octaves hold grows by the same factor g^2 from the one above to the
                 // one below: 1 + share (g - 1) = g^near.
@@ -793,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, B == kFewBins ? 2 : 1) sample_rows_k
                 __syncthreads();
                 if (b > 0) z.end = min(z.end, (u64)sh.edge[0] << a.id_bits);
                 if (b < B - 1) z.lo = max(z.lo, (u64)sh.edge[1] << a.id_bits);
-                near = inner ? sh.near : -1.f;
+                if (inner) near = sh.near;
             } else {
                 z.lo += (u64)(B - 1 - b) << c.shift;
                 z.end = min(z.end, z.lo + (1ull << c.shift));
@@ -807,10 +808,12 @@ __global__ void __launch_bounds__(kThreads, B == kFewBins ? 2 : 1) sample_rows_k
                                                                               : z.inside.n > (unsigned)kPart);
         all = !cut_more && stage < 2 && down <= (unsigned)kList;
         if (cut_more) {
-            // in parts of equal spans of logits while they have places enough between them, then of keys
+            // In parts of equal spans of logits while they have places enough between them, then of keys; of keys at once where such
+            // a part had all of the tokens.  (Equal logits stop the spans at some 1e-6 of their value, but zeros at 1e-30 only: 8
+            // rows of 151,936 of which half are 0 took 614 us.)
             const unsigned low = (unsigned)(z.lo >> a.id_bits), high = (unsigned)((z.end - 1ull) >> a.id_bits);
             const float xl = ord_value(low), xh = ord_value(high), width = xh * (1.f / B) - xl * (1.f / B);
-            c.by_value = high - low > 64u && width > fmaxf(fmaxf(fabsf(xl), fabsf(xh)) * 1e-6f, 1e-30f);
+            c.by_value = near > -2.f && high - low > 64u && width > fmaxf(fmaxf(fabsf(xl), fabsf(xh)) * 1e-6f, 1e-30f);
             c.top = xh;
             c.inv = 1.f / width;
             if (near >= 0.f && c.by_value) {  // narrow parts about the place where the border should be
