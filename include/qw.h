@@ -283,7 +283,8 @@ int qw_batch_fork(qw_batch *b, int32_t src, int32_t dst, int32_t n);
  */
 int qw_batch_sample(qw_batch *b, int32_t n_seq, const float *u_dev, const float *temperature_dev, const int32_t *top_k_dev,
                     const float *top_p_dev, const float *min_p_dev, int32_t *next_tokens_host);
-/* f32 logits [n_seq][vocab] of the last step (device), n = n_seq * vocab; a later prompt or fork puts its own into its sequence's row. */
+/* f32 logits [n_seq][vocab] of the last step (device), n = n_seq * vocab; a later prompt or fork puts its own into its
+ * sequence's row. */
 int qw_batch_logits(qw_batch *b, float *dst_dev, int64_t n);
 /* f32 [n_layers + 1][n_seq][hidden] residual stream of the last step (the model's
  * QW_DEBUG_HIDDEN flag must have been set for that step). */
@@ -431,8 +432,8 @@ int qw_tree_attention(const qw_kv_view *kv, const qw_tree_attention_args *args, 
  * mask; args->mask NULL: itself and the ones before it (one node: the attention of a batched decode step).  Row (b, i) of out is
  *   sum_j softmax_j(scale q . k_j) v_j over the prefix's and its own positions j that it sees, 0 if it sees none.
  * args, its rows that are left as they were and its arithmetic are qw_tree_attention's, but 16-bit softmax weights are summed
- * as they are rounded for the product (not beside bf16 queries over 8-bit rows); what one sequence holds does not reach another one, NaN and infinities included.  A prefix_len
- * outside [0, prefix->max_ctx] makes every row NaN.  out and q share no element (QW_INVALID_ARGUMENT if they are the same).
+ * as they are rounded for the product (not beside bf16 queries over 8-bit rows); what one sequence holds does not
+ * reach another one, NaN and infinities included.  A prefix_len outside [0, prefix->max_ctx] makes every row NaN.  out and q share no element (QW_INVALID_ARGUMENT if they are the same).
  * max_prefix: about the prefix's length as the host knows it (see max_len).  A scratch for some sizes does for smaller ones.
  * n_seq x n_max x query heads of a KV head <= 2^20.
  */

@@ -715,7 +715,7 @@ __global__ void __launch_bounds__(256) kv_shadow_kernel(const KT *kc, const KT *
 // shared-memory bandwidth, not the tensor core or the softmax, that set the block time.
 // A softmax warp may be one block ahead of another, as S_{j+1} waits for no P_j: P_j and P_{j+1} have barriers of their own (on one
 // barrier the faster warp's two arrivals stood for the slower one's, and P_j V_j ran with 32 rows of an older P, in one of
-// some 300 prompts of 2,000 rows).  Two ahead it is not: S_{j+2} is issued behind P_j V_j.
+// 42 prompts of 2,048 rows a layer).  Two ahead it is not: S_{j+2} is issued behind P_j V_j.
 // O is rescaled only when a row's running max grows by more than 8 (factor 256): O and
 // the row sum l always refer to the same reference max, so O / l is unaffected, and
 // p <= 2^8 stays well inside fp16.

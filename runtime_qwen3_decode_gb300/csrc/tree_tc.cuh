@@ -94,7 +94,7 @@ struct Cfg {
     static constexpr float kLag = kBf16 ? 8.f : 6.f, kLift = kBf16 ? 0.f : 9.f;
     // PREFIX: sums of softmax weights are of the rounded ones, so that the result is a mean and what a large weight is off by does
     // not move it (16 rows over 200 keys: up to 1.43 times as far off as one rounding of the result leaves them, else
-    // 1.77).  bf16 results beside fp16 weights (8-bit rows) do not show it, and would pay 8%.
+    // 1.77).  bf16 results beside fp16 weights (8-bit rows) do not show it.
     static constexpr bool kSumRounded = !(SRC == SRC_Q8_F16 && TERMS == 1);
     static constexpr int kElem = SRC == SRC_Q8_F16 ? 1 : SRC == SRC_F32_F16 || SRC == SRC_F32_BF16 ? 4 : 2;
     static constexpr int kThreads = 32 * (kDirect ? kPlainWarps : kPlainWarps + kConvWarps - 2);
@@ -938,7 +938,8 @@ __global__ void __launch_bounds__(Cfg<SRC, D, TERMS, TILE>::kThreads, 1)
             }
             if (nodes < 64) mask &= (1ull << nodes) - 1ull;
             const bool scaled_row = !C::kBf16 && a.dtype == QW_DT_BF16 && live;
-            // not below the least normal number: times 0 a hidden score would be NaN, and such a row's seen ones round to 0 all the same
+            // not below the least normal number: times 0 a hidden score (-inf) would be NaN, and the seen ones of such a row are 0
+            // beside it all the same
             const float sc = a.scale_log2 == 0.f ? 1.f : fmaxf(fabsf(a.scale_log2) * (scaled_row ? row_scale[r] : 1.f), FLT_MIN);
             float m_used = -INFINITY, l = 0.f;
             int mine = 0;  // tiles of this segment that this group has done
